@@ -537,6 +537,159 @@ kdaStatus_t kda_chunk_bwd_ws(const void *q, const void *k, const void *v,
                              float *d_initial_state, const kdaShape_t *shape, void *workspace,
                              size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The full-attention layers of a mixed stack.  KDA is deployed in stacks that
+ * keep some softmax-attention layers ("Linear Attention, From Scratch to Kimi
+ * 3": three KDA layers to one full-attention layer).  These entry points
+ * serve such a layer beside the KDA ones: attention over whole packed
+ * prompts, the paged key-value cache's append (with the position rotation
+ * applied on the way), and one token of every sequence attending to its
+ * cache.  With query head j reading key-value head
+ * j / G, G = num_heads / num_kv_heads:
+ *
+ *     z_ij = scale <q_i, k_j>,  j <= i          (one sequence's tokens)
+ *     lse_i = ln sum_j exp(z_ij)
+ *     o_i   = sum_j exp(z_ij - lse_i) v_j
+ *
+ * The pages give softmax attention as motivation only; the formula is the
+ * whole definition.  Masked places contribute nothing,
+ * whatever the masked keys and values hold (infinities and NaN included).
+ * Forward only: these are the serving path.
+ * ---------------------------------------------------------------------------
+ */
+typedef struct {
+    int32_t num_seqs;      /* N >= 1 */
+    int32_t total_tokens;  /* T >= 0: rows of q, k, v; must equal N (step) */
+    int32_t num_heads;     /* HQ >= 1: query heads */
+    int32_t num_kv_heads;  /* HKV >= 1, divides HQ; HQ / HKV <= 128 */
+    int32_t head_dim;      /* d in {16, 32, 64, 128} */
+    int32_t dtype;         /* kdaDtype_t of q, k, v, out and the cache */
+    int32_t engine;        /* kda_attn_fwd: kdaEngine_t; ignored by the others */
+    int32_t out_f32;       /* 1: out is float32 for bf16 inputs */
+    int64_t q_stride;      /* elements from one token's row to the next in q, k */
+    int64_t k_stride;      /*   and v (views of a fused projection); 0 =        */
+    int64_t v_stride;      /*   contiguous.  Heads and channels stay contiguous;*/
+                           /*   a stride is a multiple of 16 bytes              */
+} kdaAttnShape_t;
+
+/* A paged key-value cache: fixed-size pages of one layer, and for every
+   sequence the pages that hold its tokens, in order. */
+typedef struct {
+    void *k;                     /* [num_pages, HKV, page_size, d] dtype, 16-byte aligned */
+    void *v;                     /* same layout */
+    const int32_t *block_table;  /* device [N, max_pages]: page of token p is entry
+                                    p / page_size of its sequence's row */
+    int32_t num_pages;           /* >= 0 */
+    int32_t page_size;           /* 16, 32, 64, 128 or 256 tokens */
+    int32_t max_pages;           /* entries per row of block_table, >= 0 */
+} kdaPagedCache_t;
+
+/* Position rotation: a table of cosines and sines per position.  Pair m
+   (m < rot_dim / 2) of channels (a, b) turns by the table's angle,
+       y_a = x_a cos - x_b sin,   y_b = x_b cos + x_a sin,
+   computed in fp32 and rounded once; channels from rot_dim on are copied. */
+typedef struct {
+    const float *table;     /* device [num_positions, rot_dim]: rot_dim / 2 cosines,
+                               then rot_dim / 2 sines; 16-byte aligned */
+    int32_t num_positions;
+    int32_t rot_dim;        /* a multiple of 16, <= d */
+    int32_t interleaved;    /* 0: pair m is channels (m, m + rot_dim / 2);
+                               1: channels (2m, 2m + 1) */
+} kdaRope_t;
+
+/*
+ * kda_attn_fwd -- causal softmax attention over packed whole prompts.
+ *
+ *   q           [T, HQ, d]   dtype (token stride q_stride)
+ *   k, v        [T, HKV, d]  dtype (k_stride, v_stride)
+ *   scale       host float, finite and > 0
+ *   cu_seqlens  [N + 1] int32 device, as for kda_chunk_fwd (clamped to [0, T]);
+ *               NULL when N == 1.  Rows of out and lse outside every sequence
+ *               are left as they were.
+ *   out         [T, HQ, d]   dtype (float32 if shape->out_f32), contiguous
+ *   lse         [T, HQ]      float32 or NULL: ln of each row's sum of
+ *               exponentials, for joining with attention over other keys
+ *
+ * KDA_ENGINE_TENSOR: tcgen05/TMEM tiles, bf16 with d = 64 or 128 (what AUTO
+ * takes for these); KDA_ENGINE_SIMT: fp32 CUDA-core arithmetic, every
+ * supported shape.  The tensor engine rounds the softmax weights to bf16 for
+ * their product with v (their sum is taken in fp32 before the rounding).
+ * Allocates nothing; errors detectable on the host return before any launch.
+ */
+kdaStatus_t kda_attn_fwd(const void *q, const void *k, const void *v, float scale,
+                         const int32_t *cu_seqlens, void *out, float *lse,
+                         const kdaAttnShape_t *shape, cudaStream_t stream);
+
+/*
+ * kda_cache_append -- write new tokens' keys and values to the paged cache,
+ * rotating queries and keys by their positions on the way.
+ *
+ * Token i (from 0) of sequence s is at position p = cache_lens[s] + i: it
+ * rotates by row p of rope->table and its key and value go to row
+ * p % page_size of page block_table[s][p / page_size].
+ *
+ *   q           [T, HQ, d] dtype or NULL (then q_out is NULL too)
+ *   k, v        [T, HKV, d] dtype
+ *   cu_seqlens  [N + 1] int32 device; NULL when N == 1 (one sequence) or
+ *               T == N (one token of every sequence).  Rows outside every
+ *               sequence are not read, and their outputs are left as they were.
+ *   cache_lens  [N] int32 device: tokens each sequence holds before the call
+ *               (not changed by the call)
+ *   rope        NULL: no rotation (q is copied to q_out, k as it is)
+ *   q_out       [T, HQ, d] dtype contiguous, or NULL; may be q (contiguous)
+ *   k_out       [T, HKV, d] dtype contiguous: the rotated keys, for
+ *               kda_attn_fwd; or NULL; may be k (contiguous)
+ *
+ * A token whose block-table entry is negative is not written to the cache
+ * (its q_out / k_out are).  A token whose position has no block-table entry
+ * (negative, or past max_pages pages), whose page is >= num_pages, or, with
+ * rope, whose position is not in the table, is skipped whole and sets
+ * KDA_ERR_INVALID_ARG in the device status word (kda_device_status).  Two
+ * tokens must not share a row of the cache.  A sequence's
+ * first kda_attn_step after the call counts the new tokens in seq_lens.
+ * Allocates nothing.
+ */
+kdaStatus_t kda_cache_append(const void *q, const void *k, const void *v,
+                             const int32_t *cu_seqlens, const int32_t *cache_lens,
+                             const kdaRope_t *rope, void *q_out, void *k_out,
+                             const kdaPagedCache_t *cache, const kdaAttnShape_t *shape,
+                             cudaStream_t stream);
+
+/*
+ * kda_attn_step -- one token of each of N sequences attends to the first
+ * seq_lens[s] tokens of its paged cache (its own key and value, appended by
+ * kda_cache_append, among them).
+ *
+ *   q         [N, HQ, d] dtype (token stride q_stride; k_stride, v_stride ignored)
+ *   seq_lens  [N] int32 device.  A length <= 0 is a sequence without keys:
+ *             out = 0, lse = -inf (rows that pad a batch).
+ *   out       [N, HQ, d] dtype (float32 if shape->out_f32)
+ *   lse       [N, HQ] float32 or NULL
+ *
+ * Rows of the pages behind a sequence's length are never read.  Several
+ * sequences may share pages.  A length beyond max_pages * page_size is cut to
+ * it, and the tokens of a page that is negative or >= num_pages are left out;
+ * both set KDA_ERR_INVALID_ARG in the device status word.
+ * Scratch (partial results of sequences that several thread blocks share):
+ * kda_attn_step_workspace_size() bytes, taken with cudaMallocAsync /
+ * cudaFreeAsync on `stream`; kda_attn_step_ws takes the caller's instead.
+ */
+kdaStatus_t kda_attn_step(const void *q, const kdaPagedCache_t *cache, const int32_t *seq_lens,
+                          float scale, void *out, float *lse, const kdaAttnShape_t *shape,
+                          cudaStream_t stream);
+
+/* Bytes of device scratch kda_attn_step_ws needs on the current device for
+   any cache and lengths with `shape`.  *bytes is written on success. */
+kdaStatus_t kda_attn_step_workspace_size(const kdaAttnShape_t *shape, size_t *bytes);
+
+/* kda_attn_step with caller-owned scratch: `workspace` is a device buffer of
+   at least kda_attn_step_workspace_size() bytes, 256-byte aligned, not used by
+   anything else until the work on `stream` is done.  Allocates nothing. */
+kdaStatus_t kda_attn_step_ws(const void *q, const kdaPagedCache_t *cache, const int32_t *seq_lens,
+                             float scale, void *out, float *lse, const kdaAttnShape_t *shape,
+                             void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char *kda_status_string(kdaStatus_t status);
 
@@ -546,7 +699,8 @@ const char *kda_status_string(kdaStatus_t status);
  * KDA_ERR_TIMEOUT if a bounded wait inside a kernel gave up since the last
  * call (that kernel's outputs are then invalid), or KDA_ERR_INVALID_ARG if
  * kda_recurrent_fwd met a state index >= num_slots (that sequence was
- * skipped).  Returns KDA_ERR_CUDA if the synchronisation itself fails.
+ * skipped) or kda_cache_append / kda_attn_step a position, page or length
+ * outside the cache (skipped as they document).  Returns KDA_ERR_CUDA if the synchronisation itself fails.
  */
 kdaStatus_t kda_device_status(cudaStream_t stream);
 

@@ -17,6 +17,9 @@ The functions carry the C names:
 * ``kda_recurrent_bwd`` -- gradients of the recurrence;
 * ``kda_chunk_fwd_ws_diag`` -- the prefill with a chosen wait limit, optionally
   without its chunk-parallel stage (tests of the timeout path);
+* ``kda_attn_fwd``, ``kda_cache_append``, ``kda_attn_step`` -- the full-attention layers of a
+  mixed stack: causal attention over packed prompts, rotation and append to a paged cache,
+  one token of every sequence over its cache;
 * ``kda_chunk_path_counts`` -- how the decayed products were evaluated;
 * ``kda_status_string``, ``kda_device_status``.
 """
@@ -62,6 +65,26 @@ class kdaConvShape_t(ctypes.Structure):
     _fields_ = [("num_seqs", ctypes.c_int32), ("total_tokens", ctypes.c_int32),
                 ("channels", ctypes.c_int32), ("width", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("activation", ctypes.c_int32)]
+
+
+class kdaAttnShape_t(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("total_tokens", ctypes.c_int32),
+                ("num_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("engine", ctypes.c_int32), ("out_f32", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64)]
+
+
+class kdaPagedCache_t(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class kdaRope_t(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("num_positions", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 class KdaError(RuntimeError):
@@ -136,6 +159,19 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.kda_chunk_bwd_ws.restype = ctypes.c_int
     lib.kda_chunk_bwd_workspace_size.argtypes = [shp, ctypes.POINTER(ctypes.c_size_t)]
     lib.kda_chunk_bwd_workspace_size.restype = ctypes.c_int
+    ashp = ctypes.POINTER(kdaAttnShape_t)
+    cachep, ropep = ctypes.POINTER(kdaPagedCache_t), ctypes.POINTER(kdaRope_t)
+    lib.kda_attn_fwd.argtypes = [vp, vp, vp, ctypes.c_float, ip, vp, fp, ashp, vp]
+    lib.kda_attn_fwd.restype = ctypes.c_int
+    lib.kda_cache_append.argtypes = [vp, vp, vp, ip, ip, ropep, vp, vp, cachep, ashp, vp]
+    lib.kda_cache_append.restype = ctypes.c_int
+    lib.kda_attn_step.argtypes = [vp, cachep, ip, ctypes.c_float, vp, fp, ashp, vp]
+    lib.kda_attn_step.restype = ctypes.c_int
+    lib.kda_attn_step_workspace_size.argtypes = [ashp, ctypes.POINTER(ctypes.c_size_t)]
+    lib.kda_attn_step_workspace_size.restype = ctypes.c_int
+    lib.kda_attn_step_ws.argtypes = [vp, cachep, ip, ctypes.c_float, vp, fp, ashp, vp,
+                                     ctypes.c_size_t, vp]
+    lib.kda_attn_step_ws.restype = ctypes.c_int
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_device_status.argtypes = [vp]
@@ -713,6 +749,263 @@ def kda_chunk_bwd(q, k, v, log_alpha, beta, scale: float, initial_state=None,
         _ptr(dk), _ptr(dv), _ptr(dlog), _ptr(db), _ptr(dS0), ctypes.byref(shape), wp,
         int(n.value), _stream_handle(stream)), "kda_chunk_bwd_ws")
     return dq, dk, dv, dlog, db, dS0
+
+
+# ---------------------------------------------------------------------------
+# the full-attention layer
+# ---------------------------------------------------------------------------
+
+def make_attn_shape(N, T, HQ, HKV, d, dtype_code, engine=KDA_ENGINE_AUTO, out_f32=0, q_stride=0,
+                    k_stride=0, v_stride=0) -> kdaAttnShape_t:
+    """HQ / HKV: query / key-value heads; strides: elements from one token's
+    row to the next (0: contiguous)."""
+    return kdaAttnShape_t(int(N), int(T), int(HQ), int(HKV), int(d), int(dtype_code), int(engine),
+                          int(out_f32), int(q_stride), int(k_stride), int(v_stride))
+
+
+def _rows(t, name, dtype=None, shape=None) -> int:
+    """Checks [T, heads, d] rows whose heads and channels are contiguous (a
+    slice of a fused projection is fine); returns the token stride (0:
+    contiguous)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, d]")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return 0
+    T, H, d = t.shape
+    st, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (H > 1 and sh != d) or (T > 1 and st < H * d):
+        raise ValueError(f"{name}: heads and channels of a token must be contiguous")
+    if T <= 1:
+        return 0
+    if st * t.element_size() % 16:
+        raise ValueError(f"{name}: the token stride must be a multiple of 16 bytes")
+    return st
+
+
+def _paged_cache(k_cache, v_cache, block_table, dtype, N, HKV, d) -> kdaPagedCache_t:
+    torch = _torch()
+    _require(k_cache, "k_cache", dtype)
+    if k_cache is None or k_cache.dim() != 4 or k_cache.shape[1] != HKV or k_cache.shape[3] != d:
+        raise ValueError("k_cache must be [pages, HKV, page_size, d]")
+    if v_cache is None:
+        raise ValueError("v_cache must be [pages, HKV, page_size, d]")
+    _require(v_cache, "v_cache", dtype, k_cache.shape)
+    _require(block_table, "block_table", torch.int32)
+    if block_table is None or block_table.dim() != 2 or block_table.shape[0] != N:
+        raise ValueError(f"block_table must be [{N}, pages per sequence]")
+    return kdaPagedCache_t(_ptr(k_cache), _ptr(v_cache), _ptr(block_table), k_cache.shape[0],
+                           k_cache.shape[2], block_table.shape[1])
+
+
+class _on_device:
+    """The tensors' device as the current one for a call; all tensors share it."""
+
+    def __init__(self, *tensors):
+        torch = _torch()
+        devs = {t.device for t in tensors if t is not None}
+        if len(devs) != 1:
+            raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
+        dev = devs.pop()
+        self.guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _launch_stream(stream, *made):
+    """The handle of the call's stream; tensors the call made are marked as
+    used on it, so that their memory outlives the work."""
+    torch = _torch()
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    for t in made:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def _attn_out(q, out, out_f32):
+    """(out, freshly made out or None, out_f32 flag)."""
+    torch = _torch()
+    odt = _out_dtype(q, out, out_f32)
+    if odt not in (q.dtype, torch.float32):
+        raise TypeError("out must have the dtype of q, or float32")
+    made = None
+    if out is None:
+        out = made = torch.empty(q.shape, dtype=odt, device=q.device)
+    _require(out, "out", odt, q.shape)
+    return out, made, int(odt != q.dtype)
+
+
+def kda_attn_fwd(q, k, v, scale: float, cu_seqlens=None, out=None, lse=None, *, engine="auto",
+                 stream=None, out_f32: bool = False):
+    """Causal softmax attention over packed whole prompts (C: kda_attn_fwd).
+    Returns ``(out, lse)``.
+
+    q: [T, HQ, d] bf16/fp32; k, v: [T, HKV, d] with HKV a divisor of HQ (query
+    head j reads key-value head j // (HQ // HKV)); the token strides are free
+    (slices of a fused projection), heads and channels contiguous.
+    cu_seqlens: int32 [N + 1] on the device (None: one sequence).  ``lse``: a
+    [T, HQ] fp32 tensor that receives each row's log of the sum of
+    exponentials, or None.  ``engine``: "auto" takes the tensor cores for bf16
+    with d = 64 or 128, "simt" is fp32 arithmetic on CUDA cores.
+    """
+    torch = _torch()
+    qs = _rows(q, "q")
+    T, HQ, d = q.shape
+    ks = _rows(k, "k", q.dtype)
+    HKV = k.shape[1]
+    if tuple(k.shape) != (T, HKV, d):
+        raise ValueError(f"k must be [{T}, HKV, {d}], got {tuple(k.shape)}")
+    vs = _rows(v, "v", q.dtype, (T, HKV, d))
+    if HKV == 0 or HQ % HKV:
+        raise ValueError(f"q has {HQ} heads, not a multiple of k's {HKV}")
+    N = 1
+    if cu_seqlens is not None:
+        _require(cu_seqlens, "cu_seqlens", torch.int32)
+        N = cu_seqlens.numel() - 1
+    _require(lse, "lse", torch.float32, (T, HQ))
+    out, made, f32 = _attn_out(q, out, out_f32)
+    eng = _ENGINES[engine] if isinstance(engine, str) else int(engine)
+    shape = make_attn_shape(N, T, HQ, HKV, d, _dtype_code(q), eng, f32, qs, ks, vs)
+    with _on_device(q, k, v, cu_seqlens, out, lse):
+        _check(load().kda_attn_fwd(_ptr(q), _ptr(k), _ptr(v), float(scale), _ptr(cu_seqlens),
+                                   _ptr(out), _ptr(lse), ctypes.byref(shape),
+                                   _launch_stream(stream, made)), "kda_attn_fwd")
+    return out, lse
+
+
+def kda_cache_append(k, v, k_cache, v_cache, block_table, cache_lens, cu_seqlens=None, *, q=None,
+                     q_out=None, k_out=None, rope=None, rope_interleaved: bool = False,
+                     stream=None):
+    """Append new tokens' keys and values to a paged cache, rotating q and k by
+    their positions on the way (C: kda_cache_append).  Returns
+    ``(q_out, k_out)``.
+
+    k, v: [T, HKV, d] bf16/fp32 (free token strides); k_cache / v_cache:
+    [pages, HKV, page_size, d], updated in place; block_table: int32
+    [N, pages per sequence]; cache_lens: int32 [N], the tokens every sequence
+    holds already; cu_seqlens: int32 [N + 1] on the device (None: one sequence,
+    or one token of every sequence when T == N).  ``rope``: fp32
+    [positions, rot_dim], cosines then sines, or None; ``rope_interleaved``
+    pairs neighbouring channels instead of the halves of rot_dim.  With ``q``
+    [T, HQ, d] the rotated queries come back in ``q_out`` (made if None; may
+    be q); ``k_out`` [T, HKV, d] receives the rotated keys if given (may be k).
+    """
+    torch = _torch()
+    ks = _rows(k, "k")
+    T, HKV, d = k.shape
+    vs = _rows(v, "v", k.dtype, (T, HKV, d))
+    HQ, qs, made = HKV, 0, None
+    if q is not None:
+        qs = _rows(q, "q", k.dtype)
+        HQ = q.shape[1]
+        if tuple(q.shape) != (T, HQ, d):
+            raise ValueError(f"q must be [{T}, HQ, {d}], got {tuple(q.shape)}")
+        if HKV == 0 or HQ % HKV:
+            raise ValueError(f"q has {HQ} heads, not a multiple of k's {HKV}")
+        if q_out is None:
+            q_out = made = torch.empty((T, HQ, d), dtype=q.dtype, device=q.device)
+        _require(q_out, "q_out", q.dtype, (T, HQ, d))
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    _require(k_out, "k_out", k.dtype, (T, HKV, d))
+    _require(cache_lens, "cache_lens", torch.int32)
+    if cache_lens is None or cache_lens.dim() != 1:
+        raise ValueError("cache_lens must be [N]")
+    N = cache_lens.numel()
+    if cu_seqlens is not None:
+        _require(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,))
+    elif N not in (1, T):
+        raise ValueError(f"{T} tokens of {N} sequences need cu_seqlens")
+    cache = _paged_cache(k_cache, v_cache, block_table, k.dtype, N, HKV, d)
+    rp = None
+    if rope is not None:
+        _require(rope, "rope", torch.float32)
+        if rope.dim() != 2:
+            raise ValueError("rope must be [positions, rot_dim]")
+        rp = ctypes.byref(kdaRope_t(_ptr(rope), rope.shape[0], rope.shape[1],
+                                    int(bool(rope_interleaved))))
+    shape = make_attn_shape(N, T, HQ, HKV, d, _dtype_code(k), 0, 0, qs, ks, vs)
+    with _on_device(k, v, q, k_cache, v_cache, block_table, cache_lens, cu_seqlens, q_out, k_out,
+                    rope):
+        _check(load().kda_cache_append(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(cache_lens), rp, _ptr(q_out),
+            _ptr(k_out), ctypes.byref(cache), ctypes.byref(shape),
+            _launch_stream(stream, made)), "kda_cache_append")
+    return q_out, k_out
+
+
+_step_bytes = {}
+
+
+def kda_attn_step_workspace_size(shape: kdaAttnShape_t) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().kda_attn_step_workspace_size(ctypes.byref(shape), ctypes.byref(n)),
+           "kda_attn_step_workspace_size")
+    return int(n.value)
+
+
+def kda_attn_step(q, k_cache, v_cache, block_table, seq_lens, scale: float, out=None, lse=None, *,
+                  workspace=None, stream=None, out_f32: bool = False):
+    """One token of every sequence attends to its paged cache (C:
+    kda_attn_step_ws).  Returns ``(out, lse)``.
+
+    q: [N, HQ, d] bf16/fp32; k_cache / v_cache: [pages, HKV, page_size, d];
+    block_table: int32 [N, pages per sequence]; seq_lens: int32 [N], the tokens
+    to attend to (0: a padding row, out = 0).  ``lse``: a [N, HQ] fp32 tensor
+    or None.  Scratch: ``workspace``, a uint8 CUDA tensor of at least
+    kda_attn_step_workspace_size() + 255 bytes that nothing else uses until
+    the work is done, or a fresh one per call (so that captured graphs and
+    calls on other streams never share it).
+    """
+    torch = _torch()
+    qs = _rows(q, "q")
+    N, HQ, d = q.shape
+    if k_cache is None or k_cache.dim() != 4:
+        raise ValueError("k_cache must be [pages, HKV, page_size, d]")
+    HKV = k_cache.shape[1]
+    if HKV == 0 or HQ % HKV:
+        raise ValueError(f"q has {HQ} heads, not a multiple of the cache's {HKV}")
+    cache = _paged_cache(k_cache, v_cache, block_table, q.dtype, N, HKV, d)
+    _require(seq_lens, "seq_lens", torch.int32, (N,))
+    if seq_lens is None:
+        raise ValueError("seq_lens must be [N]")
+    _require(lse, "lse", torch.float32, (N, HQ))
+    out, made, f32 = _attn_out(q, out, out_f32)
+    shape = make_attn_shape(N, N, HQ, HKV, d, _dtype_code(q), 0, f32, qs)
+    with _on_device(q, k_cache, v_cache, block_table, seq_lens, out, lse, workspace):
+        key = (q.device.index, d, HQ // HKV, q.dtype)  # what the size depends on
+        nbytes = _step_bytes.get(key)
+        if nbytes is None:
+            nbytes = _step_bytes[key] = kda_attn_step_workspace_size(shape)
+        ws_made = None
+        if workspace is None:
+            workspace = ws_made = torch.empty(nbytes + 256, dtype=torch.uint8, device=q.device)
+        _require(workspace, "workspace", torch.uint8)
+        wp = (workspace.data_ptr() + 255) // 256 * 256
+        left = workspace.numel() - (wp - workspace.data_ptr())
+        _check(load().kda_attn_step_ws(
+            _ptr(q), ctypes.byref(cache), _ptr(seq_lens), float(scale), _ptr(out), _ptr(lse),
+            ctypes.byref(shape), wp, max(left, 0), _launch_stream(stream, made, ws_made)),
+            "kda_attn_step_ws")
+    return out, lse
 
 
 def kda_device_status(stream=None) -> int:

@@ -202,6 +202,9 @@ kdaStatus_t host_layout(const kdaShape_t *s, HostLayout *L) {
 }
 
 }  // namespace
+
+int *device_status_word() { return device_status_ptr(); }
+
 }  // namespace kda
 
 using namespace kda;

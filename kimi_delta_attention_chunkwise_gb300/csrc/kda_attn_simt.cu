@@ -1,0 +1,262 @@
+// kda_attn_simt.cu -- causal attention over packed prompts in fp32 on CUDA
+// cores: every supported shape, and the engine of fp32 inputs.
+//
+//     z_ij = scale <q_i, k_j>  (j <= i),   o_i = sum_j e^{z_ij} v_j / sum_j e^{z_ij}
+//
+// One pass over the keys with a running maximum and sum per row, in base 2
+// (z scaled by log2 e).  The rows of a tile are (token, query head) pairs of
+// one key-value head, token-major, so grouped heads share every key and value
+// that is brought in and a group of any size fills its tiles.
+//
+// A CTA of 256 threads owns 64 rows and walks the keys in tiles of 64: a
+// thread computes a 4 x 4 block of scores (rows 4 ty + a, keys tx + 16 b) and
+// D / 16 columns of 4 output rows.  The 16 threads of a row share its
+// statistics through shuffles.  Bound by shared-memory reads (8 16-byte reads
+// for 64 multiply-adds); the weights overwrite the key tile, which keeps two
+// CTAs on an SM.
+#include <cstdint>
+#include <cuda_bf16.h>
+
+#include "kda_attn_common.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kRows = 64, kKeys = 64, kThreads = 256;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+template <int D>
+constexpr int kq_stride() { return D + 4; }  // rows 4 banks apart: 16-byte reads without conflicts
+constexpr int kPStride = kKeys + 4;
+
+template <int D>
+constexpr size_t smem_bytes() {
+    const size_t kbuf = kKeys * kq_stride<D>() > kRows * kPStride ? kKeys * kq_stride<D>()
+                                                                  : kRows * kPStride;
+    return (kRows * kq_stride<D>() + kbuf + kKeys * D) * sizeof(float);
+}
+
+// 4 consecutive elements as floats
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+    const uint2 x = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xFFFF0000u),
+                       __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xFFFF0000u));
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 2) attn_simt_kernel(const AttnArgs a) {
+    constexpr int KS = kq_stride<D>();
+    constexpr int CW = D >= 64 ? 4 : D / 16;      // columns of one vector
+    constexpr int CN = D >= 64 ? D / 64 : 1;      // vectors per thread, 64 columns apart
+    extern __shared__ float smem[];
+    float *sq = smem;
+    float *sk = smem + kRows * KS;
+    float *sp = sk;                                // the weights, once the scores are done
+    float *sv = smem + (smem_bytes<D>() / sizeof(float) - kKeys * D);
+    __shared__ SeqTile s_tile;
+    __shared__ int s_found;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    if (tid < 32) {
+        SeqTile t;
+        const bool ok = find_seq_tile(a.cu_seqlens, a.N, a.T, a.G, kRows, blockIdx.x, t);
+        if (tid == 0) {
+            s_found = ok;
+            if (ok) s_tile = t;
+        }
+    }
+    __syncthreads();
+    if (!s_found) return;
+    const SeqTile st = s_tile;
+    const int32_t kvh = blockIdx.y;
+    const int32_t len = st.end - st.begin;
+    const int64_t row0 = (int64_t)st.tile * kRows;          // first row, of len * G
+    const int64_t nrows = (int64_t)len * a.G;
+    const int32_t last_token = (int32_t)(min(row0 + kRows, nrows) - 1) / a.G;
+    const int32_t first_token = (int32_t)(row0 / a.G);
+
+    for (int i = tid; i < kRows * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+        const int64_t row = row0 + r;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row < nrows) {
+            const int32_t tok = (int32_t)(row / a.G), h = (int32_t)(row % a.G);
+            x = load4(static_cast<const T *>(a.q) + (st.begin + (int64_t)tok) * a.q_stride +
+                      ((int64_t)kvh * a.G + h) * D + c);
+        }
+        *reinterpret_cast<float4 *>(sq + r * KS + c) = x;
+    }
+    int32_t tok[4];  // token of each of the thread's rows (-1: no such row)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t row = row0 + ty * 4 + i;
+        tok[i] = row < nrows ? (int32_t)(row / a.G) : -1;
+    }
+    const float c2 = a.scale * kLog2e;
+    float m[4], l[4], acc[4][CN][CW];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int n = 0; n < CN; ++n)
+#pragma unroll
+            for (int j = 0; j < CW; ++j) acc[i][n][j] = 0.f;
+    }
+
+    for (int32_t k0 = 0; k0 <= last_token; k0 += kKeys) {
+        __syncthreads();  // the last tile's weights and values are done with
+        for (int i = tid; i < kKeys * (D / 4); i += kThreads) {
+            const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+            if (k0 + r <= last_token) {
+                const int64_t t = st.begin + (int64_t)k0 + r;
+                x = load4(static_cast<const T *>(a.k) + t * a.k_stride + (int64_t)kvh * D + c);
+                y = load4(static_cast<const T *>(a.v) + t * a.v_stride + (int64_t)kvh * D + c);
+            }
+            *reinterpret_cast<float4 *>(sk + r * KS + c) = x;
+            *reinterpret_cast<float4 *>(sv + r * D + c) = y;
+        }
+        __syncthreads();
+        float s[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < D; c += 4) {
+            float4 qv[4], kv[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                qv[i] = *reinterpret_cast<const float4 *>(sq + (ty * 4 + i) * KS + c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                kv[j] = *reinterpret_cast<const float4 *>(sk + (tx + 16 * j) * KS + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
+                    s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
+                    s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
+                    s[i][j] = fmaf(qv[i].w, kv[j].w, s[i][j]);
+                }
+        }
+        const bool masked = k0 + kKeys - 1 > first_token;  // some key is past some row
+        __syncthreads();  // the keys are done with: the weights take their place
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float mx = m[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (masked && k0 + tx + 16 * j > tok[i]) s[i][j] = -INFINITY;
+                mx = fmaxf(mx, s[i][j]);
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            // a row without keys so far keeps weights of 0 (and no NaN)
+            const float ref = mx == -INFINITY ? 0.f : mx;
+            const float corr = exp2f((m[i] - ref) * c2);
+            m[i] = mx;
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = exp2f((s[i][j] - ref) * c2);
+                sp[(ty * 4 + i) * kPStride + tx + 16 * j] = p;
+                sum += p;
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            l[i] = l[i] * corr + sum;
+#pragma unroll
+            for (int n = 0; n < CN; ++n)
+#pragma unroll
+                for (int j = 0; j < CW; ++j) acc[i][n][j] *= corr;
+        }
+        __syncthreads();
+        const int32_t kend = min(kKeys, last_token + 1 - k0);
+        for (int kk = 0; kk < kend; kk += 4) {
+            float4 pv[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                pv[i] = *reinterpret_cast<const float4 *>(sp + (ty * 4 + i) * kPStride + kk);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                float vv[CN][CW];
+#pragma unroll
+                for (int n = 0; n < CN; ++n) {
+                    const float *src = sv + (kk + u) * D + n * 64 + tx * CW;
+                    if constexpr (CW == 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(src);
+                        vv[n][0] = x.x; vv[n][1] = x.y; vv[n][2] = x.z; vv[n][3] = x.w;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < CW; ++j) vv[n][j] = src[j];
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float p = u == 0 ? pv[i].x : u == 1 ? pv[i].y : u == 2 ? pv[i].z : pv[i].w;
+                    // a masked key adds nothing, whatever its value row holds
+                    if (masked && k0 + kk + u > tok[i]) continue;
+#pragma unroll
+                    for (int n = 0; n < CN; ++n)
+#pragma unroll
+                        for (int j = 0; j < CW; ++j)
+                            acc[i][n][j] = fmaf(p, vv[n][j], acc[i][n][j]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (tok[i] < 0) continue;
+        const int64_t row = row0 + ty * 4 + i;
+        const int64_t t = st.begin + (int64_t)tok[i];
+        const int64_t head = (int64_t)kvh * a.G + row % a.G;
+        const float inv = 1.f / l[i];
+        if (a.lse && tx == 0) a.lse[t * a.HQ + head] = (m[i] * c2 + log2f(l[i])) * kLn2;
+#pragma unroll
+        for (int n = 0; n < CN; ++n)
+#pragma unroll
+            for (int j = 0; j < CW; ++j) {
+                const int64_t o = (t * a.HQ + head) * D + n * 64 + tx * CW + j;
+                const float y = acc[i][n][j] * inv;
+                if (a.out_f32) static_cast<float *>(a.out)[o] = y;
+                else static_cast<__nv_bfloat16 *>(a.out)[o] = __float2bfloat16_rn(y);
+            }
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_t(const AttnArgs &a, cudaStream_t stream) {
+    constexpr size_t bytes = smem_bytes<D>();
+    const cudaError_t e = cudaFuncSetAttribute(
+        attn_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    // every sequence's last tile may be short: at most N more than the rows fill
+    const int64_t tiles = (int64_t)a.T * a.G / kRows + a.N;
+    const dim3 grid((unsigned)tiles, (unsigned)a.HKV);
+    attn_simt_kernel<T, D><<<grid, kThreads, bytes, stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_d(const AttnArgs &a, cudaStream_t stream) {
+    switch (a.D) {
+        case 16: return launch_t<T, 16>(a, stream);
+        case 32: return launch_t<T, 32>(a, stream);
+        case 64: return launch_t<T, 64>(a, stream);
+        case 128: return launch_t<T, 128>(a, stream);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_attn_simt(const AttnArgs &a, cudaStream_t stream) {
+    if (a.dtype == KDA_DTYPE_BF16) return launch_d<__nv_bfloat16>(a, stream);
+    return launch_d<float>(a, stream);
+}
+
+}  // namespace kda

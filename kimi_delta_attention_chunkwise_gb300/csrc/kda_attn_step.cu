@@ -1,0 +1,489 @@
+// kda_attn_step.cu -- one token of every sequence attends to its paged cache.
+//
+//     z_j = scale <q, K_j>,  o = sum_j e^{z_j} V_j / sum_j e^{z_j}    (j < len)
+//
+// Memory-bound: every cached row is read once and used by the G query heads of
+// its group.  The work of all sequences is cut into equal shares, whatever
+// their lengths: the tiles of 64 tokens of every (sequence, key-value head,
+// block of query heads) form one line, and CTA c of a grid that fills the GPU
+// once takes the tiles from U c / grid to U (c + 1) / grid.  A CTA holds a
+// running maximum, sum and weighted sum per query head (base 2) while it stays
+// within one (sequence, head) item; an item that lies in one CTA is written
+// out there, and an item that several share leaves one partial result per CTA
+// (at most two per CTA: its first and its last item) for a second kernel to
+// join.  No atomics: the same lengths give the same bits.
+//
+// Within a tile each of the CTA's 4 warps takes 16 tokens (one page holds
+// them) and keeps its own running state, so the main loop has no barrier; the
+// warps' states are joined when the CTA leaves an item.
+#include <algorithm>
+#include <cstdint>
+#include <cuda_bf16.h>
+
+#include "kda_internal.cuh"
+#include "tc_ptx.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kTile = 64, kWarps = 4, kThreads = 32 * kWarps, kWarpTokens = 16;
+constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// ---------------------------------------------------------------------------
+// the line of tiles
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ int32_t clamp_len(const AttnStepArgs &a, int32_t s) {
+    return min(max(a.seq_lens[s], 0), a.max_pages << a.page_shift);
+}
+__device__ __forceinline__ int32_t tiles_of(int32_t len) { return (len + kTile - 1) / kTile; }
+
+// Prefix sums of the sequences' tiles, each thread holding a run of sequences.
+template <int THREADS>
+struct Line {
+    int64_t total;   // tiles of all sequences
+    int64_t before;  // tiles before this thread's run
+    int32_t s0, s1;  // this thread's run
+    __device__ void scan(const AttnStepArgs &a, int64_t *sm /* [THREADS / 32] */) {
+        const int tid = threadIdx.x, lane = tid & 31;
+        const int32_t per = (a.N + THREADS - 1) / THREADS;
+        s0 = min(tid * per, a.N);
+        s1 = min(s0 + per, a.N);
+        int64_t mine = 0;
+        for (int32_t s = s0; s < s1; ++s) {
+            mine += tiles_of(clamp_len(a, s));
+            if (a.seq_lens[s] > (a.max_pages << a.page_shift)) *a.status = KDA_ERR_INVALID_ARG;
+        }
+        int64_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        if (lane == 31) sm[tid >> 5] = incl;
+        __syncthreads();
+        before = incl - mine;
+        total = 0;
+        for (int w = 0; w < THREADS / 32; ++w) {
+            if (w < (tid >> 5)) before += sm[w];
+            total += sm[w];
+        }
+    }
+    // The sequence of unit u (u < total * items) and the units before it, to
+    // *seq / *base in shared memory.
+    __device__ void find(const AttnStepArgs &a, int64_t u, int32_t items, int32_t *seq,
+                         int64_t *base) const {
+        int64_t b = before * items;
+        if (u >= b) {
+            for (int32_t s = s0; s < s1; ++s) {
+                const int64_t n = (int64_t)tiles_of(clamp_len(a, s)) * items;
+                if (u < b + n) {
+                    *seq = s;
+                    *base = b;
+                    break;
+                }
+                b += n;
+            }
+        }
+        __syncthreads();
+    }
+};
+
+__device__ __forceinline__ int64_t share_start(int64_t units, int32_t c, int32_t grid) {
+    return units * c / grid;
+}
+
+// ---------------------------------------------------------------------------
+// CUDA-core core: fp32 arithmetic, 4 query heads, any supported type and width
+// ---------------------------------------------------------------------------
+// A lane owns 8 channels; D / 8 lanes make a token, 256 / D tokens a step.
+// Every group of D / 8 lanes keeps its own running state over its tokens.
+template <typename T, int D>
+struct SimtCore {
+    using Type = T;
+    static constexpr int kD = D, kRows = 4, kCtas = 3;
+    static constexpr int LPT = D / 8, TPW = 32 / LPT;
+    // tokens whose keys and values are in flight together: 16, or 8 where 16
+    // would take 128 registers
+    static constexpr int NB = (sizeof(T) == 4 && D == 128) ? 4 : kWarpTokens / TPW;
+    static constexpr int RAW = sizeof(T) / 2;  // 16-byte vectors per lane and token
+
+    float q[kRows][8], acc[kRows][8], m[kRows], l[kRows];
+    float c2;
+
+    __device__ static void unpack(const uint4 (&x)[RAW], float (&f)[8]) {
+#pragma unroll
+        for (int i = 0; i < RAW; ++i) {
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (sizeof(T) == 4) {
+                    f[4 * i + j] = __uint_as_float(w[j]);
+                } else {
+                    f[2 * j] = __uint_as_float(w[j] << 16);
+                    f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+                }
+            }
+        }
+    }
+    __device__ void init(const T *qp, int rows, float scale) {
+        const int cl = (threadIdx.x & 31) % LPT;
+        c2 = scale * kLog2e;
+#pragma unroll
+        for (int h = 0; h < kRows; ++h) {
+            uint4 x[RAW];
+#pragma unroll
+            for (int i = 0; i < RAW; ++i)
+                x[i] = h < rows ? *(reinterpret_cast<const uint4 *>(qp + h * D + cl * 8) + i)
+                                : make_uint4(0, 0, 0, 0);
+            unpack(x, q[h]);
+            m[h] = -INFINITY;
+            l[h] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[h][j] = 0.f;
+        }
+    }
+    // `n` (1..16) tokens whose rows start at kp / vp
+    __device__ void tile(const T *kp, const T *vp, int n) {
+        const int lane = threadIdx.x & 31, cl = lane % LPT, sub = lane / LPT;
+#pragma unroll 1
+        for (int b = 0; b < kWarpTokens; b += NB * TPW) {
+            if (b >= n) break;
+            uint4 kr[NB][RAW], vr[NB][RAW];
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int t = b + i * TPW + sub;
+#pragma unroll
+                for (int r = 0; r < RAW; ++r) {
+                    kr[i][r] = t < n ? *(reinterpret_cast<const uint4 *>(kp + t * D + cl * 8) + r)
+                                     : make_uint4(0, 0, 0, 0);
+                    vr[i][r] = t < n ? *(reinterpret_cast<const uint4 *>(vp + t * D + cl * 8) + r)
+                                     : make_uint4(0, 0, 0, 0);
+                }
+            }
+            float s[kRows][NB];
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                float f[8];
+                unpack(kr[i], f);
+#pragma unroll
+                for (int h = 0; h < kRows; ++h) {
+                    float d = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) d = fmaf(q[h][j], f[j], d);
+                    s[h][i] = d;
+                }
+            }
+#pragma unroll
+            for (int o = 1; o < LPT; o <<= 1)
+#pragma unroll
+                for (int h = 0; h < kRows; ++h)
+#pragma unroll
+                    for (int i = 0; i < NB; ++i)
+                        s[h][i] += __shfl_xor_sync(0xffffffffu, s[h][i], o);
+#pragma unroll
+            for (int h = 0; h < kRows; ++h) {
+                float mx = m[h];
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    if (b + i * TPW + sub >= n) s[h][i] = -INFINITY;
+                    mx = fmaxf(mx, s[h][i]);
+                }
+                const float ref = mx == -INFINITY ? 0.f : mx;
+                const float corr = exp2f((m[h] - ref) * c2);
+                m[h] = mx;
+                l[h] *= corr;
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    s[h][i] = exp2f((s[h][i] - ref) * c2);
+                    l[h] += s[h][i];
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[h][j] *= corr;
+            }
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                float f[8];
+                unpack(vr[i], f);
+#pragma unroll
+                for (int h = 0; h < kRows; ++h)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) acc[h][j] = fmaf(s[h][i], f[j], acc[h][j]);
+            }
+        }
+    }
+    // the warp's state: weighted sums [kRows][D], maxima (base 2) and sums [kRows]
+    __device__ void finish(float *sacc, float *sm, float *sl) {
+        const int lane = threadIdx.x & 31, cl = lane % LPT, sub = lane / LPT;
+#pragma unroll
+        for (int h = 0; h < kRows; ++h) {
+            float mx = m[h];
+#pragma unroll
+            for (int o = LPT; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float w = mx == -INFINITY ? 0.f : exp2f((m[h] - mx) * c2);
+            float sum = l[h] * w;
+#pragma unroll
+            for (int o = LPT; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float x = acc[h][j] * w;
+#pragma unroll
+                for (int o = LPT; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                if (sub == 0) sacc[h * D + cl * 8 + j] = x;
+            }
+            if (lane == 0) {
+                sm[h] = mx * c2;
+                sl[h] = sum;
+            }
+        }
+    }
+};
+
+// ---------------------------------------------------------------------------
+// the kernels
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void store_out(const AttnStepArgs &a, int64_t i, float y) {
+    if (a.out_f32) static_cast<float *>(a.out)[i] = y;
+    else static_cast<__nv_bfloat16 *>(a.out)[i] = __float2bfloat16_rn(y);
+}
+
+template <class Core>
+__global__ void __launch_bounds__(kThreads, Core::kCtas)
+attn_step_kernel(const AttnStepArgs a, float *part) {
+    using T = typename Core::Type;
+    constexpr int D = Core::kD, R = Core::kRows;
+    __shared__ float s_acc[kWarps][R * D], s_m[kWarps][R], s_l[kWarps][R];
+    __shared__ int64_t s_scan[kWarps], s_base;
+    __shared__ int32_t s_seq;
+    const int tid = threadIdx.x, warp = tid >> 5;
+    tc::pdl_launch_dependents();
+    const int32_t blocks = (a.G + R - 1) / R;  // blocks of query heads
+    const int32_t items = a.HKV * blocks;
+    Line<kThreads> line;
+    line.scan(a, s_scan);
+    const int64_t units = line.total * items;
+    const int32_t grid = (int32_t)gridDim.x, c = (int32_t)blockIdx.x;
+    // sequences without keys
+    for (int32_t s = c; s < a.N; s += grid) {
+        if (clamp_len(a, s) > 0) continue;
+        for (int32_t i = tid; i < a.HQ * D; i += kThreads) store_out(a, (int64_t)s * a.HQ * D + i, 0.f);
+        if (a.lse)
+            for (int32_t i = tid; i < a.HQ; i += kThreads) a.lse[(int64_t)s * a.HQ + i] = -INFINITY;
+    }
+    const int64_t u0 = share_start(units, c, grid), u1 = share_start(units, c + 1, grid);
+    if (u0 >= u1) return;
+    line.find(a, u0, items, &s_seq, &s_base);
+    int32_t s = s_seq;
+    int64_t base = s_base;
+    Core core;
+    for (int64_t u = u0; u < u1;) {
+        const int32_t len = clamp_len(a, s), tiles = tiles_of(len);
+        if (u >= base + (int64_t)tiles * items) {
+            base += (int64_t)tiles * items;
+            ++s;
+            continue;
+        }
+        const int32_t item = (int32_t)((u - base) / tiles);
+        const int32_t tile0 = (int32_t)((u - base) - (int64_t)item * tiles);
+        const int32_t tile1 = (int32_t)min((int64_t)tiles, tile0 + (u1 - u));
+        const int32_t kvh = item / blocks, h0 = (item - kvh * blocks) * R;
+        const int32_t rows = min(R, a.G - h0);
+        const int64_t head = (int64_t)kvh * a.G + h0;
+        core.init(static_cast<const T *>(a.q) + s * a.q_stride + head * D, rows, a.scale);
+        const int32_t *table = a.block_table + (int64_t)s * a.max_pages;
+        for (int32_t t = tile0; t < tile1; ++t) {
+            const int32_t tok = t * kTile + warp * kWarpTokens;
+            if (tok >= len) break;
+            const int32_t page = table[tok >> a.page_shift];
+            if (page < 0 || page >= a.num_pages) {
+                *a.status = KDA_ERR_INVALID_ARG;
+                continue;
+            }
+            const int64_t row = (((int64_t)page * a.HKV + kvh) << a.page_shift) +
+                                (tok & ((1 << a.page_shift) - 1));
+            core.tile(static_cast<const T *>(a.k_cache) + row * D,
+                      static_cast<const T *>(a.v_cache) + row * D, min(kWarpTokens, len - tok));
+        }
+        core.finish(s_acc[warp], s_m[warp], s_l[warp]);
+        __syncthreads();
+        // join the warps
+        const bool whole = tile0 == 0 && tile1 == tiles;
+        float *slot = part + ((int64_t)c * 2 + (u == u0 ? 0 : 1)) * (R * (D + 2));
+        for (int i = tid; i < rows * D; i += kThreads) {
+            const int r = i / D, col = i % D;
+            float mx = s_m[0][r];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][r]);
+            const float ref = mx == -INFINITY ? 0.f : mx;
+            float o = 0.f, l = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = exp2f(s_m[w][r] - ref);
+                o += s_acc[w][i] * f;
+                l += s_l[w][r] * f;
+            }
+            if (whole) {
+                store_out(a, ((int64_t)s * a.HQ + head + r) * D + col, l == 0.f ? 0.f : o / l);
+                if (a.lse && col == 0)
+                    a.lse[(int64_t)s * a.HQ + head + r] = l == 0.f ? -INFINITY
+                                                                 : (mx + log2f(l)) * kLn2;
+            } else {
+                slot[i] = o;
+                if (col == 0) {
+                    slot[R * D + r] = mx;
+                    slot[R * D + R + r] = l;
+                }
+            }
+        }
+        __syncthreads();
+        u += tile1 - tile0;
+    }
+}
+
+// Joins the items that several CTAs of the step share: CTA (c, r) handles
+// query head r of the item that CTA c of the step is the second to work on.
+template <int D, int R>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnStepArgs a,
+                                                                 const float *part, int32_t grid) {
+    __shared__ int64_t s_scan[kJoinWarps], s_base;
+    __shared__ int32_t s_seq;
+    __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int32_t blocks = (a.G + R - 1) / R, items = a.HKV * blocks;
+    Line<kJoinThreads> line;
+    line.scan(a, s_scan);
+    const int64_t units = line.total * items;
+    const int32_t c = (int32_t)blockIdx.x + 1;
+    const int64_t start = share_start(units, c, grid);
+    const bool any = start < units;
+    if (any) line.find(a, start, items, &s_seq, &s_base);
+    // every CTA waits for the step to end, so that whatever follows this
+    // kernel in the stream also follows the step
+    tc::pdl_wait_primaries();
+    if (!any) return;
+    const int32_t s = s_seq;
+    const int32_t tiles = tiles_of(clamp_len(a, s));
+    const int32_t item = (int32_t)((start - s_base) / tiles);
+    const int64_t first = s_base + (int64_t)item * tiles, last = first + tiles;  // the item's units
+    if (start == first || share_start(units, c - 1, grid) > first) return;
+    const int32_t kvh = item / blocks, h0 = (item - kvh * blocks) * R, r = blockIdx.y;
+    if (h0 + r >= a.G) return;
+    float mx = -INFINITY, l = 0.f, o[(D + 31) / 32];
+#pragma unroll
+    for (int j = 0; j < (D + 31) / 32; ++j) o[j] = 0.f;
+    // this warp's CTAs of the step: c - 1 + warp, then every kJoinWarps-th
+    for (int32_t i = c - 1 + warp; i < grid; i += kJoinWarps) {
+        const int64_t b = share_start(units, i, grid);
+        if (b >= last) break;
+        if (i >= c && b >= share_start(units, i + 1, grid)) continue;  // an empty share
+        const float *slot = part + ((int64_t)i * 2 + ((i == c - 1 && b != first) ? 1 : 0)) *
+                                       (R * (D + 2));
+        const float sm = slot[R * D + r], sl = slot[R * D + R + r];
+        float x[(D + 31) / 32];
+#pragma unroll
+        for (int j = 0; j < (D + 31) / 32; ++j)
+            x[j] = (D >= 32 || lane < D) ? slot[r * D + j * 32 + lane] : 0.f;
+        const float nm = fmaxf(mx, sm), ref = nm == -INFINITY ? 0.f : nm;
+        const float f0 = exp2f(mx - ref), f1 = exp2f(sm - ref);
+        mx = nm;
+        l = l * f0 + sl * f1;
+#pragma unroll
+        for (int j = 0; j < (D + 31) / 32; ++j) o[j] = o[j] * f0 + x[j] * f1;
+    }
+#pragma unroll
+    for (int j = 0; j < (D + 31) / 32; ++j)
+        if (D >= 32 || lane < D) s_o[warp][j * 32 + lane] = o[j];
+    if (lane == 0) {
+        s_m[warp] = mx;
+        s_l[warp] = l;
+    }
+    __syncthreads();
+    for (int col = tid; col < D; col += kJoinThreads) {
+        float m = s_m[0];
+#pragma unroll
+        for (int w = 1; w < kJoinWarps; ++w) m = fmaxf(m, s_m[w]);
+        const float ref = m == -INFINITY ? 0.f : m;
+        float y = 0.f, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            const float f = exp2f(s_m[w] - ref);
+            y += s_o[w][col] * f;
+            sum += s_l[w] * f;
+        }
+        const int64_t head = (int64_t)s * a.HQ + (int64_t)kvh * a.G + h0 + r;
+        store_out(a, head * D + col, sum == 0.f ? 0.f : y / sum);
+        if (a.lse && col == 0) a.lse[head] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+    }
+}
+
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return n;
+}
+
+template <class Core>
+cudaError_t launch_core(const AttnStepArgs &a, cudaStream_t stream) {
+    constexpr int D = Core::kD, R = Core::kRows;
+    const int sms = sm_count();
+    if (!sms) return cudaErrorUnknown;
+    // no more CTAs than the longest possible line has tiles
+    const int64_t most = (int64_t)a.N * a.HKV * ((a.G + R - 1) / R) *
+                         (((int64_t)a.max_pages << a.page_shift) / kTile + 1);
+    const int grid = (int)std::min<int64_t>((int64_t)sms * Core::kCtas, std::max<int64_t>(most, 1));
+    float *part = static_cast<float *>(a.workspace);
+    attn_step_kernel<Core><<<grid, kThreads, 0, stream>>>(a, part);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || grid == 1) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)std::min<int32_t>(R, a.G));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<D, R>, a, static_cast<const float *>(part),
+                              (int32_t)grid);
+}
+
+// The core of a problem, as a call of f.template operator()<Core>().
+template <class F>
+auto with_core(int32_t D, int32_t G, int32_t dtype, F f) {
+    (void)G;
+    if (dtype == KDA_DTYPE_BF16) {
+        switch (D) {
+            case 16: return f(SimtCore<__nv_bfloat16, 16>{});
+            case 32: return f(SimtCore<__nv_bfloat16, 32>{});
+            case 64: return f(SimtCore<__nv_bfloat16, 64>{});
+            default: return f(SimtCore<__nv_bfloat16, 128>{});
+        }
+    }
+    switch (D) {
+        case 16: return f(SimtCore<float, 16>{});
+        case 32: return f(SimtCore<float, 32>{});
+        case 64: return f(SimtCore<float, 64>{});
+        default: return f(SimtCore<float, 128>{});
+    }
+}
+
+}  // namespace
+
+size_t attn_step_workspace_bytes(int32_t D, int32_t G, int32_t dtype) {
+    const int sms = sm_count();
+    return with_core(D, G, dtype, [&](auto core) -> size_t {
+        using Core = decltype(core);
+        return (size_t)sms * Core::kCtas * 2 * Core::kRows * (Core::kD + 2) * sizeof(float);
+    });
+}
+
+cudaError_t launch_attn_step(const AttnStepArgs &a, cudaStream_t stream) {
+    return with_core(a.D, a.G, a.dtype, [&](auto core) -> cudaError_t {
+        return launch_core<decltype(core)>(a, stream);
+    });
+}
+
+}  // namespace kda

@@ -175,6 +175,59 @@ struct ConvArgs {
 };
 cudaError_t launch_short_conv(const ConvArgs &a, cudaStream_t stream);
 
+// The full-attention layer (kda_attn_api.cu validates; strides in elements,
+// never 0 here).
+struct AttnArgs {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t *cu_seqlens;     // device [N + 1] or nullptr (one sequence)
+    float scale;
+    void *out;                     // [T, HQ, D]
+    float *lse;                    // [T, HQ] or nullptr
+    int32_t N, T, HQ, HKV, G, D;   // G = HQ / HKV
+    int32_t dtype, out_f32;
+    int *status;
+};
+cudaError_t launch_attn_simt(const AttnArgs &a, cudaStream_t stream);
+
+struct AppendArgs {
+    const void *q, *k, *v;         // q may be nullptr
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t *cu_seqlens;     // nullptr: see one_each
+    int32_t one_each;              // no offsets: token t is sequence t (else one sequence)
+    const int32_t *cache_lens;     // [N]
+    const float *rope;             // [P, rot] or nullptr
+    int32_t positions, rot, interleaved;
+    void *q_out, *k_out;           // may be nullptr
+    void *k_cache, *v_cache;
+    const int32_t *block_table;
+    int32_t num_pages, page_shift, max_pages;
+    int32_t N, T, HQ, HKV, D, dtype;
+    int *status;
+};
+cudaError_t launch_cache_append(const AppendArgs &a, cudaStream_t stream);
+
+struct AttnStepArgs {
+    const void *q;
+    int64_t q_stride;
+    const void *k_cache, *v_cache;
+    const int32_t *block_table;
+    int32_t num_pages, page_shift, max_pages;
+    const int32_t *seq_lens;       // [N]
+    float scale;
+    void *out;                     // [N, HQ, D]
+    float *lse;                    // [N, HQ] or nullptr
+    int32_t N, HQ, HKV, G, D, dtype, out_f32;
+    void *workspace;
+    int *status;
+};
+// Scratch of the step on the current device (0: the query failed).
+size_t attn_step_workspace_bytes(int32_t D, int32_t G, int32_t dtype);
+cudaError_t launch_attn_step(const AttnStepArgs &a, cudaStream_t stream);
+
+// Device address of the status word on the current device (kda_api.cu).
+int *device_status_word();
+
 // fp32 CUDA-core chunk engine (kda_chunk_simt.cu).  Needs no scratch.
 cudaError_t launch_chunk_simt(const ChunkArgs &a, cudaStream_t stream);
 
