@@ -119,7 +119,9 @@ kdaStatus_t kda_attn_fwd(const void *q, const void *k, const void *v, float scal
         for (const void *p : vec)
             if (!p || !aligned(p, 16)) return KDA_ERR_INVALID_ARG;
     }
-    if (shape->engine == KDA_ENGINE_TENSOR) return KDA_ERR_UNSUPPORTED;
+    const bool tensor_ok = shape->dtype == KDA_DTYPE_BF16 &&
+                           (shape->head_dim == 64 || shape->head_dim == 128);
+    if (shape->engine == KDA_ENGINE_TENSOR && !tensor_ok) return KDA_ERR_UNSUPPORTED;
     if (shape->total_tokens == 0) return KDA_SUCCESS;
     AttnArgs a;
     a.q = q; a.k = k; a.v = v;
@@ -133,7 +135,8 @@ kdaStatus_t kda_attn_fwd(const void *q, const void *k, const void *v, float scal
     a.out_f32 = shape->dtype == KDA_DTYPE_F32 ? 1 : shape->out_f32;
     a.status = device_status_word();
     if (!a.status) return cuda_status(cudaErrorUnknown);
-    return cuda_status(launch_attn_simt(a, stream));
+    return cuda_status(tensor_ok && shape->engine != KDA_ENGINE_SIMT ? launch_attn_tc(a, stream)
+                                                                     : launch_attn_simt(a, stream));
 }
 
 kdaStatus_t kda_cache_append(const void *q, const void *k, const void *v,

@@ -1,0 +1,595 @@
+// kda_attn_tc.cu -- causal attention over packed prompts on the tensor cores:
+// bf16, head width D = 64 or 128.
+//
+//     z_ij = scale <q_i, k_j>  (j <= i),   o_i = sum_j e^{z_ij} v_j / sum_j e^{z_ij}
+//
+// One pass over the keys with a running reference and sum per row, in base 2.
+// The rows of a tile are (token, query head) pairs of one key-value head:
+// R = floor(128 / G) tokens times the G heads of a group, brought in by one
+// tensor copy, so that grouped heads share every key and value tile.
+//
+// A CTA owns two such tiles of 128 rows (consecutive tokens) and walks the
+// keys in tiles of 128.  Per row tile t and key tile j:
+//
+//     S_t = Q_t K_j^T          tcgen05, operands in shared memory, D in TMEM
+//     P_t = 2^{c S_t - ref}    one thread per row; bf16, over S_t's columns
+//     O_t (+)= P_t V_j         tcgen05, A = P_t from TMEM, V_j as it lies
+//
+// The two row tiles alternate: while the softmax of one runs, the tensor core
+// works for the other.  Warps: 0-3 and 4-7 the softmax of tile 0 and 1, 8-11
+// rescale the O_t when a row's reference moves and write the results, 12
+// issues the MMAs, 13 the copies, 14-15 make masked values harmless.
+//
+// The reference of a row moves only when the row's maximum has passed it by
+// more than 2^8: until then the weights stay below 2^8, which costs fp32 sums
+// nothing and bf16 weights no precision (a floating-point scale), and the
+// rescaling of O_t (a read and write of 128 x D fp32) is left out.
+//
+// The weights are rounded to bf16 for the tensor core (relative 2^-8, the
+// operand type of V); their sum is taken in fp32 before the rounding.
+//
+// Masked places: scores are masked by selection, so masked keys are free to
+// hold anything.  A masked weight is an exact 0, but 0 times an infinity or a
+// NaN in a value row is NaN: warps 14-15 look through every value tile that
+// holds a masked place before the MMA reads it, set the rows behind the CTA's
+// last token to zero and replace non-finite values by zero; if there were
+// any, the rows that do see them get them added at the end (`bad`).
+//
+// Waits are bounded: one that gives up sets KDA_ERR_TIMEOUT in the status
+// word, every role leaves its loop, and the CTA ends after its copies and
+// MMAs in flight.
+#include <cstdint>
+#include <cstring>
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "kda_attn_common.cuh"
+#include "tc_ptx.cuh"
+
+namespace kda {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 512;
+constexpr int kRowTile = 128, kKeyTile = 128;
+constexpr long long kWaitLimit = 2000000000LL;  // SM clocks, about a second
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kMoveBy = 8.f;  // powers of two a row's maximum may pass its reference by
+
+template <int D>
+struct Cfg {
+    static constexpr int PANELS = D / 64;                 // 128-byte column panels
+    static constexpr uint32_t PANEL = kRowTile * 128;     // bytes
+    static constexpr uint32_t TILE = PANELS * PANEL;      // one Q, K or V tile
+    static constexpr int STAGES = D == 128 ? 5 : 8;       // K and V tiles in flight
+    static constexpr uint32_t S_COL = 128, O_BASE = 256;  // TMEM columns: S_0, S_1, O_0, O_1
+    static constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, kKeyTile);
+    static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D) | (1u << 16);  // V is N-major
+};
+
+struct Shared {
+    uint64_t q_full[2], kv_full[8], kv_empty[8], v_raw[3], v_half[3];
+    uint64_t s_full[2], p_full[2], m_ready[2], o_ready[2], pv_done[2], drained;
+    uint32_t tmem;
+    int32_t found, abort, bad;
+    SeqTile tile;
+    float scale[2][kRowTile], sum[2][kRowTile];
+};
+
+// The tiles start at the dynamic shared memory's base, which is 1024-byte
+// aligned (the kernel has no other shared memory); Shared follows them.
+template <int D>
+constexpr uint32_t smem_bytes() {
+    return (2 + Cfg<D>::STAGES) * Cfg<D>::TILE + (uint32_t)sizeof(Shared);
+}
+static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "227 KB per CTA");
+
+// O[128 x N] (+)= P[128 x 16 steps] V: A from TMEM
+__device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Descriptor of an N-major tile with the 128-byte swizzle: 64 columns to a
+// panel, panels PANEL bytes apart (leading offset), 8 rows 1024 bytes (stride
+// offset).
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t panel) {
+    return sdesc_sw128(saddr) & ~(0x3FFFull << 16) | (static_cast<uint64_t>(panel >> 4) << 16);
+}
+
+// 32 columns of TMEM in flight; the wait names the registers, so that nothing
+// reads them before it.
+__device__ __forceinline__ void ld32_nowait(uint32_t taddr, float *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+          "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+          "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
+          "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
+          "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void wait_ld32(float *v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                   "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
+                   "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]),
+                   "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                   "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
+                   "+f"(v[30]), "+f"(v[31])::"memory");
+}
+__device__ __forceinline__ void st16_nowait(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+        "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ float2 f2_add(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// What the CTA works on.
+struct Job {
+    int32_t len;        // tokens of the sequence
+    int32_t q0[2];      // first token of each row tile
+    int32_t nt[2];      // tokens of each row tile (0: none)
+    int32_t nk[2];      // key tiles of each row tile
+    int32_t n;          // key tiles of the CTA
+    int32_t last;       // the CTA's last token
+    int32_t first_mask; // first key tile with a masked place
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+               const __grid_constant__ CUtensorMap map_v, const AttnArgs a) {
+    using C = Cfg<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *sq = smem, *skv = smem + 2 * C::TILE;
+    Shared &sh = *reinterpret_cast<Shared *>(skv + C::STAGES * C::TILE);
+    if (smem_u32(smem) & 1023u) {  // the swizzled tiles would not match their descriptors
+        *a.status = KDA_ERR_CUDA;
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int32_t R = kRowTile / a.G;  // tokens of a row tile
+
+    if (warp == 0) {
+        SeqTile t;
+        const bool ok = find_seq_tile(a.cu_seqlens, a.N, a.T, 1, 2 * R, blockIdx.x / a.HKV, t);
+        if (lane == 0) {
+            sh.found = ok;
+            if (ok) sh.tile = t;
+            sh.abort = 0;
+            sh.bad = 0;
+        }
+    } else if (warp == 1 && lane == 0) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&sh.q_full[t], 1);
+            mbar_init(&sh.s_full[t], 1);
+            mbar_init(&sh.p_full[t], 4);
+            mbar_init(&sh.m_ready[t], 4);
+            mbar_init(&sh.o_ready[t], 4);
+            mbar_init(&sh.pv_done[t], 1);
+        }
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(&sh.kv_full[i], 1);
+            mbar_init(&sh.kv_empty[i], 1);
+        }
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&sh.v_raw[i], 1);
+            mbar_init(&sh.v_half[i], 2);
+        }
+        mbar_init(&sh.drained, 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    if (!sh.found) return;
+    if (warp == 12) {
+        tmem_alloc(&sh.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const int32_t kvh = blockIdx.x % a.HKV, begin = sh.tile.begin;
+    Job job;
+    job.len = sh.tile.end - begin;
+    job.n = 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        job.q0[t] = (sh.tile.tile * 2 + t) * R;
+        job.nt[t] = min(max(job.len - job.q0[t], 0), R);
+        job.nk[t] = job.nt[t] > 0 ? (job.q0[t] + job.nt[t] - 1) / kKeyTile + 1 : 0;
+        job.n = max(job.n, job.nk[t]);
+    }
+    job.last = min(job.q0[0] + 2 * R, job.len) - 1;
+    job.first_mask = (job.q0[0] + 1) / kKeyTile;
+
+    auto wait = [&](uint64_t *bar, uint32_t phase) -> bool {
+        if (mbar_wait_bounded(bar, phase & 1, kWaitLimit)) return true;
+        sh.abort = 1;
+        *a.status = KDA_ERR_TIMEOUT;
+        return false;
+    };
+    // the same for a whole warp, which leaves it together
+    auto wait_warp = [&](uint64_t *bar, uint32_t phase) -> bool {
+        const bool ok = wait(bar, phase);
+        return __all_sync(0xffffffffu, ok && !*static_cast<volatile int32_t *>(&sh.abort));
+    };
+
+    if (warp < 8) {
+        // ---- softmax: one thread per row --------------------------------
+        regs_inc<192>();
+        const int t = warp >> 2, row = tid & 127;
+        const uint32_t lane_base = (uint32_t)(warp & 3) * 32;
+        const uint32_t s_addr = tmem_addr(tmem, lane_base, t * C::S_COL);
+        const int32_t tok = job.q0[t] + row / a.G;
+        const float c2 = a.scale * kLog2e;
+        const int32_t n = t == 0 ? job.nk[0] : job.nk[1];
+        float ref = -INFINITY, sum = 0.f;  // the reference times c2
+        for (int32_t j = 0; j < n; ++j) {
+            if (!wait_warp(&sh.s_full[t], j)) break;
+            tc_fence_after();
+            float s[128];
+            ld32_nowait(s_addr, s);
+            ld32_nowait(s_addr + 32, s + 32);
+            ld32_nowait(s_addr + 64, s + 64);
+            ld32_nowait(s_addr + 96, s + 96);
+            wait_ld32(s);
+            wait_ld32(s + 32);
+            wait_ld32(s + 64);
+            wait_ld32(s + 96);
+            const int32_t seen = tok - j * kKeyTile;  // columns up to this one are seen
+            if ((j + 1) * kKeyTile - 1 > job.q0[t]) {
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    if (i > seen) s[i] = -INFINITY;
+            }
+            float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
+#pragma unroll
+            for (int i = 4; i < 128; i += 4) {
+                m0 = fmaxf(m0, s[i]);
+                m1 = fmaxf(m1, s[i + 1]);
+                m2 = fmaxf(m2, s[i + 2]);
+                m3 = fmaxf(m3, s[i + 3]);
+            }
+            const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * c2;
+            if (!(top - ref <= kMoveBy)) {  // also on the first tile
+                const float next = fmaxf(ref, top);
+                // a row whose scores are all -inf so far keeps weights of 0
+                const float to = next == -INFINITY ? 0.f : next;
+                const float f = exp2_approx(ref - to);
+                if (j > 0) sh.scale[t][row] = f;
+                sum *= f;
+                ref = next;
+            } else if (j > 0) {
+                sh.scale[t][row] = 1.f;
+            }
+            __syncwarp();
+            if (j > 0 && lane == 0) mbar_arrive(&sh.m_ready[t]);
+            __syncwarp();
+            const float neg = ref == -INFINITY ? 0.f : -ref;
+            const float2 c22 = make_float2(c2, c2), neg2 = make_float2(neg, neg);
+            float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                uint32_t p[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float2 x = f2_fma(make_float2(s[h * 32 + 2 * i], s[h * 32 + 2 * i + 1]), c22, neg2);
+                    x.x = exp2_approx(x.x);
+                    x.y = exp2_approx(x.y);
+                    if (i & 1) acc1 = f2_add(acc1, x);
+                    else acc0 = f2_add(acc0, x);
+                    p[i] = pack_bf16x2(x.x, x.y);
+                }
+                st16_nowait(s_addr + h * 16, p);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full[t]);
+            __syncwarp();
+            acc0 = f2_add(acc0, acc1);
+            sum += acc0.x + acc0.y;
+        }
+        if (n > 0) {
+            sh.sum[t][row] = sum;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.m_ready[t]);
+            const int tk = row / a.G;
+            if (a.lse && tk < (t == 0 ? job.nt[0] : job.nt[1]))
+                a.lse[((int64_t)begin + tok) * a.HQ + (int64_t)kvh * a.G + (row - tk * a.G)] =
+                    (ref + log2f(sum)) * kLn2;
+        }
+    } else if (warp < 12) {
+        // ---- rescaling and results --------------------------------------
+        regs_dec<80>();
+        const int row = tid & 127;
+        const uint32_t lane_base = (uint32_t)(warp & 3) * 32;
+        bool ok = true;
+        for (int32_t j = 1; j < job.n && ok; ++j) {
+#pragma unroll 1
+            for (int t = 0; t < 2 && ok; ++t) {
+                if (j >= job.nk[t]) continue;
+                ok = wait_warp(&sh.m_ready[t], j - 1);
+                if (!ok) break;
+                const float f = sh.scale[t][row];
+                if (__any_sync(0xffffffffu, f != 1.f)) {
+                    ok = wait_warp(&sh.pv_done[t], j - 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t o = tmem_addr(tmem, lane_base, C::O_BASE + t * D);
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        float x[32];
+                        ld32_nowait(o + c, x);
+                        wait_ld32(x);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] *= f;
+                        tmem_st32(o + c, x);
+                    }
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.o_ready[t]);
+                __syncwarp();
+            }
+        }
+#pragma unroll 1
+        for (int t = 0; t < 2 && ok; ++t) {
+            const int32_t n = job.nk[t];
+            if (n == 0) continue;
+            ok = wait_warp(&sh.m_ready[t], n - 1) && wait_warp(&sh.pv_done[t], n - 1);
+            if (!ok) break;
+            tc_fence_after();
+            const int32_t tk = row / a.G;
+            const float inv = 1.f / sh.sum[t][row];
+            const int64_t token = (int64_t)begin + job.q0[t] + tk;
+            const int64_t head = (int64_t)kvh * a.G + (row - tk * a.G);
+            const bool mine = tk < job.nt[t];
+            const uint32_t o = tmem_addr(tmem, lane_base, C::O_BASE + t * D);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                float x[32];
+                __syncwarp();  // the load is the whole warp's
+                ld32_nowait(o + c, x);
+                wait_ld32(x);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] *= inv;
+                if (!mine) continue;
+                if (sh.bad) {
+                    // non-finite values of the tiles that were looked through
+                    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) +
+                                             (int64_t)begin * a.v_stride + (int64_t)kvh * D + c;
+                    for (int32_t k = job.first_mask * kKeyTile; k <= job.q0[t] + tk; ++k)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float y = __bfloat162float(v[k * a.v_stride + i]);
+                            if (!isfinite(y)) x[i] += y;
+                        }
+                }
+                const int64_t at = (token * a.HQ + head) * D + c;
+                if (a.out_f32) {
+                    float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                } else {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        dst[i] = make_uint4(pack_bf16x2(x[8 * i], x[8 * i + 1]),
+                                            pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
+                                            pack_bf16x2(x[8 * i + 4], x[8 * i + 5]),
+                                            pack_bf16x2(x[8 * i + 6], x[8 * i + 7]));
+                }
+            }
+        }
+    } else {
+        regs_dec<48>();
+        if (warp == 12) {
+            // ---- MMAs ---------------------------------------------------
+            if (lane == 0) {
+                const uint32_t q_base = smem_u32(sq), kv_base = smem_u32(skv);
+                auto scores = [&](int t, uint32_t stage) {
+                    mma_panels(tmem + t * C::S_COL, q_base + t * C::TILE, C::PANEL,
+                               kv_base + stage * C::TILE, C::PANEL, D / 16, C::IDESC_QK, false);
+                    mma_commit(&sh.s_full[t]);
+                };
+                bool ok = true;
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (job.nk[t] == 0) continue;
+                    ok = wait(&sh.q_full[t], 0) && (t > 0 || wait(&sh.kv_full[0], 0));
+                    if (!ok) break;
+                    tc_fence_after();
+                    scores(t, 0);
+                }
+                if (ok) mma_commit(&sh.kv_empty[0]);
+                for (int32_t j = 0; j < job.n && ok; ++j) {
+                    const uint32_t ev = 2 * j + 1, ek = 2 * j + 2;
+                    const uint32_t sv = ev % C::STAGES, sk = ek % C::STAGES;
+                    ok = wait(&sh.kv_full[sv], ev / C::STAGES);
+                    if (!ok) break;
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        if (j >= job.nk[t]) continue;
+                        ok = wait(&sh.p_full[t], j) && (j == 0 || wait(&sh.o_ready[t], j - 1));
+                        if (!ok || sh.abort) break;
+                        tc_fence_after();
+                        const uint32_t v = kv_base + sv * C::TILE;
+#pragma unroll
+                        for (int ks = 0; ks < kKeyTile / 16; ++ks)
+                            mma_tmem_a(tmem + C::O_BASE + t * D, tmem + t * C::S_COL + ks * 8,
+                                       sdesc_mn(v + ks * 2048, C::PANEL), C::IDESC_PV,
+                                       (j > 0 || ks > 0) ? 1u : 0u);
+                        mma_commit(&sh.pv_done[t]);
+                        if (j + 1 < job.nk[t]) {
+                            ok = wait(&sh.kv_full[sk], ek / C::STAGES);
+                            if (!ok) break;
+                            tc_fence_after();
+                            scores(t, sk);
+                        }
+                    }
+                    if (!ok || sh.abort) break;
+                    mma_commit(&sh.kv_empty[sv]);
+                    if (j + 1 < job.n) mma_commit(&sh.kv_empty[sk]);
+                }
+            }
+        } else if (warp == 13) {
+            // ---- copies -------------------------------------------------
+            if (lane == 0) {
+                const uint32_t q_bytes = (uint32_t)(R * a.G) * 128 * C::PANELS;
+                auto load_q = [&](int t) {
+                    if (job.nk[t] == 0) return;
+                    mbar_arrive_expect_tx(&sh.q_full[t], q_bytes);
+                    for (int p = 0; p < C::PANELS; ++p)
+                        tma_load_3d(sq + t * C::TILE + p * C::PANEL, &map_q, p * 64, kvh * a.G,
+                                    begin + job.q0[t], &sh.q_full[t]);
+                };
+                uint32_t loaded = 0;
+                bool ok = true;
+                load_q(0);
+                for (int32_t e = 0; e < 2 * job.n && ok; ++e) {
+                    const uint32_t s = e % C::STAGES;
+                    if (e >= C::STAGES) {
+                        ok = wait(&sh.kv_empty[s], e / C::STAGES - 1) && !sh.abort;
+                        if (!ok) break;
+                    }
+                    // a value tile with masked places goes by way of warps 14-15
+                    const int32_t j = e >> 1;
+                    uint64_t *full = (e & 1) && j >= job.first_mask
+                                         ? &sh.v_raw[j - job.first_mask] : &sh.kv_full[s];
+                    mbar_arrive_expect_tx(full, C::TILE);
+                    for (int p = 0; p < C::PANELS; ++p)
+                        tma_load_3d(skv + s * C::TILE + p * C::PANEL, (e & 1) ? &map_v : &map_k,
+                                    p * 64, kvh, begin + j * kKeyTile, full);
+                    loaded = e + 1;
+                    if (e == 0) load_q(1);
+                }
+                // the CTA may end when every copy has landed and every commit
+                // that names a barrier of its shared memory has arrived
+                for (int t = 0; t < 2; ++t)
+                    if (job.nk[t]) (void)mbar_wait_bounded(&sh.q_full[t], 0, kWaitLimit);
+                for (int32_t j = job.first_mask; j < job.n && 2 * j + 1 < (int32_t)loaded; ++j)
+                    (void)mbar_wait_bounded(&sh.v_raw[j - job.first_mask], 0, kWaitLimit);
+                for (uint32_t e = loaded > C::STAGES ? loaded - C::STAGES : 0; e < loaded; ++e) {
+                    const uint32_t s = e % C::STAGES, phase = (e / C::STAGES) & 1;
+                    (void)mbar_wait_bounded(&sh.kv_full[s], phase, kWaitLimit);
+                    if (ok && !sh.abort) ok = wait(&sh.kv_empty[s], phase);
+                }
+            }
+        } else {
+            // ---- masked value tiles -------------------------------------
+            const int who = tid - 14 * 32;  // 0..63
+            for (int32_t j = job.first_mask; j < job.n; ++j) {
+                const uint32_t ev = 2 * j + 1, sv = ev % C::STAGES;
+                // (a barrier of its own, used once: these warps do not follow
+                // the ring's phases)
+                if (!wait_warp(&sh.v_raw[j - job.first_mask], 0)) break;
+                const int32_t rows = job.last + 1 - j * kKeyTile;  // rows the CTA sees
+                uint8_t *v = skv + sv * C::TILE;
+                bool found = false;
+                for (int i = who; i < C::PANELS * kKeyTile * 8; i += 64) {
+                    const int r = (i >> 3) & (kKeyTile - 1);
+                    uint4 *p = reinterpret_cast<uint4 *>(v + i * 16);
+                    if (r >= rows) {
+                        *p = make_uint4(0, 0, 0, 0);
+                        continue;
+                    }
+                    uint4 x = *p;
+                    uint32_t *w = &x.x;
+                    uint32_t any = 0;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) any |= (w[b] & 0x7F807F80u) + 0x00800080u;
+                    if (any & 0x80008000u) {  // an exponent of all ones
+                        found = true;
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            if ((w[b] & 0x7F80u) == 0x7F80u) w[b] &= 0xFFFF0000u;
+                            if ((w[b] & 0x7F800000u) == 0x7F800000u) w[b] &= 0x0000FFFFu;
+                        }
+                        *p = x;
+                    }
+                }
+                if (found) sh.bad = 1;
+                fence_proxy_async();
+                __syncwarp();
+                uint64_t *half = &sh.v_half[j - job.first_mask];
+                if (lane == 0) {
+                    mbar_arrive(half);
+                    if (warp == 14 && wait(half, 0)) mbar_arrive(&sh.kv_full[sv]);
+                }
+                __syncwarp();
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        if (sh.abort) {
+            // MMAs may still be in flight: one more commit follows them all
+            if (lane == 0) {
+                mma_commit(&sh.drained);
+                (void)mbar_wait_bounded(&sh.drained, 0, kWaitLimit);
+            }
+            __syncwarp();
+        }
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D>
+cudaError_t launch_t(const AttnArgs &a, cudaStream_t stream) {
+    const int32_t R = kRowTile / a.G;
+    CUtensorMap mq, mk, mv;
+    memset(&mq, 0, sizeof(mq));
+    memset(&mk, 0, sizeof(mk));
+    memset(&mv, 0, sizeof(mv));
+    if (!encode_rows_map(&mq, a.q, D, a.HQ, a.T, a.q_stride, (uint32_t)a.G, (uint32_t)R) ||
+        !encode_rows_map(&mk, a.k, D, a.HKV, a.T, a.k_stride, 1, kKeyTile) ||
+        !encode_rows_map(&mv, a.v, D, a.HKV, a.T, a.v_stride, 1, kKeyTile))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = cudaFuncSetAttribute(
+        attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D>());
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = (int64_t)a.T / (2 * R) + a.N;
+    if (tiles * a.HKV > INT32_MAX) return cudaErrorInvalidValue;
+    attn_tc_kernel<D><<<(unsigned)(tiles * a.HKV), kThreads, smem_bytes<D>(), stream>>>(mq, mk, mv, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t stream) {
+    return a.D == 64 ? launch_t<64>(a, stream) : launch_t<128>(a, stream);
+}
+
+}  // namespace kda

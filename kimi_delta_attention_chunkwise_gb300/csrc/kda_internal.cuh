@@ -189,6 +189,8 @@ struct AttnArgs {
     int *status;
 };
 cudaError_t launch_attn_simt(const AttnArgs &a, cudaStream_t stream);
+// tcgen05 engine (kda_attn_tc.cu): bf16, D = 64 or 128.
+cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t stream);
 
 struct AppendArgs {
     const void *q, *k, *v;         // q may be nullptr
@@ -241,6 +243,11 @@ cudaError_t launch_recurrent_fwd(const RecurArgs &a, cudaStream_t stream);
 bool encode_tile_map(CUtensorMap *m, const void *base, CUtensorMapDataType dt, size_t esize,
                      int32_t T, int32_t H, uint32_t box_x = 128,
                      CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_NONE);
+// A bf16 [T, heads, d] tensor with a token stride (in elements) as a 3-D map
+// {d, heads, T} whose box is [box_tokens x box_heads] rows of 64 channels
+// with the 128-byte swizzle; rows past T read as zero (kda_chunk_tc.cu).
+bool encode_rows_map(CUtensorMap *m, const void *base, int32_t d, int32_t heads, int32_t T,
+                     int64_t stride, uint32_t box_heads, uint32_t box_tokens);
 // KDA_LAUNCH_ORDER=sequential in the environment: every multi-kernel path
 // runs its kernels one after another (kda_chunk_tc.cu).
 bool sequential_order_forced();
