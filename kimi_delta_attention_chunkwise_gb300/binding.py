@@ -763,23 +763,50 @@ def make_attn_shape(N, T, HQ, HKV, d, dtype_code, engine=KDA_ENGINE_AUTO, out_f3
                           int(out_f32), int(q_stride), int(k_stride), int(v_stride))
 
 
-def _rows(t, name, dtype=None, shape=None) -> int:
-    """Checks [T, heads, d] rows whose heads and channels are contiguous (a
-    slice of a fused projection is fine); returns the token stride (0:
-    contiguous)."""
+# These calls are a few microseconds of GPU work when they are small, so their
+# checks read each property of a tensor once and format nothing but errors.
+
+def _misfit(t, name, dev, dtype, shape=None):
+    """Raises what is wrong with an argument that failed a check."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, d]")
-    if dtype is not None and t.dtype != dtype:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the call's other tensors on "
+                         f"cuda:{dev}")
+    if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.is_contiguous():
-        return 0
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _first(t, name):
+    """(device index, dtype, kdaDtype_t) of the tensor that fixes a call's."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dev = t.get_device()  # -1: a host tensor
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev, t.dtype, _dtype_code(t)
+
+
+def _whole(t, name, dev, dtype, shape) -> int:
+    """Address of a contiguous tensor of this shape."""
+    try:
+        if t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _misfit(t, name, dev, dtype, shape)
+
+
+def _token_stride(t, name) -> int:
+    """The token stride of [T, heads, d] rows whose heads and channels are
+    contiguous (a slice of a fused projection is fine)."""
     T, H, d = t.shape
     st, sh, sd = t.stride()
     if (d > 1 and sd != 1) or (H > 1 and sh != d) or (T > 1 and st < H * d):
@@ -791,66 +818,72 @@ def _rows(t, name, dtype=None, shape=None) -> int:
     return st
 
 
-def _paged_cache(k_cache, v_cache, block_table, dtype, N, HKV, d) -> kdaPagedCache_t:
-    torch = _torch()
-    _require(k_cache, "k_cache", dtype)
-    if k_cache is None or k_cache.dim() != 4 or k_cache.shape[1] != HKV or k_cache.shape[3] != d:
-        raise ValueError("k_cache must be [pages, HKV, page_size, d]")
-    if v_cache is None:
-        raise ValueError("v_cache must be [pages, HKV, page_size, d]")
-    _require(v_cache, "v_cache", dtype, k_cache.shape)
-    _require(block_table, "block_table", torch.int32)
-    if block_table is None or block_table.dim() != 2 or block_table.shape[0] != N:
+def _rows(t, name, dev, dtype):
+    """[T, heads, d] rows: (shape, token stride)."""
+    try:
+        fits = t.get_device() == dev and t.dtype is dtype
+    except AttributeError:
+        fits = False
+    if not fits:
+        _misfit(t, name, dev, dtype)
+    size = t.shape
+    if len(size) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, d]")
+    return size, (0 if t.is_contiguous() else _token_stride(t, name))
+
+
+def _grouped(HQ, HKV, what):
+    if HKV == 0 or HQ % HKV:
+        raise ValueError(f"q has {HQ} heads, not a multiple of {what} {HKV}")
+
+
+def _paged_cache(k_cache, v_cache, block_table, dev, dtype, i32, N, d):
+    """(the C description, HKV)."""
+    size = getattr(k_cache, "shape", ())
+    if len(size) != 4 or size[3] != d:
+        raise ValueError(f"k_cache must be [pages, HKV, page_size, {d}]")
+    kp = _whole(k_cache, "k_cache", dev, dtype, size)
+    vp = _whole(v_cache, "v_cache", dev, dtype, size)
+    width = getattr(block_table, "shape", ())
+    if len(width) != 2 or width[0] != N:
         raise ValueError(f"block_table must be [{N}, pages per sequence]")
-    return kdaPagedCache_t(_ptr(k_cache), _ptr(v_cache), _ptr(block_table), k_cache.shape[0],
-                           k_cache.shape[2], block_table.shape[1])
+    tp = _whole(block_table, "block_table", dev, i32, width)
+    return kdaPagedCache_t(kp, vp, tp, size[0], size[2], width[1]), size[1]
 
 
-class _on_device:
-    """The tensors' device as the current one for a call; all tensors share it."""
-
-    def __init__(self, *tensors):
-        torch = _torch()
-        devs = {t.device for t in tensors if t is not None}
-        if len(devs) != 1:
-            raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
-        dev = devs.pop()
-        self.guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _attn_out(q, shape, dev, dt, out, out_f32, torch):
+    """(out, its address, freshly made out or None, out_f32 flag)."""
+    if out is None:
+        f32 = out_f32 and dt is not torch.float32
+        out = torch.empty(shape, dtype=torch.float32 if f32 else dt, device=q.device)
+        return out, out.data_ptr(), out, f32
+    odt = getattr(out, "dtype", None)
+    if odt is not dt and odt is not torch.float32:
+        raise TypeError("out must have the dtype of q, or float32")
+    return out, _whole(out, "out", dev, odt, shape), None, odt is not dt
 
 
-def _launch_stream(stream, *made):
-    """The handle of the call's stream; tensors the call made are marked as
-    used on it, so that their memory outlives the work."""
+def _attn_launch(where, dev, stream, made, fn, *args):
+    """Calls fn(*args, stream) with the tensors' device current.  On a stream
+    other than the current one, the tensors the call made are marked as used
+    there, so that their memory outlives the work."""
     torch = _torch()
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream)
-    for t in made:
-        if t is not None:
-            t.record_stream(stream)
-    return stream.cuda_stream
-
-
-def _attn_out(q, out, out_f32):
-    """(out, freshly made out or None, out_f32 flag)."""
-    torch = _torch()
-    odt = _out_dtype(q, out, out_f32)
-    if odt not in (q.dtype, torch.float32):
-        raise TypeError("out must have the dtype of q, or float32")
-    made = None
-    if out is None:
-        out = made = torch.empty(q.shape, dtype=odt, device=q.device)
-    _require(out, "out", odt, q.shape)
-    return out, made, int(odt != q.dtype)
+        s = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=dev)
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
+        s = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, s)
+    if status != KDA_SUCCESS:
+        raise KdaError(status, where)
 
 
 def kda_attn_fwd(q, k, v, scale: float, cu_seqlens=None, out=None, lse=None, *, engine="auto",
@@ -867,27 +900,26 @@ def kda_attn_fwd(q, k, v, scale: float, cu_seqlens=None, out=None, lse=None, *, 
     with d = 64 or 128, "simt" is fp32 arithmetic on CUDA cores.
     """
     torch = _torch()
-    qs = _rows(q, "q")
-    T, HQ, d = q.shape
-    ks = _rows(k, "k", q.dtype)
-    HKV = k.shape[1]
-    if tuple(k.shape) != (T, HKV, d):
-        raise ValueError(f"k must be [{T}, HKV, {d}], got {tuple(k.shape)}")
-    vs = _rows(v, "v", q.dtype, (T, HKV, d))
-    if HKV == 0 or HQ % HKV:
-        raise ValueError(f"q has {HQ} heads, not a multiple of k's {HKV}")
-    N = 1
+    dev, dt, code = _first(q, "q")
+    size, qs = _rows(q, "q", dev, dt)
+    T, HQ, d = size
+    ksize, ks = _rows(k, "k", dev, dt)
+    HKV = ksize[1]
+    vsize, vs = _rows(v, "v", dev, dt)
+    if ksize != (T, HKV, d) or vsize != ksize:
+        raise ValueError(f"k and v must be [{T}, HKV, {d}], got {tuple(ksize)}, {tuple(vsize)}")
+    _grouped(HQ, HKV, "k's")
+    N, cup, lsep = 1, None, None
     if cu_seqlens is not None:
-        _require(cu_seqlens, "cu_seqlens", torch.int32)
         N = cu_seqlens.numel() - 1
-    _require(lse, "lse", torch.float32, (T, HQ))
-    out, made, f32 = _attn_out(q, out, out_f32)
+        cup = _whole(cu_seqlens, "cu_seqlens", dev, torch.int32, (N + 1,))
+    if lse is not None:
+        lsep = _whole(lse, "lse", dev, torch.float32, (T, HQ))
+    out, op, made, f32 = _attn_out(q, size, dev, dt, out, out_f32, torch)
     eng = _ENGINES[engine] if isinstance(engine, str) else int(engine)
-    shape = make_attn_shape(N, T, HQ, HKV, d, _dtype_code(q), eng, f32, qs, ks, vs)
-    with _on_device(q, k, v, cu_seqlens, out, lse):
-        _check(load().kda_attn_fwd(_ptr(q), _ptr(k), _ptr(v), float(scale), _ptr(cu_seqlens),
-                                   _ptr(out), _ptr(lse), ctypes.byref(shape),
-                                   _launch_stream(stream, made)), "kda_attn_fwd")
+    shape = kdaAttnShape_t(N, T, HQ, HKV, d, code, eng, f32, qs, ks, vs)
+    _attn_launch("kda_attn_fwd", dev, stream, (made,), load().kda_attn_fwd, q.data_ptr(),
+                 k.data_ptr(), v.data_ptr(), scale, cup, op, lsep, ctypes.byref(shape))
     return out, lse
 
 
@@ -909,46 +941,49 @@ def kda_cache_append(k, v, k_cache, v_cache, block_table, cache_lens, cu_seqlens
     be q); ``k_out`` [T, HKV, d] receives the rotated keys if given (may be k).
     """
     torch = _torch()
-    ks = _rows(k, "k")
-    T, HKV, d = k.shape
-    vs = _rows(v, "v", k.dtype, (T, HKV, d))
-    HQ, qs, made = HKV, 0, None
+    dev, dt, code = _first(k, "k")
+    i32 = torch.int32
+    size, ks = _rows(k, "k", dev, dt)
+    T, HKV, d = size
+    vsize, vs = _rows(v, "v", dev, dt)
+    if vsize != size:
+        raise ValueError(f"v must have shape {tuple(size)}, got {tuple(vsize)}")
+    HQ, qs, made, qp, qop, kop, cup, rp = HKV, 0, None, None, None, None, None, None
     if q is not None:
-        qs = _rows(q, "q", k.dtype)
-        HQ = q.shape[1]
-        if tuple(q.shape) != (T, HQ, d):
-            raise ValueError(f"q must be [{T}, HQ, {d}], got {tuple(q.shape)}")
-        if HKV == 0 or HQ % HKV:
-            raise ValueError(f"q has {HQ} heads, not a multiple of k's {HKV}")
+        qsize, qs = _rows(q, "q", dev, dt)
+        HQ = qsize[1]
+        if qsize != (T, HQ, d):
+            raise ValueError(f"q must be [{T}, HQ, {d}], got {tuple(qsize)}")
+        _grouped(HQ, HKV, "k's")
+        qp = q.data_ptr()
         if q_out is None:
-            q_out = made = torch.empty((T, HQ, d), dtype=q.dtype, device=q.device)
-        _require(q_out, "q_out", q.dtype, (T, HQ, d))
+            q_out = made = torch.empty(qsize, dtype=dt, device=q.device)
+        qop = _whole(q_out, "q_out", dev, dt, qsize)
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    _require(k_out, "k_out", k.dtype, (T, HKV, d))
-    _require(cache_lens, "cache_lens", torch.int32)
-    if cache_lens is None or cache_lens.dim() != 1:
+    if k_out is not None:
+        kop = _whole(k_out, "k_out", dev, dt, size)
+    if cache_lens is None:
         raise ValueError("cache_lens must be [N]")
     N = cache_lens.numel()
+    lp = _whole(cache_lens, "cache_lens", dev, i32, (N,))
     if cu_seqlens is not None:
-        _require(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,))
-    elif N not in (1, T):
+        cup = _whole(cu_seqlens, "cu_seqlens", dev, i32, (N + 1,))
+    elif N != T and N != 1:
         raise ValueError(f"{T} tokens of {N} sequences need cu_seqlens")
-    cache = _paged_cache(k_cache, v_cache, block_table, k.dtype, N, HKV, d)
-    rp = None
+    cache, heads = _paged_cache(k_cache, v_cache, block_table, dev, dt, i32, N, d)
+    if heads != HKV:
+        raise ValueError(f"k has {HKV} heads, the cache {heads}")
     if rope is not None:
-        _require(rope, "rope", torch.float32)
-        if rope.dim() != 2:
+        rsize = rope.shape
+        if len(rsize) != 2:
             raise ValueError("rope must be [positions, rot_dim]")
-        rp = ctypes.byref(kdaRope_t(_ptr(rope), rope.shape[0], rope.shape[1],
-                                    int(bool(rope_interleaved))))
-    shape = make_attn_shape(N, T, HQ, HKV, d, _dtype_code(k), 0, 0, qs, ks, vs)
-    with _on_device(k, v, q, k_cache, v_cache, block_table, cache_lens, cu_seqlens, q_out, k_out,
-                    rope):
-        _check(load().kda_cache_append(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(cache_lens), rp, _ptr(q_out),
-            _ptr(k_out), ctypes.byref(cache), ctypes.byref(shape),
-            _launch_stream(stream, made)), "kda_cache_append")
+        rp = ctypes.byref(kdaRope_t(_whole(rope, "rope", dev, torch.float32, rsize), *rsize,
+                                    bool(rope_interleaved)))
+    shape = kdaAttnShape_t(N, T, HQ, HKV, d, code, 0, 0, qs, ks, vs)
+    _attn_launch("kda_cache_append", dev, stream, (made,), load().kda_cache_append, qp,
+                 k.data_ptr(), v.data_ptr(), cup, lp, rp, qop, kop, ctypes.byref(cache),
+                 ctypes.byref(shape))
     return q_out, k_out
 
 
@@ -976,35 +1011,29 @@ def kda_attn_step(q, k_cache, v_cache, block_table, seq_lens, scale: float, out=
     calls on other streams never share it).
     """
     torch = _torch()
-    qs = _rows(q, "q")
-    N, HQ, d = q.shape
-    if k_cache is None or k_cache.dim() != 4:
-        raise ValueError("k_cache must be [pages, HKV, page_size, d]")
-    HKV = k_cache.shape[1]
-    if HKV == 0 or HQ % HKV:
-        raise ValueError(f"q has {HQ} heads, not a multiple of the cache's {HKV}")
-    cache = _paged_cache(k_cache, v_cache, block_table, q.dtype, N, HKV, d)
-    _require(seq_lens, "seq_lens", torch.int32, (N,))
-    if seq_lens is None:
-        raise ValueError("seq_lens must be [N]")
-    _require(lse, "lse", torch.float32, (N, HQ))
-    out, made, f32 = _attn_out(q, out, out_f32)
-    shape = make_attn_shape(N, N, HQ, HKV, d, _dtype_code(q), 0, f32, qs)
-    with _on_device(q, k_cache, v_cache, block_table, seq_lens, out, lse, workspace):
-        key = (q.device.index, d, HQ // HKV, q.dtype)  # what the size depends on
-        nbytes = _step_bytes.get(key)
-        if nbytes is None:
+    dev, dt, code = _first(q, "q")
+    size, qs = _rows(q, "q", dev, dt)
+    N, HQ, d = size
+    cache, HKV = _paged_cache(k_cache, v_cache, block_table, dev, dt, torch.int32, N, d)
+    _grouped(HQ, HKV, "the cache's")
+    lp = _whole(seq_lens, "seq_lens", dev, torch.int32, (N,))
+    lsep = None if lse is None else _whole(lse, "lse", dev, torch.float32, (N, HQ))
+    out, op, made, f32 = _attn_out(q, size, dev, dt, out, out_f32, torch)
+    shape = kdaAttnShape_t(N, N, HQ, HKV, d, code, 0, f32, qs, 0, 0)
+    key = (dev, d, HQ // HKV, code)  # what the size depends on
+    nbytes = _step_bytes.get(key)
+    if nbytes is None:
+        with torch.cuda.device(dev):
             nbytes = _step_bytes[key] = kda_attn_step_workspace_size(shape)
-        ws_made = None
-        if workspace is None:
-            workspace = ws_made = torch.empty(nbytes + 256, dtype=torch.uint8, device=q.device)
-        _require(workspace, "workspace", torch.uint8)
-        wp = (workspace.data_ptr() + 255) // 256 * 256
-        left = workspace.numel() - (wp - workspace.data_ptr())
-        _check(load().kda_attn_step_ws(
-            _ptr(q), ctypes.byref(cache), _ptr(seq_lens), float(scale), _ptr(out), _ptr(lse),
-            ctypes.byref(shape), wp, max(left, 0), _launch_stream(stream, made, ws_made)),
-            "kda_attn_step_ws")
+    ws_made = None
+    if workspace is None:
+        workspace = ws_made = torch.empty(nbytes + 256, dtype=torch.uint8, device=q.device)
+    size = workspace.numel()
+    base = _whole(workspace, "workspace", dev, torch.uint8, (size,))
+    wp = (base + 255) // 256 * 256
+    _attn_launch("kda_attn_step", dev, stream, (made, ws_made), load().kda_attn_step_ws,
+                 q.data_ptr(), ctypes.byref(cache), lp, scale, op, lsep, ctypes.byref(shape), wp,
+                 max(size - (wp - base), 0))
     return out, lse
 
 

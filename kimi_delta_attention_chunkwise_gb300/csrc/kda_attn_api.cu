@@ -98,6 +98,18 @@ kdaStatus_t plan_attn_step(const void *q, const kdaPagedCache_t *cache, const in
 }
 
 }  // namespace
+
+int device_sms() {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+    if (dev < 64) n = known[dev].load(std::memory_order_relaxed);
+    if (n) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 }  // namespace kda
 
 using namespace kda;

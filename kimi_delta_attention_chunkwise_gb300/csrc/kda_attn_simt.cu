@@ -231,8 +231,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_simt_kernel(const AttnArgs a
 template <typename T, int D>
 cudaError_t launch_t(const AttnArgs &a, cudaStream_t stream) {
     constexpr size_t bytes = smem_bytes<D>();
-    const cudaError_t e = cudaFuncSetAttribute(
-        attn_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    const cudaError_t e = allow_smem<attn_simt_kernel<T, D>>(bytes);
     if (e != cudaSuccess) return e;
     // every sequence's last tile may be short: at most N more than the rows fill
     const int64_t tiles = (int64_t)a.T * a.G / kRows + a.N;

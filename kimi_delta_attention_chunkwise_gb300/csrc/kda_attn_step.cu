@@ -102,6 +102,7 @@ template <typename T, int D>
 struct SimtCore {
     using Type = T;
     static constexpr int kD = D, kRows = 4, kCtas = 3;
+    static constexpr bool kAhead = false;
     static constexpr int LPT = D / 8, TPW = 32 / LPT;
     // tokens whose keys and values are in flight together: 16, or 8 where 16
     // would take 128 registers
@@ -240,6 +241,204 @@ struct SimtCore {
 };
 
 // ---------------------------------------------------------------------------
+// tensor-core core: bf16, D = 64 or 128, 8 NT query heads
+// ---------------------------------------------------------------------------
+// Scores and outputs are computed transposed, so that the 16-row side of
+// mma.sync.m16n8k16 is filled by tokens (then channels) and its 8-column side
+// by query heads:
+//     S^T [16 tokens x 8 heads] = K Q^T,   O^T [16 channels x 8 heads] += V^T P^T
+// Every operand comes straight from global memory in 16-byte vectors, without
+// shared memory, because a contraction may visit its index in any order as
+// long as both operands agree, and the rows of O^T may be any channels:
+//   * lane (g, t) = (lane / 4, lane % 4) of the K operand holds tokens g and
+//     g + 8, channels 8 (4 j + t) .. + 7 of step pair j; Q likewise;
+//   * lane (g, t) of the V operand holds tokens 2t, 2t + 1, 2t + 8, 2t + 9,
+//     channels 8 g .. + 7 (and 64 + 8 g .. + 7), and pairs the tokens'
+//     channels with byte permutes.
+// The weights P^T go from the accumulator's layout to the operand's by an 8x8
+// transpose (movmatrix).  They are rounded to bf16 (V's type, relative 2^-8);
+// their sum is taken in fp32 before the rounding.  The reference of the
+// exponentials moves only when a score passes it by more than 2^8, by a vote
+// of the warp: most tiles need no shuffles and no rescaling.
+// mma.sync, not tcgen05: 16 query rows at most use an eighth of its 128-row
+// tile, and at HBM speed an SM gets one such instruction's operands per ~20
+// cycles.
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+// 16 bytes that are read once
+__device__ __forceinline__ uint4 load_once(const void *p) {
+    uint4 x;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                 : "l"(p));
+    return x;
+}
+
+template <int D, int NT>
+struct MmaCore {
+    using Type = __nv_bfloat16;
+    static constexpr int kD = D, kRows = 8 * NT, kCtas = NT == 1 ? 3 : 2;
+    static constexpr bool kAhead = true;
+    static constexpr int J = D / 32;   // 16-byte vectors of a token row per lane (K, Q)
+    static constexpr int VC = D / 64;  // and of V
+    static constexpr int MT = D / 16;  // channel tiles of O^T
+    static constexpr float kMoveBy = 8.f;
+
+    uint4 q[NT][J], k[2][J], v[4][VC];
+    float o[MT][NT][4], s[NT][4], ref[NT][2], sum[NT][2];
+    float c2;
+
+    __device__ void init(const Type *qp, int rows, float scale) {
+        const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+        c2 = scale * kLog2e;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int h = n * 8 + g;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                q[n][j] = h < rows ? *reinterpret_cast<const uint4 *>(qp + h * D + (j * 4 + t) * 8)
+                                   : make_uint4(0, 0, 0, 0);
+            ref[n][0] = ref[n][1] = -INFINITY;
+            sum[n][0] = sum[n][1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][n][e] = 0.f;
+        }
+    }
+    // rows kp / vp .. of n tokens (rows from n on are not read: zeros)
+    __device__ void load_k(const Type *kp, int n) {
+        const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                k[r][j] = g + 8 * r < n ? load_once(kp + (g + 8 * r) * D + (j * 4 + t) * 8)
+                                        : make_uint4(0, 0, 0, 0);
+    }
+    __device__ void load_v(const Type *vp, int n) {
+        const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int tok = 2 * t + (r & 1) + 8 * (r >> 1);
+#pragma unroll
+            for (int c = 0; c < VC; ++c)
+                v[r][c] = tok < n ? load_once(vp + tok * D + c * 64 + g * 8)
+                                  : make_uint4(0, 0, 0, 0);
+        }
+    }
+    __device__ void scores() {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                mma_16816(s[n], k[0][j].x, k[1][j].x, k[0][j].y, k[1][j].y, q[n][j].x, q[n][j].y);
+                mma_16816(s[n], k[0][j].z, k[1][j].z, k[0][j].w, k[1][j].w, q[n][j].z, q[n][j].w);
+            }
+        }
+    }
+    // weights of the tile's n tokens and their product with V
+    __device__ void values(int n_tok) {
+        const int g = (threadIdx.x & 31) >> 2;
+        uint32_t p[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if (n_tok < kWarpTokens) {
+                if (g >= n_tok) s[n][0] = s[n][1] = -INFINITY;
+                if (g + 8 >= n_tok) s[n][2] = s[n][3] = -INFINITY;
+            }
+            float top[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) top[e] = fmaxf(s[n][e], s[n][e + 2]) * c2;
+            // (NaN compares false: a NaN score moves nothing and shows in the sums)
+            const bool move = top[0] > ref[n][0] + kMoveBy || top[1] > ref[n][1] + kMoveBy;
+            if (__any_sync(0xffffffffu, move)) {
+                float f[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float m = fmaxf(top[e], ref[n][e]);
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1)
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+                    f[e] = m == -INFINITY ? 1.f : exp2f(ref[n][e] - m);
+                    ref[n][e] = m;
+                    sum[n][e] *= f[e];
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[i][n][e] *= f[e & 1];
+            }
+            float w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float r = ref[n][e & 1];
+                w[e] = tc::exp2_approx(fmaf(s[n][e], c2, r == -INFINITY ? 0.f : -r));
+                sum[n][e & 1] += w[e];
+            }
+            p[n][0] = transpose_8x8(tc::pack_bf16x2(w[0], w[1]));
+            p[n][1] = transpose_8x8(tc::pack_bf16x2(w[2], w[3]));
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            // channel i of a lane's vector: D = 128: rows g and g + 8 of the
+            // tile are channels 8 g + i and 64 + 8 g + i; D = 64: 8 g + i and
+            // 8 g + 4 + i
+            uint32_t a[4];
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int hi = 0; hi < 2; ++hi) {
+                    const uint4 &x = v[2 * hi][VC == 2 ? r : 0], &y = v[2 * hi + 1][VC == 2 ? r : 0];
+                    const int ch = VC == 2 ? i : i + 4 * r;
+                    const uint32_t xw = (&x.x)[ch >> 1], yw = (&y.x)[ch >> 1];
+                    a[r + 2 * hi] = __byte_perm(xw, yw, (ch & 1) ? 0x7632 : 0x5410);
+                }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                mma_16816(o[i][n], a[0], a[1], a[2], a[3], p[n][0], p[n][1]);
+        }
+    }
+    __device__ void finish(float *sacc, float *sm, float *sl) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float l = sum[n][e];
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+                if (g == 0) {
+                    sm[n * 8 + 2 * t + e] = ref[n][e];
+                    sl[n * 8 + 2 * t + e] = l;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int h = n * 8 + 2 * t + (e & 1);
+                    const int ch = VC == 2 ? 64 * (e >> 1) + 8 * g + i : 8 * g + 4 * (e >> 1) + i;
+                    sacc[h * D + ch] = o[i][n][e];
+                }
+        }
+    }
+};
+
+// ---------------------------------------------------------------------------
 // the kernels
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void store_out(const AttnStepArgs &a, int64_t i, float y) {
@@ -291,18 +490,50 @@ attn_step_kernel(const AttnStepArgs a, float *part) {
         const int64_t head = (int64_t)kvh * a.G + h0;
         core.init(static_cast<const T *>(a.q) + s * a.q_stride + head * D, rows, a.scale);
         const int32_t *table = a.block_table + (int64_t)s * a.max_pages;
-        for (int32_t t = tile0; t < tile1; ++t) {
+        // this warp's tokens of tile t: the page's table entry, and the rows
+        auto page_of = [&](int32_t t) -> int32_t {
             const int32_t tok = t * kTile + warp * kWarpTokens;
-            if (tok >= len) break;
-            const int32_t page = table[tok >> a.page_shift];
+            return t < tile1 && tok < len ? table[tok >> a.page_shift] : -1;
+        };
+        auto rows_of = [&](int32_t t, int32_t page, int64_t &at) -> int {
+            const int32_t tok = t * kTile + warp * kWarpTokens;
+            at = 0;
+            if (t >= tile1 || tok >= len) return 0;
             if (page < 0 || page >= a.num_pages) {
                 *a.status = KDA_ERR_INVALID_ARG;
-                continue;
+                return 0;
             }
-            const int64_t row = (((int64_t)page * a.HKV + kvh) << a.page_shift) +
-                                (tok & ((1 << a.page_shift) - 1));
-            core.tile(static_cast<const T *>(a.k_cache) + row * D,
-                      static_cast<const T *>(a.v_cache) + row * D, min(kWarpTokens, len - tok));
+            at = ((((int64_t)page * a.HKV + kvh) << a.page_shift) +
+                  (tok & ((1 << a.page_shift) - 1))) * D;
+            return min(kWarpTokens, len - tok);
+        };
+        const T *kc = static_cast<const T *>(a.k_cache), *vc = static_cast<const T *>(a.v_cache);
+        if constexpr (Core::kAhead) {
+            // the next tile's keys are on their way while this one's weights
+            // and values are worked on, its values while the next scores are,
+            // and its table entry a tile earlier
+            int64_t at, next_at;
+            int n = rows_of(tile0, page_of(tile0), at), next_n;
+            int32_t next_page = page_of(tile0 + 1);
+            core.load_k(kc + at, n);
+            core.load_v(vc + at, n);
+            for (int32_t t = tile0; t < tile1; ++t) {
+                next_n = rows_of(t + 1, next_page, next_at);
+                next_page = page_of(t + 2);
+                core.scores();
+                core.load_k(kc + next_at, next_n);
+                if (n > 0) core.values(n);
+                core.load_v(vc + next_at, next_n);
+                n = next_n;
+            }
+        } else {
+            int32_t next_page = page_of(tile0);
+            for (int32_t t = tile0; t < tile1; ++t) {
+                int64_t at;
+                const int n = rows_of(t, next_page, at);
+                next_page = page_of(t + 1);
+                if (n > 0) core.tile(kc + at, vc + at, n);
+            }
         }
         core.finish(s_acc[warp], s_m[warp], s_l[warp]);
         __syncthreads();
@@ -416,18 +647,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnStepA
     }
 }
 
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    return n;
-}
-
 template <class Core>
 cudaError_t launch_core(const AttnStepArgs &a, cudaStream_t stream) {
     constexpr int D = Core::kD, R = Core::kRows;
-    const int sms = sm_count();
+    const int sms = device_sms();
     if (!sms) return cudaErrorUnknown;
     // no more CTAs than the longest possible line has tiles
     const int64_t most = (int64_t)a.N * a.HKV * ((a.G + R - 1) / R) *
@@ -453,13 +676,16 @@ cudaError_t launch_core(const AttnStepArgs &a, cudaStream_t stream) {
 // The core of a problem, as a call of f.template operator()<Core>().
 template <class F>
 auto with_core(int32_t D, int32_t G, int32_t dtype, F f) {
-    (void)G;
     if (dtype == KDA_DTYPE_BF16) {
         switch (D) {
             case 16: return f(SimtCore<__nv_bfloat16, 16>{});
             case 32: return f(SimtCore<__nv_bfloat16, 32>{});
-            case 64: return f(SimtCore<__nv_bfloat16, 64>{});
-            default: return f(SimtCore<__nv_bfloat16, 128>{});
+            case 64:
+                if (G <= 8) return f(MmaCore<64, 1>{});
+                return f(MmaCore<64, 2>{});
+            default:
+                if (G <= 8) return f(MmaCore<128, 1>{});
+                return f(MmaCore<128, 2>{});
         }
     }
     switch (D) {
@@ -473,7 +699,7 @@ auto with_core(int32_t D, int32_t G, int32_t dtype, F f) {
 }  // namespace
 
 size_t attn_step_workspace_bytes(int32_t D, int32_t G, int32_t dtype) {
-    const int sms = sm_count();
+    const int sms = device_sms();
     return with_core(D, G, dtype, [&](auto core) -> size_t {
         using Core = decltype(core);
         return (size_t)sms * Core::kCtas * 2 * Core::kRows * (Core::kD + 2) * sizeof(float);

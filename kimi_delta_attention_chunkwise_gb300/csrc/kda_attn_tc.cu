@@ -577,8 +577,7 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t stream) {
         !encode_rows_map(&mk, a.k, D, a.HKV, a.T, a.k_stride, 1, kKeyTile) ||
         !encode_rows_map(&mv, a.v, D, a.HKV, a.T, a.v_stride, 1, kKeyTile))
         return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(
-        attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<D>());
+    const cudaError_t e = allow_smem<attn_tc_kernel<D>>(smem_bytes<D>());
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)a.T / (2 * R) + a.N;
     if (tiles * a.HKV > INT32_MAX) return cudaErrorInvalidValue;

@@ -2,6 +2,7 @@
 // Not part of the public ABI (that is include/kda.h).
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -229,6 +230,24 @@ cudaError_t launch_attn_step(const AttnStepArgs &a, cudaStream_t stream);
 
 // Device address of the status word on the current device (kda_api.cu).
 int *device_status_word();
+
+// SMs of the current device, asked for once per device (kda_attn_api.cu; 0:
+// the query failed).
+int device_sms();
+
+// Raises a kernel's dynamic shared memory limit, once per device.
+template <auto Kernel>
+cudaError_t allow_smem(size_t bytes) {
+    static std::atomic<uint64_t> done{0};  // one bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // fp32 CUDA-core chunk engine (kda_chunk_simt.cu).  Needs no scratch.
 cudaError_t launch_chunk_simt(const ChunkArgs &a, cudaStream_t stream);
