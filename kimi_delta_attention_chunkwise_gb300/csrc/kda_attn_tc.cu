@@ -70,7 +70,7 @@ struct Cfg {
 
 struct Shared {
     uint64_t q_full[2], kv_full[8], kv_empty[8], v_raw[3], v_half[3];
-    uint64_t s_full[2], p_full[2], m_ready[2], o_ready[2], pv_done[2], drained;
+    uint64_t s_full[2], p_full[2], m_ready[2], pv_done[2], drained;
     uint32_t tmem;
     int32_t found, abort, bad;
     SeqTile tile;
@@ -84,6 +84,18 @@ constexpr uint32_t smem_bytes() {
     return (2 + Cfg<D>::STAGES) * Cfg<D>::TILE + (uint32_t)sizeof(Shared);
 }
 static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "227 KB per CTA");
+
+// One lane of a converged warp.  The MMA warp runs its control flow as a whole
+// and only the MMAs and commits sit under this: the operands then stay in
+// uniform registers (issued from `if (lane == 0)`, every MMA took ~115 cycles
+// to issue, longer than the 64 it runs).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
 
 // O[128 x N] (+)= P[128 x 16 steps] V: A from TMEM
 __device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
@@ -192,9 +204,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sh.q_full[t], 1);
             mbar_init(&sh.s_full[t], 1);
-            mbar_init(&sh.p_full[t], 4);
+            mbar_init(&sh.p_full[t], 8);  // 4 warps of weights, 4 of O_t
             mbar_init(&sh.m_ready[t], 4);
-            mbar_init(&sh.o_ready[t], 4);
             mbar_init(&sh.pv_done[t], 1);
         }
         for (int i = 0; i < C::STAGES; ++i) {
@@ -233,15 +244,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     job.first_mask = (job.q0[0] + 1) / kKeyTile;
 
     auto wait = [&](uint64_t *bar, uint32_t phase) -> bool {
+        if (mbar_try_wait(bar, phase & 1)) return true;
         if (mbar_wait_bounded(bar, phase & 1, kWaitLimit)) return true;
         sh.abort = 1;
         *a.status = KDA_ERR_TIMEOUT;
         return false;
     };
-    // the same for a whole warp, which leaves it together
+    // the same for a whole warp, which goes on or gives up together
     auto wait_warp = [&](uint64_t *bar, uint32_t phase) -> bool {
-        const bool ok = wait(bar, phase);
-        return __all_sync(0xffffffffu, ok && !*static_cast<volatile int32_t *>(&sh.abort));
+        return __all_sync(0xffffffffu, wait(bar, phase));
     };
 
     if (warp < 8) {
@@ -335,10 +346,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         const int row = tid & 127;
         const uint32_t lane_base = (uint32_t)(warp & 3) * 32;
         bool ok = true;
-        for (int32_t j = 1; j < job.n && ok; ++j) {
+        for (int32_t j = 0; j < job.n && ok; ++j) {
 #pragma unroll 1
             for (int t = 0; t < 2 && ok; ++t) {
                 if (j >= job.nk[t]) continue;
+                if (j == 0) {  // the first product overwrites O_t
+                    if (lane == 0) mbar_arrive(&sh.p_full[t]);
+                    continue;
+                }
                 ok = wait_warp(&sh.m_ready[t], j - 1);
                 if (!ok) break;
                 const float f = sh.scale[t][row];
@@ -359,7 +374,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     tc_fence_before();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.o_ready[t]);
+                if (lane == 0) mbar_arrive(&sh.p_full[t]);
                 __syncwarp();
             }
         }
@@ -417,50 +432,73 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         regs_dec<48>();
         if (warp == 12) {
             // ---- MMAs ---------------------------------------------------
-            if (lane == 0) {
-                const uint32_t q_base = smem_u32(sq), kv_base = smem_u32(skv);
-                auto scores = [&](int t, uint32_t stage) {
-                    mma_panels(tmem + t * C::S_COL, q_base + t * C::TILE, C::PANEL,
-                               kv_base + stage * C::TILE, C::PANEL, D / 16, C::IDESC_QK, false);
+            const uint32_t q_base = smem_u32(sq), kv_base = smem_u32(skv);
+            auto scores = [&](int t, uint32_t stage) {
+                const uint64_t qd = sdesc_sw128(q_base + t * C::TILE);
+                const uint64_t kd = sdesc_sw128(kv_base + stage * C::TILE);
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t step = ((ks >> 2) * C::PANEL + (ks & 3) * 32) >> 4;
+                        mma_half(tmem + t * C::S_COL, qd + step, kd + step, C::IDESC_QK, ks > 0);
+                    }
                     mma_commit(&sh.s_full[t]);
-                };
-                bool ok = true;
-                for (int t = 0; t < 2 && ok; ++t) {
-                    if (job.nk[t] == 0) continue;
-                    ok = wait(&sh.q_full[t], 0) && (t > 0 || wait(&sh.kv_full[0], 0));
+                }
+                __syncwarp();
+            };
+            bool ok = true;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (job.nk[t] == 0 || !ok) continue;
+                ok = wait_warp(&sh.q_full[t], 0) && (t > 0 || wait_warp(&sh.kv_full[0], 0));
+                if (!ok) break;
+                tc_fence_after();
+                scores(t, 0);
+            }
+            if (ok && elect_one()) mma_commit(&sh.kv_empty[0]);
+            __syncwarp();
+            for (int32_t j = 0; j < job.n && ok; ++j) {
+                const uint32_t ev = 2 * j + 1, ek = 2 * j + 2;
+                const uint32_t sv = ev % C::STAGES, sk = ek % C::STAGES;
+                const uint64_t vd = sdesc_mn(kv_base + sv * C::TILE, C::PANEL);
+                // both tiles of the step before its first product, so that
+                // nothing but the weights stands before an MMA
+                ok = wait_warp(&sh.kv_full[sv], ev / C::STAGES) &&
+                     (j + 1 >= job.n || wait_warp(&sh.kv_full[sk], ek / C::STAGES));
+                if (!ok) break;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (j >= job.nk[t] || !ok) continue;
+                    ok = wait_warp(&sh.p_full[t], j);
                     if (!ok) break;
                     tc_fence_after();
-                    scores(t, 0);
-                }
-                if (ok) mma_commit(&sh.kv_empty[0]);
-                for (int32_t j = 0; j < job.n && ok; ++j) {
-                    const uint32_t ev = 2 * j + 1, ek = 2 * j + 2;
-                    const uint32_t sv = ev % C::STAGES, sk = ek % C::STAGES;
-                    ok = wait(&sh.kv_full[sv], ev / C::STAGES);
-                    if (!ok) break;
-                    for (int t = 0; t < 2 && ok; ++t) {
-                        if (j >= job.nk[t]) continue;
-                        ok = wait(&sh.p_full[t], j) && (j == 0 || wait(&sh.o_ready[t], j - 1));
-                        if (!ok || sh.abort) break;
-                        tc_fence_after();
-                        const uint32_t v = kv_base + sv * C::TILE;
+                    const bool more = j + 1 < job.nk[t];
+                    const uint64_t qd = sdesc_sw128(q_base + t * C::TILE);
+                    const uint64_t kd = sdesc_sw128(kv_base + sk * C::TILE);
+                    if (elect_one()) {
 #pragma unroll
                         for (int ks = 0; ks < kKeyTile / 16; ++ks)
                             mma_tmem_a(tmem + C::O_BASE + t * D, tmem + t * C::S_COL + ks * 8,
-                                       sdesc_mn(v + ks * 2048, C::PANEL), C::IDESC_PV,
-                                       (j > 0 || ks > 0) ? 1u : 0u);
+                                       vd + ks * (2048 >> 4), C::IDESC_PV, (j > 0 || ks > 0) ? 1u : 0u);
                         mma_commit(&sh.pv_done[t]);
-                        if (j + 1 < job.nk[t]) {
-                            ok = wait(&sh.kv_full[sk], ek / C::STAGES);
-                            if (!ok) break;
-                            tc_fence_after();
-                            scores(t, sk);
+                        if (more) {
+#pragma unroll
+                            for (int ks = 0; ks < D / 16; ++ks) {
+                                const uint32_t step = ((ks >> 2) * C::PANEL + (ks & 3) * 32) >> 4;
+                                mma_half(tmem + t * C::S_COL, qd + step, kd + step, C::IDESC_QK,
+                                         ks > 0);
+                            }
+                            mma_commit(&sh.s_full[t]);
                         }
                     }
-                    if (!ok || sh.abort) break;
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (elect_one()) {
                     mma_commit(&sh.kv_empty[sv]);
                     if (j + 1 < job.n) mma_commit(&sh.kv_empty[sk]);
                 }
+                __syncwarp();
             }
         } else if (warp == 13) {
             // ---- copies -------------------------------------------------
@@ -479,7 +517,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 for (int32_t e = 0; e < 2 * job.n && ok; ++e) {
                     const uint32_t s = e % C::STAGES;
                     if (e >= C::STAGES) {
-                        ok = wait(&sh.kv_empty[s], e / C::STAGES - 1) && !sh.abort;
+                        ok = wait(&sh.kv_empty[s], e / C::STAGES - 1);
                         if (!ok) break;
                     }
                     // a value tile with masked places goes by way of warps 14-15
@@ -555,7 +593,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     if (warp == 12) {
         if (sh.abort) {
             // MMAs may still be in flight: one more commit follows them all
-            if (lane == 0) {
+            if (elect_one()) {
                 mma_commit(&sh.drained);
                 (void)mbar_wait_bounded(&sh.drained, 0, kWaitLimit);
             }
