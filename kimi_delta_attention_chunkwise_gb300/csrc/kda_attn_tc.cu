@@ -55,6 +55,7 @@ constexpr int kThreads = 512;
 constexpr int kRowTile = 128, kKeyTile = 128;
 constexpr long long kWaitLimit = 2000000000LL;  // SM clocks, about a second
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kEarly = 96;  // keys whose weights are handed over first
 constexpr float kMoveBy = 8.f;  // powers of two a row's maximum may pass its reference by
 
 template <int D>
@@ -70,11 +71,11 @@ struct Cfg {
 
 struct Shared {
     uint64_t q_full[2], kv_full[8], kv_empty[8], v_raw[3], v_half[3];
-    uint64_t s_full[2], p_full[2], m_ready[2], pv_done[2], drained;
+    uint64_t s_full[2], p_full[2], p_rest[2], sum_ready[2], pv_done[2], drained;
     uint32_t tmem;
     int32_t found, abort, bad;
     SeqTile tile;
-    float scale[2][kRowTile], sum[2][kRowTile];
+    float sum[2][kRowTile];
 };
 
 // The tiles start at the dynamic shared memory's base, which is 1024-byte
@@ -156,6 +157,11 @@ __device__ __forceinline__ float2 f2_add(float2 a, float2 b) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 template <int N>
 __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -204,8 +210,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sh.q_full[t], 1);
             mbar_init(&sh.s_full[t], 1);
-            mbar_init(&sh.p_full[t], 8);  // 4 warps of weights, 4 of O_t
-            mbar_init(&sh.m_ready[t], 4);
+            mbar_init(&sh.p_full[t], 4);
+            mbar_init(&sh.p_rest[t], 4);
+            mbar_init(&sh.sum_ready[t], 4);
             mbar_init(&sh.pv_done[t], 1);
         }
         for (int i = 0; i < C::STAGES; ++i) {
@@ -261,11 +268,19 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         const int t = warp >> 2, row = tid & 127;
         const uint32_t lane_base = (uint32_t)(warp & 3) * 32;
         const uint32_t s_addr = tmem_addr(tmem, lane_base, t * C::S_COL);
+        const uint32_t o_addr = tmem_addr(tmem, lane_base, C::O_BASE + t * D);
         const int32_t tok = job.q0[t] + row / a.G;
         const float c2 = a.scale * kLog2e;
         const int32_t n = t == 0 ? job.nk[0] : job.nk[1];
         float ref = -INFINITY, sum = 0.f;  // the reference times c2
         for (int32_t j = 0; j < n; ++j) {
+            if ((warp & 3) == 0) {
+                // the MMAs that follow these weights read V_j and K_j+1: their
+                // arrival is waited for here, where there is time
+                const uint32_t ev = 2 * j + 1, ek = 2 * j + 2;
+                if (!wait_warp(&sh.kv_full[ev % C::STAGES], ev / C::STAGES)) break;
+                if (j + 1 < n && !wait_warp(&sh.kv_full[ek % C::STAGES], ek / C::STAGES)) break;
+            }
             if (!wait_warp(&sh.s_full[t], j)) break;
             tc_fence_after();
             float s[128];
@@ -283,29 +298,39 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 for (int i = 0; i < 128; ++i)
                     if (i > seen) s[i] = -INFINITY;
             }
-            float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
+            float m[4];
 #pragma unroll
-            for (int i = 4; i < 128; i += 4) {
-                m0 = fmaxf(m0, s[i]);
-                m1 = fmaxf(m1, s[i + 1]);
-                m2 = fmaxf(m2, s[i + 2]);
-                m3 = fmaxf(m3, s[i + 3]);
+            for (int i = 0; i < 4; ++i) m[i] = fmaxf(s[i], s[i + 4]);
+#pragma unroll
+            for (int i = 8; i < 128; i += 8)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) m[e] = max3(m[e], s[i + e], s[i + e + 4]);
+            const float top = fmaxf(max3(m[0], m[1], m[2]), m[3]) * c2;
+            const bool move = !(top - ref <= kMoveBy);  // also on the first tile
+            if (__any_sync(0xffffffffu, move)) {
+                float f = 1.f;
+                if (move) {
+                    const float next = fmaxf(ref, top);
+                    // a row whose scores are all -inf so far keeps weights of 0
+                    f = exp2_approx(ref - (next == -INFINITY ? 0.f : next));
+                    sum *= f;
+                    ref = next;
+                }
+                __syncwarp();
+                // rescale the row's outputs: S_j came after the product of
+                // tile j - 1, so O is at rest
+                if (j > 0) {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        float x[16];
+                        tmem_ld16(o_addr + c, x);
+                        uint32_t y[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(x[i] * f);
+                        st16_nowait(o_addr + c, y);
+                    }
+                }
             }
-            const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * c2;
-            if (!(top - ref <= kMoveBy)) {  // also on the first tile
-                const float next = fmaxf(ref, top);
-                // a row whose scores are all -inf so far keeps weights of 0
-                const float to = next == -INFINITY ? 0.f : next;
-                const float f = exp2_approx(ref - to);
-                if (j > 0) sh.scale[t][row] = f;
-                sum *= f;
-                ref = next;
-            } else if (j > 0) {
-                sh.scale[t][row] = 1.f;
-            }
-            __syncwarp();
-            if (j > 0 && lane == 0) mbar_arrive(&sh.m_ready[t]);
-            __syncwarp();
             const float neg = ref == -INFINITY ? 0.f : -ref;
             const float2 c22 = make_float2(c2, c2), neg2 = make_float2(neg, neg);
             float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
@@ -322,67 +347,39 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     p[i] = pack_bf16x2(x.x, x.y);
                 }
                 st16_nowait(s_addr + h * 16, p);
+                if (h >= 2) {
+                    // the product starts on the first kEarly keys' weights
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(h == 2 ? &sh.p_full[t] : &sh.p_rest[t]);
+                    __syncwarp();
+                }
             }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_full[t]);
-            __syncwarp();
             acc0 = f2_add(acc0, acc1);
             sum += acc0.x + acc0.y;
         }
         if (n > 0) {
             sh.sum[t][row] = sum;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.m_ready[t]);
+            if (lane == 0) mbar_arrive(&sh.sum_ready[t]);
             const int tk = row / a.G;
             if (a.lse && tk < (t == 0 ? job.nt[0] : job.nt[1]))
                 a.lse[((int64_t)begin + tok) * a.HQ + (int64_t)kvh * a.G + (row - tk * a.G)] =
                     (ref + log2f(sum)) * kLn2;
         }
     } else if (warp < 12) {
-        // ---- rescaling and results --------------------------------------
+        // ---- results ----------------------------------------------------
         regs_dec<80>();
         const int row = tid & 127;
         const uint32_t lane_base = (uint32_t)(warp & 3) * 32;
         bool ok = true;
-        for (int32_t j = 0; j < job.n && ok; ++j) {
-#pragma unroll 1
-            for (int t = 0; t < 2 && ok; ++t) {
-                if (j >= job.nk[t]) continue;
-                if (j == 0) {  // the first product overwrites O_t
-                    if (lane == 0) mbar_arrive(&sh.p_full[t]);
-                    continue;
-                }
-                ok = wait_warp(&sh.m_ready[t], j - 1);
-                if (!ok) break;
-                const float f = sh.scale[t][row];
-                if (__any_sync(0xffffffffu, f != 1.f)) {
-                    ok = wait_warp(&sh.pv_done[t], j - 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t o = tmem_addr(tmem, lane_base, C::O_BASE + t * D);
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        float x[32];
-                        ld32_nowait(o + c, x);
-                        wait_ld32(x);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] *= f;
-                        tmem_st32(o + c, x);
-                    }
-                    tc_fence_before();
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_full[t]);
-                __syncwarp();
-            }
-        }
 #pragma unroll 1
         for (int t = 0; t < 2 && ok; ++t) {
             const int32_t n = job.nk[t];
             if (n == 0) continue;
-            ok = wait_warp(&sh.m_ready[t], n - 1) && wait_warp(&sh.pv_done[t], n - 1);
+            // (the sums come after S_n-1, so only the last product is open)
+            ok = wait_warp(&sh.sum_ready[t], 0) && wait_warp(&sh.pv_done[t], n - 1);
             if (!ok) break;
             tc_fence_after();
             const int32_t tk = row / a.G;
@@ -432,74 +429,58 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         regs_dec<48>();
         if (warp == 12) {
             // ---- MMAs ---------------------------------------------------
-            const uint32_t q_base = smem_u32(sq), kv_base = smem_u32(skv);
-            auto scores = [&](int t, uint32_t stage) {
-                const uint64_t qd = sdesc_sw128(q_base + t * C::TILE);
-                const uint64_t kd = sdesc_sw128(kv_base + stage * C::TILE);
-                if (elect_one()) {
+            if (elect_one()) {
+                const uint32_t q_base = smem_u32(sq), kv_base = smem_u32(skv);
+                auto scores = [&](int t, uint32_t stage) {
+                    const uint64_t qd = sdesc_sw128(q_base + t * C::TILE);
+                    const uint64_t kd = sdesc_sw128(kv_base + stage * C::TILE);
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
                         const uint32_t step = ((ks >> 2) * C::PANEL + (ks & 3) * 32) >> 4;
                         mma_half(tmem + t * C::S_COL, qd + step, kd + step, C::IDESC_QK, ks > 0);
                     }
                     mma_commit(&sh.s_full[t]);
-                }
-                __syncwarp();
-            };
-            bool ok = true;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (job.nk[t] == 0 || !ok) continue;
-                ok = wait_warp(&sh.q_full[t], 0) && (t > 0 || wait_warp(&sh.kv_full[0], 0));
-                if (!ok) break;
-                tc_fence_after();
-                scores(t, 0);
-            }
-            if (ok && elect_one()) mma_commit(&sh.kv_empty[0]);
-            __syncwarp();
-            for (int32_t j = 0; j < job.n && ok; ++j) {
-                const uint32_t ev = 2 * j + 1, ek = 2 * j + 2;
-                const uint32_t sv = ev % C::STAGES, sk = ek % C::STAGES;
-                const uint64_t vd = sdesc_mn(kv_base + sv * C::TILE, C::PANEL);
-                // both tiles of the step before its first product, so that
-                // nothing but the weights stands before an MMA
-                ok = wait_warp(&sh.kv_full[sv], ev / C::STAGES) &&
-                     (j + 1 >= job.n || wait_warp(&sh.kv_full[sk], ek / C::STAGES));
-                if (!ok) break;
+                };
+                bool ok = true;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    if (j >= job.nk[t] || !ok) continue;
-                    ok = wait_warp(&sh.p_full[t], j);
+                    if (job.nk[t] == 0 || !ok) continue;
+                    ok = wait(&sh.q_full[t], 0) && (t > 0 || wait(&sh.kv_full[0], 0));
                     if (!ok) break;
                     tc_fence_after();
-                    const bool more = j + 1 < job.nk[t];
-                    const uint64_t qd = sdesc_sw128(q_base + t * C::TILE);
-                    const uint64_t kd = sdesc_sw128(kv_base + sk * C::TILE);
-                    if (elect_one()) {
+                    scores(t, 0);
+                }
+                if (ok) mma_commit(&sh.kv_empty[0]);
+                for (int32_t j = 0; j < job.n && ok; ++j) {
+                    const uint32_t sv = (2 * j + 1) % C::STAGES, sk = (2 * j + 2) % C::STAGES;
+                    const uint64_t vd = sdesc_mn(kv_base + sv * C::TILE, C::PANEL);
 #pragma unroll
-                        for (int ks = 0; ks < kKeyTile / 16; ++ks)
+                    for (int t = 0; t < 2; ++t) {
+                        if (j >= job.nk[t] || !ok) continue;
+                        auto product = [&](int ks) {
                             mma_tmem_a(tmem + C::O_BASE + t * D, tmem + t * C::S_COL + ks * 8,
                                        vd + ks * (2048 >> 4), C::IDESC_PV, (j > 0 || ks > 0) ? 1u : 0u);
-                        mma_commit(&sh.pv_done[t]);
-                        if (more) {
+                        };
+                        // V_j and K_j+1 have arrived when the weights have
+                        ok = wait(&sh.p_full[t], j);
+                        if (!ok) break;
+                        tc_fence_after();
 #pragma unroll
-                            for (int ks = 0; ks < D / 16; ++ks) {
-                                const uint32_t step = ((ks >> 2) * C::PANEL + (ks & 3) * 32) >> 4;
-                                mma_half(tmem + t * C::S_COL, qd + step, kd + step, C::IDESC_QK,
-                                         ks > 0);
-                            }
-                            mma_commit(&sh.s_full[t]);
-                        }
+                        for (int ks = 0; ks < kEarly / 16; ++ks) product(ks);
+                        ok = wait(&sh.p_rest[t], j);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int ks = kEarly / 16; ks < kKeyTile / 16; ++ks) product(ks);
+                        mma_commit(&sh.pv_done[t]);
+                        if (j + 1 < job.nk[t]) scores(t, sk);
                     }
-                    __syncwarp();
-                }
-                if (!ok) break;
-                if (elect_one()) {
+                    if (!ok) break;
                     mma_commit(&sh.kv_empty[sv]);
                     if (j + 1 < job.n) mma_commit(&sh.kv_empty[sk]);
                 }
-                __syncwarp();
             }
+            __syncwarp();
         } else if (warp == 13) {
             // ---- copies -------------------------------------------------
             if (lane == 0) {
