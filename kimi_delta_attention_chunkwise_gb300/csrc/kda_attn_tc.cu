@@ -16,9 +16,16 @@
 //     O_t (+)= P_t V_j         tcgen05, A = P_t from TMEM, V_j as it lies
 //
 // The two row tiles alternate: while the softmax of one runs, the tensor core
-// works for the other.  Warps: 0-3 and 4-7 the softmax of tile 0 and 1, 8-11
-// rescale the O_t when a row's reference moves and write the results, 12
-// issues the MMAs, 13 the copies, 14-15 make masked values harmless.
+// works for the other.  Warps: 0-3 and 4-7 the softmax and the results of tile
+// 0 and 1, 8 issues the MMAs, 9 the copies and finds the work, 10-11 make
+// masked values harmless and see to it that tiles have arrived.
+//
+// A CTA works on one item (two row tiles of one key-value head) after another:
+// when it has begun one, it takes the grid's next block that has not started
+// (clusterlaunchcontrol), so that the next item's first copies and scores run
+// beside the last item's results, and long and short items even out.  Items
+// are numbered with a sequence's last tiles first (the longest under the
+// causal mask).
 //
 // The reference of a row moves only when the row's maximum has passed it by
 // more than 2^8: until then the weights stay below 2^8, which costs fp32 sums
@@ -30,7 +37,7 @@
 //
 // Masked places: scores are masked by selection, so masked keys are free to
 // hold anything.  A masked weight is an exact 0, but 0 times an infinity or a
-// NaN in a value row is NaN: warps 14-15 look through every value tile that
+// NaN in a value row is NaN: warps 10-11 look through every value tile that
 // holds a masked place before the MMA reads it, set the rows behind the CTA's
 // last token to zero and replace non-finite values by zero; if there were
 // any, the rows that do see them get them added at the end (`bad`).
@@ -51,7 +58,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 384;
 constexpr int kRowTile = 128, kKeyTile = 128;
 constexpr long long kWaitLimit = 2000000000LL;  // SM clocks, about a second
 constexpr float kLn2 = 0.6931471805599453f;
@@ -69,13 +76,31 @@ struct Cfg {
     static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D) | (1u << 16);  // V is N-major
 };
 
+// What a CTA works on: two row tiles of one key-value head.
+struct Job {
+    int32_t begin, len;  // the sequence's tokens in the packed axis
+    int32_t kvh;
+    int32_t q0[2];       // first token of each row tile
+    int32_t nt[2];       // tokens of each row tile (0: none)
+    int32_t nk[2];       // key tiles of each row tile
+    int32_t n;           // key tiles of the item (0: no more work)
+    int32_t last;        // the item's last token
+    int32_t first_mask;  // first key tile with a masked place
+};
+
+constexpr int kJobs = 2;      // items known at a time
+constexpr int kMasked = 4;    // masked value tiles in flight at most: the ring holds no more
+constexpr int kJobUsers = 11; // warps that read a job: 0-8, 10, 11
+
 struct Shared {
-    uint64_t q_full[2], kv_full[8], kv_empty[8], v_raw[3], v_half[3];
-    uint64_t s_full[2], p_full[2], p_rest[2], sum_ready[2], pv_done[2], drained;
+    uint64_t q_full[2], q_empty[2], kv_full[8], kv_empty[8], v_raw[kMasked], v_half[kMasked];
+    uint64_t s_full[2], p_full[2], p_rest[2], pv_done[2], o_free[2];
+    uint64_t job_full[kJobs], job_empty[kJobs], next_full, drained;
+    uint4 next;  // the answer to the request for another block
+    Job job[kJobs];
+    int32_t bad[kJobs];
     uint32_t tmem;
-    int32_t found, abort, bad;
-    SeqTile tile;
-    float sum[2][kRowTile];
+    int32_t abort;
 };
 
 // The tiles start at the dynamic shared memory's base, which is 1024-byte
@@ -171,16 +196,31 @@ __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// What the CTA works on.
-struct Job {
-    int32_t len;        // tokens of the sequence
-    int32_t q0[2];      // first token of each row tile
-    int32_t nt[2];      // tokens of each row tile (0: none)
-    int32_t nk[2];      // key tiles of each row tile
-    int32_t n;          // key tiles of the CTA
-    int32_t last;       // the CTA's last token
-    int32_t first_mask; // first key tile with a masked place
-};
+// Asks for a block of the grid that has not started, to be worked on here;
+// 16 bytes of answer go to `to`.
+__device__ __forceinline__ void request_block(uint4 *to, uint64_t *bar) {
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+        "[%0], [%1];" ::"r"(smem_u32(to)),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ bool answered_block(const uint4 *from, uint32_t &index) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+        : "=&r"(got), "=&r"(x)
+        : "r"(smem_u32(from))
+        : "memory");
+    index = x;
+    return got != 0;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -197,381 +237,465 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int32_t R = kRowTile / a.G;  // tokens of a row tile
 
-    if (warp == 0) {
-        SeqTile t;
-        const bool ok = find_seq_tile(a.cu_seqlens, a.N, a.T, 1, 2 * R, blockIdx.x / a.HKV, t);
-        if (lane == 0) {
-            sh.found = ok;
-            if (ok) sh.tile = t;
-            sh.abort = 0;
-            sh.bad = 0;
-        }
-    } else if (warp == 1 && lane == 0) {
+    if (warp == 0 && lane == 0) {
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sh.q_full[t], 1);
+            mbar_init(&sh.q_empty[t], 1);
             mbar_init(&sh.s_full[t], 1);
-            mbar_init(&sh.p_full[t], 4);
+            mbar_init(&sh.p_full[t], 5);  // four warps of weights, and K and V have arrived
             mbar_init(&sh.p_rest[t], 4);
-            mbar_init(&sh.sum_ready[t], 4);
             mbar_init(&sh.pv_done[t], 1);
+            mbar_init(&sh.o_free[t], 4);
         }
         for (int i = 0; i < C::STAGES; ++i) {
             mbar_init(&sh.kv_full[i], 1);
             mbar_init(&sh.kv_empty[i], 1);
         }
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < kMasked; ++i) {
             mbar_init(&sh.v_raw[i], 1);
             mbar_init(&sh.v_half[i], 2);
         }
+        for (int i = 0; i < kJobs; ++i) {
+            mbar_init(&sh.job_full[i], 1);
+            mbar_init(&sh.job_empty[i], kJobUsers);
+        }
+        mbar_init(&sh.next_full, 1);
         mbar_init(&sh.drained, 1);
+        sh.abort = 0;
         fence_mbar_init();
-    }
-    __syncthreads();
-    if (!sh.found) return;
-    if (warp == 12) {
+        fence_proxy_async();
+    } else if (warp == 8) {
         tmem_alloc(&sh.tmem, 512);
         tmem_relinquish();
+    } else if (warp == 9 && lane < 3) {
+        const CUtensorMap *m = lane == 0 ? &map_q : lane == 1 ? &map_k : &map_v;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    const int32_t kvh = blockIdx.x % a.HKV, begin = sh.tile.begin;
-    Job job;
-    job.len = sh.tile.end - begin;
-    job.n = 0;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        job.q0[t] = (sh.tile.tile * 2 + t) * R;
-        job.nt[t] = min(max(job.len - job.q0[t], 0), R);
-        job.nk[t] = job.nt[t] > 0 ? (job.q0[t] + job.nt[t] - 1) / kKeyTile + 1 : 0;
-        job.n = max(job.n, job.nk[t]);
-    }
-    job.last = min(job.q0[0] + 2 * R, job.len) - 1;
-    job.first_mask = (job.q0[0] + 1) / kKeyTile;
 
-    auto wait = [&](uint64_t *bar, uint32_t phase) -> bool {
-        if (mbar_try_wait(bar, phase & 1)) return true;
-        if (mbar_wait_bounded(bar, phase & 1, kWaitLimit)) return true;
+    // Waits of one thread and of a whole warp (which goes on or gives up
+    // together).  `use` counts the barrier's phases.
+    auto wait = [&](uint64_t *bar, uint32_t use) -> bool {
+        if (mbar_try_wait(bar, use & 1)) return true;
+        if (mbar_wait_bounded(bar, use & 1, kWaitLimit)) return true;
         sh.abort = 1;
         *a.status = KDA_ERR_TIMEOUT;
         return false;
     };
-    // the same for a whole warp, which goes on or gives up together
-    auto wait_warp = [&](uint64_t *bar, uint32_t phase) -> bool {
-        return __all_sync(0xffffffffu, wait(bar, phase));
+    auto wait_warp = [&](uint64_t *bar, uint32_t use) -> bool {
+        return __all_sync(0xffffffffu, wait(bar, use));
+    };
+    auto arrive_warp = [&](uint64_t *bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
     };
 
     if (warp < 8) {
-        // ---- softmax: one thread per row --------------------------------
-        regs_inc<192>();
+        // ---- softmax and results: one thread per row ---------------------
+        regs_inc<208>();
         const int t = warp >> 2, row = tid & 127;
         const uint32_t lane_base = (uint32_t)(warp & 3) * 32;
         const uint32_t s_addr = tmem_addr(tmem, lane_base, t * C::S_COL);
         const uint32_t o_addr = tmem_addr(tmem, lane_base, C::O_BASE + t * D);
-        const int32_t tok = job.q0[t] + row / a.G;
+        const int tk = row / a.G;  // the row's token within the tile
         const float c2 = a.scale * kLog2e;
-        const int32_t n = t == 0 ? job.nk[0] : job.nk[1];
-        float ref = -INFINITY, sum = 0.f;  // the reference times c2
-        for (int32_t j = 0; j < n; ++j) {
-            if ((warp & 3) == 0) {
-                // the MMAs that follow these weights read V_j and K_j+1: their
-                // arrival is waited for here, where there is time
-                const uint32_t ev = 2 * j + 1, ek = 2 * j + 2;
-                if (!wait_warp(&sh.kv_full[ev % C::STAGES], ev / C::STAGES)) break;
-                if (j + 1 < n && !wait_warp(&sh.kv_full[ek % C::STAGES], ek / C::STAGES)) break;
-            }
-            if (!wait_warp(&sh.s_full[t], j)) break;
-            tc_fence_after();
-            float s[128];
-            ld32_nowait(s_addr, s);
-            ld32_nowait(s_addr + 32, s + 32);
-            ld32_nowait(s_addr + 64, s + 64);
-            ld32_nowait(s_addr + 96, s + 96);
-            wait_ld32(s);
-            wait_ld32(s + 32);
-            wait_ld32(s + 64);
-            wait_ld32(s + 96);
-            const int32_t seen = tok - j * kKeyTile;  // columns up to this one are seen
-            if ((j + 1) * kKeyTile - 1 > job.q0[t]) {
+        uint32_t it = 0;  // key tiles of this row tile so far
+        for (uint32_t item = 0;; ++item) {
+            const Job &job = sh.job[item % kJobs];
+            if (!wait_warp(&sh.job_full[item % kJobs], item / kJobs) || job.n == 0) break;
+            const int32_t n = job.nk[t], q0 = job.q0[t], tok = q0 + tk;
+            float ref = -INFINITY, sum = 0.f;  // the reference times c2
+            bool ok = true;
+            for (int32_t j = 0; j < n; ++j) {
+                ok = wait_warp(&sh.s_full[t], it + j);
+                if (!ok) break;
+                tc_fence_after();
+                float s[128];
+                ld32_nowait(s_addr, s);
+                ld32_nowait(s_addr + 32, s + 32);
+                ld32_nowait(s_addr + 64, s + 64);
+                ld32_nowait(s_addr + 96, s + 96);
+                wait_ld32(s);
+                wait_ld32(s + 32);
+                wait_ld32(s + 64);
+                wait_ld32(s + 96);
+                const int32_t seen = tok - j * kKeyTile;  // columns up to this one are seen
+                if ((j + 1) * kKeyTile - 1 > q0) {
 #pragma unroll
-                for (int i = 0; i < 128; ++i)
-                    if (i > seen) s[i] = -INFINITY;
-            }
-            float m[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) m[i] = fmaxf(s[i], s[i + 4]);
-#pragma unroll
-            for (int i = 8; i < 128; i += 8)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) m[e] = max3(m[e], s[i + e], s[i + e + 4]);
-            const float top = fmaxf(max3(m[0], m[1], m[2]), m[3]) * c2;
-            const bool move = !(top - ref <= kMoveBy);  // also on the first tile
-            if (__any_sync(0xffffffffu, move)) {
-                float f = 1.f;
-                if (move) {
-                    const float next = fmaxf(ref, top);
-                    // a row whose scores are all -inf so far keeps weights of 0
-                    f = exp2_approx(ref - (next == -INFINITY ? 0.f : next));
-                    sum *= f;
-                    ref = next;
+                    for (int i = 0; i < 128; ++i)
+                        if (i > seen) s[i] = -INFINITY;
                 }
-                __syncwarp();
-                // rescale the row's outputs: S_j came after the product of
-                // tile j - 1, so O is at rest
-                if (j > 0) {
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
-                        float x[16];
-                        tmem_ld16(o_addr + c, x);
-                        uint32_t y[16];
+                float m[4];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(x[i] * f);
-                        st16_nowait(o_addr + c, y);
+                for (int i = 0; i < 4; ++i) m[i] = fmaxf(s[i], s[i + 4]);
+#pragma unroll
+                for (int i = 8; i < 128; i += 8)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) m[e] = max3(m[e], s[i + e], s[i + e + 4]);
+                const float top = fmaxf(max3(m[0], m[1], m[2]), m[3]) * c2;
+                const bool move = !(top - ref <= kMoveBy);  // also on the first tile
+                if (__any_sync(0xffffffffu, move)) {
+                    float f = 1.f;
+                    if (move) {
+                        const float next = fmaxf(ref, top);
+                        // a row whose scores are all -inf so far keeps weights of 0
+                        f = exp2_approx(ref - (next == -INFINITY ? 0.f : next));
+                        sum *= f;
+                        ref = next;
+                    }
+                    __syncwarp();
+                    // rescale the row's outputs: S_j came after the product of
+                    // tile j - 1, so O is at rest
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            float x[16];
+                            tmem_ld16(o_addr + c, x);
+                            uint32_t y[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(x[i] * f);
+                            st16_nowait(o_addr + c, y);
+                        }
                     }
                 }
-            }
-            const float neg = ref == -INFINITY ? 0.f : -ref;
-            const float2 c22 = make_float2(c2, c2), neg2 = make_float2(neg, neg);
-            float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
+                const float neg = ref == -INFINITY ? 0.f : -ref;
+                const float2 c22 = make_float2(c2, c2), neg2 = make_float2(neg, neg);
+                float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                uint32_t p[16];
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t p[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float2 x = f2_fma(make_float2(s[h * 32 + 2 * i], s[h * 32 + 2 * i + 1]), c22, neg2);
-                    x.x = exp2_approx(x.x);
-                    x.y = exp2_approx(x.y);
-                    if (i & 1) acc1 = f2_add(acc1, x);
-                    else acc0 = f2_add(acc0, x);
-                    p[i] = pack_bf16x2(x.x, x.y);
+                    for (int i = 0; i < 16; ++i) {
+                        float2 x = f2_fma(make_float2(s[h * 32 + 2 * i], s[h * 32 + 2 * i + 1]), c22,
+                                          neg2);
+                        x.x = exp2_approx(x.x);
+                        x.y = exp2_approx(x.y);
+                        if (i & 1) acc1 = f2_add(acc1, x);
+                        else acc0 = f2_add(acc0, x);
+                        p[i] = pack_bf16x2(x.x, x.y);
+                    }
+                    st16_nowait(s_addr + h * 16, p);
+                    if (h >= 2) {
+                        // the product starts on the first kEarly keys' weights
+                        tmem_wait_st();
+                        tc_fence_before();
+                        arrive_warp(h == 2 ? &sh.p_full[t] : &sh.p_rest[t]);
+                        __syncwarp();
+                    }
                 }
-                st16_nowait(s_addr + h * 16, p);
-                if (h >= 2) {
-                    // the product starts on the first kEarly keys' weights
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(h == 2 ? &sh.p_full[t] : &sh.p_rest[t]);
-                    __syncwarp();
-                }
+                acc0 = f2_add(acc0, acc1);
+                sum += acc0.x + acc0.y;
             }
-            acc0 = f2_add(acc0, acc1);
-            sum += acc0.x + acc0.y;
-        }
-        if (n > 0) {
-            sh.sum[t][row] = sum;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.sum_ready[t]);
-            const int tk = row / a.G;
-            if (a.lse && tk < (t == 0 ? job.nt[0] : job.nt[1]))
-                a.lse[((int64_t)begin + tok) * a.HQ + (int64_t)kvh * a.G + (row - tk * a.G)] =
-                    (ref + log2f(sum)) * kLn2;
-        }
-    } else if (warp < 12) {
-        // ---- results ----------------------------------------------------
-        regs_dec<80>();
-        const int row = tid & 127;
-        const uint32_t lane_base = (uint32_t)(warp & 3) * 32;
-        bool ok = true;
-#pragma unroll 1
-        for (int t = 0; t < 2 && ok; ++t) {
-            const int32_t n = job.nk[t];
-            if (n == 0) continue;
-            // (the sums come after S_n-1, so only the last product is open)
-            ok = wait_warp(&sh.sum_ready[t], 0) && wait_warp(&sh.pv_done[t], n - 1);
             if (!ok) break;
-            tc_fence_after();
-            const int32_t tk = row / a.G;
-            const float inv = 1.f / sh.sum[t][row];
-            const int64_t token = (int64_t)begin + job.q0[t] + tk;
-            const int64_t head = (int64_t)kvh * a.G + (row - tk * a.G);
-            const bool mine = tk < job.nt[t];
-            const uint32_t o = tmem_addr(tmem, lane_base, C::O_BASE + t * D);
+            if (n > 0) {
+                // results (S_n-1 came after the product of tile n - 2, so only
+                // the last product is open)
+                if (!wait_warp(&sh.pv_done[t], it + n - 1)) break;
+                tc_fence_after();
+                const float inv = 1.f / sum;
+                const int64_t token = (int64_t)job.begin + tok;
+                const int64_t head = (int64_t)job.kvh * a.G + (row - tk * a.G);
+                const bool mine = tk < job.nt[t];
+                const bool bad = sh.bad[item % kJobs] != 0;
+                if (mine && a.lse) a.lse[token * a.HQ + head] = (ref + log2f(sum)) * kLn2;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                float x[32];
-                __syncwarp();  // the load is the whole warp's
-                ld32_nowait(o + c, x);
-                wait_ld32(x);
+                for (int c = 0; c < D; c += 32) {
+                    float x[32];
+                    __syncwarp();  // the load is the whole warp's
+                    ld32_nowait(o_addr + c, x);
+                    wait_ld32(x);
+                    if (c + 32 == D) {
+                        tc_fence_before();
+                        arrive_warp(&sh.o_free[t]);
+                    }
+                    if (!mine) continue;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] *= inv;
-                if (!mine) continue;
-                if (sh.bad) {
-                    // non-finite values of the tiles that were looked through
-                    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) +
-                                             (int64_t)begin * a.v_stride + (int64_t)kvh * D + c;
-                    for (int32_t k = job.first_mask * kKeyTile; k <= job.q0[t] + tk; ++k)
+                    for (int i = 0; i < 32; ++i) x[i] *= inv;
+                    if (bad) {
+                        // non-finite values of the tiles that were looked through
+                        const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) +
+                                                 (int64_t)job.begin * a.v_stride +
+                                                 (int64_t)job.kvh * D + c;
+                        for (int32_t k = job.first_mask * kKeyTile; k <= tok; ++k)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float y = __bfloat162float(v[k * a.v_stride + i]);
-                            if (!isfinite(y)) x[i] += y;
-                        }
+                            for (int i = 0; i < 32; ++i) {
+                                const float y = __bfloat162float(v[k * a.v_stride + i]);
+                                if (!isfinite(y)) x[i] += y;
+                            }
+                    }
+                    const int64_t at = (token * a.HQ + head) * D + c;
+                    if (a.out_f32) {
+                        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                    } else {
+                        uint4 *dst =
+                            reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            dst[i] = make_uint4(pack_bf16x2(x[8 * i], x[8 * i + 1]),
+                                                pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
+                                                pack_bf16x2(x[8 * i + 4], x[8 * i + 5]),
+                                                pack_bf16x2(x[8 * i + 6], x[8 * i + 7]));
+                    }
                 }
-                const int64_t at = (token * a.HQ + head) * D + c;
-                if (a.out_f32) {
-                    float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-                } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        dst[i] = make_uint4(pack_bf16x2(x[8 * i], x[8 * i + 1]),
-                                            pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
-                                            pack_bf16x2(x[8 * i + 4], x[8 * i + 5]),
-                                            pack_bf16x2(x[8 * i + 6], x[8 * i + 7]));
-                }
+                it += n;
             }
+            arrive_warp(&sh.job_empty[item % kJobs]);
+            __syncwarp();
         }
     } else {
-        regs_dec<48>();
-        if (warp == 12) {
+        regs_dec<88>();
+        if (warp == 8) {
             // ---- MMAs ---------------------------------------------------
             if (elect_one()) {
                 const uint32_t q_base = smem_u32(sq), kv_base = smem_u32(skv);
-                auto scores = [&](int t, uint32_t stage) {
-                    const uint64_t qd = sdesc_sw128(q_base + t * C::TILE);
-                    const uint64_t kd = sdesc_sw128(kv_base + stage * C::TILE);
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t step = ((ks >> 2) * C::PANEL + (ks & 3) * 32) >> 4;
-                        mma_half(tmem + t * C::S_COL, qd + step, kd + step, C::IDESC_QK, ks > 0);
-                    }
-                    mma_commit(&sh.s_full[t]);
-                };
+                uint32_t e0 = 0, it[2] = {0, 0}, used[2] = {0, 0};
                 bool ok = true;
+                for (uint32_t item = 0; ok; ++item) {
+                    if (!wait(&sh.job_full[item % kJobs], item / kJobs)) break;
+                    const Job &job = sh.job[item % kJobs];
+                    const int32_t n = job.n, nk[2] = {job.nk[0], job.nk[1]};
+                    if (n == 0) break;
+                    // S_t of key tile j from the ring's `stage`; the last one
+                    // frees the queries
+                    auto scores = [&](int t, int32_t j, uint32_t stage) {
+                        const uint64_t qd = sdesc_sw128(q_base + t * C::TILE);
+                        const uint64_t kd = sdesc_sw128(kv_base + stage * C::TILE);
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (job.nk[t] == 0 || !ok) continue;
-                    ok = wait(&sh.q_full[t], 0) && (t > 0 || wait(&sh.kv_full[0], 0));
-                    if (!ok) break;
-                    tc_fence_after();
-                    scores(t, 0);
-                }
-                if (ok) mma_commit(&sh.kv_empty[0]);
-                for (int32_t j = 0; j < job.n && ok; ++j) {
-                    const uint32_t sv = (2 * j + 1) % C::STAGES, sk = (2 * j + 2) % C::STAGES;
-                    const uint64_t vd = sdesc_mn(kv_base + sv * C::TILE, C::PANEL);
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            const uint32_t step = ((ks >> 2) * C::PANEL + (ks & 3) * 32) >> 4;
+                            mma_half(tmem + t * C::S_COL, qd + step, kd + step, C::IDESC_QK, ks > 0);
+                        }
+                        mma_commit(&sh.s_full[t]);
+                        if (j == nk[t] - 1) mma_commit(&sh.q_empty[t]);
+                    };
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        if (j >= job.nk[t] || !ok) continue;
-                        auto product = [&](int ks) {
-                            mma_tmem_a(tmem + C::O_BASE + t * D, tmem + t * C::S_COL + ks * 8,
-                                       vd + ks * (2048 >> 4), C::IDESC_PV, (j > 0 || ks > 0) ? 1u : 0u);
-                        };
-                        // V_j and K_j+1 have arrived when the weights have
-                        ok = wait(&sh.p_full[t], j);
+                        if (nk[t] == 0 || !ok) continue;
+                        ok = wait(&sh.q_full[t], used[t]) &&
+                             (t > 0 || wait(&sh.kv_full[e0 % C::STAGES], e0 / C::STAGES));
                         if (!ok) break;
                         tc_fence_after();
-#pragma unroll
-                        for (int ks = 0; ks < kEarly / 16; ++ks) product(ks);
-                        ok = wait(&sh.p_rest[t], j);
-                        if (!ok) break;
-                        tc_fence_after();
-#pragma unroll
-                        for (int ks = kEarly / 16; ks < kKeyTile / 16; ++ks) product(ks);
-                        mma_commit(&sh.pv_done[t]);
-                        if (j + 1 < job.nk[t]) scores(t, sk);
+                        scores(t, 0, e0 % C::STAGES);
                     }
                     if (!ok) break;
-                    mma_commit(&sh.kv_empty[sv]);
-                    if (j + 1 < job.n) mma_commit(&sh.kv_empty[sk]);
+                    mma_commit(&sh.kv_empty[e0 % C::STAGES]);
+                    for (int32_t j = 0; j < n && ok; ++j) {
+                        const uint32_t sv = (e0 + 2 * j + 1) % C::STAGES;
+                        const uint32_t sk = (e0 + 2 * j + 2) % C::STAGES;
+                        const uint64_t vd = sdesc_mn(kv_base + sv * C::TILE, C::PANEL);
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (j >= nk[t] || !ok) continue;
+                            auto product = [&](int ks) {
+                                mma_tmem_a(tmem + C::O_BASE + t * D, tmem + t * C::S_COL + ks * 8,
+                                           vd + ks * (2048 >> 4), C::IDESC_PV,
+                                           (j > 0 || ks > 0) ? 1u : 0u);
+                            };
+                            // the last item's O_t has been read; V_j and K_j+1
+                            // have arrived when the weights have
+                            ok = (j > 0 || used[t] == 0 || wait(&sh.o_free[t], used[t] - 1)) &&
+                                 wait(&sh.p_full[t], it[t] + j);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int ks = 0; ks < kEarly / 16; ++ks) product(ks);
+                            ok = wait(&sh.p_rest[t], it[t] + j);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int ks = kEarly / 16; ks < kKeyTile / 16; ++ks) product(ks);
+                            mma_commit(&sh.pv_done[t]);
+                            if (j + 1 < nk[t]) scores(t, j + 1, sk);
+                        }
+                        if (!ok) break;
+                        mma_commit(&sh.kv_empty[sv]);
+                        if (j + 1 < n) mma_commit(&sh.kv_empty[sk]);
+                    }
+                    e0 += 2 * n;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        it[t] += nk[t];
+                        used[t] += nk[t] > 0;
+                    }
+                    mbar_arrive(&sh.job_empty[item % kJobs]);
                 }
             }
             __syncwarp();
-        } else if (warp == 13) {
-            // ---- copies -------------------------------------------------
-            if (lane == 0) {
-                const uint32_t q_bytes = (uint32_t)(R * a.G) * 128 * C::PANELS;
-                auto load_q = [&](int t) {
-                    if (job.nk[t] == 0) return;
-                    mbar_arrive_expect_tx(&sh.q_full[t], q_bytes);
-                    for (int p = 0; p < C::PANELS; ++p)
-                        tma_load_3d(sq + t * C::TILE + p * C::PANEL, &map_q, p * 64, kvh * a.G,
-                                    begin + job.q0[t], &sh.q_full[t]);
-                };
-                uint32_t loaded = 0;
-                bool ok = true;
-                load_q(0);
-                for (int32_t e = 0; e < 2 * job.n && ok; ++e) {
-                    const uint32_t s = e % C::STAGES;
-                    if (e >= C::STAGES) {
-                        ok = wait(&sh.kv_empty[s], e / C::STAGES - 1);
-                        if (!ok) break;
+        } else if (warp == 9) {
+            // ---- work and copies ----------------------------------------
+            const uint32_t q_bytes = (uint32_t)(R * a.G) * 128 * C::PANELS;
+            uint32_t index = blockIdx.x, e0 = 0, masked = 0, used[2] = {0, 0};
+            bool ok = true, asked = false, have = true;
+            uint32_t item = 0;
+            for (; ok; ++item) {
+                SeqTile st;
+                const bool found = have && find_seq_tile(a.cu_seqlens, a.N, a.T, 1, 2 * R,
+                                                         index / a.HKV, st);
+                Job job;
+                job.n = 0;
+                if (found) {
+                    job.begin = st.begin;
+                    job.len = st.end - st.begin;
+                    job.kvh = index % a.HKV;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        job.q0[t] = (st.tile * 2 + t) * R;
+                        job.nt[t] = min(max(job.len - job.q0[t], 0), R);
+                        job.nk[t] = job.nt[t] > 0 ? (job.q0[t] + job.nt[t] - 1) / kKeyTile + 1 : 0;
+                        job.n = max(job.n, job.nk[t]);
                     }
-                    // a value tile with masked places goes by way of warps 14-15
-                    const int32_t j = e >> 1;
-                    uint64_t *full = (e & 1) && j >= job.first_mask
-                                         ? &sh.v_raw[j - job.first_mask] : &sh.kv_full[s];
-                    mbar_arrive_expect_tx(full, C::TILE);
-                    for (int p = 0; p < C::PANELS; ++p)
-                        tma_load_3d(skv + s * C::TILE + p * C::PANEL, (e & 1) ? &map_v : &map_k,
-                                    p * 64, kvh, begin + j * kKeyTile, full);
-                    loaded = e + 1;
-                    if (e == 0) load_q(1);
+                    job.last = min(job.q0[0] + 2 * R, job.len) - 1;
+                    job.first_mask = (job.q0[0] + 1) / kKeyTile;
                 }
-                // the CTA may end when every copy has landed and every commit
-                // that names a barrier of its shared memory has arrived
+                if (item >= kJobs) ok = wait_warp(&sh.job_empty[item % kJobs], item / kJobs - 1);
+                if (!ok) break;
+                if (lane == 0) {
+                    sh.job[item % kJobs] = job;
+                    sh.bad[item % kJobs] = 0;
+                    mbar_arrive(&sh.job_full[item % kJobs]);
+                }
+                if (!found) break;
+                if (lane == 0) {
+                    auto load_q = [&](int t) {
+                        if (job.nk[t] == 0 || !ok) return;
+                        if (used[t] > 0) ok = wait(&sh.q_empty[t], used[t] - 1);
+                        if (!ok) return;
+                        mbar_arrive_expect_tx(&sh.q_full[t], q_bytes);
+#pragma unroll
+                        for (int p = 0; p < C::PANELS; ++p)
+                            tma_load_3d(sq + t * C::TILE + p * C::PANEL, &map_q, p * 64,
+                                        job.kvh * a.G, job.begin + job.q0[t], &sh.q_full[t]);
+                        ++used[t];
+                    };
+                    load_q(0);
+                    for (int32_t i = 0; i < 2 * job.n && ok; ++i) {
+                        const uint32_t s = e0 % C::STAGES;
+                        // not before the item's last tiles: a CTA with a long
+                        // item ahead would hold a second one back from others
+                        if (i == 2 * job.n - 2) {
+                            request_block(&sh.next, &sh.next_full);
+                            asked = true;
+                        }
+                        if (e0 >= C::STAGES) ok = wait(&sh.kv_empty[s], e0 / C::STAGES - 1);
+                        if (!ok) break;
+                        // a value tile with masked places goes by way of warps 10-11
+                        const int32_t j = i >> 1;
+                        const bool m = (i & 1) && j >= job.first_mask;
+                        uint64_t *full = m ? &sh.v_raw[masked % kMasked] : &sh.kv_full[s];
+                        masked += m;
+                        mbar_arrive_expect_tx(full, C::TILE);
+#pragma unroll
+                        for (int p = 0; p < C::PANELS; ++p)
+                            tma_load_3d(skv + s * C::TILE + p * C::PANEL, (i & 1) ? &map_v : &map_k,
+                                        p * 64, job.kvh, job.begin + j * kKeyTile, full);
+                        ++e0;
+                        if (i == 0) load_q(1);
+                    }
+                }
+                ok = __all_sync(0xffffffffu, ok) && wait_warp(&sh.next_full, item);
+                if (!ok) break;
+                asked = false;
+                have = answered_block(&sh.next, index);
+                fence_proxy_async();  // the answer is read before it is overwritten
+                __syncwarp();
+            }
+            if (lane == 0) {
+                // the CTA may end when every copy and answer has landed and
+                // every commit that names one of its barriers has arrived
+                if (asked) (void)mbar_wait_bounded(&sh.next_full, item & 1, kWaitLimit);
                 for (int t = 0; t < 2; ++t)
-                    if (job.nk[t]) (void)mbar_wait_bounded(&sh.q_full[t], 0, kWaitLimit);
-                for (int32_t j = job.first_mask; j < job.n && 2 * j + 1 < (int32_t)loaded; ++j)
-                    (void)mbar_wait_bounded(&sh.v_raw[j - job.first_mask], 0, kWaitLimit);
-                for (uint32_t e = loaded > C::STAGES ? loaded - C::STAGES : 0; e < loaded; ++e) {
-                    const uint32_t s = e % C::STAGES, phase = (e / C::STAGES) & 1;
-                    (void)mbar_wait_bounded(&sh.kv_full[s], phase, kWaitLimit);
-                    if (ok && !sh.abort) ok = wait(&sh.kv_empty[s], phase);
+                    if (used[t]) {
+                        (void)mbar_wait_bounded(&sh.q_full[t], (used[t] - 1) & 1, kWaitLimit);
+                        if (ok && !sh.abort) ok = wait(&sh.q_empty[t], used[t] - 1);
+                    }
+                for (uint32_t m = masked > kMasked ? masked - kMasked : 0; m < masked; ++m)
+                    (void)mbar_wait_bounded(&sh.v_raw[m % kMasked], (m / kMasked) & 1, kWaitLimit);
+                for (uint32_t e = e0 > C::STAGES ? e0 - C::STAGES : 0; e < e0; ++e) {
+                    if (ok && !sh.abort) ok = wait(&sh.kv_empty[e % C::STAGES], e / C::STAGES);
+                    else (void)mbar_wait_bounded(&sh.kv_full[e % C::STAGES], (e / C::STAGES) & 1, kWaitLimit);
                 }
             }
         } else {
-            // ---- masked value tiles -------------------------------------
-            const int who = tid - 14 * 32;  // 0..63
-            for (int32_t j = job.first_mask; j < job.n; ++j) {
-                const uint32_t ev = 2 * j + 1, sv = ev % C::STAGES;
-                // (a barrier of its own, used once: these warps do not follow
-                // the ring's phases)
-                if (!wait_warp(&sh.v_raw[j - job.first_mask], 0)) break;
-                const int32_t rows = job.last + 1 - j * kKeyTile;  // rows the CTA sees
-                uint8_t *v = skv + sv * C::TILE;
-                bool found = false;
-                for (int i = who; i < C::PANELS * kKeyTile * 8; i += 64) {
-                    const int r = (i >> 3) & (kKeyTile - 1);
-                    uint4 *p = reinterpret_cast<uint4 *>(v + i * 16);
-                    if (r >= rows) {
-                        *p = make_uint4(0, 0, 0, 0);
-                        continue;
-                    }
-                    uint4 x = *p;
-                    uint32_t *w = &x.x;
-                    uint32_t any = 0;
+            // ---- masked value tiles, and arrivals ------------------------
+            const int who = tid - 10 * 32;  // 0..63
+            uint32_t e0 = 0, masked = 0, it[2] = {0, 0};
+            bool ok = true;
+            for (uint32_t item = 0; ok; ++item) {
+                if (!wait_warp(&sh.job_full[item % kJobs], item / kJobs)) break;
+                const Job &job = sh.job[item % kJobs];
+                const int32_t n = job.n, first_mask = job.first_mask, last = job.last;
+                const int32_t nk[2] = {job.nk[0], job.nk[1]};
+                if (n == 0) break;
+                for (int32_t j = warp == 10 ? 0 : first_mask; j < n && ok; ++j) {
+                    const uint32_t ev = e0 + 2 * j + 1, ek = ev + 1, sv = ev % C::STAGES;
+                    if (j >= first_mask) {
+                        const uint32_t mi = masked % kMasked, mu = masked / kMasked;
+                        ++masked;
+                        ok = wait_warp(&sh.v_raw[mi], mu);
+                        if (!ok) break;
+                        const int32_t rows = last + 1 - j * kKeyTile;  // rows the item sees
+                        uint8_t *v = skv + sv * C::TILE;
+                        bool found = false;
+#pragma unroll 4
+                        for (int i = who; i < C::PANELS * kKeyTile * 8; i += 64) {
+                            const int r = (i >> 3) & (kKeyTile - 1);
+                            uint4 *p = reinterpret_cast<uint4 *>(v + i * 16);
+                            uint4 x = r < rows ? *p : make_uint4(0, 0, 0, 0);
+                            uint32_t *w = &x.x;
+                            uint32_t any = 0;
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) any |= (w[b] & 0x7F807F80u) + 0x00800080u;
-                    if (any & 0x80008000u) {  // an exponent of all ones
-                        found = true;
+                            for (int b = 0; b < 4; ++b) any |= (w[b] & 0x7F807F80u) + 0x00800080u;
+                            any &= 0x80008000u;  // an exponent of all ones
+                            if (any) {
+                                found = true;
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            if ((w[b] & 0x7F80u) == 0x7F80u) w[b] &= 0xFFFF0000u;
-                            if ((w[b] & 0x7F800000u) == 0x7F800000u) w[b] &= 0x0000FFFFu;
+                                for (int b = 0; b < 4; ++b) {
+                                    if ((w[b] & 0x7F80u) == 0x7F80u) w[b] &= 0xFFFF0000u;
+                                    if ((w[b] & 0x7F800000u) == 0x7F800000u) w[b] &= 0x0000FFFFu;
+                                }
+                            }
+                            if (any || r >= rows) *p = x;
                         }
-                        *p = x;
+                        if (found) sh.bad[item % kJobs] = 1;
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&sh.v_half[mi]);
+                            if (warp == 10 && wait(&sh.v_half[mi], mu)) mbar_arrive(&sh.kv_full[sv]);
+                        }
+                        __syncwarp();
+                    }
+                    if (warp == 10) {
+                        // V_j and K_j+1 have arrived: one of the arrivals that
+                        // let the product and the next scores go
+                        ok = wait_warp(&sh.kv_full[sv], ev / C::STAGES) &&
+                             (j + 1 >= n || wait_warp(&sh.kv_full[ek % C::STAGES], ek / C::STAGES));
+                        if (!ok) break;
+                        if (lane < 2 && j < nk[lane]) mbar_arrive(&sh.p_full[lane]);
+                        __syncwarp();
+                        // not a phase ahead of the weights
+                        for (int t = 0; t < 2 && ok; ++t)
+                            if (j < nk[t]) ok = wait_warp(&sh.p_full[t], it[t] + j);
                     }
                 }
-                if (found) sh.bad = 1;
-                fence_proxy_async();
-                __syncwarp();
-                uint64_t *half = &sh.v_half[j - job.first_mask];
-                if (lane == 0) {
-                    mbar_arrive(half);
-                    if (warp == 14 && wait(half, 0)) mbar_arrive(&sh.kv_full[sv]);
-                }
+                if (!ok) break;
+                e0 += 2 * n;
+                it[0] += nk[0];
+                it[1] += nk[1];
+                arrive_warp(&sh.job_empty[item % kJobs]);
                 __syncwarp();
             }
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == 8) {
         if (sh.abort) {
             // MMAs may still be in flight: one more commit follows them all
             if (elect_one()) {
