@@ -671,21 +671,25 @@ kdaStatus_t kda_cache_append(const void *q, const void *k, const void *v,
  * sequences may share pages.  A length beyond max_pages * page_size is cut to
  * it, and the tokens of a page that is negative or >= num_pages are left out;
  * both set KDA_ERR_INVALID_ARG in the device status word.
- * Scratch (partial results of sequences that several thread blocks share):
- * kda_attn_step_workspace_size() bytes, taken with cudaMallocAsync /
- * cudaFreeAsync on `stream`; kda_attn_step_ws takes the caller's instead.
+ * Scratch (partial results of sequences that several thread blocks share; 0
+ * bytes for short tables): kda_attn_step_workspace_size() bytes, taken with
+ * cudaMallocAsync / cudaFreeAsync on `stream`; kda_attn_step_ws takes the
+ * caller's instead.
  */
 kdaStatus_t kda_attn_step(const void *q, const kdaPagedCache_t *cache, const int32_t *seq_lens,
                           float scale, void *out, float *lse, const kdaAttnShape_t *shape,
                           cudaStream_t stream);
 
-/* Bytes of device scratch kda_attn_step_ws needs on the current device for
-   any cache and lengths with `shape`.  *bytes is written on success. */
-kdaStatus_t kda_attn_step_workspace_size(const kdaAttnShape_t *shape, size_t *bytes);
+/* Bytes of device scratch kda_attn_step_ws needs on the current device with
+   these sizes of cache and shape, whatever the lengths.  *bytes is written on
+   success. */
+kdaStatus_t kda_attn_step_workspace_size(const kdaPagedCache_t *cache, const kdaAttnShape_t *shape,
+                                         size_t *bytes);
 
 /* kda_attn_step with caller-owned scratch: `workspace` is a device buffer of
    at least kda_attn_step_workspace_size() bytes, 256-byte aligned, not used by
-   anything else until the work on `stream` is done.  Allocates nothing. */
+   anything else until the work on `stream` is done (NULL where that is 0).
+   Allocates nothing. */
 kdaStatus_t kda_attn_step_ws(const void *q, const kdaPagedCache_t *cache, const int32_t *seq_lens,
                              float scale, void *out, float *lse, const kdaAttnShape_t *shape,
                              void *workspace, size_t workspace_bytes, cudaStream_t stream);

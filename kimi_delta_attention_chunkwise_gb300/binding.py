@@ -167,7 +167,7 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.kda_cache_append.restype = ctypes.c_int
     lib.kda_attn_step.argtypes = [vp, cachep, ip, ctypes.c_float, vp, fp, ashp, vp]
     lib.kda_attn_step.restype = ctypes.c_int
-    lib.kda_attn_step_workspace_size.argtypes = [ashp, ctypes.POINTER(ctypes.c_size_t)]
+    lib.kda_attn_step_workspace_size.argtypes = [cachep, ashp, ctypes.POINTER(ctypes.c_size_t)]
     lib.kda_attn_step_workspace_size.restype = ctypes.c_int
     lib.kda_attn_step_ws.argtypes = [vp, cachep, ip, ctypes.c_float, vp, fp, ashp, vp,
                                      ctypes.c_size_t, vp]
@@ -763,11 +763,13 @@ def make_attn_shape(N, T, HQ, HKV, d, dtype_code, engine=KDA_ENGINE_AUTO, out_f3
                           int(out_f32), int(q_stride), int(k_stride), int(v_stride))
 
 
-# These calls are a few microseconds of GPU work when they are small, so their
-# checks read each property of a tensor once and format nothing but errors.
+# Small calls of these are a few microseconds of GPU work, so each function
+# first asks, in one expression that reads every property once, whether all
+# its tensors are what they usually are; _explain() and _token_stride() deal
+# with the rest: they raise what is wrong, or find the strides of views.
 
-def _misfit(t, name, dev, dtype, shape=None):
-    """Raises what is wrong with an argument that failed a check."""
+def _explain(t, name, dev, dtype, shape=None, contiguous=True):
+    """Raises what is wrong with an argument, if anything is."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -780,33 +782,29 @@ def _misfit(t, name, dev, dtype, shape=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    raise ValueError(f"{name} must be contiguous")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
-def _first(t, name):
-    """(device index, dtype, kdaDtype_t) of the tensor that fixes a call's."""
+def _lead(t, name):
+    """(device index, dtype, [tokens, heads, d]) of the tensor that fixes a call's."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     dev = t.get_device()  # -1: a host tensor
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return dev, t.dtype, _dtype_code(t)
-
-
-def _whole(t, name, dev, dtype, shape) -> int:
-    """Address of a contiguous tensor of this shape."""
-    try:
-        if t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    _misfit(t, name, dev, dtype, shape)
+    size = t.shape
+    if len(size) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, d]")
+    return dev, t.dtype, size
 
 
 def _token_stride(t, name) -> int:
     """The token stride of [T, heads, d] rows whose heads and channels are
-    contiguous (a slice of a fused projection is fine)."""
+    contiguous (a slice of a fused projection is fine); 0: contiguous."""
+    if t.is_contiguous():
+        return 0
     T, H, d = t.shape
     st, sh, sd = t.stride()
     if (d > 1 and sd != 1) or (H > 1 and sh != d) or (T > 1 and st < H * d):
@@ -818,18 +816,14 @@ def _token_stride(t, name) -> int:
     return st
 
 
-def _rows(t, name, dev, dtype):
-    """[T, heads, d] rows: (shape, token stride)."""
+def _whole(t, name, dev, dtype, shape) -> int:
+    """Address of a contiguous tensor of this shape."""
     try:
-        fits = t.get_device() == dev and t.dtype is dtype
+        if t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
     except AttributeError:
-        fits = False
-    if not fits:
-        _misfit(t, name, dev, dtype)
-    size = t.shape
-    if len(size) != 3:
-        raise ValueError(f"{name} must be [tokens, heads, d]")
-    return size, (0 if t.is_contiguous() else _token_stride(t, name))
+        pass
+    _explain(t, name, dev, dtype, shape)
 
 
 def _grouped(HQ, HKV, what):
@@ -837,25 +831,43 @@ def _grouped(HQ, HKV, what):
         raise ValueError(f"q has {HQ} heads, not a multiple of {what} {HKV}")
 
 
-def _paged_cache(k_cache, v_cache, block_table, dev, dtype, i32, N, d):
-    """(the C description, HKV)."""
-    size = getattr(k_cache, "shape", ())
+def _cache_shape(k_cache, v_cache, block_table, dev, dtype, i32, N, d):
+    """Raises what is wrong with a paged cache."""
+    _explain(k_cache, "k_cache", dev, dtype)
+    size = k_cache.shape
     if len(size) != 4 or size[3] != d:
         raise ValueError(f"k_cache must be [pages, HKV, page_size, {d}]")
-    kp = _whole(k_cache, "k_cache", dev, dtype, size)
-    vp = _whole(v_cache, "v_cache", dev, dtype, size)
-    width = getattr(block_table, "shape", ())
-    if len(width) != 2 or width[0] != N:
+    _explain(v_cache, "v_cache", dev, dtype, size)
+    _explain(block_table, "block_table", dev, i32)
+    if block_table.dim() != 2 or block_table.shape[0] != N:
         raise ValueError(f"block_table must be [{N}, pages per sequence]")
-    tp = _whole(block_table, "block_table", dev, i32, width)
-    return kdaPagedCache_t(kp, vp, tp, size[0], size[2], width[1]), size[1]
+
+
+def _paged_cache(k_cache, v_cache, block_table, dev, dtype, i32, N, d):
+    """(the C description, HKV)."""
+    try:
+        size, width = k_cache.shape, block_table.shape
+        if not (len(size) == 4 and size[3] == d and len(width) == 2 and width[0] == N
+                and k_cache.get_device() == dev and v_cache.get_device() == dev
+                and block_table.get_device() == dev and k_cache.dtype is dtype
+                and v_cache.dtype is dtype and block_table.dtype is i32 and v_cache.shape == size
+                and k_cache.is_contiguous() and v_cache.is_contiguous()
+                and block_table.is_contiguous()):
+            _cache_shape(k_cache, v_cache, block_table, dev, dtype, i32, N, d)
+    except AttributeError:
+        _cache_shape(k_cache, v_cache, block_table, dev, dtype, i32, N, d)
+    return kdaPagedCache_t(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), size[0],
+                           size[2], width[1]), size[1]
 
 
 def _attn_out(q, shape, dev, dt, out, out_f32, torch):
     """(out, its address, freshly made out or None, out_f32 flag)."""
     if out is None:
         f32 = out_f32 and dt is not torch.float32
-        out = torch.empty(shape, dtype=torch.float32 if f32 else dt, device=q.device)
+        if f32 or not q.is_contiguous():
+            out = torch.empty(shape, dtype=torch.float32 if f32 else dt, device=q.device)
+        else:
+            out = torch.empty_like(q)
         return out, out.data_ptr(), out, f32
     odt = getattr(out, "dtype", None)
     if odt is not dt and odt is not torch.float32:
@@ -863,7 +875,7 @@ def _attn_out(q, shape, dev, dt, out, out_f32, torch):
     return out, _whole(out, "out", dev, odt, shape), None, odt is not dt
 
 
-def _attn_launch(where, dev, stream, made, fn, *args):
+def _attn_launch(where, dev, stream, made, made_too, fn, *args):
     """Calls fn(*args, stream) with the tensors' device current.  On a stream
     other than the current one, the tensors the call made are marked as used
     there, so that their memory outlives the work."""
@@ -873,7 +885,7 @@ def _attn_launch(where, dev, stream, made, fn, *args):
     else:
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=dev)
-        for t in made:
+        for t in (made, made_too):
             if t is not None:
                 t.record_stream(stream)
         s = stream.cuda_stream
@@ -900,14 +912,19 @@ def kda_attn_fwd(q, k, v, scale: float, cu_seqlens=None, out=None, lse=None, *, 
     with d = 64 or 128, "simt" is fp32 arithmetic on CUDA cores.
     """
     torch = _torch()
-    dev, dt, code = _first(q, "q")
-    size, qs = _rows(q, "q", dev, dt)
+    dev, dt, size = _lead(q, "q")
     T, HQ, d = size
-    ksize, ks = _rows(k, "k", dev, dt)
-    HKV = ksize[1]
-    vsize, vs = _rows(v, "v", dev, dt)
-    if ksize != (T, HKV, d) or vsize != ksize:
-        raise ValueError(f"k and v must be [{T}, HKV, {d}], got {tuple(ksize)}, {tuple(vsize)}")
+    qs = ks = vs = 0
+    ksize = getattr(k, "shape", ())
+    HKV = ksize[1] if len(ksize) == 3 else 0
+    if not (HKV and ksize == (T, HKV, d) and getattr(v, "shape", None) == ksize
+            and k.get_device() == dev and v.get_device() == dev and k.dtype is dt
+            and v.dtype is dt and q.is_contiguous() and k.is_contiguous() and v.is_contiguous()):
+        for t, name in ((k, "k"), (v, "v")):
+            _explain(t, name, dev, dt, None, False)
+            if t.dim() != 3 or t.shape != (T, k.shape[1], d):
+                raise ValueError(f"{name} must be [{T}, HKV, {d}], got {tuple(t.shape)}")
+        qs, ks, vs = _token_stride(q, "q"), _token_stride(k, "k"), _token_stride(v, "v")
     _grouped(HQ, HKV, "k's")
     N, cup, lsep = 1, None, None
     if cu_seqlens is not None:
@@ -917,8 +934,8 @@ def kda_attn_fwd(q, k, v, scale: float, cu_seqlens=None, out=None, lse=None, *, 
         lsep = _whole(lse, "lse", dev, torch.float32, (T, HQ))
     out, op, made, f32 = _attn_out(q, size, dev, dt, out, out_f32, torch)
     eng = _ENGINES[engine] if isinstance(engine, str) else int(engine)
-    shape = kdaAttnShape_t(N, T, HQ, HKV, d, code, eng, f32, qs, ks, vs)
-    _attn_launch("kda_attn_fwd", dev, stream, (made,), load().kda_attn_fwd, q.data_ptr(),
+    shape = kdaAttnShape_t(N, T, HQ, HKV, d, _dtype_code(q), eng, f32, qs, ks, vs)
+    _attn_launch("kda_attn_fwd", dev, stream, made, None, load().kda_attn_fwd, q.data_ptr(),
                  k.data_ptr(), v.data_ptr(), scale, cup, op, lsep, ctypes.byref(shape))
     return out, lse
 
@@ -941,19 +958,24 @@ def kda_cache_append(k, v, k_cache, v_cache, block_table, cache_lens, cu_seqlens
     be q); ``k_out`` [T, HKV, d] receives the rotated keys if given (may be k).
     """
     torch = _torch()
-    dev, dt, code = _first(k, "k")
+    dev, dt, size = _lead(k, "k")
     i32 = torch.int32
-    size, ks = _rows(k, "k", dev, dt)
     T, HKV, d = size
-    vsize, vs = _rows(v, "v", dev, dt)
-    if vsize != size:
-        raise ValueError(f"v must have shape {tuple(size)}, got {tuple(vsize)}")
-    HQ, qs, made, qp, qop, kop, cup, rp = HKV, 0, None, None, None, None, None, None
+    HQ, qs, ks, vs = HKV, 0, 0, 0
+    made = qp = qop = kop = cup = rp = None
+    if not (getattr(v, "shape", None) == size and v.get_device() == dev and v.dtype is dt
+            and k.is_contiguous() and v.is_contiguous()):
+        _explain(v, "v", dev, dt, size, False)
+        ks, vs = _token_stride(k, "k"), _token_stride(v, "v")
     if q is not None:
-        qsize, qs = _rows(q, "q", dev, dt)
-        HQ = qsize[1]
-        if qsize != (T, HQ, d):
-            raise ValueError(f"q must be [{T}, HQ, {d}], got {tuple(qsize)}")
+        qsize = getattr(q, "shape", ())
+        HQ = qsize[1] if len(qsize) == 3 else 0
+        if not (qsize == (T, HQ, d) and q.get_device() == dev and q.dtype is dt
+                and q.is_contiguous()):
+            _explain(q, "q", dev, dt, None, False)
+            if qsize != (T, HQ, d):
+                raise ValueError(f"q must be [{T}, HQ, {d}], got {tuple(qsize)}")
+            qs = _token_stride(q, "q")
         _grouped(HQ, HKV, "k's")
         qp = q.data_ptr()
         if q_out is None:
@@ -978,22 +1000,23 @@ def kda_cache_append(k, v, k_cache, v_cache, block_table, cache_lens, cu_seqlens
         rsize = rope.shape
         if len(rsize) != 2:
             raise ValueError("rope must be [positions, rot_dim]")
-        rp = ctypes.byref(kdaRope_t(_whole(rope, "rope", dev, torch.float32, rsize), *rsize,
-                                    bool(rope_interleaved)))
-    shape = kdaAttnShape_t(N, T, HQ, HKV, d, code, 0, 0, qs, ks, vs)
-    _attn_launch("kda_cache_append", dev, stream, (made,), load().kda_cache_append, qp,
+        rp = ctypes.byref(kdaRope_t(_whole(rope, "rope", dev, torch.float32, rsize), rsize[0],
+                                    rsize[1], bool(rope_interleaved)))
+    shape = kdaAttnShape_t(N, T, HQ, HKV, d, _dtype_code(k), 0, 0, qs, ks, vs)
+    _attn_launch("kda_cache_append", dev, stream, made, None, load().kda_cache_append, qp,
                  k.data_ptr(), v.data_ptr(), cup, lp, rp, qop, kop, ctypes.byref(cache),
                  ctypes.byref(shape))
     return q_out, k_out
 
 
-_step_bytes = {}
+_step_bytes = {}  # by what the size depends on
 
 
-def kda_attn_step_workspace_size(shape: kdaAttnShape_t) -> int:
+def kda_attn_step_workspace_size(cache: kdaPagedCache_t, shape: kdaAttnShape_t) -> int:
+    """Bytes of scratch kda_attn_step needs with these sizes, on the current device."""
     n = ctypes.c_size_t(0)
-    _check(load().kda_attn_step_workspace_size(ctypes.byref(shape), ctypes.byref(n)),
-           "kda_attn_step_workspace_size")
+    _check(load().kda_attn_step_workspace_size(ctypes.byref(cache), ctypes.byref(shape),
+                                               ctypes.byref(n)), "kda_attn_step_workspace_size")
     return int(n.value)
 
 
@@ -1011,29 +1034,36 @@ def kda_attn_step(q, k_cache, v_cache, block_table, seq_lens, scale: float, out=
     calls on other streams never share it).
     """
     torch = _torch()
-    dev, dt, code = _first(q, "q")
-    size, qs = _rows(q, "q", dev, dt)
+    dev, dt, size = _lead(q, "q")
     N, HQ, d = size
+    qs = _token_stride(q, "q")
     cache, HKV = _paged_cache(k_cache, v_cache, block_table, dev, dt, torch.int32, N, d)
     _grouped(HQ, HKV, "the cache's")
     lp = _whole(seq_lens, "seq_lens", dev, torch.int32, (N,))
     lsep = None if lse is None else _whole(lse, "lse", dev, torch.float32, (N, HQ))
     out, op, made, f32 = _attn_out(q, size, dev, dt, out, out_f32, torch)
+    code = _dtype_code(q)
     shape = kdaAttnShape_t(N, N, HQ, HKV, d, code, 0, f32, qs, 0, 0)
-    key = (dev, d, HQ // HKV, code)  # what the size depends on
-    nbytes = _step_bytes.get(key)
-    if nbytes is None:
-        with torch.cuda.device(dev):
-            nbytes = _step_bytes[key] = kda_attn_step_workspace_size(shape)
-    ws_made = None
+    wp = left = 0
+    made_too = None
     if workspace is None:
-        workspace = ws_made = torch.empty(nbytes + 256, dtype=torch.uint8, device=q.device)
-    size = workspace.numel()
-    base = _whole(workspace, "workspace", dev, torch.uint8, (size,))
-    wp = (base + 255) // 256 * 256
-    _attn_launch("kda_attn_step", dev, stream, (made, ws_made), load().kda_attn_step_ws,
+        key = (dev, code, N, HQ, HKV, d, cache.page_size, cache.max_pages)
+        need = _step_bytes.get(key)
+        if need is None:
+            if len(_step_bytes) >= 4096:
+                _step_bytes.clear()
+            with torch.cuda.device(dev):
+                need = _step_bytes[key] = kda_attn_step_workspace_size(cache, shape)
+        if need:
+            workspace = made_too = torch.empty(need + 256, dtype=torch.uint8, device=q.device)
+    if workspace is not None:
+        left = workspace.numel()
+        base = _whole(workspace, "workspace", dev, torch.uint8, (left,))
+        wp = (base + 255) // 256 * 256
+        left = max(left - (wp - base), 0)
+    _attn_launch("kda_attn_step", dev, stream, made, made_too, load().kda_attn_step_ws,
                  q.data_ptr(), ctypes.byref(cache), lp, scale, op, lsep, ctypes.byref(shape), wp,
-                 max(size - (wp - base), 0))
+                 left)
     return out, lse
 
 

@@ -72,28 +72,35 @@ kdaStatus_t check_cache(const kdaPagedCache_t *c, int32_t *page_shift) {
     return KDA_SUCCESS;
 }
 
-kdaStatus_t plan_attn_step(const void *q, const kdaPagedCache_t *cache, const int32_t *seq_lens,
-                           float scale, void *out, float *lse, const kdaAttnShape_t *shape,
-                           AttnStepArgs &a) {
+// What the step's sizes say, before its pointers.
+kdaStatus_t step_sizes(const kdaPagedCache_t *cache, const kdaAttnShape_t *shape, AttnStepArgs &a) {
     kdaStatus_t st = check_attn_shape(shape);
     if (st != KDA_SUCCESS) return st;
     int32_t page_shift = 0;
     st = check_cache(cache, &page_shift);
     if (st != KDA_SUCCESS) return st;
     if (shape->total_tokens != shape->num_seqs) return KDA_ERR_INVALID_ARG;
+    a.num_pages = cache->num_pages; a.page_shift = page_shift; a.max_pages = cache->max_pages;
+    a.N = shape->num_seqs; a.HQ = shape->num_heads; a.HKV = shape->num_kv_heads;
+    a.G = a.HQ / a.HKV; a.D = shape->head_dim; a.dtype = shape->dtype;
+    a.out_f32 = shape->dtype == KDA_DTYPE_F32 ? 1 : shape->out_f32;
+    a.workspace = nullptr;
+    a.status = nullptr;
+    return KDA_SUCCESS;
+}
+
+kdaStatus_t plan_attn_step(const void *q, const kdaPagedCache_t *cache, const int32_t *seq_lens,
+                           float scale, void *out, float *lse, const kdaAttnShape_t *shape,
+                           AttnStepArgs &a) {
+    const kdaStatus_t st = step_sizes(cache, shape, a);
+    if (st != KDA_SUCCESS) return st;
     if (!scale_ok(scale)) return KDA_ERR_INVALID_ARG;
     if (!q || !aligned(q, 16) || !out || !aligned(out, 16)) return KDA_ERR_INVALID_ARG;
     if (!seq_lens || !aligned(seq_lens, 4) || !aligned(lse, 4)) return KDA_ERR_INVALID_ARG;
     a.q = q;
     a.q_stride = token_stride(shape->q_stride, shape->num_heads, shape->head_dim);
     a.k_cache = cache->k; a.v_cache = cache->v; a.block_table = cache->block_table;
-    a.num_pages = cache->num_pages; a.page_shift = page_shift; a.max_pages = cache->max_pages;
     a.seq_lens = seq_lens; a.scale = scale; a.out = out; a.lse = lse;
-    a.N = shape->num_seqs; a.HQ = shape->num_heads; a.HKV = shape->num_kv_heads;
-    a.G = a.HQ / a.HKV; a.D = shape->head_dim; a.dtype = shape->dtype;
-    a.out_f32 = shape->dtype == KDA_DTYPE_F32 ? 1 : shape->out_f32;
-    a.workspace = nullptr;
-    a.status = nullptr;
     return KDA_SUCCESS;
 }
 
@@ -206,16 +213,13 @@ kdaStatus_t kda_cache_append(const void *q, const void *k, const void *v,
     return cuda_status(launch_cache_append(a, stream));
 }
 
-kdaStatus_t kda_attn_step_workspace_size(const kdaAttnShape_t *shape, size_t *bytes) {
+kdaStatus_t kda_attn_step_workspace_size(const kdaPagedCache_t *cache, const kdaAttnShape_t *shape,
+                                         size_t *bytes) {
     if (!bytes) return KDA_ERR_INVALID_ARG;
-    const kdaStatus_t st = check_attn_shape(shape);
+    AttnStepArgs a;
+    const kdaStatus_t st = step_sizes(cache, shape, a);
     if (st != KDA_SUCCESS) return st;
-    const size_t n = attn_step_workspace_bytes(shape->head_dim,
-                                               shape->num_heads / shape->num_kv_heads,
-                                               shape->dtype);
-    if (n == 0) return cuda_status(cudaErrorUnknown);
-    *bytes = n;
-    return KDA_SUCCESS;
+    return cuda_status(attn_step_workspace_bytes(a, bytes));
 }
 
 kdaStatus_t kda_attn_step_ws(const void *q, const kdaPagedCache_t *cache, const int32_t *seq_lens,
@@ -224,10 +228,11 @@ kdaStatus_t kda_attn_step_ws(const void *q, const kdaPagedCache_t *cache, const 
     AttnStepArgs a;
     kdaStatus_t st = plan_attn_step(q, cache, seq_lens, scale, out, lse, shape, a);
     if (st != KDA_SUCCESS) return st;
-    if (!workspace || !aligned(workspace, 256)) return KDA_ERR_INVALID_ARG;
-    const size_t need = attn_step_workspace_bytes(a.D, a.G, a.dtype);
-    if (need == 0) return cuda_status(cudaErrorUnknown);
-    if (workspace_bytes < need) return KDA_ERR_INVALID_ARG;
+    if (!aligned(workspace, 256)) return KDA_ERR_INVALID_ARG;
+    size_t need = 0;
+    st = cuda_status(attn_step_workspace_bytes(a, &need));
+    if (st != KDA_SUCCESS) return st;
+    if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_INVALID_ARG;
     a.workspace = workspace;
     a.status = device_status_word();
     if (!a.status) return cuda_status(cudaErrorUnknown);
@@ -240,10 +245,12 @@ kdaStatus_t kda_attn_step(const void *q, const kdaPagedCache_t *cache, const int
     AttnStepArgs a;
     kdaStatus_t st = plan_attn_step(q, cache, seq_lens, scale, out, lse, shape, a);
     if (st != KDA_SUCCESS) return st;
-    const size_t need = attn_step_workspace_bytes(a.D, a.G, a.dtype);
-    if (need == 0) return cuda_status(cudaErrorUnknown);
+    size_t need = 0;
+    st = cuda_status(attn_step_workspace_bytes(a, &need));
+    if (st != KDA_SUCCESS) return st;
     a.status = device_status_word();
     if (!a.status) return cuda_status(cudaErrorUnknown);
+    if (need == 0) return cuda_status(launch_attn_step(a, stream));
     void *ws = nullptr;
     if (cudaMallocAsync(&ws, need, stream) != cudaSuccess) {
         (void)cudaGetLastError();

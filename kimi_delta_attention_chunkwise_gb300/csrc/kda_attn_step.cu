@@ -18,6 +18,7 @@
 // warps' states are joined when the CTA leaves an item.
 #include <algorithm>
 #include <cstdint>
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include "kda_internal.cuh"
@@ -27,6 +28,10 @@ namespace kda {
 namespace {
 
 constexpr int kTile = 64, kWarps = 4, kThreads = 32 * kWarps, kWarpTokens = 16;
+// The direct kernel's longest run of tokens per CTA by the table's size, for
+// items that are all resident at once and for more than that.
+constexpr int kDirectTokens = 1024, kDirectMany = 256;
+constexpr int kFewItems = 32;
 constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -87,10 +92,23 @@ struct Line {
         }
         __syncthreads();
     }
+    // The units before sequence `seq`, to *base in shared memory.
+    __device__ void base_of(const AttnStepArgs &a, int32_t seq, int32_t items, int64_t *base) const {
+        if (seq >= s0 && seq < s1) {
+            int64_t b = before;
+            for (int32_t s = s0; s < seq; ++s) b += tiles_of(clamp_len(a, s));
+            *base = b * items;
+        }
+        __syncthreads();
+    }
 };
 
 __device__ __forceinline__ int64_t share_start(int64_t units, int32_t c, int32_t grid) {
     return units * c / grid;
+}
+// The CTAs that work: no share is empty.
+__device__ __forceinline__ int32_t workers(int64_t units, int32_t grid) {
+    return (int32_t)min((int64_t)grid, units);
 }
 
 // ---------------------------------------------------------------------------
@@ -446,12 +464,93 @@ __device__ __forceinline__ void store_out(const AttnStepArgs &a, int64_t i, floa
     else static_cast<__nv_bfloat16 *>(a.out)[i] = __float2bfloat16_rn(y);
 }
 
+// One item's tiles tile0 .. tile1 - 1 into the warp's state.
+template <class Core>
+__device__ __forceinline__ void walk_tiles(const AttnStepArgs &a, Core &core, int32_t s,
+                                           int32_t kvh, int32_t len, int32_t tile0, int32_t tile1) {
+    using T = typename Core::Type;
+    constexpr int D = Core::kD;
+    const int warp = threadIdx.x >> 5;
+    const int32_t *table = a.block_table + (int64_t)s * a.max_pages;
+    // this warp's tokens of tile t: the page's table entry, and the rows
+    auto page_of = [&](int32_t t) -> int32_t {
+        const int32_t tok = t * kTile + warp * kWarpTokens;
+        return t < tile1 && tok < len ? table[tok >> a.page_shift] : -1;
+    };
+    auto rows_of = [&](int32_t t, int32_t page, int64_t &at) -> int {
+        const int32_t tok = t * kTile + warp * kWarpTokens;
+        at = 0;
+        if (t >= tile1 || tok >= len) return 0;
+        if (page < 0 || page >= a.num_pages) {
+            *a.status = KDA_ERR_INVALID_ARG;
+            return 0;
+        }
+        at = ((((int64_t)page * a.HKV + kvh) << a.page_shift) +
+              (tok & ((1 << a.page_shift) - 1))) * D;
+        return min(kWarpTokens, len - tok);
+    };
+    const T *kc = static_cast<const T *>(a.k_cache), *vc = static_cast<const T *>(a.v_cache);
+    if constexpr (Core::kAhead) {
+        // the next tile's keys are on their way while this one's weights and
+        // values are worked on, its values while the next scores are, and its
+        // table entry a tile earlier
+        int64_t at, next_at;
+        int n = rows_of(tile0, page_of(tile0), at), next_n;
+        int32_t next_page = page_of(tile0 + 1);
+        core.load_k(kc + at, n);
+        core.load_v(vc + at, n);
+        for (int32_t t = tile0; t < tile1; ++t) {
+            next_n = rows_of(t + 1, next_page, next_at);
+            next_page = page_of(t + 2);
+            core.scores();
+            core.load_k(kc + next_at, next_n);
+            if (n > 0) core.values(n);
+            core.load_v(vc + next_at, next_n);
+            n = next_n;
+        }
+    } else {
+        int32_t next_page = page_of(tile0);
+        for (int32_t t = tile0; t < tile1; ++t) {
+            int64_t at;
+            const int n = rows_of(t, next_page, at);
+            next_page = page_of(t + 1);
+            if (n > 0) core.tile(kc + at, vc + at, n);
+        }
+    }
+}
+
+// The four warps' states, joined.
+template <class Core>
+struct Joined {
+    float acc[kWarps][Core::kRows * Core::kD], m[kWarps][Core::kRows], l[kWarps][Core::kRows];
+    // element i of row r: the weighted sum, maximum (base 2) and sum
+    __device__ void get(int r, int i, float &o, float &mx, float &sum) const {
+        mx = m[0][r];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, m[w][r]);
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        o = sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = exp2f(m[w][r] - ref);
+            o += acc[w][i] * f;
+            sum += l[w][r] * f;
+        }
+    }
+};
+
+__device__ __forceinline__ void store_row(const AttnStepArgs &a, int64_t head, int D, int col,
+                                          float o, float mx, float sum) {
+    store_out(a, head * D + col, sum == 0.f ? 0.f : o / sum);
+    if (a.lse && col == 0) a.lse[head] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+}
+
 template <class Core>
 __global__ void __launch_bounds__(kThreads, Core::kCtas)
 attn_step_kernel(const AttnStepArgs a, float *part) {
     using T = typename Core::Type;
     constexpr int D = Core::kD, R = Core::kRows;
-    __shared__ float s_acc[kWarps][R * D], s_m[kWarps][R], s_l[kWarps][R];
+    __shared__ Joined<Core> state;
     __shared__ int64_t s_scan[kWarps], s_base;
     __shared__ int32_t s_seq;
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -461,16 +560,15 @@ attn_step_kernel(const AttnStepArgs a, float *part) {
     Line<kThreads> line;
     line.scan(a, s_scan);
     const int64_t units = line.total * items;
-    const int32_t grid = (int32_t)gridDim.x, c = (int32_t)blockIdx.x;
+    const int32_t grid = workers(units, (int32_t)gridDim.x), c = (int32_t)blockIdx.x;
     // sequences without keys
-    for (int32_t s = c; s < a.N; s += grid) {
+    for (int32_t s = c; s < a.N; s += gridDim.x) {
         if (clamp_len(a, s) > 0) continue;
-        for (int32_t i = tid; i < a.HQ * D; i += kThreads) store_out(a, (int64_t)s * a.HQ * D + i, 0.f);
-        if (a.lse)
-            for (int32_t i = tid; i < a.HQ; i += kThreads) a.lse[(int64_t)s * a.HQ + i] = -INFINITY;
+        for (int32_t i = tid; i < a.HQ * D; i += kThreads)
+            store_row(a, (int64_t)s * a.HQ + i / D, D, i % D, 0.f, 0.f, 0.f);
     }
+    if (c >= grid) return;
     const int64_t u0 = share_start(units, c, grid), u1 = share_start(units, c + 1, grid);
-    if (u0 >= u1) return;
     line.find(a, u0, items, &s_seq, &s_base);
     int32_t s = s_seq;
     int64_t base = s_base;
@@ -489,80 +587,22 @@ attn_step_kernel(const AttnStepArgs a, float *part) {
         const int32_t rows = min(R, a.G - h0);
         const int64_t head = (int64_t)kvh * a.G + h0;
         core.init(static_cast<const T *>(a.q) + s * a.q_stride + head * D, rows, a.scale);
-        const int32_t *table = a.block_table + (int64_t)s * a.max_pages;
-        // this warp's tokens of tile t: the page's table entry, and the rows
-        auto page_of = [&](int32_t t) -> int32_t {
-            const int32_t tok = t * kTile + warp * kWarpTokens;
-            return t < tile1 && tok < len ? table[tok >> a.page_shift] : -1;
-        };
-        auto rows_of = [&](int32_t t, int32_t page, int64_t &at) -> int {
-            const int32_t tok = t * kTile + warp * kWarpTokens;
-            at = 0;
-            if (t >= tile1 || tok >= len) return 0;
-            if (page < 0 || page >= a.num_pages) {
-                *a.status = KDA_ERR_INVALID_ARG;
-                return 0;
-            }
-            at = ((((int64_t)page * a.HKV + kvh) << a.page_shift) +
-                  (tok & ((1 << a.page_shift) - 1))) * D;
-            return min(kWarpTokens, len - tok);
-        };
-        const T *kc = static_cast<const T *>(a.k_cache), *vc = static_cast<const T *>(a.v_cache);
-        if constexpr (Core::kAhead) {
-            // the next tile's keys are on their way while this one's weights
-            // and values are worked on, its values while the next scores are,
-            // and its table entry a tile earlier
-            int64_t at, next_at;
-            int n = rows_of(tile0, page_of(tile0), at), next_n;
-            int32_t next_page = page_of(tile0 + 1);
-            core.load_k(kc + at, n);
-            core.load_v(vc + at, n);
-            for (int32_t t = tile0; t < tile1; ++t) {
-                next_n = rows_of(t + 1, next_page, next_at);
-                next_page = page_of(t + 2);
-                core.scores();
-                core.load_k(kc + next_at, next_n);
-                if (n > 0) core.values(n);
-                core.load_v(vc + next_at, next_n);
-                n = next_n;
-            }
-        } else {
-            int32_t next_page = page_of(tile0);
-            for (int32_t t = tile0; t < tile1; ++t) {
-                int64_t at;
-                const int n = rows_of(t, next_page, at);
-                next_page = page_of(t + 1);
-                if (n > 0) core.tile(kc + at, vc + at, n);
-            }
-        }
-        core.finish(s_acc[warp], s_m[warp], s_l[warp]);
+        walk_tiles(a, core, s, kvh, len, tile0, tile1);
+        core.finish(state.acc[warp], state.m[warp], state.l[warp]);
         __syncthreads();
-        // join the warps
         const bool whole = tile0 == 0 && tile1 == tiles;
         float *slot = part + ((int64_t)c * 2 + (u == u0 ? 0 : 1)) * (R * (D + 2));
         for (int i = tid; i < rows * D; i += kThreads) {
             const int r = i / D, col = i % D;
-            float mx = s_m[0][r];
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][r]);
-            const float ref = mx == -INFINITY ? 0.f : mx;
-            float o = 0.f, l = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = exp2f(s_m[w][r] - ref);
-                o += s_acc[w][i] * f;
-                l += s_l[w][r] * f;
-            }
+            float o, mx, sum;
+            state.get(r, i, o, mx, sum);
             if (whole) {
-                store_out(a, ((int64_t)s * a.HQ + head + r) * D + col, l == 0.f ? 0.f : o / l);
-                if (a.lse && col == 0)
-                    a.lse[(int64_t)s * a.HQ + head + r] = l == 0.f ? -INFINITY
-                                                                 : (mx + log2f(l)) * kLn2;
+                store_row(a, (int64_t)s * a.HQ + head + r, D, col, o, mx, sum);
             } else {
                 slot[i] = o;
                 if (col == 0) {
                     slot[R * D + r] = mx;
-                    slot[R * D + R + r] = l;
+                    slot[R * D + R + r] = sum;
                 }
             }
         }
@@ -571,11 +611,79 @@ attn_step_kernel(const AttnStepArgs a, float *part) {
     }
 }
 
-// Joins the items that several CTAs of the step share: CTA (c, r) handles
-// query head r of the item that CTA c of the step is the second to work on.
+// Short tables: one cluster per item, its CTAs (1, 2, 4 or 8) taking equal
+// runs of the item's tiles and joining their states through distributed shared
+// memory.  No look-up of the line, no scratch and no second kernel, which is
+// what a small step spends its time on; lengths even out less.
+template <class Core>
+__global__ void __launch_bounds__(kThreads, Core::kCtas)
+attn_step_direct_kernel(const AttnStepArgs a) {
+    using T = typename Core::Type;
+    constexpr int D = Core::kD, R = Core::kRows;
+    __shared__ Joined<Core> state;
+    __shared__ float s_o[R * D], s_m[R], s_l[R];
+    namespace cg = cooperative_groups;
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int32_t ctas = (int32_t)cluster.num_blocks(), rank = (int32_t)cluster.block_rank();
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const int32_t blocks = (a.G + R - 1) / R, items = a.HKV * blocks;
+    const int32_t index = (int32_t)(blockIdx.x / (uint32_t)ctas);
+    const int32_t s = index / items, item = index - s * items;
+    const int32_t kvh = item / blocks, h0 = (item - kvh * blocks) * R;
+    const int32_t rows = min(R, a.G - h0);
+    const int64_t head = (int64_t)kvh * a.G + h0;
+    Core core;
+    core.init(static_cast<const T *>(a.q) + s * a.q_stride + head * D, rows, a.scale);
+    const int32_t len = clamp_len(a, s), tiles = tiles_of(len);
+    if (tid == 0 && a.seq_lens[s] > (a.max_pages << a.page_shift)) *a.status = KDA_ERR_INVALID_ARG;
+    walk_tiles(a, core, s, kvh, len, (int32_t)((int64_t)tiles * rank / ctas),
+               (int32_t)((int64_t)tiles * (rank + 1) / ctas));
+    core.finish(state.acc[warp], state.m[warp], state.l[warp]);
+    __syncthreads();
+    if (ctas == 1) {
+        for (int i = tid; i < rows * D; i += kThreads) {
+            float o, mx, sum;
+            state.get(i / D, i, o, mx, sum);
+            store_row(a, (int64_t)s * a.HQ + head + i / D, D, i % D, o, mx, sum);
+        }
+        return;
+    }
+    for (int i = tid; i < rows * D; i += kThreads) {
+        float o, mx, sum;
+        state.get(i / D, i, o, mx, sum);
+        s_o[i] = o;
+        if (i % D == 0) {
+            s_m[i / D] = mx;
+            s_l[i / D] = sum;
+        }
+    }
+    cluster.sync();
+    for (int i = rank * kThreads + tid; i < rows * D; i += ctas * kThreads) {
+        const int r = i / D;
+        float mx = -INFINITY, sum = 0.f, o = 0.f;
+        for (int32_t c = 0; c < ctas; ++c) mx = fmaxf(mx, *cluster.map_shared_rank(&s_m[r], c));
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        for (int32_t c = 0; c < ctas; ++c) {
+            const float f = exp2f(*cluster.map_shared_rank(&s_m[r], c) - ref);
+            o += *cluster.map_shared_rank(&s_o[i], c) * f;
+            sum += *cluster.map_shared_rank(&s_l[r], c) * f;
+        }
+        store_row(a, (int64_t)s * a.HQ + head + r, D, i % D, o, mx, sum);
+    }
+    cluster.sync();  // no CTA ends while another reads its shared memory
+}
+
+// Joins the items that several CTAs of the step share, one item per CTA:
+// by_item: CTA (x, y) has item x; else it has the item that CTA x + 1 of the
+// step is the second to work on (whichever makes the smaller grid).  Query
+// heads y * per .. of the item; a warp takes one query head and every parts-th
+// of the item's CTAs.
 template <int D, int R>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnStepArgs a,
-                                                                 const float *part, int32_t grid) {
+                                                                 const float *part,
+                                                                 int32_t step_grid, int32_t per,
+                                                                 int32_t by_item) {
+    constexpr int N = (D + 31) / 32;  // columns per lane
     __shared__ int64_t s_scan[kJoinWarps], s_base;
     __shared__ int32_t s_seq;
     __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
@@ -584,67 +692,96 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnStepA
     Line<kJoinThreads> line;
     line.scan(a, s_scan);
     const int64_t units = line.total * items;
-    const int32_t c = (int32_t)blockIdx.x + 1;
-    const int64_t start = share_start(units, c, grid);
-    const bool any = start < units;
-    if (any) line.find(a, start, items, &s_seq, &s_base);
+    const int32_t grid = workers(units, step_grid);
+    const bool any = units > 0 && (by_item || (int32_t)blockIdx.x + 1 < grid);
+    const int64_t start = by_item || !any ? 0 : share_start(units, (int32_t)blockIdx.x + 1, grid);
+    if (by_item) {
+        if (tid == 0) s_seq = (int32_t)blockIdx.x / items;
+        line.base_of(a, (int32_t)blockIdx.x / items, items, &s_base);
+    } else if (any) {
+        line.find(a, start, items, &s_seq, &s_base);
+    }
     // every CTA waits for the step to end, so that whatever follows this
     // kernel in the stream also follows the step
     tc::pdl_wait_primaries();
     if (!any) return;
     const int32_t s = s_seq;
     const int32_t tiles = tiles_of(clamp_len(a, s));
-    const int32_t item = (int32_t)((start - s_base) / tiles);
+    if (tiles == 0) return;  // by_item: written by the step
+    const int32_t item = by_item ? (int32_t)blockIdx.x - s * items : (int32_t)((start - s_base) / tiles);
     const int64_t first = s_base + (int64_t)item * tiles, last = first + tiles;  // the item's units
-    if (start == first || share_start(units, c - 1, grid) > first) return;
-    const int32_t kvh = item / blocks, h0 = (item - kvh * blocks) * R, r = blockIdx.y;
-    if (h0 + r >= a.G) return;
-    float mx = -INFINITY, l = 0.f, o[(D + 31) / 32];
+    // the first of the step's CTAs on the item: the last that starts at or before it
+    const int32_t c0 = by_item ? (int32_t)(((first + 1) * grid - 1) / units) : (int32_t)blockIdx.x;
+    if (by_item ? share_start(units, c0 + 1, grid) >= last
+                : start == first || share_start(units, c0, grid) > first)
+        return;
+    const int32_t kvh = item / blocks, h0 = (item - kvh * blocks) * R;
+    const int32_t r0 = blockIdx.y * per, rows = min(min(per, R), a.G - h0 - r0);
+    if (rows <= 0) return;
+    int32_t abreast = 1;  // query heads at a time, a power of two
+    while (abreast < rows && abreast < kJoinWarps) abreast *= 2;
+    const int32_t parts = kJoinWarps / abreast;
+    for (int32_t rb = 0; rb < rows; rb += abreast) {
+        const int32_t r = rb + (warp & (abreast - 1));
+        float mx = -INFINITY, l = 0.f, o[N];
 #pragma unroll
-    for (int j = 0; j < (D + 31) / 32; ++j) o[j] = 0.f;
-    // this warp's CTAs of the step: c - 1 + warp, then every kJoinWarps-th
-    for (int32_t i = c - 1 + warp; i < grid; i += kJoinWarps) {
-        const int64_t b = share_start(units, i, grid);
-        if (b >= last) break;
-        if (i >= c && b >= share_start(units, i + 1, grid)) continue;  // an empty share
-        const float *slot = part + ((int64_t)i * 2 + ((i == c - 1 && b != first) ? 1 : 0)) *
-                                       (R * (D + 2));
-        const float sm = slot[R * D + r], sl = slot[R * D + R + r];
-        float x[(D + 31) / 32];
+        for (int j = 0; j < N; ++j) o[j] = 0.f;
+        if (r < rows) {
+#pragma unroll 2
+            for (int32_t i = c0 + warp / abreast; i < grid; i += parts) {
+                const int64_t b = share_start(units, i, grid);
+                if (b >= last) break;
+                const float *slot = part + ((int64_t)i * 2 + ((i == c0 && b != first) ? 1 : 0)) *
+                                               (R * (D + 2));
+                const float sm = slot[R * D + r0 + r], sl = slot[R * D + R + r0 + r];
+                float x[N];
 #pragma unroll
-        for (int j = 0; j < (D + 31) / 32; ++j)
-            x[j] = (D >= 32 || lane < D) ? slot[r * D + j * 32 + lane] : 0.f;
-        const float nm = fmaxf(mx, sm), ref = nm == -INFINITY ? 0.f : nm;
-        const float f0 = exp2f(mx - ref), f1 = exp2f(sm - ref);
-        mx = nm;
-        l = l * f0 + sl * f1;
+                for (int j = 0; j < N; ++j)
+                    x[j] = (D >= 32 || lane < D) ? slot[(r0 + r) * D + j * 32 + lane] : 0.f;
+                const float nm = fmaxf(mx, sm), ref = nm == -INFINITY ? 0.f : nm;
+                const float f0 = exp2f(mx - ref), f1 = exp2f(sm - ref);
+                mx = nm;
+                l = l * f0 + sl * f1;
 #pragma unroll
-        for (int j = 0; j < (D + 31) / 32; ++j) o[j] = o[j] * f0 + x[j] * f1;
-    }
-#pragma unroll
-    for (int j = 0; j < (D + 31) / 32; ++j)
-        if (D >= 32 || lane < D) s_o[warp][j * 32 + lane] = o[j];
-    if (lane == 0) {
-        s_m[warp] = mx;
-        s_l[warp] = l;
-    }
-    __syncthreads();
-    for (int col = tid; col < D; col += kJoinThreads) {
-        float m = s_m[0];
-#pragma unroll
-        for (int w = 1; w < kJoinWarps; ++w) m = fmaxf(m, s_m[w]);
-        const float ref = m == -INFINITY ? 0.f : m;
-        float y = 0.f, sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) {
-            const float f = exp2f(s_m[w] - ref);
-            y += s_o[w][col] * f;
-            sum += s_l[w] * f;
+                for (int j = 0; j < N; ++j) o[j] = o[j] * f0 + x[j] * f1;
+            }
         }
-        const int64_t head = (int64_t)s * a.HQ + (int64_t)kvh * a.G + h0 + r;
-        store_out(a, head * D + col, sum == 0.f ? 0.f : y / sum);
-        if (a.lse && col == 0) a.lse[head] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (D >= 32 || lane < D) s_o[warp][j * 32 + lane] = o[j];
+        if (lane == 0) {
+            s_m[warp] = mx;
+            s_l[warp] = l;
+        }
+        __syncthreads();
+        for (int i = tid; i < min(abreast, rows - rb) * D; i += kJoinThreads) {
+            const int w0 = i / D, col = i % D;
+            float m = s_m[w0];
+            for (int w = w0 + abreast; w < kJoinWarps; w += abreast) m = fmaxf(m, s_m[w]);
+            const float ref = m == -INFINITY ? 0.f : m;
+            float y = 0.f, sum = 0.f;
+            for (int w = w0; w < kJoinWarps; w += abreast) {
+                const float f = exp2f(s_m[w] - ref);
+                y += s_o[w][col] * f;
+                sum += s_l[w] * f;
+            }
+            const int64_t head = (int64_t)s * a.HQ + (int64_t)kvh * a.G + h0 + r0 + rb + w0;
+            store_row(a, head, D, col, y, m, sum);
+        }
+        __syncthreads();
     }
+}
+
+// CTAs of a cluster for the direct kernel, or 0: the line of tiles.
+int direct_ctas(int64_t items, int64_t capacity, int64_t slots) {
+    int ctas = 1;
+    while (ctas < 8 && items * ctas * 2 <= slots && capacity > (int64_t)ctas * kTile) ctas *= 2;
+    return capacity <= (int64_t)ctas * (items <= slots ? kDirectTokens : kDirectMany) ? ctas : 0;
+}
+
+template <class Core>
+int64_t step_items(const AttnStepArgs &a) {
+    return (int64_t)a.N * a.HKV * ((a.G + Core::kRows - 1) / Core::kRows);
 }
 
 template <class Core>
@@ -652,25 +789,40 @@ cudaError_t launch_core(const AttnStepArgs &a, cudaStream_t stream) {
     constexpr int D = Core::kD, R = Core::kRows;
     const int sms = device_sms();
     if (!sms) return cudaErrorUnknown;
+    const int64_t capacity = (int64_t)a.max_pages << a.page_shift;
+    const int64_t items = step_items<Core>(a), slots = (int64_t)sms * Core::kCtas;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    const int ctas = direct_ctas(items, capacity, slots);
+    if (ctas > 0) {
+        if (items * ctas > INT32_MAX) return cudaErrorInvalidValue;
+        cfg.gridDim = dim3((unsigned)(items * ctas));
+        cfg.blockDim = dim3(kThreads);
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)ctas;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, attn_step_direct_kernel<Core>, a);
+    }
     // no more CTAs than the longest possible line has tiles
-    const int64_t most = (int64_t)a.N * a.HKV * ((a.G + R - 1) / R) *
-                         (((int64_t)a.max_pages << a.page_shift) / kTile + 1);
-    const int grid = (int)std::min<int64_t>((int64_t)sms * Core::kCtas, std::max<int64_t>(most, 1));
+    const int grid = (int)std::min(slots, items * (capacity / kTile + 1));
     float *part = static_cast<float *>(a.workspace);
     attn_step_kernel<Core><<<grid, kThreads, 0, stream>>>(a, part);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || grid == 1) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)std::min<int32_t>(R, a.G));
+    // few items: each is shared by many CTAs, and a join CTA takes one query
+    // head; else all of an item's
+    const int32_t most_rows = std::min<int32_t>(R, a.G), per = items < kFewItems ? 1 : most_rows;
+    const bool by_item = items < grid;
+    cfg.gridDim = dim3((unsigned)(by_item ? items : grid - 1), (unsigned)((most_rows + per - 1) / per));
     cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, attn_join_kernel<D, R>, a, static_cast<const float *>(part),
-                              (int32_t)grid);
+                              (int32_t)grid, per, (int32_t)by_item);
 }
 
 // The core of a problem, as a call of f.template operator()<Core>().
@@ -698,12 +850,16 @@ auto with_core(int32_t D, int32_t G, int32_t dtype, F f) {
 
 }  // namespace
 
-size_t attn_step_workspace_bytes(int32_t D, int32_t G, int32_t dtype) {
+cudaError_t attn_step_workspace_bytes(const AttnStepArgs &a, size_t *bytes) {
     const int sms = device_sms();
-    return with_core(D, G, dtype, [&](auto core) -> size_t {
+    if (!sms) return cudaErrorUnknown;
+    *bytes = with_core(a.D, a.G, a.dtype, [&](auto core) -> size_t {
         using Core = decltype(core);
-        return (size_t)sms * Core::kCtas * 2 * Core::kRows * (Core::kD + 2) * sizeof(float);
+        const int64_t slots = (int64_t)sms * Core::kCtas;
+        if (direct_ctas(step_items<Core>(a), (int64_t)a.max_pages << a.page_shift, slots)) return 0;
+        return (size_t)slots * 2 * Core::kRows * (Core::kD + 2) * sizeof(float);
     });
+    return cudaSuccess;
 }
 
 cudaError_t launch_attn_step(const AttnStepArgs &a, cudaStream_t stream) {

@@ -22,6 +22,10 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
+#ifndef KTOK
+#define KTOK 4
+#endif
+constexpr int kFewTokens = 1024;
 
 template <typename T>
 struct Row;  // 16 bytes of a row as floats
@@ -114,101 +118,124 @@ __device__ Place find_place(const AppendArgs &a, int32_t t) {
     return p;
 }
 
+// A unit: two 16-byte vectors of one head's row.
+struct Unit {
+    int32_t tk, head, c0, c1;  // token of the CTA, row (q, k, v heads), first channels
+    bool halves;               // the two vectors pair up
+};
+
 template <typename T, int D, int TOK>
 __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs a) {
     constexpr int V = Row<T>::V;
     constexpr int UNITS = D / V / 2;  // units per head row
     __shared__ Place place[TOK];
     const int32_t t0 = blockIdx.x * TOK;
-    if (threadIdx.x < TOK) place[threadIdx.x] = find_place(a, t0 + threadIdx.x);
-    __syncthreads();
-    const int32_t rows = a.HQ + 2 * a.HKV;  // q heads, k heads, v heads
+    const int32_t rows = a.HQ + 2 * a.HKV;
     const int32_t half = a.rot >> 1;
-    const int32_t total = TOK * rows * UNITS;
-    for (int32_t i = threadIdx.x; i < total; i += kThreads) {
+    const int32_t total = min(TOK, a.T - t0) * rows * UNITS;
+    auto unit_of = [&](int32_t i) {
+        Unit w;
         const int32_t u = i % UNITS, r = i / UNITS;
-        const int32_t tk = r / rows, head = r - tk * rows;
-        const Place p = place[tk];
-        if (p.pos < 0) continue;
-        const int64_t t = t0 + tk;
-        // channels of the unit's two vectors
-        int32_t c0, c1;
-        const bool halves = a.rot > 0 && !a.interleaved && u * V < half;
-        if (halves) {
-            c0 = u * V;
-            c1 = c0 + half;
-        } else {
-            c0 = 2 * u * V;
-            c1 = c0 + V;
-        }
+        w.tk = r / rows;
+        w.head = r - w.tk * rows;
+        w.halves = a.rot > 0 && !a.interleaved && u * V < half;
+        w.c0 = w.halves ? u * V : 2 * u * V;
+        w.c1 = w.halves ? w.c0 + half : w.c0 + V;
+        return w;
+    };
+    // inputs do not wait for the look-up: every row of [0, T) may be read
+    auto load = [&](int32_t i, uint4 &x0, uint4 &x1) {
+        const Unit w = unit_of(i);
+        const int64_t t = t0 + w.tk;
         const T *src;
-        T *dst0 = nullptr, *dst1 = nullptr;  // contiguous output, cache row
-        bool rotate = a.rot > 0;
-        if (head < a.HQ) {
-            src = static_cast<const T *>(a.q) + t * a.q_stride + (int64_t)head * D;
-            dst0 = static_cast<T *>(a.q_out) + (t * a.HQ + head) * D;
+        if (w.head < a.HQ) {
+            src = static_cast<const T *>(a.q) + t * a.q_stride + (int64_t)w.head * D;
+        } else if (w.head < a.HQ + a.HKV) {
+            src = static_cast<const T *>(a.k) + t * a.k_stride + (int64_t)(w.head - a.HQ) * D;
         } else {
-            const int32_t h = head - a.HQ;
+            src = static_cast<const T *>(a.v) + t * a.v_stride + (int64_t)(w.head - a.HQ - a.HKV) * D;
+        }
+        x0 = *reinterpret_cast<const uint4 *>(src + w.c0);
+        x1 = *reinterpret_cast<const uint4 *>(src + w.c1);
+    };
+    auto finish = [&](int32_t i, uint4 x0, uint4 x1) {
+        const Unit w = unit_of(i);
+        const Place p = place[w.tk];
+        if (p.pos < 0) return;
+        const int64_t t = t0 + w.tk;
+        T *dst0 = nullptr, *dst1 = nullptr;  // contiguous output, cache row
+        bool rotate = w.c0 < a.rot;
+        if (w.head < a.HQ) {
+            dst0 = static_cast<T *>(a.q_out) + (t * a.HQ + w.head) * D;
+        } else {
+            const int32_t h = w.head - a.HQ;
             const bool is_k = h < a.HKV;
             const int32_t kh = is_k ? h : h - a.HKV;
-            const int64_t row = p.page + ((int64_t)kh << a.page_shift);
-            if (is_k) {
-                src = static_cast<const T *>(a.k) + t * a.k_stride + (int64_t)kh * D;
-                if (a.k_out) dst0 = static_cast<T *>(a.k_out) + (t * a.HKV + kh) * D;
-                if (p.page >= 0) dst1 = static_cast<T *>(a.k_cache) + row * D;
-            } else {
-                src = static_cast<const T *>(a.v) + t * a.v_stride + (int64_t)kh * D;
-                if (p.page >= 0) dst1 = static_cast<T *>(a.v_cache) + row * D;
-                rotate = false;
-            }
-            if (!dst0 && !dst1) continue;
+            const int64_t row = (p.page + ((int64_t)kh << a.page_shift)) * D;
+            if (p.page >= 0) dst1 = static_cast<T *>(is_k ? a.k_cache : a.v_cache) + row;
+            if (is_k && a.k_out) dst0 = static_cast<T *>(a.k_out) + (t * a.HKV + kh) * D;
+            rotate = rotate && is_k;
         }
-        uint4 x0 = *reinterpret_cast<const uint4 *>(src + c0);
-        uint4 x1 = *reinterpret_cast<const uint4 *>(src + c1);
-        if (rotate && c0 < a.rot) {
+        if (rotate) {
             const float *cs = a.rope + (int64_t)p.pos * a.rot;
-            float f0[V], f1[V];
+            float f0[V], f1[V], c[V], s[V];
             Row<T>::unpack(x0, f0);
             Row<T>::unpack(x1, f1);
-            if (halves) {
+            // the angles of the unit's V pairs: halves: pairs c0 .. c0 + V - 1;
+            // interleaved: c0 / 2 .. (both vectors lie inside rot_dim, a
+            // multiple of 2 V)
+            const float *ca = cs + (w.halves ? w.c0 : w.c0 / 2), *sa = ca + half;
 #pragma unroll
-                for (int j = 0; j < V; j += 4) {
-                    const float4 c = __ldg(reinterpret_cast<const float4 *>(cs + c0 + j));
-                    const float4 s = __ldg(reinterpret_cast<const float4 *>(cs + half + c0 + j));
-                    turn(f0[j], f1[j], c.x, s.x);
-                    turn(f0[j + 1], f1[j + 1], c.y, s.y);
-                    turn(f0[j + 2], f1[j + 2], c.z, s.z);
-                    turn(f0[j + 3], f1[j + 3], c.w, s.w);
-                }
+            for (int j = 0; j < V; j += 4) {
+                const float4 cv = __ldg(reinterpret_cast<const float4 *>(ca + j));
+                const float4 sv = __ldg(reinterpret_cast<const float4 *>(sa + j));
+                c[j] = cv.x; c[j + 1] = cv.y; c[j + 2] = cv.z; c[j + 3] = cv.w;
+                s[j] = sv.x; s[j + 1] = sv.y; s[j + 2] = sv.z; s[j + 3] = sv.w;
+            }
+            if (w.halves) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) turn(f0[j], f1[j], c[j], s[j]);
             } else {
-                // both vectors lie inside rot_dim (a multiple of 2 V)
 #pragma unroll
                 for (int j = 0; j < V / 2; ++j) {
-                    const int32_t m = c0 / 2 + j;
-                    turn(f0[2 * j], f0[2 * j + 1], __ldg(cs + m), __ldg(cs + half + m));
-                    turn(f1[2 * j], f1[2 * j + 1], __ldg(cs + m + V / 2),
-                         __ldg(cs + half + m + V / 2));
+                    turn(f0[2 * j], f0[2 * j + 1], c[j], s[j]);
+                    turn(f1[2 * j], f1[2 * j + 1], c[V / 2 + j], s[V / 2 + j]);
                 }
             }
             x0 = Row<T>::pack(f0);
             x1 = Row<T>::pack(f1);
         }
         if (dst0) {
-            *reinterpret_cast<uint4 *>(dst0 + c0) = x0;
-            *reinterpret_cast<uint4 *>(dst0 + c1) = x1;
+            *reinterpret_cast<uint4 *>(dst0 + w.c0) = x0;
+            *reinterpret_cast<uint4 *>(dst0 + w.c1) = x1;
         }
         if (dst1) {
-            *reinterpret_cast<uint4 *>(dst1 + c0) = x0;
-            *reinterpret_cast<uint4 *>(dst1 + c1) = x1;
+            *reinterpret_cast<uint4 *>(dst1 + w.c0) = x0;
+            *reinterpret_cast<uint4 *>(dst1 + w.c1) = x1;
         }
+    };
+    // the next unit's vectors are on their way while this one's are worked on
+    uint4 x0 = {}, x1 = {}, y0 = {}, y1 = {};
+    if ((int32_t)threadIdx.x < total) load(threadIdx.x, x0, x1);
+    if (threadIdx.x < TOK) place[threadIdx.x] = find_place(a, t0 + threadIdx.x);
+    __syncthreads();
+    for (int32_t i = threadIdx.x; i < total; i += kThreads) {
+        if (i + kThreads < total) load(i + kThreads, y0, y1);
+        finish(i, x0, x1);
+        x0 = y0;
+        x1 = y1;
     }
 }
 
 template <typename T, int D>
 cudaError_t launch_t(const AppendArgs &a, cudaStream_t stream) {
-    constexpr int TOK = 4;
-    cache_append_kernel<T, D, TOK>
-        <<<(unsigned)((a.T + TOK - 1) / TOK), kThreads, 0, stream>>>(a);
+    if (a.T <= kFewTokens) {
+        cache_append_kernel<T, D, 1><<<(unsigned)a.T, kThreads, 0, stream>>>(a);
+    } else {
+        constexpr int TOK = KTOK;
+        cache_append_kernel<T, D, TOK>
+            <<<(unsigned)((a.T + TOK - 1) / TOK), kThreads, 0, stream>>>(a);
+    }
     return cudaGetLastError();
 }
 

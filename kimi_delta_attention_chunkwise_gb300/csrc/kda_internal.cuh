@@ -224,8 +224,8 @@ struct AttnStepArgs {
     void *workspace;
     int *status;
 };
-// Scratch of the step on the current device (0: the query failed).
-size_t attn_step_workspace_bytes(int32_t D, int32_t G, int32_t dtype);
+// Scratch of the step on the current device, for these sizes and any lengths.
+cudaError_t attn_step_workspace_bytes(const AttnStepArgs &a, size_t *bytes);
 cudaError_t launch_attn_step(const AttnStepArgs &a, cudaStream_t stream);
 
 // Device address of the status word on the current device (kda_api.cu).

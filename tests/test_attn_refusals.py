@@ -67,7 +67,8 @@ def test_shape_invalid(lib, kw):
     assert _fwd(lib, s, cu=FAKE) == INVALID
     assert _append(lib, s, cu=FAKE) == INVALID
     n = ctypes.c_size_t(0)
-    assert lib.kda_attn_step_workspace_size(ctypes.byref(s), ctypes.byref(n)) == INVALID
+    assert lib.kda_attn_step_workspace_size(ctypes.byref(_cache()), ctypes.byref(s),
+                                            ctypes.byref(n)) == INVALID
 
 
 @pytest.mark.parametrize("kw", SHAPES_UNSUPPORTED)
@@ -140,8 +141,12 @@ def test_step_arguments(lib):
         assert _step(lib, s, **{name: None}) == INVALID
     assert _step(lib, s, q=FAKE + 8) == INVALID
     assert _step(lib, s, lse=FAKE + 1) == INVALID
-    assert _step(lib, s, ws=None) == INVALID
     assert _step(lib, s, ws=FAKE + 16) == INVALID                # 256-byte alignment
+    n = ctypes.c_size_t(0)
+    size = lib.kda_attn_step_workspace_size
+    assert size(None, ctypes.byref(s), ctypes.byref(n)) == INVALID
+    assert size(ctypes.byref(_cache()), ctypes.byref(s), None) == INVALID
+    assert size(ctypes.byref(_cache()), ctypes.byref(_shape(N=2)), ctypes.byref(n)) == INVALID
 
 
 def test_binding_refuses_host_and_misfit_tensors():

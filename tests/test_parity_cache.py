@@ -174,6 +174,13 @@ def _paged(seed, lens, HKV, d, page, dtype, garbage=float("nan")):
     return ks, vs, kc.cuda(), vc.cuda(), table.cuda()
 
 
+def _widen(table):
+    """The table with room for 16384 pages a sequence (none there)."""
+    wide = torch.full((table.shape[0], 16384), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    return wide
+
+
 def _check_step(q, ks, vs, scale, out, lse, weights_bf16):
     for s in range(q.shape[0]):
         n = ks[s].shape[0]
@@ -202,10 +209,14 @@ STEP = [
 
 @pytest.mark.parametrize("lens,HQ,HKV,d,page", STEP)
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_step(lens, HQ, HKV, d, page, dtype):
-    """Rows behind a sequence's length hold NaN and are never used."""
+@pytest.mark.parametrize("wide", [False, True])
+def test_step(lens, HQ, HKV, d, page, dtype, wide):
+    """Rows behind a sequence's length hold NaN and are never used.  Short
+    tables and wide ones take different kernels."""
     N = len(lens)
     ks, vs, kc, vc, table = _paged(HQ + d, lens, HKV, d, page, dtype)
+    if wide:
+        table = _widen(table)
     q = _randn(1, N, HQ, d, dtype=dtype).cuda()
     lse = torch.full((N, HQ), float("nan"), device="cuda")
     out, _ = kda.kda_attn_step(q, kc, vc, table, _i32(lens), d ** -0.5, None, lse)
@@ -295,11 +306,15 @@ def test_step_offsets_past_32_bits(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_step_streams_graphs_and_workspace(dtype):
+@pytest.mark.parametrize("wide", [False, True])
+def test_step_streams_graphs_and_workspace(dtype, wide):
     """Two calls at once, two captured graphs replayed with other lengths, and
-    a caller's workspace all give the bits of a plain call."""
+    a caller's workspace all give the bits of a plain call; with a short table
+    (no scratch) and with a wide one."""
     lens, HQ, HKV, d, page = [3000, 17, 900, 0, 64], 8, 2, 128, 16
     ks, vs, kc, vc, table = _paged(7, lens, HKV, d, page, dtype)
+    if wide:
+        table = _widen(table)
     q = [_randn(i, 5, HQ, d, dtype=dtype).cuda() for i in (1, 2)]
     l1, l2 = _i32(lens), _i32([100, 0, 900, 0, 3])
     want = {(i, j): kda.kda_attn_step(q[i], kc, vc, table, l, 0.1)[0]
@@ -328,16 +343,19 @@ def test_step_streams_graphs_and_workspace(dtype):
         for i in (0, 1):
             assert torch.equal(outs[i], want[i, j])
     shape = kda.make_attn_shape(5, 5, HQ, HKV, d, kda.KDA_DTYPE_BF16 if dtype == "bf16" else kda.KDA_DTYPE_F32)
-    ws = torch.empty(kda.kda_attn_step_workspace_size(shape) + 256, dtype=torch.uint8, device="cuda")
+    cache = kda.kdaPagedCache_t(kc.data_ptr(), vc.data_ptr(), table.data_ptr(), kc.shape[0], page,
+                                table.shape[1])
+    need = kda.kda_attn_step_workspace_size(cache, shape)
+    assert (need > 0) == wide
+    ws = torch.empty(need + 256, dtype=torch.uint8, device="cuda")
     out, _ = kda.kda_attn_step(q[0], kc, vc, table, l1, 0.1, workspace=ws)
     assert torch.equal(out, want[0, 1])
-    with pytest.raises(kda.KdaError):
-        kda.kda_attn_step(q[0], kc, vc, table, l1, 0.1, workspace=ws[:1024])
+    if wide:
+        with pytest.raises(kda.KdaError):
+            kda.kda_attn_step(q[0], kc, vc, table, l1, 0.1, workspace=ws[:1024])
     # the library's own scratch (C entry without a workspace)
     import ctypes
     from kimi_delta_attention_chunkwise_gb300 import binding
-    cache = kda.kdaPagedCache_t(kc.data_ptr(), vc.data_ptr(), table.data_ptr(), kc.shape[0], page,
-                                table.shape[1])
     out2 = torch.empty_like(out)
     rc = binding.load().kda_attn_step(q[0].data_ptr(), ctypes.byref(cache), l1.data_ptr(), 0.1,
                                       out2.data_ptr(), None, ctypes.byref(shape),
