@@ -8,12 +8,19 @@
 // one key-value head, token-major, so grouped heads share every key and value
 // that is brought in and a group of any size fills its tiles.
 //
-// A CTA of 256 threads owns 64 rows and walks the keys in tiles of 64: a
-// thread computes a 4 x 4 block of scores (rows 4 ty + a, keys tx + 16 b) and
-// D / 16 columns of 4 output rows.  The 16 threads of a row share its
-// statistics through shuffles.  Bound by shared-memory reads (8 16-byte reads
-// for 64 multiply-adds); the weights overwrite the key tile, which keeps two
-// CTAs on an SM.
+// A group of threads owns ROWS rows and walks the keys in tiles of 64: a thread
+// computes a 4 x 4 block of scores (rows 4 ty + a, keys tx + 16 b) and D / 16
+// columns of 4 output rows.  The 16 threads of a row share its statistics
+// through shuffles; the weights overwrite the key tile.  Per 4 channels a warp
+// issues 64 multiply-adds and reads 12 shared-memory wavefronts, so four warps
+// keep the pipes of their quarter of an SM 3/4 busy on both.
+//
+// Large problems: one group of 256 threads per CTA, 64 rows (4096 tokens, 16
+// heads, d = 128: 35 TFLOP/s of fp32).  Problems whose tiles would not fill the
+// GPU twice: four groups of 128 threads (two for d = 128) share 32 rows, each
+// taking every fourth (second) key tile, and join their states at the end: more
+// CTAs and fewer steps in a row (1025 tokens of 3 sequences, 6/2 heads, d = 64:
+// 66 -> 31 us).
 #include <cstdint>
 #include <cuda_bf16.h>
 
@@ -22,18 +29,21 @@
 namespace kda {
 namespace {
 
-constexpr int kRows = 64, kKeys = 64, kThreads = 256;
+constexpr int kKeys = 64;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int D>
 constexpr int kq_stride() { return D + 4; }  // rows 4 banks apart: 16-byte reads without conflicts
 constexpr int kPStride = kKeys + 4;
 
-template <int D>
+// Floats of a group's key buffer (the weights fit in it too), and of a CTA.
+template <int D, int ROWS>
+constexpr int key_floats() {
+    return kKeys * kq_stride<D>() > ROWS * kPStride ? kKeys * kq_stride<D>() : ROWS * kPStride;
+}
+template <int D, int ROWS, int GROUPS>
 constexpr size_t smem_bytes() {
-    const size_t kbuf = kKeys * kq_stride<D>() > kRows * kPStride ? kKeys * kq_stride<D>()
-                                                                  : kRows * kPStride;
-    return (kRows * kq_stride<D>() + kbuf + kKeys * D) * sizeof(float);
+    return (ROWS * kq_stride<D>() + GROUPS * (key_floats<D, ROWS>() + kKeys * D)) * sizeof(float);
 }
 
 // 4 consecutive elements as floats
@@ -44,23 +54,29 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
                        __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xFFFF0000u));
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 2) attn_simt_kernel(const AttnArgs a) {
+template <typename T, int D, int ROWS, int GROUPS>
+__global__ void __launch_bounds__(GROUPS * ROWS * 4, GROUPS * ROWS > 64 || (GROUPS > 1 && D == 128) ? 1 : 2)
+attn_simt_kernel(const AttnArgs a) {
+    constexpr int kRows = ROWS, kGroup = ROWS * 4, kThreads = GROUPS * kGroup;
     constexpr int KS = kq_stride<D>();
     constexpr int CW = D >= 64 ? 4 : D / 16;      // columns of one vector
     constexpr int CN = D >= 64 ? D / 64 : 1;      // vectors per thread, 64 columns apart
     extern __shared__ float smem[];
+    const int group = threadIdx.x / kGroup, tid = threadIdx.x % kGroup, tx = tid & 15, ty = tid >> 4;
     float *sq = smem;
-    float *sk = smem + kRows * KS;
-    float *sp = sk;                                // the weights, once the scores are done
-    float *sv = smem + (smem_bytes<D>() / sizeof(float) - kKeys * D);
+    float *sk = smem + kRows * KS + group * (key_floats<D, ROWS>() + kKeys * D);
+    float *sp = sk;  // the weights, once the scores are done
+    float *sv = sk + key_floats<D, ROWS>();
     __shared__ SeqTile s_tile;
     __shared__ int s_found;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    if (tid < 32) {
+    auto sync_group = [&]() {
+        if (GROUPS == 1) __syncthreads();
+        else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(kGroup) : "memory");
+    };
+    if (threadIdx.x < 32) {
         SeqTile t;
         const bool ok = find_seq_tile(a.cu_seqlens, a.N, a.T, a.G, kRows, blockIdx.x, t);
-        if (tid == 0) {
+        if (threadIdx.x == 0) {
             s_found = ok;
             if (ok) s_tile = t;
         }
@@ -75,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_simt_kernel(const AttnArgs a
     const int32_t last_token = (int32_t)(min(row0 + kRows, nrows) - 1) / a.G;
     const int32_t first_token = (int32_t)(row0 / a.G);
 
-    for (int i = tid; i < kRows * (D / 4); i += kThreads) {
+    for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
         const int r = i / (D / 4), c = (i % (D / 4)) * 4;
         const int64_t row = row0 + r;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -104,9 +120,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_simt_kernel(const AttnArgs a
             for (int j = 0; j < CW; ++j) acc[i][n][j] = 0.f;
     }
 
-    for (int32_t k0 = 0; k0 <= last_token; k0 += kKeys) {
-        __syncthreads();  // the last tile's weights and values are done with
-        for (int i = tid; i < kKeys * (D / 4); i += kThreads) {
+    __syncthreads();  // the queries
+    for (int32_t k0 = group * kKeys; k0 <= last_token; k0 += GROUPS * kKeys) {
+        sync_group();  // the last tile's weights and values are done with
+        for (int i = tid; i < kKeys * (D / 4); i += kGroup) {
             const int r = i / (D / 4), c = (i % (D / 4)) * 4;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
             if (k0 + r <= last_token) {
@@ -117,12 +134,13 @@ __global__ void __launch_bounds__(kThreads, 2) attn_simt_kernel(const AttnArgs a
             *reinterpret_cast<float4 *>(sk + r * KS + c) = x;
             *reinterpret_cast<float4 *>(sv + r * D + c) = y;
         }
-        __syncthreads();
-        float s[4][4];
+        sync_group();
+        // sums over the even and the odd channels, two to an instruction
+        float2 s2[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+            for (int j = 0; j < 4; ++j) s2[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
         for (int c = 0; c < D; c += 4) {
             float4 qv[4], kv[4];
@@ -136,14 +154,19 @@ __global__ void __launch_bounds__(kThreads, 2) attn_simt_kernel(const AttnArgs a
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
-                    s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
-                    s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
-                    s[i][j] = fmaf(qv[i].w, kv[j].w, s[i][j]);
+                    s2[i][j] = f2_fma(make_float2(qv[i].x, qv[i].y),
+                                      make_float2(kv[j].x, kv[j].y), s2[i][j]);
+                    s2[i][j] = f2_fma(make_float2(qv[i].z, qv[i].w),
+                                      make_float2(kv[j].z, kv[j].w), s2[i][j]);
                 }
         }
+        float s[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = s2[i][j].x + s2[i][j].y;
         const bool masked = k0 + kKeys - 1 > first_token;  // some key is past some row
-        __syncthreads();  // the keys are done with: the weights take their place
+        sync_group();  // the keys are done with: the weights take their place
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float mx = m[i];
@@ -173,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_simt_kernel(const AttnArgs a
 #pragma unroll
                 for (int j = 0; j < CW; ++j) acc[i][n][j] *= corr;
         }
-        __syncthreads();
+        sync_group();
         const int32_t kend = min(kKeys, last_token + 1 - k0);
         for (int kk = 0; kk < kend; kk += 4) {
             float4 pv[4];
@@ -200,13 +223,59 @@ __global__ void __launch_bounds__(kThreads, 2) attn_simt_kernel(const AttnArgs a
                     // a masked key adds nothing, whatever its value row holds
                     if (masked && k0 + kk + u > tok[i]) continue;
 #pragma unroll
-                    for (int n = 0; n < CN; ++n)
+                    for (int n = 0; n < CN; ++n) {
+                        if constexpr (CW == 1) {
+                            acc[i][n][0] = fmaf(p, vv[n][0], acc[i][n][0]);
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < CW; ++j)
-                            acc[i][n][j] = fmaf(p, vv[n][j], acc[i][n][j]);
+                            for (int j = 0; j < CW; j += 2) {
+                                const float2 y = f2_fma(make_float2(p, p),
+                                                        make_float2(vv[n][j], vv[n][j + 1]),
+                                                        make_float2(acc[i][n][j], acc[i][n][j + 1]));
+                                acc[i][n][j] = y.x;
+                                acc[i][n][j + 1] = y.y;
+                            }
+                        }
+                    }
                 }
             }
         }
+    }
+    if constexpr (GROUPS > 1) {
+        // the other groups' states through the (now free) tiles: weighted
+        // sums, maximum and sum of every row
+        __syncthreads();
+        if (group > 0) {
+            float *mine = smem + (group - 1) * ROWS * (D + 2);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float *r = mine + (ty * 4 + i) * (D + 2);
+                if (tx == 0) {
+                    r[D] = m[i];
+                    r[D + 1] = l[i];
+                }
+#pragma unroll
+                for (int n = 0; n < CN; ++n)
+#pragma unroll
+                    for (int j = 0; j < CW; ++j) r[n * 64 + tx * CW + j] = acc[i][n][j];
+            }
+        }
+        __syncthreads();
+        if (group > 0) return;
+        for (int g = 1; g < GROUPS; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float *r = smem + ((g - 1) * ROWS + ty * 4 + i) * (D + 2);
+                const float mx = fmaxf(m[i], r[D]), ref = mx == -INFINITY ? 0.f : mx;
+                const float f0 = exp2f((m[i] - ref) * c2), f1 = exp2f((r[D] - ref) * c2);
+                m[i] = mx;
+                l[i] = l[i] * f0 + r[D + 1] * f1;
+#pragma unroll
+                for (int n = 0; n < CN; ++n)
+#pragma unroll
+                    for (int j = 0; j < CW; ++j)
+                        acc[i][n][j] = acc[i][n][j] * f0 + r[n * 64 + tx * CW + j] * f1;
+            }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -228,16 +297,26 @@ __global__ void __launch_bounds__(kThreads, 2) attn_simt_kernel(const AttnArgs a
     }
 }
 
-template <typename T, int D>
-cudaError_t launch_t(const AttnArgs &a, cudaStream_t stream) {
-    constexpr size_t bytes = smem_bytes<D>();
-    const cudaError_t e = allow_smem<attn_simt_kernel<T, D>>(bytes);
+template <typename T, int D, int ROWS, int GROUPS>
+cudaError_t launch_rows(const AttnArgs &a, cudaStream_t stream) {
+    constexpr size_t bytes = smem_bytes<D, ROWS, GROUPS>();
+    static_assert((GROUPS - 1) * ROWS * (D + 2) * sizeof(float) <= bytes, "the join fits");
+    const cudaError_t e = allow_smem<attn_simt_kernel<T, D, ROWS, GROUPS>>(bytes);
     if (e != cudaSuccess) return e;
     // every sequence's last tile may be short: at most N more than the rows fill
-    const int64_t tiles = (int64_t)a.T * a.G / kRows + a.N;
+    const int64_t tiles = (int64_t)a.T * a.G / ROWS + a.N;
     const dim3 grid((unsigned)tiles, (unsigned)a.HKV);
-    attn_simt_kernel<T, D><<<grid, kThreads, bytes, stream>>>(a);
+    attn_simt_kernel<T, D, ROWS, GROUPS><<<grid, GROUPS * ROWS * 4, bytes, stream>>>(a);
     return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_t(const AttnArgs &a, cudaStream_t stream) {
+    const int64_t tiles = ((int64_t)a.T * a.G / 64 + 1) * a.HKV;
+    // (D = 128: two groups are what shared memory holds)
+    if (tiles < 2 * (int64_t)device_sms())
+        return launch_rows<T, D, 32, (D == 128 ? 2 : 4)>(a, stream);
+    return launch_rows<T, D, 64, 1>(a, stream);
 }
 
 template <typename T>
