@@ -632,8 +632,8 @@ kdaStatus_t kda_attn_fwd(const void *q, const void *k, const void *v, float scal
  *   q           [T, HQ, d] dtype or NULL (then q_out is NULL too)
  *   k, v        [T, HKV, d] dtype
  *   cu_seqlens  [N + 1] int32 device; NULL when N == 1 (one sequence) or
- *               T == N (one token of every sequence).  Rows outside every
- *               sequence are not read, and their outputs are left as they were.
+ *               T == N (one token of every sequence).  Outputs of rows outside
+ *               every sequence are left as they were.
  *   cache_lens  [N] int32 device: tokens each sequence holds before the call
  *               (not changed by the call)
  *   rope        NULL: no rotation (q is copied to q_out, k as it is)

@@ -11,8 +11,9 @@
 // once, in 16-byte vectors.  A work unit is two vectors of one head's row:
 // the two whose channels pair up (halves), or any two neighbours
 // (interleaved pairs, and channels past rot_dim).  A CTA takes TOK tokens:
-// one thread per token looks its position and page up, then all threads walk
-// the CTA's units (heads of q, then k, then v).
+// one thread per token looks its position and page up (two dependent reads)
+// while the others' first vectors are already on their way, then all threads
+// walk the CTA's units (heads of q, then k, then v), one unit ahead.
 #include <cstdint>
 #include <cuda_bf16.h>
 
@@ -21,10 +22,10 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 256;
-#ifndef KTOK
-#define KTOK 4
-#endif
+// Up to so many tokens a CTA of 256 threads takes one (256 tokens, 32/8 heads:
+// 3.2 us); beyond, CTAs of 128 threads take two (16384 tokens: 73 us, 6.1 TB/s,
+// where a plain copy of as many bytes runs at 5.3; 4 tokens to 256 threads:
+// 78 us).
 constexpr int kFewTokens = 1024;
 
 template <typename T>
@@ -124,8 +125,8 @@ struct Unit {
     bool halves;               // the two vectors pair up
 };
 
-template <typename T, int D, int TOK>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs a) {
+template <typename T, int D, int TOK, int kThreads>
+__global__ void __launch_bounds__(kThreads, TOK == 1 ? 1 : 9) cache_append_kernel(const AppendArgs a) {
     constexpr int V = Row<T>::V;
     constexpr int UNITS = D / V / 2;  // units per head row
     __shared__ Place place[TOK];
@@ -230,11 +231,9 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const AppendArgs
 template <typename T, int D>
 cudaError_t launch_t(const AppendArgs &a, cudaStream_t stream) {
     if (a.T <= kFewTokens) {
-        cache_append_kernel<T, D, 1><<<(unsigned)a.T, kThreads, 0, stream>>>(a);
+        cache_append_kernel<T, D, 1, 256><<<(unsigned)a.T, 256, 0, stream>>>(a);
     } else {
-        constexpr int TOK = KTOK;
-        cache_append_kernel<T, D, TOK>
-            <<<(unsigned)((a.T + TOK - 1) / TOK), kThreads, 0, stream>>>(a);
+        cache_append_kernel<T, D, 2, 128><<<(unsigned)((a.T + 1) / 2), 128, 0, stream>>>(a);
     }
     return cudaGetLastError();
 }
