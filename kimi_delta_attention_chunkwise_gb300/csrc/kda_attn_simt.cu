@@ -75,7 +75,8 @@ attn_simt_kernel(const AttnArgs a) {
     };
     if (threadIdx.x < 32) {
         SeqTile t;
-        const bool ok = find_seq_tile(a.cu_seqlens, a.N, a.T, a.G, kRows, blockIdx.x, t);
+        TileCursor cursor;
+        const bool ok = find_seq_tile(a.cu_seqlens, a.N, a.T, a.G, kRows, blockIdx.x, cursor, t);
         if (threadIdx.x == 0) {
             s_found = ok;
             if (ok) s_tile = t;

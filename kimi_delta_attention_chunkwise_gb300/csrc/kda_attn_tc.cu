@@ -533,10 +533,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             uint32_t index = blockIdx.x, e0 = 0, masked = 0, used[2] = {0, 0};
             bool ok = true, asked = false, have = true;
             uint32_t item = 0;
+            TileCursor cursor;
             for (; ok; ++item) {
                 SeqTile st;
                 const bool found = have && find_seq_tile(a.cu_seqlens, a.N, a.T, 1, 2 * R,
-                                                         index / a.HKV, st);
+                                                         index / a.HKV, cursor, st);
                 Job job;
                 job.n = 0;
                 if (found) {
@@ -723,7 +724,6 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t stream) {
     const cudaError_t e = allow_smem<attn_tc_kernel<D>>(smem_bytes<D>());
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)a.T / (2 * R) + a.N;
-    if (tiles * a.HKV > INT32_MAX) return cudaErrorInvalidValue;
     attn_tc_kernel<D><<<(unsigned)(tiles * a.HKV), kThreads, smem_bytes<D>(), stream>>>(mq, mk, mv, a);
     return cudaGetLastError();
 }

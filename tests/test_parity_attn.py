@@ -131,9 +131,7 @@ def test_masked_places_do_not_reach_a_row(dtype, engine, d, value):
     out, _ = kda.kda_attn_fwd(q, k, v, 0.1, _cu(lens), engine=engine)
     out2, _ = kda.kda_attn_fwd(q, k2, v, 0.1, _cu(lens), engine=engine)
     wb = _tensor(dtype, d, engine)
-    keep = torch.ones(sum(lens), dtype=torch.bool)
-    keep[bad:360] = False
-    for o, kk, heads in ((out, k, slice(0, HQ)), (out2, k2, slice(2, 2))):
+    for o, kk in ((out, k), (out2, k2)):
         ref = reference(q[60:bad], kk[60:bad], v[60:bad], 0.1, 0)
         check(o[60:bad], None, ref, bad - 60, d, wb)
         for a, n in ((0, 60), (360, 60)):
@@ -178,6 +176,45 @@ def test_more_sequences_than_a_warp_and_garbage_offsets():
         kda.kda_attn_fwd(q, k, v, 0.1, bad, guard[4:-4], engine=engine)
         torch.cuda.synchronize()
         assert (guard[:4] == 3).all() and (guard[-4:] == 3).all()
+
+
+@pytest.mark.parametrize("engine", ["auto", "simt"])
+def test_thousands_of_sequences(engine):
+    """More sequences than one search step covers, empty ones among them: every
+    row is some sequence's, and none is missed."""
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 6, (3000,), generator=g).tolist()
+    T = sum(lens)
+    q, k, v = _qkv(31, T, 2, 1, 64, "bf16")
+    out = torch.full((T, 2, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    kda.kda_attn_fwd(q, k, v, 0.1, _cu(lens), out, engine=engine)
+    _check_packed(q, k, v, 0.1, lens, out, None, engine != "simt")
+
+
+@pytest.mark.parametrize("engine,d", [("auto", 128), ("auto", 64), ("simt", 64)])
+def test_a_rows_own_nan_stays_its_own(engine, d):
+    """A NaN query makes its row NaN and no other."""
+    q, k, v = _qkv(37, 300, 6, 2, d, "bf16")
+    q[100, 1, 3] = float("nan")
+    out, _ = kda.kda_attn_fwd(q, k, v, 0.1, engine=engine)
+    assert torch.isnan(out[100, 1]).all()
+    out[100, 1], q[100, 1, 3] = 0, 0
+    ref = reference(q, k, v, 0.1, 0)
+    keep = torch.ones(300, 6, dtype=torch.bool)
+    keep[100, 1] = False
+    flat = [x[keep][:, None] for x in ref]
+    check(out.cpu()[keep][:, None], None, flat, 300, d, engine != "simt")
+
+
+def test_nothing_to_do():
+    q, k, v = _qkv(1, 0, 4, 2, 64, "bf16")
+    out, _ = kda.kda_attn_fwd(q, k, v, 0.1, _cu([0, 0]))
+    assert out.shape == q.shape
+    q, k, v = _qkv(1, 5, 4, 2, 64, "bf16")
+    out = torch.full_like(q, 3.0)
+    for engine in ("auto", "simt"):
+        kda.kda_attn_fwd(q, k, v, 0.1, _cu([0, 0]), out, engine=engine)
+        assert (out == 3).all()
 
 
 def test_offsets_past_32_bits():
