@@ -38,7 +38,7 @@
 // Masked places: scores are masked by selection, so masked keys are free to
 // hold anything.  A masked weight is an exact 0, but 0 times an infinity or a
 // NaN in a value row is NaN: warps 10-11 look through every value tile that
-// holds a masked place before the MMA reads it, set the rows behind the CTA's
+// holds a masked place before the MMA reads it, set the rows behind the item's
 // last token to zero and replace non-finite values by zero; if there were
 // any, the rows that do see them get them added at the end (`bad`).
 //
@@ -182,6 +182,36 @@ __device__ __forceinline__ float2 f2_add(float2 a, float2 b) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
+// Eight 16-byte vectors of each of eight neighbouring lanes, transposed: v[i]
+// of lane j becomes v[j] of lane i.
+__device__ __forceinline__ void transpose_8(uint4 (&v)[8], int lane) {
+#pragma unroll
+    for (int m = 1; m < 8; m <<= 1) {
+        const bool up = lane & m;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i & m) continue;
+            uint4 &lo = v[i], &hi = v[i | m];
+            uint4 x = up ? lo : hi;
+            x.x = __shfl_xor_sync(0xffffffffu, x.x, m);
+            x.y = __shfl_xor_sync(0xffffffffu, x.y, m);
+            x.z = __shfl_xor_sync(0xffffffffu, x.z, m);
+            x.w = __shfl_xor_sync(0xffffffffu, x.w, m);
+            if (up) lo = x;
+            else hi = x;
+        }
+    }
+}
+// Not 0 if one of eight bf16 has an exponent of all ones (infinity or NaN):
+// its exponent field carries into the sign's place.
+__device__ __forceinline__ uint32_t all_ones(const uint4 &x) {
+    uint32_t y = 0;
+    y |= (x.x & 0x7F807F80u) + 0x00800080u;
+    y |= (x.y & 0x7F807F80u) + 0x00800080u;
+    y |= (x.z & 0x7F807F80u) + 0x00800080u;
+    y |= (x.w & 0x7F807F80u) + 0x00800080u;
+    return y & 0x80008000u;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -206,7 +236,8 @@ __device__ __forceinline__ void request_block(uint4 *to, uint64_t *bar) {
         "r"(smem_u32(bar))
         : "memory");
 }
-__device__ __forceinline__ bool answered_block(const uint4 *from, uint32_t &index) {
+constexpr uint32_t kNoBlock = 0xffffffffu;  // every block has started (no more requests then)
+__device__ __forceinline__ uint32_t answered_block(const uint4 *from) {
     uint32_t got, x;
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
@@ -218,8 +249,7 @@ __device__ __forceinline__ bool answered_block(const uint4 *from, uint32_t &inde
         : "=&r"(got), "=&r"(x)
         : "r"(smem_u32(from))
         : "memory");
-    index = x;
-    return got != 0;
+    return got ? x : kNoBlock;
 }
 
 template <int D>
@@ -399,21 +429,23 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 const int64_t token = (int64_t)job.begin + tok;
                 const int64_t head = (int64_t)job.kvh * a.G + (row - tk * a.G);
                 const bool mine = tk < job.nt[t];
-                const bool bad = sh.bad[item % kJobs] != 0;
+                const bool bad = mine && sh.bad[item % kJobs] != 0;
                 if (mine && a.lse) a.lse[token * a.HQ + head] = (ref + log2f(sum)) * kLn2;
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    float x[32];
-                    __syncwarp();  // the load is the whole warp's
-                    ld32_nowait(o_addr + c, x);
-                    wait_ld32(x);
-                    if (c + 32 == D) {
+                const int64_t at = mine ? (token * a.HQ + head) * D : -1;
+                // columns c .. c + N - 1 of the row, ready to be rounded
+                auto columns = [&](int c, auto &x) {
+                    constexpr int N = sizeof(x) / sizeof(float);
+                    __syncwarp();  // the loads are the whole warp's
+#pragma unroll
+                    for (int i = 0; i < N; i += 32) ld32_nowait(o_addr + c + i, x + i);
+#pragma unroll
+                    for (int i = 0; i < N; i += 32) wait_ld32(x + i);
+                    if (c + N == D) {
                         tc_fence_before();
                         arrive_warp(&sh.o_free[t]);
                     }
-                    if (!mine) continue;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] *= inv;
+                    for (int i = 0; i < N; ++i) x[i] *= inv;
                     if (bad) {
                         // non-finite values of the tiles that were looked through
                         const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) +
@@ -421,26 +453,50 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                                                  (int64_t)job.kvh * D + c;
                         for (int32_t k = job.first_mask * kKeyTile; k <= tok; ++k)
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
+                            for (int i = 0; i < N; ++i) {
                                 const float y = __bfloat162float(v[k * a.v_stride + i]);
                                 if (!isfinite(y)) x[i] += y;
                             }
                     }
-                    const int64_t at = (token * a.HQ + head) * D + c;
-                    if (a.out_f32) {
-                        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at);
+                    __syncwarp();
+                };
+                // eight lanes store 128 bytes of one row at a time: a lane's
+                // own 16 bytes of 32 rows at once would be 32 lines a store
+                // (5 us for a tile, more than a short item's other work)
+                auto store = [&](uint4 (&v)[8], char *base, int es) {
+                    transpose_8(v, lane);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        const int64_t o = __shfl_sync(0xffffffffu, at, (lane & 24) + r);
+                        if (o >= 0) *reinterpret_cast<uint4 *>(base + o * es + (lane & 7) * 16) = v[r];
+                    }
+                };
+                if (a.out_f32) {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        float x[32];
+                        columns(c, x);
+                        uint4 v[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-                    } else {
-                        uint4 *dst =
-                            reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at);
+                            v[i] = make_uint4(__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]),
+                                              __float_as_uint(x[4 * i + 2]),
+                                              __float_as_uint(x[4 * i + 3]));
+                        store(v, reinterpret_cast<char *>(static_cast<float *>(a.out) + c), 4);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 64) {
+                        float x[64];
+                        columns(c, x);
+                        uint4 v[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            dst[i] = make_uint4(pack_bf16x2(x[8 * i], x[8 * i + 1]),
-                                                pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
-                                                pack_bf16x2(x[8 * i + 4], x[8 * i + 5]),
-                                                pack_bf16x2(x[8 * i + 6], x[8 * i + 7]));
+                        for (int i = 0; i < 8; ++i)
+                            v[i] = make_uint4(pack_bf16x2(x[8 * i], x[8 * i + 1]),
+                                              pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
+                                              pack_bf16x2(x[8 * i + 4], x[8 * i + 5]),
+                                              pack_bf16x2(x[8 * i + 6], x[8 * i + 7]));
+                        store(v, reinterpret_cast<char *>(static_cast<__nv_bfloat16 *>(a.out) + c), 2);
                     }
                 }
                 it += n;
@@ -460,6 +516,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     if (!wait(&sh.job_full[item % kJobs], item / kJobs)) break;
                     const Job &job = sh.job[item % kJobs];
                     const int32_t n = job.n, nk[2] = {job.nk[0], job.nk[1]};
+                    const int32_t last[2] = {job.q0[0] + job.nt[0] - 1, job.q0[1] + job.nt[1] - 1};
                     if (n == 0) break;
                     // S_t of key tile j from the ring's `stage`; the last one
                     // frees the queries
@@ -497,6 +554,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                                            vd + ks * (2048 >> 4), C::IDESC_PV,
                                            (j > 0 || ks > 0) ? 1u : 0u);
                             };
+                            // steps of 16 keys that some row of the tile sees
+                            const int32_t steps = min(8, (last[t] - j * kKeyTile) / 16 + 1);
                             // the last item's O_t has been read; V_j and K_j+1
                             // have arrived when the weights have
                             ok = (j > 0 || used[t] == 0 || wait(&sh.o_free[t], used[t] - 1)) &&
@@ -504,12 +563,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll
-                            for (int ks = 0; ks < kEarly / 16; ++ks) product(ks);
+                            for (int ks = 0; ks < kEarly / 16; ++ks)
+                                if (ks < steps) product(ks);
                             ok = wait(&sh.p_rest[t], it[t] + j);
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll
-                            for (int ks = kEarly / 16; ks < kKeyTile / 16; ++ks) product(ks);
+                            for (int ks = kEarly / 16; ks < kKeyTile / 16; ++ks)
+                                if (ks < steps) product(ks);
                             mma_commit(&sh.pv_done[t]);
                             if (j + 1 < nk[t]) scores(t, j + 1, sk);
                         }
@@ -531,13 +592,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             // ---- work and copies ----------------------------------------
             const uint32_t q_bytes = (uint32_t)(R * a.G) * 128 * C::PANELS;
             uint32_t index = blockIdx.x, e0 = 0, masked = 0, used[2] = {0, 0};
-            bool ok = true, asked = false, have = true;
-            uint32_t item = 0;
+            bool ok = true, asked = false;
+            uint32_t item = 0, asks = 0;
             TileCursor cursor;
             for (; ok; ++item) {
                 SeqTile st;
-                const bool found = have && find_seq_tile(a.cu_seqlens, a.N, a.T, 1, 2 * R,
-                                                         index / a.HKV, cursor, st);
+                const bool found = index != kNoBlock &&
+                                   find_seq_tile(a.cu_seqlens, a.N, a.T, 1, 2 * R, index / a.HKV,
+                                                 cursor, st);
                 Job job;
                 job.n = 0;
                 if (found) {
@@ -561,7 +623,22 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     sh.bad[item % kJobs] = 0;
                     mbar_arrive(&sh.job_full[item % kJobs]);
                 }
-                if (!found) break;
+                if (!found) {
+                    // the grid's other blocks have nothing to do either: they
+                    // are taken here, which is cheaper than their starting
+                    while (index != kNoBlock && ok) {
+                        if (lane == 0) request_block(&sh.next, &sh.next_full);
+                        asked = true;
+                        ok = wait_warp(&sh.next_full, asks);
+                        if (!ok) break;
+                        asked = false;
+                        ++asks;
+                        index = answered_block(&sh.next);
+                        fence_proxy_async();  // the answer is read before it is overwritten
+                        __syncwarp();
+                    }
+                    break;
+                }
                 if (lane == 0) {
                     auto load_q = [&](int t) {
                         if (job.nk[t] == 0 || !ok) return;
@@ -599,17 +676,18 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         if (i == 0) load_q(1);
                     }
                 }
-                ok = __all_sync(0xffffffffu, ok) && wait_warp(&sh.next_full, item);
+                ok = __all_sync(0xffffffffu, ok) && wait_warp(&sh.next_full, asks);
                 if (!ok) break;
                 asked = false;
-                have = answered_block(&sh.next, index);
+                ++asks;
+                index = answered_block(&sh.next);
                 fence_proxy_async();  // the answer is read before it is overwritten
                 __syncwarp();
             }
             if (lane == 0) {
                 // the CTA may end when every copy and answer has landed and
                 // every commit that names one of its barriers has arrived
-                if (asked) (void)mbar_wait_bounded(&sh.next_full, item & 1, kWaitLimit);
+                if (asked) (void)mbar_wait_bounded(&sh.next_full, asks & 1, kWaitLimit);
                 for (int t = 0; t < 2; ++t)
                     if (used[t]) {
                         (void)mbar_wait_bounded(&sh.q_full[t], (used[t] - 1) & 1, kWaitLimit);
@@ -640,28 +718,39 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         ++masked;
                         ok = wait_warp(&sh.v_raw[mi], mu);
                         if (!ok) break;
-                        const int32_t rows = last + 1 - j * kKeyTile;  // rows the item sees
-                        uint8_t *v = skv + sv * C::TILE;
+                        // rows the item sees, and those the MMAs read
+                        const int32_t rows = min(kKeyTile, last + 1 - j * kKeyTile);
+                        const int32_t read = (rows + 15) & ~15;
                         bool found = false;
-#pragma unroll 4
-                        for (int i = who; i < C::PANELS * kKeyTile * 8; i += 64) {
-                            const int r = (i >> 3) & (kKeyTile - 1);
-                            uint4 *p = reinterpret_cast<uint4 *>(v + i * 16);
-                            uint4 x = r < rows ? *p : make_uint4(0, 0, 0, 0);
-                            uint32_t *w = &x.x;
-                            uint32_t any = 0;
+#pragma unroll 1
+                        for (int p = 0; p < C::PANELS; ++p) {
+                            uint4 *v = reinterpret_cast<uint4 *>(skv + sv * C::TILE + p * C::PANEL);
+                            for (int i = rows * 8 + who; i < read * 8; i += 64)
+                                v[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+                            for (int i0 = who; i0 < rows * 8; i0 += 64 * 8) {
+                                uint4 x[8];
+                                uint32_t any = 0;
 #pragma unroll
-                            for (int b = 0; b < 4; ++b) any |= (w[b] & 0x7F807F80u) + 0x00800080u;
-                            any &= 0x80008000u;  // an exponent of all ones
-                            if (any) {
+                                for (int u = 0; u < 8; ++u)
+                                    x[u] = i0 + u * 64 < rows * 8 ? v[i0 + u * 64]
+                                                                  : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                                for (int u = 0; u < 8; ++u) any |= all_ones(x[u]);
+                                if (any == 0) continue;
                                 found = true;
 #pragma unroll
-                                for (int b = 0; b < 4; ++b) {
-                                    if ((w[b] & 0x7F80u) == 0x7F80u) w[b] &= 0xFFFF0000u;
-                                    if ((w[b] & 0x7F800000u) == 0x7F800000u) w[b] &= 0x0000FFFFu;
+                                for (int u = 0; u < 8; ++u) {
+                                    if (all_ones(x[u]) == 0) continue;
+                                    uint32_t *w = &x[u].x;
+#pragma unroll
+                                    for (int b = 0; b < 4; ++b) {
+                                        if ((w[b] & 0x7F80u) == 0x7F80u) w[b] &= 0xFFFF0000u;
+                                        if ((w[b] & 0x7F800000u) == 0x7F800000u) w[b] &= 0x0000FFFFu;
+                                    }
+                                    v[i0 + u * 64] = x[u];
                                 }
                             }
-                            if (any || r >= rows) *p = x;
                         }
                         if (found) sh.bad[item % kJobs] = 1;
                         fence_proxy_async();
