@@ -555,7 +555,8 @@ kdaStatus_t kda_chunk_bwd_ws(const void *q, const void *k, const void *v,
  * The pages give softmax attention as motivation only; the formula is the
  * whole definition.  Masked places contribute nothing,
  * whatever the masked keys and values hold (infinities and NaN included).
- * Forward only: these are the serving path.
+ * Forward only: these are the serving path.  No output may overlap an input
+ * but where kda_cache_append says so.
  * ---------------------------------------------------------------------------
  */
 typedef struct {

@@ -95,7 +95,7 @@ kdaStatus_t plan_attn_step(const void *q, const kdaPagedCache_t *cache, const in
     const kdaStatus_t st = step_sizes(cache, shape, a);
     if (st != KDA_SUCCESS) return st;
     if (!scale_ok(scale)) return KDA_ERR_INVALID_ARG;
-    if (!q || !aligned(q, 16) || !out || !aligned(out, 16)) return KDA_ERR_INVALID_ARG;
+    if (!q || !aligned(q, 16) || !out || !aligned(out, 16) || out == q) return KDA_ERR_INVALID_ARG;
     if (!seq_lens || !aligned(seq_lens, 4) || !aligned(lse, 4)) return KDA_ERR_INVALID_ARG;
     a.q = q;
     a.q_stride = token_stride(shape->q_stride, shape->num_heads, shape->head_dim);
@@ -137,6 +137,7 @@ kdaStatus_t kda_attn_fwd(const void *q, const void *k, const void *v, float scal
         const void *vec[] = {q, k, v, out};
         for (const void *p : vec)
             if (!p || !aligned(p, 16)) return KDA_ERR_INVALID_ARG;
+        if (out == q || out == k || out == v) return KDA_ERR_INVALID_ARG;  // read after written
     }
     const bool tensor_ok = shape->dtype == KDA_DTYPE_BF16 &&
                            (shape->head_dim == 64 || shape->head_dim == 128);

@@ -8,7 +8,7 @@ import torch
 import kimi_delta_attention_chunkwise_gb300 as kda
 from kimi_delta_attention_chunkwise_gb300 import binding, build
 
-FAKE = 0x10000  # never dereferenced
+FAKE, OTHER = 0x10000, 0x20000  # never dereferenced
 OK, INVALID, UNSUPPORTED = (kda.KDA_SUCCESS, kda.KDA_ERR_INVALID_ARG, kda.KDA_ERR_UNSUPPORTED)
 
 
@@ -31,7 +31,7 @@ def _cache(**kw):
 
 
 def _fwd(lib, shape, scale=0.125, cu=None, **kw):
-    p = dict(q=FAKE, k=FAKE, v=FAKE, out=FAKE, lse=None)
+    p = dict(q=FAKE, k=FAKE, v=FAKE, out=OTHER, lse=None)
     p.update(kw)
     return lib.kda_attn_fwd(p["q"], p["k"], p["v"], ctypes.c_float(scale), cu, p["out"], p["lse"],
                             ctypes.byref(shape) if shape is not None else None, None)
@@ -47,7 +47,7 @@ def _append(lib, shape, cache=None, cu=None, rope=None, **kw):
 
 
 def _step(lib, shape, cache=None, scale=0.125, ws=FAKE, nbytes=1 << 40, **kw):
-    p = dict(q=FAKE, lens=FAKE, out=FAKE, lse=None)
+    p = dict(q=FAKE, lens=FAKE, out=OTHER, lse=None)
     p.update(kw)
     cache = _cache() if cache is None else cache
     return lib.kda_attn_step_ws(p["q"], ctypes.byref(cache), p["lens"], ctypes.c_float(scale),
@@ -86,6 +86,7 @@ def test_fwd_arguments(lib):
     for name in ("q", "k", "v", "out"):
         assert _fwd(lib, _shape(), **{name: None}) == INVALID
         assert _fwd(lib, _shape(), **{name: FAKE + 8}) == INVALID
+    assert _fwd(lib, _shape(), out=FAKE) == INVALID              # in place
     assert _fwd(lib, _shape(), lse=FAKE + 2) == INVALID
     assert _fwd(lib, _shape(), cu=FAKE + 2) == INVALID
     assert _fwd(lib, _shape(engine=7)) == INVALID
@@ -140,6 +141,7 @@ def test_step_arguments(lib):
     for name in ("q", "out", "lens"):
         assert _step(lib, s, **{name: None}) == INVALID
     assert _step(lib, s, q=FAKE + 8) == INVALID
+    assert _step(lib, s, out=FAKE) == INVALID                    # in place
     assert _step(lib, s, lse=FAKE + 1) == INVALID
     assert _step(lib, s, ws=FAKE + 16) == INVALID                # 256-byte alignment
     n = ctypes.c_size_t(0)

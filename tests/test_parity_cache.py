@@ -99,6 +99,61 @@ def test_append_one_token_each_in_place_and_without_q(dtype):
                                        table, held, [1] * N, page))
 
 
+def test_append_one_sequence_without_offsets():
+    T, HKV, d, page, held = 70, 2, 128, 64, 60
+    k, v = (_randn(i, T, HKV, d, dtype="bf16") for i in (1, 2))
+    table, pages = tables([3], 3)
+    kc = _randn(3, pages, HKV, page, d, dtype="bf16")
+    gk, gv = kc.cuda(), kc.cuda()
+    kda.kda_cache_append(k.cuda(), v.cuda(), gk, gv, table.cuda(), _i32([held]))
+    assert torch.equal(gk.cpu(), _fill(kc, k, table, [held], [T], page))
+    assert torch.equal(gv.cpu(), _fill(kc, v, table, [held], [T], page))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_append_many_tokens_and_graph_replay(dtype):
+    """More tokens than take the one-token CTAs, an odd number of them; a
+    captured call replayed on other tokens and lengths."""
+    HQ, HKV, d, page = 3, 3, 64, 32
+    lens, held = [700, 1, 0, 800], [3, 100, 50, 31]
+    T = sum(lens)
+    need = [(h + n + 40 + page - 1) // page for h, n in zip(held, lens)]
+    table, pages = tables(need, max(need))
+    rope = rope_table(1000, d)
+    x = [_randn(i, T, HKV, d, dtype=dtype) for i in range(6)]
+    zero = torch.zeros(pages, HKV, page, d, dtype=DT[dtype])
+    gk, gv = zero.cuda(), zero.cuda()
+    q, k, v = (t.cuda() for t in x[:3])
+    now, q_out, k_out = _i32(held), torch.empty_like(q), torch.empty_like(k)
+    cu, gt, gr = _cu(lens), table.cuda(), rope.cuda()
+
+    def call():
+        kda.kda_cache_append(k, v, gk, gv, gt, now, cu, q=q, q_out=q_out, k_out=k_out, rope=gr)
+
+    def expect(data, at):
+        pos = torch.cat([torch.arange(h, h + n) for h, n in zip(at, lens)])
+        rk = rotate(data[1], pos, rope, False)
+        assert torch.equal(q_out.cpu(), rotate(data[0], pos, rope, False))
+        assert torch.equal(k_out.cpu(), rk)
+        assert torch.equal(gk.cpu(), _fill(zero, rk, table, at, lens, page))
+        assert torch.equal(gv.cpu(), _fill(zero, data[2], table, at, lens, page))
+
+    call()
+    expect(x[:3], held)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    moved = [h + 37 for h in held]
+    for t, new in zip((q, k, v), x[3:]):
+        t.copy_(new)
+    now.copy_(_i32(moved))
+    gk.zero_()
+    gv.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    expect(x[3:], moved)
+
+
 def test_append_views_and_rows_outside_sequences():
     HQ, HKV, d, page, T = 4, 2, 64, 16, 60
     lens, start, held = [20, 13], 9, [3, 40]
