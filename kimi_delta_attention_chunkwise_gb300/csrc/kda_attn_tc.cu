@@ -62,7 +62,6 @@ constexpr int kThreads = 384;
 constexpr int kRowTile = 128, kKeyTile = 128;
 constexpr long long kWaitLimit = 2000000000LL;  // SM clocks, about a second
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kEarly = 96;  // keys whose weights are handed over first
 constexpr float kMoveBy = 8.f;  // powers of two a row's maximum may pass its reference by
 
 template <int D>
@@ -71,6 +70,11 @@ struct Cfg {
     static constexpr uint32_t PANEL = kRowTile * 128;     // bytes
     static constexpr uint32_t TILE = PANELS * PANEL;      // one Q, K or V tile
     static constexpr int STAGES = D == 128 ? 5 : 8;       // K and V tiles in flight
+    // keys whose weights are handed over first, so that the product starts
+    // while the others' are taken (8192 tokens, 40/8 heads, d = 128: 32 keys
+    // 458 us, 64 473, 96 482, in four parts 465; d = 64, 32/8 heads: 64 keys
+    // 266 us, 32 280, 96 268)
+    static constexpr int EARLY = D == 128 ? 32 : 64;
     static constexpr uint32_t S_COL = 128, O_BASE = 256;  // TMEM columns: S_0, S_1, O_0, O_1
     static constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, kKeyTile);
     static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D) | (1u << 16);  // V is N-major
@@ -408,11 +412,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         p[i] = pack_bf16x2(x.x, x.y);
                     }
                     st16_nowait(s_addr + h * 16, p);
-                    if (h >= 2) {
-                        // the product starts on the first kEarly keys' weights
+                    if (h == C::EARLY / 32 - 1 || h == 3) {
                         tmem_wait_st();
                         tc_fence_before();
-                        arrive_warp(h == 2 ? &sh.p_full[t] : &sh.p_rest[t]);
+                        arrive_warp(h < 3 ? &sh.p_full[t] : &sh.p_rest[t]);
                         __syncwarp();
                     }
                 }
@@ -563,13 +566,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll
-                            for (int ks = 0; ks < kEarly / 16; ++ks)
+                            for (int ks = 0; ks < C::EARLY / 16; ++ks)
                                 if (ks < steps) product(ks);
                             ok = wait(&sh.p_rest[t], it[t] + j);
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll
-                            for (int ks = kEarly / 16; ks < kKeyTile / 16; ++ks)
+                            for (int ks = C::EARLY / 16; ks < kKeyTile / 16; ++ks)
                                 if (ks < steps) product(ks);
                             mma_commit(&sh.pv_done[t]);
                             if (j + 1 < nk[t]) scores(t, j + 1, sk);
