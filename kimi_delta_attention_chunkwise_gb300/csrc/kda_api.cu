@@ -3,6 +3,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "kda_attn.cuh"
 #include "kda_internal.cuh"
 
 namespace kda {

@@ -3,7 +3,7 @@
 #include <cmath>
 #include <cstdint>
 
-#include "kda_internal.cuh"
+#include "kda_attn.cuh"
 
 namespace kda {
 namespace {

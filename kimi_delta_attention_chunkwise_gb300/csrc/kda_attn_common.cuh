@@ -4,7 +4,7 @@
 
 #include <cstdint>
 
-#include "kda_internal.cuh"
+#include "kda_attn.cuh"
 
 namespace kda {
 

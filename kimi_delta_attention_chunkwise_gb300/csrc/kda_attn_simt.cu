@@ -25,6 +25,7 @@
 #include <cuda_bf16.h>
 
 #include "kda_attn_common.cuh"
+#include "kda_internal.cuh"
 
 namespace kda {
 namespace {

@@ -21,6 +21,7 @@
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
+#include "kda_attn.cuh"
 #include "kda_internal.cuh"
 #include "tc_ptx.cuh"
 

@@ -48,12 +48,18 @@
 #include <cstdint>
 #include <cstring>
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
 #include "kda_attn_common.cuh"
+#include "kda_internal.cuh"
 #include "tc_ptx.cuh"
 
 namespace kda {
+
+// cuTensorMapEncodeTiled, fetched from the driver once (kda_chunk_tc.cu).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
 namespace {
 
 using namespace tc;
@@ -800,6 +806,23 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+}
+
+// A bf16 [T, heads, D] tensor with a token stride (in elements) as a 3-D map
+// {D, heads, T} whose box is [box_tokens x box_heads] rows of 64 channels with
+// the 128-byte swizzle; rows past T read as zero.
+bool encode_rows_map(CUtensorMap *m, const void *base, int32_t d, int32_t heads, int32_t T,
+                     int64_t stride, uint32_t box_heads, uint32_t box_tokens) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)T};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64u, box_heads, box_tokens};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D>

@@ -17,7 +17,7 @@
 #include <cstdint>
 #include <cuda_bf16.h>
 
-#include "kda_internal.cuh"
+#include "kda_attn.cuh"
 
 namespace kda {
 namespace {
