@@ -20,12 +20,17 @@
 // 0 and 1, 8 issues the MMAs, 9 the copies and finds the work, 10-11 make
 // masked values harmless and see to it that tiles have arrived.
 //
+// S_t of key tile j + 1 and the product of tile j use the same columns of TMEM
+// (S over P): one thread issues both, and the tensor core runs them in order.
+//
 // A CTA works on one item (two row tiles of one key-value head) after another:
-// when it has begun one, it takes the grid's next block that has not started
-// (clusterlaunchcontrol), so that the next item's first copies and scores run
-// beside the last item's results, and long and short items even out.  Items
-// are numbered with a sequence's last tiles first (the longest under the
-// causal mask).
+// with the last copies of one it takes the grid's next block that has not
+// started (clusterlaunchcontrol), so that the next item's first copies and
+// scores run beside the last item's results, and long and short items even
+// out.  (Taken any earlier, a CTA with a long item ahead holds a second one
+// back from idle ones: 4096 tokens, 16 heads, 71 us instead of 52.)  Items are
+// numbered with a sequence's last tiles first (the longest under the causal
+// mask).
 //
 // The reference of a row moves only when the row's maximum has passed it by
 // more than 2^8: until then the weights stay below 2^8, which costs fp32 sums
@@ -45,6 +50,13 @@
 // Waits are bounded: one that gives up sets KDA_ERR_TIMEOUT in the status
 // word, every role leaves its loop, and the CTA ends after its copies and
 // MMAs in flight.
+//
+// What bounds it: d = 128: the tensor core (16384 tokens, 32/8 heads: 1.27 ms,
+// 1.73 PFLOP/s of the mask's lower half, 0.90 of a library matrix product's
+// best; the clocks come down with it).  d = 64: the softmax's chain of latencies
+// (8192 tokens, 32/8 heads: 1.04 PFLOP/s).  Short sequences: an item's chain of
+// copy, scores, weights, product and store (1000 x 64 tokens, 32/8 heads: 274
+// us, 4.8 TB/s).
 #include <cstdint>
 #include <cstring>
 #include <cuda.h>
@@ -121,10 +133,10 @@ constexpr uint32_t smem_bytes() {
 }
 static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "227 KB per CTA");
 
-// One lane of a converged warp.  The MMA warp runs its control flow as a whole
-// and only the MMAs and commits sit under this: the operands then stay in
-// uniform registers (issued from `if (lane == 0)`, every MMA took ~115 cycles
-// to issue, longer than the 64 it runs).
+// One lane of a converged warp, in the form whose branch the compiler knows to
+// be one thread's: the MMAs' operands then stay in uniform registers (issued
+// from `if (lane == 0)`, every MMA took ~115 cycles to issue, longer than the 64
+// it runs).
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile(
@@ -347,6 +359,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             const Job &job = sh.job[item % kJobs];
             if (!wait_warp(&sh.job_full[item % kJobs], item / kJobs) || job.n == 0) break;
             const int32_t n = job.nk[t], q0 = job.q0[t], tok = q0 + tk;
+            const bool mine = tk < job.nt[t];  // the row is a token's
             float ref = -INFINITY, sum = 0.f;  // the reference times c2
             bool ok = true;
             for (int32_t j = 0; j < n; ++j) {
@@ -376,7 +389,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
 #pragma unroll
                     for (int e = 0; e < 4; ++e) m[e] = max3(m[e], s[i + e], s[i + e + 4]);
                 const float top = fmaxf(max3(m[0], m[1], m[2]), m[3]) * c2;
-                const bool move = !(top - ref <= kMoveBy);  // also on the first tile
+                // (also on the first tile; rows without a token of their own
+                // hold anything, and would ask every time for a NaN)
+                const bool move = mine && !(top - ref <= kMoveBy);
                 if (__any_sync(0xffffffffu, move)) {
                     float f = 1.f;
                     if (move) {
@@ -437,7 +452,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 const float inv = 1.f / sum;
                 const int64_t token = (int64_t)job.begin + tok;
                 const int64_t head = (int64_t)job.kvh * a.G + (row - tk * a.G);
-                const bool mine = tk < job.nt[t];
                 const bool bad = mine && sh.bad[item % kJobs] != 0;
                 if (mine && a.lse) a.lse[token * a.HQ + head] = (ref + log2f(sum)) * kLn2;
                 const int64_t at = mine ? (token * a.HQ + head) * D : -1;
@@ -469,9 +483,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     }
                     __syncwarp();
                 };
-                // eight lanes store 128 bytes of one row at a time: a lane's
-                // own 16 bytes of 32 rows at once would be 32 lines a store
-                // (5 us for a tile, more than a short item's other work)
+                // eight lanes store 128 bytes of one row at a time (a lane's
+                // own 16 bytes of 32 rows at once are 32 lines a store: 1000 x
+                // 64 tokens 666 us where this took 621)
                 auto store = [&](uint4 (&v)[8], char *base, int es) {
                     transpose_8(v, lane);
 #pragma unroll
