@@ -55,14 +55,6 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
                        __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xFFFF0000u));
 }
 
-// (not inlined: what it keeps in registers is not the main loop's business)
-__device__ __noinline__ bool find_tile(const AttnArgs &a, int32_t tile_rows, uint32_t index,
-                                       SeqTile &out) {
-    TileCursor cursor;
-    return find_seq_tile(a.cu_seqlens, a.N, a.T, (uint32_t)a.G, (uint32_t)tile_rows, index, cursor,
-                         out);
-}
-
 template <typename T, int D, int ROWS, int GROUPS>
 __global__ void __launch_bounds__(GROUPS * ROWS * 4, GROUPS * ROWS > 64 || (GROUPS > 1 && D == 128) ? 1 : 2)
 attn_simt_kernel(const AttnArgs a) {
@@ -84,7 +76,9 @@ attn_simt_kernel(const AttnArgs a) {
     };
     if (threadIdx.x < 32) {
         SeqTile t;
-        const bool ok = find_tile(a, kRows, blockIdx.x, t);
+        TileCursor cursor;
+        const bool ok = find_seq_tile(a.cu_seqlens, a.N, a.T, (uint32_t)a.G, (uint32_t)kRows,
+                                      blockIdx.x, cursor, t);
         if (threadIdx.x == 0) {
             s_found = ok;
             if (ok) s_tile = t;

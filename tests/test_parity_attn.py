@@ -258,6 +258,28 @@ def test_streams_and_graph_replay():
         assert torch.equal(out, w)
 
 
+def test_beside_a_kda_layer_on_another_stream():
+    """A mixed stack's two kinds of layer at once: the prompt attention and the
+    KDA prefill on two streams give the bits they give one after another."""
+    T, H, d = 1500, 16, 128
+    q, k, v = _qkv(41, T, H, 4, d, "bf16")
+    x = [t / t.float().norm(dim=-1, keepdim=True) for t in _qkv(42, T, H, H, d, "bf16")[:2]]
+    x = [t.bfloat16() for t in x] + [_qkv(43, T, H, H, d, "bf16")[2]]
+    g = torch.Generator().manual_seed(44)
+    la = (-torch.rand(T, H, d, generator=g) * 0.1).cuda()
+    beta = torch.rand(T, H, generator=g).cuda()
+    cu = _cu([700, 800])
+    attn = lambda s=None: kda.kda_attn_fwd(q, k, v, 0.1, cu, stream=s)[0]
+    mixer = lambda s=None: kda.kda_chunk_fwd(*x, la, beta, 0.1, None, cu, stream=s)[0]
+    want = attn(), mixer()
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(20):
+        got = attn(s1), mixer(s2)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_tensor_engine_refuses_what_it_lacks():
     q, k, v = _qkv(1, 8, 2, 1, 32, "bf16")
     with pytest.raises(kda.KdaError) as e:
