@@ -319,9 +319,18 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     } else if (warp == 8) {
         tmem_alloc(&sh.tmem, 512);
         tmem_relinquish();
-    } else if (warp == 9 && lane < 3) {
-        const CUtensorMap *m = lane == 0 ? &map_q : lane == 1 ? &map_k : &map_v;
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+    }
+    // warp 9 looks the first item up in the meantime
+    TileCursor cursor;
+    SeqTile st;
+    bool found = false;
+    if (warp == 9) {
+        if (lane < 3) {
+            const CUtensorMap *m = lane == 0 ? &map_q : lane == 1 ? &map_k : &map_v;
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+        }
+        __syncwarp();
+        found = find_seq_tile(a.cu_seqlens, a.N, a.T, 1, 2 * R, blockIdx.x / a.HKV, cursor, st);
     }
     tc_fence_before();
     __syncthreads();
@@ -617,12 +626,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             uint32_t index = blockIdx.x, e0 = 0, masked = 0, used[2] = {0, 0};
             bool ok = true, asked = false;
             uint32_t item = 0, asks = 0;
-            TileCursor cursor;
             for (; ok; ++item) {
-                SeqTile st;
-                const bool found = index != kNoBlock &&
-                                   find_seq_tile(a.cu_seqlens, a.N, a.T, 1, 2 * R, index / a.HKV,
-                                                 cursor, st);
+                if (item > 0)
+                    found = index != kNoBlock && find_seq_tile(a.cu_seqlens, a.N, a.T, 1, 2 * R,
+                                                               index / a.HKV, cursor, st);
                 Job job;
                 job.n = 0;
                 if (found) {
