@@ -87,7 +87,7 @@ struct Cfg {
     static constexpr int PANELS = D / 64;                 // 128-byte column panels
     static constexpr uint32_t PANEL = kRowTile * 128;     // bytes
     static constexpr uint32_t TILE = PANELS * PANEL;      // one Q, K or V tile
-    static constexpr int STAGES = D == 128 ? 5 : 8;       // K and V tiles in flight
+    static constexpr int STAGES = D == 128 ? 4 : 8;       // K and V tiles in flight
     // keys whose weights are handed over first, so that the product starts
     // while the others' are taken (8192 tokens, 40/8 heads, d = 128: 32 keys
     // 458 us, 64 473, 96 482, in four parts 465; d = 64, 32/8 heads: 64 keys
@@ -125,11 +125,14 @@ struct Shared {
     int32_t abort;
 };
 
+constexpr uint32_t kStage = 32 * 128;  // bytes a softmax warp's results pass through
+
 // The tiles start at the dynamic shared memory's base, which is 1024-byte
-// aligned (the kernel has no other shared memory); Shared follows them.
+// aligned (the kernel has no other shared memory); the results' bytes and
+// Shared follow them.
 template <int D>
 constexpr uint32_t smem_bytes() {
-    return (2 + Cfg<D>::STAGES) * Cfg<D>::TILE + (uint32_t)sizeof(Shared);
+    return (2 + Cfg<D>::STAGES) * Cfg<D>::TILE + 8 * kStage + (uint32_t)sizeof(Shared);
 }
 static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "227 KB per CTA");
 
@@ -204,26 +207,6 @@ __device__ __forceinline__ float2 f2_add(float2 a, float2 b) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
-// Eight 16-byte vectors of each of eight neighbouring lanes, transposed: v[i]
-// of lane j becomes v[j] of lane i.
-__device__ __forceinline__ void transpose_8(uint4 (&v)[8], int lane) {
-#pragma unroll
-    for (int m = 1; m < 8; m <<= 1) {
-        const bool up = lane & m;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (i & m) continue;
-            uint4 &lo = v[i], &hi = v[i | m];
-            uint4 x = up ? lo : hi;
-            x.x = __shfl_xor_sync(0xffffffffu, x.x, m);
-            x.y = __shfl_xor_sync(0xffffffffu, x.y, m);
-            x.z = __shfl_xor_sync(0xffffffffu, x.z, m);
-            x.w = __shfl_xor_sync(0xffffffffu, x.w, m);
-            if (up) lo = x;
-            else hi = x;
-        }
-    }
-}
 // Not 0 if one of eight bf16 has an exponent of all ones (infinity or NaN):
 // its exponent field carries into the sign's place.
 __device__ __forceinline__ uint32_t all_ones(const uint4 &x) {
@@ -280,8 +263,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                const __grid_constant__ CUtensorMap map_v, const AttnArgs a) {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint8_t *sq = smem, *skv = smem + 2 * C::TILE;
-    Shared &sh = *reinterpret_cast<Shared *>(skv + C::STAGES * C::TILE);
+    uint8_t *sq = smem, *skv = smem + 2 * C::TILE, *sout = skv + C::STAGES * C::TILE;
+    Shared &sh = *reinterpret_cast<Shared *>(sout + 8 * kStage);
     if (smem_u32(smem) & 1023u) {  // the swizzled tiles would not match their descriptors
         *a.status = KDA_ERR_CUDA;
         return;
@@ -492,16 +475,24 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     }
                     __syncwarp();
                 };
-                // eight lanes store 128 bytes of one row at a time (a lane's
-                // own 16 bytes of 32 rows at once are 32 lines a store: 1000 x
-                // 64 tokens 666 us where this took 621)
-                auto store = [&](uint4 (&v)[8], char *base, int es) {
-                    transpose_8(v, lane);
+                // 128 bytes of every row, by way of shared memory (the 128-byte
+                // swizzle keeps both sides free of bank conflicts): eight lanes
+                // store one row's at a time, whole lines
+                uint8_t *mine_out = sout + warp * kStage;
+                auto store = [&](const uint4 (&v)[8], char *base, int es) {
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) {
-                        const int64_t o = __shfl_sync(0xffffffffu, at, (lane & 24) + r);
-                        if (o >= 0) *reinterpret_cast<uint4 *>(base + o * es + (lane & 7) * 16) = v[r];
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4 *>(mine_out + sw128_chunk(lane, i)) = v[i];
+                    __syncwarp();
+#pragma unroll
+                    for (int r = 0; r < 32; r += 4) {
+                        const int rr = r + (lane >> 3);
+                        const uint4 x =
+                            *reinterpret_cast<const uint4 *>(mine_out + sw128_chunk(rr, lane & 7));
+                        const int64_t o = __shfl_sync(0xffffffffu, at, rr);
+                        if (o >= 0) *reinterpret_cast<uint4 *>(base + o * es + (lane & 7) * 16) = x;
                     }
+                    __syncwarp();
                 };
                 if (a.out_f32) {
 #pragma unroll 1
