@@ -77,7 +77,7 @@ namespace {
 using namespace tc;
 
 constexpr int kThreads = 384;
-constexpr int kRowTile = 128, kKeyTile = 128;
+constexpr int kRowTile = 128;
 constexpr long long kWaitLimit = 2000000000LL;  // SM clocks, about a second
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMoveBy = 8.f;  // powers of two a row's maximum may pass its reference by
@@ -86,15 +86,18 @@ template <int D>
 struct Cfg {
     static constexpr int PANELS = D / 64;                 // 128-byte column panels
     static constexpr uint32_t PANEL = kRowTile * 128;     // bytes
-    static constexpr uint32_t TILE = PANELS * PANEL;      // one Q, K or V tile
-    static constexpr int STAGES = D == 128 ? 4 : 8;       // K and V tiles in flight
+    static constexpr uint32_t Q_TILE = PANELS * PANEL;
+    // keys of a tile, and score tiles of a row tile in TMEM
+    static constexpr int KEYS = D == 128 ? 128 : 64, BUFS = D == 128 ? 1 : 2;
+    static constexpr uint32_t KV_PANEL = KEYS * 128, TILE = PANELS * KV_PANEL;  // one K or V tile
+    static constexpr int STAGES = D == 128 ? 4 : 12;      // K and V tiles in flight
     // keys whose weights are handed over first, so that the product starts
     // while the others' are taken (8192 tokens, 40/8 heads, d = 128: 32 keys
     // 458 us, 64 473, 96 482, in four parts 465; d = 64, 32/8 heads: 64 keys
     // 266 us, 32 280, 96 268)
-    static constexpr int EARLY = D == 128 ? 32 : 64;
+    static constexpr int EARLY = 32;
     static constexpr uint32_t S_COL = 128, O_BASE = 256;  // TMEM columns: S_0, S_1, O_0, O_1
-    static constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, kKeyTile);
+    static constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, KEYS);
     static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D) | (1u << 16);  // V is N-major
 };
 
@@ -111,12 +114,14 @@ struct Job {
 };
 
 constexpr int kJobs = 2;      // items known at a time
-constexpr int kMasked = 4;    // masked value tiles in flight at most: the ring holds no more
+constexpr int kMasked = 8;    // masked value tiles in flight at most: the ring holds no more
+constexpr int kMaxStages = 12, kMaxBufs = 2;
 constexpr int kJobUsers = 11; // warps that read a job: 0-8, 10, 11
 
 struct Shared {
-    uint64_t q_full[2], q_empty[2], kv_full[8], kv_empty[8], v_raw[kMasked], v_half[kMasked];
-    uint64_t s_full[2], p_full[2], p_rest[2], pv_done[2], o_free[2];
+    uint64_t q_full[2], q_empty[2], kv_full[kMaxStages], kv_empty[kMaxStages], v_raw[kMasked], v_half[kMasked];
+    uint64_t s_full[2][kMaxBufs], p_full[2][kMaxBufs], p_rest[2][kMaxBufs], pv_done[2][kMaxBufs];
+    uint64_t o_free[2];
     uint64_t job_full[kJobs], job_empty[kJobs], next_full, drained;
     uint4 next;  // the answer to the request for another block
     Job job[kJobs];
@@ -132,7 +137,7 @@ constexpr uint32_t kStage = 32 * 128;  // bytes a softmax warp's results pass th
 // Shared follow them.
 template <int D>
 constexpr uint32_t smem_bytes() {
-    return (2 + Cfg<D>::STAGES) * Cfg<D>::TILE + 8 * kStage + (uint32_t)sizeof(Shared);
+    return 2 * Cfg<D>::Q_TILE + Cfg<D>::STAGES * Cfg<D>::TILE + 8 * kStage + (uint32_t)sizeof(Shared);
 }
 static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "227 KB per CTA");
 
@@ -263,7 +268,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                const __grid_constant__ CUtensorMap map_v, const AttnArgs a) {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint8_t *sq = smem, *skv = smem + 2 * C::TILE, *sout = skv + C::STAGES * C::TILE;
+    uint8_t *sq = smem, *skv = smem + 2 * C::Q_TILE, *sout = skv + C::STAGES * C::TILE;
     Shared &sh = *reinterpret_cast<Shared *>(sout + 8 * kStage);
     if (smem_u32(smem) & 1023u) {  // the swizzled tiles would not match their descriptors
         *a.status = KDA_ERR_CUDA;
@@ -276,10 +281,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sh.q_full[t], 1);
             mbar_init(&sh.q_empty[t], 1);
-            mbar_init(&sh.s_full[t], 1);
-            mbar_init(&sh.p_full[t], 5);  // four warps of weights, and K and V have arrived
-            mbar_init(&sh.p_rest[t], 4);
-            mbar_init(&sh.pv_done[t], 1);
+            for (int b = 0; b < C::BUFS; ++b) {
+                mbar_init(&sh.s_full[t][b], 1);
+                mbar_init(&sh.p_full[t][b], 5);  // four warps of weights, and K and V have arrived
+                mbar_init(&sh.p_rest[t][b], 4);
+                mbar_init(&sh.pv_done[t][b], 1);
+            }
             mbar_init(&sh.o_free[t], 4);
         }
         for (int i = 0; i < C::STAGES; ++i) {
@@ -342,7 +349,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         regs_inc<208>();
         const int t = warp >> 2, row = tid & 127;
         const uint32_t lane_base = (uint32_t)(warp & 3) * 32;
-        const uint32_t s_addr = tmem_addr(tmem, lane_base, t * C::S_COL);
         const uint32_t o_addr = tmem_addr(tmem, lane_base, C::O_BASE + t * D);
         const int tk = row / a.G;  // the row's token within the tile
         const float c2 = a.scale * kLog2e;
@@ -355,29 +361,28 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             float ref = -INFINITY, sum = 0.f;  // the reference times c2
             bool ok = true;
             for (int32_t j = 0; j < n; ++j) {
-                ok = wait_warp(&sh.s_full[t], it + j);
+                const uint32_t buf = (it + j) % C::BUFS, use = (it + j) / C::BUFS;
+                const uint32_t s_addr =
+                    tmem_addr(tmem, lane_base, t * C::S_COL + buf * C::KEYS);
+                ok = wait_warp(&sh.s_full[t][buf], use);
                 if (!ok) break;
                 tc_fence_after();
-                float s[128];
-                ld32_nowait(s_addr, s);
-                ld32_nowait(s_addr + 32, s + 32);
-                ld32_nowait(s_addr + 64, s + 64);
-                ld32_nowait(s_addr + 96, s + 96);
-                wait_ld32(s);
-                wait_ld32(s + 32);
-                wait_ld32(s + 64);
-                wait_ld32(s + 96);
-                const int32_t seen = tok - j * kKeyTile;  // columns up to this one are seen
-                if ((j + 1) * kKeyTile - 1 > q0) {
+                float s[C::KEYS];
 #pragma unroll
-                    for (int i = 0; i < 128; ++i)
+                for (int i = 0; i < C::KEYS; i += 32) ld32_nowait(s_addr + i, s + i);
+#pragma unroll
+                for (int i = 0; i < C::KEYS; i += 32) wait_ld32(s + i);
+                const int32_t seen = tok - j * C::KEYS;  // columns up to this one are seen
+                if ((j + 1) * C::KEYS - 1 > q0) {
+#pragma unroll
+                    for (int i = 0; i < C::KEYS; ++i)
                         if (i > seen) s[i] = -INFINITY;
                 }
                 float m[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) m[i] = fmaxf(s[i], s[i + 4]);
 #pragma unroll
-                for (int i = 8; i < 128; i += 8)
+                for (int i = 8; i < C::KEYS; i += 8)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) m[e] = max3(m[e], s[i + e], s[i + e + 4]);
                 const float top = fmaxf(max3(m[0], m[1], m[2]), m[3]) * c2;
@@ -394,9 +399,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         ref = next;
                     }
                     __syncwarp();
-                    // rescale the row's outputs: S_j came after the product of
-                    // tile j - 1, so O is at rest
+                    // rescale the row's outputs once the product of tile j - 1
+                    // is done (with one score tile, S_j came after it)
                     if (j > 0) {
+                        if (C::BUFS > 1) {
+                            const uint32_t g = it + j - 1;
+                            ok = wait_warp(&sh.pv_done[t][g % C::BUFS], g / C::BUFS);
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
 #pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
                             float x[16];
@@ -412,7 +423,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 const float2 c22 = make_float2(c2, c2), neg2 = make_float2(neg, neg);
                 float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
+                for (int h = 0; h < C::KEYS / 32; ++h) {
                     uint32_t p[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -425,10 +436,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         p[i] = pack_bf16x2(x.x, x.y);
                     }
                     st16_nowait(s_addr + h * 16, p);
-                    if (h == C::EARLY / 32 - 1 || h == 3) {
+                    if (h == C::EARLY / 32 - 1 || h == C::KEYS / 32 - 1) {
                         tmem_wait_st();
                         tc_fence_before();
-                        arrive_warp(h < 3 ? &sh.p_full[t] : &sh.p_rest[t]);
+                        arrive_warp(h < C::KEYS / 32 - 1 ? &sh.p_full[t][buf] : &sh.p_rest[t][buf]);
                         __syncwarp();
                     }
                 }
@@ -437,9 +448,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             }
             if (!ok) break;
             if (n > 0) {
-                // results (S_n-1 came after the product of tile n - 2, so only
-                // the last product is open)
-                if (!wait_warp(&sh.pv_done[t], it + n - 1)) break;
+                const uint32_t g = it + n - 1;
+                if (!wait_warp(&sh.pv_done[t][g % C::BUFS], g / C::BUFS)) break;
                 tc_fence_after();
                 const float inv = 1.f / sum;
                 const int64_t token = (int64_t)job.begin + tok;
@@ -466,7 +476,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) +
                                                  (int64_t)job.begin * a.v_stride +
                                                  (int64_t)job.kvh * D + c;
-                        for (int32_t k = job.first_mask * kKeyTile; k <= tok; ++k)
+                        for (int32_t k = job.first_mask * C::KEYS; k <= tok; ++k)
 #pragma unroll
                             for (int i = 0; i < N; ++i) {
                                 const float y = __bfloat162float(v[k * a.v_stride + i]);
@@ -541,65 +551,73 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     const int32_t n = job.n, nk[2] = {job.nk[0], job.nk[1]};
                     const int32_t last[2] = {job.q0[0] + job.nt[0] - 1, job.q0[1] + job.nt[1] - 1};
                     if (n == 0) break;
-                    // S_t of key tile j from the ring's `stage`; the last one
-                    // frees the queries
-                    auto scores = [&](int t, int32_t j, uint32_t stage) {
-                        const uint64_t qd = sdesc_sw128(q_base + t * C::TILE);
-                        const uint64_t kd = sdesc_sw128(kv_base + stage * C::TILE);
+                    // S_t of key tile j; the last one frees the queries
+                    auto scores = [&](int t, int32_t j) {
+                        const uint32_t g = it[t] + j, buf = g % C::BUFS;
+                        const uint64_t qd = sdesc_sw128(q_base + t * C::Q_TILE);
+                        const uint64_t kd = sdesc_sw128(kv_base + (e0 + 2 * j) % C::STAGES * C::TILE);
 #pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks) {
-                            const uint32_t step = ((ks >> 2) * C::PANEL + (ks & 3) * 32) >> 4;
-                            mma_half(tmem + t * C::S_COL, qd + step, kd + step, C::IDESC_QK, ks > 0);
-                        }
-                        mma_commit(&sh.s_full[t]);
+                        for (int ks = 0; ks < D / 16; ++ks)
+                            mma_half(tmem + t * C::S_COL + buf * C::KEYS,
+                                     qd + (((ks >> 2) * C::PANEL + (ks & 3) * 32) >> 4),
+                                     kd + (((ks >> 2) * C::KV_PANEL + (ks & 3) * 32) >> 4),
+                                     C::IDESC_QK, ks > 0);
+                        mma_commit(&sh.s_full[t][buf]);
                         if (j == nk[t] - 1) mma_commit(&sh.q_empty[t]);
                     };
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (nk[t] == 0 || !ok) continue;
-                        ok = wait(&sh.q_full[t], used[t]) &&
-                             (t > 0 || wait(&sh.kv_full[e0 % C::STAGES], e0 / C::STAGES));
-                        if (!ok) break;
-                        tc_fence_after();
-                        scores(t, 0, e0 % C::STAGES);
-                    }
-                    if (!ok) break;
-                    mma_commit(&sh.kv_empty[e0 % C::STAGES]);
-                    for (int32_t j = 0; j < n && ok; ++j) {
-                        const uint32_t sv = (e0 + 2 * j + 1) % C::STAGES;
-                        const uint32_t sk = (e0 + 2 * j + 2) % C::STAGES;
-                        const uint64_t vd = sdesc_mn(kv_base + sv * C::TILE, C::PANEL);
+                    for (int j = 0; j < C::BUFS; ++j) {
+                        if (j >= n || !ok) continue;
+                        const uint32_t e = e0 + 2 * j;
+                        ok = wait(&sh.kv_full[e % C::STAGES], e / C::STAGES);
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             if (j >= nk[t] || !ok) continue;
+                            if (j == 0) ok = wait(&sh.q_full[t], used[t]);
+                            if (!ok) break;
+                            tc_fence_after();
+                            scores(t, j);
+                        }
+                        if (ok) mma_commit(&sh.kv_empty[e % C::STAGES]);
+                    }
+                    if (!ok) break;
+                    for (int32_t j = 0; j < n && ok; ++j) {
+                        const uint32_t sv = (e0 + 2 * j + 1) % C::STAGES;
+                        const uint64_t vd = sdesc_mn(kv_base + sv * C::TILE, C::KV_PANEL);
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (j >= nk[t] || !ok) continue;
+                            const uint32_t g = it[t] + j, buf = g % C::BUFS, use = g / C::BUFS;
                             auto product = [&](int ks) {
-                                mma_tmem_a(tmem + C::O_BASE + t * D, tmem + t * C::S_COL + ks * 8,
+                                mma_tmem_a(tmem + C::O_BASE + t * D,
+                                           tmem + t * C::S_COL + buf * C::KEYS + ks * 8,
                                            vd + ks * (2048 >> 4), C::IDESC_PV,
                                            (j > 0 || ks > 0) ? 1u : 0u);
                             };
                             // steps of 16 keys that some row of the tile sees
-                            const int32_t steps = min(8, (last[t] - j * kKeyTile) / 16 + 1);
-                            // the last item's O_t has been read; V_j and K_j+1
-                            // have arrived when the weights have
+                            const int32_t steps = min(C::KEYS / 16, (last[t] - j * C::KEYS) / 16 + 1);
+                            // the last item's O_t has been read; V_j and the
+                            // next scores' K have arrived when the weights have
                             ok = (j > 0 || used[t] == 0 || wait(&sh.o_free[t], used[t] - 1)) &&
-                                 wait(&sh.p_full[t], it[t] + j);
+                                 wait(&sh.p_full[t][buf], use);
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll
                             for (int ks = 0; ks < C::EARLY / 16; ++ks)
                                 if (ks < steps) product(ks);
-                            ok = wait(&sh.p_rest[t], it[t] + j);
+                            ok = wait(&sh.p_rest[t][buf], use);
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll
-                            for (int ks = C::EARLY / 16; ks < kKeyTile / 16; ++ks)
+                            for (int ks = C::EARLY / 16; ks < C::KEYS / 16; ++ks)
                                 if (ks < steps) product(ks);
-                            mma_commit(&sh.pv_done[t]);
-                            if (j + 1 < nk[t]) scores(t, j + 1, sk);
+                            mma_commit(&sh.pv_done[t][buf]);
+                            if (j + C::BUFS < nk[t]) scores(t, j + C::BUFS);
                         }
                         if (!ok) break;
                         mma_commit(&sh.kv_empty[sv]);
-                        if (j + 1 < n) mma_commit(&sh.kv_empty[sk]);
+                        if (j + C::BUFS < n)
+                            mma_commit(&sh.kv_empty[(e0 + 2 * (j + C::BUFS)) % C::STAGES]);
                     }
                     e0 += 2 * n;
 #pragma unroll
@@ -631,11 +649,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     for (int t = 0; t < 2; ++t) {
                         job.q0[t] = (st.tile * 2 + t) * R;
                         job.nt[t] = min(max(job.len - job.q0[t], 0), R);
-                        job.nk[t] = job.nt[t] > 0 ? (job.q0[t] + job.nt[t] - 1) / kKeyTile + 1 : 0;
+                        job.nk[t] = job.nt[t] > 0 ? (job.q0[t] + job.nt[t] - 1) / C::KEYS + 1 : 0;
                         job.n = max(job.n, job.nk[t]);
                     }
                     job.last = min(job.q0[0] + 2 * R, job.len) - 1;
-                    job.first_mask = (job.q0[0] + 1) / kKeyTile;
+                    job.first_mask = (job.q0[0] + 1) / C::KEYS;
                 }
                 if (item >= kJobs) ok = wait_warp(&sh.job_empty[item % kJobs], item / kJobs - 1);
                 if (!ok) break;
@@ -668,7 +686,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         mbar_arrive_expect_tx(&sh.q_full[t], q_bytes);
 #pragma unroll
                         for (int p = 0; p < C::PANELS; ++p)
-                            tma_load_3d(sq + t * C::TILE + p * C::PANEL, &map_q, p * 64,
+                            tma_load_3d(sq + t * C::Q_TILE + p * C::PANEL, &map_q, p * 64,
                                         job.kvh * a.G, job.begin + job.q0[t], &sh.q_full[t]);
                         ++used[t];
                     };
@@ -691,8 +709,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         mbar_arrive_expect_tx(full, C::TILE);
 #pragma unroll
                         for (int p = 0; p < C::PANELS; ++p)
-                            tma_load_3d(skv + s * C::TILE + p * C::PANEL, (i & 1) ? &map_v : &map_k,
-                                        p * 64, job.kvh, job.begin + j * kKeyTile, full);
+                            tma_load_3d(skv + s * C::TILE + p * C::KV_PANEL, (i & 1) ? &map_v : &map_k,
+                                        p * 64, job.kvh, job.begin + j * C::KEYS, full);
                         ++e0;
                         if (i == 0) load_q(1);
                     }
@@ -733,19 +751,19 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 const int32_t nk[2] = {job.nk[0], job.nk[1]};
                 if (n == 0) break;
                 for (int32_t j = warp == 10 ? 0 : first_mask; j < n && ok; ++j) {
-                    const uint32_t ev = e0 + 2 * j + 1, ek = ev + 1, sv = ev % C::STAGES;
+                    const uint32_t ev = e0 + 2 * j + 1, ek = e0 + 2 * (j + C::BUFS), sv = ev % C::STAGES;
                     if (j >= first_mask) {
                         const uint32_t mi = masked % kMasked, mu = masked / kMasked;
                         ++masked;
                         ok = wait_warp(&sh.v_raw[mi], mu);
                         if (!ok) break;
                         // rows the item sees, and those the MMAs read
-                        const int32_t rows = min(kKeyTile, last + 1 - j * kKeyTile);
+                        const int32_t rows = min(C::KEYS, last + 1 - j * C::KEYS);
                         const int32_t read = (rows + 15) & ~15;
                         bool found = false;
 #pragma unroll 1
                         for (int p = 0; p < C::PANELS; ++p) {
-                            uint4 *v = reinterpret_cast<uint4 *>(skv + sv * C::TILE + p * C::PANEL);
+                            uint4 *v = reinterpret_cast<uint4 *>(skv + sv * C::TILE + p * C::KV_PANEL);
                             for (int i = rows * 8 + who; i < read * 8; i += 64)
                                 v[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
@@ -783,16 +801,20 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         __syncwarp();
                     }
                     if (warp == 10) {
-                        // V_j and K_j+1 have arrived: one of the arrivals that
-                        // let the product and the next scores go
+                        // V_j and the next scores' K have arrived: one of the
+                        // arrivals that let the product and those scores go
                         ok = wait_warp(&sh.kv_full[sv], ev / C::STAGES) &&
-                             (j + 1 >= n || wait_warp(&sh.kv_full[ek % C::STAGES], ek / C::STAGES));
+                             (j + C::BUFS >= n ||
+                              wait_warp(&sh.kv_full[ek % C::STAGES], ek / C::STAGES));
                         if (!ok) break;
-                        if (lane < 2 && j < nk[lane]) mbar_arrive(&sh.p_full[lane]);
+                        if (lane < 2 && j < (lane ? nk[1] : nk[0]))
+                            mbar_arrive(&sh.p_full[lane][((lane ? it[1] : it[0]) + j) % C::BUFS]);
                         __syncwarp();
                         // not a phase ahead of the weights
                         for (int t = 0; t < 2 && ok; ++t)
-                            if (j < nk[t]) ok = wait_warp(&sh.p_full[t], it[t] + j);
+                            if (j < nk[t])
+                                ok = wait_warp(&sh.p_full[t][(it[t] + j) % C::BUFS],
+                                               (it[t] + j) / C::BUFS);
                     }
                 }
                 if (!ok) break;
@@ -845,8 +867,8 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t stream) {
     memset(&mk, 0, sizeof(mk));
     memset(&mv, 0, sizeof(mv));
     if (!encode_rows_map(&mq, a.q, D, a.HQ, a.T, a.q_stride, (uint32_t)a.G, (uint32_t)R) ||
-        !encode_rows_map(&mk, a.k, D, a.HKV, a.T, a.k_stride, 1, kKeyTile) ||
-        !encode_rows_map(&mv, a.v, D, a.HKV, a.T, a.v_stride, 1, kKeyTile))
+        !encode_rows_map(&mk, a.k, D, a.HKV, a.T, a.k_stride, 1, Cfg<D>::KEYS) ||
+        !encode_rows_map(&mv, a.v, D, a.HKV, a.T, a.v_stride, 1, Cfg<D>::KEYS))
         return cudaErrorInvalidValue;
     const cudaError_t e = allow_smem<attn_tc_kernel<D>>(smem_bytes<D>());
     if (e != cudaSuccess) return e;
