@@ -9,7 +9,8 @@
 // tensor copy, so that grouped heads share every key and value tile.
 //
 // A CTA owns two such tiles of 128 rows (consecutive tokens) and walks the
-// keys in tiles of 128.  Per row tile t and key tile j:
+// keys in tiles of 128, or of 64 where sequences are short (launch_attn_tc).
+// Per row tile t and key tile j:
 //
 //     S_t = Q_t K_j^T          tcgen05, operands in shared memory, D in TMEM
 //     P_t = 2^{c S_t - ref}    one thread per row; bf16, over S_t's columns
@@ -20,8 +21,10 @@
 // 0 and 1, 8 issues the MMAs, 9 the copies and finds the work, 10-11 make
 // masked values harmless and see to it that tiles have arrived.
 //
-// S_t of key tile j + 1 and the product of tile j use the same columns of TMEM
-// (S over P): one thread issues both, and the tensor core runs them in order.
+// The weights lie over the scores that they came from, and a row tile has 128
+// columns of TMEM for them: one tile of 128 keys, or two of 64.  So the scores
+// of key tile j + 1 (j + 2) go where the weights of tile j are, after their
+// product: one thread issues both, and the tensor core runs them in order.
 //
 // A CTA works on one item (two row tiles of one key-value head) after another:
 // with the last copies of one it takes the grid's next block that has not
@@ -55,8 +58,8 @@
 // 1.73 PFLOP/s of the mask's lower half, 0.90 of a library matrix product's
 // best; the clocks come down with it).  d = 64: the softmax's chain of latencies
 // (8192 tokens, 32/8 heads: 1.04 PFLOP/s).  Short sequences: an item's chain of
-// copy, scores, weights, product and store (1000 x 64 tokens, 32/8 heads: 274
-// us, 4.8 TB/s).
+// copy, scores, weights, product and store (1000 x 64 tokens, 32/8 heads: 202
+// us, 6.5 TB/s).
 #include <cstdint>
 #include <cstring>
 #include <cuda.h>
@@ -82,20 +85,20 @@ constexpr long long kWaitLimit = 2000000000LL;  // SM clocks, about a second
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMoveBy = 8.f;  // powers of two a row's maximum may pass its reference by
 
-template <int D>
+template <int D, int K>
 struct Cfg {
     static constexpr int PANELS = D / 64;                 // 128-byte column panels
     static constexpr uint32_t PANEL = kRowTile * 128;     // bytes
     static constexpr uint32_t Q_TILE = PANELS * PANEL;
     // keys of a tile, and score tiles of a row tile in TMEM
-    static constexpr int KEYS = D == 128 ? 128 : 64, BUFS = D == 128 ? 1 : 2;
+    static constexpr int KEYS = K, BUFS = 128 / K;
     static constexpr uint32_t KV_PANEL = KEYS * 128, TILE = PANELS * KV_PANEL;  // one K or V tile
-    static constexpr int STAGES = D == 128 ? 4 : 12;      // K and V tiles in flight
+    static constexpr int STAGES = D == 128 ? 4 * BUFS : 8 + 4 * (BUFS - 1);  // K and V tiles in flight
     // keys whose weights are handed over first, so that the product starts
     // while the others' are taken (8192 tokens, 40/8 heads, d = 128: 32 keys
     // 458 us, 64 473, 96 482, in four parts 465; d = 64, 32/8 heads: 64 keys
-    // 266 us, 32 280, 96 268)
-    static constexpr int EARLY = 32;
+    // 266 us, 32 280, 96 268).  Tiles of 64 keys go over in one
+    static constexpr int EARLY = K == 128 && D == 128 ? 32 : 64;
     static constexpr uint32_t S_COL = 128, O_BASE = 256;  // TMEM columns: S_0, S_1, O_0, O_1
     static constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, KEYS);
     static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D) | (1u << 16);  // V is N-major
@@ -119,7 +122,8 @@ constexpr int kMaxStages = 12, kMaxBufs = 2;
 constexpr int kJobUsers = 11; // warps that read a job: 0-8, 10, 11
 
 struct Shared {
-    uint64_t q_full[2], q_empty[2], kv_full[kMaxStages], kv_empty[kMaxStages], v_raw[kMasked], v_half[kMasked];
+    uint64_t q_full[2], q_empty[2], kv_full[kMaxStages], kv_empty[kMaxStages];
+    uint64_t v_raw[kMasked], v_half[kMasked];
     uint64_t s_full[2][kMaxBufs], p_full[2][kMaxBufs], p_rest[2][kMaxBufs], pv_done[2][kMaxBufs];
     uint64_t o_free[2];
     uint64_t job_full[kJobs], job_empty[kJobs], next_full, drained;
@@ -135,11 +139,16 @@ constexpr uint32_t kStage = 32 * 128;  // bytes a softmax warp's results pass th
 // The tiles start at the dynamic shared memory's base, which is 1024-byte
 // aligned (the kernel has no other shared memory); the results' bytes and
 // Shared follow them.
-template <int D>
+template <int D, int K>
 constexpr uint32_t smem_bytes() {
-    return 2 * Cfg<D>::Q_TILE + Cfg<D>::STAGES * Cfg<D>::TILE + 8 * kStage + (uint32_t)sizeof(Shared);
+    using C = Cfg<D, K>;
+    static_assert(C::STAGES <= kMaxStages && C::BUFS <= kMaxBufs && C::STAGES / 2 <= kMasked,
+                  "room for the barriers");
+    return 2 * C::Q_TILE + C::STAGES * C::TILE + 8 * kStage + (uint32_t)sizeof(Shared);
 }
-static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "227 KB per CTA");
+static_assert(smem_bytes<128, 128>() <= 232448 && smem_bytes<128, 64>() <= 232448 &&
+                  smem_bytes<64, 128>() <= 232448 && smem_bytes<64, 64>() <= 232448,
+              "227 KB per CTA");
 
 // One lane of a converged warp, in the form whose branch the compiler knows to
 // be one thread's: the MMAs' operands then stay in uniform registers (issued
@@ -262,11 +271,11 @@ __device__ __forceinline__ uint32_t answered_block(const uint4 *from) {
     return got ? x : kNoBlock;
 }
 
-template <int D>
+template <int D, int K>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                const __grid_constant__ CUtensorMap map_v, const AttnArgs a) {
-    using C = Cfg<D>;
+    using C = Cfg<D, K>;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *sq = smem, *skv = smem + 2 * C::Q_TILE, *sout = skv + C::STAGES * C::TILE;
     Shared &sh = *reinterpret_cast<Shared *>(sout + 8 * kStage);
@@ -362,8 +371,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             bool ok = true;
             for (int32_t j = 0; j < n; ++j) {
                 const uint32_t buf = (it + j) % C::BUFS, use = (it + j) / C::BUFS;
-                const uint32_t s_addr =
-                    tmem_addr(tmem, lane_base, t * C::S_COL + buf * C::KEYS);
+                const uint32_t s_addr = tmem_addr(tmem, lane_base, t * C::S_COL + buf * C::KEYS);
                 ok = wait_warp(&sh.s_full[t][buf], use);
                 if (!ok) break;
                 tc_fence_after();
@@ -439,7 +447,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     if (h == C::EARLY / 32 - 1 || h == C::KEYS / 32 - 1) {
                         tmem_wait_st();
                         tc_fence_before();
-                        arrive_warp(h < C::KEYS / 32 - 1 ? &sh.p_full[t][buf] : &sh.p_rest[t][buf]);
+                        arrive_warp(h == C::EARLY / 32 - 1 ? &sh.p_full[t][buf]
+                                                           : &sh.p_rest[t][buf]);
                         __syncwarp();
                     }
                 }
@@ -605,9 +614,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
 #pragma unroll
                             for (int ks = 0; ks < C::EARLY / 16; ++ks)
                                 if (ks < steps) product(ks);
-                            ok = wait(&sh.p_rest[t][buf], use);
-                            if (!ok) break;
-                            tc_fence_after();
+                            if (C::EARLY < C::KEYS) {
+                                ok = wait(&sh.p_rest[t][buf], use);
+                                if (!ok) break;
+                                tc_fence_after();
+                            }
 #pragma unroll
                             for (int ks = C::EARLY / 16; ks < C::KEYS / 16; ++ks)
                                 if (ks < steps) product(ks);
@@ -751,7 +762,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 const int32_t nk[2] = {job.nk[0], job.nk[1]};
                 if (n == 0) break;
                 for (int32_t j = warp == 10 ? 0 : first_mask; j < n && ok; ++j) {
-                    const uint32_t ev = e0 + 2 * j + 1, ek = e0 + 2 * (j + C::BUFS), sv = ev % C::STAGES;
+                    const uint32_t ev = e0 + 2 * j + 1, sv = ev % C::STAGES;
+                    const uint32_t ek = e0 + 2 * (j + C::BUFS);
                     if (j >= first_mask) {
                         const uint32_t mi = masked % kMasked, mu = masked / kMasked;
                         ++masked;
@@ -859,7 +871,7 @@ bool encode_rows_map(CUtensorMap *m, const void *base, int32_t d, int32_t heads,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, int K>
 cudaError_t launch_t(const AttnArgs &a, cudaStream_t stream) {
     const int32_t R = kRowTile / a.G;
     CUtensorMap mq, mk, mv;
@@ -867,20 +879,36 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t stream) {
     memset(&mk, 0, sizeof(mk));
     memset(&mv, 0, sizeof(mv));
     if (!encode_rows_map(&mq, a.q, D, a.HQ, a.T, a.q_stride, (uint32_t)a.G, (uint32_t)R) ||
-        !encode_rows_map(&mk, a.k, D, a.HKV, a.T, a.k_stride, 1, Cfg<D>::KEYS) ||
-        !encode_rows_map(&mv, a.v, D, a.HKV, a.T, a.v_stride, 1, Cfg<D>::KEYS))
+        !encode_rows_map(&mk, a.k, D, a.HKV, a.T, a.k_stride, 1, K) ||
+        !encode_rows_map(&mv, a.v, D, a.HKV, a.T, a.v_stride, 1, K))
         return cudaErrorInvalidValue;
-    const cudaError_t e = allow_smem<attn_tc_kernel<D>>(smem_bytes<D>());
+    const cudaError_t e = allow_smem<attn_tc_kernel<D, K>>(smem_bytes<D, K>());
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)a.T / (2 * R) + a.N;
-    attn_tc_kernel<D><<<(unsigned)(tiles * a.HKV), kThreads, smem_bytes<D>(), stream>>>(mq, mk, mv, a);
+    attn_tc_kernel<D, K>
+        <<<(unsigned)(tiles * a.HKV), kThreads, smem_bytes<D, K>(), stream>>>(mq, mk, mv, a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
+// 128 keys to a tile where rows see many keys: half as many hand-overs between
+// the tensor core and the softmax (16 x 4096 tokens, 32/8 heads: d = 128 1409
+// us, 64 keys 1636; d = 64 1156, 1241).  64 keys, and two score tiles to a row
+// tile, where they see few: less of a tile lies behind the diagonal, and the
+// scores of one tile are taken while the other's softmax runs (1000 x 64
+// tokens, 32/8 heads: d = 128 202 us, 128 keys 243; d = 64 167, 214; 300
+// prompts of 200 tokens on average: 353, 390; 301, 337).  The host knows the
+// mean length alone, so that decides.  At d = 128 and groups of fewer than
+// four, whose tiles are long in tokens, the gain ends at short prompts (32/16
+// heads, 128 of 512 tokens on average: 500 us, 128 keys 496; 600 of 96: 388,
+// 429); a lone prompt has no other work to fill the hand-overs with (400
+// tokens, 32/8 heads, d = 64: 11.1 us, 128 keys 9.9; 100 tokens 7.4, 7.6).
 cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t stream) {
-    return a.D == 64 ? launch_t<64>(a, stream) : launch_t<128>(a, stream);
+    const int64_t few = a.N == 1 ? 128 : a.D == 64 || a.G >= 4 ? 512 : 64;
+    const bool small = a.T <= few * a.N;
+    if (a.D == 64) return small ? launch_t<64, 64>(a, stream) : launch_t<64, 128>(a, stream);
+    return small ? launch_t<128, 64>(a, stream) : launch_t<128, 128>(a, stream);
 }
 
 }  // namespace kda

@@ -289,3 +289,23 @@ def test_tensor_engine_refuses_what_it_lacks():
         kda.kda_attn_fwd(q.half(), k.half(), v.half(), 0.1)
     with pytest.raises(ValueError):
         kda.kda_attn_fwd(q, k[:, :0], v[:, :0], 0.1)
+
+
+@pytest.mark.parametrize("HQ,HKV,d", [(8, 2, 128), (4, 2, 128), (4, 2, 64), (3, 3, 64)])
+@pytest.mark.parametrize("mean", [64, 128, 512])
+@pytest.mark.parametrize("over", [0, 1])
+def test_both_key_tiles(HQ, HKV, d, mean, over):
+    """Tiles of 64 and of 128 keys, on both sides of the lengths at which one
+    gives way to the other, with a prompt much longer than the mean; and
+    with infinite values in the later tokens' odd channels."""
+    for lens in ([mean + over], [mean * 5 - 70 + 5 * over, 0, 0, 70, 0]):
+        T = sum(lens)
+        q, k, v = _qkv(mean + over, T, HQ, HKV, d, "bf16")
+        lse = torch.empty(T, HQ, device="cuda")
+        out, _ = kda.kda_attn_fwd(q, k, v, d ** -0.5, _cu(lens), None, lse)
+        _check_packed(q, k, v, d ** -0.5, lens, out, lse, True)
+        bad = v.clone()
+        bad[T // 2:, :, 1::2] = float("inf")
+        again, _ = kda.kda_attn_fwd(q, k, bad, d ** -0.5, _cu(lens))
+        assert torch.equal(again[:T // 2], out[:T // 2])
+        assert torch.equal(again[..., ::2], out[..., ::2])
