@@ -309,3 +309,20 @@ def test_both_key_tiles(HQ, HKV, d, mean, over):
         again, _ = kda.kda_attn_fwd(q, k, bad, d ** -0.5, _cu(lens))
         assert torch.equal(again[:T // 2], out[:T // 2])
         assert torch.equal(again[..., ::2], out[..., ::2])
+
+
+@pytest.mark.parametrize("lens,HQ,HKV", [([430, 1, 390], 12, 4), ([50, 64, 1] * 70, 2, 1)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+def test_core_engine_with_tiles_for_every_sm(lens, HQ, HKV, dtype, d):
+    """The CUDA-core engine's larger tiles: long and one-tile sequences, and
+    infinite values in the later tokens' odd channels."""
+    T = sum(lens)
+    q, k, v = _qkv(d, T, HQ, HKV, d, dtype)
+    lse = torch.empty(T, HQ, device="cuda")
+    out, _ = kda.kda_attn_fwd(q, k, v, d ** -0.5, _cu(lens), None, lse, engine="simt")
+    _check_packed(q, k, v, d ** -0.5, lens, out, lse, False)
+    v[T // 2:, :, 1::2] = float("inf")
+    again, _ = kda.kda_attn_fwd(q, k, v, d ** -0.5, _cu(lens), engine="simt")
+    assert torch.equal(again[:T // 2], out[:T // 2])
+    assert torch.equal(again[..., ::2], out[..., ::2])
