@@ -21,10 +21,12 @@
 // 0 and 1, 8 issues the MMAs, 9 the copies and finds the work, 10-11 make
 // masked values harmless and see to it that tiles have arrived.
 //
-// The weights lie over the scores that they came from, and a row tile has 128
-// columns of TMEM for them: one tile of 128 keys, or two of 64.  So the scores
-// of key tile j + 1 (j + 2) go where the weights of tile j are, after their
-// product: one thread issues both, and the tensor core runs them in order.
+// The weights lie over the scores that they came from, in one score tile of
+// TMEM.  With 128 keys a row tile has one of its own: the scores of key tile j +
+// 1 go where the weights of tile j are, after their product: one thread issues
+// both, and the tensor core runs them in order.  With 64 keys there are four (d
+// = 64: six), and the units (row tile, key tile) take them in turn, the scores
+// that many units ahead of the products.
 //
 // A CTA works on one item (two row tiles of one key-value head) after another:
 // with the last copies of one it takes the grid's next block that has not
@@ -58,7 +60,7 @@
 // 1.73 PFLOP/s of the mask's lower half, 0.90 of a library matrix product's
 // best; the clocks come down with it).  d = 64: the softmax's chain of latencies
 // (8192 tokens, 32/8 heads: 1.04 PFLOP/s).  Short sequences: an item's chain of
-// copy, scores, weights, product and store (1000 x 64 tokens, 32/8 heads: 202
+// copy, scores, weights, product and store (1000 x 64 tokens, 32/8 heads: 201
 // us, 6.5 TB/s).
 #include <cstdint>
 #include <cstring>
@@ -90,16 +92,30 @@ struct Cfg {
     static constexpr int PANELS = D / 64;                 // 128-byte column panels
     static constexpr uint32_t PANEL = kRowTile * 128;     // bytes
     static constexpr uint32_t Q_TILE = PANELS * PANEL;
-    // keys of a tile, and score tiles of a row tile in TMEM
-    static constexpr int KEYS = K, BUFS = 128 / K;
+    // Keys of a tile.  Score tiles in TMEM: one per row tile, or (RING) what the
+    // outputs leave room for, taken in turn by the units.
+    static constexpr int KEYS = K;
+    static constexpr bool RING = K == 64;
+    static constexpr int SLOTS = RING ? (512 - 2 * D) / K : 2;
+    static constexpr int DEPTH = RING ? SLOTS : 1;  // score tiles that one row tile may have
     static constexpr uint32_t KV_PANEL = KEYS * 128, TILE = PANELS * KV_PANEL;  // one K or V tile
-    static constexpr int STAGES = D == 128 ? 4 * BUFS : 8 + 4 * (BUFS - 1);  // K and V tiles in flight
+    static constexpr int STAGES = D == 128 ? 512 / K : K == 128 ? 8 : 12;  // K and V tiles in flight
+    // Units that the scores run ahead of the products (RING).  Their keys are
+    // at most STAGES / 2 - 1 key tiles ahead, so that at a wait for K_j the tile
+    // before on its barrier is done with, with the products of the tile at hand:
+    // a lone row tile goes a key tile per unit, two go one per two units (and
+    // the second one's last, two at most, one by one).
+    __device__ static constexpr int32_t ahead(int32_t nk1) {
+        return nk1 == 0 ? STAGES / 2 - 1 : SLOTS;
+    }
+    static_assert(!RING || (SLOTS > STAGES / 2 - 1 && (SLOTS + 2) / 2 <= STAGES / 2 - 1),
+                  "a lone row tile, two row tiles");
     // keys whose weights are handed over first, so that the product starts
     // while the others' are taken (8192 tokens, 40/8 heads, d = 128: 32 keys
     // 458 us, 64 473, 96 482, in four parts 465; d = 64, 32/8 heads: 64 keys
     // 266 us, 32 280, 96 268).  Tiles of 64 keys go over in one
     static constexpr int EARLY = K == 128 && D == 128 ? 32 : 64;
-    static constexpr uint32_t S_COL = 128, O_BASE = 256;  // TMEM columns: S_0, S_1, O_0, O_1
+    static constexpr uint32_t O_BASE = SLOTS * KEYS;  // TMEM columns: scores, O_0, O_1
     static constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, KEYS);
     static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D) | (1u << 16);  // V is N-major
 };
@@ -116,16 +132,32 @@ struct Job {
     int32_t first_mask;  // first key tile with a masked place
 };
 
+// The (row tile, key tile) pairs of an item in the order in which they are
+// worked on: (0, 0), (1, 0), (0, 1), ... as far as each row tile goes.  The
+// second goes at least as far as the first, or there is none.
+struct Unit {
+    int32_t t, j;
+};
+__device__ __forceinline__ Unit unit_at(int32_t u, int32_t nk0, int32_t nk1) {
+    if (nk1 == 0) return {0, u};
+    if (u < 2 * nk0) return {u & 1, u >> 1};
+    return {1, u - nk0};
+}
+__device__ __forceinline__ int32_t unit_of(int t, int32_t j, int32_t nk0, int32_t nk1) {
+    if (nk1 == 0) return j;
+    return t == 0 ? 2 * j : j < nk0 ? 2 * j + 1 : nk0 + j;
+}
+
 constexpr int kJobs = 2;      // items known at a time
 constexpr int kMasked = 8;    // masked value tiles in flight at most: the ring holds no more
-constexpr int kMaxStages = 12, kMaxBufs = 2;
+constexpr int kMaxStages = 12, kMaxSlots = 6;
 constexpr int kJobUsers = 11; // warps that read a job: 0-8, 10, 11
 
 struct Shared {
     uint64_t q_full[2], q_empty[2], kv_full[kMaxStages], kv_empty[kMaxStages];
     uint64_t v_raw[kMasked], v_half[kMasked];
-    uint64_t s_full[2][kMaxBufs], p_full[2][kMaxBufs], p_rest[2][kMaxBufs], pv_done[2][kMaxBufs];
-    uint64_t o_free[2];
+    uint64_t s_full[2][kMaxSlots], pv_done[2][kMaxSlots], o_free[2];  // by row tile
+    uint64_t p_full[kMaxSlots], p_rest[kMaxSlots];                    // by score tile
     uint64_t job_full[kJobs], job_empty[kJobs], next_full, drained;
     uint4 next;  // the answer to the request for another block
     Job job[kJobs];
@@ -142,7 +174,7 @@ constexpr uint32_t kStage = 32 * 128;  // bytes a softmax warp's results pass th
 template <int D, int K>
 constexpr uint32_t smem_bytes() {
     using C = Cfg<D, K>;
-    static_assert(C::STAGES <= kMaxStages && C::BUFS <= kMaxBufs && C::STAGES / 2 <= kMasked,
+    static_assert(C::STAGES <= kMaxStages && C::SLOTS <= kMaxSlots && C::STAGES / 2 <= kMasked,
                   "room for the barriers");
     return 2 * C::Q_TILE + C::STAGES * C::TILE + 8 * kStage + (uint32_t)sizeof(Shared);
 }
@@ -290,13 +322,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sh.q_full[t], 1);
             mbar_init(&sh.q_empty[t], 1);
-            for (int b = 0; b < C::BUFS; ++b) {
+            for (int b = 0; b < C::DEPTH; ++b) {
                 mbar_init(&sh.s_full[t][b], 1);
-                mbar_init(&sh.p_full[t][b], 5);  // four warps of weights, and K and V have arrived
-                mbar_init(&sh.p_rest[t][b], 4);
                 mbar_init(&sh.pv_done[t][b], 1);
             }
             mbar_init(&sh.o_free[t], 4);
+        }
+        for (int b = 0; b < C::SLOTS; ++b) {
+            mbar_init(&sh.p_full[b], 5);  // four warps of weights, and K and V have arrived
+            mbar_init(&sh.p_rest[b], 4);
         }
         for (int i = 0; i < C::STAGES; ++i) {
             mbar_init(&sh.kv_full[i], 1);
@@ -361,20 +395,36 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         const uint32_t o_addr = tmem_addr(tmem, lane_base, C::O_BASE + t * D);
         const int tk = row / a.G;  // the row's token within the tile
         const float c2 = a.scale * kLog2e;
-        uint32_t it = 0;  // key tiles of this row tile so far
+        uint32_t it = 0, units = 0;  // key tiles of this row tile, and units, so far
+        // The scores, and the product, of the row tile's x-th key tile are done.
+        // A row tile has barriers of its own for both, since it may be items
+        // ahead of the other one (those without a second row tile), and as many
+        // as scores run ahead: at a wait for x the phase before on its barrier
+        // is done, and the next cannot be.
+        auto scores_done = [&](uint32_t x) -> bool {
+            if (!wait_warp(&sh.s_full[t][x % C::DEPTH], x / C::DEPTH)) return false;
+            tc_fence_after();
+            return true;
+        };
+        auto product_done = [&](uint32_t x) -> bool {
+            if (!wait_warp(&sh.pv_done[t][x % C::DEPTH], x / C::DEPTH)) return false;
+            tc_fence_after();
+            return true;
+        };
         for (uint32_t item = 0;; ++item) {
             const Job &job = sh.job[item % kJobs];
             if (!wait_warp(&sh.job_full[item % kJobs], item / kJobs) || job.n == 0) break;
             const int32_t n = job.nk[t], q0 = job.q0[t], tok = q0 + tk;
+            const int32_t nk0 = job.nk[0], nk1 = job.nk[1];
             const bool mine = tk < job.nt[t];  // the row is a token's
             float ref = -INFINITY, sum = 0.f;  // the reference times c2
             bool ok = true;
             for (int32_t j = 0; j < n; ++j) {
-                const uint32_t buf = (it + j) % C::BUFS, use = (it + j) / C::BUFS;
-                const uint32_t s_addr = tmem_addr(tmem, lane_base, t * C::S_COL + buf * C::KEYS);
-                ok = wait_warp(&sh.s_full[t][buf], use);
+                const uint32_t slot =
+                    C::RING ? (units + unit_of(t, j, nk0, nk1)) % C::SLOTS : (uint32_t)t;
+                const uint32_t s_addr = tmem_addr(tmem, lane_base, slot * C::KEYS);
+                ok = scores_done(it + j);
                 if (!ok) break;
-                tc_fence_after();
                 float s[C::KEYS];
 #pragma unroll
                 for (int i = 0; i < C::KEYS; i += 32) ld32_nowait(s_addr + i, s + i);
@@ -407,15 +457,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         ref = next;
                     }
                     __syncwarp();
-                    // rescale the row's outputs once the product of tile j - 1
-                    // is done (with one score tile, S_j came after it)
+                    // rescale the row's outputs, once the last product is done
+                    // (with one score tile, these scores came after it)
                     if (j > 0) {
-                        if (C::BUFS > 1) {
-                            const uint32_t g = it + j - 1;
-                            ok = wait_warp(&sh.pv_done[t][g % C::BUFS], g / C::BUFS);
-                            if (!ok) break;
-                            tc_fence_after();
-                        }
+                        ok = !C::RING || product_done(it + j - 1);
+                        if (!ok) break;
 #pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
                             float x[16];
@@ -447,8 +493,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     if (h == C::EARLY / 32 - 1 || h == C::KEYS / 32 - 1) {
                         tmem_wait_st();
                         tc_fence_before();
-                        arrive_warp(h == C::EARLY / 32 - 1 ? &sh.p_full[t][buf]
-                                                           : &sh.p_rest[t][buf]);
+                        arrive_warp(h == C::EARLY / 32 - 1 ? &sh.p_full[slot] : &sh.p_rest[slot]);
                         __syncwarp();
                     }
                 }
@@ -457,9 +502,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             }
             if (!ok) break;
             if (n > 0) {
-                const uint32_t g = it + n - 1;
-                if (!wait_warp(&sh.pv_done[t][g % C::BUFS], g / C::BUFS)) break;
-                tc_fence_after();
+                if (!product_done(it + n - 1)) break;
                 const float inv = 1.f / sum;
                 const int64_t token = (int64_t)job.begin + tok;
                 const int64_t head = (int64_t)job.kvh * a.G + (row - tk * a.G);
@@ -543,6 +586,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 }
                 it += n;
             }
+            units += nk0 + nk1;
             arrive_warp(&sh.job_empty[item % kJobs]);
             __syncwarp();
         }
@@ -552,90 +596,120 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             // ---- MMAs ---------------------------------------------------
             if (elect_one()) {
                 const uint32_t q_base = smem_u32(sq), kv_base = smem_u32(skv);
-                uint32_t e0 = 0, it[2] = {0, 0}, used[2] = {0, 0};
+                uint32_t e0 = 0, units = 0, used0 = 0, used1 = 0, it0 = 0, it1 = 0;
                 bool ok = true;
                 for (uint32_t item = 0; ok; ++item) {
                     if (!wait(&sh.job_full[item % kJobs], item / kJobs)) break;
                     const Job &job = sh.job[item % kJobs];
-                    const int32_t n = job.n, nk[2] = {job.nk[0], job.nk[1]};
-                    const int32_t last[2] = {job.q0[0] + job.nt[0] - 1, job.q0[1] + job.nt[1] - 1};
+                    const int32_t n = job.n, nk0 = job.nk[0], nk1 = job.nk[1], nu = nk0 + nk1;
+                    const int32_t last0 = job.q0[0] + job.nt[0] - 1;
+                    const int32_t last1 = job.q0[1] + job.nt[1] - 1;
                     if (n == 0) break;
-                    // S_t of key tile j; the last one frees the queries
-                    auto scores = [&](int t, int32_t j) {
-                        const uint32_t g = it[t] + j, buf = g % C::BUFS;
+                    // S of row tile t and key tile j; the row tile's last one
+                    // frees the queries
+                    auto scores = [&](int t, int32_t j, uint32_t slot) {
                         const uint64_t qd = sdesc_sw128(q_base + t * C::Q_TILE);
                         const uint64_t kd = sdesc_sw128(kv_base + (e0 + 2 * j) % C::STAGES * C::TILE);
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks)
-                            mma_half(tmem + t * C::S_COL + buf * C::KEYS,
+                            mma_half(tmem + slot * C::KEYS,
                                      qd + (((ks >> 2) * C::PANEL + (ks & 3) * 32) >> 4),
                                      kd + (((ks >> 2) * C::KV_PANEL + (ks & 3) * 32) >> 4),
                                      C::IDESC_QK, ks > 0);
-                        mma_commit(&sh.s_full[t][buf]);
-                        if (j == nk[t] - 1) mma_commit(&sh.q_empty[t]);
+                        mma_commit(&sh.s_full[t][((t ? it1 : it0) + j) % C::DEPTH]);
+                        if (j == (t ? nk1 : nk0) - 1) mma_commit(&sh.q_empty[t]);
                     };
-#pragma unroll
-                    for (int j = 0; j < C::BUFS; ++j) {
-                        if (j >= n || !ok) continue;
+                    // its queries and keys have arrived (the item's first ones)
+                    auto arrived = [&](int t, int32_t j) -> bool {
                         const uint32_t e = e0 + 2 * j;
-                        ok = wait(&sh.kv_full[e % C::STAGES], e / C::STAGES);
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            if (j >= nk[t] || !ok) continue;
-                            if (j == 0) ok = wait(&sh.q_full[t], used[t]);
-                            if (!ok) break;
-                            tc_fence_after();
-                            scores(t, j);
-                        }
-                        if (ok) mma_commit(&sh.kv_empty[e % C::STAGES]);
-                    }
-                    if (!ok) break;
-                    for (int32_t j = 0; j < n && ok; ++j) {
+                        ok = wait(&sh.kv_full[e % C::STAGES], e / C::STAGES) &&
+                             (j > 0 || wait(&sh.q_full[t], t ? used1 : used0));
+                        tc_fence_after();
+                        return ok;
+                    };
+                    // O_t (+)= P V_j, from a score tile in its use-th use
+                    auto products = [&](int t, int32_t j, uint32_t slot, uint32_t use) -> bool {
                         const uint32_t sv = (e0 + 2 * j + 1) % C::STAGES;
                         const uint64_t vd = sdesc_mn(kv_base + sv * C::TILE, C::KV_PANEL);
+                        auto product = [&](int ks) {
+                            mma_tmem_a(tmem + C::O_BASE + t * D, tmem + slot * C::KEYS + ks * 8,
+                                       vd + ks * (2048 >> 4), C::IDESC_PV,
+                                       (j > 0 || ks > 0) ? 1u : 0u);
+                        };
+                        // steps of 16 keys that some row of the tile sees
+                        const int32_t steps =
+                            min(C::KEYS / 16, ((t ? last1 : last0) - j * C::KEYS) / 16 + 1);
+                        // the last item's O_t has been read; V_j and the keys
+                        // of the scores to come have arrived when the weights have
+                        const uint32_t before = t ? used1 : used0;
+                        ok = (j > 0 || before == 0 || wait(&sh.o_free[t], before - 1)) &&
+                             wait(&sh.p_full[slot], use);
+                        if (!ok) return false;
+                        tc_fence_after();
 #pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            if (j >= nk[t] || !ok) continue;
-                            const uint32_t g = it[t] + j, buf = g % C::BUFS, use = g / C::BUFS;
-                            auto product = [&](int ks) {
-                                mma_tmem_a(tmem + C::O_BASE + t * D,
-                                           tmem + t * C::S_COL + buf * C::KEYS + ks * 8,
-                                           vd + ks * (2048 >> 4), C::IDESC_PV,
-                                           (j > 0 || ks > 0) ? 1u : 0u);
-                            };
-                            // steps of 16 keys that some row of the tile sees
-                            const int32_t steps = min(C::KEYS / 16, (last[t] - j * C::KEYS) / 16 + 1);
-                            // the last item's O_t has been read; V_j and the
-                            // next scores' K have arrived when the weights have
-                            ok = (j > 0 || used[t] == 0 || wait(&sh.o_free[t], used[t] - 1)) &&
-                                 wait(&sh.p_full[t][buf], use);
-                            if (!ok) break;
+                        for (int ks = 0; ks < C::EARLY / 16; ++ks)
+                            if (ks < steps) product(ks);
+                        if (C::EARLY < C::KEYS) {
+                            ok = wait(&sh.p_rest[slot], use);
+                            if (!ok) return false;
                             tc_fence_after();
-#pragma unroll
-                            for (int ks = 0; ks < C::EARLY / 16; ++ks)
-                                if (ks < steps) product(ks);
-                            if (C::EARLY < C::KEYS) {
-                                ok = wait(&sh.p_rest[t][buf], use);
-                                if (!ok) break;
-                                tc_fence_after();
-                            }
-#pragma unroll
-                            for (int ks = C::EARLY / 16; ks < C::KEYS / 16; ++ks)
-                                if (ks < steps) product(ks);
-                            mma_commit(&sh.pv_done[t][buf]);
-                            if (j + C::BUFS < nk[t]) scores(t, j + C::BUFS);
                         }
-                        if (!ok) break;
-                        mma_commit(&sh.kv_empty[sv]);
-                        if (j + C::BUFS < n)
-                            mma_commit(&sh.kv_empty[(e0 + 2 * (j + C::BUFS)) % C::STAGES]);
-                    }
-                    e0 += 2 * n;
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        it[t] += nk[t];
-                        used[t] += nk[t] > 0;
+                        for (int ks = C::EARLY / 16; ks < C::KEYS / 16; ++ks)
+                            if (ks < steps) product(ks);
+                        mma_commit(&sh.pv_done[t][((t ? it1 : it0) + j) % C::DEPTH]);
+                        return true;
+                    };
+                    if constexpr (C::RING) {
+                        const int32_t ahead = C::ahead(nk1);
+                        auto unit_scores = [&](int32_t u) {
+                            const Unit x = unit_at(u, nk0, nk1);
+                            scores(x.t, x.j, (units + u) % C::SLOTS);
+                            if (x.t == 1 || x.j >= nk1)
+                                mma_commit(&sh.kv_empty[(e0 + 2 * x.j) % C::STAGES]);
+                        };
+                        for (int32_t u = 0; u < min(ahead, nu); ++u) {
+                            const Unit x = unit_at(u, nk0, nk1);
+                            if (!arrived(x.t, x.j)) break;
+                            unit_scores(u);
+                        }
+                        for (int32_t u = 0; u < nu && ok; ++u) {
+                            const Unit x = unit_at(u, nk0, nk1);
+                            const uint32_t g = units + u;
+                            if (!products(x.t, x.j, g % C::SLOTS, g / C::SLOTS)) break;
+                            if (x.t == 1 || x.j >= nk1)
+                                mma_commit(&sh.kv_empty[(e0 + 2 * x.j + 1) % C::STAGES]);
+                            if (u + ahead < nu) unit_scores(u + ahead);
+                        }
+                    } else {
+                        // (row tiles known to the compiler: operands of the
+                        // MMAs stay in uniform registers)
+                        if (!arrived(0, 0)) break;
+                        scores(0, 0, 0);
+                        if (nk1 > 0) {
+                            if (!arrived(1, 0)) break;
+                            scores(1, 0, 1);
+                        }
+                        mma_commit(&sh.kv_empty[e0 % C::STAGES]);
+                        for (int32_t j = 0; j < n && ok; ++j) {
+#pragma unroll
+                            for (int t = 0; t < 2; ++t) {
+                                if (j >= (t ? nk1 : nk0) || !ok) continue;
+                                if (!products(t, j, t, (t ? it1 : it0) + j)) break;
+                                if (j + 1 < (t ? nk1 : nk0)) scores(t, j + 1, t);
+                            }
+                            if (!ok) break;
+                            mma_commit(&sh.kv_empty[(e0 + 2 * j + 1) % C::STAGES]);
+                            if (j + 1 < n) mma_commit(&sh.kv_empty[(e0 + 2 * j + 2) % C::STAGES]);
+                        }
                     }
+                    if (!ok) break;
+                    e0 += 2 * n;
+                    units += nu;
+                    used0 += 1;
+                    used1 += nk1 > 0;
+                    it0 += nk0;
+                    it1 += nk1;
                     mbar_arrive(&sh.job_empty[item % kJobs]);
                 }
             }
@@ -753,17 +827,27 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         } else {
             // ---- masked value tiles, and arrivals ------------------------
             const int who = tid - 10 * 32;  // 0..63
-            uint32_t e0 = 0, masked = 0, it[2] = {0, 0};
+            uint32_t e0 = 0, masked = 0, units = 0, it0 = 0, it1 = 0;
             bool ok = true;
             for (uint32_t item = 0; ok; ++item) {
                 if (!wait_warp(&sh.job_full[item % kJobs], item / kJobs)) break;
                 const Job &job = sh.job[item % kJobs];
                 const int32_t n = job.n, first_mask = job.first_mask, last = job.last;
-                const int32_t nk[2] = {job.nk[0], job.nk[1]};
+                const int32_t nk0 = job.nk[0], nk1 = job.nk[1], nu = nk0 + nk1;
                 if (n == 0) break;
+                // the score tile of (t, j), and its use
+                auto slot_of = [&](int t, int32_t j) -> uint32_t {
+                    return C::RING ? (units + unit_of(t, j, nk0, nk1)) % C::SLOTS : (uint32_t)t;
+                };
+                auto use_of = [&](int t, int32_t j) -> uint32_t {
+                    return C::RING ? (units + unit_of(t, j, nk0, nk1)) / C::SLOTS
+                                   : (t ? it1 : it0) + j;
+                };
+                // from the keys that no wait of the MMAs' thread covers
+                const int32_t ahead = C::ahead(nk1);
+                int32_t next_k = C::RING ? unit_at(min(ahead, nu) - 1, nk0, nk1).j + 1 : 1;
                 for (int32_t j = warp == 10 ? 0 : first_mask; j < n && ok; ++j) {
                     const uint32_t ev = e0 + 2 * j + 1, sv = ev % C::STAGES;
-                    const uint32_t ek = e0 + 2 * (j + C::BUFS);
                     if (j >= first_mask) {
                         const uint32_t mi = masked % kMasked, mu = masked / kMasked;
                         ++masked;
@@ -813,26 +897,34 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         __syncwarp();
                     }
                     if (warp == 10) {
-                        // V_j and the next scores' K have arrived: one of the
-                        // arrivals that let the product and those scores go
-                        ok = wait_warp(&sh.kv_full[sv], ev / C::STAGES) &&
-                             (j + C::BUFS >= n ||
-                              wait_warp(&sh.kv_full[ek % C::STAGES], ek / C::STAGES));
+                        // V_j has arrived, and the keys of the scores that
+                        // follow its products (in time for their barrier: see
+                        // Cfg::ahead): one of the arrivals that let those go
+                        ok = wait_warp(&sh.kv_full[sv], ev / C::STAGES);
+                        int32_t to = min(j + 1, n - 1);
+                        if (C::RING) {
+                            const int32_t u = unit_of(nk1 > j, j, nk0, nk1) + ahead;
+                            to = unit_at(min(u, nu - 1), nk0, nk1).j;
+                        }
+                        for (; next_k <= to && ok; ++next_k) {
+                            const uint32_t ek = e0 + 2 * next_k;
+                            ok = wait_warp(&sh.kv_full[ek % C::STAGES], ek / C::STAGES);
+                        }
                         if (!ok) break;
-                        if (lane < 2 && j < (lane ? nk[1] : nk[0]))
-                            mbar_arrive(&sh.p_full[lane][((lane ? it[1] : it[0]) + j) % C::BUFS]);
+                        if (lane < 2 && j < (lane ? nk1 : nk0))
+                            mbar_arrive(&sh.p_full[slot_of(lane, j)]);
                         __syncwarp();
                         // not a phase ahead of the weights
                         for (int t = 0; t < 2 && ok; ++t)
-                            if (j < nk[t])
-                                ok = wait_warp(&sh.p_full[t][(it[t] + j) % C::BUFS],
-                                               (it[t] + j) / C::BUFS);
+                            if (j < (t ? nk1 : nk0))
+                                ok = wait_warp(&sh.p_full[slot_of(t, j)], use_of(t, j));
                     }
                 }
                 if (!ok) break;
                 e0 += 2 * n;
-                it[0] += nk[0];
-                it[1] += nk[1];
+                units += nu;
+                it0 += nk0;
+                it1 += nk1;
                 arrive_warp(&sh.job_empty[item % kJobs]);
                 __syncwarp();
             }
@@ -893,20 +985,17 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t stream) {
 }  // namespace
 
 // 128 keys to a tile where rows see many keys: half as many hand-overs between
-// the tensor core and the softmax (16 x 4096 tokens, 32/8 heads: d = 128 1409
-// us, 64 keys 1636; d = 64 1156, 1241).  64 keys, and two score tiles to a row
-// tile, where they see few: less of a tile lies behind the diagonal, and the
-// scores of one tile are taken while the other's softmax runs (1000 x 64
-// tokens, 32/8 heads: d = 128 202 us, 128 keys 243; d = 64 167, 214; 300
-// prompts of 200 tokens on average: 353, 390; 301, 337).  The host knows the
-// mean length alone, so that decides.  At d = 128 and groups of fewer than
-// four, whose tiles are long in tokens, the gain ends at short prompts (32/16
-// heads, 128 of 512 tokens on average: 500 us, 128 keys 496; 600 of 96: 388,
-// 429); a lone prompt has no other work to fill the hand-overs with (400
-// tokens, 32/8 heads, d = 64: 11.1 us, 128 keys 9.9; 100 tokens 7.4, 7.6).
+// the tensor core and the softmax (16 x 4096 tokens, 32/8 heads: d = 128 1406
+// us, 64 keys 1752; d = 64 1170, 1421).  64 keys, and a ring of score tiles,
+// where they see few: less of a tile lies behind the diagonal, and scores are
+// taken ahead while the softmax runs (1000 x 64 tokens, 32/8 heads: d = 128 201
+// us, 128 keys 248; d = 64 147, 226; 300 prompts of 200 tokens on average: 308,
+// 393; 266, 333; 100 of 700: 601, 615; 411, 461; with 16/16 heads 399, 385;
+// 338, 343).  The host knows the mean length alone, so that decides.  A lone
+// prompt has no other work to fill the hand-overs with (400 tokens, 32/8 heads:
+// 12.5 us, 128 keys 11.9; 100 tokens 8.7, 9.2).
 cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t stream) {
-    const int64_t few = a.N == 1 ? 128 : a.D == 64 || a.G >= 4 ? 512 : 64;
-    const bool small = a.T <= few * a.N;
+    const bool small = a.T <= (int64_t)(a.N == 1 ? 128 : 512) * a.N;
     if (a.D == 64) return small ? launch_t<64, 64>(a, stream) : launch_t<64, 128>(a, stream);
     return small ? launch_t<128, 64>(a, stream) : launch_t<128, 128>(a, stream);
 }

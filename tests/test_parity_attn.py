@@ -326,3 +326,19 @@ def test_core_engine_with_tiles_for_every_sm(lens, HQ, HKV, dtype, d):
     again, _ = kda.kda_attn_fwd(q, k, v, d ** -0.5, _cu(lens), engine="simt")
     assert torch.equal(again[:T // 2], out[:T // 2])
     assert torch.equal(again[..., ::2], out[..., ::2])
+
+
+@pytest.mark.parametrize("HQ,HKV,d", [(8, 8, 128), (8, 8, 64), (16, 4, 64)])
+@pytest.mark.parametrize("longest", [300, 1400])
+def test_items_of_one_and_two_row_tiles_in_turn(HQ, HKV, d, longest):
+    """Ragged sequences, many items to a CTA: items with one row tile and with
+    two follow one another in every order."""
+    g = torch.Generator().manual_seed(longest + d)
+    lens = torch.randint(1, longest, (60000 // longest,), generator=g).tolist()
+    q, k, v = _qkv(longest, sum(lens), HQ, HKV, d, "bf16")
+    lse = torch.empty(sum(lens), HQ, device="cuda")
+    out, _ = kda.kda_attn_fwd(q, k, v, d ** -0.5, _cu(lens), None, lse)
+    for _ in range(5):
+        assert torch.equal(kda.kda_attn_fwd(q, k, v, d ** -0.5, _cu(lens))[0], out)
+    assert kda.kda_device_status() == 0
+    _check_packed(q, k, v, d ** -0.5, lens, out, lse, True)
