@@ -22,11 +22,13 @@
 // masked values harmless and see to it that tiles have arrived.
 //
 // The weights lie over the scores that they came from, in one score tile of
-// TMEM.  With 128 keys a row tile has one of its own: the scores of key tile j +
-// 1 go where the weights of tile j are, after their product: one thread issues
-// both, and the tensor core runs them in order.  With 64 keys there are four (d
-// = 64: six), and the units (row tile, key tile) take them in turn, the scores
-// that many units ahead of the products.
+// TMEM.  With 128 keys and d = 128 a row tile has one of its own: the scores of
+// key tile j + 1 go where the weights of tile j are, after their product: one
+// thread issues both, and the tensor core runs them in order.  Otherwise there
+// is room for more (64 keys: four, d = 64: six; 128 keys, d = 64: three), and
+// the units (row tile, key tile) take them in turn, the scores that many units
+// ahead of the products.  (Two in turn at d = 128: 4096 tokens, 16 heads, 52 us
+// instead of 50, whose row tiles the compiler knows.)
 //
 // A CTA works on one item (two row tiles of one key-value head) after another:
 // with the last copies of one it takes the grid's next block that has not
@@ -95,7 +97,7 @@ struct Cfg {
     // Keys of a tile.  Score tiles in TMEM: one per row tile, or (RING) what the
     // outputs leave room for, taken in turn by the units.
     static constexpr int KEYS = K;
-    static constexpr bool RING = K == 64;
+    static constexpr bool RING = !(D == 128 && K == 128);
     static constexpr int SLOTS = RING ? (512 - 2 * D) / K : 2;
     static constexpr int DEPTH = RING ? SLOTS : 1;  // score tiles that one row tile may have
     static constexpr uint32_t KV_PANEL = KEYS * 128, TILE = PANELS * KV_PANEL;  // one K or V tile
@@ -106,10 +108,9 @@ struct Cfg {
     // a lone row tile goes a key tile per unit, two go one per two units (and
     // the second one's last, two at most, one by one).
     __device__ static constexpr int32_t ahead(int32_t nk1) {
-        return nk1 == 0 ? STAGES / 2 - 1 : SLOTS;
+        return nk1 == 0 && SLOTS > STAGES / 2 - 1 ? STAGES / 2 - 1 : SLOTS;
     }
-    static_assert(!RING || (SLOTS > STAGES / 2 - 1 && (SLOTS + 2) / 2 <= STAGES / 2 - 1),
-                  "a lone row tile, two row tiles");
+    static_assert(!RING || (SLOTS + 2) / 2 <= STAGES / 2 - 1, "two row tiles");
     // keys whose weights are handed over first, so that the product starts
     // while the others' are taken (8192 tokens, 40/8 heads, d = 128: 32 keys
     // 458 us, 64 473, 96 482, in four parts 465; d = 64, 32/8 heads: 64 keys
