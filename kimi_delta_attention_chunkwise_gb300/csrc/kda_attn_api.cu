@@ -47,7 +47,7 @@ kdaStatus_t check_attn_shape(const kdaAttnShape_t *s) {
     const int32_t d = s->head_dim;
     if (d != 16 && d != 32 && d != 64 && d != 128) return KDA_ERR_UNSUPPORTED;
     if (s->num_heads / s->num_kv_heads > 128) return KDA_ERR_UNSUPPORTED;
-    if (s->num_heads > 65535) return KDA_ERR_UNSUPPORTED;  // heads index grid.y
+    if (s->num_heads > 65535) return KDA_ERR_UNSUPPORTED;  // (documented)
     if ((int64_t)s->total_tokens * s->num_heads > INT32_MAX ||
         (int64_t)s->num_seqs * s->num_heads > INT32_MAX)
         return KDA_ERR_UNSUPPORTED;  // (token, head) counts travel as int32
