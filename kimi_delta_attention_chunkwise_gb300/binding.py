@@ -763,6 +763,20 @@ def make_attn_shape(N, T, HQ, HKV, d, dtype_code, engine=KDA_ENGINE_AUTO, out_f3
                           int(out_f32), int(q_stride), int(k_stride), int(v_stride))
 
 
+_shape_refs = {}  # by the sizes they describe
+
+
+def _shape_ref(*sizes):
+    """A reference to the C description of a call's sizes (make_attn_shape's
+    arguments).  Nothing changes a description, so calls share them."""
+    ref = _shape_refs.get(sizes)
+    if ref is None:
+        if len(_shape_refs) >= 4096:
+            _shape_refs.clear()
+        ref = _shape_refs[sizes] = ctypes.byref(kdaAttnShape_t(*sizes))
+    return ref
+
+
 # Small calls of these are a few microseconds of GPU work, so each function
 # first asks, in one expression that reads every property once, whether all
 # its tensors are what they usually are; _explain() and _token_stride() deal
@@ -786,9 +800,9 @@ def _explain(t, name, dev, dtype, shape=None, contiguous=True):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _lead(t, name):
-    """(device index, dtype, [tokens, heads, d]) of the tensor that fixes a call's."""
-    torch = _torch()
+def _lead(t, name, torch):
+    """(device index, dtype and its code, [tokens, heads, d]) of the tensor
+    that fixes a call's."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     dev = t.get_device()  # -1: a host tensor
@@ -797,7 +811,8 @@ def _lead(t, name):
     size = t.shape
     if len(size) != 3:
         raise ValueError(f"{name} must be [tokens, heads, d]")
-    return dev, t.dtype, size
+    dt = t.dtype
+    return dev, dt, KDA_DTYPE_BF16 if dt is torch.bfloat16 else _dtype_code(t), size
 
 
 def _token_stride(t, name) -> int:
@@ -875,11 +890,10 @@ def _attn_out(q, shape, dev, dt, out, out_f32, torch):
     return out, _whole(out, "out", dev, odt, shape), None, odt is not dt
 
 
-def _attn_launch(where, dev, stream, made, made_too, fn, *args):
+def _attn_launch(where, torch, dev, stream, made, made_too, fn, *args):
     """Calls fn(*args, stream) with the tensors' device current.  On a stream
     other than the current one, the tensors the call made are marked as used
     there, so that their memory outlives the work."""
-    torch = _torch()
     if stream is None:
         s = torch._C._cuda_getCurrentRawStream(dev)
     else:
@@ -912,7 +926,7 @@ def kda_attn_fwd(q, k, v, scale: float, cu_seqlens=None, out=None, lse=None, *, 
     with d = 64 or 128, "simt" is fp32 arithmetic on CUDA cores.
     """
     torch = _torch()
-    dev, dt, size = _lead(q, "q")
+    dev, dt, code, size = _lead(q, "q", torch)
     T, HQ, d = size
     qs = ks = vs = 0
     ksize = getattr(k, "shape", ())
@@ -934,9 +948,9 @@ def kda_attn_fwd(q, k, v, scale: float, cu_seqlens=None, out=None, lse=None, *, 
         lsep = _whole(lse, "lse", dev, torch.float32, (T, HQ))
     out, op, made, f32 = _attn_out(q, size, dev, dt, out, out_f32, torch)
     eng = _ENGINES[engine] if isinstance(engine, str) else int(engine)
-    shape = kdaAttnShape_t(N, T, HQ, HKV, d, _dtype_code(q), eng, f32, qs, ks, vs)
-    _attn_launch("kda_attn_fwd", dev, stream, made, None, load().kda_attn_fwd, q.data_ptr(),
-                 k.data_ptr(), v.data_ptr(), scale, cup, op, lsep, ctypes.byref(shape))
+    shape = _shape_ref(N, T, HQ, HKV, d, code, eng, f32, qs, ks, vs)
+    _attn_launch("kda_attn_fwd", torch, dev, stream, made, None, load().kda_attn_fwd, q.data_ptr(),
+                 k.data_ptr(), v.data_ptr(), scale, cup, op, lsep, shape)
     return out, lse
 
 
@@ -958,7 +972,7 @@ def kda_cache_append(k, v, k_cache, v_cache, block_table, cache_lens, cu_seqlens
     be q); ``k_out`` [T, HKV, d] receives the rotated keys if given (may be k).
     """
     torch = _torch()
-    dev, dt, size = _lead(k, "k")
+    dev, dt, code, size = _lead(k, "k", torch)
     i32 = torch.int32
     T, HKV, d = size
     HQ, qs, ks, vs = HKV, 0, 0, 0
@@ -1002,10 +1016,10 @@ def kda_cache_append(k, v, k_cache, v_cache, block_table, cache_lens, cu_seqlens
             raise ValueError("rope must be [positions, rot_dim]")
         rp = ctypes.byref(kdaRope_t(_whole(rope, "rope", dev, torch.float32, rsize), rsize[0],
                                     rsize[1], bool(rope_interleaved)))
-    shape = kdaAttnShape_t(N, T, HQ, HKV, d, _dtype_code(k), 0, 0, qs, ks, vs)
-    _attn_launch("kda_cache_append", dev, stream, made, None, load().kda_cache_append, qp,
+    shape = _shape_ref(N, T, HQ, HKV, d, code, 0, 0, qs, ks, vs)
+    _attn_launch("kda_cache_append", torch, dev, stream, made, None, load().kda_cache_append, qp,
                  k.data_ptr(), v.data_ptr(), cup, lp, rp, qop, kop, ctypes.byref(cache),
-                 ctypes.byref(shape))
+                 shape)
     return q_out, k_out
 
 
@@ -1034,7 +1048,7 @@ def kda_attn_step(q, k_cache, v_cache, block_table, seq_lens, scale: float, out=
     calls on other streams never share it).
     """
     torch = _torch()
-    dev, dt, size = _lead(q, "q")
+    dev, dt, code, size = _lead(q, "q", torch)
     N, HQ, d = size
     qs = _token_stride(q, "q")
     cache, HKV = _paged_cache(k_cache, v_cache, block_table, dev, dt, torch.int32, N, d)
@@ -1042,8 +1056,7 @@ def kda_attn_step(q, k_cache, v_cache, block_table, seq_lens, scale: float, out=
     lp = _whole(seq_lens, "seq_lens", dev, torch.int32, (N,))
     lsep = None if lse is None else _whole(lse, "lse", dev, torch.float32, (N, HQ))
     out, op, made, f32 = _attn_out(q, size, dev, dt, out, out_f32, torch)
-    code = _dtype_code(q)
-    shape = kdaAttnShape_t(N, N, HQ, HKV, d, code, 0, f32, qs, 0, 0)
+    shape = _shape_ref(N, N, HQ, HKV, d, code, 0, f32, qs, 0, 0)
     wp = left = 0
     made_too = None
     if workspace is None:
@@ -1053,7 +1066,7 @@ def kda_attn_step(q, k_cache, v_cache, block_table, seq_lens, scale: float, out=
             if len(_step_bytes) >= 4096:
                 _step_bytes.clear()
             with torch.cuda.device(dev):
-                need = _step_bytes[key] = kda_attn_step_workspace_size(cache, shape)
+                need = _step_bytes[key] = kda_attn_step_workspace_size(cache, shape._obj)
         if need:
             workspace = made_too = torch.empty(need + 256, dtype=torch.uint8, device=q.device)
     if workspace is not None:
@@ -1061,9 +1074,8 @@ def kda_attn_step(q, k_cache, v_cache, block_table, seq_lens, scale: float, out=
         base = _whole(workspace, "workspace", dev, torch.uint8, (left,))
         wp = (base + 255) // 256 * 256
         left = max(left - (wp - base), 0)
-    _attn_launch("kda_attn_step", dev, stream, made, made_too, load().kda_attn_step_ws,
-                 q.data_ptr(), ctypes.byref(cache), lp, scale, op, lsep, ctypes.byref(shape), wp,
-                 left)
+    _attn_launch("kda_attn_step", torch, dev, stream, made, made_too, load().kda_attn_step_ws,
+                 q.data_ptr(), ctypes.byref(cache), lp, scale, op, lsep, shape, wp, left)
     return out, lse
 
 
