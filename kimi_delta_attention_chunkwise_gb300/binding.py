@@ -875,34 +875,50 @@ def _paged_cache(k_cache, v_cache, block_table, dev, dtype, i32, N, d):
                            size[2], width[1]), size[1]
 
 
-def _attn_out(q, shape, dev, dt, out, out_f32, torch):
-    """(out, its address, freshly made out or None, out_f32 flag)."""
+def _call_stream(stream, dev, torch):
+    """The stream a call was given (a torch stream on the tensors' device, or a
+    raw handle); None where that is the current one."""
+    raw = isinstance(stream, int)
+    if not raw and stream.device_index != dev:
+        raise ValueError(f"stream is on cuda:{stream.device_index}, the call's tensors on "
+                         f"cuda:{dev}")
+    if (stream if raw else stream.cuda_stream) == torch._C._cuda_getCurrentRawStream(dev):
+        return None
+    return torch.cuda.ExternalStream(stream, device=dev) if raw else stream
+
+
+def _empty(shape, dtype, device, stream, torch, returned=True):
+    """A tensor that the call writes, from the pool of the stream that writes
+    it: a block that another stream freed may still be read by work queued
+    there.  What the caller gets is marked as used on the current stream too,
+    so that its block comes back only after that stream's work."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _attn_out(q, shape, dev, dt, out, out_f32, stream, torch):
+    """(out, its address, out_f32 flag)."""
     if out is None:
         f32 = out_f32 and dt is not torch.float32
-        if f32 or not q.is_contiguous():
-            out = torch.empty(shape, dtype=torch.float32 if f32 else dt, device=q.device)
+        if f32 or stream is not None or not q.is_contiguous():
+            out = _empty(shape, torch.float32 if f32 else dt, q.device, stream, torch)
         else:
             out = torch.empty_like(q)
-        return out, out.data_ptr(), out, f32
+        return out, out.data_ptr(), f32
     odt = getattr(out, "dtype", None)
     if odt is not dt and odt is not torch.float32:
         raise TypeError("out must have the dtype of q, or float32")
-    return out, _whole(out, "out", dev, odt, shape), None, odt is not dt
+    return out, _whole(out, "out", dev, odt, shape), odt is not dt
 
 
-def _attn_launch(where, torch, dev, stream, made, made_too, fn, *args):
-    """Calls fn(*args, stream) with the tensors' device current.  On a stream
-    other than the current one, the tensors the call made are marked as used
-    there, so that their memory outlives the work."""
-    if stream is None:
-        s = torch._C._cuda_getCurrentRawStream(dev)
-    else:
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=dev)
-        for t in (made, made_too):
-            if t is not None:
-                t.record_stream(stream)
-        s = stream.cuda_stream
+def _attn_launch(where, torch, dev, stream, fn, *args):
+    """Calls fn(*args, stream) with the tensors' device current."""
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     if torch._C._cuda_getDevice() == dev:
         status = fn(*args, s)
     else:
@@ -946,10 +962,12 @@ def kda_attn_fwd(q, k, v, scale: float, cu_seqlens=None, out=None, lse=None, *, 
         cup = _whole(cu_seqlens, "cu_seqlens", dev, torch.int32, (N + 1,))
     if lse is not None:
         lsep = _whole(lse, "lse", dev, torch.float32, (T, HQ))
-    out, op, made, f32 = _attn_out(q, size, dev, dt, out, out_f32, torch)
+    if stream is not None:
+        stream = _call_stream(stream, dev, torch)
+    out, op, f32 = _attn_out(q, size, dev, dt, out, out_f32, stream, torch)
     eng = _ENGINES[engine] if isinstance(engine, str) else int(engine)
     shape = _shape_ref(N, T, HQ, HKV, d, code, eng, f32, qs, ks, vs)
-    _attn_launch("kda_attn_fwd", torch, dev, stream, made, None, load().kda_attn_fwd, q.data_ptr(),
+    _attn_launch("kda_attn_fwd", torch, dev, stream, load().kda_attn_fwd, q.data_ptr(),
                  k.data_ptr(), v.data_ptr(), scale, cup, op, lsep, shape)
     return out, lse
 
@@ -976,7 +994,9 @@ def kda_cache_append(k, v, k_cache, v_cache, block_table, cache_lens, cu_seqlens
     i32 = torch.int32
     T, HKV, d = size
     HQ, qs, ks, vs = HKV, 0, 0, 0
-    made = qp = qop = kop = cup = rp = None
+    qp = qop = kop = cup = rp = None
+    if stream is not None:
+        stream = _call_stream(stream, dev, torch)
     if not (getattr(v, "shape", None) == size and v.get_device() == dev and v.dtype is dt
             and k.is_contiguous() and v.is_contiguous()):
         _explain(v, "v", dev, dt, size, False)
@@ -993,7 +1013,7 @@ def kda_cache_append(k, v, k_cache, v_cache, block_table, cache_lens, cu_seqlens
         _grouped(HQ, HKV, "k's")
         qp = q.data_ptr()
         if q_out is None:
-            q_out = made = torch.empty(qsize, dtype=dt, device=q.device)
+            q_out = _empty(qsize, dt, q.device, stream, torch)
         qop = _whole(q_out, "q_out", dev, dt, qsize)
     elif q_out is not None:
         raise ValueError("q_out needs q")
@@ -1017,9 +1037,8 @@ def kda_cache_append(k, v, k_cache, v_cache, block_table, cache_lens, cu_seqlens
         rp = ctypes.byref(kdaRope_t(_whole(rope, "rope", dev, torch.float32, rsize), rsize[0],
                                     rsize[1], bool(rope_interleaved)))
     shape = _shape_ref(N, T, HQ, HKV, d, code, 0, 0, qs, ks, vs)
-    _attn_launch("kda_cache_append", torch, dev, stream, made, None, load().kda_cache_append, qp,
-                 k.data_ptr(), v.data_ptr(), cup, lp, rp, qop, kop, ctypes.byref(cache),
-                 shape)
+    _attn_launch("kda_cache_append", torch, dev, stream, load().kda_cache_append, qp, k.data_ptr(),
+                 v.data_ptr(), cup, lp, rp, qop, kop, ctypes.byref(cache), shape)
     return q_out, k_out
 
 
@@ -1044,8 +1063,9 @@ def kda_attn_step(q, k_cache, v_cache, block_table, seq_lens, scale: float, out=
     to attend to (0: a padding row, out = 0).  ``lse``: a [N, HQ] fp32 tensor
     or None.  Scratch: ``workspace``, a uint8 CUDA tensor of at least
     kda_attn_step_workspace_size() + 255 bytes that nothing else uses until
-    the work is done, or a fresh one per call (so that captured graphs and
-    calls on other streams never share it).
+    the work is done, or a fresh one per call from the pool of the stream the
+    call runs on (so that captured graphs and calls on other streams never
+    share it).
     """
     torch = _torch()
     dev, dt, code, size = _lead(q, "q", torch)
@@ -1055,10 +1075,11 @@ def kda_attn_step(q, k_cache, v_cache, block_table, seq_lens, scale: float, out=
     _grouped(HQ, HKV, "the cache's")
     lp = _whole(seq_lens, "seq_lens", dev, torch.int32, (N,))
     lsep = None if lse is None else _whole(lse, "lse", dev, torch.float32, (N, HQ))
-    out, op, made, f32 = _attn_out(q, size, dev, dt, out, out_f32, torch)
+    if stream is not None:
+        stream = _call_stream(stream, dev, torch)
+    out, op, f32 = _attn_out(q, size, dev, dt, out, out_f32, stream, torch)
     shape = _shape_ref(N, N, HQ, HKV, d, code, 0, f32, qs, 0, 0)
     wp = left = 0
-    made_too = None
     if workspace is None:
         key = (dev, code, N, HQ, HKV, d, cache.page_size, cache.max_pages)
         need = _step_bytes.get(key)
@@ -1068,14 +1089,14 @@ def kda_attn_step(q, k_cache, v_cache, block_table, seq_lens, scale: float, out=
             with torch.cuda.device(dev):
                 need = _step_bytes[key] = kda_attn_step_workspace_size(cache, shape._obj)
         if need:
-            workspace = made_too = torch.empty(need + 256, dtype=torch.uint8, device=q.device)
+            workspace = _empty(need + 256, torch.uint8, q.device, stream, torch, returned=False)
     if workspace is not None:
         left = workspace.numel()
         base = _whole(workspace, "workspace", dev, torch.uint8, (left,))
         wp = (base + 255) // 256 * 256
         left = max(left - (wp - base), 0)
-    _attn_launch("kda_attn_step", torch, dev, stream, made, made_too, load().kda_attn_step_ws,
-                 q.data_ptr(), ctypes.byref(cache), lp, scale, op, lsep, shape, wp, left)
+    _attn_launch("kda_attn_step", torch, dev, stream, load().kda_attn_step_ws, q.data_ptr(),
+                 ctypes.byref(cache), lp, scale, op, lsep, shape, wp, left)
     return out, lse
 
 
