@@ -42,7 +42,10 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 __device__ __forceinline__ int32_t clamp_len(const AttnStepArgs &a, int32_t s) {
     return min(max(a.seq_lens[s], 0), a.max_pages << a.page_shift);
 }
-__device__ __forceinline__ int32_t tiles_of(int32_t len) { return (len + kTile - 1) / kTile; }
+// (len + kTile - 1 would overflow in the last tile below 2^31)
+__device__ __forceinline__ int32_t tiles_of(int32_t len) {
+    return len / kTile + (len % kTile != 0);
+}
 
 // Prefix sums of the sequences' tiles, each thread holding a run of sequences.
 template <int THREADS>
@@ -474,14 +477,17 @@ __device__ __forceinline__ void walk_tiles(const AttnStepArgs &a, Core &core, in
     const int warp = threadIdx.x >> 5;
     const int32_t *table = a.block_table + (int64_t)s * a.max_pages;
     // this warp's tokens of tile t: the page's table entry, and the rows
+    // (tiles from tile1 on, whose tokens may pass 2^31, are not asked for)
     auto page_of = [&](int32_t t) -> int32_t {
+        if (t >= tile1) return -1;
         const int32_t tok = t * kTile + warp * kWarpTokens;
-        return t < tile1 && tok < len ? table[tok >> a.page_shift] : -1;
+        return tok < len ? table[tok >> a.page_shift] : -1;
     };
     auto rows_of = [&](int32_t t, int32_t page, int64_t &at) -> int {
-        const int32_t tok = t * kTile + warp * kWarpTokens;
         at = 0;
-        if (t >= tile1 || tok >= len) return 0;
+        if (t >= tile1) return 0;
+        const int32_t tok = t * kTile + warp * kWarpTokens;
+        if (tok >= len) return 0;
         if (page < 0 || page >= a.num_pages) {
             *a.status = KDA_ERR_INVALID_ARG;
             return 0;

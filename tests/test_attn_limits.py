@@ -1,0 +1,64 @@
+"""The full-attention layer at the ends of the sizes it accepts."""
+import pytest
+import torch
+
+import kimi_delta_attention_chunkwise_gb300 as kda
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+TOP = 1 << 31
+
+
+@pytest.fixture
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from kimi_delta_attention_chunkwise_gb300 import build
+    build.build()
+    torch.cuda.empty_cache()
+
+
+def _randn(seed, *shape, dtype):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(DT[dtype])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("f32", 16)])
+@pytest.mark.parametrize("length", [TOP - 65, TOP - 63, TOP - 32])
+def test_step_lengths_up_to_2_31(gpu, dtype, d, length):
+    """A table of 2^31 - 32 tokens whose entries name one page of 32 over and
+    over, beside a sequence of 70 tokens.  A row's weight is its number of
+    occurrences times its exponential.
+
+    Bound: the accumulators of the sums and of the outputs take at most two
+    additions per tile of 64 tokens, with a whole step of fp32 (2^-23) each, and
+    a CTA has its share of the tiles (plus the joins', far fewer than a tenth).
+    Weights of bf16 values are rounded by 2^-8 at most, and so is the output."""
+    page, width = 32, TOP // 32 - 1
+    k, v = (_randn(i, 1, 1, page, d, dtype=dtype) for i in (1, 2))
+    v += 1   # (means that are not near zero)
+    q = _randn(3, 2, 1, d, dtype=dtype)
+    table = torch.zeros(2, width, dtype=torch.int32, device="cuda")
+    lens = [length, 70]
+    lse = torch.full((2, 1), float("nan"), device="cuda")
+    out = torch.full((2, 1, d), float("nan"), dtype=DT[dtype], device="cuda")
+    scale = d ** -0.5
+    kda.kda_attn_step(q.cuda(), k.cuda(), v.cuda(), table,
+                      torch.tensor(lens, dtype=torch.int32, device="cuda"), scale, out, lse)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    additions = 2.2 * (length / 64 / sms + 1)
+    for s, n in enumerate(lens):
+        count = n // page + (torch.arange(page) < n % page)
+        z = scale * (k[0, 0].double() @ q[s, 0].double())
+        w = count * torch.exp(z - z.max())
+        want = (w @ v[0, 0].double()) / w.sum()
+        size = (w @ v[0, 0].double().abs()) / w.sum()
+        rel = additions * 2.0 ** -23 + 1e-4
+        assert abs(lse[s, 0].item() - (z.max() + w.sum().log()).item()) <= rel + 1e-5
+        assert ((out[s, 0].cpu().double() - want).abs() <= (2 * rel + 2.0 ** -7) * size).all()
+    # the last row of the table, too, takes a new token
+    if length == TOP - 32:
+        kc, vc = torch.zeros(1, 1, page, d, dtype=DT[dtype], device="cuda"), v.cuda()
+        new = _randn(4, 2, 1, d, dtype=dtype).cuda()
+        kda.kda_cache_append(new, new, kc, vc, table,
+                             torch.tensor([length - 1, 3], dtype=torch.int32, device="cuda"))
+        assert torch.equal(kc[0, 0, 31], new[0, 0]) and torch.equal(kc[0, 0, 3], new[1, 0])
