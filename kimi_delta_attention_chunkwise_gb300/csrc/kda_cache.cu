@@ -233,7 +233,7 @@ cudaError_t launch_t(const AppendArgs &a, cudaStream_t stream) {
     if (a.T <= kFewTokens) {
         cache_append_kernel<T, D, 1, 256><<<(unsigned)a.T, 256, 0, stream>>>(a);
     } else {
-        cache_append_kernel<T, D, 2, 128><<<(unsigned)((a.T + 1) / 2), 128, 0, stream>>>(a);
+        cache_append_kernel<T, D, 2, 128><<<(unsigned)(a.T / 2 + a.T % 2), 128, 0, stream>>>(a);
     }
     return cudaGetLastError();
 }

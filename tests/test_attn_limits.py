@@ -62,3 +62,27 @@ def test_step_lengths_up_to_2_31(gpu, dtype, d, length):
         kda.kda_cache_append(new, new, kc, vc, table,
                              torch.tensor([length - 1, 3], dtype=torch.int32, device="cuda"))
         assert torch.equal(kc[0, 0, 31], new[0, 0]) and torch.equal(kc[0, 0, 3], new[1, 0])
+
+
+@pytest.mark.gpu
+def test_append_of_2_31_less_one_tokens(gpu):
+    """The largest token count: all but the first and the last few rows lie
+    outside every sequence.  (64 GB of keys, which are the values too.)"""
+    T, d, page = TOP - 1, 16, 16
+    if torch.cuda.mem_get_info()[0] < 3 * T * d:
+        pytest.skip("not enough free memory")
+    x = torch.empty(T, 1, d, dtype=torch.bfloat16, device="cuda")
+    rows = _randn(1, 6, 1, d, dtype="bf16").cuda()
+    x[:3], x[T - 3:] = rows[:3], rows[3:]
+    kc = torch.zeros(2, 1, page, d, dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    table = torch.tensor([[0], [1]], dtype=torch.int32, device="cuda")
+    for cu, page_of in (((0, 3, 3), 0), ((T - 3, T - 3, T), 1)):
+        want = torch.zeros_like(kc)
+        want[page_of, 0, 5:8] = rows[:3, 0] if page_of == 0 else rows[3:, 0]
+        kc.zero_(), vc.zero_()
+        kda.kda_cache_append(x, x, kc, vc, table, i32(5, 5), i32(*cu))
+        assert torch.equal(kc, want) and torch.equal(vc, want)
+    del x
+    torch.cuda.empty_cache()
