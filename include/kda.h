@@ -560,7 +560,7 @@ kdaStatus_t kda_chunk_bwd_ws(const void *q, const void *k, const void *v,
  * ---------------------------------------------------------------------------
  */
 typedef struct {
-    int32_t num_seqs;      /* N >= 1 */
+    int32_t num_seqs;      /* N >= 1, at most 2^30 */
     int32_t total_tokens;  /* T >= 0: rows of q, k, v; must equal N (step) */
     int32_t num_heads;     /* HQ >= 1: query heads */
     int32_t num_kv_heads;  /* HKV >= 1, divides HQ; HQ / HKV <= 128 */

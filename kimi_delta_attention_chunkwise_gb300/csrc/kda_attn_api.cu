@@ -48,6 +48,8 @@ kdaStatus_t check_attn_shape(const kdaAttnShape_t *s) {
     if (d != 16 && d != 32 && d != 64 && d != 128) return KDA_ERR_UNSUPPORTED;
     if (s->num_heads / s->num_kv_heads > 128) return KDA_ERR_UNSUPPORTED;
     if (s->num_heads > 65535) return KDA_ERR_UNSUPPORTED;  // (documented)
+    // (the kernels' walks over the sequences add up to N + 1 to an index in int32)
+    if (s->num_seqs > (1 << 30)) return KDA_ERR_UNSUPPORTED;
     if ((int64_t)s->total_tokens * s->num_heads > INT32_MAX ||
         (int64_t)s->num_seqs * s->num_heads > INT32_MAX)
         return KDA_ERR_UNSUPPORTED;  // (token, head) counts travel as int32

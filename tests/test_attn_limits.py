@@ -1,4 +1,6 @@
 """The full-attention layer at the ends of the sizes it accepts."""
+import ctypes
+
 import pytest
 import torch
 
@@ -15,6 +17,25 @@ def gpu():
     from kimi_delta_attention_chunkwise_gb300 import build
     build.build()
     torch.cuda.empty_cache()
+
+
+def test_more_than_2_30_sequences_are_refused():
+    """The kernels find a token's sequence, and the sequences' tiles, with sums
+    of two sequence indices in 32 bits."""
+    from kimi_delta_attention_chunkwise_gb300 import binding, build
+    build.build()
+    lib, fake, other = binding.load(), 0x10000, 0x20000   # never dereferenced
+    cache = kda.kdaPagedCache_t(fake, fake, fake, 4, 16, 2)
+    n = ctypes.c_size_t(0)
+    for N, T, code in (((1 << 30) + 1, 9, kda.KDA_ERR_UNSUPPORTED),
+                       (TOP - 1, 9, kda.KDA_ERR_UNSUPPORTED), (1 << 30, 0, kda.KDA_SUCCESS)):
+        s = ctypes.byref(kda.make_attn_shape(N, T, 1, 1, 64, kda.KDA_DTYPE_BF16))
+        assert lib.kda_attn_fwd(fake, fake, fake, 0.1, fake, other, None, s, None) == code
+        assert lib.kda_cache_append(None, fake, fake, fake, fake, None, None, None,
+                                    ctypes.byref(cache), s, None) == code
+    s = ctypes.byref(kda.make_attn_shape((1 << 30) + 1, (1 << 30) + 1, 1, 1, 64, kda.KDA_DTYPE_BF16))
+    assert lib.kda_attn_step_workspace_size(ctypes.byref(cache), s, ctypes.byref(n)) == \
+        kda.KDA_ERR_UNSUPPORTED
 
 
 def _randn(seed, *shape, dtype):
