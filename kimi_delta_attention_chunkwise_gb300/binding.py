@@ -759,8 +759,18 @@ def make_attn_shape(N, T, HQ, HKV, d, dtype_code, engine=KDA_ENGINE_AUTO, out_f3
                     k_stride=0, v_stride=0) -> kdaAttnShape_t:
     """HQ / HKV: query / key-value heads; strides: elements from one token's
     row to the next (0: contiguous)."""
+    _fit_i32(N, T, HQ, HKV, d)
     return kdaAttnShape_t(int(N), int(T), int(HQ), int(HKV), int(d), int(dtype_code), int(engine),
                           int(out_f32), int(q_stride), int(k_stride), int(v_stride))
+
+
+_I32_MAX = (1 << 31) - 1
+
+
+def _fit_i32(*sizes):
+    """Sizes travel to C in 32 bits; ctypes would cut them off silently."""
+    if max(sizes) > _I32_MAX:
+        raise ValueError(f"sizes beyond 2^31 - 1 are not supported: {max(sizes)}")
 
 
 _shape_refs = {}  # by the sizes they describe
@@ -771,6 +781,7 @@ def _shape_ref(*sizes):
     arguments).  Nothing changes a description, so calls share them."""
     ref = _shape_refs.get(sizes)
     if ref is None:
+        _fit_i32(*sizes[:5])
         if len(_shape_refs) >= 4096:
             _shape_refs.clear()
         ref = _shape_refs[sizes] = ctypes.byref(kdaAttnShape_t(*sizes))
@@ -871,6 +882,8 @@ def _paged_cache(k_cache, v_cache, block_table, dev, dtype, i32, N, d):
             _cache_shape(k_cache, v_cache, block_table, dev, dtype, i32, N, d)
     except AttributeError:
         _cache_shape(k_cache, v_cache, block_table, dev, dtype, i32, N, d)
+    if size[0] > _I32_MAX or width[1] > _I32_MAX:
+        _fit_i32(size[0], width[1])
     return kdaPagedCache_t(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), size[0],
                            size[2], width[1]), size[1]
 
@@ -1034,6 +1047,8 @@ def kda_cache_append(k, v, k_cache, v_cache, block_table, cache_lens, cu_seqlens
         rsize = rope.shape
         if len(rsize) != 2:
             raise ValueError("rope must be [positions, rot_dim]")
+        if rsize[0] > _I32_MAX:
+            _fit_i32(rsize[0])
         rp = ctypes.byref(kdaRope_t(_whole(rope, "rope", dev, torch.float32, rsize), rsize[0],
                                     rsize[1], bool(rope_interleaved)))
     shape = _shape_ref(N, T, HQ, HKV, d, code, 0, 0, qs, ks, vs)

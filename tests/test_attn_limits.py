@@ -38,6 +38,25 @@ def test_more_than_2_30_sequences_are_refused():
         kda.KDA_ERR_UNSUPPORTED
 
 
+def test_sizes_past_32_bits_are_refused_not_cut_off():
+    """2^32 + 5 of anything would arrive as 5."""
+    from kimi_delta_attention_chunkwise_gb300 import binding
+    many = (1 << 32) + 5
+    for i in range(5):
+        sizes = [1, 1, 1, 1, 64]
+        sizes[i] = many
+        with pytest.raises(ValueError, match="2\\^31"):
+            kda.make_attn_shape(*sizes, kda.KDA_DTYPE_BF16)
+        with pytest.raises(ValueError, match="2\\^31"):
+            binding._shape_ref(*sizes, kda.KDA_DTYPE_BF16, 0, 0, 0, 0, 0)
+    meta = lambda *s, dt=torch.bfloat16: torch.empty(s, dtype=dt, device="meta")   # device -1
+    for pages, width in ((4, many), (many, 4)):
+        cache = meta(pages, 1, 16, 16)
+        with pytest.raises(ValueError, match="2\\^31"):
+            binding._paged_cache(cache, cache, meta(1, width, dt=torch.int32), -1, torch.bfloat16,
+                                 torch.int32, 1, 16)
+
+
 def _randn(seed, *shape, dtype):
     return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(DT[dtype])
 
