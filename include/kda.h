@@ -664,7 +664,8 @@ kdaStatus_t kda_cache_append(const void *q, const void *k, const void *v,
  *
  *   q         [N, HQ, d] dtype (token stride q_stride; k_stride, v_stride ignored)
  *   seq_lens  [N] int32 device.  A length <= 0 is a sequence without keys:
- *             out = 0, lse = -inf (rows that pad a batch).
+ *             out = 0, lse = -inf (rows that pad a batch).  (A row whose keys all
+ *             score -inf is the formula's: out NaN, lse = -inf, as in kda_attn_fwd.)
  *   out       [N, HQ, d] dtype (float32 if shape->out_f32)
  *   lse       [N, HQ] float32 or NULL
  *

@@ -17,6 +17,7 @@
 // them) and keeps its own running state, so the main loop has no barrier; the
 // warps' states are joined when the CTA leaves an item.
 #include <algorithm>
+#include <cfloat>
 #include <cstdint>
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -113,6 +114,14 @@ __device__ __forceinline__ int64_t share_start(int64_t units, int32_t c, int32_t
 // The CTAs that work: no share is empty.
 __device__ __forceinline__ int32_t workers(int64_t units, int32_t grid) {
     return (int32_t)min((int64_t)grid, units);
+}
+
+// A state's maximum as the joins take it.  -inf says that no key was seen; a
+// state that saw keys whose scores are all -inf keeps its sum of 0 with the
+// lowest finite number, so that the row comes out as the definition's 0 / 0 if
+// no other state has more.
+__device__ __forceinline__ float state_max(float m, bool seen) {
+    return seen ? fmaxf(m, -FLT_MAX) : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------
@@ -236,7 +245,7 @@ struct SimtCore {
         }
     }
     // the warp's state: weighted sums [kRows][D], maxima (base 2) and sums [kRows]
-    __device__ void finish(float *sacc, float *sm, float *sl) {
+    __device__ void finish(float *sacc, float *sm, float *sl, bool seen) {
         const int lane = threadIdx.x & 31, cl = lane % LPT, sub = lane / LPT;
 #pragma unroll
         for (int h = 0; h < kRows; ++h) {
@@ -255,7 +264,7 @@ struct SimtCore {
                 if (sub == 0) sacc[h * D + cl * 8 + j] = x;
             }
             if (lane == 0) {
-                sm[h] = mx * c2;
+                sm[h] = state_max(mx * c2, seen);
                 sl[h] = sum;
             }
         }
@@ -434,7 +443,7 @@ struct MmaCore {
                 mma_16816(o[i][n], a[0], a[1], a[2], a[3], p[n][0], p[n][1]);
         }
     }
-    __device__ void finish(float *sacc, float *sm, float *sl) {
+    __device__ void finish(float *sacc, float *sm, float *sl, bool seen) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -444,7 +453,7 @@ struct MmaCore {
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
                 if (g == 0) {
-                    sm[n * 8 + 2 * t + e] = ref[n][e];
+                    sm[n * 8 + 2 * t + e] = state_max(ref[n][e], seen);
                     sl[n * 8 + 2 * t + e] = l;
                 }
             }
@@ -468,9 +477,10 @@ __device__ __forceinline__ void store_out(const AttnStepArgs &a, int64_t i, floa
     else static_cast<__nv_bfloat16 *>(a.out)[i] = __float2bfloat16_rn(y);
 }
 
-// One item's tiles tile0 .. tile1 - 1 into the warp's state.
+// One item's tiles tile0 .. tile1 - 1 into the warp's state; false if there was
+// no key in them for the warp.
 template <class Core>
-__device__ __forceinline__ void walk_tiles(const AttnStepArgs &a, Core &core, int32_t s,
+__device__ __forceinline__ bool walk_tiles(const AttnStepArgs &a, Core &core, int32_t s,
                                            int32_t kvh, int32_t len, int32_t tile0, int32_t tile1) {
     using T = typename Core::Type;
     constexpr int D = Core::kD;
@@ -497,6 +507,7 @@ __device__ __forceinline__ void walk_tiles(const AttnStepArgs &a, Core &core, in
         return min(kWarpTokens, len - tok);
     };
     const T *kc = static_cast<const T *>(a.k_cache), *vc = static_cast<const T *>(a.v_cache);
+    bool seen = false;
     if constexpr (Core::kAhead) {
         // the next tile's keys are on their way while this one's weights and
         // values are worked on, its values while the next scores are, and its
@@ -512,6 +523,7 @@ __device__ __forceinline__ void walk_tiles(const AttnStepArgs &a, Core &core, in
             core.scores();
             core.load_k(kc + next_at, next_n);
             if (n > 0) core.values(n);
+            seen = seen || n > 0;
             core.load_v(vc + next_at, next_n);
             n = next_n;
         }
@@ -522,8 +534,10 @@ __device__ __forceinline__ void walk_tiles(const AttnStepArgs &a, Core &core, in
             const int n = rows_of(t, next_page, at);
             next_page = page_of(t + 1);
             if (n > 0) core.tile(kc + at, vc + at, n);
+            seen = seen || n > 0;
         }
     }
+    return seen;
 }
 
 // The four warps' states, joined.
@@ -546,10 +560,11 @@ struct Joined {
     }
 };
 
+// (mx = -inf: no keys)
 __device__ __forceinline__ void store_row(const AttnStepArgs &a, int64_t head, int D, int col,
                                           float o, float mx, float sum) {
-    store_out(a, head * D + col, sum == 0.f ? 0.f : o / sum);
-    if (a.lse && col == 0) a.lse[head] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+    store_out(a, head * D + col, mx == -INFINITY ? 0.f : o / sum);
+    if (a.lse && col == 0) a.lse[head] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
 template <class Core>
@@ -572,7 +587,7 @@ attn_step_kernel(const AttnStepArgs a, float *part) {
     for (int32_t s = c; s < a.N; s += gridDim.x) {
         if (clamp_len(a, s) > 0) continue;
         for (int32_t i = tid; i < a.HQ * D; i += kThreads)
-            store_row(a, (int64_t)s * a.HQ + i / D, D, i % D, 0.f, 0.f, 0.f);
+            store_row(a, (int64_t)s * a.HQ + i / D, D, i % D, 0.f, -INFINITY, 0.f);
     }
     if (c >= grid) return;
     const int64_t u0 = share_start(units, c, grid), u1 = share_start(units, c + 1, grid);
@@ -594,8 +609,8 @@ attn_step_kernel(const AttnStepArgs a, float *part) {
         const int32_t rows = min(R, a.G - h0);
         const int64_t head = (int64_t)kvh * a.G + h0;
         core.init(static_cast<const T *>(a.q) + s * a.q_stride + head * D, rows, a.scale);
-        walk_tiles(a, core, s, kvh, len, tile0, tile1);
-        core.finish(state.acc[warp], state.m[warp], state.l[warp]);
+        const bool seen = walk_tiles(a, core, s, kvh, len, tile0, tile1);
+        core.finish(state.acc[warp], state.m[warp], state.l[warp], seen);
         __syncthreads();
         const bool whole = tile0 == 0 && tile1 == tiles;
         float *slot = part + ((int64_t)c * 2 + (u == u0 ? 0 : 1)) * (R * (D + 2));
@@ -643,9 +658,9 @@ attn_step_direct_kernel(const AttnStepArgs a) {
     core.init(static_cast<const T *>(a.q) + s * a.q_stride + head * D, rows, a.scale);
     const int32_t len = clamp_len(a, s), tiles = tiles_of(len);
     if (tid == 0 && a.seq_lens[s] > (a.max_pages << a.page_shift)) *a.status = KDA_ERR_INVALID_ARG;
-    walk_tiles(a, core, s, kvh, len, (int32_t)((int64_t)tiles * rank / ctas),
-               (int32_t)((int64_t)tiles * (rank + 1) / ctas));
-    core.finish(state.acc[warp], state.m[warp], state.l[warp]);
+    const bool seen = walk_tiles(a, core, s, kvh, len, (int32_t)((int64_t)tiles * rank / ctas),
+                                 (int32_t)((int64_t)tiles * (rank + 1) / ctas));
+    core.finish(state.acc[warp], state.m[warp], state.l[warp], seen);
     __syncthreads();
     if (ctas == 1) {
         for (int i = tid; i < rows * D; i += kThreads) {

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import kimi_delta_attention_chunkwise_gb300 as kda
+from attn_testutil import check, reference
 
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
 TOP = 1 << 31
@@ -126,3 +127,66 @@ def test_append_of_2_31_less_one_tokens(gpu):
         assert torch.equal(kc, want) and torch.equal(vc, want)
     del x
     torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d,HQ,HKV", [("bf16", 128, 8, 2), ("bf16", 64, 12, 1), ("bf16", 32, 4, 2),
+                                            ("f32", 64, 6, 2), ("f32", 128, 2, 2)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_step_scores_of_minus_infinity(gpu, dtype, d, HQ, HKV, wide):
+    """Keys whose scores are -inf weigh nothing; a sequence that has no others
+    gives the formula's 0 / 0 and ln 0 = -inf, as the prompt attention does.  Out
+    = 0 is for sequences without keys."""
+    page, pages = 64, 48
+    lens = [900, 900, 900, 70, 1, 0, 900]
+    dead = [900, 0, 700, 70, 1, 0, 899]     # the first so many tokens score -inf
+    N = len(lens)
+    q = _randn(1, N, HQ, d, dtype=dtype)
+    q[..., 0] = 1
+    ks, vs = ([_randn(10 * s + i, n, HKV, d, dtype=dtype) for s, n in enumerate(lens)] for i in (2, 3))
+    kc, vc = (torch.zeros(N * 15, HKV, page, d, dtype=DT[dtype]) for _ in range(2))
+    table = torch.full((N, 16384 if wide else 15), -1, dtype=torch.int32)
+    for s, n in enumerate(lens):
+        ks[s][:dead[s], :, 0] = -float("inf")
+        table[s, :15] = torch.arange(15) + 15 * s
+        for c, x in ((kc, ks[s]), (vc, vs[s])):
+            rows = torch.zeros(15 * page, HKV, d, dtype=DT[dtype])
+            rows[:n] = x
+            c[15 * s:15 * s + 15] = rows.view(15, page, HKV, d).transpose(1, 2)
+    lse = torch.zeros(N, HQ, device="cuda")
+    out, _ = kda.kda_attn_step(q.cuda(), kc.cuda(), vc.cuda(), table.cuda(),
+                               torch.tensor(lens, dtype=torch.int32, device="cuda"), 0.1, None, lse)
+    for s, n in enumerate(lens):
+        if n == 0:
+            assert (out[s] == 0).all() and (lse[s] == -float("inf")).all()
+        elif dead[s] == n:
+            assert torch.isnan(out[s]).all() and (lse[s] == -float("inf")).all()
+        else:
+            left = n - dead[s]
+            check(out[s:s + 1], lse[s:s + 1], reference(q[s:s + 1], ks[s][dead[s]:], vs[s][dead[s]:],
+                                                        0.1, left - 1), n, d, dtype == "bf16" and d >= 64)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,engine,d", [("bf16", "auto", 128), ("bf16", "auto", 64),
+                                            ("bf16", "simt", 64), ("f32", "auto", 64)])
+@pytest.mark.parametrize("lens", [[400], [130, 60] + [40] * 20])
+def test_prompt_scores_of_minus_infinity(gpu, dtype, engine, d, lens):
+    """The same in prompts: a sequence's first tokens see nothing but -inf."""
+    HQ, HKV, T = 4, 2, sum(lens)
+    q, k, v = (_randn(i, T, h, d, dtype=dtype) for i, h in ((1, HQ), (2, HKV), (3, HKV)))
+    q[..., 0] = 1
+    cu = [0]
+    for n in lens:
+        k[cu[-1]:cu[-1] + n // 2, :, 0] = -float("inf")
+        cu.append(cu[-1] + n)
+    lse = torch.zeros(T, HQ, device="cuda")
+    out, _ = kda.kda_attn_fwd(q.cuda(), k.cuda(), v.cuda(), 0.1,
+                              torch.tensor(cu, dtype=torch.int32, device="cuda"), None, lse,
+                              engine=engine)
+    for a, n in zip(cu, lens):
+        m = n // 2
+        assert torch.isnan(out[a:a + m]).all() and (lse[a:a + m] == -float("inf")).all()
+        b, e = a + m, a + n
+        check(out[b:e], lse[b:e], reference(q[b:e], k[b:e], v[b:e], 0.1, 0), n, d,
+              dtype == "bf16" and engine == "auto")
