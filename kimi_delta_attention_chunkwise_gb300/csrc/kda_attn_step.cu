@@ -272,7 +272,7 @@ struct SimtCore {
 };
 
 // ---------------------------------------------------------------------------
-// tensor-core core: bf16, D = 64 or 128, 8 NT query heads
+// tensor-core core: bf16, D = 64 or 128, 8 NT query heads (FOLD: 4)
 // ---------------------------------------------------------------------------
 // Scores and outputs are computed transposed, so that the 16-row side of
 // mma.sync.m16n8k16 is filled by tokens (then channels) and its 8-column side
@@ -287,8 +287,14 @@ struct SimtCore {
 //     channels 8 g .. + 7 (and 64 + 8 g .. + 7), and pairs the tokens'
 //     channels with byte permutes.
 // The weights P^T go from the accumulator's layout to the operand's by an 8x8
-// transpose (movmatrix).  They are rounded to bf16 (V's type, relative 2^-8);
-// their sum is taken in fp32 before the rounding.  The reference of the
+// transpose (movmatrix), as two bf16 parts that leave 2^-15 of a weight out
+// (split_weights; one part alone leaves 2^-8, as much as the output's own
+// rounding).  Each part takes a product, but with at most 4 query heads (FOLD)
+// the 8 columns hold the heads twice, the second time for the low parts, and
+// one product serves both (64 sequences of 512-8192 tokens, 32/8 heads, d =
+// 128: 194.8 us, two products 205, one rounded part 197; 64 sequences of 4000
+// tokens, 64/8 heads: two products 164.3 us, one part 163.9; 128/8 heads:
+// 187.5, 180.8).  The reference of the
 // exponentials moves only when a score passes it by more than 2^8, by a vote
 // of the warp: most tiles need no shuffles and no rescaling.
 // mma.sync, not tcgen05: 16 query rows at most use an eighth of its 128-row
@@ -316,10 +322,26 @@ __device__ __forceinline__ uint4 load_once(const void *p) {
     return x;
 }
 
-template <int D, int NT>
+// w (>= 0) as hi + lo in bf16: hi is w cut off (by less than 2^-7 of w), lo the
+// rest rounded (2^-8 of it).  lo stays positive where hi is, by 2^-20 of w and
+// 2^-126 at least: 0 times an infinity among the values would be a NaN.
+__device__ __forceinline__ float rest_of(float w, float hi) {
+    float lo;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(lo) : "f"(w - hi), "f"(hi * 0x1p-20f), "f"(fminf(hi, 0x1p-126f)));
+    return lo;
+}
+__device__ __forceinline__ void split_weights(float w0, float w1, uint32_t &hi, uint32_t &lo) {
+    hi = __byte_perm(__float_as_uint(w0), __float_as_uint(w1), 0x7632);
+    lo = tc::pack_bf16x2(rest_of(w0, __uint_as_float(hi << 16)),
+                         rest_of(w1, __uint_as_float(hi & 0xFFFF0000u)));
+}
+
+template <int D, int NT, bool FOLD = false>
 struct MmaCore {
+    static_assert(!FOLD || NT == 1, "the heads twice in 8 columns");
     using Type = __nv_bfloat16;
-    static constexpr int kD = D, kRows = 8 * NT, kCtas = NT == 1 ? 3 : 2;
+    static constexpr int kD = D, kRows = FOLD ? 4 : 8 * NT, kCtas = NT == 1 ? 3 : 2;
+    static constexpr int kParts = FOLD ? 1 : 2;  // products of the weights
     static constexpr bool kAhead = true;
     static constexpr int J = D / 32;   // 16-byte vectors of a token row per lane (K, Q)
     static constexpr int VC = D / 64;  // and of V
@@ -335,7 +357,7 @@ struct MmaCore {
         c2 = scale * kLog2e;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int h = n * 8 + g;
+            const int h = FOLD ? g & 3 : n * 8 + g;
 #pragma unroll
             for (int j = 0; j < J; ++j)
                 q[n][j] = h < rows ? *reinterpret_cast<const uint4 *>(qp + h * D + (j * 4 + t) * 8)
@@ -384,7 +406,8 @@ struct MmaCore {
     // weights of the tile's n tokens and their product with V
     __device__ void values(int n_tok) {
         const int g = (threadIdx.x & 31) >> 2;
-        uint32_t p[NT][2];
+        const bool low = FOLD && (threadIdx.x & 2);  // columns 4-7
+        uint32_t p[NT][kParts][2];  // by part (high, low) and half of the tokens
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             if (n_tok < kWarpTokens) {
@@ -420,8 +443,13 @@ struct MmaCore {
                 w[e] = tc::exp2_approx(fmaf(s[n][e], c2, r == -INFINITY ? 0.f : -r));
                 sum[n][e & 1] += w[e];
             }
-            p[n][0] = transpose_8x8(tc::pack_bf16x2(w[0], w[1]));
-            p[n][1] = transpose_8x8(tc::pack_bf16x2(w[2], w[3]));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                uint32_t hi, lo;
+                split_weights(w[2 * e], w[2 * e + 1], hi, lo);
+                p[n][0][e] = transpose_8x8(low ? lo : hi);
+                if (!FOLD) p[n][kParts - 1][e] = transpose_8x8(lo);
+            }
         }
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
@@ -440,7 +468,9 @@ struct MmaCore {
                 }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                mma_16816(o[i][n], a[0], a[1], a[2], a[3], p[n][0], p[n][1]);
+#pragma unroll
+                for (int part = kParts - 1; part >= 0; --part)
+                    mma_16816(o[i][n], a[0], a[1], a[2], a[3], p[n][part][0], p[n][part][1]);
         }
     }
     __device__ void finish(float *sacc, float *sm, float *sl, bool seen) {
@@ -452,7 +482,7 @@ struct MmaCore {
                 float l = sum[n][e];
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-                if (g == 0) {
+                if (g == 0 && 2 * t < kRows) {
                     sm[n * 8 + 2 * t + e] = state_max(ref[n][e], seen);
                     sl[n * 8 + 2 * t + e] = l;
                 }
@@ -463,7 +493,9 @@ struct MmaCore {
                 for (int e = 0; e < 4; ++e) {
                     const int h = n * 8 + 2 * t + (e & 1);
                     const int ch = VC == 2 ? 64 * (e >> 1) + 8 * g + i : 8 * g + 4 * (e >> 1) + i;
-                    sacc[h * D + ch] = o[i][n][e];
+                    float x = o[i][n][e];
+                    if (FOLD) x += __shfl_xor_sync(0xffffffffu, x, 2);
+                    if (h < kRows) sacc[h * D + ch] = x;
                 }
         }
     }
@@ -855,9 +887,11 @@ auto with_core(int32_t D, int32_t G, int32_t dtype, F f) {
             case 16: return f(SimtCore<__nv_bfloat16, 16>{});
             case 32: return f(SimtCore<__nv_bfloat16, 32>{});
             case 64:
+                if (G <= 4) return f(MmaCore<64, 1, true>{});
                 if (G <= 8) return f(MmaCore<64, 1>{});
                 return f(MmaCore<64, 2>{});
             default:
+                if (G <= 4) return f(MmaCore<128, 1, true>{});
                 if (G <= 8) return f(MmaCore<128, 1>{});
                 return f(MmaCore<128, 2>{});
         }

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import kimi_delta_attention_chunkwise_gb300 as kda
-from attn_testutil import check, reference
+from attn_testutil import U, check, reference
 
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
 TOP = 1 << 31
@@ -190,3 +190,67 @@ def test_prompt_scores_of_minus_infinity(gpu, dtype, engine, d, lens):
         b, e = a + m, a + n
         check(out[b:e], lse[b:e], reference(q[b:e], k[b:e], v[b:e], 0.1, 0), n, d,
               dtype == "bf16" and engine == "auto")
+
+
+def _step_case(seed, lens, HQ, HKV, d, dtype, wide):
+    """q, a sequence's keys and values, caches with pages of 32 in order, table."""
+    N, page, most = len(lens), 32, (max(lens) + 31) // 32
+    q = _randn(seed, N, HQ, d, dtype=dtype)
+    ks, vs = ([_randn(seed + 10 * s + i, n, HKV, d, dtype=dtype) for s, n in enumerate(lens)]
+              for i in (1, 2))
+    table = torch.full((N, 16384 if wide else most), -1, dtype=torch.int32)
+    for s in range(N):
+        table[s, :most] = torch.arange(most) + most * s
+
+    def cache(rows):
+        c = torch.zeros(N * most, HKV, page, d, dtype=DT[dtype])
+        for s, n in enumerate(lens):
+            x = torch.zeros(most * page, HKV, d, dtype=DT[dtype])
+            x[:n] = rows[s]
+            c[most * s:most * (s + 1)] = x.view(most, page, HKV, d).transpose(1, 2)
+        return c.cuda()
+
+    return q, ks, vs, cache, table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+
+GROUPS = [(1, 1, 64), (3, 1, 128), (8, 2, 128), (8, 2, 64), (5, 1, 128), (16, 2, 64), (12, 1, 128),
+          (32, 2, 64), (40, 1, 128)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("HQ,HKV,d", GROUPS)
+@pytest.mark.parametrize("wide", [False, True])
+def test_step_keeps_its_weights_bits(gpu, HQ, HKV, d, wide):
+    """bf16 with float32 results: the weights' two parts leave 2^-15 of them out
+    (2^-7 cut off, then rounded by 2^-8) and may add 2^-20, not the 2^-8 of one
+    rounded part; a key's two products are two additions."""
+    lens = [513, 64, 1, 2000]
+    q, ks, vs, cache, table, n32 = _step_case(HQ + d, lens, HQ, HKV, d, "bf16", wide)
+    out, _ = kda.kda_attn_step(q.cuda(), cache(ks), cache(vs), table, n32, d ** -0.5, out_f32=True)
+    for s, n in enumerate(lens):
+        o, A, _, z1 = reference(q[s:s + 1], ks[s], vs[s], d ** -0.5, n - 1)
+        rel = 2 * ((d + 8) * U * z1 + 4 * U * (2 * z1 + 2)) + 3 * (n + 16) * U + 2.0 ** -15 + 2.0 ** -20
+        assert ((out[s:s + 1].cpu().double() - o).abs() <= rel[..., None] * A + U * o.abs()).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("HQ,HKV,d,dtype", [(*g, "bf16") for g in GROUPS] +
+                         [(4, 2, 32, "bf16"), (6, 2, 64, "f32"), (8, 1, 128, "f32")])
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+def test_step_infinite_values(gpu, HQ, HKV, d, dtype, wide, value):
+    """A non-finite value shows in its channel, however small its weight (down
+    to the smallest normal number), and in no other channel."""
+    lens = [300, 90]
+    q, ks, vs, cache, table, n32 = _step_case(HQ, lens, HQ, HKV, d, dtype, wide)
+    q[..., 0], q[..., 1:] = 1, 0        # scores: the keys' first channel
+    for gap in (0.0, 1.0, 30.0, 100.0, 124.0):
+        for s in (0, 1):
+            ks[s][..., 0] = 0
+            ks[s][77, :, 0] = -gap      # 2^-gap of the largest weight
+            vs[s][77, :, 5] = value
+        out, _ = kda.kda_attn_step(q.cuda(), cache(ks), cache(vs), table, n32, 0.6931471805599453)
+        seen = out[..., 5].float()
+        assert (torch.isnan(seen) if value != value else seen == value).all()
+        rest = torch.cat((out[..., :5], out[..., 6:]), dim=-1)
+        assert torch.isfinite(rest).all()
