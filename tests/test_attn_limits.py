@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import kimi_delta_attention_chunkwise_gb300 as kda
-from attn_testutil import U, check, reference
+from attn_testutil import U, check, reference, rope_table, rotate, tables
 
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
 TOP = 1 << 31
@@ -254,3 +254,56 @@ def test_step_infinite_values(gpu, HQ, HKV, d, dtype, wide, value):
         assert (torch.isnan(seen) if value != value else seen == value).all()
         rest = torch.cat((out[..., :5], out[..., 6:]), dim=-1)
         assert torch.isfinite(rest).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("HQ,HKV,d", [(4, 2, 128), (8, 2, 64), (3, 3, 64), (7, 1, 128)])
+@pytest.mark.parametrize("before", [0, 77])
+def test_long_prompts_on_the_tensor_cores(gpu, HQ, HKV, d, before):
+    """Rows from a prompt's start, its middle and its end, and a short prompt in
+    front of it."""
+    n = 9001
+    q, k, v = (_randn(i + d, before + n, h, d, dtype="bf16") for i, h in ((1, HQ), (2, HKV), (3, HKV)))
+    cu = torch.tensor(([0] if before else []) + [before, before + n], dtype=torch.int32).cuda()
+    lse = torch.full((before + n, HQ), float("nan"), device="cuda")
+    out, _ = kda.kda_attn_fwd(q.cuda(), k.cuda(), v.cuda(), d ** -0.5, cu, None, lse, engine="tensor")
+    assert not torch.isnan(out).any() and not torch.isnan(lse).any()
+    for a, b in ((0, 150), (2490, 2640), (5000, 5130), (n - 300, n)):
+        rows = slice(before + a, before + b)
+        check(out[rows], lse[rows],
+              reference(q[rows], k[before:before + b], v[before:before + b], d ** -0.5, a), b, d, True)
+    if before:
+        check(out[:before], lse[:before], reference(q[:before], k[:before], v[:before], d ** -0.5, 0),
+              before, d, True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,rot,inter", [(64, 32, True), (128, 128, True), (32, 32, True), (16, 16, False),
+                                         (128, 48, False)])
+def test_append_of_more_tokens_than_ctas_of_one_take(gpu, dtype, d, rot, inter):
+    """Past 1024 tokens a CTA takes two; both pairings, parts of a head, and
+    rows outside every sequence."""
+    HQ, HKV, page, lens, held, T = 6, 2, 32, [1100, 0, 403], [500, 7, 31], 1506
+    q, k, v = (_randn(i + d, T, h, d, dtype=dtype) for i, h in ((1, HQ), (2, HKV), (3, HKV)))
+    need = [(h + n + page - 1) // page for h, n in zip(held, lens)]
+    table, pages = tables(need, max(need))
+    rope = rope_table(1700, rot)
+    pos = torch.cat([torch.arange(h, h + n) for h, n in zip(held, lens)])
+    want_q, want_k = (torch.full_like(x, 3) for x in (q, k))
+    want_q[1:1504], want_k[1:1504] = (rotate(x[1:1504], pos, rope, inter) for x in (q, k))
+    kc, vc = (torch.zeros(pages, HKV, page, d, dtype=DT[dtype]) for _ in range(2))
+    gk, gv = kc.cuda(), vc.cuda()
+    t = 1
+    for s, n in enumerate(lens):
+        for p in range(held[s], held[s] + n):
+            b = int(table[s, p // page])
+            kc[b, :, p % page], vc[b, :, p % page] = want_k[t], v[t]
+            t += 1
+    q_out, k_out = (torch.full_like(x, 3, device="cuda") for x in (q, k))
+    kda.kda_cache_append(k.cuda(), v.cuda(), gk, gv, table.cuda(),
+                         torch.tensor(held, dtype=torch.int32).cuda(),
+                         torch.tensor([1, 1101, 1101, 1504], dtype=torch.int32).cuda(), q=q.cuda(),
+                         q_out=q_out, k_out=k_out, rope=rope.cuda(), rope_interleaved=inter)
+    assert torch.equal(q_out.cpu(), want_q) and torch.equal(k_out.cpu(), want_k)
+    assert torch.equal(gk.cpu(), kc) and torch.equal(gv.cpu(), vc)
