@@ -221,6 +221,40 @@ def _stream_handle(stream) -> int:
     return stream.cuda_stream
 
 
+def _call_stream(stream, dev, torch):
+    """The stream a call was given (a torch stream on the tensors' device, or a
+    raw handle); None where that is the current one."""
+    raw = isinstance(stream, int)
+    if not raw and stream.device_index != dev:
+        raise ValueError(f"stream is on cuda:{stream.device_index}, the call's tensors on "
+                         f"cuda:{dev}")
+    if (stream if raw else stream.cuda_stream) == torch._C._cuda_getCurrentRawStream(dev):
+        return None
+    return torch.cuda.ExternalStream(stream, device=dev) if raw else stream
+
+
+def _empty(shape, dtype, device, stream, torch, returned=True):
+    """A tensor that the call writes, from the pool of the stream that writes
+    it: a block that another stream freed may still be read by work queued
+    there.  What the caller gets is marked as used on the current stream too,
+    so that its block comes back only after that stream's work."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _made(shape, dtype, like, stream):
+    """A result of a call on `stream`, on the device of `like`."""
+    torch = _torch()
+    if stream is not None:
+        stream = _call_stream(stream, like.get_device(), torch)
+    return _empty(shape, dtype, like.device, stream, torch)
+
+
 def _dtype_code(t) -> int:
     torch = _torch()
     if t.dtype == torch.bfloat16:
@@ -308,13 +342,15 @@ def _workspace(nbytes: int, device, stream=None):
            _stream_handle(stream))
     buf = _ws_cache.get(key)
     if buf is None or buf.numel() < nbytes:
-        buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+        if stream is not None:
+            stream = _call_stream(stream, key[0], torch)
+        buf = _empty(nbytes + 256, torch.uint8, device, stream, torch, returned=False)
         _ws_cache[key] = buf
     return buf
 
 
 def _prefill_args(q, k, v, log_alpha, beta, initial_state, cu_seqlens, out, final_state,
-                  chunk_size, engine, out_f32=False, prologue=None, on_host=False):
+                  chunk_size, engine, out_f32=False, prologue=None, on_host=False, stream=None):
     torch = _torch()
     _req = lambda t, name, dtype=None, shape=None: _require(t, name, dtype, shape, on_host)
     for name, t in (("q", q), ("k", k), ("v", v)):
@@ -340,9 +376,10 @@ def _prefill_args(q, k, v, log_alpha, beta, initial_state, cu_seqlens, out, fina
     if odt not in (q.dtype, torch.float32):
         raise TypeError("out must have the dtype of q, or float32")
     if out is None:
-        out = torch.empty((T, HV, dv), dtype=odt, device=q.device)
         if on_host:
-            out = out.pin_memory()
+            out = torch.empty((T, HV, dv), dtype=odt, device=q.device).pin_memory()
+        else:
+            out = _made((T, HV, dv), odt, q, stream)
     _req(out, "out", odt, (T, HV, dv))
     _req(final_state, "final_state", torch.float32, (N, HV, dk, dv))
     eng = _ENGINES[engine] if isinstance(engine, str) else int(engine)
@@ -372,7 +409,7 @@ def kda_chunk_fwd(q, k, v, log_alpha, beta, scale: float, initial_state=None,
     """
     shape, out = _prefill_args(q, k, v, log_alpha, beta, initial_state, cu_seqlens, out,
                                final_state, chunk_size, engine, out_f32,
-                               (l2norm_qk, beta_logits, gate))
+                               (l2norm_qk, beta_logits, gate), stream=stream)
     lib = load()
     s = _stream_handle(stream)
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), float(scale),
@@ -400,7 +437,7 @@ def kda_chunk_fwd_static(q, k, v, log_alpha, beta, scale: float, initial_state=N
     the array are refused (KDA_ERR_UNSUPPORTED).  Arguments as kda_chunk_fwd."""
     shape, out = _prefill_args(q, k, v, log_alpha, beta, initial_state, cu_seqlens, out,
                                final_state, chunk_size, engine, out_f32,
-                               (l2norm_qk, beta_logits, gate))
+                               (l2norm_qk, beta_logits, gate), stream=stream)
     _check(load().kda_chunk_fwd_static(
         _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), float(scale),
         _ptr(initial_state), _ptr(cu_seqlens), _ptr(out), _ptr(final_state),
@@ -418,7 +455,7 @@ def kda_chunk_fwd_ws_timed(q, k, v, log_alpha, beta, scale: float, initial_state
     launch stream.  Returns ``(out, final_state, n_recorded)``."""
     shape, out = _prefill_args(q, k, v, log_alpha, beta, initial_state, cu_seqlens, out,
                                final_state, chunk_size, engine, out_f32,
-                               (l2norm_qk, beta_logits, gate))
+                               (l2norm_qk, beta_logits, gate), stream=stream)
     nbytes = kda_chunk_fwd_workspace_size(shape)
     ws = _workspace(nbytes, q.device, stream)
     wp = None if ws is None else (ws.data_ptr() + 255) // 256 * 256
@@ -441,7 +478,7 @@ def kda_chunk_fwd_ws_diag(q, k, v, log_alpha, beta, scale: float, initial_state,
     out and the device status word reports KDA_ERR_TIMEOUT.  Returns
     ``(out, final_state)``."""
     shape, out = _prefill_args(q, k, v, log_alpha, beta, initial_state, cu_seqlens, out,
-                               final_state, chunk_size, KDA_ENGINE_TENSOR, out_f32)
+                               final_state, chunk_size, KDA_ENGINE_TENSOR, out_f32, stream=stream)
     nbytes = kda_chunk_fwd_workspace_size(shape)
     ws = _workspace(nbytes, q.device, stream)
     wp = None if ws is None else (ws.data_ptr() + 255) // 256 * 256
@@ -504,7 +541,7 @@ def kda_chunk_fwd_ws(q, k, v, log_alpha, beta, scale: float, initial_state, cu_s
                      stream=None):
     """kda_chunk_fwd with an explicit workspace tensor (uint8, >= the size query)."""
     shape, out = _prefill_args(q, k, v, log_alpha, beta, initial_state, cu_seqlens, out,
-                               final_state, chunk_size, engine)
+                               final_state, chunk_size, engine, stream=stream)
     nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(load().kda_chunk_fwd_ws(
         _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), float(scale),
@@ -540,7 +577,7 @@ def kda_recurrent_step(q, k, v, log_alpha, beta, scale: float, state, out=None, 
     if odt not in (q.dtype, torch.float32):
         raise TypeError("out must have the dtype of q, or float32")
     if out is None:
-        out = torch.empty((N, HV, dv), dtype=odt, device=q.device)
+        out = _made((N, HV, dv), odt, q, stream)
     _require(out, "out", odt, (N, HV, dv))
     bits, gb, ga = _prologue(l2norm_qk, beta_logits, gate, HV, dk)
     shape = make_shape(N, N, H, dk, dv, _dtype_code(q),
@@ -592,7 +629,7 @@ def kda_recurrent_fwd(q, k, v, log_alpha, beta, scale: float, state_pool, cu_seq
     if odt not in (q.dtype, torch.float32):
         raise TypeError("out must have the dtype of q, or float32")
     if out is None:
-        out = torch.empty((T, HV, dv), dtype=odt, device=q.device)
+        out = _made((T, HV, dv), odt, q, stream)
     _require(out, "out", odt, (T, HV, dv))
     bits, gb, ga = _prologue(l2norm_qk, beta_logits, gate, HV, dk)
     shape = make_shape(N, T, H, dk, dv, _dtype_code(q),
@@ -632,7 +669,7 @@ def kda_short_conv_fwd(x, weight, bias=None, cu_seqlens=None, cache_in=None, cac
     _require(cache_in, "cache_in", x.dtype, (N, C, W))
     _require(cache_out, "cache_out", x.dtype, (N, C, W))
     if y is None:
-        y = torch.empty_like(x)
+        y = _made(x.shape, x.dtype, x, stream)
     _require(y, "y", x.dtype, (T, C))
     shape = kdaConvShape_t(N, T, C, W, _dtype_code(x), int(bool(silu)))
     _check(load().kda_short_conv_fwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(cu_seqlens),
@@ -658,7 +695,7 @@ def kda_short_conv_step(x, weight, cache, bias=None, y=None, *, silu: bool = Fal
     _require(bias, "bias", torch.float32, (C,))
     _require(cache, "cache", x.dtype, (N, C, W))
     if y is None:
-        y = torch.empty_like(x)
+        y = _made(x.shape, x.dtype, x, stream)
     _require(y, "y", x.dtype, (N, C))
     shape = kdaConvShape_t(N, N, C, W, _dtype_code(x), int(bool(silu)))
     _check(load().kda_short_conv_step(_ptr(x), _ptr(weight), _ptr(bias), _ptr(cache), _ptr(y),
@@ -692,11 +729,10 @@ def kda_recurrent_bwd(q, k, v, log_alpha, beta, scale: float, initial_state=None
     _require(initial_state, "initial_state", torch.float32, (N, H, dk_, dv_))
     _require(d_out, "d_out", q.dtype, (T, H, dv_))
     _require(d_final_state, "d_final_state", torch.float32, (N, H, dk_, dv_))
-    f32 = dict(dtype=torch.float32, device=q.device)
-    dq, dk, dlog = (torch.empty((T, H, dk_), **f32) for _ in range(3))
-    dv = torch.empty((T, H, dv_), **f32)
-    db = torch.empty((T, H), **f32)
-    dS0 = torch.empty((N, H, dk_, dv_), **f32) if want_initial else None
+    made = lambda *size: _made(size, torch.float32, q, stream)
+    dq, dk, dlog = (made(T, H, dk_) for _ in range(3))
+    dv, db = made(T, H, dv_), made(T, H)
+    dS0 = made(N, H, dk_, dv_) if want_initial else None
     shape = make_shape(N, T, H, dk_, dv_, _dtype_code(q))
     _check(load().kda_recurrent_bwd(
         _ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), float(scale),
@@ -731,11 +767,10 @@ def kda_chunk_bwd(q, k, v, log_alpha, beta, scale: float, initial_state=None,
     _require(initial_state, "initial_state", torch.float32, (N, H, dk_, dv_))
     _require(d_out, "d_out", q.dtype, (T, H, dv_))
     _require(d_final_state, "d_final_state", torch.float32, (N, H, dk_, dv_))
-    f32 = dict(dtype=torch.float32, device=q.device)
-    dq, dk, dlog = (torch.empty((T, H, dk_), **f32) for _ in range(3))
-    dv = torch.empty((T, H, dv_), **f32)
-    db = torch.empty((T, H), **f32)
-    dS0 = torch.empty((N, H, dk_, dv_), **f32) if want_initial else None
+    made = lambda *size: _made(size, torch.float32, q, stream)
+    dq, dk, dlog = (made(T, H, dk_) for _ in range(3))
+    dv, db = made(T, H, dv_), made(T, H)
+    dS0 = made(N, H, dk_, dv_) if want_initial else None
     shape = make_shape(N, T, H, dk_, dv_, _dtype_code(q))
     # scratch from the binding's per-device cache (no allocation per call)
     n = ctypes.c_size_t(0)
@@ -886,32 +921,6 @@ def _paged_cache(k_cache, v_cache, block_table, dev, dtype, i32, N, d):
         _fit_i32(size[0], width[1])
     return kdaPagedCache_t(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), size[0],
                            size[2], width[1]), size[1]
-
-
-def _call_stream(stream, dev, torch):
-    """The stream a call was given (a torch stream on the tensors' device, or a
-    raw handle); None where that is the current one."""
-    raw = isinstance(stream, int)
-    if not raw and stream.device_index != dev:
-        raise ValueError(f"stream is on cuda:{stream.device_index}, the call's tensors on "
-                         f"cuda:{dev}")
-    if (stream if raw else stream.cuda_stream) == torch._C._cuda_getCurrentRawStream(dev):
-        return None
-    return torch.cuda.ExternalStream(stream, device=dev) if raw else stream
-
-
-def _empty(shape, dtype, device, stream, torch, returned=True):
-    """A tensor that the call writes, from the pool of the stream that writes
-    it: a block that another stream freed may still be read by work queued
-    there.  What the caller gets is marked as used on the current stream too,
-    so that its block comes back only after that stream's work."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    if returned:
-        t.record_stream(torch.cuda.current_stream(device))
-    return t
 
 
 def _attn_out(q, shape, dev, dt, out, out_f32, stream, torch):

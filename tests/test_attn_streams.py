@@ -3,6 +3,7 @@ a call makes comes from the pool of the stream that writes it.  A block of the
 current stream's pool may still be read by work queued there, which only that
 stream's later work may overwrite."""
 import contextlib
+import functools
 from types import SimpleNamespace
 
 import pytest
@@ -46,11 +47,14 @@ class _Notes:
         current = lambda dev=None: self.now
         self.cuda = SimpleNamespace(stream=self._as_current, current_stream=current,
                                     device=lambda dev: contextlib.nullcontext(),
+                                    current_device=lambda: 0,
                                     ExternalStream=lambda h, device=None: _stream(h))
         self._C = SimpleNamespace(_cuda_getCurrentRawStream=lambda dev: self.now.cuda_stream,
                                   _cuda_getDevice=lambda: 0)
 
     def __getattr__(self, name):
+        if name.startswith("kda_"):
+            return self._size if name.endswith("_size") else functools.partial(self._launch, name)
         return getattr(torch, name)
 
     @contextlib.contextmanager
@@ -70,20 +74,12 @@ class _Notes:
         return self._note(_dev(*t.shape, dtype=t.dtype))
 
     # libkda
-    def kda_attn_step_workspace_size(self, cache, shape, n):
-        n._obj.value = 4096
+    def _size(self, *args):
+        args[-1]._obj.value = 4096
         return 0
 
-    def kda_attn_fwd(self, *args):
-        self.launched.append(("fwd", args[-1]))
-        return 0
-
-    def kda_cache_append(self, *args):
-        self.launched.append(("append", args[-1]))
-        return 0
-
-    def kda_attn_step_ws(self, *args):
-        self.launched.append(("step", args[-1]))
+    def _launch(self, name, *args):
+        self.launched.append((name, args[-1]))
         return 0
 
 
@@ -93,6 +89,7 @@ def notes(monkeypatch):
     monkeypatch.setattr(binding, "_torch", lambda: n)
     monkeypatch.setattr(binding, "load", lambda: n)
     monkeypatch.setattr(binding, "_step_bytes", {})
+    monkeypatch.setattr(binding, "_ws_cache", {})
     return n
 
 
@@ -218,3 +215,28 @@ def test_results_leave_the_current_streams_pending_reads_alone(gpu, raw):
             torch.cuda.synchronize()
             assert (kept == i + 1).all() and torch.equal(got, want)
             del got
+
+
+@pytest.mark.gpu
+def test_a_captured_call_on_a_forked_stream(gpu):
+    """A call on a stream that a capture has forked: its tensors live in the
+    graph's memory, and replays on other queries give their results."""
+    N, HQ, HKV, d, page = 8, 8, 2, 128, 64
+    kc, vc, table = _cache(N, 16384, HKV, d, page, BF16)
+    lens = torch.tensor([512, 500, 3, 64, 0, 333, 512, 100], dtype=I32, device="cuda")
+    q = [_randn(i, N, HQ, d) for i in (5, 6)]
+    want = [kda.kda_attn_step(x, kc, vc, table, lens, 0.1)[0] for x in q]
+    static, side = q[0].clone(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        out, _ = kda.kda_attn_step(static, kc, vc, table, lens, 0.1, stream=side)
+        here, _ = kda.kda_attn_step(static, kc, vc, table, lens, 0.1)
+        torch.cuda.current_stream().wait_stream(side)
+        both = torch.cat((out, here))
+    for x, w in ((q[1], want[1]), (q[0], want[0]), (q[1], want[1])):
+        static.copy_(x)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(both, torch.cat((w, w)))
