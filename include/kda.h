@@ -562,7 +562,8 @@ kdaStatus_t kda_chunk_bwd_ws(const void *q, const void *k, const void *v,
 typedef struct {
     int32_t num_seqs;      /* N >= 1, at most 2^30 */
     int32_t total_tokens;  /* T >= 0: rows of q, k, v; must equal N (step) */
-    int32_t num_heads;     /* HQ >= 1: query heads */
+    int32_t num_heads;     /* HQ >= 1: query heads; HQ <= 65535, T HQ and N HQ <= 2^31 - 1,
+                              and T HQ / 16 + N HKV <= 2^31 - 1 (kda_attn_fwd) */
     int32_t num_kv_heads;  /* HKV >= 1, divides HQ; HQ / HKV <= 128 */
     int32_t head_dim;      /* d in {16, 32, 64, 128} */
     int32_t dtype;         /* kdaDtype_t of q, k, v, out and the cache */
@@ -583,7 +584,8 @@ typedef struct {
                                     p / page_size of its sequence's row */
     int32_t num_pages;           /* >= 0 */
     int32_t page_size;           /* 16, 32, 64, 128 or 256 tokens */
-    int32_t max_pages;           /* entries per row of block_table, >= 0 */
+    int32_t max_pages;           /* entries per row of block_table, >= 0;
+                                    max_pages * page_size <= 2^31 - 1 */
 } kdaPagedCache_t;
 
 /* Position rotation: a table of cosines and sines per position.  Pair m

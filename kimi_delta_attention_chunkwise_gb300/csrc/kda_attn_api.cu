@@ -144,10 +144,9 @@ kdaStatus_t kda_attn_fwd(const void *q, const void *k, const void *v, float scal
     const bool tensor_ok = shape->dtype == KDA_DTYPE_BF16 &&
                            (shape->head_dim == 64 || shape->head_dim == 128);
     if (shape->engine == KDA_ENGINE_TENSOR && !tensor_ok) return KDA_ERR_UNSUPPORTED;
-    // (items index a one-dimensional grid)
-    const int32_t group = shape->num_heads / shape->num_kv_heads;
-    if (((int64_t)shape->total_tokens / (2 * (128 / group)) + shape->num_seqs) *
-            shape->num_kv_heads > INT32_MAX)
+    // (items index a one-dimensional grid; the smallest tiles have 16 rows)
+    if ((int64_t)shape->total_tokens * shape->num_heads / 16 +
+            (int64_t)shape->num_seqs * shape->num_kv_heads > INT32_MAX)
         return KDA_ERR_UNSUPPORTED;
     if (shape->total_tokens == 0) return KDA_SUCCESS;
     AttnArgs a;

@@ -39,6 +39,19 @@ def test_more_than_2_30_sequences_are_refused():
         kda.KDA_ERR_UNSUPPORTED
 
 
+def test_grids_past_2_31_blocks_are_refused():
+    """One more tile of rows than a grid holds, whichever engine takes it."""
+    from kimi_delta_attention_chunkwise_gb300 import binding, build
+    build.build()
+    lib, fake, other = binding.load(), 0x10000, 0x20000   # never dereferenced
+    for dtype in (kda.KDA_DTYPE_F32, kda.KDA_DTYPE_BF16):
+        for N, T, H in (((1 << 30) - 1, 40, 2), ((1 << 24) - 1, 1 << 24, 127)):
+            assert max(N * H, T * H) < TOP <= T * H // 16 + N * H
+            s = ctypes.byref(kda.make_attn_shape(N, T, H, H, 64, dtype))
+            assert lib.kda_attn_fwd(fake, fake, fake, 0.1, fake, other, None, s, None) == \
+                kda.KDA_ERR_UNSUPPORTED
+
+
 def test_sizes_past_32_bits_are_refused_not_cut_off():
     """2^32 + 5 of anything would arrive as 5."""
     from kimi_delta_attention_chunkwise_gb300 import binding
