@@ -58,10 +58,11 @@
 // word, every role leaves its loop, and the CTA ends after its copies and
 // MMAs in flight.
 //
-// What bounds it: d = 128: the tensor core (16384 tokens, 32/8 heads: 1.27 ms,
-// 1.73 PFLOP/s of the mask's lower half, 0.90 of a library matrix product's
-// best; the clocks come down with it).  d = 64: the softmax's chain of latencies
-// (8192 tokens, 32/8 heads: 1.04 PFLOP/s).  Short sequences: an item's chain of
+// What bounds it: d = 128: the tensor core, and the power it draws (16384 tokens,
+// 32/8 heads: 1.22-1.32 ms as the clocks come down, 1.67-1.81 PFLOP/s of the
+// mask's lower half, 0.87-0.94 of a library matrix product's best).  d = 64: the
+// softmax (8192 tokens, 32/8 heads: 257 us, 1.07 PFLOP/s): a key tile's tensor
+// work is half, its weights are not.  Short sequences: an item's chain of
 // copy, scores, weights, product and store (1000 x 64 tokens, 32/8 heads: 201
 // us, 6.5 TB/s).
 #include <cstdint>
@@ -992,7 +993,11 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t stream) {
 // taken ahead while the softmax runs (1000 x 64 tokens, 32/8 heads: d = 128 201
 // us, 128 keys 248; d = 64 147, 226; 300 prompts of 200 tokens on average: 308,
 // 393; 266, 333; 100 of 700: 601, 615; 411, 461; with 16/16 heads 399, 385;
-// 338, 343).  The host knows the mean length alone, so that decides.  A lone
+// 338, 343).  So the border lies between 512 and 700 tokens or above, by width
+// and group; one border for all gives up as much as 12% (d = 64, 32/8 heads, a
+// mean of 700).  The host knows the mean length alone, so that decides, and
+// empty sequences count in it: one prompt of 16384 tokens with 63 empty ones
+// takes 64-key tiles (d = 128: 1663 us, alone 1217; d = 64: 1352, 970).  A lone
 // prompt has no other work to fill the hand-overs with (400 tokens, 32/8 heads:
 // 12.5 us, 128 keys 11.9; 100 tokens 8.7, 9.2).
 cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t stream) {
