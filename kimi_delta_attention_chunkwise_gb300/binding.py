@@ -224,13 +224,13 @@ def _stream_handle(stream) -> int:
 def _call_stream(stream, dev, torch):
     """The stream a call was given (a torch stream on the tensors' device, or a
     raw handle); None where that is the current one."""
-    raw = isinstance(stream, int)
-    if not raw and stream.device_index != dev:
-        raise ValueError(f"stream is on cuda:{stream.device_index}, the call's tensors on "
-                         f"cuda:{dev}")
-    if (stream if raw else stream.cuda_stream) == torch._C._cuda_getCurrentRawStream(dev):
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    index = getattr(stream, "device_index", None)   # (None: a handle)
+    if index is not None and index != dev:
+        raise ValueError(f"stream is on cuda:{index}, the call's tensors on cuda:{dev}")
+    if handle == torch._C._cuda_getCurrentRawStream(dev):
         return None
-    return torch.cuda.ExternalStream(stream, device=dev) if raw else stream
+    return stream if index is not None else torch.cuda.ExternalStream(handle, device=dev)
 
 
 def _empty(shape, dtype, device, stream, torch, returned=True):

@@ -109,9 +109,9 @@ def _calls(stream):
     ]
 
 
-@pytest.mark.parametrize("raw", [False, True])
-def test_another_streams_call_makes_its_tensors_there(notes, raw):
-    for call in _calls(22 if raw else _stream(22)):
+@pytest.mark.parametrize("stream", [_stream(22), 22, SimpleNamespace(cuda_stream=22)])
+def test_another_streams_call_makes_its_tensors_there(notes, stream):
+    for call in _calls(stream):
         notes.made.clear()
         notes.launched.clear()
         returned = call()
