@@ -704,6 +704,100 @@ kdaStatus_t kda_attn_step_ws(const void *q, const kdaPagedCache_t *cache, const 
                              float scale, void *out, float *lse, const kdaAttnShape_t *shape,
                              void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * A paged cache of 8-bit codes: half the bytes of a bf16 one.  A row (one
+ * token's key, or value, of one head) of d channels is held as d whole numbers
+ * and one scale:
+ *
+ *     top = max_c |x_c|     code_c = rint(x_c * (127 / top))     scale = top / 127
+ *
+ * (each operation rounded to fp32, rint to the even neighbour); it stands for
+ * code_c * scale, which is off from x_c by half a scale (and fp32's rounding).
+ * A row whose top is below 2^-100 is held as zeros with a scale of 0.  A row
+ * with an infinity or a NaN is held as zeros with a scale of NaN, and whatever
+ * attends to it is NaN.
+ * ---------------------------------------------------------------------------
+ */
+typedef struct {
+    void *k;                     /* codes: int8 [num_pages, HKV, page_size, d], 16-byte aligned */
+    void *v;                     /* same layout */
+    float *k_scale;              /* float32 [num_pages, HKV, page_size] */
+    float *v_scale;              /* same layout */
+    const int32_t *block_table;  /* the rest as in kdaPagedCache_t */
+    int32_t num_pages;
+    int32_t page_size;
+    int32_t max_pages;
+} kdaPagedCacheQ8_t;
+
+/*
+ * kda_cache_append_q8 -- kda_cache_append to a cache of 8-bit codes.  The
+ * codes and scales are the rotated fp32 row's, before any rounding to dtype.
+ * Arguments, places and errors as there, and
+ *
+ *   k_stored  [T, HKV, d] dtype contiguous, or NULL: what the new keys' codes
+ *             stand for (code * scale in fp32, rounded to dtype), for a prompt
+ *             that is to attend to what later tokens will see; no other tensor
+ *             of the call
+ *   v_stored  the values, likewise
+ *
+ * k_out holds the rotated keys as they are before the coding.  Allocates
+ * nothing.
+ */
+kdaStatus_t kda_cache_append_q8(const void *q, const void *k, const void *v,
+                                const int32_t *cu_seqlens, const int32_t *cache_lens,
+                                const kdaRope_t *rope, void *q_out, void *k_out, void *k_stored,
+                                void *v_stored, const kdaPagedCacheQ8_t *cache,
+                                const kdaAttnShape_t *shape, cudaStream_t stream);
+
+/*
+ * kda_attn_step_q8 -- kda_attn_step over a cache of 8-bit codes: the keys and
+ * values are code * scale.  shape->dtype is q's (and out's, unless out_f32).
+ * The scales multiply scores and weights in fp32; the softmax weights keep
+ * 2^-15 or better in every product.  Arguments, lengths, pages, scratch and
+ * errors as for kda_attn_step.
+ */
+kdaStatus_t kda_attn_step_q8(const void *q, const kdaPagedCacheQ8_t *cache,
+                             const int32_t *seq_lens, float scale, void *out, float *lse,
+                             const kdaAttnShape_t *shape, cudaStream_t stream);
+kdaStatus_t kda_attn_step_q8_workspace_size(const kdaPagedCacheQ8_t *cache,
+                                            const kdaAttnShape_t *shape, size_t *bytes);
+kdaStatus_t kda_attn_step_q8_ws(const void *q, const kdaPagedCacheQ8_t *cache,
+                                const int32_t *seq_lens, float scale, void *out, float *lse,
+                                const kdaAttnShape_t *shape, void *workspace,
+                                size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * kda_attn_step_shared -- kda_attn_step for sequences that have their first
+ * pages in common (a system prompt, several answers to one prompt): those
+ * pages are read once for all of them.
+ *
+ *   shared_pages  [1] int32 device: the first *shared_pages entries of
+ *                 block_table are the same in the row of every sequence that
+ *                 has shared_pages * page_size tokens or more
+ *
+ * The result is kda_attn_step's with the same arguments (sums in another
+ * order).  A sequence with fewer tokens is worked on by itself, and its row of
+ * block_table may hold anything behind them.  Where the rows do differ, the
+ * first such sequence's entries are taken for all.  A number below 0 or above
+ * max_pages is cut to it and sets KDA_ERR_INVALID_ARG in the device status
+ * word; so does a shared page that is negative or >= num_pages, whose tokens
+ * are left out for every sequence that shares it.  Lengths, pages, scratch
+ * (the rows' partial results over the shared tokens among it) and errors as
+ * for kda_attn_step.
+ */
+kdaStatus_t kda_attn_step_shared(const void *q, const kdaPagedCache_t *cache,
+                                 const int32_t *seq_lens, const int32_t *shared_pages, float scale,
+                                 void *out, float *lse, const kdaAttnShape_t *shape,
+                                 cudaStream_t stream);
+kdaStatus_t kda_attn_step_shared_workspace_size(const kdaPagedCache_t *cache,
+                                                const kdaAttnShape_t *shape, size_t *bytes);
+kdaStatus_t kda_attn_step_shared_ws(const void *q, const kdaPagedCache_t *cache,
+                                    const int32_t *seq_lens, const int32_t *shared_pages,
+                                    float scale, void *out, float *lse,
+                                    const kdaAttnShape_t *shape, void *workspace,
+                                    size_t workspace_bytes, cudaStream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char *kda_status_string(kdaStatus_t status);
 
@@ -713,8 +807,8 @@ const char *kda_status_string(kdaStatus_t status);
  * KDA_ERR_TIMEOUT if a bounded wait inside a kernel gave up since the last
  * call (that kernel's outputs are then invalid), or KDA_ERR_INVALID_ARG if
  * kda_recurrent_fwd met a state index >= num_slots (that sequence was
- * skipped) or kda_cache_append / kda_attn_step a position, page or length
- * outside the cache (skipped as they document).  Returns KDA_ERR_CUDA if the synchronisation itself fails.
+ * skipped) or kda_cache_append / kda_attn_step (or a form of theirs) a position,
+ * page or length outside the cache (skipped as they document).  Returns KDA_ERR_CUDA if the synchronisation itself fails.
  */
 kdaStatus_t kda_device_status(cudaStream_t stream);
 

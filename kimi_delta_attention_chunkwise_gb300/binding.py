@@ -20,6 +20,8 @@ The functions carry the C names:
 * ``kda_attn_fwd``, ``kda_cache_append``, ``kda_attn_step`` -- the full-attention layers of a
   mixed stack: causal attention over packed prompts, rotation and append to a paged cache,
   one token of every sequence over its cache;
+* ``kda_cache_append_q8``, ``kda_attn_step_q8`` -- the same over a cache of 8-bit codes;
+* ``kda_attn_step_shared`` -- the step of sequences that have their first pages in common;
 * ``kda_chunk_path_counts`` -- how the decayed products were evaluated;
 * ``kda_status_string``, ``kda_device_status``.
 """
@@ -80,6 +82,13 @@ class kdaPagedCache_t(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("block_table", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class kdaPagedCacheQ8_t(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
 
 
 class kdaRope_t(ctypes.Structure):
@@ -172,6 +181,21 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.kda_attn_step_ws.argtypes = [vp, cachep, ip, ctypes.c_float, vp, fp, ashp, vp,
                                      ctypes.c_size_t, vp]
     lib.kda_attn_step_ws.restype = ctypes.c_int
+    q8p = ctypes.POINTER(kdaPagedCacheQ8_t)
+    lib.kda_cache_append_q8.argtypes = [vp, vp, vp, ip, ip, ropep, vp, vp, vp, vp, q8p, ashp, vp]
+    lib.kda_attn_step_q8.argtypes = [vp, q8p, ip, ctypes.c_float, vp, fp, ashp, vp]
+    lib.kda_attn_step_q8_workspace_size.argtypes = [q8p, ashp, ctypes.POINTER(ctypes.c_size_t)]
+    lib.kda_attn_step_q8_ws.argtypes = [vp, q8p, ip, ctypes.c_float, vp, fp, ashp, vp,
+                                        ctypes.c_size_t, vp]
+    lib.kda_attn_step_shared.argtypes = [vp, cachep, ip, ip, ctypes.c_float, vp, fp, ashp, vp]
+    lib.kda_attn_step_shared_workspace_size.argtypes = [cachep, ashp,
+                                                        ctypes.POINTER(ctypes.c_size_t)]
+    lib.kda_attn_step_shared_ws.argtypes = [vp, cachep, ip, ip, ctypes.c_float, vp, fp, ashp, vp,
+                                            ctypes.c_size_t, vp]
+    for name in ("cache_append_q8", "attn_step_q8", "attn_step_q8_workspace_size",
+                 "attn_step_q8_ws", "attn_step_shared", "attn_step_shared_workspace_size",
+                 "attn_step_shared_ws"):
+        getattr(lib, "kda_" + name).restype = ctypes.c_int
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_device_status.argtypes = [vp]
@@ -923,6 +947,15 @@ def _paged_cache(k_cache, v_cache, block_table, dev, dtype, i32, N, d):
                            size[2], width[1]), size[1]
 
 
+def _cache_q8(k_cache, v_cache, k_scale, v_scale, block_table, dev, N, d, torch):
+    """(the C description of a cache of 8-bit codes, HKV)."""
+    cache, HKV = _paged_cache(k_cache, v_cache, block_table, dev, torch.int8, torch.int32, N, d)
+    size, f32 = k_cache.shape[:3], torch.float32
+    return kdaPagedCacheQ8_t(cache.k, cache.v, _whole(k_scale, "k_scale", dev, f32, size),
+                             _whole(v_scale, "v_scale", dev, f32, size), cache.block_table,
+                             cache.num_pages, cache.page_size, cache.max_pages), HKV
+
+
 def _attn_out(q, shape, dev, dt, out, out_f32, stream, torch):
     """(out, its address, out_f32 flag)."""
     if out is None:
@@ -1066,6 +1099,78 @@ def kda_cache_append(k, v, k_cache, v_cache, block_table, cache_lens, cu_seqlens
     return q_out, k_out
 
 
+def kda_cache_append_q8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cache_lens,
+                        cu_seqlens=None, *, q=None, q_out=None, k_out=None, k_stored=None,
+                        v_stored=None, rope=None, rope_interleaved: bool = False, stream=None):
+    """kda_cache_append to a cache of 8-bit codes (C: kda_cache_append_q8).
+    Returns ``(q_out, k_out)``.
+
+    k_cache / v_cache: int8 [pages, HKV, page_size, d]; k_scale / v_scale: fp32
+    [pages, HKV, page_size]; all four updated in place.  ``k_stored`` and
+    ``v_stored`` [T, HKV, d], of k's type, receive what the new rows' codes stand
+    for if given; ``k_out`` the rotated keys as they are.  The rest as for
+    kda_cache_append.
+    """
+    torch = _torch()
+    dev, dt, code, size = _lead(k, "k", torch)
+    i32 = torch.int32
+    T, HKV, d = size
+    HQ, qs, ks, vs = HKV, 0, 0, 0
+    qp = qop = kop = ksp = vsp = cup = rp = None
+    if stream is not None:
+        stream = _call_stream(stream, dev, torch)
+    if not (getattr(v, "shape", None) == size and v.get_device() == dev and v.dtype is dt
+            and k.is_contiguous() and v.is_contiguous()):
+        _explain(v, "v", dev, dt, size, False)
+        ks, vs = _token_stride(k, "k"), _token_stride(v, "v")
+    if cache_lens is None:
+        raise ValueError("cache_lens must be [N]")
+    N = cache_lens.numel()
+    lp = _whole(cache_lens, "cache_lens", dev, i32, (N,))
+    if cu_seqlens is not None:
+        cup = _whole(cu_seqlens, "cu_seqlens", dev, i32, (N + 1,))
+    elif N != T and N != 1:
+        raise ValueError(f"{T} tokens of {N} sequences need cu_seqlens")
+    cache, heads = _cache_q8(k_cache, v_cache, k_scale, v_scale, block_table, dev, N, d, torch)
+    if heads != HKV:
+        raise ValueError(f"k has {HKV} heads, the cache {heads}")
+    if rope is not None:
+        rsize = rope.shape
+        if len(rsize) != 2:
+            raise ValueError("rope must be [positions, rot_dim]")
+        if rsize[0] > _I32_MAX:
+            _fit_i32(rsize[0])
+        rp = ctypes.byref(kdaRope_t(_whole(rope, "rope", dev, torch.float32, rsize), rsize[0],
+                                    rsize[1], bool(rope_interleaved)))
+    if k_out is not None:
+        kop = _whole(k_out, "k_out", dev, dt, size)
+    if k_stored is not None:
+        ksp = _whole(k_stored, "k_stored", dev, dt, size)
+    if v_stored is not None:
+        vsp = _whole(v_stored, "v_stored", dev, dt, size)
+    if q is not None:
+        qsize = getattr(q, "shape", ())
+        HQ = qsize[1] if len(qsize) == 3 else 0
+        if not (qsize == (T, HQ, d) and q.get_device() == dev and q.dtype is dt
+                and q.is_contiguous()):
+            _explain(q, "q", dev, dt, None, False)
+            if qsize != (T, HQ, d):
+                raise ValueError(f"q must be [{T}, HQ, {d}], got {tuple(qsize)}")
+            qs = _token_stride(q, "q")
+        _grouped(HQ, HKV, "k's")
+        qp = q.data_ptr()
+        if q_out is None:
+            q_out = _empty(qsize, dt, q.device, stream, torch)
+        qop = _whole(q_out, "q_out", dev, dt, qsize)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    shape = _shape_ref(N, T, HQ, HKV, d, code, 0, 0, qs, ks, vs)
+    _attn_launch("kda_cache_append_q8", torch, dev, stream, load().kda_cache_append_q8, qp,
+                 k.data_ptr(), v.data_ptr(), cup, lp, rp, qop, kop, ksp, vsp, ctypes.byref(cache),
+                 shape)
+    return q_out, k_out
+
+
 _step_bytes = {}  # by what the size depends on
 
 
@@ -1121,6 +1226,105 @@ def kda_attn_step(q, k_cache, v_cache, block_table, seq_lens, scale: float, out=
         left = max(left - (wp - base), 0)
     _attn_launch("kda_attn_step", torch, dev, stream, load().kda_attn_step_ws, q.data_ptr(),
                  ctypes.byref(cache), lp, scale, op, lsep, shape, wp, left)
+    return out, lse
+
+
+def kda_attn_step_q8_workspace_size(cache: kdaPagedCacheQ8_t, shape: kdaAttnShape_t) -> int:
+    """Bytes of scratch kda_attn_step_q8 needs with these sizes, on the current device."""
+    n = ctypes.c_size_t(0)
+    _check(load().kda_attn_step_q8_workspace_size(ctypes.byref(cache), ctypes.byref(shape),
+                                                  ctypes.byref(n)),
+           "kda_attn_step_q8_workspace_size")
+    return int(n.value)
+
+
+def kda_attn_step_shared_workspace_size(cache: kdaPagedCache_t, shape: kdaAttnShape_t) -> int:
+    """Bytes of scratch kda_attn_step_shared needs with these sizes, on the current device."""
+    n = ctypes.c_size_t(0)
+    _check(load().kda_attn_step_shared_workspace_size(ctypes.byref(cache), ctypes.byref(shape),
+                                                      ctypes.byref(n)),
+           "kda_attn_step_shared_workspace_size")
+    return int(n.value)
+
+
+def _step_scratch(kind, size_of, workspace, cache, shape, q, dev, code, N, HQ, HKV, d, stream,
+                  torch):
+    """(tensor to keep until the launch, address, bytes) of a step's scratch:
+    the caller's, or a fresh one from the pool of the stream the call runs on."""
+    if workspace is None:
+        key = (dev, code, N, HQ, HKV, d, cache.page_size, cache.max_pages, kind)
+        need = _step_bytes.get(key)
+        if need is None:
+            if len(_step_bytes) >= 4096:
+                _step_bytes.clear()
+            with torch.cuda.device(dev):
+                need = _step_bytes[key] = size_of(cache, shape._obj)
+        if not need:
+            return None, 0, 0
+        workspace = _empty(need + 256, torch.uint8, q.device, stream, torch, returned=False)
+    left = workspace.numel()
+    base = _whole(workspace, "workspace", dev, torch.uint8, (left,))
+    at = (base + 255) // 256 * 256
+    return workspace, at, max(left - (at - base), 0)
+
+
+def kda_attn_step_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale: float,
+                     out=None, lse=None, *, workspace=None, stream=None, out_f32: bool = False):
+    """One token of every sequence attends to its paged cache of 8-bit codes (C:
+    kda_attn_step_q8_ws).  Returns ``(out, lse)``.
+
+    q: [N, HQ, d] bf16/fp32; k_cache / v_cache: int8 [pages, HKV, page_size, d];
+    k_scale / v_scale: fp32 [pages, HKV, page_size].  The rest, scratch among it
+    (kda_attn_step_q8_workspace_size), as for kda_attn_step.
+    """
+    torch = _torch()
+    dev, dt, code, size = _lead(q, "q", torch)
+    N, HQ, d = size
+    qs = _token_stride(q, "q")
+    cache, HKV = _cache_q8(k_cache, v_cache, k_scale, v_scale, block_table, dev, N, d, torch)
+    _grouped(HQ, HKV, "the cache's")
+    lp = _whole(seq_lens, "seq_lens", dev, torch.int32, (N,))
+    lsep = None if lse is None else _whole(lse, "lse", dev, torch.float32, (N, HQ))
+    if stream is not None:
+        stream = _call_stream(stream, dev, torch)
+    out, op, f32 = _attn_out(q, size, dev, dt, out, out_f32, stream, torch)
+    shape = _shape_ref(N, N, HQ, HKV, d, code, 0, f32, qs, 0, 0)
+    kept, wp, left = _step_scratch("q8", kda_attn_step_q8_workspace_size, workspace, cache, shape,
+                                   q, dev, code, N, HQ, HKV, d, stream, torch)
+    _attn_launch("kda_attn_step_q8", torch, dev, stream, load().kda_attn_step_q8_ws, q.data_ptr(),
+                 ctypes.byref(cache), lp, scale, op, lsep, shape, wp, left)
+    return out, lse
+
+
+def kda_attn_step_shared(q, k_cache, v_cache, block_table, seq_lens, shared_pages, scale: float,
+                         out=None, lse=None, *, workspace=None, stream=None,
+                         out_f32: bool = False):
+    """kda_attn_step for sequences that have their first pages in common, which
+    are read once for all of them (C: kda_attn_step_shared_ws).  Returns
+    ``(out, lse)``.
+
+    ``shared_pages``: int32 [1] on the device: so many leading entries of
+    block_table are the same in the row of every sequence that has that many
+    pages' tokens or more.  The rest, scratch among it
+    (kda_attn_step_shared_workspace_size), and the result as for kda_attn_step.
+    """
+    torch = _torch()
+    dev, dt, code, size = _lead(q, "q", torch)
+    N, HQ, d = size
+    qs = _token_stride(q, "q")
+    cache, HKV = _paged_cache(k_cache, v_cache, block_table, dev, dt, torch.int32, N, d)
+    _grouped(HQ, HKV, "the cache's")
+    lp = _whole(seq_lens, "seq_lens", dev, torch.int32, (N,))
+    sp = _whole(shared_pages, "shared_pages", dev, torch.int32, (1,))
+    lsep = None if lse is None else _whole(lse, "lse", dev, torch.float32, (N, HQ))
+    if stream is not None:
+        stream = _call_stream(stream, dev, torch)
+    out, op, f32 = _attn_out(q, size, dev, dt, out, out_f32, stream, torch)
+    shape = _shape_ref(N, N, HQ, HKV, d, code, 0, f32, qs, 0, 0)
+    kept, wp, left = _step_scratch("shared", kda_attn_step_shared_workspace_size, workspace, cache,
+                                   shape, q, dev, code, N, HQ, HKV, d, stream, torch)
+    _attn_launch("kda_attn_step_shared", torch, dev, stream, load().kda_attn_step_shared_ws,
+                 q.data_ptr(), ctypes.byref(cache), lp, sp, scale, op, lsep, shape, wp, left)
     return out, lse
 
 

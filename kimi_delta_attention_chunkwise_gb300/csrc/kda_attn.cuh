@@ -37,6 +37,9 @@ struct AppendArgs {
     int32_t positions, rot, interleaved;
     void *q_out, *k_out;           // may be nullptr
     void *k_cache, *v_cache;
+    int32_t q8;                    // a cache of 8-bit codes, with scales [pages, HKV, page]
+    float *k_scale, *v_scale;
+    void *k_stored, *v_stored;     // what the codes stand for, [T, HKV, D]; may be nullptr
     const int32_t *block_table;
     int32_t num_pages, page_shift, max_pages;
     int32_t N, T, HQ, HKV, D, dtype;
@@ -48,6 +51,7 @@ struct AttnStepArgs {
     const void *q;
     int64_t q_stride;
     const void *k_cache, *v_cache;
+    const float *k_scale, *v_scale;  // [pages, HKV, page] (8-bit caches)
     const int32_t *block_table;
     int32_t num_pages, page_shift, max_pages;
     const int32_t *seq_lens;       // [N]
@@ -57,10 +61,19 @@ struct AttnStepArgs {
     int32_t N, HQ, HKV, G, D, dtype, out_f32;
     void *workspace;
     int *status;
+    // kda_attn_step_shared: the leading pages that the sequences share, and the
+    // states of every row over them, cut among at most `splits` CTAs
+    const int32_t *shared_pages;     // device [1]
+    void *prefix;
+    int32_t splits;
 };
 // Scratch of the step on the current device, for these sizes and any lengths.
 cudaError_t attn_step_workspace_bytes(const AttnStepArgs &a, size_t *bytes);
 cudaError_t launch_attn_step(const AttnStepArgs &a, cudaStream_t stream);
+cudaError_t attn_step_q8_workspace_bytes(const AttnStepArgs &a, size_t *bytes);
+cudaError_t launch_attn_step_q8(const AttnStepArgs &a, cudaStream_t stream);
+cudaError_t attn_step_shared_workspace_bytes(const AttnStepArgs &a, size_t *bytes);
+cudaError_t launch_attn_step_shared(const AttnStepArgs &a, cudaStream_t stream);
 
 // Device address of the status word on the current device (kda_api.cu).
 int *device_status_word();

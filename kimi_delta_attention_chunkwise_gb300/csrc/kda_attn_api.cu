@@ -74,6 +74,15 @@ kdaStatus_t check_cache(const kdaPagedCache_t *c, int32_t *page_shift) {
     return KDA_SUCCESS;
 }
 
+// A cache of 8-bit codes as one of any type, and its scales.
+kdaStatus_t check_cache_q8(const kdaPagedCacheQ8_t *c, kdaPagedCache_t &same) {
+    if (!c) return KDA_ERR_INVALID_ARG;
+    if (c->num_pages > 0 && (!c->k_scale || !c->v_scale)) return KDA_ERR_INVALID_ARG;
+    if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)) return KDA_ERR_INVALID_ARG;
+    same = {c->k, c->v, c->block_table, c->num_pages, c->page_size, c->max_pages};
+    return KDA_SUCCESS;
+}
+
 // What the step's sizes say, before its pointers.
 kdaStatus_t step_sizes(const kdaPagedCache_t *cache, const kdaAttnShape_t *shape, AttnStepArgs &a) {
     kdaStatus_t st = check_attn_shape(shape);
@@ -88,6 +97,10 @@ kdaStatus_t step_sizes(const kdaPagedCache_t *cache, const kdaAttnShape_t *shape
     a.out_f32 = shape->dtype == KDA_DTYPE_F32 ? 1 : shape->out_f32;
     a.workspace = nullptr;
     a.status = nullptr;
+    a.k_scale = a.v_scale = nullptr;
+    a.shared_pages = nullptr;
+    a.prefix = nullptr;
+    a.splits = 0;
     return KDA_SUCCESS;
 }
 
@@ -103,6 +116,129 @@ kdaStatus_t plan_attn_step(const void *q, const kdaPagedCache_t *cache, const in
     a.q_stride = token_stride(shape->q_stride, shape->num_heads, shape->head_dim);
     a.k_cache = cache->k; a.v_cache = cache->v; a.block_table = cache->block_table;
     a.seq_lens = seq_lens; a.scale = scale; a.out = out; a.lse = lse;
+    return KDA_SUCCESS;
+}
+
+// The arguments of an append (nothing is written to `a` that a call without
+// tokens would need).
+kdaStatus_t plan_append(const void *q, const void *k, const void *v, const int32_t *cu_seqlens,
+                        const int32_t *cache_lens, const kdaRope_t *rope, void *q_out, void *k_out,
+                        const kdaPagedCache_t *cache, const kdaAttnShape_t *shape, AppendArgs &a) {
+    kdaStatus_t st = check_attn_shape(shape);
+    if (st != KDA_SUCCESS) return st;
+    int32_t page_shift = 0;
+    st = check_cache(cache, &page_shift);
+    if (st != KDA_SUCCESS) return st;
+    if (!cu_seqlens && shape->num_seqs != 1 && shape->num_seqs != shape->total_tokens)
+        return KDA_ERR_INVALID_ARG;
+    if (!cache_lens || !aligned(cache_lens, 4) || !aligned(cu_seqlens, 4))
+        return KDA_ERR_INVALID_ARG;
+    if (!q && q_out) return KDA_ERR_INVALID_ARG;
+    if (q && !q_out) return KDA_ERR_INVALID_ARG;
+    if (shape->total_tokens > 0 && (!k || !v)) return KDA_ERR_INVALID_ARG;
+    const void *vec[] = {q, k, v, q_out, k_out};
+    for (const void *p : vec)
+        if (!aligned(p, 16)) return KDA_ERR_INVALID_ARG;
+    a.q_stride = token_stride(shape->q_stride, shape->num_heads, shape->head_dim);
+    a.k_stride = token_stride(shape->k_stride, shape->num_kv_heads, shape->head_dim);
+    a.v_stride = token_stride(shape->v_stride, shape->num_kv_heads, shape->head_dim);
+    // in place: a row's output must be the row itself
+    if (q && q_out == q && a.q_stride != (int64_t)shape->num_heads * shape->head_dim)
+        return KDA_ERR_INVALID_ARG;
+    if (k_out && k_out == k && a.k_stride != (int64_t)shape->num_kv_heads * shape->head_dim)
+        return KDA_ERR_INVALID_ARG;
+    if (rope) {
+        if (!rope->table || !aligned(rope->table, 16) || rope->num_positions < 0 ||
+            (rope->interleaved != 0 && rope->interleaved != 1) || rope->rot_dim < 1)
+            return KDA_ERR_INVALID_ARG;
+        if (rope->rot_dim % 16 != 0 || rope->rot_dim > shape->head_dim) return KDA_ERR_UNSUPPORTED;
+    }
+    if (shape->total_tokens == 0) return KDA_SUCCESS;
+    a.q = q; a.k = k; a.v = v;
+    a.cu_seqlens = cu_seqlens;
+    a.one_each = !cu_seqlens && shape->num_seqs == shape->total_tokens;
+    a.cache_lens = cache_lens;
+    a.rope = rope ? rope->table : nullptr;
+    a.positions = rope ? rope->num_positions : 0;
+    a.rot = rope ? rope->rot_dim : 0;
+    a.interleaved = rope ? rope->interleaved : 0;
+    a.q_out = q_out; a.k_out = k_out;
+    a.k_cache = cache->k; a.v_cache = cache->v; a.block_table = cache->block_table;
+    a.num_pages = cache->num_pages; a.page_shift = page_shift; a.max_pages = cache->max_pages;
+    a.N = shape->num_seqs; a.T = shape->total_tokens;
+    a.HQ = q ? shape->num_heads : 0; a.HKV = shape->num_kv_heads; a.D = shape->head_dim;
+    a.dtype = shape->dtype;
+    a.q8 = 0;
+    a.k_scale = a.v_scale = nullptr;
+    a.k_stored = a.v_stored = nullptr;
+    return KDA_SUCCESS;
+}
+
+kdaStatus_t run_append(AppendArgs &a, cudaStream_t stream) {
+    a.status = device_status_word();
+    if (!a.status) return cuda_status(cudaErrorUnknown);
+    return cuda_status(launch_cache_append(a, stream));
+}
+
+// A step's scratch and launch, by kind.
+using StepBytes = cudaError_t (*)(const AttnStepArgs &, size_t *);
+using StepLaunch = cudaError_t (*)(const AttnStepArgs &, cudaStream_t);
+
+// With the caller's scratch.
+kdaStatus_t run_step_ws(AttnStepArgs &a, StepBytes bytes, StepLaunch launch, void *workspace,
+                        size_t workspace_bytes, cudaStream_t stream) {
+    if (!aligned(workspace, 256)) return KDA_ERR_INVALID_ARG;
+    size_t need = 0;
+    const kdaStatus_t st = cuda_status(bytes(a, &need));
+    if (st != KDA_SUCCESS) return st;
+    if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_INVALID_ARG;
+    a.workspace = workspace;
+    a.status = device_status_word();
+    if (!a.status) return cuda_status(cudaErrorUnknown);
+    return cuda_status(launch(a, stream));
+}
+
+// With scratch taken on the stream.
+kdaStatus_t run_step(AttnStepArgs &a, StepBytes bytes, StepLaunch launch, cudaStream_t stream) {
+    size_t need = 0;
+    const kdaStatus_t st = cuda_status(bytes(a, &need));
+    if (st != KDA_SUCCESS) return st;
+    a.status = device_status_word();
+    if (!a.status) return cuda_status(cudaErrorUnknown);
+    if (need == 0) return cuda_status(launch(a, stream));
+    void *ws = nullptr;
+    if (cudaMallocAsync(&ws, need, stream) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return KDA_ERR_CUDA;
+    }
+    a.workspace = ws;
+    const cudaError_t e = launch(a, stream);
+    const cudaError_t f = cudaFreeAsync(ws, stream);
+    return cuda_status(e != cudaSuccess ? e : f);
+}
+
+// kda_attn_step_q8's arguments
+kdaStatus_t plan_step_q8(const void *q, const kdaPagedCacheQ8_t *cache, const int32_t *seq_lens,
+                         float scale, void *out, float *lse, const kdaAttnShape_t *shape,
+                         AttnStepArgs &a) {
+    kdaPagedCache_t same;
+    kdaStatus_t st = check_cache_q8(cache, same);
+    if (st != KDA_SUCCESS) return st;
+    st = plan_attn_step(q, &same, seq_lens, scale, out, lse, shape, a);
+    if (st != KDA_SUCCESS) return st;
+    a.k_scale = cache->k_scale;
+    a.v_scale = cache->v_scale;
+    return KDA_SUCCESS;
+}
+
+// kda_attn_step_shared's arguments
+kdaStatus_t plan_step_shared(const void *q, const kdaPagedCache_t *cache, const int32_t *seq_lens,
+                             const int32_t *shared_pages, float scale, void *out, float *lse,
+                             const kdaAttnShape_t *shape, AttnStepArgs &a) {
+    const kdaStatus_t st = plan_attn_step(q, cache, seq_lens, scale, out, lse, shape, a);
+    if (st != KDA_SUCCESS) return st;
+    if (!shared_pages || !aligned(shared_pages, 4)) return KDA_ERR_INVALID_ARG;
+    a.shared_pages = shared_pages;
     return KDA_SUCCESS;
 }
 
@@ -170,54 +306,35 @@ kdaStatus_t kda_cache_append(const void *q, const void *k, const void *v,
                              const kdaRope_t *rope, void *q_out, void *k_out,
                              const kdaPagedCache_t *cache, const kdaAttnShape_t *shape,
                              cudaStream_t stream) {
-    kdaStatus_t st = check_attn_shape(shape);
-    if (st != KDA_SUCCESS) return st;
-    int32_t page_shift = 0;
-    st = check_cache(cache, &page_shift);
-    if (st != KDA_SUCCESS) return st;
-    if (!cu_seqlens && shape->num_seqs != 1 && shape->num_seqs != shape->total_tokens)
-        return KDA_ERR_INVALID_ARG;
-    if (!cache_lens || !aligned(cache_lens, 4) || !aligned(cu_seqlens, 4))
-        return KDA_ERR_INVALID_ARG;
-    if (!q && q_out) return KDA_ERR_INVALID_ARG;
-    if (q && !q_out) return KDA_ERR_INVALID_ARG;
-    if (shape->total_tokens > 0 && (!k || !v)) return KDA_ERR_INVALID_ARG;
-    const void *vec[] = {q, k, v, q_out, k_out};
-    for (const void *p : vec)
-        if (!aligned(p, 16)) return KDA_ERR_INVALID_ARG;
     AppendArgs a;
-    a.q_stride = token_stride(shape->q_stride, shape->num_heads, shape->head_dim);
-    a.k_stride = token_stride(shape->k_stride, shape->num_kv_heads, shape->head_dim);
-    a.v_stride = token_stride(shape->v_stride, shape->num_kv_heads, shape->head_dim);
-    // in place: a row's output must be the row itself
-    if (q && q_out == q && a.q_stride != (int64_t)shape->num_heads * shape->head_dim)
+    const kdaStatus_t st =
+        plan_append(q, k, v, cu_seqlens, cache_lens, rope, q_out, k_out, cache, shape, a);
+    if (st != KDA_SUCCESS || shape->total_tokens == 0) return st;
+    return run_append(a, stream);
+}
+
+kdaStatus_t kda_cache_append_q8(const void *q, const void *k, const void *v,
+                                const int32_t *cu_seqlens, const int32_t *cache_lens,
+                                const kdaRope_t *rope, void *q_out, void *k_out, void *k_stored,
+                                void *v_stored, const kdaPagedCacheQ8_t *cache,
+                                const kdaAttnShape_t *shape, cudaStream_t stream) {
+    kdaPagedCache_t same;
+    kdaStatus_t st = check_cache_q8(cache, same);
+    if (st != KDA_SUCCESS) return st;
+    AppendArgs a;
+    st = plan_append(q, k, v, cu_seqlens, cache_lens, rope, q_out, k_out, &same, shape, a);
+    if (st != KDA_SUCCESS) return st;
+    // what the codes stand for lies in tensors of its own
+    const void *others[] = {q, k, v, q_out, k_out};
+    for (const void *p : others)
+        if ((k_stored && k_stored == p) || (v_stored && v_stored == p)) return KDA_ERR_INVALID_ARG;
+    if ((k_stored && k_stored == v_stored) || !aligned(k_stored, 16) || !aligned(v_stored, 16))
         return KDA_ERR_INVALID_ARG;
-    if (k_out && k_out == k && a.k_stride != (int64_t)shape->num_kv_heads * shape->head_dim)
-        return KDA_ERR_INVALID_ARG;
-    if (rope) {
-        if (!rope->table || !aligned(rope->table, 16) || rope->num_positions < 0 ||
-            (rope->interleaved != 0 && rope->interleaved != 1) || rope->rot_dim < 1)
-            return KDA_ERR_INVALID_ARG;
-        if (rope->rot_dim % 16 != 0 || rope->rot_dim > shape->head_dim) return KDA_ERR_UNSUPPORTED;
-    }
     if (shape->total_tokens == 0) return KDA_SUCCESS;
-    a.q = q; a.k = k; a.v = v;
-    a.cu_seqlens = cu_seqlens;
-    a.one_each = !cu_seqlens && shape->num_seqs == shape->total_tokens;
-    a.cache_lens = cache_lens;
-    a.rope = rope ? rope->table : nullptr;
-    a.positions = rope ? rope->num_positions : 0;
-    a.rot = rope ? rope->rot_dim : 0;
-    a.interleaved = rope ? rope->interleaved : 0;
-    a.q_out = q_out; a.k_out = k_out;
-    a.k_cache = cache->k; a.v_cache = cache->v; a.block_table = cache->block_table;
-    a.num_pages = cache->num_pages; a.page_shift = page_shift; a.max_pages = cache->max_pages;
-    a.N = shape->num_seqs; a.T = shape->total_tokens;
-    a.HQ = q ? shape->num_heads : 0; a.HKV = shape->num_kv_heads; a.D = shape->head_dim;
-    a.dtype = shape->dtype;
-    a.status = device_status_word();
-    if (!a.status) return cuda_status(cudaErrorUnknown);
-    return cuda_status(launch_cache_append(a, stream));
+    a.q8 = 1;
+    a.k_scale = cache->k_scale; a.v_scale = cache->v_scale;
+    a.k_stored = k_stored; a.v_stored = v_stored;
+    return run_append(a, stream);
 }
 
 kdaStatus_t kda_attn_step_workspace_size(const kdaPagedCache_t *cache, const kdaAttnShape_t *shape,
@@ -233,40 +350,84 @@ kdaStatus_t kda_attn_step_ws(const void *q, const kdaPagedCache_t *cache, const 
                              float scale, void *out, float *lse, const kdaAttnShape_t *shape,
                              void *workspace, size_t workspace_bytes, cudaStream_t stream) {
     AttnStepArgs a;
-    kdaStatus_t st = plan_attn_step(q, cache, seq_lens, scale, out, lse, shape, a);
+    const kdaStatus_t st = plan_attn_step(q, cache, seq_lens, scale, out, lse, shape, a);
     if (st != KDA_SUCCESS) return st;
-    if (!aligned(workspace, 256)) return KDA_ERR_INVALID_ARG;
-    size_t need = 0;
-    st = cuda_status(attn_step_workspace_bytes(a, &need));
-    if (st != KDA_SUCCESS) return st;
-    if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_INVALID_ARG;
-    a.workspace = workspace;
-    a.status = device_status_word();
-    if (!a.status) return cuda_status(cudaErrorUnknown);
-    return cuda_status(launch_attn_step(a, stream));
+    return run_step_ws(a, attn_step_workspace_bytes, launch_attn_step, workspace, workspace_bytes,
+                       stream);
 }
 
 kdaStatus_t kda_attn_step(const void *q, const kdaPagedCache_t *cache, const int32_t *seq_lens,
                           float scale, void *out, float *lse, const kdaAttnShape_t *shape,
                           cudaStream_t stream) {
     AttnStepArgs a;
-    kdaStatus_t st = plan_attn_step(q, cache, seq_lens, scale, out, lse, shape, a);
+    const kdaStatus_t st = plan_attn_step(q, cache, seq_lens, scale, out, lse, shape, a);
     if (st != KDA_SUCCESS) return st;
-    size_t need = 0;
-    st = cuda_status(attn_step_workspace_bytes(a, &need));
+    return run_step(a, attn_step_workspace_bytes, launch_attn_step, stream);
+}
+
+kdaStatus_t kda_attn_step_q8_workspace_size(const kdaPagedCacheQ8_t *cache,
+                                            const kdaAttnShape_t *shape, size_t *bytes) {
+    if (!bytes) return KDA_ERR_INVALID_ARG;
+    kdaPagedCache_t same;
+    kdaStatus_t st = check_cache_q8(cache, same);
     if (st != KDA_SUCCESS) return st;
-    a.status = device_status_word();
-    if (!a.status) return cuda_status(cudaErrorUnknown);
-    if (need == 0) return cuda_status(launch_attn_step(a, stream));
-    void *ws = nullptr;
-    if (cudaMallocAsync(&ws, need, stream) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return KDA_ERR_CUDA;
-    }
-    a.workspace = ws;
-    const cudaError_t e = launch_attn_step(a, stream);
-    const cudaError_t f = cudaFreeAsync(ws, stream);
-    return cuda_status(e != cudaSuccess ? e : f);
+    AttnStepArgs a;
+    st = step_sizes(&same, shape, a);
+    if (st != KDA_SUCCESS) return st;
+    return cuda_status(attn_step_q8_workspace_bytes(a, bytes));
+}
+
+kdaStatus_t kda_attn_step_q8_ws(const void *q, const kdaPagedCacheQ8_t *cache,
+                                const int32_t *seq_lens, float scale, void *out, float *lse,
+                                const kdaAttnShape_t *shape, void *workspace,
+                                size_t workspace_bytes, cudaStream_t stream) {
+    AttnStepArgs a;
+    const kdaStatus_t st = plan_step_q8(q, cache, seq_lens, scale, out, lse, shape, a);
+    if (st != KDA_SUCCESS) return st;
+    return run_step_ws(a, attn_step_q8_workspace_bytes, launch_attn_step_q8, workspace,
+                       workspace_bytes, stream);
+}
+
+kdaStatus_t kda_attn_step_q8(const void *q, const kdaPagedCacheQ8_t *cache,
+                             const int32_t *seq_lens, float scale, void *out, float *lse,
+                             const kdaAttnShape_t *shape, cudaStream_t stream) {
+    AttnStepArgs a;
+    const kdaStatus_t st = plan_step_q8(q, cache, seq_lens, scale, out, lse, shape, a);
+    if (st != KDA_SUCCESS) return st;
+    return run_step(a, attn_step_q8_workspace_bytes, launch_attn_step_q8, stream);
+}
+
+kdaStatus_t kda_attn_step_shared_workspace_size(const kdaPagedCache_t *cache,
+                                                const kdaAttnShape_t *shape, size_t *bytes) {
+    if (!bytes) return KDA_ERR_INVALID_ARG;
+    AttnStepArgs a;
+    const kdaStatus_t st = step_sizes(cache, shape, a);
+    if (st != KDA_SUCCESS) return st;
+    return cuda_status(attn_step_shared_workspace_bytes(a, bytes));
+}
+
+kdaStatus_t kda_attn_step_shared_ws(const void *q, const kdaPagedCache_t *cache,
+                                    const int32_t *seq_lens, const int32_t *shared_pages,
+                                    float scale, void *out, float *lse,
+                                    const kdaAttnShape_t *shape, void *workspace,
+                                    size_t workspace_bytes, cudaStream_t stream) {
+    AttnStepArgs a;
+    const kdaStatus_t st =
+        plan_step_shared(q, cache, seq_lens, shared_pages, scale, out, lse, shape, a);
+    if (st != KDA_SUCCESS) return st;
+    return run_step_ws(a, attn_step_shared_workspace_bytes, launch_attn_step_shared, workspace,
+                       workspace_bytes, stream);
+}
+
+kdaStatus_t kda_attn_step_shared(const void *q, const kdaPagedCache_t *cache,
+                                 const int32_t *seq_lens, const int32_t *shared_pages, float scale,
+                                 void *out, float *lse, const kdaAttnShape_t *shape,
+                                 cudaStream_t stream) {
+    AttnStepArgs a;
+    const kdaStatus_t st =
+        plan_step_shared(q, cache, seq_lens, shared_pages, scale, out, lse, shape, a);
+    if (st != KDA_SUCCESS) return st;
+    return run_step(a, attn_step_shared_workspace_bytes, launch_attn_step_shared, stream);
 }
 
 }  // extern "C"

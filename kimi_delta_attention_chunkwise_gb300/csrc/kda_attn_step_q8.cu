@@ -1,0 +1,58 @@
+// kda_attn_step_q8.cu -- kda_attn_step_q8: one token of every sequence over a
+// paged cache of 8-bit codes (the kernels: kda_attn_step.cuh).
+//
+//     z_j = scale ks_j <q, kcode_j>,  o = sum_j e^{z_j} vs_j vcode_j / sum_j e^{z_j}
+//
+// A token's key and value are 2 D bytes of codes and 8 of scales to a key-value
+// head, half of what a bf16 cache holds.  The scales stay outside the products,
+// which are exact products of codes in fp32 (bf16 operands hold codes exactly).
+#include "kda_attn_step.cuh"
+
+namespace kda {
+namespace {
+
+using Bf16 = __nv_bfloat16;
+
+// The core of a problem, as a call of f(Core{}).
+template <class F>
+auto with_core_q8(int32_t D, int32_t G, int32_t dtype, F f) {
+    if (dtype == KDA_DTYPE_BF16) {
+        switch (D) {
+            case 16: return f(SimtCore<Bf16, 16, int8_t>{});
+            case 32: return f(SimtCore<Bf16, 32, int8_t>{});
+            case 64:
+                if (G <= 4) return f(MmaCore<64, 1, true, int8_t>{});
+                if (G <= 8) return f(MmaCore<64, 1, false, int8_t>{});
+                return f(MmaCore<64, 2, false, int8_t>{});
+            default:
+                if (G <= 4) return f(MmaCore<128, 1, true, int8_t>{});
+                if (G <= 8) return f(MmaCore<128, 1, false, int8_t>{});
+                return f(MmaCore<128, 2, false, int8_t>{});
+        }
+    }
+    switch (D) {
+        case 16: return f(SimtCore<float, 16, int8_t>{});
+        case 32: return f(SimtCore<float, 32, int8_t>{});
+        case 64: return f(SimtCore<float, 64, int8_t>{});
+        default: return f(SimtCore<float, 128, int8_t>{});
+    }
+}
+
+}  // namespace
+
+cudaError_t attn_step_q8_workspace_bytes(const AttnStepArgs &a, size_t *bytes) {
+    const int sms = device_sms();
+    if (!sms) return cudaErrorUnknown;
+    *bytes = with_core_q8(a.D, a.G, a.dtype, [&](auto core) -> size_t {
+        return part_bytes<decltype(core)>(a, sms);
+    });
+    return cudaSuccess;
+}
+
+cudaError_t launch_attn_step_q8(const AttnStepArgs &a, cudaStream_t stream) {
+    return with_core_q8(a.D, a.G, a.dtype, [&](auto core) -> cudaError_t {
+        return launch_core<decltype(core)>(a, stream);
+    });
+}
+
+}  // namespace kda

@@ -14,6 +14,13 @@
 // one thread per token looks its position and page up (two dependent reads)
 // while the others' first vectors are already on their way, then all threads
 // walk the CTA's units (heads of q, then k, then v), one unit ahead.
+//
+// A cache of 8-bit codes (kda_cache_append_q8) holds a row of a head as
+//     code = rint(x * (127 / top)),   scale = top / 127,   top = max |x|
+// of the rotated fp32 row, with each of these operations rounded to fp32: what
+// the codes stand for is off by half a scale at most (and fp32's rounding).
+// top is the maximum over the row's neighbouring lanes, as integers, in which
+// infinities and NaN are above every number.
 #include <cstdint>
 #include <cuda_bf16.h>
 
@@ -125,8 +132,43 @@ struct Unit {
     bool halves;               // the two vectors pair up
 };
 
-template <typename T, int D, int TOK, int kThreads>
-__global__ void __launch_bounds__(kThreads, TOK == 1 ? 1 : 9) cache_append_kernel(const AppendArgs a) {
+// A row's codes and what they stand for.
+constexpr float kSmallest = 0x1p-100f;  // (below it, 127 / top might not be a number)
+struct Coder {
+    float scale, turn;
+    // `top`: the bits of the row's largest magnitude
+    __device__ explicit Coder(uint32_t top) {
+        const float t = __uint_as_float(top);
+        scale = __fdiv_rn(t, 127.f);
+        turn = __fdiv_rn(127.f, t);
+        if (top >= 0x7F800000u) {  // an infinity or a NaN: no code stands for it
+            scale = __uint_as_float(0x7FC00000u);
+            turn = 0.f;
+        } else if (t < kSmallest) {
+            scale = turn = 0.f;
+        }
+    }
+    // (x is finite where turn is not 0)
+    __device__ float code(float x) const { return turn == 0.f ? 0.f : rintf(__fmul_rn(x, turn)); }
+};
+template <int V>
+__device__ __forceinline__ void store_codes(int8_t *to, const float (&c)[V]) {
+    uint32_t w[V / 4];
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+        // a whole number from -127 to 127 above 1.5 * 2^23 is the sum's low byte
+        const float *x = c + 4 * i;
+        uint32_t b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = __float_as_uint(x[j] + 12582912.f);
+        w[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    }
+    if constexpr (V == 8) *reinterpret_cast<uint2 *>(to) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t *>(to) = w[0];
+}
+
+template <typename T, int D, int TOK, int kThreads, bool Q8>
+__global__ void __launch_bounds__(kThreads, TOK == 1 ? 1 : Q8 ? 6 : 9) cache_append_kernel(const AppendArgs a) {
     constexpr int V = Row<T>::V;
     constexpr int UNITS = D / V / 2;  // units per head row
     __shared__ Place place[TOK];
@@ -159,7 +201,101 @@ __global__ void __launch_bounds__(kThreads, TOK == 1 ? 1 : 9) cache_append_kerne
         x0 = *reinterpret_cast<const uint4 *>(src + w.c0);
         x1 = *reinterpret_cast<const uint4 *>(src + w.c1);
     };
+    // turns the pairs of a unit whose first channel is below rot_dim
+    auto rotate_unit = [&](const Unit &w, int32_t pos, float (&f0)[V], float (&f1)[V]) {
+        const float *cs = a.rope + (int64_t)pos * a.rot;
+        float c[V], s[V];
+        // the angles of the unit's V pairs: halves: pairs c0 .. c0 + V - 1;
+        // interleaved: c0 / 2 .. (both vectors lie inside rot_dim, a
+        // multiple of 2 V)
+        const float *ca = cs + (w.halves ? w.c0 : w.c0 / 2), *sa = ca + half;
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+            const float4 cv = __ldg(reinterpret_cast<const float4 *>(ca + j));
+            const float4 sv = __ldg(reinterpret_cast<const float4 *>(sa + j));
+            c[j] = cv.x; c[j + 1] = cv.y; c[j + 2] = cv.z; c[j + 3] = cv.w;
+            s[j] = sv.x; s[j + 1] = sv.y; s[j + 2] = sv.z; s[j + 3] = sv.w;
+        }
+        if (w.halves) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) turn(f0[j], f1[j], c[j], s[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) {
+                turn(f0[2 * j], f0[2 * j + 1], c[j], s[j]);
+                turn(f1[2 * j], f1[2 * j + 1], c[V / 2 + j], s[V / 2 + j]);
+            }
+        }
+    };
+    // Q8: the unit's part of its row to the cache's codes (called by whole warps)
+    auto finish_q8 = [&](int32_t i, uint4 x0, uint4 x1) {
+        const bool here = i < total;
+        const Unit w = unit_of(here ? i : 0);
+        const Place p = place[w.tk];
+        const bool is_q = w.head < a.HQ, is_k = !is_q && w.head < a.HQ + a.HKV;
+        const int32_t kh = w.head - a.HQ - (is_k || is_q ? 0 : a.HKV);
+        const int64_t t = t0 + w.tk;
+        float f0[V], f1[V];
+        Row<T>::unpack(x0, f0);
+        Row<T>::unpack(x1, f1);
+        const bool live = here && p.pos >= 0;
+        const bool turned = live && (is_q || is_k) && w.c0 < a.rot;
+        if (turned) rotate_unit(w, p.pos, f0, f1);
+        auto put = [&](T *row, const float (&y0)[V], const float (&y1)[V]) {
+            *reinterpret_cast<uint4 *>(row + w.c0) = Row<T>::pack(y0);
+            *reinterpret_cast<uint4 *>(row + w.c1) = Row<T>::pack(y1);
+        };
+        // (what is not turned is copied: packing it again would change NaN's bits)
+        auto put_turned = [&](T *row) {
+            if (turned) {
+                put(row, f0, f1);
+            } else {
+                *reinterpret_cast<uint4 *>(row + w.c0) = x0;
+                *reinterpret_cast<uint4 *>(row + w.c1) = x1;
+            }
+        };
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            top = max(top, max(__float_as_uint(f0[j]) & 0x7FFFFFFFu, __float_as_uint(f1[j]) & 0x7FFFFFFFu));
+#pragma unroll
+        for (int o = 1; o < UNITS; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (!live) return;
+        if (is_q) {
+            put_turned(static_cast<T *>(a.q_out) + (t * a.HQ + w.head) * D);
+            return;
+        }
+        const Coder coder(top);
+        float c0[V], c1[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            c0[j] = coder.code(f0[j]);
+            c1[j] = coder.code(f1[j]);
+        }
+        if (p.page >= 0) {
+            const int64_t row = p.page + ((int64_t)kh << a.page_shift);
+            int8_t *to = static_cast<int8_t *>(is_k ? a.k_cache : a.v_cache) + row * D;
+            store_codes<V>(to + w.c0, c0);
+            store_codes<V>(to + w.c1, c1);
+            if (i % UNITS == 0) (is_k ? a.k_scale : a.v_scale)[row] = coder.scale;
+        }
+        const int64_t out = (t * a.HKV + kh) * D;
+        if (is_k && a.k_out) put_turned(static_cast<T *>(a.k_out) + out);
+        T *stored = static_cast<T *>(is_k ? a.k_stored : a.v_stored);
+        if (stored) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                c0[j] = __fmul_rn(c0[j], coder.scale);
+                c1[j] = __fmul_rn(c1[j], coder.scale);
+            }
+            put(stored + out, c0, c1);
+        }
+    };
     auto finish = [&](int32_t i, uint4 x0, uint4 x1) {
+        if constexpr (Q8) {
+            finish_q8(i, x0, x1);
+            return;
+        }
         const Unit w = unit_of(i);
         const Place p = place[w.tk];
         if (p.pos < 0) return;
@@ -178,31 +314,10 @@ __global__ void __launch_bounds__(kThreads, TOK == 1 ? 1 : 9) cache_append_kerne
             rotate = rotate && is_k;
         }
         if (rotate) {
-            const float *cs = a.rope + (int64_t)p.pos * a.rot;
-            float f0[V], f1[V], c[V], s[V];
+            float f0[V], f1[V];
             Row<T>::unpack(x0, f0);
             Row<T>::unpack(x1, f1);
-            // the angles of the unit's V pairs: halves: pairs c0 .. c0 + V - 1;
-            // interleaved: c0 / 2 .. (both vectors lie inside rot_dim, a
-            // multiple of 2 V)
-            const float *ca = cs + (w.halves ? w.c0 : w.c0 / 2), *sa = ca + half;
-#pragma unroll
-            for (int j = 0; j < V; j += 4) {
-                const float4 cv = __ldg(reinterpret_cast<const float4 *>(ca + j));
-                const float4 sv = __ldg(reinterpret_cast<const float4 *>(sa + j));
-                c[j] = cv.x; c[j + 1] = cv.y; c[j + 2] = cv.z; c[j + 3] = cv.w;
-                s[j] = sv.x; s[j + 1] = sv.y; s[j + 2] = sv.z; s[j + 3] = sv.w;
-            }
-            if (w.halves) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) turn(f0[j], f1[j], c[j], s[j]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < V / 2; ++j) {
-                    turn(f0[2 * j], f0[2 * j + 1], c[j], s[j]);
-                    turn(f1[2 * j], f1[2 * j + 1], c[V / 2 + j], s[V / 2 + j]);
-                }
-            }
+            rotate_unit(w, p.pos, f0, f1);
             x0 = Row<T>::pack(f0);
             x1 = Row<T>::pack(f1);
         }
@@ -220,40 +335,55 @@ __global__ void __launch_bounds__(kThreads, TOK == 1 ? 1 : 9) cache_append_kerne
     if ((int32_t)threadIdx.x < total) load(threadIdx.x, x0, x1);
     if (threadIdx.x < TOK) place[threadIdx.x] = find_place(a, t0 + threadIdx.x);
     __syncthreads();
-    for (int32_t i = threadIdx.x; i < total; i += kThreads) {
-        if (i + kThreads < total) load(i + kThreads, y0, y1);
-        finish(i, x0, x1);
-        x0 = y0;
-        x1 = y1;
+    if constexpr (Q8) {
+        // whole warps: a row's lanes look for its maximum together
+        for (int32_t i = threadIdx.x; i - (int32_t)(threadIdx.x & 31) < total; i += kThreads) {
+            if (i + kThreads < total) load(i + kThreads, y0, y1);
+            finish(i, x0, x1);
+            x0 = y0;
+            x1 = y1;
+        }
+    } else {
+        for (int32_t i = threadIdx.x; i < total; i += kThreads) {
+            if (i + kThreads < total) load(i + kThreads, y0, y1);
+            finish(i, x0, x1);
+            x0 = y0;
+            x1 = y1;
+        }
     }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool Q8>
 cudaError_t launch_t(const AppendArgs &a, cudaStream_t stream) {
     if (a.T <= kFewTokens) {
-        cache_append_kernel<T, D, 1, 256><<<(unsigned)a.T, 256, 0, stream>>>(a);
+        cache_append_kernel<T, D, 1, 256, Q8><<<(unsigned)a.T, 256, 0, stream>>>(a);
     } else {
-        cache_append_kernel<T, D, 2, 128><<<(unsigned)(a.T / 2 + a.T % 2), 128, 0, stream>>>(a);
+        cache_append_kernel<T, D, 2, 128, Q8><<<(unsigned)(a.T / 2 + a.T % 2), 128, 0, stream>>>(a);
     }
     return cudaGetLastError();
 }
 
-template <typename T>
+template <typename T, bool Q8>
 cudaError_t launch_d(const AppendArgs &a, cudaStream_t stream) {
     switch (a.D) {
-        case 16: return launch_t<T, 16>(a, stream);
-        case 32: return launch_t<T, 32>(a, stream);
-        case 64: return launch_t<T, 64>(a, stream);
-        case 128: return launch_t<T, 128>(a, stream);
+        case 16: return launch_t<T, 16, Q8>(a, stream);
+        case 32: return launch_t<T, 32, Q8>(a, stream);
+        case 64: return launch_t<T, 64, Q8>(a, stream);
+        case 128: return launch_t<T, 128, Q8>(a, stream);
     }
     return cudaErrorInvalidValue;
+}
+
+template <bool Q8>
+cudaError_t launch_q(const AppendArgs &a, cudaStream_t stream) {
+    if (a.dtype == KDA_DTYPE_BF16) return launch_d<__nv_bfloat16, Q8>(a, stream);
+    return launch_d<float, Q8>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_append(const AppendArgs &a, cudaStream_t stream) {
-    if (a.dtype == KDA_DTYPE_BF16) return launch_d<__nv_bfloat16>(a, stream);
-    return launch_d<float>(a, stream);
+    return a.q8 ? launch_q<true>(a, stream) : launch_q<false>(a, stream);
 }
 
 }  // namespace kda
