@@ -61,11 +61,12 @@ struct AttnStepArgs {
     int32_t N, HQ, HKV, G, D, dtype, out_f32;
     void *workspace;
     int *status;
-    // kda_attn_step_shared: the leading pages that the sequences share, and the
-    // states of every row over them, cut among at most `splits` CTAs
+    // kda_attn_step_shared: the leading pages that the sequences share, the states
+    // of every row over them in at most `splits` pieces, and how their work is
+    // cut: blocks of prefix_rows rows, prefix_grid CTAs
     const int32_t *shared_pages;     // device [1]
     void *prefix;
-    int32_t splits;
+    int32_t splits, prefix_rows, prefix_grid;
 };
 // Scratch of the step on the current device, for these sizes and any lengths.
 cudaError_t attn_step_workspace_bytes(const AttnStepArgs &a, size_t *bytes);
@@ -74,6 +75,11 @@ cudaError_t attn_step_q8_workspace_bytes(const AttnStepArgs &a, size_t *bytes);
 cudaError_t launch_attn_step_q8(const AttnStepArgs &a, cudaStream_t stream);
 cudaError_t attn_step_shared_workspace_bytes(const AttnStepArgs &a, size_t *bytes);
 cudaError_t launch_attn_step_shared(const AttnStepArgs &a, cudaStream_t stream);
+
+// tcgen05 engine of the shared tokens (kda_attn_prefix_tc.cu): bf16, D = 64 or 128.
+// Rows to a block, by the number of sequences.
+int32_t prefix_tc_rows(const AttnStepArgs &a);
+cudaError_t launch_prefix_tc(const AttnStepArgs &a, cudaStream_t stream);
 
 // Device address of the status word on the current device (kda_api.cu).
 int *device_status_word();

@@ -100,7 +100,7 @@ kdaStatus_t step_sizes(const kdaPagedCache_t *cache, const kdaAttnShape_t *shape
     a.k_scale = a.v_scale = nullptr;
     a.shared_pages = nullptr;
     a.prefix = nullptr;
-    a.splits = 0;
+    a.splits = a.prefix_rows = a.prefix_grid = 0;
     return KDA_SUCCESS;
 }
 

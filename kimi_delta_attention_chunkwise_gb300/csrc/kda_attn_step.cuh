@@ -52,21 +52,71 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 __device__ __forceinline__ int32_t shared_tokens(const AttnStepArgs &a) {
     return min(max(*a.shared_pages, 0), a.max_pages) << a.page_shift;
 }
-// The shared tokens are cut among at most a.splits CTAs, in tiles of kPrefixTile.
-constexpr int kPrefixTile = 128;
-__device__ __forceinline__ int32_t prefix_tiles(int32_t tokens) {
-    return tokens / kPrefixTile + (tokens % kPrefixTile != 0);
+constexpr int kPrefixTile = 128;  // tokens
+
+// CTA c of `grid` takes units share_start(c) .. share_start(c + 1) - 1 of a line.
+__device__ __forceinline__ int64_t share_start(int64_t units, int32_t c, int32_t grid) {
+    return units * c / grid;
 }
-// One split's states of every row (a row: sequence * HQ + query head).
+// The CTAs that work: no share is empty.
+__device__ __forceinline__ int32_t workers(int64_t units, int32_t grid) {
+    return (int32_t)min((int64_t)grid, units);
+}
+// The first of the CTAs that work on a line's units from `first` on: the last
+// whose share starts at or before it.
+__device__ __forceinline__ int32_t first_worker(int64_t units, int64_t first, int32_t grid) {
+    return (int32_t)(((first + 1) * grid - 1) / units);
+}
+
+// The shared tokens' work: the tiles of every item (a key-value head and a block
+// of a.prefix_rows rows, a row being sequence * G + query head of the group) form
+// a line, of which every CTA takes an equal share.  An item's pieces are counted
+// from the first CTA that works on it.
+struct PrefixLine {
+    int32_t tiles, blocks, grid;
+    int64_t units;
+    __device__ PrefixLine(const AttnStepArgs &a, int32_t shared) {
+        const int32_t rows = a.N * a.G;
+        tiles = shared / kPrefixTile + (shared % kPrefixTile != 0);
+        blocks = rows / a.prefix_rows + (rows % a.prefix_rows != 0);
+        units = (int64_t)tiles * a.HKV * blocks;
+        grid = workers(units, a.prefix_grid);
+    }
+};
+struct PrefixPiece {
+    int32_t kvh, block;
+    int32_t tile0, tile1;  // its tiles
+    int32_t index;         // which of the item's pieces
+    bool last;             // the item's last one
+    __device__ PrefixPiece(const PrefixLine &p, int32_t c, int64_t u, int64_t u1) {
+        const int32_t item = (int32_t)(u / p.tiles);
+        const int64_t first = (int64_t)item * p.tiles;
+        kvh = item / p.blocks;
+        block = item - kvh * p.blocks;
+        tile0 = (int32_t)(u - first);
+        tile1 = (int32_t)min((int64_t)p.tiles, u1 - first);
+        index = c - first_worker(p.units, first, p.grid);
+        last = tile1 == p.tiles;
+    }
+};
+// One piece's states of every row (here a row is sequence * HQ + query head), and
+// the number of pieces that a row has.
 struct PrefixState {
     float *o, *m, *l;  // weighted sums [rows, D], maxima (base 2) and sums [rows]
+    int32_t *pieces;   // [rows]
 };
-__device__ __forceinline__ PrefixState prefix_state(const AttnStepArgs &a, int D, int32_t split) {
+// (splits: the pieces a row may have, and one more for its own tokens' state
+// where one CTA of the step has it whole)
+__host__ __device__ inline size_t prefix_bytes(int64_t rows, int D, int32_t splits) {
+    return (size_t)rows * ((size_t)splits * (D + 2) + 1) * sizeof(float);
+}
+__device__ __forceinline__ PrefixState prefix_state(const AttnStepArgs &a, int D, int32_t piece) {
     const int64_t rows = (int64_t)a.N * a.HQ;
     float *o = static_cast<float *>(a.prefix);
     float *m = o + rows * D * a.splits;
     float *l = m + rows * a.splits;
-    return {o + rows * D * split, m + rows * split, l + rows * split};
+    return {o + rows * D * piece, m + rows * piece, l + rows * piece,
+            reinterpret_cast<int32_t *>(l + rows * a.splits)};
 }
 
 // ---------------------------------------------------------------------------
@@ -173,14 +223,6 @@ struct Line {
         __syncthreads();
     }
 };
-
-__device__ __forceinline__ int64_t share_start(int64_t units, int32_t c, int32_t grid) {
-    return units * c / grid;
-}
-// The CTAs that work: no share is empty.
-__device__ __forceinline__ int32_t workers(int64_t units, int32_t grid) {
-    return (int32_t)min((int64_t)grid, units);
-}
 
 // A state's maximum as the joins take it.  -inf says that no key was seen; a
 // state that saw keys whose scores are all -inf keeps its sum of 0 with the
@@ -812,32 +854,9 @@ struct Joined {
     }
 };
 
-// A row's result from its state (mx = -inf: no keys), joined with its states of
-// the shared tokens where there are any.
-template <bool SHARED>
+// (mx = -inf: no keys)
 __device__ __forceinline__ void store_row(const AttnStepArgs &a, int64_t head, int D, int col,
                                           float o, float mx, float sum) {
-    if constexpr (SHARED) {
-        const int32_t shared = shared_tokens(a);
-        if (shared > 0 && clamp_len(a, (int32_t)(head / a.HQ)) >= shared) {
-            const int32_t n = min(a.splits, prefix_tiles(shared));
-            const PrefixState p = prefix_state(a, D, 0);
-            const int64_t rows = (int64_t)a.N * a.HQ;
-            float top = mx;
-            for (int32_t i = 0; i < n; ++i) top = fmaxf(top, p.m[i * rows + head]);
-            const float ref = top == -INFINITY ? 0.f : top;
-            const float f = exp2f(mx - ref);
-            o *= f;
-            sum *= f;
-#pragma unroll 4
-            for (int32_t i = 0; i < n; ++i) {
-                const float w = exp2f(p.m[i * rows + head] - ref);
-                o += p.o[(i * rows + head) * D + col] * w;
-                sum += p.l[i * rows + head] * w;
-            }
-            mx = top;
-        }
-    }
     store_out(a, head * D + col, mx == -INFINITY ? 0.f : o / sum);
     if (a.lse && col == 0) a.lse[head] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
@@ -858,26 +877,16 @@ attn_step_kernel(const AttnStepArgs a, float *part) {
     line.scan(a, s_scan);
     const int64_t units = line.total * items;
     const int32_t grid = workers(units, (int32_t)gridDim.x), c = (int32_t)blockIdx.x;
-    // sequences without keys (of their own: SHARED)
-    auto store_empty = [&] {
-        for (int32_t s = c; s < a.N; s += gridDim.x) {
-            if (span_of<SHARED>(a, s).len() > 0) continue;
-            for (int32_t i = tid; i < a.HQ * D; i += kThreads)
-                store_row<SHARED>(a, (int64_t)s * a.HQ + i / D, D, i % D, 0.f, -INFINITY, 0.f);
-        }
-    };
-    // SHARED: the kernel that works on the shared tokens may still run.  No CTA
-    // ends before that has, so that what waits for this kernel has waited for
-    // both.
-    bool waited = !SHARED;
-    auto wait_prefix = [&] {
-        if (!waited) tc::pdl_wait_primaries();
-        waited = true;
-    };
-    if (!SHARED) store_empty();
+    // sequences without keys (SHARED: the join's)
+    for (int32_t s = c; s < a.N && !SHARED; s += gridDim.x) {
+        if (clamp_len(a, s) > 0) continue;
+        for (int32_t i = tid; i < a.HQ * D; i += kThreads)
+            store_row(a, (int64_t)s * a.HQ + i / D, D, i % D, 0.f, -INFINITY, 0.f);
+    }
+    // SHARED: no CTA ends before the kernel that works on the shared tokens has,
+    // so that what waits for this kernel has waited for both
     if (c >= grid) {
-        wait_prefix();
-        if (SHARED) store_empty();
+        if (SHARED) tc::pdl_wait_primaries();
         return;
     }
     const int64_t u0 = share_start(units, c, grid), u1 = share_start(units, c + 1, grid);
@@ -905,14 +914,21 @@ attn_step_kernel(const AttnStepArgs a, float *part) {
         core.finish(state.acc[warp], state.m[warp], state.l[warp], seen);
         __syncthreads();
         const bool whole = tile0 == 0 && tile1 == tiles;
-        if (whole) wait_prefix();
         float *slot = part + ((int64_t)c * 2 + (u == u0 ? 0 : 1)) * (R * (D + 2));
         for (int i = tid; i < rows * D; i += kThreads) {
             const int r = i / D, col = i % D;
             float o, mx, sum;
             state.get(r, i, o, mx, sum);
-            if (whole) {
-                store_row<SHARED>(a, (int64_t)s * a.HQ + head + r, D, col, o, mx, sum);
+            if (whole && SHARED) {
+                const PrefixState p = prefix_state(a, D, a.splits - 1);
+                const int64_t at = (int64_t)s * a.HQ + head + r;
+                p.o[at * D + col] = o;
+                if (col == 0) {
+                    p.m[at] = mx;
+                    p.l[at] = sum;
+                }
+            } else if (whole) {
+                store_row(a, (int64_t)s * a.HQ + head + r, D, col, o, mx, sum);
             } else {
                 slot[i] = o;
                 if (col == 0) {
@@ -924,15 +940,14 @@ attn_step_kernel(const AttnStepArgs a, float *part) {
         __syncthreads();
         u += tile1 - tile0;
     }
-    wait_prefix();
-    if (SHARED) store_empty();
+    if (SHARED) tc::pdl_wait_primaries();
 }
 
 // Short tables: one cluster per item, its CTAs (1, 2, 4 or 8) taking equal
 // runs of the item's tiles and joining their states through distributed shared
 // memory.  No look-up of the line, no scratch and no second kernel, which is
 // what a small step spends its time on; lengths even out less.
-template <class Core, bool SHARED>
+template <class Core>
 __global__ void __launch_bounds__(kThreads, Core::kCtas)
 attn_step_direct_kernel(const AttnStepArgs a) {
     using T = typename Core::Type;
@@ -952,20 +967,18 @@ attn_step_direct_kernel(const AttnStepArgs a) {
     Core core;
     const T *qp = static_cast<const T *>(a.q) + s * a.q_stride + head * D;
     core.init([&](int h) { return qp + h * D; }, rows, a.scale);
-    const Span span = span_of<SHARED>(a, s);
-    const int32_t tiles = tiles_of(span.len());
+    const int32_t len = clamp_len(a, s), tiles = tiles_of(len);
     if (tid == 0 && a.seq_lens[s] > (a.max_pages << a.page_shift)) *a.status = KDA_ERR_INVALID_ARG;
-    const bool seen = walk_tiles(a, core, s, kvh, span.first, span.end,
+    const bool seen = walk_tiles(a, core, s, kvh, 0, len,
                                  (int32_t)((int64_t)tiles * rank / ctas),
                                  (int32_t)((int64_t)tiles * (rank + 1) / ctas));
     core.finish(state.acc[warp], state.m[warp], state.l[warp], seen);
     __syncthreads();
-    if (SHARED) tc::pdl_wait_primaries();
     if (ctas == 1) {
         for (int i = tid; i < rows * D; i += kThreads) {
             float o, mx, sum;
             state.get(i / D, i, o, mx, sum);
-            store_row<SHARED>(a, (int64_t)s * a.HQ + head + i / D, D, i % D, o, mx, sum);
+            store_row(a, (int64_t)s * a.HQ + head + i / D, D, i % D, o, mx, sum);
         }
         return;
     }
@@ -989,7 +1002,7 @@ attn_step_direct_kernel(const AttnStepArgs a) {
             o += *cluster.map_shared_rank(&s_o[i], c) * f;
             sum += *cluster.map_shared_rank(&s_l[r], c) * f;
         }
-        store_row<SHARED>(a, (int64_t)s * a.HQ + head + r, D, i % D, o, mx, sum);
+        store_row(a, (int64_t)s * a.HQ + head + r, D, i % D, o, mx, sum);
     }
     cluster.sync();  // no CTA ends while another reads its shared memory
 }
@@ -999,7 +1012,7 @@ attn_step_direct_kernel(const AttnStepArgs a) {
 // step is the second to work on (whichever makes the smaller grid).  Query
 // heads y * per .. of the item; a warp takes one query head and every parts-th
 // of the item's CTAs.
-template <int D, int R, bool SHARED>
+template <int D, int R>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnStepArgs a,
                                                                  const float *part,
                                                                  int32_t step_grid, int32_t per,
@@ -1010,7 +1023,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnStepA
     __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int32_t blocks = (a.G + R - 1) / R, items = a.HKV * blocks;
-    Line<kJoinThreads, SHARED> line;
+    Line<kJoinThreads, false> line;
     line.scan(a, s_scan);
     const int64_t units = line.total * items;
     const int32_t grid = workers(units, step_grid);
@@ -1027,12 +1040,12 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnStepA
     tc::pdl_wait_primaries();
     if (!any) return;
     const int32_t s = s_seq;
-    const int32_t tiles = tiles_of(span_of<SHARED>(a, s).len());
+    const int32_t tiles = tiles_of(clamp_len(a, s));
     if (tiles == 0) return;  // by_item: written by the step
     const int32_t item = by_item ? (int32_t)blockIdx.x - s * items : (int32_t)((start - s_base) / tiles);
     const int64_t first = s_base + (int64_t)item * tiles, last = first + tiles;  // the item's units
-    // the first of the step's CTAs on the item: the last that starts at or before it
-    const int32_t c0 = by_item ? (int32_t)(((first + 1) * grid - 1) / units) : (int32_t)blockIdx.x;
+    // the first of the step's CTAs on the item
+    const int32_t c0 = by_item ? first_worker(units, first, grid) : (int32_t)blockIdx.x;
     if (by_item ? share_start(units, c0 + 1, grid) >= last
                 : start == first || share_start(units, c0, grid) > first)
         return;
@@ -1087,7 +1100,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnStepA
                 sum += s_l[w] * f;
             }
             const int64_t head = (int64_t)s * a.HQ + (int64_t)kvh * a.G + h0 + r0 + rb + w0;
-            store_row<SHARED>(a, head, D, col, y, m, sum);
+            store_row(a, head, D, col, y, m, sum);
         }
         __syncthreads();
     }
@@ -1113,9 +1126,15 @@ int64_t step_items(const AttnStepArgs &a) {
     return (int64_t)a.N * a.HKV * ((a.G + Core::kRows - 1) / Core::kRows);
 }
 
-// SHARED: after the kernel that works on the shared tokens, as a programmatic
-// dependent of it.
-template <class Core, bool SHARED = false>
+// CTAs of the line of tiles: one wave, and no more than the longest possible line
+// has tiles.
+template <class Core>
+int line_grid(const AttnStepArgs &a, int sms) {
+    const int64_t capacity = (int64_t)a.max_pages << a.page_shift;
+    return (int)std::min((int64_t)sms * Core::kCtas, step_items<Core>(a) * (capacity / kTile + 1));
+}
+
+template <class Core>
 cudaError_t launch_core(const AttnStepArgs &a, cudaStream_t stream) {
     constexpr int D = Core::kD, R = Core::kRows;
     const int sms = device_sms();
@@ -1123,7 +1142,7 @@ cudaError_t launch_core(const AttnStepArgs &a, cudaStream_t stream) {
     const int64_t capacity = (int64_t)a.max_pages << a.page_shift;
     const int64_t items = step_items<Core>(a), slots = (int64_t)sms * Core::kCtas;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     cfg.stream = stream;
     cfg.attrs = attr;
     const int ctas = direct_ctas(items, capacity, slots);
@@ -1134,18 +1153,13 @@ cudaError_t launch_core(const AttnStepArgs &a, cudaStream_t stream) {
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = (unsigned)ctas;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        attr[1] = follows_on();
-        cfg.numAttrs = SHARED ? 2 : 1;
-        return cudaLaunchKernelEx(&cfg, attn_step_direct_kernel<Core, SHARED>, a);
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, attn_step_direct_kernel<Core>, a);
     }
-    // no more CTAs than the longest possible line has tiles
-    const int grid = (int)std::min(slots, items * (capacity / kTile + 1));
+    const int grid = line_grid<Core>(a, sms);
     float *part = static_cast<float *>(a.workspace);
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kThreads);
-    attr[0] = follows_on();
-    cfg.numAttrs = SHARED ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_step_kernel<Core, SHARED>, a, part);
+    attn_step_kernel<Core, false><<<grid, kThreads, 0, stream>>>(a, part);
+    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || grid == 1) return e;
     // few items: each is shared by many CTAs, and a join CTA takes one query
     // head; else all of an item's
@@ -1153,18 +1167,23 @@ cudaError_t launch_core(const AttnStepArgs &a, cudaStream_t stream) {
     const bool by_item = items < grid;
     cfg.gridDim = dim3((unsigned)(by_item ? items : grid - 1), (unsigned)((most_rows + per - 1) / per));
     cfg.blockDim = dim3(kJoinThreads);
+    attr[0] = follows_on();
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<D, R, SHARED>, a,
-                              static_cast<const float *>(part), (int32_t)grid, per,
-                              (int32_t)by_item);
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<D, R>, a, static_cast<const float *>(part),
+                              (int32_t)grid, per, (int32_t)by_item);
 }
 
-// Scratch of the line of tiles (0: the direct kernel needs none).
+// Scratch of the line of tiles.
+template <class Core>
+size_t line_bytes(int sms) {
+    return (size_t)sms * Core::kCtas * 2 * Core::kRows * (Core::kD + 2) * sizeof(float);
+}
+// Scratch of the step (the direct kernel needs none).
 template <class Core>
 size_t part_bytes(const AttnStepArgs &a, int sms) {
     const int64_t slots = (int64_t)sms * Core::kCtas;
     if (direct_ctas(step_items<Core>(a), (int64_t)a.max_pages << a.page_shift, slots)) return 0;
-    return (size_t)slots * 2 * Core::kRows * (Core::kD + 2) * sizeof(float);
+    return line_bytes<Core>(sms);
 }
 
 // The core of a problem whose cache has the queries' type, as a call of f(Core{}).
