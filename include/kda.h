@@ -722,7 +722,7 @@ kdaStatus_t kda_attn_step_ws(const void *q, const kdaPagedCache_t *cache, const 
 typedef struct {
     void *k;                     /* codes: int8 [num_pages, HKV, page_size, d], 16-byte aligned */
     void *v;                     /* same layout */
-    float *k_scale;              /* float32 [num_pages, HKV, page_size] */
+    float *k_scale;              /* float32 [num_pages, HKV, page_size], 16-byte aligned */
     float *v_scale;              /* same layout */
     const int32_t *block_table;  /* the rest as in kdaPagedCache_t */
     int32_t num_pages;

@@ -78,7 +78,7 @@ kdaStatus_t check_cache(const kdaPagedCache_t *c, int32_t *page_shift) {
 kdaStatus_t check_cache_q8(const kdaPagedCacheQ8_t *c, kdaPagedCache_t &same) {
     if (!c) return KDA_ERR_INVALID_ARG;
     if (c->num_pages > 0 && (!c->k_scale || !c->v_scale)) return KDA_ERR_INVALID_ARG;
-    if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)) return KDA_ERR_INVALID_ARG;
+    if (!aligned(c->k_scale, 16) || !aligned(c->v_scale, 16)) return KDA_ERR_INVALID_ARG;
     same = {c->k, c->v, c->block_table, c->num_pages, c->page_size, c->max_pages};
     return KDA_SUCCESS;
 }
@@ -100,6 +100,7 @@ kdaStatus_t step_sizes(const kdaPagedCache_t *cache, const kdaAttnShape_t *shape
     a.k_scale = a.v_scale = nullptr;
     a.shared_pages = nullptr;
     a.prefix = nullptr;
+    a.owners = nullptr;
     a.splits = a.prefix_rows = a.prefix_grid = 0;
     return KDA_SUCCESS;
 }

@@ -1,0 +1,448 @@
+// kda_attn_flat.cuh -- the step's line of tiles cut among warps: kda_attn_step_q8's
+// and kda_attn_step_shared's kernels for bf16 queries with D = 64 or 128, and the
+// join that both end with.
+//
+// The units, 16 or 32 tokens of a (sequence, head) item, form one line, of which
+// every warp takes an equal share.  A warp's units come to shared memory in a
+// ring of its own, ahead of the one it works on and across the borders of items:
+// a block of 16 tokens is neighbouring rows of a page, one bulk copy of keys, one
+// of values (and two of scales).  Nothing in the loop waits for another warp, and
+// short items cost no start of their own.  At the end of an item the warp writes
+// the item's results, or its part's state for the join.  (kda_attn_step's kernel,
+// whose CTAs share a tile of 64 tokens and hold the next one's rows in registers,
+// gets 0.63 of the memory's rate out of 8-bit rows, half as many bytes to a tile,
+// and of sequences of a few hundred tokens.)
+#pragma once
+
+#include "kda_attn_step.cuh"
+
+namespace kda {
+namespace {
+
+constexpr long long kFlatWait = 2000000000LL;  // SM clocks, about a second
+
+// Where a warp is in the line: unit `tile` of `tiles` of sequence s under key-value
+// head kvh and block `block` of its query heads.
+template <bool SHARED, int UNIT>
+struct LineCursor {
+    int32_t s, kvh, block, tile, tiles, first, end;
+    __device__ void enter(const AttnStepArgs &a, int32_t seq) {
+        s = seq;
+        const Span span = span_of<SHARED>(a, s);
+        first = span.first;
+        end = span.end;
+        tiles = tiles_of<UNIT>(span.len());
+    }
+    // unit u, which is one of sequence seq's, whose units start at base
+    __device__ void seek(const AttnStepArgs &a, int32_t blocks, int32_t seq, int64_t base, int64_t u) {
+        enter(a, seq);
+        const int32_t item = (int32_t)((u - base) / tiles);
+        tile = (int32_t)((u - base) - (int64_t)item * tiles);
+        kvh = item / blocks;
+        block = item - kvh * blocks;
+    }
+    // the next unit (there is one)
+    __device__ void next(const AttnStepArgs &a, int32_t blocks) {
+        if (++tile < tiles) return;
+        tile = 0;
+        if (++block < blocks) return;
+        block = 0;
+        if (++kvh < a.HKV) return;
+        kvh = 0;
+        do enter(a, s + 1);
+        while (tiles == 0);
+    }
+    __device__ int32_t token() const { return first + tile * UNIT; }
+};
+
+template <class Core>
+struct FlatCfg {
+    // what the CTAs of an SM leave of its shared memory, in blocks of 16 tokens to
+    // a warp
+    static constexpr int ROOM = (228 * 1024 / Core::kCtas - 2048) / (int)(kWarps * Core::kBlockBytes);
+    // 32 tokens to a unit where two units of them fit: what a unit costs besides
+    // its tokens is a third of the instructions
+    static constexpr int SUB = ROOM >= 4 ? 2 : 1, UNIT = SUB * kWarpTokens;
+    static constexpr int RING = ROOM / SUB < 4 ? ROOM / SUB : 4;  // units
+    static constexpr uint32_t UNIT_BYTES = SUB * Core::kBlockBytes;
+    static constexpr uint32_t SMEM = kWarps * RING * UNIT_BYTES;
+    static_assert(RING >= 2 && RING * SUB <= 32, "shared memory of an SM");
+};
+
+// Neighbouring channels of a row's result from its state (mx = -inf: no keys).
+template <int N>
+__device__ __forceinline__ void store_run(const AttnStepArgs &a, int64_t head, int D, int ch,
+                                          const float (&o)[N], float mx, float sum) {
+    float y[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] = mx == -INFINITY ? 0.f : o[i] / sum;
+    if (a.out_f32) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + head * D + ch + i) =
+                make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + head * D + ch + i) =
+                make_uint2(tc::pack_bf16x2(y[i], y[i + 1]), tc::pack_bf16x2(y[i + 2], y[i + 3]));
+    }
+    if (a.lse && ch == 0) a.lse[head] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * kLn2;
+}
+
+template <class Core, bool SHARED>
+__global__ void __launch_bounds__(kThreads, Core::kCtas)
+attn_flat_kernel(const AttnStepArgs a, float *part) {
+    using T = typename Core::Type;
+    using C = typename Core::Cell;
+    using Cfg = FlatCfg<Core>;
+    constexpr int D = Core::kD, R = Core::kRows, RING = Cfg::RING, SUB = Cfg::SUB;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t s_scan[kWarps], s_base[kWarps];
+    __shared__ int32_t s_seq[kWarps];
+    __shared__ uint64_t s_full[kWarps][RING];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    tc::pdl_launch_dependents();
+    const int32_t blocks = (a.G + R - 1) / R;  // blocks of query heads
+    const int32_t items = a.HKV * blocks;
+    Line<kThreads, SHARED, Cfg::UNIT> line;
+    line.scan(a, s_scan);
+    const int64_t units = line.total * items;
+    const int32_t grid = workers(units, (int32_t)gridDim.x * kWarps);
+    // sequences without keys (SHARED: the join's)
+    for (int32_t s = (int32_t)blockIdx.x; s < a.N && !SHARED; s += gridDim.x) {
+        if (clamp_len(a, s) > 0) continue;
+        for (int32_t i = tid; i < a.HQ * D; i += kThreads)
+            store_row(a, (int64_t)s * a.HQ + i / D, D, i % D, 0.f, -INFINITY, 0.f);
+    }
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const int32_t c = (int32_t)blockIdx.x * kWarps + w;
+        if (c < grid) line.look(a, share_start(units, c, grid), items, &s_seq[w], &s_base[w]);
+    }
+    if (tid == 0) {
+        for (int w = 0; w < kWarps; ++w)
+            for (int x = 0; x < RING; ++x) tc::mbar_init(&s_full[w][x], SUB);
+        tc::fence_mbar_init();
+        tc::fence_proxy_async();
+    }
+    __syncthreads();
+    const int32_t c = (int32_t)blockIdx.x * kWarps + warp;  // this worker
+    if (c < grid) {
+        const int64_t u0 = share_start(units, c, grid), u1 = share_start(units, c + 1, grid);
+        uint8_t *ring = smem + warp * RING * Cfg::UNIT_BYTES;
+        uint64_t *full = s_full[warp];
+        LineCursor<SHARED, Cfg::UNIT> here, ahead;
+        here.seek(a, blocks, s_seq[warp], s_base[warp], u0);
+        ahead = here;
+        // lane i < SUB: the i-th block of the unit at `ahead`, and its page's entry
+        const int32_t mine = min(lane, SUB - 1) * kWarpTokens;
+        auto entry_of = [&]() -> int32_t {
+            const int32_t tok = ahead.token() + mine;
+            return tok < ahead.end
+                       ? a.block_table[(int64_t)ahead.s * a.max_pages + (tok >> a.page_shift)]
+                       : 0;
+        };
+        uint32_t good = 0;   // a bit per block in the ring: it is there
+        uint32_t phase = 0;  // a bit per unit's barrier
+        int64_t au = u0;     // the unit at `ahead`
+        int32_t page = entry_of();
+        // starts the copies of the unit at `ahead` to place x of the ring
+        auto copy_next = [&](int32_t x) {
+            if (au >= u1) return;
+            const int32_t tok = ahead.token() + mine, n = min(kWarpTokens, ahead.end - tok);
+            const bool there = page >= 0 && page < a.num_pages, ok = there && n > 0;
+            if (lane < SUB) {
+                if (ok) {
+                    const int64_t row = (((int64_t)page * a.HKV + ahead.kvh) << a.page_shift) +
+                                        (tok & ((1 << a.page_shift) - 1));
+                    uint8_t *to = ring + x * Cfg::UNIT_BYTES + lane * Core::kBlockBytes;
+                    const uint32_t rows = n * Core::kRowBytes;
+                    tc::mbar_arrive_expect_tx(&full[x], 2 * rows + (Core::kScaled ? 128 : 0));
+                    tc::bulk_g2s(to, static_cast<const C *>(a.k_cache) + row * D, rows, &full[x]);
+                    tc::bulk_g2s(to + Core::kHalf, static_cast<const C *>(a.v_cache) + row * D,
+                                 rows, &full[x]);
+                    if constexpr (Core::kScaled) {  // (all 16, which lie in the page)
+                        tc::bulk_g2s(to + 2 * Core::kHalf, a.k_scale + row, 64, &full[x]);
+                        tc::bulk_g2s(to + 2 * Core::kHalf + 64, a.v_scale + row, 64, &full[x]);
+                    }
+                } else {
+                    if (!there) *a.status = KDA_ERR_INVALID_ARG;
+                    tc::mbar_arrive(&full[x]);
+                }
+            }
+            constexpr uint32_t all = (1u << SUB) - 1;
+            good = (good & ~(all << (x * SUB))) |
+                   ((__ballot_sync(0xffffffffu, ok) & all) << (x * SUB));
+            if (++au < u1) {
+                ahead.next(a, blocks);
+                page = entry_of();
+            }
+        };
+        auto wait = [&](int32_t x) -> bool {
+            const uint32_t p = phase >> x & 1;
+            const bool done = tc::mbar_try_wait(&full[x], p) ||
+                              tc::mbar_wait_bounded(&full[x], p, kFlatWait);
+            phase ^= 1u << x;
+            return __all_sync(0xffffffffu, done);
+        };
+#pragma unroll
+        for (int x = 0; x < RING; ++x) copy_next(x);
+        Core core;
+        bool fresh = true, seen = false, first_item = true;
+        int32_t x = 0;
+        int64_t u = u0;
+        for (; u < u1; ++u) {
+            const int32_t rows = min(R, a.G - here.block * R);
+            const int64_t head = (int64_t)here.kvh * a.G + here.block * R;
+            if (fresh) {
+                const T *qp = static_cast<const T *>(a.q) + here.s * a.q_stride + head * D;
+                core.init([&](int h) { return qp + h * D; }, rows, a.scale);
+                fresh = seen = false;
+            }
+            if (!wait(x)) {
+                *a.status = KDA_ERR_TIMEOUT;
+                break;
+            }
+            const uint32_t blocks_good = good >> (x * SUB);
+            const int32_t left = here.end - here.token();
+#pragma unroll 1
+            for (int b = 0; b < SUB; ++b) {
+                const bool ok = blocks_good >> b & 1;
+                const int n = min(kWarpTokens, left - b * kWarpTokens);
+                if (ok) {
+                    uint8_t *block = ring + x * Cfg::UNIT_BYTES + b * Core::kBlockBytes;
+                    if (n < kWarpTokens) {
+                        Core::clear_rest(block, n);
+                        tc::fence_proxy_async();  // before copies to this place
+                        __syncwarp();
+                    }
+                    core.fetch(block);
+                }
+                if (b == SUB - 1) {
+                    __syncwarp();
+                    copy_next(x);
+                }
+                if (ok) {
+                    core.scores();
+                    core.values(n);
+                    seen = true;
+                }
+            }
+            x = x + 1 == RING ? 0 : x + 1;
+            const bool ends = here.tile + 1 == here.tiles;
+            if (ends || u + 1 == u1) {
+                const int64_t first = u - here.tile;  // the item's first unit
+                const bool whole = ends && first >= u0;
+                const int64_t row = (int64_t)here.s * a.HQ + head;
+                if (whole && !SHARED) {
+                    core.finish_rows(seen, rows, [&](int h, int ch, auto &y, float m, float l) {
+                        store_run(a, row + h, D, ch, y, m, l);
+                    });
+                } else {
+                    // a whole item's state, or the worker's first or last part's
+                    float *to, *to_m, *to_l;
+                    if (whole) {
+                        const PrefixState p = prefix_state(a, D, a.splits - 1);
+                        to = p.o + row * D;
+                        to_m = p.m + row;
+                        to_l = p.l + row;
+                    } else {
+                        to = part + ((int64_t)c * 2 + (first_item ? 0 : 1)) * (R * (D + 2));
+                        to_m = to + R * D;
+                        to_l = to_m + R;
+                    }
+                    core.finish_rows(seen, rows, [&](int h, int ch, auto &y, float m, float l) {
+#pragma unroll
+                        for (int i = 0; i < (int)(sizeof(y) / sizeof(float)); i += 4)
+                            *reinterpret_cast<float4 *>(to + h * D + ch + i) =
+                                make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+                        if (ch == 0) {
+                            to_m[h] = m;
+                            to_l[h] = l;
+                        }
+                    });
+                }
+                if (ends && lane == 0)
+                    a.owners[(int64_t)here.s * items + here.kvh * blocks + here.block] =
+                        owners_of(units, first, c, grid);
+                fresh = true;
+                first_item = false;
+            }
+            if (u + 1 < u1) here.next(a, blocks);
+        }
+        // (a wait gave up: the CTA may end when the copies behind it have landed)
+        for (; u < au; ++u) {
+            (void)wait(x);
+            x = x + 1 == RING ? 0 : x + 1;
+        }
+    }
+    if (SHARED) tc::pdl_wait_primaries();
+}
+
+// Joins what workers have left of every row: parts of its item, or its item's
+// state (kda_attn_step_q8's are results already), and its states over the shared
+// tokens.  `parts` warps to a row, so many rows to a CTA as its 8 warps have;
+// a row's maxima and sums one to a lane, its weighted sums four loads abreast.
+// tile: tokens of a unit of the line.
+template <int D, int R, bool SHARED>
+__global__ void __launch_bounds__(kJoinThreads) attn_rows_join_kernel(const AttnStepArgs a,
+                                                                      const float *part,
+                                                                      int32_t parts) {
+    constexpr int N = (D + 31) / 32;  // columns per lane
+    __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int32_t blocks = (a.G + R - 1) / R;
+    const int32_t abreast = kJoinWarps / parts;  // rows of the CTA
+    const int64_t row = (int64_t)blockIdx.x * abreast + warp / parts, rows = (int64_t)a.N * a.HQ;
+    const int32_t s = row < rows ? (int32_t)(row / a.HQ) : 0;
+    const int32_t hq = row < rows ? (int32_t)(row - (int64_t)s * a.HQ) : 0;
+    const int32_t kvh = hq / a.G, block = (hq - kvh * a.G) / R, r = hq - kvh * a.G - block * R;
+    const Span span = span_of<SHARED>(a, s);
+    // the kernels before this one have ended
+    tc::pdl_wait_primaries();
+    const int2 who = a.owners[((int64_t)s * a.HKV + kvh) * blocks + block];
+    int32_t own = span.len() > 0 ? who.y >> 1 : 0;
+    const int32_t pieces =
+        SHARED && span.first > 0 ? prefix_state(a, D, 0).pieces[row < rows ? row : 0] : 0;
+    const bool done = !SHARED && own <= 1;  // written by the worker, or there were no keys
+    if (row >= rows || done) own = 0;
+    const int32_t all = row >= rows || done ? 0 : own + pieces;
+    float mx = -INFINITY, l = 0.f, o[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) o[j] = 0.f;
+    // state i: its weighted sums, maximum and sum
+    auto state_of = [&](int32_t i, const float *&so, const float *&sm, const float *&sl) {
+        if (i < own && own > 1) {
+            const float *slot =
+                part + ((int64_t)(who.x + i) * 2 + (i == 0 ? who.y & 1 : 0)) * (R * (D + 2));
+            so = slot + r * D;
+            sm = slot + R * D + r;
+            sl = slot + R * D + R + r;
+        } else {
+            const PrefixState p = prefix_state(a, D, i < own ? a.splits - 1 : i - own);
+            so = p.o + row * D;
+            sm = p.m + row;
+            sl = p.l + row;
+        }
+    };
+    for (int32_t i0 = warp % parts; i0 < all; i0 += 32 * parts) {
+        const int32_t i = i0 + lane * parts;
+        float m = -INFINITY, sum = 0.f;
+        if (i < all) {
+            const float *so, *sm, *sl;
+            state_of(i, so, sm, sl);
+            m = *sm;
+            sum = *sl;
+        }
+        float top = fmaxf(mx, m);
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        const float ref = top == -INFINITY ? 0.f : top;
+        const float f = exp2f(mx - ref), w = exp2f(m - ref);
+        sum *= w;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        mx = top;
+        l = l * f + sum;
+#pragma unroll
+        for (int j = 0; j < N; ++j) o[j] *= f;
+        const int32_t n = min(32, (all - i0 + parts - 1) / parts);
+#pragma unroll 4
+        for (int32_t k = 0; k < n; ++k) {
+            const float wk = __shfl_sync(0xffffffffu, w, k);
+            const float *so, *sm, *sl;
+            state_of(i0 + k * parts, so, sm, sl);
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (D >= 32 || lane < D) o[j] += so[j * 32 + lane] * wk;
+        }
+    }
+    if (parts > 1) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (D >= 32 || lane < D) s_o[warp][j * 32 + lane] = o[j];
+        if (lane == 0) {
+            s_m[warp] = mx;
+            s_l[warp] = l;
+        }
+        __syncthreads();
+        if (warp % parts) return;
+        float top = mx;
+        for (int w = 1; w < parts; ++w) top = fmaxf(top, s_m[warp + w]);
+        const float ref = top == -INFINITY ? 0.f : top;
+        const float f = exp2f(mx - ref);
+        l *= f;
+#pragma unroll
+        for (int j = 0; j < N; ++j) o[j] *= f;
+        for (int w = 1; w < parts; ++w) {
+            const float fw = exp2f(s_m[warp + w] - ref);
+            l += s_l[warp + w] * fw;
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (D >= 32 || lane < D) o[j] += s_o[warp + w][j * 32 + lane] * fw;
+        }
+        mx = top;
+    }
+    if (row >= rows || done) return;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (D >= 32 || lane < D) store_row(a, row, D, j * 32 + lane, o[j], mx, l);
+}
+
+// Warps to a row of the join: as many as keep the GPU's warps busy.
+inline int32_t join_parts(int64_t rows, int sms) {
+    int32_t parts = 1;
+    while (parts < kJoinWarps && rows * parts * 2 <= (int64_t)sms * 32) parts *= 2;
+    return parts;
+}
+
+// Bytes of workers' parts, and of owners.
+template <class Core>
+size_t flat_part_bytes(int sms) {
+    return (size_t)sms * Core::kCtas * kWarps * 2 * Core::kRows * (Core::kD + 2) * sizeof(float);
+}
+template <class Core>
+size_t owners_bytes(const AttnStepArgs &a) {
+    return ((size_t)step_items<Core>(a) * sizeof(int2) + 255) / 256 * 256;
+}
+
+// The join, a programmatic dependent of the kernel before.
+template <class Core, bool SHARED>
+cudaError_t launch_rows_join(const AttnStepArgs &a, const float *part, int sms,
+                             cudaStream_t stream) {
+    const int64_t rows = (int64_t)a.N * a.HQ;
+    const int32_t parts = join_parts(rows, sms), abreast = kJoinWarps / parts;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr = follows_on();
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3((unsigned)((rows + abreast - 1) / abreast));
+    cfg.blockDim = dim3(kJoinThreads);
+    return cudaLaunchKernelEx(&cfg, attn_rows_join_kernel<Core::kD, Core::kRows, SHARED>, a, part,
+                              parts);
+}
+
+// The flat kernel (SHARED: a programmatic dependent of the kernel before).
+template <class Core, bool SHARED>
+cudaError_t launch_flat(const AttnStepArgs &a, float *part, int sms, cudaStream_t stream) {
+    const int64_t capacity = (int64_t)a.max_pages << a.page_shift;
+    // one wave, and no more warps than the longest possible line has units
+    const int64_t most = step_items<Core>(a) * (capacity / FlatCfg<Core>::UNIT + 1);
+    const int64_t grid = std::min((int64_t)sms * Core::kCtas, (most + kWarps - 1) / kWarps);
+    const cudaError_t e = allow_smem<attn_flat_kernel<Core, SHARED>>(FlatCfg<Core>::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr = follows_on();
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = SHARED ? 1 : 0;
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = FlatCfg<Core>::SMEM;
+    return cudaLaunchKernelEx(&cfg, attn_flat_kernel<Core, SHARED>, a, part);
+}
+
+}  // namespace
+}  // namespace kda

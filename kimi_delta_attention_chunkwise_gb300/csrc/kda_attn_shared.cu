@@ -9,7 +9,7 @@
 // step of kda_attn_step.cuh from token S on, whose CTAs start as those of the
 // first leave; it leaves states, too, and a third kernel joins all of a row's.  A
 // sequence that holds less than S tokens is all the step's.
-#include "kda_attn_step.cuh"
+#include "kda_attn_flat.cuh"
 
 namespace kda {
 namespace {
@@ -71,160 +71,50 @@ __global__ void __launch_bounds__(kThreads, Core::kCtas) attn_prefix_kernel(cons
     }
 }
 
-// Joins the states of an item of the step (a sequence's tokens under one block of
-// query heads) with those of the shared tokens.  One CTA to an item; a warp
-// takes one query head and every parts-th of its states: their maxima and sums
-// one to a lane, then the weighted sums, four loads in flight.
-template <int D, int R>
-__global__ void __launch_bounds__(kJoinThreads) attn_shared_join_kernel(const AttnStepArgs a,
-                                                                        const float *part,
-                                                                        int32_t step_grid) {
-    constexpr int N = (D + 31) / 32;  // columns per lane
-    __shared__ int64_t s_scan[kJoinWarps], s_base;
-    __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int32_t blocks = (a.G + R - 1) / R, items = a.HKV * blocks;
-    const int32_t s = (int32_t)blockIdx.x / items, item = (int32_t)blockIdx.x - s * items;
-    Line<kJoinThreads, true> line;
-    line.scan(a, s_scan);
-    line.base_of(a, s, items, &s_base);
-    const int64_t units = line.total * items;
-    const int32_t grid = workers(units, step_grid);
-    const Span span = span_of<true>(a, s);
-    const int32_t tiles = tiles_of(span.len());
-    // the step's CTAs on the item
-    const int64_t first = s_base + (int64_t)item * tiles, end = first + tiles;
-    const int32_t c0 = tiles ? first_worker(units, first, grid) : 0;
-    const int32_t own = tiles ? first_worker(units, end - 1, grid) - c0 + 1 : 0;
-    const bool late = tiles && share_start(units, c0, grid) != first;  // c0's second slot
-    const int32_t kvh = item / blocks, h0 = (item - kvh * blocks) * R;
-    const int32_t rows = min(R, a.G - h0);
-    const bool shares = span.first > 0;
-    // the kernels before this one have ended
-    tc::pdl_wait_primaries();
-    int32_t abreast = 1;  // query heads at a time, a power of two
-    while (abreast < rows && abreast < kJoinWarps) abreast *= 2;
-    const int32_t parts = kJoinWarps / abreast;
-    for (int32_t rb = 0; rb < rows; rb += abreast) {
-        const int32_t r = rb + (warp & (abreast - 1));
-        const int64_t row = (int64_t)s * a.HQ + (int64_t)kvh * a.G + h0 + r;
-        float mx = -INFINITY, l = 0.f, o[N];
-#pragma unroll
-        for (int j = 0; j < N; ++j) o[j] = 0.f;
-        if (r < rows) {
-            const int32_t pieces = shares ? prefix_state(a, D, 0).pieces[row] : 0;
-            const int32_t all = own + pieces;
-            // state i: its weighted sums, maximum and sum
-            auto state_of = [&](int32_t i, const float *&so, const float *&sm, const float *&sl) {
-                if (i < own && own > 1) {
-                    const float *slot = part + ((int64_t)(c0 + i) * 2 + (i == 0 && late ? 1 : 0)) *
-                                                   (R * (D + 2));
-                    so = slot + r * D;
-                    sm = slot + R * D + r;
-                    sl = slot + R * D + R + r;
-                } else {
-                    const PrefixState p = prefix_state(a, D, i < own ? a.splits - 1 : i - own);
-                    so = p.o + row * D;
-                    sm = p.m + row;
-                    sl = p.l + row;
-                }
-            };
-            for (int32_t i0 = warp / abreast; i0 < all; i0 += 32 * parts) {
-                const int32_t i = i0 + lane * parts;
-                float m = -INFINITY, sum = 0.f;
-                if (i < all) {
-                    const float *so, *sm, *sl;
-                    state_of(i, so, sm, sl);
-                    m = *sm;
-                    sum = *sl;
-                }
-                float top = fmaxf(mx, m);
-#pragma unroll
-                for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                const float ref = top == -INFINITY ? 0.f : top;
-                const float f = exp2f(mx - ref), w = exp2f(m - ref);
-                sum *= w;
-#pragma unroll
-                for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-                mx = top;
-                l = l * f + sum;
-#pragma unroll
-                for (int j = 0; j < N; ++j) o[j] *= f;
-                const int32_t n = min(32, (all - i0 + parts - 1) / parts);
-#pragma unroll 4
-                for (int32_t k = 0; k < n; ++k) {
-                    const float wk = __shfl_sync(0xffffffffu, w, k);
-                    const float *so, *sm, *sl;
-                    state_of(i0 + k * parts, so, sm, sl);
-#pragma unroll
-                    for (int j = 0; j < N; ++j)
-                        if (D >= 32 || lane < D) o[j] += so[j * 32 + lane] * wk;
-                }
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (D >= 32 || lane < D) s_o[warp][j * 32 + lane] = o[j];
-        if (lane == 0) {
-            s_m[warp] = mx;
-            s_l[warp] = l;
-        }
-        __syncthreads();
-        for (int i = tid; i < min(abreast, rows - rb) * D; i += kJoinThreads) {
-            const int w0 = i / D, col = i % D;
-            float m = s_m[w0];
-            for (int w = w0 + abreast; w < kJoinWarps; w += abreast) m = fmaxf(m, s_m[w]);
-            const float ref = m == -INFINITY ? 0.f : m;
-            float y = 0.f, sum = 0.f;
-            for (int w = w0; w < kJoinWarps; w += abreast) {
-                const float f = exp2f(s_m[w] - ref);
-                y += s_o[w][col] * f;
-                sum += s_l[w] * f;
-            }
-            store_row(a, (int64_t)s * a.HQ + (int64_t)kvh * a.G + h0 + rb + w0, D, col, y, m, sum);
-        }
-        __syncthreads();
-    }
+// Scratch of the step's parts.
+template <class Core>
+size_t rest_bytes(int sms) {
+    if constexpr (Core::kAhead) return flat_part_bytes<Core>(sms);
+    else return line_bytes<Core>(sms);
 }
 
 // The step from the shared tokens on, and the join, each a programmatic dependent
 // of the kernel before.
 template <class Core>
-cudaError_t launch_rest(const AttnStepArgs &a, cudaStream_t stream) {
-    const int sms = device_sms();
-    const int64_t items = step_items<Core>(a);
-    if (items > INT32_MAX) return cudaErrorInvalidValue;
-    const int32_t grid = line_grid<Core>(a, sms);
+cudaError_t launch_rest(const AttnStepArgs &a, int sms, cudaStream_t stream) {
     float *part = static_cast<float *>(a.workspace);
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr = follows_on();
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kThreads);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_step_kernel<Core, true>, a, part);
-    if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3((unsigned)items);
-    cfg.blockDim = dim3(kJoinThreads);
-    return cudaLaunchKernelEx(&cfg, attn_shared_join_kernel<Core::kD, Core::kRows>, a,
-                              static_cast<const float *>(part), grid);
+    cudaError_t e;
+    if constexpr (Core::kAhead) {
+        e = launch_flat<Core, true>(a, part, sms, stream);
+    } else {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr = follows_on();
+        cfg.stream = stream;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        cfg.gridDim = dim3((unsigned)line_grid<Core>(a, sms));
+        cfg.blockDim = dim3(kThreads);
+        e = cudaLaunchKernelEx(&cfg, attn_step_kernel<Core, true>, a, part);
+    }
+    return e != cudaSuccess ? e : launch_rows_join<Core, true>(a, part, sms, stream);
 }
 
 // How a call's work on the shared tokens is cut, and its scratch in bytes.
 struct Plan {
     bool tensor;
     int32_t rows, grid, splits;
-    size_t part, prefix;
+    size_t part, owners, prefix;  // in this order
 };
 
 cudaError_t plan_of(const AttnStepArgs &a, Plan &p) {
     const int sms = device_sms();
     if (!sms) return cudaErrorUnknown;
-    p.part = with_core(a.D, a.G, a.dtype, [&](auto core) -> size_t {
-        return line_bytes<decltype(core)>(sms);
+    with_core(a.D, a.G, a.dtype, [&](auto core) -> int {
+        using Core = decltype(core);
+        p.part = (rest_bytes<Core>(sms) + 255) / 256 * 256;
+        p.owners = owners_bytes<Core>(a);
+        return 0;
     });
-    p.part = (p.part + 255) / 256 * 256;
     p.tensor = a.dtype == KDA_DTYPE_BF16 && a.D >= 64 && (int64_t)a.N * a.G > kFewRows;
     int64_t slots = sms;
     if (p.tensor) {
@@ -255,7 +145,7 @@ cudaError_t plan_of(const AttnStepArgs &a, Plan &p) {
 cudaError_t attn_step_shared_workspace_bytes(const AttnStepArgs &a, size_t *bytes) {
     Plan p;
     const cudaError_t e = plan_of(a, p);
-    if (e == cudaSuccess) *bytes = p.part + p.prefix;
+    if (e == cudaSuccess) *bytes = p.part + p.owners + p.prefix;
     return e;
 }
 
@@ -267,7 +157,9 @@ cudaError_t launch_attn_step_shared(const AttnStepArgs &args, cudaStream_t strea
     a.splits = p.splits;
     a.prefix_rows = p.rows;
     a.prefix_grid = p.grid;
-    a.prefix = static_cast<char *>(a.workspace) + p.part;
+    char *ws = static_cast<char *>(a.workspace);
+    a.owners = reinterpret_cast<int2 *>(ws + p.part);
+    a.prefix = ws + p.part + p.owners;
     if (p.tensor) {
         e = launch_prefix_tc(a, stream);
     } else {
@@ -278,7 +170,7 @@ cudaError_t launch_attn_step_shared(const AttnStepArgs &args, cudaStream_t strea
     }
     if (e != cudaSuccess) return e;
     return with_core(a.D, a.G, a.dtype, [&](auto core) -> cudaError_t {
-        return launch_rest<decltype(core)>(a, stream);
+        return launch_rest<decltype(core)>(a, device_sms(), stream);
     });
 }
 

@@ -68,6 +68,14 @@ __device__ __forceinline__ int32_t first_worker(int64_t units, int64_t first, in
     return (int32_t)(((first + 1) * grid - 1) / units);
 }
 
+// The workers whose shares hold an item's units from `first` on, as the last of
+// them, `c`, writes them down for the join: {the first of them, their number,
+// times two, and one if the first has another item before}.
+__device__ __forceinline__ int2 owners_of(int64_t units, int64_t first, int32_t c, int32_t grid) {
+    const int32_t c0 = first_worker(units, first, grid);
+    return make_int2(c0, (c - c0 + 1) * 2 + (share_start(units, c0, grid) != first));
+}
+
 // The shared tokens' work: the tiles of every item (a key-value head and a block
 // of a.prefix_rows rows, a row being sequence * G + query head of the group) form
 // a line, of which every CTA takes an equal share.  An item's pieces are counted
@@ -143,8 +151,9 @@ __device__ __forceinline__ Span span_of(const AttnStepArgs &a, int32_t s) {
     return {0, len};
 }
 // (len + kTile - 1 would overflow in the last tile below 2^31)
+template <int TILE = kTile>
 __device__ __forceinline__ int32_t tiles_of(int32_t len) {
-    return len / kTile + (len % kTile != 0);
+    return len / TILE + (len % TILE != 0);
 }
 
 // The first sequence that holds all `shared` tokens (N: none does), for the
@@ -165,7 +174,7 @@ __device__ __forceinline__ int32_t sharing_sequence(const AttnStepArgs &a, int32
 }
 
 // Prefix sums of the sequences' tiles, each thread holding a run of sequences.
-template <int THREADS, bool SHARED>
+template <int THREADS, bool SHARED, int TILE = kTile>
 struct Line {
     int64_t total;   // tiles of all sequences
     int64_t before;  // tiles before this thread's run
@@ -177,7 +186,7 @@ struct Line {
         s1 = min(s0 + per, a.N);
         int64_t mine = 0;
         for (int32_t s = s0; s < s1; ++s) {
-            mine += tiles_of(span_of<SHARED>(a, s).len());
+            mine += tiles_of<TILE>(span_of<SHARED>(a, s).len());
             if (a.seq_lens[s] > (a.max_pages << a.page_shift)) *a.status = KDA_ERR_INVALID_ARG;
         }
         int64_t incl = mine;
@@ -196,13 +205,18 @@ struct Line {
         }
     }
     // The sequence of unit u (u < total * items) and the units before it, to
-    // *seq / *base in shared memory.
+    // *seq / *base in shared memory (`look`, without the barrier).
     __device__ void find(const AttnStepArgs &a, int64_t u, int32_t items, int32_t *seq,
+                         int64_t *base) const {
+        look(a, u, items, seq, base);
+        __syncthreads();
+    }
+    __device__ void look(const AttnStepArgs &a, int64_t u, int32_t items, int32_t *seq,
                          int64_t *base) const {
         int64_t b = before * items;
         if (u >= b) {
             for (int32_t s = s0; s < s1; ++s) {
-                const int64_t n = (int64_t)tiles_of(span_of<SHARED>(a, s).len()) * items;
+                const int64_t n = (int64_t)tiles_of<TILE>(span_of<SHARED>(a, s).len()) * items;
                 if (u < b + n) {
                     *seq = s;
                     *base = b;
@@ -211,13 +225,12 @@ struct Line {
                 b += n;
             }
         }
-        __syncthreads();
     }
     // The units before sequence `seq`, to *base in shared memory.
     __device__ void base_of(const AttnStepArgs &a, int32_t seq, int32_t items, int64_t *base) const {
         if (seq >= s0 && seq < s1) {
             int64_t b = before;
-            for (int32_t s = s0; s < seq; ++s) b += tiles_of(span_of<SHARED>(a, s).len());
+            for (int32_t s = s0; s < seq; ++s) b += tiles_of<TILE>(span_of<SHARED>(a, s).len());
             *base = b * items;
         }
         __syncthreads();
@@ -479,25 +492,53 @@ __device__ __forceinline__ float rest_of(float w, float hi) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(lo) : "f"(w - hi), "f"(hi * 0x1p-20f), "f"(fminf(hi, 0x1p-126f)));
     return lo;
 }
+// (FINITE: no value is an infinity, and lo may be 0)
+template <bool FINITE>
 __device__ __forceinline__ void split_weights(float w0, float w1, uint32_t &hi, uint32_t &lo) {
     hi = __byte_perm(__float_as_uint(w0), __float_as_uint(w1), 0x7632);
-    lo = tc::pack_bf16x2(rest_of(w0, __uint_as_float(hi << 16)),
-                         rest_of(w1, __uint_as_float(hi & 0xFFFF0000u)));
+    const float h0 = __uint_as_float(hi << 16), h1 = __uint_as_float(hi & 0xFFFF0000u);
+    lo = FINITE ? tc::pack_bf16x2(w0 - h0, w1 - h1)
+                : tc::pack_bf16x2(rest_of(w0, h0), rest_of(w1, h1));
 }
 
 //
-// A cache of 8-bit codes (C = int8_t) goes the same way: a code is an exact
-// bf16, so that its products with q and with the weights are those of the
+// A cache of 8-bit codes (C = int8_t) goes the same way: a code is exact in f16 and
+// in bf16, so that its products with q and with the weights are those of the
 // values up to the row's scale, which multiplies the score and the weight.  A
 // lane's 16-byte vectors hold twice as many channels: 16 (4 j + t) .. + 15 of
-// the keys and queries, 16 g .. + 15 (D = 64: 8 g .. + 7) of the values.  A code
-// becomes a bf16 by way of 128 + its low 7 bits (whose bit pattern is 0x4300 and
-// those bits), less 128, or less 256 where its sign is set (0x4300 and the sign
-// bit in the exponent): four instructions to two codes, with the byte permute.
-__device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t x /* 0x43cc43cc, cc the codes */) {
+// the keys and queries, 16 g .. + 15 (D = 64: 8 g .. + 7) of the values.
+//
+// What a code costs decides the kernel's speed (the byte permutes and bitwise
+// operations run at half the rate).  With u = code + 128 as the low byte of a
+// 16-bit number:
+//   * f16 (keys): 0x6400 | u is 1024 + u; less 1152.  The queries go to f16 too,
+//     each row times the power of two that brings its largest to 2^14 .. 2^15:
+//     exact down to 2^-31 of it, and what is smaller is off by 2^-39 of it;
+//   * bf16 (values, whose weights times scales need bf16's range): 0x4300 | u is
+//     v = 128 + u below u = 128 and 2 u from there on, so that with w = v - 256
+//     the code is w below 0 and w / 2 from there on, w - max(w / 2, 0): three
+//     operations that round nothing.
+__device__ __forceinline__ uint32_t codes_to_f16x2(uint32_t x /* 0x64uu64uu */) {
     uint32_t y;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x & 0xFF7FFF7Fu), "r"(x & 0xFF80FF80u));
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0xE480E480u));  // - 1152
     return y;
+}
+__device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t x /* 0x43uu43uu */) {
+    uint32_t w, h, y;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(w) : "r"(x), "r"(0xC380C380u));  // - 256
+    asm("fma.rn.relu.bf16x2 %0, %1, %2, %3;"                                // / 2 - 128, or 0
+        : "=r"(h)
+        : "r"(x), "r"(0x3F003F00u), "r"(0xC300C300u));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(w), "r"(h));
+    return y;
+}
+__device__ __forceinline__ void mma_16816_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint2 load_once8(const void *p) {
     uint2 x;
@@ -523,9 +564,38 @@ struct MmaCore {
 
     uint4 q[NT][J], k[2][KC], v[4][VV];
     float kf[2], vf[2];  // scales of tokens g and g + 8 (kScaled)
+    float qf[NT][2];     // what the queries' rows 2 t and 2 t + 1 were divided by (kScaled)
     float o[MT][NT][4], s[NT][4], ref[NT][2], sum[NT][2];
     float c2;
 
+    // Query rows of block n from bf16 to f16, and their factors.
+    __device__ void to_f16(int n) {
+        uint32_t top = 0;  // the row's largest magnitude
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const uint32_t x = (&q[n][j].x)[w], lo = x & 0x7FFFu, hi = x >> 16 & 0x7FFFu;
+                top = max(top, max(lo, hi));
+            }
+#pragma unroll
+        for (int x = 1; x < 4; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
+        // (an infinity or a NaN keeps the numbers beside it finite: exponent 254)
+        const uint32_t e = min(max(top >> 7, 27u), 254u);
+        const float f = __uint_as_float((268u - e) << 23);  // 2^(14 - (e - 127))
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                uint32_t &x = (&q[n][j].x)[w];
+                x = tc::pack_f16x2(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xFFFF0000u) * f);
+            }
+        // the factor back: rows are the accumulators' columns
+        const float back = __uint_as_float((e - 14u) << 23);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            qf[n][x] = __shfl_sync(0xffffffffu, back, (2 * (threadIdx.x & 3) + x) * 4);
+    }
     // first channel of the lane's j-th vector of a query row
     __device__ static int q_channel(int j, int t) {
         return kScaled ? ((j >> 1) * 4 + t) * 16 + (j & 1) * 8 : (j * 4 + t) * 8;
@@ -542,6 +612,7 @@ struct MmaCore {
             for (int j = 0; j < J; ++j)
                 q[n][j] = h < rows ? *reinterpret_cast<const uint4 *>(row(h) + q_channel(j, t))
                                    : make_uint4(0, 0, 0, 0);
+            if constexpr (kScaled) to_f16(n);
             ref[n][0] = ref[n][1] = -INFINITY;
             sum[n][0] = sum[n][1] = 0.f;
 #pragma unroll
@@ -589,12 +660,61 @@ struct MmaCore {
             for (int r = 0; r < 2; ++r) vf[r] = g + 8 * r < n ? __ldg(vsp + g + 8 * r) : 0.f;
         }
     }
+    // 16 tokens that have been copied to shared memory (kda_attn_flat.cuh): keys,
+    // values, then the scales of both.
+    static constexpr uint32_t kRowBytes = D * sizeof(C), kHalf = kWarpTokens * kRowBytes;
+    static constexpr uint32_t kBlockBytes = 2 * kHalf + (kScaled ? 2 * kWarpTokens * 4 : 0);
+    __device__ void fetch(const uint8_t *from) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int j = 0; j < KC; ++j)
+                k[r][j] = *reinterpret_cast<const uint4 *>(from + (g + 8 * r) * kRowBytes +
+                                                           (j * 4 + t) * 16);
+        from += kHalf;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const uint8_t *row = from + (2 * t + (r & 1) + 8 * (r >> 1)) * kRowBytes;
+#pragma unroll
+            for (int c = 0; c < VV; ++c) {
+                if constexpr (kScaled && D == 64) {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(row + g * 8);
+                    v[r][c].x = x.x;
+                    v[r][c].y = x.y;
+                } else {
+                    v[r][c] = *reinterpret_cast<const uint4 *>(row + c * 128 + g * 16);
+                }
+            }
+        }
+        if constexpr (kScaled) {
+            const float *f = reinterpret_cast<const float *>(from + kHalf);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                kf[r] = f[g + 8 * r];
+                vf[r] = f[kWarpTokens + g + 8 * r];
+            }
+        }
+    }
+    // Rows from n on of such a block, which nothing was copied to, as no product may see
+    // them: zero values (codes are finite as they are: zero scales will do).
+    __device__ static void clear_rest(uint8_t *block, int n) {
+        const int lane = threadIdx.x & 31;
+        if constexpr (kScaled) {
+            float *f = reinterpret_cast<float *>(block + 2 * kHalf);
+            if ((lane & 15) >= n) f[lane] = 0.f;
+        } else {
+            for (uint32_t i = n * kRowBytes / 16 + lane; i < kHalf / 16; i += 32)
+                reinterpret_cast<uint4 *>(block + kHalf)[i] = make_uint4(0, 0, 0, 0);
+        }
+    }
     __device__ void scores() {
         if constexpr (kScaled) {
+            float s2[NT][4];  // (two chains of products)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+                for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
 #pragma unroll
             for (int j = 0; j < KC; ++j)
 #pragma unroll
@@ -602,20 +722,22 @@ struct MmaCore {
                     uint32_t a[2][2];  // by token (g, g + 8) and channel pair
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const uint32_t x = (&k[r][j].x)[w];
-                        a[r][0] = codes_to_bf16x2(__byte_perm(x, 0x43434343u, 0x4140));
-                        a[r][1] = codes_to_bf16x2(__byte_perm(x, 0x43434343u, 0x4342));
+                        const uint32_t x = (&k[r][j].x)[w] ^ 0x80808080u;
+                        a[r][0] = codes_to_f16x2(__byte_perm(x, 0x64646464u, 0x4140));
+                        a[r][1] = codes_to_f16x2(__byte_perm(x, 0x64646464u, 0x4342));
                     }
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         const uint32_t *b = &q[n][2 * j + (w >> 1)].x + 2 * (w & 1);
-                        mma_16816(s[n], a[0][0], a[1][0], a[0][1], a[1][1], b[0], b[1]);
+                        mma_16816_f16(w & 1 ? s2[n] : s[n], a[0][0], a[1][0], a[0][1], a[1][1],
+                                      b[0], b[1]);
                     }
                 }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] *= kf[e >> 1];
+                for (int e = 0; e < 4; ++e)
+                    s[n][e] = (s[n][e] + s2[n][e]) * qf[n][e & 1] * kf[e >> 1];
         } else {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -675,7 +797,7 @@ struct MmaCore {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 uint32_t hi, lo;
-                split_weights(w[2 * e], w[2 * e + 1], hi, lo);
+                split_weights<kScaled>(w[2 * e], w[2 * e + 1], hi, lo);
                 p[n][0][e] = transpose_8x8(low ? lo : hi);
                 if (!FOLD) p[n][kParts - 1][e] = transpose_8x8(lo);
             }
@@ -698,7 +820,8 @@ struct MmaCore {
 #pragma unroll
                     for (int hi = 0; hi < 2; ++hi) {
                         const int word = w + r * (MT / 4);
-                        const uint32_t x = (&v[2 * hi][0].x)[word], y = (&v[2 * hi + 1][0].x)[word];
+                        const uint32_t x = (&v[2 * hi][0].x)[word] ^ 0x80808080u,
+                                       y = (&v[2 * hi + 1][0].x)[word] ^ 0x80808080u;
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const uint32_t z = __byte_perm(x, y, h ? 0x7362 : 0x5140);
@@ -731,6 +854,32 @@ struct MmaCore {
                 product(i, a);
             }
         }
+    }
+    // The warp's state, MT channels of a query head at a time from the lane that
+    // holds them: put(head, first channel, weighted sums, maximum (base 2), sum).
+    template <class Put>
+    __device__ void finish_rows(bool seen, int rows, Put put) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int h = n * 8 + 2 * t + e;
+                float l = sum[n][e];
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+#pragma unroll
+                for (int hi = 0; hi < 2; ++hi) {
+                    float y[MT];
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        y[i] = o[i][n][e + 2 * hi];
+                        if (FOLD) y[i] += __shfl_xor_sync(0xffffffffu, y[i], 2);
+                    }
+                    const int ch = !kScaled && VC == 2 ? 64 * hi + 8 * g : 2 * MT * g + MT * hi;
+                    if (h < rows) put(h, ch, y, state_max(ref[n][e], seen), l);
+                }
+            }
     }
     __device__ void finish(float *sacc, float *sm, float *sl, bool seen) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -938,6 +1087,9 @@ attn_step_kernel(const AttnStepArgs a, float *part) {
             }
         }
         __syncthreads();
+        if (SHARED && tid == 0 && tile1 == tiles)
+            a.owners[(int64_t)s * items + item] =
+                owners_of(units, base + (int64_t)item * tiles, c, grid);
         u += tile1 - tile0;
     }
     if (SHARED) tc::pdl_wait_primaries();
@@ -1135,27 +1287,32 @@ int line_grid(const AttnStepArgs &a, int sms) {
 }
 
 template <class Core>
-cudaError_t launch_core(const AttnStepArgs &a, cudaStream_t stream) {
-    constexpr int D = Core::kD, R = Core::kRows;
-    const int sms = device_sms();
-    if (!sms) return cudaErrorUnknown;
-    const int64_t capacity = (int64_t)a.max_pages << a.page_shift;
-    const int64_t items = step_items<Core>(a), slots = (int64_t)sms * Core::kCtas;
+int step_direct_ctas(const AttnStepArgs &a, int sms) {
+    return direct_ctas(step_items<Core>(a), (int64_t)a.max_pages << a.page_shift,
+                       (int64_t)sms * Core::kCtas);
+}
+
+template <class Core>
+cudaError_t launch_direct(const AttnStepArgs &a, int ctas, cudaStream_t stream) {
+    const int64_t items = step_items<Core>(a);
+    if (items * ctas > INT32_MAX) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.stream = stream;
     cfg.attrs = attr;
-    const int ctas = direct_ctas(items, capacity, slots);
-    if (ctas > 0) {
-        if (items * ctas > INT32_MAX) return cudaErrorInvalidValue;
-        cfg.gridDim = dim3((unsigned)(items * ctas));
-        cfg.blockDim = dim3(kThreads);
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)ctas;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, attn_step_direct_kernel<Core>, a);
-    }
+    cfg.gridDim = dim3((unsigned)(items * ctas));
+    cfg.blockDim = dim3(kThreads);
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_step_direct_kernel<Core>, a);
+}
+
+template <class Core>
+cudaError_t launch_line(const AttnStepArgs &a, int sms, cudaStream_t stream) {
+    constexpr int D = Core::kD, R = Core::kRows;
+    const int64_t items = step_items<Core>(a);
     const int grid = line_grid<Core>(a, sms);
     float *part = static_cast<float *>(a.workspace);
     attn_step_kernel<Core, false><<<grid, kThreads, 0, stream>>>(a, part);
@@ -1165,10 +1322,13 @@ cudaError_t launch_core(const AttnStepArgs &a, cudaStream_t stream) {
     // head; else all of an item's
     const int32_t most_rows = std::min<int32_t>(R, a.G), per = items < kFewItems ? 1 : most_rows;
     const bool by_item = items < grid;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr = follows_on();
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
     cfg.gridDim = dim3((unsigned)(by_item ? items : grid - 1), (unsigned)((most_rows + per - 1) / per));
     cfg.blockDim = dim3(kJoinThreads);
-    attr[0] = follows_on();
-    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, attn_join_kernel<D, R>, a, static_cast<const float *>(part),
                               (int32_t)grid, per, (int32_t)by_item);
 }
@@ -1178,14 +1338,6 @@ template <class Core>
 size_t line_bytes(int sms) {
     return (size_t)sms * Core::kCtas * 2 * Core::kRows * (Core::kD + 2) * sizeof(float);
 }
-// Scratch of the step (the direct kernel needs none).
-template <class Core>
-size_t part_bytes(const AttnStepArgs &a, int sms) {
-    const int64_t slots = (int64_t)sms * Core::kCtas;
-    if (direct_ctas(step_items<Core>(a), (int64_t)a.max_pages << a.page_shift, slots)) return 0;
-    return line_bytes<Core>(sms);
-}
-
 // The core of a problem whose cache has the queries' type, as a call of f(Core{}).
 template <class F>
 auto with_core(int32_t D, int32_t G, int32_t dtype, F f) {

@@ -6,7 +6,7 @@
 // A token's key and value are 2 D bytes of codes and 8 of scales to a key-value
 // head, half of what a bf16 cache holds.  The scales stay outside the products,
 // which are exact products of codes in fp32 (bf16 operands hold codes exactly).
-#include "kda_attn_step.cuh"
+#include "kda_attn_flat.cuh"
 
 namespace kda {
 namespace {
@@ -38,20 +38,44 @@ auto with_core_q8(int32_t D, int32_t G, int32_t dtype, F f) {
     }
 }
 
+// Scratch: workers' parts, then owners (none for short tables).
+template <class Core>
+size_t q8_bytes(const AttnStepArgs &a, int sms) {
+    if (step_direct_ctas<Core>(a, sms)) return 0;
+    if constexpr (Core::kAhead) return flat_part_bytes<Core>(sms) + owners_bytes<Core>(a);
+    else return line_bytes<Core>(sms);
+}
+
+template <class Core>
+cudaError_t launch_q8(AttnStepArgs a, int sms, cudaStream_t stream) {
+    if (const int ctas = step_direct_ctas<Core>(a, sms)) return launch_direct<Core>(a, ctas, stream);
+    if constexpr (Core::kAhead) {
+        float *part = static_cast<float *>(a.workspace);
+        a.owners = reinterpret_cast<int2 *>(static_cast<char *>(a.workspace) +
+                                            flat_part_bytes<Core>(sms));
+        const cudaError_t e = launch_flat<Core, false>(a, part, sms, stream);
+        return e != cudaSuccess ? e : launch_rows_join<Core, false>(a, part, sms, stream);
+    } else {
+        return launch_line<Core>(a, sms, stream);
+    }
+}
+
 }  // namespace
 
 cudaError_t attn_step_q8_workspace_bytes(const AttnStepArgs &a, size_t *bytes) {
     const int sms = device_sms();
     if (!sms) return cudaErrorUnknown;
     *bytes = with_core_q8(a.D, a.G, a.dtype, [&](auto core) -> size_t {
-        return part_bytes<decltype(core)>(a, sms);
+        return q8_bytes<decltype(core)>(a, sms);
     });
     return cudaSuccess;
 }
 
 cudaError_t launch_attn_step_q8(const AttnStepArgs &a, cudaStream_t stream) {
+    const int sms = device_sms();
+    if (!sms) return cudaErrorUnknown;
     return with_core_q8(a.D, a.G, a.dtype, [&](auto core) -> cudaError_t {
-        return launch_core<decltype(core)>(a, stream);
+        return launch_q8<decltype(core)>(a, sms, stream);
     });
 }
 
