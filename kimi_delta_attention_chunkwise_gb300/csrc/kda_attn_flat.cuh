@@ -206,7 +206,7 @@ attn_flat_kernel(const AttnStepArgs a, float *part) {
             }
             const uint32_t blocks_good = good >> (x * SUB);
             const int32_t left = here.end - here.token();
-#pragma unroll 1
+#pragma unroll
             for (int b = 0; b < SUB; ++b) {
                 const bool ok = blocks_good >> b & 1;
                 const int n = min(kWarpTokens, left - b * kWarpTokens);

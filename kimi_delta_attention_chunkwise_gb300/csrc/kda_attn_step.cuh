@@ -514,7 +514,12 @@ __device__ __forceinline__ void split_weights(float w0, float w1, uint32_t &hi, 
 //   * f16 (keys): 0x6400 | u is 1024 + u; less 1152.  The queries go to f16 too,
 //     each row times the power of two that brings its largest to 2^14 .. 2^15:
 //     exact down to 2^-31 of it, and what is smaller is off by 2^-39 of it;
-//   * bf16 (values, whose weights times scales need bf16's range): 0x4300 | u is
+//   * f16 for the values, too, with at most 4 query heads, where the weights' low
+//     parts have columns of their own and go there times 2^11.  The weights are
+//     lifted by 2^7 and the scales divided by vref, a power of two that none has
+//     passed so far, so that the product lies below 2^15: weights down to 2^-28 of
+//     a row's largest keep 2^-15, smaller ones 2^-43 of the largest, times vref;
+//   * bf16 for the values else (whose range needs no reference): 0x4300 | u is
 //     v = 128 + u below u = 128 and 2 u from there on, so that with w = v - 256
 //     the code is w below 0 and w / 2 from there on, w - max(w / 2, 0): three
 //     operations that round nothing.
@@ -534,11 +539,19 @@ __device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t x /* 0x43uu43uu */)
 }
 __device__ __forceinline__ void mma_16816_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                               uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// (the product alone)
+__device__ __forceinline__ void mma_16816_f16_first(float (&c)[4], uint32_t a0, uint32_t a1,
+                                                    uint32_t a2, uint32_t a3, uint32_t b0,
+                                                    uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint2 load_once8(const void *p) {
     uint2 x;
@@ -561,6 +574,12 @@ struct MmaCore {
     static constexpr int KC = kScaled ? J / 2 : J, VV = kScaled ? 1 : VC;  // as they lie in the cache
     static constexpr int MT = D / 16;  // channel tiles of O^T
     static constexpr float kMoveBy = 8.f;
+    // weights and values as f16 (kScaled): the weights' lift, and what the low
+    // parts are multiplied by
+    static constexpr bool kF16 = kScaled && FOLD;
+    static constexpr float kLift = kF16 ? 7.f : 0.f, kLow = kF16 ? 0x1p11f : 1.f;
+    static constexpr float kNoRef = kF16 ? -FLT_MAX : -INFINITY;
+    float vref, vback;  // (kF16) the scales' reference, its reciprocal
 
     uint4 q[NT][J], k[2][KC], v[4][VV];
     float kf[2], vf[2];  // scales of tokens g and g + 8 (kScaled)
@@ -605,6 +624,7 @@ struct MmaCore {
     __device__ void init(Row row, int rows, float scale) {
         const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
         c2 = scale * kLog2e;
+        vref = vback = 0.f;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int h = FOLD ? g & 3 : n * 8 + g;
@@ -613,7 +633,7 @@ struct MmaCore {
                 q[n][j] = h < rows ? *reinterpret_cast<const uint4 *>(row(h) + q_channel(j, t))
                                    : make_uint4(0, 0, 0, 0);
             if constexpr (kScaled) to_f16(n);
-            ref[n][0] = ref[n][1] = -INFINITY;
+            ref[n][0] = ref[n][1] = kNoRef;
             sum[n][0] = sum[n][1] = 0.f;
 #pragma unroll
             for (int i = 0; i < MT; ++i)
@@ -712,10 +732,6 @@ struct MmaCore {
         if constexpr (kScaled) {
             float s2[NT][4];  // (two chains of products)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
-#pragma unroll
             for (int j = 0; j < KC; ++j)
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
@@ -729,8 +745,11 @@ struct MmaCore {
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         const uint32_t *b = &q[n][2 * j + (w >> 1)].x + 2 * (w & 1);
-                        mma_16816_f16(w & 1 ? s2[n] : s[n], a[0][0], a[1][0], a[0][1], a[1][1],
-                                      b[0], b[1]);
+                        float(&to)[4] = w & 1 ? s2[n] : s[n];
+                        if (j == 0 && w < 2)
+                            mma_16816_f16_first(to, a[0][0], a[1][0], a[0][1], a[1][1], b[0], b[1]);
+                        else
+                            mma_16816_f16(to, a[0][0], a[1][0], a[0][1], a[1][1], b[0], b[1]);
                     }
                 }
 #pragma unroll
@@ -753,8 +772,105 @@ struct MmaCore {
             }
         }
     }
+    // values() for kF16
+    __device__ void values_f16(int n_tok) {
+        const int g = (threadIdx.x & 31) >> 2;
+        const bool low = threadIdx.x & 2;  // columns 4-7
+        if (n_tok < kWarpTokens) {
+            if (g >= n_tok) s[0][0] = s[0][1] = -INFINITY;
+            if (g + 8 >= n_tok) s[0][2] = s[0][3] = -INFINITY;
+        }
+        float top[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) top[e] = fmaxf(s[0][e], s[0][e + 2]) * c2;
+        const float v_top = fmaxf(vf[0], vf[1]);
+        // (NaN compares false: a NaN score moves nothing and shows in the sums, a
+        // NaN scale in the weights)
+        const bool move = top[0] > ref[0][0] + (kMoveBy + kLift) ||
+                          top[1] > ref[0][1] + (kMoveBy + kLift) || v_top > vref;
+        if (__any_sync(0xffffffffu, move)) {
+            float f[2], m = v_top;
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+            float fv = 1.f;
+            if (m > vref) {  // the power of two above it
+                const uint32_t e = min((__float_as_uint(m) >> 23) + 1, 253u);
+                vback = __uint_as_float((254 - e) << 23);
+                fv = vref * vback;
+                vref = __uint_as_float(e << 23);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float r = fmaxf(top[e], ref[0][e] + kLift);
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, x));
+                r = fmaxf(r - kLift, -FLT_MAX);
+                f[e] = exp2f(ref[0][e] - r);
+                ref[0][e] = r;
+                sum[0][e] *= f[e];
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][0][e] *= f[e & 1] * fv;
+        }
+        uint32_t p[2];  // by half of the tokens
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float by = vf[h] * vback;
+            float w[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                w[e] = tc::exp2_approx(fmaf(s[0][2 * h + e], c2, -ref[0][e]));
+                sum[0][e] += w[e];
+                w[e] *= by;
+            }
+            const __half2 hi = __floats2half2_rn(w[0], w[1]);
+            const float2 back = __half22float2(hi);
+            const __half2 lo = __floats2half2_rn((w[0] - back.x) * kLow, (w[1] - back.y) * kLow);
+            const __half2 mine = low ? lo : hi;
+            p[h] = transpose_8x8(*reinterpret_cast<const uint32_t *>(&mine));
+        }
+        // rows g and g + 8 of channel tile i are bytes i and MT + i of a lane's
+        // vectors; words of four bytes at a time
+#pragma unroll
+        for (int w = 0; w < MT / 4; ++w) {
+            uint32_t a[4][4];
+            value_words<0x64646464u>(w, a);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                mma_16816_f16(o[4 * w + c][0], codes_to_f16x2(a[c][0]), codes_to_f16x2(a[c][1]),
+                              codes_to_f16x2(a[c][2]), codes_to_f16x2(a[c][3]), p[0], p[1]);
+        }
+    }
+    // The codes plus 128 of word w of the lane's value vectors (kScaled), below the
+    // bytes of MAGIC: by byte of the word, then operand register.
+    template <uint32_t MAGIC>
+    __device__ void value_words(int w, uint32_t (&a)[4][4]) const {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
+                const int word = w + r * (MT / 4);
+                const uint32_t x = (&v[2 * hi][0].x)[word] ^ 0x80808080u,
+                               y = (&v[2 * hi + 1][0].x)[word] ^ 0x80808080u;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t z = __byte_perm(x, y, h ? 0x7362 : 0x5140);
+                    a[2 * h][r + 2 * hi] = __byte_perm(z, MAGIC, 0x4140);
+                    a[2 * h + 1][r + 2 * hi] = __byte_perm(z, MAGIC, 0x4342);
+                }
+            }
+    }
     // weights of the tile's n tokens and their product with V
     __device__ void values(int n_tok) {
+        if constexpr (kF16) {
+            values_f16(n_tok);
+        } else {
+            values_bf16(n_tok);
+        }
+    }
+    __device__ void values_bf16(int n_tok) {
         const int g = (threadIdx.x & 31) >> 2;
         const bool low = FOLD && (threadIdx.x & 2);  // columns 4-7
         uint32_t p[NT][kParts][2];  // by part (high, low) and half of the tokens
@@ -810,29 +926,17 @@ struct MmaCore {
                     mma_16816(o[i][n], a[0], a[1], a[2], a[3], p[n][part][0], p[n][part][1]);
         };
         if constexpr (kScaled) {
-            // rows g and g + 8 of channel tile i are bytes i and MT + i of a lane's
-            // vectors; words of four bytes at a time
+            // (as in values_f16)
 #pragma unroll
             for (int w = 0; w < MT / 4; ++w) {
-                uint32_t a[4][4];  // by byte of the word, then operand register
+                uint32_t a[4][4];
+                value_words<0x43434343u>(w, a);
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
+                for (int c = 0; c < 4; ++c) {
 #pragma unroll
-                    for (int hi = 0; hi < 2; ++hi) {
-                        const int word = w + r * (MT / 4);
-                        const uint32_t x = (&v[2 * hi][0].x)[word] ^ 0x80808080u,
-                                       y = (&v[2 * hi + 1][0].x)[word] ^ 0x80808080u;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t z = __byte_perm(x, y, h ? 0x7362 : 0x5140);
-                            a[2 * h][r + 2 * hi] =
-                                codes_to_bf16x2(__byte_perm(z, 0x43434343u, 0x4140));
-                            a[2 * h + 1][r + 2 * hi] =
-                                codes_to_bf16x2(__byte_perm(z, 0x43434343u, 0x4342));
-                        }
-                    }
-#pragma unroll
-                for (int c = 0; c < 4; ++c) product(4 * w + c, a[c]);
+                    for (int r = 0; r < 4; ++r) a[c][r] = codes_to_bf16x2(a[c][r]);
+                    product(4 * w + c, a[c]);
+                }
             }
         } else {
 #pragma unroll
@@ -874,7 +978,8 @@ struct MmaCore {
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
                         y[i] = o[i][n][e + 2 * hi];
-                        if (FOLD) y[i] += __shfl_xor_sync(0xffffffffu, y[i], 2);
+                        if (FOLD) y[i] += __shfl_xor_sync(0xffffffffu, y[i], 2) * (1.f / kLow);
+                        if (kF16) y[i] *= vref;
                     }
                     const int ch = !kScaled && VC == 2 ? 64 * hi + 8 * g : 2 * MT * g + MT * hi;
                     if (h < rows) put(h, ch, y, state_max(ref[n][e], seen), l);
@@ -904,7 +1009,8 @@ struct MmaCore {
                                    : VC == 2 ? 64 * (e >> 1) + 8 * g + i
                                              : 8 * g + 4 * (e >> 1) + i;
                     float x = o[i][n][e];
-                    if (FOLD) x += __shfl_xor_sync(0xffffffffu, x, 2);
+                    if (FOLD) x += __shfl_xor_sync(0xffffffffu, x, 2) * (1.f / kLow);
+                    if (kF16) x *= vref;
                     if (h < kRows) sacc[h * D + ch] = x;
                 }
         }

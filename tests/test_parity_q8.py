@@ -326,6 +326,45 @@ def test_step_scales_far_from_one(dtype, d, size):
                _weights(dtype, d) + 2.0 ** -23 + n * 2.0 ** -24)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("HQ", [2, 8])
+@pytest.mark.parametrize("below", [8.0, 17.0, 26.0])
+def test_step_small_weights_beside_a_large_one(d, HQ, below):
+    """One key takes nearly all the weight and has a value of zero; the result is
+    what the others, e^-below of it each, leave.  Weights down to 2^-28 of the
+    largest keep 2^-15; below (26 / ln 2 = 37.5 powers of two) they are off by
+    2^-43 of it (and at most 4 query heads; with more, by 2^-15 of their own).
+    Scores of tens: the roundings of their exponentials are check()'s."""
+    n, page, HKV = 300, 16, 1
+    g = torch.Generator().manual_seed(d)
+    ks, vs, (kc, vc, kf, vf), table = paged_q8(6, [n], HKV, d, page)
+    q = torch.ones(1, HQ, d, dtype=torch.bfloat16)
+    # scores: token 0 has below more than the others'
+    k = torch.randint(-3, 4, (n, HKV, d), generator=g, dtype=torch.int8)
+    k[0] = 100
+    f = torch.full((n, HKV), below / (100 * d))
+    f[1:] *= 0.01
+    v = torch.randint(1, 128, (n, HKV, d), generator=g, dtype=torch.int8)
+    fv = 0.01 * (1 + torch.rand(n, HKV, generator=g))
+    fv[0] = 0.0
+    need = -(-n // page)
+    t = torch.arange(need, dtype=torch.int32)[None]
+    put = lambda shape, x, dt: _put_rows(torch.zeros(shape, dtype=dt), x, t, n)
+    cache = (put((need, HKV, page, d), k, torch.int8), put((need, HKV, page, d), v, torch.int8),
+             put((need, HKV, page), f, torch.float32), put((need, HKV, page), fv, torch.float32))
+    rows = [k.double() * f.double()[..., None], v.double() * fv.double()[..., None]]
+    for table_ in (t, widen(t)):
+        out, _ = kda.kda_attn_step_q8(q.cuda(), *(x.cuda() for x in cache), table_.cuda(), i32([n]),
+                                      1.0, out_f32=True)
+        # the small weights' 2^-43 of the largest, over what there is of them
+        small = n * 2.0 ** -43 * 2 * 127 * 0.02 / (n * math.exp(-below) * 0.5)
+        check_rows(q, [rows[0]], [rows[1]], 1.0, out, None, TWO_PARTS + small)
+
+
+def _put_rows(cache, rows, table, n):
+    return put(cache, rows, table, [0], [n])
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
 def test_step_rows_that_no_code_stands_for(dtype, d):
     """A NaN scale makes NaN of what attends to it, and of nothing else; a scale
