@@ -5,15 +5,18 @@
 // The units, 16 or 32 tokens of a (sequence, head) item, form one line, of which
 // every warp takes an equal share.  A warp's units come to shared memory in a
 // ring of its own, ahead of the one it works on and across the borders of items:
-// a block of 16 tokens is neighbouring rows of a page, one bulk copy of keys, one
-// of values (and two of scales).  Nothing in the loop waits for another warp, and
-// short items cost no start of their own.  At the end of an item the warp writes
+// neighbouring rows of a page, one copy of keys and one of values (and two of
+// scales).  Nothing in the loop waits for another warp, and short items cost no
+// start of their own.  At the end of an item the warp writes
 // the item's results, or its part's state for the join.  (kda_attn_step's kernel,
 // whose CTAs share a tile of 64 tokens and hold the next one's rows in registers,
 // gets 0.63 of the memory's rate out of 8-bit rows, half as many bytes to a tile,
 // and of sequences of a few hundred tokens.)
 #pragma once
 
+#include <cstring>
+
+#include "kda_attn_ptx.cuh"
 #include "kda_attn_step.cuh"
 
 namespace kda {
@@ -57,16 +60,23 @@ struct LineCursor {
 
 template <class Core>
 struct FlatCfg {
-    // what the CTAs of an SM leave of its shared memory, in blocks of 16 tokens to
-    // a warp
-    static constexpr int ROOM = (228 * 1024 / Core::kCtas - 2048) / (int)(kWarps * Core::kBlockBytes);
+    // what an SM's CTAs leave of its shared memory, in 16 tokens to a warp
+    static constexpr uint32_t BLOCK = 2 * kWarpTokens * Core::kRowBytes;
+    static constexpr uint32_t SCALES = Core::kScaled ? 2 * kWarpTokens * 4 : 0;
+    static constexpr int ROOM = (228 * 1024 / Core::kCtas - 3072) / (int)(kWarps * (BLOCK + SCALES));
     // 32 tokens to a unit where two units of them fit: what a unit costs besides
     // its tokens is a third of the instructions
     static constexpr int SUB = ROOM >= 4 ? 2 : 1, UNIT = SUB * kWarpTokens;
     static constexpr int RING = ROOM / SUB < 4 ? ROOM / SUB : 4;  // units
-    static constexpr uint32_t UNIT_BYTES = SUB * Core::kBlockBytes;
-    static constexpr uint32_t SMEM = kWarps * RING * UNIT_BYTES;
+    static constexpr uint32_t HALF = UNIT * Core::kRowBytes;      // a unit's keys, or values
+    static constexpr uint32_t SMEM = kWarps * RING * SUB * (BLOCK + SCALES);
     static_assert(RING >= 2 && RING * SUB <= 32, "shared memory of an SM");
+    static_assert(!Core::kScaled || (SUB == 2 && HALF % 1024 == 0), "swizzled tiles");
+};
+
+// 8-bit caches: the heads of their pages as tensors.
+struct FlatMaps {
+    CUtensorMap k, v;
 };
 
 // Neighbouring channels of a row's result from its state (mx = -inf: no keys).
@@ -76,7 +86,10 @@ __device__ __forceinline__ void store_run(const AttnStepArgs &a, int64_t head, i
     float y[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) y[i] = mx == -INFINITY ? 0.f : o[i] / sum;
-    if (a.out_f32) {
+    if constexpr (N < 4) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) store_out(a, head * D + ch + i, y[i]);
+    } else if (a.out_f32) {
 #pragma unroll
         for (int i = 0; i < N; i += 4)
             *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + head * D + ch + i) =
@@ -92,19 +105,26 @@ __device__ __forceinline__ void store_run(const AttnStepArgs &a, int64_t head, i
 
 template <class Core, bool SHARED>
 __global__ void __launch_bounds__(kThreads, Core::kCtas)
-attn_flat_kernel(const AttnStepArgs a, float *part) {
+attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ FlatMaps maps) {
     using T = typename Core::Type;
     using C = typename Core::Cell;
     using Cfg = FlatCfg<Core>;
     constexpr int D = Core::kD, R = Core::kRows, RING = Cfg::RING, SUB = Cfg::SUB;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ int64_t s_scan[kWarps], s_base[kWarps];
     __shared__ int32_t s_seq[kWarps];
     __shared__ uint64_t s_full[kWarps][RING];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     tc::pdl_launch_dependents();
+    if (Core::kScaled && (tc::smem_u32(smem) & 1023u)) {  // (the swizzle goes by addresses)
+        *a.status = KDA_ERR_CUDA;
+        return;
+    }
     const int32_t blocks = (a.G + R - 1) / R;  // blocks of query heads
     const int32_t items = a.HKV * blocks;
+    // rows of a copy, and copies to a unit
+    const int32_t box = Core::kScaled ? min(1 << a.page_shift, Cfg::UNIT) : kWarpTokens;
+    const int32_t copies = Cfg::UNIT / box;
     Line<kThreads, SHARED, Cfg::UNIT> line;
     line.scan(a, s_scan);
     const int64_t units = line.total * items;
@@ -122,7 +142,7 @@ attn_flat_kernel(const AttnStepArgs a, float *part) {
     }
     if (tid == 0) {
         for (int w = 0; w < kWarps; ++w)
-            for (int x = 0; x < RING; ++x) tc::mbar_init(&s_full[w][x], SUB);
+            for (int x = 0; x < RING; ++x) tc::mbar_init(&s_full[w][x], copies);
         tc::fence_mbar_init();
         tc::fence_proxy_async();
     }
@@ -130,12 +150,15 @@ attn_flat_kernel(const AttnStepArgs a, float *part) {
     const int32_t c = (int32_t)blockIdx.x * kWarps + warp;  // this worker
     if (c < grid) {
         const int64_t u0 = share_start(units, c, grid), u1 = share_start(units, c + 1, grid);
-        uint8_t *ring = smem + warp * RING * Cfg::UNIT_BYTES;
+        uint8_t *ring = smem + warp * (RING * 2 * Cfg::HALF);
+        float *scales = reinterpret_cast<float *>(smem + kWarps * RING * 2 * Cfg::HALF) +
+                        warp * (RING * 2 * Cfg::UNIT);  // (kScaled)
         uint64_t *full = s_full[warp];
         LineCursor<SHARED, Cfg::UNIT> here, ahead;
         here.seek(a, blocks, s_seq[warp], s_base[warp], u0);
         ahead = here;
-        // lane i < SUB: the i-th block of the unit at `ahead`, and its page's entry
+        // lane i < SUB: the i-th 16 tokens of the unit at `ahead`, and the entry of the
+        // page that they lie in
         const int32_t mine = min(lane, SUB - 1) * kWarpTokens;
         auto entry_of = [&]() -> int32_t {
             const int32_t tok = ahead.token() + mine;
@@ -152,23 +175,29 @@ attn_flat_kernel(const AttnStepArgs a, float *part) {
             if (au >= u1) return;
             const int32_t tok = ahead.token() + mine, n = min(kWarpTokens, ahead.end - tok);
             const bool there = page >= 0 && page < a.num_pages, ok = there && n > 0;
-            if (lane < SUB) {
-                if (ok) {
-                    const int64_t row = (((int64_t)page * a.HKV + ahead.kvh) << a.page_shift) +
-                                        (tok & ((1 << a.page_shift) - 1));
-                    uint8_t *to = ring + x * Cfg::UNIT_BYTES + lane * Core::kBlockBytes;
-                    const uint32_t rows = n * Core::kRowBytes;
-                    tc::mbar_arrive_expect_tx(&full[x], 2 * rows + (Core::kScaled ? 128 : 0));
-                    tc::bulk_g2s(to, static_cast<const C *>(a.k_cache) + row * D, rows, &full[x]);
-                    tc::bulk_g2s(to + Core::kHalf, static_cast<const C *>(a.v_cache) + row * D,
-                                 rows, &full[x]);
-                    if constexpr (Core::kScaled) {  // (all 16, which lie in the page)
-                        tc::bulk_g2s(to + 2 * Core::kHalf, a.k_scale + row, 64, &full[x]);
-                        tc::bulk_g2s(to + 2 * Core::kHalf + 64, a.v_scale + row, 64, &full[x]);
-                    }
-                } else {
-                    if (!there) *a.status = KDA_ERR_INVALID_ARG;
+            if (n > 0 && !there) *a.status = KDA_ERR_INVALID_ARG;
+            if (lane < copies) {
+                const int64_t z = (int64_t)page * a.HKV + ahead.kvh, row = z << a.page_shift;
+                const int32_t at = tok & ((1 << a.page_shift) - 1);
+                uint8_t *to = ring + x * (2 * Cfg::HALF) + mine * Core::kRowBytes;
+                if (!ok) {
                     tc::mbar_arrive(&full[x]);
+                } else if constexpr (Core::kScaled) {
+                    // whole boxes: what lies behind the sequence is codes like any,
+                    // whose scales will be put to 0
+                    tc::mbar_arrive_expect_tx(&full[x], box * (2 * Core::kRowBytes + 8));
+                    tc::tma_load_3d(to, &maps.k, 0, at, (int32_t)z, &full[x]);
+                    tc::tma_load_3d(to + Cfg::HALF, &maps.v, 0, at, (int32_t)z, &full[x]);
+                    float *f = scales + x * (2 * Cfg::UNIT) + mine;
+                    tc::bulk_g2s(f, a.k_scale + row + at, box * 4, &full[x]);
+                    tc::bulk_g2s(f + Cfg::UNIT, a.v_scale + row + at, box * 4, &full[x]);
+                } else {
+                    const uint32_t bytes = n * Core::kRowBytes;
+                    tc::mbar_arrive_expect_tx(&full[x], 2 * bytes);
+                    tc::bulk_g2s(to, static_cast<const C *>(a.k_cache) + (row + at) * D, bytes,
+                                 &full[x]);
+                    tc::bulk_g2s(to + Cfg::HALF, static_cast<const C *>(a.v_cache) + (row + at) * D,
+                                 bytes, &full[x]);
                 }
             }
             constexpr uint32_t all = (1u << SUB) - 1;
@@ -189,6 +218,7 @@ attn_flat_kernel(const AttnStepArgs a, float *part) {
 #pragma unroll
         for (int x = 0; x < RING; ++x) copy_next(x);
         Core core;
+        core.places();
         bool fresh = true, seen = false, first_item = true;
         int32_t x = 0;
         int64_t u = u0;
@@ -211,13 +241,23 @@ attn_flat_kernel(const AttnStepArgs a, float *part) {
                 const bool ok = blocks_good >> b & 1;
                 const int n = min(kWarpTokens, left - b * kWarpTokens);
                 if (ok) {
-                    uint8_t *block = ring + x * Cfg::UNIT_BYTES + b * Core::kBlockBytes;
+                    uint8_t *keys = ring + x * (2 * Cfg::HALF) + b * kWarpTokens * Core::kRowBytes;
+                    uint8_t *values = keys + Cfg::HALF;
+                    float *f = scales + x * (2 * Cfg::UNIT) + b * kWarpTokens;
                     if (n < kWarpTokens) {
-                        Core::clear_rest(block, n);
+                        // behind the sequence: zero values, or scales, since 0 times
+                        // an infinity or a NaN would be a NaN
+                        if constexpr (Core::kScaled) {
+                            if ((lane & 15) >= n) f[(lane & 15) + (lane >> 4) * Cfg::UNIT] = 0.f;
+                        } else {
+                            for (uint32_t i = n * Core::kRowBytes / 16 + lane;
+                                 i < kWarpTokens * Core::kRowBytes / 16; i += 32)
+                                reinterpret_cast<uint4 *>(values)[i] = make_uint4(0, 0, 0, 0);
+                        }
                         tc::fence_proxy_async();  // before copies to this place
                         __syncwarp();
                     }
-                    core.fetch(block);
+                    core.fetch(keys, values, f, f + Cfg::UNIT);
                 }
                 if (b == SUB - 1) {
                     __syncwarp();
@@ -280,18 +320,31 @@ attn_flat_kernel(const AttnStepArgs a, float *part) {
     if (SHARED) tc::pdl_wait_primaries();
 }
 
+// N neighbouring floats, N = 1, 2 or 4
+template <int N>
+__device__ __forceinline__ void load_run(const float *from, float (&x)[N]) {
+    if constexpr (N == 4) {
+        const float4 y = *reinterpret_cast<const float4 *>(from);
+        x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+    } else if constexpr (N == 2) {
+        const float2 y = *reinterpret_cast<const float2 *>(from);
+        x[0] = y.x; x[1] = y.y;
+    } else {
+        x[0] = *from;
+    }
+}
+
 // Joins what workers have left of every row: parts of its item, or its item's
 // state (kda_attn_step_q8's are results already), and its states over the shared
 // tokens.  `parts` warps to a row, so many rows to a CTA as its 8 warps have;
-// a row's maxima and sums one to a lane, its weighted sums four loads abreast.
-// tile: tokens of a unit of the line.
+// a row's maxima and sums one to a lane, its weighted sums eight loads abreast.
 template <int D, int R, bool SHARED>
 __global__ void __launch_bounds__(kJoinThreads) attn_rows_join_kernel(const AttnStepArgs a,
                                                                       const float *part,
                                                                       int32_t parts) {
     constexpr int N = (D + 31) / 32;  // columns per lane
     __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, col = lane * N;
     const int32_t blocks = (a.G + R - 1) / R;
     const int32_t abreast = kJoinWarps / parts;  // rows of the CTA
     const int64_t row = (int64_t)blockIdx.x * abreast + warp / parts, rows = (int64_t)a.N * a.HQ;
@@ -299,39 +352,37 @@ __global__ void __launch_bounds__(kJoinThreads) attn_rows_join_kernel(const Attn
     const int32_t hq = row < rows ? (int32_t)(row - (int64_t)s * a.HQ) : 0;
     const int32_t kvh = hq / a.G, block = (hq - kvh * a.G) / R, r = hq - kvh * a.G - block * R;
     const Span span = span_of<SHARED>(a, s);
+    const PrefixState states = prefix_state(a, D, 0);
     // the kernels before this one have ended
     tc::pdl_wait_primaries();
     const int2 who = a.owners[((int64_t)s * a.HKV + kvh) * blocks + block];
     int32_t own = span.len() > 0 ? who.y >> 1 : 0;
-    const int32_t pieces =
-        SHARED && span.first > 0 ? prefix_state(a, D, 0).pieces[row < rows ? row : 0] : 0;
+    const int32_t pieces = SHARED && span.first > 0 ? states.pieces[row < rows ? row : 0] : 0;
     const bool done = !SHARED && own <= 1;  // written by the worker, or there were no keys
-    if (row >= rows || done) own = 0;
     const int32_t all = row >= rows || done ? 0 : own + pieces;
+    // state i's weighted sums, maximum and sum: a worker's slot, or a piece (its
+    // item's state: the last one) of arrays over the rows
+    const float *slots = part + (int64_t)who.x * 2 * (R * (D + 2));
+    const bool apart = own > 1;
+    auto slot_of = [&](int32_t i) -> const float * {
+        return slots + (i * 2 + (i == 0 ? who.y & 1 : 0)) * (int64_t)(R * (D + 2));
+    };
+    auto piece_of = [&](int32_t i) -> int64_t {
+        return (int64_t)(i < own ? a.splits - 1 : i - own) * rows + row;
+    };
+    auto sums_of = [&](int32_t i) -> const float * {
+        return i < own && apart ? slot_of(i) + r * D : states.o + piece_of(i) * D;
+    };
     float mx = -INFINITY, l = 0.f, o[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) o[j] = 0.f;
-    // state i: its weighted sums, maximum and sum
-    auto state_of = [&](int32_t i, const float *&so, const float *&sm, const float *&sl) {
-        if (i < own && own > 1) {
-            const float *slot =
-                part + ((int64_t)(who.x + i) * 2 + (i == 0 ? who.y & 1 : 0)) * (R * (D + 2));
-            so = slot + r * D;
-            sm = slot + R * D + r;
-            sl = slot + R * D + R + r;
-        } else {
-            const PrefixState p = prefix_state(a, D, i < own ? a.splits - 1 : i - own);
-            so = p.o + row * D;
-            sm = p.m + row;
-            sl = p.l + row;
-        }
-    };
     for (int32_t i0 = warp % parts; i0 < all; i0 += 32 * parts) {
         const int32_t i = i0 + lane * parts;
         float m = -INFINITY, sum = 0.f;
         if (i < all) {
-            const float *so, *sm, *sl;
-            state_of(i, so, sm, sl);
+            const bool slot = i < own && apart;
+            const float *sm = slot ? slot_of(i) + R * D + r : states.m + piece_of(i);
+            const float *sl = slot ? sm + R : states.l + piece_of(i);
             m = *sm;
             sum = *sl;
         }
@@ -348,20 +399,22 @@ __global__ void __launch_bounds__(kJoinThreads) attn_rows_join_kernel(const Attn
 #pragma unroll
         for (int j = 0; j < N; ++j) o[j] *= f;
         const int32_t n = min(32, (all - i0 + parts - 1) / parts);
-#pragma unroll 4
+#pragma unroll 8
         for (int32_t k = 0; k < n; ++k) {
             const float wk = __shfl_sync(0xffffffffu, w, k);
-            const float *so, *sm, *sl;
-            state_of(i0 + k * parts, so, sm, sl);
+            float x[N];
+            if (col < D) {
+                load_run(sums_of(i0 + k * parts) + col, x);
 #pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (D >= 32 || lane < D) o[j] += so[j * 32 + lane] * wk;
+                for (int j = 0; j < N; ++j) o[j] += x[j] * wk;
+            }
         }
     }
     if (parts > 1) {
+        if (col < D) {
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (D >= 32 || lane < D) s_o[warp][j * 32 + lane] = o[j];
+            for (int j = 0; j < N; ++j) s_o[warp][col + j] = o[j];
+        }
         if (lane == 0) {
             s_m[warp] = mx;
             s_l[warp] = l;
@@ -380,14 +433,12 @@ __global__ void __launch_bounds__(kJoinThreads) attn_rows_join_kernel(const Attn
             l += s_l[warp + w] * fw;
 #pragma unroll
             for (int j = 0; j < N; ++j)
-                if (D >= 32 || lane < D) o[j] += s_o[warp + w][j * 32 + lane] * fw;
+                if (col < D) o[j] += s_o[warp + w][col + j] * fw;
         }
         mx = top;
     }
-    if (row >= rows || done) return;
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-        if (D >= 32 || lane < D) store_row(a, row, D, j * 32 + lane, o[j], mx, l);
+    if (row >= rows || done || col >= D) return;
+    store_run(a, row, D, col, o, mx, l);
 }
 
 // Warps to a row of the join: as many as keep the GPU's warps busy.
@@ -424,15 +475,44 @@ cudaError_t launch_rows_join(const AttnStepArgs &a, const float *part, int sms,
                               parts);
 }
 
+// A cache of 8-bit codes [heads of pages, page, D] as a 3-D map whose box is up to
+// 32 rows of one page, swizzled by its rows' width.
+inline bool encode_codes_map(CUtensorMap *m, const void *base, int32_t d, int32_t page,
+                             int32_t heads, int32_t unit) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)page, (cuuint64_t)heads};
+    const cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)page * d};
+    const cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)std::min(page, unit), 1u};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The flat kernel (SHARED: a programmatic dependent of the kernel before).
 template <class Core, bool SHARED>
-cudaError_t launch_flat(const AttnStepArgs &a, float *part, int sms, cudaStream_t stream) {
+cudaError_t launch_flat(AttnStepArgs a, float *part, int sms, cudaStream_t stream) {
     const int64_t capacity = (int64_t)a.max_pages << a.page_shift;
     // one wave, and no more warps than the longest possible line has units
     const int64_t most = step_items<Core>(a) * (capacity / FlatCfg<Core>::UNIT + 1);
     const int64_t grid = std::min((int64_t)sms * Core::kCtas, (most + kWarps - 1) / kWarps);
     const cudaError_t e = allow_smem<attn_flat_kernel<Core, SHARED>>(FlatCfg<Core>::SMEM);
     if (e != cudaSuccess) return e;
+    FlatMaps maps;
+    memset(&maps, 0, sizeof(maps));
+    if (Core::kScaled) {
+        // (a cache of no pages: any address, of which nothing is read)
+        const int32_t page = 1 << a.page_shift, unit = FlatCfg<Core>::UNIT;
+        // (2^31 heads of pages are terabytes)
+        a.num_pages = std::min(a.num_pages, INT32_MAX / a.HKV);
+        const int32_t heads = std::max(a.num_pages * a.HKV, 1);
+        if (!encode_codes_map(&maps.k, a.num_pages ? a.k_cache : a.q, a.D, page, heads, unit) ||
+            !encode_codes_map(&maps.v, a.num_pages ? a.v_cache : a.q, a.D, page, heads, unit))
+            return cudaErrorInvalidValue;
+    }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr = follows_on();
     cfg.stream = stream;
@@ -441,7 +521,7 @@ cudaError_t launch_flat(const AttnStepArgs &a, float *part, int sms, cudaStream_
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = FlatCfg<Core>::SMEM;
-    return cudaLaunchKernelEx(&cfg, attn_flat_kernel<Core, SHARED>, a, part);
+    return cudaLaunchKernelEx(&cfg, attn_flat_kernel<Core, SHARED>, a, part, maps);
 }
 
 }  // namespace

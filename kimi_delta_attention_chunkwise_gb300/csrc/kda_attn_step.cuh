@@ -615,6 +615,16 @@ struct MmaCore {
         for (int x = 0; x < 2; ++x)
             qf[n][x] = __shfl_sync(0xffffffffu, back, (2 * (threadIdx.x & 3) + x) * 4);
     }
+    // The token that row r of the products is.  Any order will do; with 8-bit codes
+    // it is one in which rows that lanes read from shared memory together lie in
+    // different banks, by the swizzle of the copies that bring them (fetch()).
+    __device__ static int token_of(int r) {
+        if constexpr (!kScaled) return r;
+        if constexpr (D == 128) return r ^ ((r & 1) << 2);
+        // rows 0, 2, 4, 6: tokens 0, 1, 4, 5; the row behind each: the token's two
+        // low bits turned over
+        return ((r & 8) | (r & 4) | (r >> 1 & 1)) ^ ((r & 1) * 3);
+    }
     // first channel of the lane's j-th vector of a query row
     __device__ static int q_channel(int j, int t) {
         return kScaled ? ((j >> 1) * 4 + t) * 16 + (j & 1) * 8 : (j * 4 + t) * 8;
@@ -650,16 +660,18 @@ struct MmaCore {
         for (int r = 0; r < 2; ++r) {
 #pragma unroll
             for (int j = 0; j < KC; ++j)
-                k[r][j] = g + 8 * r < n ? load_once(kp + (g + 8 * r) * D + (j * 4 + t) * V)
-                                        : make_uint4(0, 0, 0, 0);
-            if constexpr (kScaled) kf[r] = g + 8 * r < n ? __ldg(ksp + g + 8 * r) : 0.f;
+                k[r][j] = token_of(g + 8 * r) < n
+                              ? load_once(kp + token_of(g + 8 * r) * D + (j * 4 + t) * V)
+                              : make_uint4(0, 0, 0, 0);
+            if constexpr (kScaled)
+                kf[r] = token_of(g + 8 * r) < n ? __ldg(ksp + token_of(g + 8 * r)) : 0.f;
         }
     }
     __device__ void load_v(const C *vp, const float *vsp, int n) {
         const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int tok = 2 * t + (r & 1) + 8 * (r >> 1);
+            const int tok = token_of(2 * t + (r & 1) + 8 * (r >> 1));
 #pragma unroll
             for (int c = 0; c < VV; ++c) {
                 v[r][c] = make_uint4(0, 0, 0, 0);
@@ -677,55 +689,58 @@ struct MmaCore {
         }
         if constexpr (kScaled) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) vf[r] = g + 8 * r < n ? __ldg(vsp + g + 8 * r) : 0.f;
+            for (int r = 0; r < 2; ++r)
+                vf[r] = token_of(g + 8 * r) < n ? __ldg(vsp + token_of(g + 8 * r)) : 0.f;
         }
     }
-    // 16 tokens that have been copied to shared memory (kda_attn_flat.cuh): keys,
-    // values, then the scales of both.
-    static constexpr uint32_t kRowBytes = D * sizeof(C), kHalf = kWarpTokens * kRowBytes;
-    static constexpr uint32_t kBlockBytes = 2 * kHalf + (kScaled ? 2 * kWarpTokens * 4 : 0);
-    __device__ void fetch(const uint8_t *from) {
+    // 16 tokens that have been copied to shared memory (kda_attn_flat.cuh): rows of
+    // keys, of values and the scales of both.  Rows of 8-bit codes have the copies'
+    // swizzle: 16-byte chunk c of row r lies at c ^ (r & 7) (D = 64: c ^ (r >> 1 & 3)).
+    static constexpr uint32_t kRowBytes = D * sizeof(C);
+    // the lane's places in it: key rows g (channels of j = 0 and 1), value rows 2 t
+    // and 2 t + 1, scale g; rows 8 further are 8 tokens further
+    uint32_t at_k[2], at_v[2], at_f;
+    __device__ void places() {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            at_k[i] = chunk_at(token_of(g), i * 4 + t);
+            at_v[i] = kScaled && D == 64 ? chunk_at(token_of(2 * t + i), g >> 1) + (g & 1) * 8
+                                         : chunk_at(token_of(2 * t + i), g);
+        }
+        at_f = token_of(g);
+    }
+    __device__ static uint32_t chunk_at(int token, int chunk) {
+        const int turn = !kScaled ? 0 : D == 128 ? token & 7 : token >> 1 & 3;
+        return token * kRowBytes + (chunk ^ turn) * 16;
+    }
+    __device__ void fetch(const uint8_t *keys, const uint8_t *values, const float *key_scales,
+                          const float *value_scales) {
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int j = 0; j < KC; ++j)
-                k[r][j] = *reinterpret_cast<const uint4 *>(from + (g + 8 * r) * kRowBytes +
-                                                           (j * 4 + t) * 16);
-        from += kHalf;
+            for (int j = 0; j < KC; ++j)  // (codes: two at most)
+                k[r][j] = *reinterpret_cast<const uint4 *>(
+                    keys + (kScaled ? at_k[j] : at_k[0] + j * 64) + 8 * r * kRowBytes);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const uint8_t *row = from + (2 * t + (r & 1) + 8 * (r >> 1)) * kRowBytes;
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
             for (int c = 0; c < VV; ++c) {
+                const uint8_t *x = values + at_v[r & 1] + c * 128 + (r >> 1) * 8 * kRowBytes;
                 if constexpr (kScaled && D == 64) {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(row + g * 8);
-                    v[r][c].x = x.x;
-                    v[r][c].y = x.y;
+                    const uint2 y = *reinterpret_cast<const uint2 *>(x);
+                    v[r][c].x = y.x;
+                    v[r][c].y = y.y;
                 } else {
-                    v[r][c] = *reinterpret_cast<const uint4 *>(row + c * 128 + g * 16);
+                    v[r][c] = *reinterpret_cast<const uint4 *>(x);
                 }
             }
-        }
         if constexpr (kScaled) {
-            const float *f = reinterpret_cast<const float *>(from + kHalf);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                kf[r] = f[g + 8 * r];
-                vf[r] = f[kWarpTokens + g + 8 * r];
+                kf[r] = key_scales[at_f + 8 * r];
+                vf[r] = value_scales[at_f + 8 * r];
             }
-        }
-    }
-    // Rows from n on of such a block, which nothing was copied to, as no product may see
-    // them: zero values (codes are finite as they are: zero scales will do).
-    __device__ static void clear_rest(uint8_t *block, int n) {
-        const int lane = threadIdx.x & 31;
-        if constexpr (kScaled) {
-            float *f = reinterpret_cast<float *>(block + 2 * kHalf);
-            if ((lane & 15) >= n) f[lane] = 0.f;
-        } else {
-            for (uint32_t i = n * kRowBytes / 16 + lane; i < kHalf / 16; i += 32)
-                reinterpret_cast<uint4 *>(block + kHalf)[i] = make_uint4(0, 0, 0, 0);
         }
     }
     __device__ void scores() {
@@ -777,8 +792,8 @@ struct MmaCore {
         const int g = (threadIdx.x & 31) >> 2;
         const bool low = threadIdx.x & 2;  // columns 4-7
         if (n_tok < kWarpTokens) {
-            if (g >= n_tok) s[0][0] = s[0][1] = -INFINITY;
-            if (g + 8 >= n_tok) s[0][2] = s[0][3] = -INFINITY;
+            if (token_of(g) >= n_tok) s[0][0] = s[0][1] = -INFINITY;
+            if (token_of(g + 8) >= n_tok) s[0][2] = s[0][3] = -INFINITY;
         }
         float top[2];
 #pragma unroll
@@ -877,8 +892,8 @@ struct MmaCore {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             if (n_tok < kWarpTokens) {
-                if (g >= n_tok) s[n][0] = s[n][1] = -INFINITY;
-                if (g + 8 >= n_tok) s[n][2] = s[n][3] = -INFINITY;
+                if (token_of(g) >= n_tok) s[n][0] = s[n][1] = -INFINITY;
+                if (token_of(g + 8) >= n_tok) s[n][2] = s[n][3] = -INFINITY;
             }
             float top[2];
 #pragma unroll
