@@ -37,8 +37,7 @@ struct AppendArgs {
     int32_t positions, rot, interleaved;
     void *q_out, *k_out;           // may be nullptr
     void *k_cache, *v_cache;
-    int32_t q8;                    // a cache of 8-bit codes, with scales [pages, HKV, page]
-    float *k_scale, *v_scale;
+    float *k_scale, *v_scale;      // [pages, HKV, page] (8-bit caches)
     void *k_stored, *v_stored;     // what the codes stand for, [T, HKV, D]; may be nullptr
     const int32_t *block_table;
     int32_t num_pages, page_shift, max_pages;
@@ -46,6 +45,7 @@ struct AppendArgs {
     int *status;
 };
 cudaError_t launch_cache_append(const AppendArgs &a, cudaStream_t stream);
+cudaError_t launch_cache_append_q8(const AppendArgs &a, cudaStream_t stream);
 
 struct AttnStepArgs {
     const void *q;

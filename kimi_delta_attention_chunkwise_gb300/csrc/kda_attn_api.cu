@@ -169,16 +169,16 @@ kdaStatus_t plan_append(const void *q, const void *k, const void *v, const int32
     a.N = shape->num_seqs; a.T = shape->total_tokens;
     a.HQ = q ? shape->num_heads : 0; a.HKV = shape->num_kv_heads; a.D = shape->head_dim;
     a.dtype = shape->dtype;
-    a.q8 = 0;
     a.k_scale = a.v_scale = nullptr;
     a.k_stored = a.v_stored = nullptr;
     return KDA_SUCCESS;
 }
 
-kdaStatus_t run_append(AppendArgs &a, cudaStream_t stream) {
+kdaStatus_t run_append(AppendArgs &a, cudaError_t (*launch)(const AppendArgs &, cudaStream_t),
+                       cudaStream_t stream) {
     a.status = device_status_word();
     if (!a.status) return cuda_status(cudaErrorUnknown);
-    return cuda_status(launch_cache_append(a, stream));
+    return cuda_status(launch(a, stream));
 }
 
 // A step's scratch and launch, by kind.
@@ -311,7 +311,7 @@ kdaStatus_t kda_cache_append(const void *q, const void *k, const void *v,
     const kdaStatus_t st =
         plan_append(q, k, v, cu_seqlens, cache_lens, rope, q_out, k_out, cache, shape, a);
     if (st != KDA_SUCCESS || shape->total_tokens == 0) return st;
-    return run_append(a, stream);
+    return run_append(a, launch_cache_append, stream);
 }
 
 kdaStatus_t kda_cache_append_q8(const void *q, const void *k, const void *v,
@@ -332,10 +332,9 @@ kdaStatus_t kda_cache_append_q8(const void *q, const void *k, const void *v,
     if ((k_stored && k_stored == v_stored) || !aligned(k_stored, 16) || !aligned(v_stored, 16))
         return KDA_ERR_INVALID_ARG;
     if (shape->total_tokens == 0) return KDA_SUCCESS;
-    a.q8 = 1;
     a.k_scale = cache->k_scale; a.v_scale = cache->v_scale;
     a.k_stored = k_stored; a.v_stored = v_stored;
-    return run_append(a, stream);
+    return run_append(a, launch_cache_append_q8, stream);
 }
 
 kdaStatus_t kda_attn_step_workspace_size(const kdaPagedCache_t *cache, const kdaAttnShape_t *shape,

@@ -20,7 +20,12 @@
 // of the rotated fp32 row, with each of these operations rounded to fp32: what
 // the codes stand for is off by half a scale at most (and fp32's rounding).
 // top is the maximum over the row's neighbouring lanes, as integers, in which
-// infinities and NaN are above every number.
+// infinities and NaN are above every number.  A CTA takes one token; a thread has
+// the same unit of every so-many-th row, so that it loads its angles once, and two
+// rows' vectors at a time.  More CTAs to an SM count for more than more rows in
+// flight (16384 tokens, 32/8 heads, d = 128, the values that the codes stand for
+// among the outputs: 8 CTAs 76.5 us, 5.8 TB/s; 7 with three rows 77.5, 6 79.4; one
+// row and 8 78.8; 9 spill, 84).
 #include <cstdint>
 #include <cuda_bf16.h>
 
@@ -132,6 +137,109 @@ struct Unit {
     bool halves;               // the two vectors pair up
 };
 
+template <typename T, int D, int TOK, int kThreads>
+__global__ void __launch_bounds__(kThreads, TOK == 1 ? 1 : 9) cache_append_kernel(const AppendArgs a) {
+    constexpr int V = Row<T>::V;
+    constexpr int UNITS = D / V / 2;  // units per head row
+    __shared__ Place place[TOK];
+    const int32_t t0 = blockIdx.x * TOK;
+    const int32_t rows = a.HQ + 2 * a.HKV;
+    const int32_t half = a.rot >> 1;
+    const int32_t total = min(TOK, a.T - t0) * rows * UNITS;
+    auto unit_of = [&](int32_t i) {
+        Unit w;
+        const int32_t u = i % UNITS, r = i / UNITS;
+        w.tk = r / rows;
+        w.head = r - w.tk * rows;
+        w.halves = a.rot > 0 && !a.interleaved && u * V < half;
+        w.c0 = w.halves ? u * V : 2 * u * V;
+        w.c1 = w.halves ? w.c0 + half : w.c0 + V;
+        return w;
+    };
+    // inputs do not wait for the look-up: every row of [0, T) may be read
+    auto load = [&](int32_t i, uint4 &x0, uint4 &x1) {
+        const Unit w = unit_of(i);
+        const int64_t t = t0 + w.tk;
+        const T *src;
+        if (w.head < a.HQ) {
+            src = static_cast<const T *>(a.q) + t * a.q_stride + (int64_t)w.head * D;
+        } else if (w.head < a.HQ + a.HKV) {
+            src = static_cast<const T *>(a.k) + t * a.k_stride + (int64_t)(w.head - a.HQ) * D;
+        } else {
+            src = static_cast<const T *>(a.v) + t * a.v_stride + (int64_t)(w.head - a.HQ - a.HKV) * D;
+        }
+        x0 = *reinterpret_cast<const uint4 *>(src + w.c0);
+        x1 = *reinterpret_cast<const uint4 *>(src + w.c1);
+    };
+    auto finish = [&](int32_t i, uint4 x0, uint4 x1) {
+        const Unit w = unit_of(i);
+        const Place p = place[w.tk];
+        if (p.pos < 0) return;
+        const int64_t t = t0 + w.tk;
+        T *dst0 = nullptr, *dst1 = nullptr;  // contiguous output, cache row
+        bool rotate = w.c0 < a.rot;
+        if (w.head < a.HQ) {
+            dst0 = static_cast<T *>(a.q_out) + (t * a.HQ + w.head) * D;
+        } else {
+            const int32_t h = w.head - a.HQ;
+            const bool is_k = h < a.HKV;
+            const int32_t kh = is_k ? h : h - a.HKV;
+            const int64_t row = (p.page + ((int64_t)kh << a.page_shift)) * D;
+            if (p.page >= 0) dst1 = static_cast<T *>(is_k ? a.k_cache : a.v_cache) + row;
+            if (is_k && a.k_out) dst0 = static_cast<T *>(a.k_out) + (t * a.HKV + kh) * D;
+            rotate = rotate && is_k;
+        }
+        if (rotate) {
+            const float *cs = a.rope + (int64_t)p.pos * a.rot;
+            float f0[V], f1[V], c[V], s[V];
+            Row<T>::unpack(x0, f0);
+            Row<T>::unpack(x1, f1);
+            // the angles of the unit's V pairs: halves: pairs c0 .. c0 + V - 1;
+            // interleaved: c0 / 2 .. (both vectors lie inside rot_dim, a
+            // multiple of 2 V)
+            const float *ca = cs + (w.halves ? w.c0 : w.c0 / 2), *sa = ca + half;
+#pragma unroll
+            for (int j = 0; j < V; j += 4) {
+                const float4 cv = __ldg(reinterpret_cast<const float4 *>(ca + j));
+                const float4 sv = __ldg(reinterpret_cast<const float4 *>(sa + j));
+                c[j] = cv.x; c[j + 1] = cv.y; c[j + 2] = cv.z; c[j + 3] = cv.w;
+                s[j] = sv.x; s[j + 1] = sv.y; s[j + 2] = sv.z; s[j + 3] = sv.w;
+            }
+            if (w.halves) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) turn(f0[j], f1[j], c[j], s[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) {
+                    turn(f0[2 * j], f0[2 * j + 1], c[j], s[j]);
+                    turn(f1[2 * j], f1[2 * j + 1], c[V / 2 + j], s[V / 2 + j]);
+                }
+            }
+            x0 = Row<T>::pack(f0);
+            x1 = Row<T>::pack(f1);
+        }
+        if (dst0) {
+            *reinterpret_cast<uint4 *>(dst0 + w.c0) = x0;
+            *reinterpret_cast<uint4 *>(dst0 + w.c1) = x1;
+        }
+        if (dst1) {
+            *reinterpret_cast<uint4 *>(dst1 + w.c0) = x0;
+            *reinterpret_cast<uint4 *>(dst1 + w.c1) = x1;
+        }
+    };
+    // the next unit's vectors are on their way while this one's are worked on
+    uint4 x0 = {}, x1 = {}, y0 = {}, y1 = {};
+    if ((int32_t)threadIdx.x < total) load(threadIdx.x, x0, x1);
+    if (threadIdx.x < TOK) place[threadIdx.x] = find_place(a, t0 + threadIdx.x);
+    __syncthreads();
+    for (int32_t i = threadIdx.x; i < total; i += kThreads) {
+        if (i + kThreads < total) load(i + kThreads, y0, y1);
+        finish(i, x0, x1);
+        x0 = y0;
+        x1 = y1;
+    }
+}
+
 // A row's codes and what they stand for.
 constexpr float kSmallest = 0x1p-100f;  // (below it, 127 / top might not be a number)
 struct Coder {
@@ -167,223 +275,172 @@ __device__ __forceinline__ void store_codes(int8_t *to, const float (&c)[V]) {
     else *reinterpret_cast<uint32_t *>(to) = w[0];
 }
 
-template <typename T, int D, int TOK, int kThreads, bool Q8>
-__global__ void __launch_bounds__(kThreads, TOK == 1 ? 1 : Q8 ? 6 : 9) cache_append_kernel(const AppendArgs a) {
+template <typename T, int D, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 128 ? 8 : 1) cache_append_q8_kernel(const AppendArgs a) {
     constexpr int V = Row<T>::V;
-    constexpr int UNITS = D / V / 2;  // units per head row
-    __shared__ Place place[TOK];
-    const int32_t t0 = blockIdx.x * TOK;
+    constexpr int UNITS = D / V / 2;        // units per head row
+    constexpr int STEP = kThreads / UNITS;  // rows abreast
+    constexpr int B = 2;                    // rows of a thread in flight
+    __shared__ Place place;
+    const int32_t t = blockIdx.x, half = a.rot >> 1;
     const int32_t rows = a.HQ + 2 * a.HKV;
-    const int32_t half = a.rot >> 1;
-    const int32_t total = min(TOK, a.T - t0) * rows * UNITS;
-    auto unit_of = [&](int32_t i) {
-        Unit w;
-        const int32_t u = i % UNITS, r = i / UNITS;
-        w.tk = r / rows;
-        w.head = r - w.tk * rows;
-        w.halves = a.rot > 0 && !a.interleaved && u * V < half;
-        w.c0 = w.halves ? u * V : 2 * u * V;
-        w.c1 = w.halves ? w.c0 + half : w.c0 + V;
-        return w;
-    };
-    // inputs do not wait for the look-up: every row of [0, T) may be read
-    auto load = [&](int32_t i, uint4 &x0, uint4 &x1) {
-        const Unit w = unit_of(i);
-        const int64_t t = t0 + w.tk;
-        const T *src;
-        if (w.head < a.HQ) {
-            src = static_cast<const T *>(a.q) + t * a.q_stride + (int64_t)w.head * D;
-        } else if (w.head < a.HQ + a.HKV) {
-            src = static_cast<const T *>(a.k) + t * a.k_stride + (int64_t)(w.head - a.HQ) * D;
-        } else {
-            src = static_cast<const T *>(a.v) + t * a.v_stride + (int64_t)(w.head - a.HQ - a.HKV) * D;
+    const int32_t u = (int32_t)threadIdx.x % UNITS, r0 = (int32_t)threadIdx.x / UNITS;
+    // the thread's two vectors of a row: the two whose channels pair up, or neighbours
+    const bool halves = a.rot > 0 && !a.interleaved && u * V < half;
+    const int32_t c0 = halves ? u * V : 2 * u * V, c1 = halves ? c0 + half : c0 + V;
+    const bool turns = c0 < a.rot;
+    float cs[V], sn[V];  // the angles of the unit's pairs
+    Place p;
+    for (int32_t rb = 0; rb < rows; rb += STEP * B) {
+        // inputs do not wait for the look-up: every row of [0, T) may be read
+        uint4 x0[B], x1[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const int32_t r = rb + r0 + b * STEP;
+            if (r >= rows) continue;
+            const T *src;
+            if (r < a.HQ) src = static_cast<const T *>(a.q) + t * a.q_stride + (int64_t)r * D;
+            else if (r < a.HQ + a.HKV)
+                src = static_cast<const T *>(a.k) + t * a.k_stride + (int64_t)(r - a.HQ) * D;
+            else
+                src = static_cast<const T *>(a.v) + t * a.v_stride + (int64_t)(r - a.HQ - a.HKV) * D;
+            x0[b] = *reinterpret_cast<const uint4 *>(src + c0);
+            x1[b] = *reinterpret_cast<const uint4 *>(src + c1);
         }
-        x0 = *reinterpret_cast<const uint4 *>(src + w.c0);
-        x1 = *reinterpret_cast<const uint4 *>(src + w.c1);
-    };
-    // turns the pairs of a unit whose first channel is below rot_dim
-    auto rotate_unit = [&](const Unit &w, int32_t pos, float (&f0)[V], float (&f1)[V]) {
-        const float *cs = a.rope + (int64_t)pos * a.rot;
-        float c[V], s[V];
-        // the angles of the unit's V pairs: halves: pairs c0 .. c0 + V - 1;
-        // interleaved: c0 / 2 .. (both vectors lie inside rot_dim, a
-        // multiple of 2 V)
-        const float *ca = cs + (w.halves ? w.c0 : w.c0 / 2), *sa = ca + half;
+        if (rb == 0) {
+            if (threadIdx.x == 0) place = find_place(a, t);
+            __syncthreads();
+            p = place;
+            if (p.pos < 0) return;
+            if (turns) {
+                const float *ca = a.rope + (int64_t)p.pos * a.rot + (halves ? c0 : c0 / 2);
 #pragma unroll
-        for (int j = 0; j < V; j += 4) {
-            const float4 cv = __ldg(reinterpret_cast<const float4 *>(ca + j));
-            const float4 sv = __ldg(reinterpret_cast<const float4 *>(sa + j));
-            c[j] = cv.x; c[j + 1] = cv.y; c[j + 2] = cv.z; c[j + 3] = cv.w;
-            s[j] = sv.x; s[j + 1] = sv.y; s[j + 2] = sv.z; s[j + 3] = sv.w;
-        }
-        if (w.halves) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) turn(f0[j], f1[j], c[j], s[j]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < V / 2; ++j) {
-                turn(f0[2 * j], f0[2 * j + 1], c[j], s[j]);
-                turn(f1[2 * j], f1[2 * j + 1], c[V / 2 + j], s[V / 2 + j]);
+                for (int j = 0; j < V; j += 4) {
+                    const float4 c = __ldg(reinterpret_cast<const float4 *>(ca + j));
+                    const float4 s = __ldg(reinterpret_cast<const float4 *>(ca + half + j));
+                    cs[j] = c.x; cs[j + 1] = c.y; cs[j + 2] = c.z; cs[j + 3] = c.w;
+                    sn[j] = s.x; sn[j + 1] = s.y; sn[j + 2] = s.z; sn[j + 3] = s.w;
+                }
             }
         }
-    };
-    // Q8: the unit's part of its row to the cache's codes (called by whole warps)
-    auto finish_q8 = [&](int32_t i, uint4 x0, uint4 x1) {
-        const bool here = i < total;
-        const Unit w = unit_of(here ? i : 0);
-        const Place p = place[w.tk];
-        const bool is_q = w.head < a.HQ, is_k = !is_q && w.head < a.HQ + a.HKV;
-        const int32_t kh = w.head - a.HQ - (is_k || is_q ? 0 : a.HKV);
-        const int64_t t = t0 + w.tk;
-        float f0[V], f1[V];
-        Row<T>::unpack(x0, f0);
-        Row<T>::unpack(x1, f1);
-        const bool live = here && p.pos >= 0;
-        const bool turned = live && (is_q || is_k) && w.c0 < a.rot;
-        if (turned) rotate_unit(w, p.pos, f0, f1);
-        auto put = [&](T *row, const float (&y0)[V], const float (&y1)[V]) {
-            *reinterpret_cast<uint4 *>(row + w.c0) = Row<T>::pack(y0);
-            *reinterpret_cast<uint4 *>(row + w.c1) = Row<T>::pack(y1);
-        };
-        // (what is not turned is copied: packing it again would change NaN's bits)
-        auto put_turned = [&](T *row) {
-            if (turned) {
-                put(row, f0, f1);
-            } else {
-                *reinterpret_cast<uint4 *>(row + w.c0) = x0;
-                *reinterpret_cast<uint4 *>(row + w.c1) = x1;
-            }
-        };
-        uint32_t top = 0;
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            top = max(top, max(__float_as_uint(f0[j]) & 0x7FFFFFFFu, __float_as_uint(f1[j]) & 0x7FFFFFFFu));
-#pragma unroll
-        for (int o = 1; o < UNITS; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (!live) return;
-        if (is_q) {
-            put_turned(static_cast<T *>(a.q_out) + (t * a.HQ + w.head) * D);
-            return;
-        }
-        const Coder coder(top);
-        float c0[V], c1[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            c0[j] = coder.code(f0[j]);
-            c1[j] = coder.code(f1[j]);
-        }
-        if (p.page >= 0) {
-            const int64_t row = p.page + ((int64_t)kh << a.page_shift);
-            int8_t *to = static_cast<int8_t *>(is_k ? a.k_cache : a.v_cache) + row * D;
-            store_codes<V>(to + w.c0, c0);
-            store_codes<V>(to + w.c1, c1);
-            if (i % UNITS == 0) (is_k ? a.k_scale : a.v_scale)[row] = coder.scale;
-        }
-        const int64_t out = (t * a.HKV + kh) * D;
-        if (is_k && a.k_out) put_turned(static_cast<T *>(a.k_out) + out);
-        T *stored = static_cast<T *>(is_k ? a.k_stored : a.v_stored);
-        if (stored) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                c0[j] = __fmul_rn(c0[j], coder.scale);
-                c1[j] = __fmul_rn(c1[j], coder.scale);
-            }
-            put(stored + out, c0, c1);
-        }
-    };
-    auto finish = [&](int32_t i, uint4 x0, uint4 x1) {
-        if constexpr (Q8) {
-            finish_q8(i, x0, x1);
-            return;
-        }
-        const Unit w = unit_of(i);
-        const Place p = place[w.tk];
-        if (p.pos < 0) return;
-        const int64_t t = t0 + w.tk;
-        T *dst0 = nullptr, *dst1 = nullptr;  // contiguous output, cache row
-        bool rotate = w.c0 < a.rot;
-        if (w.head < a.HQ) {
-            dst0 = static_cast<T *>(a.q_out) + (t * a.HQ + w.head) * D;
-        } else {
-            const int32_t h = w.head - a.HQ;
-            const bool is_k = h < a.HKV;
-            const int32_t kh = is_k ? h : h - a.HKV;
-            const int64_t row = (p.page + ((int64_t)kh << a.page_shift)) * D;
-            if (p.page >= 0) dst1 = static_cast<T *>(is_k ? a.k_cache : a.v_cache) + row;
-            if (is_k && a.k_out) dst0 = static_cast<T *>(a.k_out) + (t * a.HKV + kh) * D;
-            rotate = rotate && is_k;
-        }
-        if (rotate) {
+        for (int b = 0; b < B; ++b) {
+            const int32_t r = rb + r0 + b * STEP;
+            const bool here = r < rows, is_q = r < a.HQ, is_k = !is_q && r < a.HQ + a.HKV;
+            if (!__any_sync(0xffffffffu, here)) break;
             float f0[V], f1[V];
-            Row<T>::unpack(x0, f0);
-            Row<T>::unpack(x1, f1);
-            rotate_unit(w, p.pos, f0, f1);
-            x0 = Row<T>::pack(f0);
-            x1 = Row<T>::pack(f1);
-        }
-        if (dst0) {
-            *reinterpret_cast<uint4 *>(dst0 + w.c0) = x0;
-            *reinterpret_cast<uint4 *>(dst0 + w.c1) = x1;
-        }
-        if (dst1) {
-            *reinterpret_cast<uint4 *>(dst1 + w.c0) = x0;
-            *reinterpret_cast<uint4 *>(dst1 + w.c1) = x1;
-        }
-    };
-    // the next unit's vectors are on their way while this one's are worked on
-    uint4 x0 = {}, x1 = {}, y0 = {}, y1 = {};
-    if ((int32_t)threadIdx.x < total) load(threadIdx.x, x0, x1);
-    if (threadIdx.x < TOK) place[threadIdx.x] = find_place(a, t0 + threadIdx.x);
-    __syncthreads();
-    if constexpr (Q8) {
-        // whole warps: a row's lanes look for its maximum together
-        for (int32_t i = threadIdx.x; i - (int32_t)(threadIdx.x & 31) < total; i += kThreads) {
-            if (i + kThreads < total) load(i + kThreads, y0, y1);
-            finish(i, x0, x1);
-            x0 = y0;
-            x1 = y1;
-        }
-    } else {
-        for (int32_t i = threadIdx.x; i < total; i += kThreads) {
-            if (i + kThreads < total) load(i + kThreads, y0, y1);
-            finish(i, x0, x1);
-            x0 = y0;
-            x1 = y1;
+            Row<T>::unpack(x0[b], f0);
+            Row<T>::unpack(x1[b], f1);
+            const bool turned = turns && (is_q || is_k);
+            if (turned) {
+                if (halves) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) turn(f0[j], f1[j], cs[j], sn[j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < V / 2; ++j) {
+                        turn(f0[2 * j], f0[2 * j + 1], cs[j], sn[j]);
+                        turn(f1[2 * j], f1[2 * j + 1], cs[V / 2 + j], sn[V / 2 + j]);
+                    }
+                }
+            }
+            // the row as it is turned (what is not is copied: packing it again would
+            // change a NaN's bits)
+            auto put_turned = [&](T *row) {
+                *reinterpret_cast<uint4 *>(row + c0) = turned ? Row<T>::pack(f0) : x0[b];
+                *reinterpret_cast<uint4 *>(row + c1) = turned ? Row<T>::pack(f1) : x1[b];
+            };
+            if (here && is_q) put_turned(static_cast<T *>(a.q_out) + ((int64_t)t * a.HQ + r) * D);
+            // (most warps have queries alone)
+            if (!__any_sync(0xffffffffu, here && !is_q)) continue;
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                top = max(top, max(__float_as_uint(f0[j]) & 0x7FFFFFFFu,
+                                   __float_as_uint(f1[j]) & 0x7FFFFFFFu));
+#pragma unroll
+            for (int o = 1; o < UNITS; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (here && !is_q) {
+                const int32_t kh = r - a.HQ - (is_k ? 0 : a.HKV);
+                const int64_t out = ((int64_t)t * a.HKV + kh) * D;
+                if (is_k && a.k_out) put_turned(static_cast<T *>(a.k_out) + out);
+                const Coder coder(top);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    f0[j] = coder.code(f0[j]);
+                    f1[j] = coder.code(f1[j]);
+                }
+                if (p.page >= 0) {
+                    const int64_t row = p.page + ((int64_t)kh << a.page_shift);
+                    int8_t *to = static_cast<int8_t *>(is_k ? a.k_cache : a.v_cache) + row * D;
+                    store_codes<V>(to + c0, f0);
+                    store_codes<V>(to + c1, f1);
+                    if (u == 0) (is_k ? a.k_scale : a.v_scale)[row] = coder.scale;
+                }
+                T *stored = static_cast<T *>(is_k ? a.k_stored : a.v_stored);
+                if (stored) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        f0[j] = __fmul_rn(f0[j], coder.scale);
+                        f1[j] = __fmul_rn(f1[j], coder.scale);
+                    }
+                    *reinterpret_cast<uint4 *>(stored + out + c0) = Row<T>::pack(f0);
+                    *reinterpret_cast<uint4 *>(stored + out + c1) = Row<T>::pack(f1);
+                }
+            }
         }
     }
 }
 
-template <typename T, int D, bool Q8>
+template <typename T, int D>
 cudaError_t launch_t(const AppendArgs &a, cudaStream_t stream) {
     if (a.T <= kFewTokens) {
-        cache_append_kernel<T, D, 1, 256, Q8><<<(unsigned)a.T, 256, 0, stream>>>(a);
+        cache_append_kernel<T, D, 1, 256><<<(unsigned)a.T, 256, 0, stream>>>(a);
     } else {
-        cache_append_kernel<T, D, 2, 128, Q8><<<(unsigned)(a.T / 2 + a.T % 2), 128, 0, stream>>>(a);
+        cache_append_kernel<T, D, 2, 128><<<(unsigned)(a.T / 2 + a.T % 2), 128, 0, stream>>>(a);
     }
     return cudaGetLastError();
 }
 
-template <typename T, bool Q8>
+template <typename T>
 cudaError_t launch_d(const AppendArgs &a, cudaStream_t stream) {
     switch (a.D) {
-        case 16: return launch_t<T, 16, Q8>(a, stream);
-        case 32: return launch_t<T, 32, Q8>(a, stream);
-        case 64: return launch_t<T, 64, Q8>(a, stream);
-        case 128: return launch_t<T, 128, Q8>(a, stream);
+        case 16: return launch_t<T, 16>(a, stream);
+        case 32: return launch_t<T, 32>(a, stream);
+        case 64: return launch_t<T, 64>(a, stream);
+        case 128: return launch_t<T, 128>(a, stream);
     }
     return cudaErrorInvalidValue;
 }
 
-template <bool Q8>
-cudaError_t launch_q(const AppendArgs &a, cudaStream_t stream) {
-    if (a.dtype == KDA_DTYPE_BF16) return launch_d<__nv_bfloat16, Q8>(a, stream);
-    return launch_d<float, Q8>(a, stream);
+template <typename T, int D>
+cudaError_t launch_q8_t(const AppendArgs &a, cudaStream_t stream) {
+    if (a.T <= kFewTokens) cache_append_q8_kernel<T, D, 256><<<(unsigned)a.T, 256, 0, stream>>>(a);
+    else cache_append_q8_kernel<T, D, 128><<<(unsigned)a.T, 128, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_q8_d(const AppendArgs &a, cudaStream_t stream) {
+    switch (a.D) {
+        case 16: return launch_q8_t<T, 16>(a, stream);
+        case 32: return launch_q8_t<T, 32>(a, stream);
+        case 64: return launch_q8_t<T, 64>(a, stream);
+        case 128: return launch_q8_t<T, 128>(a, stream);
+    }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
 cudaError_t launch_cache_append(const AppendArgs &a, cudaStream_t stream) {
-    return a.q8 ? launch_q<true>(a, stream) : launch_q<false>(a, stream);
+    if (a.dtype == KDA_DTYPE_BF16) return launch_d<__nv_bfloat16>(a, stream);
+    return launch_d<float>(a, stream);
+}
+
+cudaError_t launch_cache_append_q8(const AppendArgs &a, cudaStream_t stream) {
+    if (a.dtype == KDA_DTYPE_BF16) return launch_q8_d<__nv_bfloat16>(a, stream);
+    return launch_q8_d<float>(a, stream);
 }
 
 }  // namespace kda
