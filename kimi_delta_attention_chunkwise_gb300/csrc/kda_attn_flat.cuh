@@ -60,21 +60,23 @@ struct LineCursor {
 
 template <class Core>
 struct FlatCfg {
+    static constexpr uint32_t ROW = Core::kPanels * Core::kPanel;  // bytes of a key
     // what an SM's CTAs leave of its shared memory, in 16 tokens to a warp
-    static constexpr uint32_t BLOCK = 2 * kWarpTokens * Core::kRowBytes;
+    static constexpr uint32_t BLOCK = 2 * kWarpTokens * ROW;
     static constexpr uint32_t SCALES = Core::kScaled ? 2 * kWarpTokens * 4 : 0;
-    static constexpr int ROOM = (228 * 1024 / Core::kCtas - 3072) / (int)(kWarps * (BLOCK + SCALES));
+    static constexpr int ROOM = (228 * 1024 / Core::kCtas - 4096) / (int)(kWarps * (BLOCK + SCALES));
     // 32 tokens to a unit where two units of them fit: what a unit costs besides
     // its tokens is a third of the instructions
     static constexpr int SUB = ROOM >= 4 ? 2 : 1, UNIT = SUB * kWarpTokens;
     static constexpr int RING = ROOM / SUB < 4 ? ROOM / SUB : 4;  // units
-    static constexpr uint32_t HALF = UNIT * Core::kRowBytes;      // a unit's keys, or values
+    static constexpr uint32_t PANEL = UNIT * Core::kPanel;        // a panel of a unit's keys
+    static constexpr uint32_t HALF = Core::kPanels * PANEL;       // a unit's keys, or values
     static constexpr uint32_t SMEM = kWarps * RING * SUB * (BLOCK + SCALES);
     static_assert(RING >= 2 && RING * SUB <= 32, "shared memory of an SM");
-    static_assert(!Core::kScaled || (SUB == 2 && HALF % 1024 == 0), "swizzled tiles");
+    static_assert(PANEL % 1024 == 0, "swizzled tiles");
 };
 
-// 8-bit caches: the heads of their pages as tensors.
+// The heads of the cache's pages as tensors.
 struct FlatMaps {
     CUtensorMap k, v;
 };
@@ -107,7 +109,6 @@ template <class Core, bool SHARED>
 __global__ void __launch_bounds__(kThreads, Core::kCtas)
 attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ FlatMaps maps) {
     using T = typename Core::Type;
-    using C = typename Core::Cell;
     using Cfg = FlatCfg<Core>;
     constexpr int D = Core::kD, R = Core::kRows, RING = Cfg::RING, SUB = Cfg::SUB;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -116,35 +117,28 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
     __shared__ uint64_t s_full[kWarps][RING];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     tc::pdl_launch_dependents();
-    if (Core::kScaled && (tc::smem_u32(smem) & 1023u)) {  // (the swizzle goes by addresses)
+    if (tc::smem_u32(smem) & 1023u) {  // (the swizzle goes by addresses)
         *a.status = KDA_ERR_CUDA;
         return;
     }
     const int32_t blocks = (a.G + R - 1) / R;  // blocks of query heads
     const int32_t items = a.HKV * blocks;
     // rows of a copy, and copies to a unit
-    const int32_t box = Core::kScaled ? min(1 << a.page_shift, Cfg::UNIT) : kWarpTokens;
-    const int32_t copies = Cfg::UNIT / box;
-    Line<kThreads, SHARED, Cfg::UNIT> line;
-    line.scan(a, s_scan);
-    const int64_t units = line.total * items;
-    const int32_t grid = workers(units, (int32_t)gridDim.x * kWarps);
-    // sequences without keys (SHARED: the join's)
-    for (int32_t s = (int32_t)blockIdx.x; s < a.N && !SHARED; s += gridDim.x) {
-        if (clamp_len(a, s) > 0) continue;
-        for (int32_t i = tid; i < a.HQ * D; i += kThreads)
-            store_row(a, (int64_t)s * a.HQ + i / D, D, i % D, 0.f, -INFINITY, 0.f);
-    }
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        const int32_t c = (int32_t)blockIdx.x * kWarps + w;
-        if (c < grid) line.look(a, share_start(units, c, grid), items, &s_seq[w], &s_base[w]);
-    }
+    const int32_t box = min(1 << a.page_shift, Cfg::UNIT), copies = Cfg::UNIT / box;
     if (tid == 0) {
         for (int w = 0; w < kWarps; ++w)
             for (int x = 0; x < RING; ++x) tc::mbar_init(&s_full[w][x], copies);
         tc::fence_mbar_init();
         tc::fence_proxy_async();
+    }
+    Line<kThreads, SHARED, Cfg::UNIT> line;
+    line.scan(a, s_scan);
+    const int64_t units = line.total * items;
+    const int32_t grid = workers(units, (int32_t)gridDim.x * kWarps);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const int32_t c = (int32_t)blockIdx.x * kWarps + w;
+        if (c < grid) line.look(a, share_start(units, c, grid), items, &s_seq[w], &s_base[w]);
     }
     __syncthreads();
     const int32_t c = (int32_t)blockIdx.x * kWarps + warp;  // this worker
@@ -154,6 +148,8 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
         float *scales = reinterpret_cast<float *>(smem + kWarps * RING * 2 * Cfg::HALF) +
                         warp * (RING * 2 * Cfg::UNIT);  // (kScaled)
         uint64_t *full = s_full[warp];
+        uint32_t good = 0;   // a bit per 16 tokens in the ring: they are there
+        uint32_t phase = 0;  // a bit per unit's barrier
         LineCursor<SHARED, Cfg::UNIT> here, ahead;
         here.seek(a, blocks, s_seq[warp], s_base[warp], u0);
         ahead = here;
@@ -166,38 +162,37 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
                        ? a.block_table[(int64_t)ahead.s * a.max_pages + (tok >> a.page_shift)]
                        : 0;
         };
-        uint32_t good = 0;   // a bit per block in the ring: it is there
-        uint32_t phase = 0;  // a bit per unit's barrier
-        int64_t au = u0;     // the unit at `ahead`
+        int64_t au = u0;  // the unit at `ahead`
         int32_t page = entry_of();
-        // starts the copies of the unit at `ahead` to place x of the ring
+        // starts the copies of the unit at `ahead` to place x of the ring: whole boxes
+        // (what lies behind the sequence is put out of the way in values())
         auto copy_next = [&](int32_t x) {
             if (au >= u1) return;
             const int32_t tok = ahead.token() + mine, n = min(kWarpTokens, ahead.end - tok);
             const bool there = page >= 0 && page < a.num_pages, ok = there && n > 0;
             if (n > 0 && !there) *a.status = KDA_ERR_INVALID_ARG;
             if (lane < copies) {
-                const int64_t z = (int64_t)page * a.HKV + ahead.kvh, row = z << a.page_shift;
-                const int32_t at = tok & ((1 << a.page_shift) - 1);
-                uint8_t *to = ring + x * (2 * Cfg::HALF) + mine * Core::kRowBytes;
                 if (!ok) {
                     tc::mbar_arrive(&full[x]);
-                } else if constexpr (Core::kScaled) {
-                    // whole boxes: what lies behind the sequence is codes like any,
-                    // whose scales will be put to 0
-                    tc::mbar_arrive_expect_tx(&full[x], box * (2 * Core::kRowBytes + 8));
-                    tc::tma_load_3d(to, &maps.k, 0, at, (int32_t)z, &full[x]);
-                    tc::tma_load_3d(to + Cfg::HALF, &maps.v, 0, at, (int32_t)z, &full[x]);
-                    float *f = scales + x * (2 * Cfg::UNIT) + mine;
-                    tc::bulk_g2s(f, a.k_scale + row + at, box * 4, &full[x]);
-                    tc::bulk_g2s(f + Cfg::UNIT, a.v_scale + row + at, box * 4, &full[x]);
                 } else {
-                    const uint32_t bytes = n * Core::kRowBytes;
-                    tc::mbar_arrive_expect_tx(&full[x], 2 * bytes);
-                    tc::bulk_g2s(to, static_cast<const C *>(a.k_cache) + (row + at) * D, bytes,
-                                 &full[x]);
-                    tc::bulk_g2s(to + Cfg::HALF, static_cast<const C *>(a.v_cache) + (row + at) * D,
-                                 bytes, &full[x]);
+                    const int64_t z = (int64_t)page * a.HKV + ahead.kvh;
+                    const int32_t at = tok & ((1 << a.page_shift) - 1);
+                    uint8_t *to = ring + x * (2 * Cfg::HALF) + mine * Core::kPanel;
+                    tc::mbar_arrive_expect_tx(
+                        &full[x], box * (2 * Cfg::ROW + (Core::kScaled ? 8 : 0)));
+#pragma unroll
+                    for (int p = 0; p < Core::kPanels; ++p) {
+                        const int32_t ch = p * (int)(Core::kPanel / sizeof(typename Core::Cell));
+                        tc::tma_load_3d(to + p * Cfg::PANEL, &maps.k, ch, at, (int32_t)z, &full[x]);
+                        tc::tma_load_3d(to + Cfg::HALF + p * Cfg::PANEL, &maps.v, ch, at, (int32_t)z,
+                                        &full[x]);
+                    }
+                    if constexpr (Core::kScaled) {
+                        const int64_t row = (z << a.page_shift) + at;
+                        float *f = scales + x * (2 * Cfg::UNIT) + mine;
+                        tc::bulk_g2s(f, a.k_scale + row, box * 4, &full[x]);
+                        tc::bulk_g2s(f + Cfg::UNIT, a.v_scale + row, box * 4, &full[x]);
+                    }
                 }
             }
             constexpr uint32_t all = (1u << SUB) - 1;
@@ -210,17 +205,17 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
         };
         auto wait = [&](int32_t x) -> bool {
             const uint32_t p = phase >> x & 1;
+            phase ^= 1u << x;
             const bool done = tc::mbar_try_wait(&full[x], p) ||
                               tc::mbar_wait_bounded(&full[x], p, kFlatWait);
-            phase ^= 1u << x;
             return __all_sync(0xffffffffu, done);
         };
 #pragma unroll
-        for (int x = 0; x < RING; ++x) copy_next(x);
+        for (int i = 0; i < RING; ++i) copy_next(i);
         Core core;
         core.places();
+        int32_t x = 0;  // the place in the ring
         bool fresh = true, seen = false, first_item = true;
-        int32_t x = 0;
         int64_t u = u0;
         for (; u < u1; ++u) {
             const int32_t rows = min(R, a.G - here.block * R);
@@ -241,7 +236,7 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
                 const bool ok = blocks_good >> b & 1;
                 const int n = min(kWarpTokens, left - b * kWarpTokens);
                 if (ok) {
-                    uint8_t *keys = ring + x * (2 * Cfg::HALF) + b * kWarpTokens * Core::kRowBytes;
+                    uint8_t *keys = ring + x * (2 * Cfg::HALF) + b * kWarpTokens * Core::kPanel;
                     uint8_t *values = keys + Cfg::HALF;
                     float *f = scales + x * (2 * Cfg::UNIT) + b * kWarpTokens;
                     if (n < kWarpTokens) {
@@ -250,14 +245,17 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
                         if constexpr (Core::kScaled) {
                             if ((lane & 15) >= n) f[(lane & 15) + (lane >> 4) * Cfg::UNIT] = 0.f;
                         } else {
-                            for (uint32_t i = n * Core::kRowBytes / 16 + lane;
-                                 i < kWarpTokens * Core::kRowBytes / 16; i += 32)
-                                reinterpret_cast<uint4 *>(values)[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                            for (int p = 0; p < Core::kPanels; ++p)
+                                for (uint32_t i = n * Core::kPanel / 16 + lane;
+                                     i < kWarpTokens * Core::kPanel / 16; i += 32)
+                                    reinterpret_cast<uint4 *>(values + p * Cfg::PANEL)[i] =
+                                        make_uint4(0, 0, 0, 0);
                         }
                         tc::fence_proxy_async();  // before copies to this place
                         __syncwarp();
                     }
-                    core.fetch(keys, values, f, f + Cfg::UNIT);
+                    core.fetch(keys, values, Cfg::PANEL, f, f + Cfg::UNIT);
                 }
                 if (b == SUB - 1) {
                     __syncwarp();
@@ -303,9 +301,10 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
                         }
                     });
                 }
-                if (ends && lane == 0)
-                    a.owners[(int64_t)here.s * items + here.kvh * blocks + here.block] =
-                        owners_of(units, first, c, grid);
+                if (ends && lane == 0) {
+                    int2 &to = a.owners[(int64_t)here.s * items + here.kvh * blocks + here.block];
+                    to = whole ? make_int2(c, 2) : owners_of(units, first, c, grid);
+                }
                 fresh = true;
                 first_item = false;
             }
@@ -358,7 +357,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_rows_join_kernel(const Attn
     const int2 who = a.owners[((int64_t)s * a.HKV + kvh) * blocks + block];
     int32_t own = span.len() > 0 ? who.y >> 1 : 0;
     const int32_t pieces = SHARED && span.first > 0 ? states.pieces[row < rows ? row : 0] : 0;
-    const bool done = !SHARED && own <= 1;  // written by the worker, or there were no keys
+    const bool done = !SHARED && own == 1;  // written by the worker
     const int32_t all = row >= rows || done ? 0 : own + pieces;
     // state i's weighted sums, maximum and sum: a worker's slot, or a piece (its
     // item's state: the last one) of arrays over the rows
@@ -475,19 +474,21 @@ cudaError_t launch_rows_join(const AttnStepArgs &a, const float *part, int sms,
                               parts);
 }
 
-// A cache of 8-bit codes [heads of pages, page, D] as a 3-D map whose box is up to
-// 32 rows of one page, swizzled by its rows' width.
-inline bool encode_codes_map(CUtensorMap *m, const void *base, int32_t d, int32_t page,
-                             int32_t heads, int32_t unit) {
+// A cache [heads of pages, page, D] as a 3-D map whose box is a panel of up to 32
+// rows of one page, swizzled by its width.
+template <class Core>
+bool encode_panel_map(CUtensorMap *m, const void *base, int32_t page, int32_t heads) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)page, (cuuint64_t)heads};
-    const cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)page * d};
-    const cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)std::min(page, unit), 1u};
+    const cuuint64_t es = sizeof(typename Core::Cell), row = Core::kD * es;
+    const cuuint64_t dims[3] = {(cuuint64_t)Core::kD, (cuuint64_t)page, (cuuint64_t)heads};
+    const cuuint64_t strides[2] = {row, row * page};
+    const cuuint32_t box[3] = {(cuuint32_t)(Core::kPanel / es),
+                               (cuuint32_t)std::min<int32_t>(page, FlatCfg<Core>::UNIT), 1u};
     const cuuint32_t estr[3] = {1u, 1u, 1u};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+    return enc(m, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+               const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               Core::kPanel == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -495,24 +496,22 @@ inline bool encode_codes_map(CUtensorMap *m, const void *base, int32_t d, int32_
 // The flat kernel (SHARED: a programmatic dependent of the kernel before).
 template <class Core, bool SHARED>
 cudaError_t launch_flat(AttnStepArgs a, float *part, int sms, cudaStream_t stream) {
-    const int64_t capacity = (int64_t)a.max_pages << a.page_shift;
-    // one wave, and no more warps than the longest possible line has units
-    const int64_t most = step_items<Core>(a) * (capacity / FlatCfg<Core>::UNIT + 1);
-    const int64_t grid = std::min((int64_t)sms * Core::kCtas, (most + kWarps - 1) / kWarps);
     const cudaError_t e = allow_smem<attn_flat_kernel<Core, SHARED>>(FlatCfg<Core>::SMEM);
     if (e != cudaSuccess) return e;
+    // (2^31 heads of pages are terabytes; a cache of no pages: any address, of which
+    // nothing is read)
+    const int32_t page = 1 << a.page_shift;
+    a.num_pages = std::min(a.num_pages, INT32_MAX / a.HKV);
+    const int32_t heads = std::max(a.num_pages * a.HKV, 1);
     FlatMaps maps;
     memset(&maps, 0, sizeof(maps));
-    if (Core::kScaled) {
-        // (a cache of no pages: any address, of which nothing is read)
-        const int32_t page = 1 << a.page_shift, unit = FlatCfg<Core>::UNIT;
-        // (2^31 heads of pages are terabytes)
-        a.num_pages = std::min(a.num_pages, INT32_MAX / a.HKV);
-        const int32_t heads = std::max(a.num_pages * a.HKV, 1);
-        if (!encode_codes_map(&maps.k, a.num_pages ? a.k_cache : a.q, a.D, page, heads, unit) ||
-            !encode_codes_map(&maps.v, a.num_pages ? a.v_cache : a.q, a.D, page, heads, unit))
-            return cudaErrorInvalidValue;
-    }
+    if (!encode_panel_map<Core>(&maps.k, a.num_pages ? a.k_cache : a.q, page, heads) ||
+        !encode_panel_map<Core>(&maps.v, a.num_pages ? a.v_cache : a.q, page, heads))
+        return cudaErrorInvalidValue;
+    // one wave, and no more warps than the longest possible line has units
+    const int64_t capacity = (int64_t)a.max_pages << a.page_shift;
+    const int64_t most = step_items<Core>(a) * (capacity / FlatCfg<Core>::UNIT + 1);
+    const int64_t grid = std::min((int64_t)sms * Core::kCtas, (most + kWarps - 1) / kWarps);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr = follows_on();
     cfg.stream = stream;

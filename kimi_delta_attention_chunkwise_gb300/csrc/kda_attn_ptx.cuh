@@ -103,6 +103,32 @@ __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Asks for a block of the grid that has not started, to be worked on here;
+// 16 bytes of answer go to `to`.
+__device__ __forceinline__ void request_block(uint4 *to, uint64_t *bar) {
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+        "[%0], [%1];" ::"r"(smem_u32(to)),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+constexpr uint32_t kNoBlock = 0xffffffffu;  // every block has started (no more requests then)
+__device__ __forceinline__ uint32_t answered_block(const uint4 *from) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+        : "=&r"(got), "=&r"(x)
+        : "r"(smem_u32(from))
+        : "memory");
+    return got ? x : kNoBlock;
+}
+
 // A bf16 [T, heads, D] tensor with a token stride (in elements) as a 3-D map
 // {D, heads, T} whose box is [box_tokens x box_heads] rows of 64 channels with
 // the 128-byte swizzle; rows past T read as zero.

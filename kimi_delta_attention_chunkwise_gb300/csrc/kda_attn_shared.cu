@@ -71,6 +71,29 @@ __global__ void __launch_bounds__(kThreads, Core::kCtas) attn_prefix_kernel(cons
     }
 }
 
+// The step's core behind the shared tokens.
+template <class F>
+auto with_rest_core(int32_t D, int32_t G, int32_t dtype, F f) {
+    if (dtype == KDA_DTYPE_BF16 && D == 64) {
+        if (G <= 4) return f(MmaCore<64, 1, true, __nv_bfloat16, true>{});
+        if (G <= 8) return f(MmaCore<64, 1, false, __nv_bfloat16, true>{});
+        return f(MmaCore<64, 2, false, __nv_bfloat16, true>{});
+    }
+    if (dtype == KDA_DTYPE_BF16 && D == 128) {
+        if (G <= 4) return f(MmaCore<128, 1, true, __nv_bfloat16, true>{});
+        if (G <= 8) return f(MmaCore<128, 1, false, __nv_bfloat16, true>{});
+        return f(MmaCore<128, 2, false, __nv_bfloat16, true>{});
+    }
+    if (dtype == KDA_DTYPE_BF16)
+        return D == 16 ? f(SimtCore<__nv_bfloat16, 16>{}) : f(SimtCore<__nv_bfloat16, 32>{});
+    switch (D) {
+        case 16: return f(SimtCore<float, 16>{});
+        case 32: return f(SimtCore<float, 32>{});
+        case 64: return f(SimtCore<float, 64>{});
+        default: return f(SimtCore<float, 128>{});
+    }
+}
+
 // Scratch of the step's parts.
 template <class Core>
 size_t rest_bytes(int sms) {
@@ -109,7 +132,7 @@ struct Plan {
 cudaError_t plan_of(const AttnStepArgs &a, Plan &p) {
     const int sms = device_sms();
     if (!sms) return cudaErrorUnknown;
-    with_core(a.D, a.G, a.dtype, [&](auto core) -> int {
+    with_rest_core(a.D, a.G, a.dtype, [&](auto core) -> int {
         using Core = decltype(core);
         p.part = (rest_bytes<Core>(sms) + 255) / 256 * 256;
         p.owners = owners_bytes<Core>(a);
@@ -169,7 +192,7 @@ cudaError_t launch_attn_step_shared(const AttnStepArgs &args, cudaStream_t strea
         });
     }
     if (e != cudaSuccess) return e;
-    return with_core(a.D, a.G, a.dtype, [&](auto core) -> cudaError_t {
+    return with_rest_core(a.D, a.G, a.dtype, [&](auto core) -> cudaError_t {
         return launch_rest<decltype(core)>(a, device_sms(), stream);
     });
 }

@@ -561,7 +561,10 @@ __device__ __forceinline__ uint2 load_once8(const void *p) {
     return x;
 }
 
-template <int D, int NT, bool FOLD = false, typename C = __nv_bfloat16>
+// TILED: rows come by way of shared memory (kda_attn_flat.cuh), in 128-byte panels
+// with the copies' swizzle; 8-bit codes always take their tokens in that order.
+template <int D, int NT, bool FOLD = false, typename C = __nv_bfloat16,
+          bool TILED = sizeof(C) == 1>
 struct MmaCore {
     static_assert(!FOLD || NT == 1, "the heads twice in 8 columns");
     using Type = __nv_bfloat16;
@@ -615,12 +618,14 @@ struct MmaCore {
         for (int x = 0; x < 2; ++x)
             qf[n][x] = __shfl_sync(0xffffffffu, back, (2 * (threadIdx.x & 3) + x) * 4);
     }
-    // The token that row r of the products is.  Any order will do; with 8-bit codes
-    // it is one in which rows that lanes read from shared memory together lie in
+    // The token that row r of the products is.  Any order will do; for tiles it is
+    // one in which rows that lanes read from shared memory together lie in
     // different banks, by the swizzle of the copies that bring them (fetch()).
+    static constexpr uint32_t kPanel = D * sizeof(C) < 128 ? D * sizeof(C) : 128;  // bytes of a row
+    static constexpr int kPanels = D * sizeof(C) / kPanel;
     __device__ static int token_of(int r) {
-        if constexpr (!kScaled) return r;
-        if constexpr (D == 128) return r ^ ((r & 1) << 2);
+        if constexpr (!TILED) return r;
+        if constexpr (kPanel == 128) return r ^ ((r & 1) << 2);
         // rows 0, 2, 4, 6: tokens 0, 1, 4, 5; the row behind each: the token's two
         // low bits turned over
         return ((r & 8) | (r & 4) | (r >> 1 & 1)) ^ ((r & 1) * 3);
@@ -693,41 +698,40 @@ struct MmaCore {
                 vf[r] = token_of(g + 8 * r) < n ? __ldg(vsp + token_of(g + 8 * r)) : 0.f;
         }
     }
-    // 16 tokens that have been copied to shared memory (kda_attn_flat.cuh): rows of
-    // keys, of values and the scales of both.  Rows of 8-bit codes have the copies'
-    // swizzle: 16-byte chunk c of row r lies at c ^ (r & 7) (D = 64: c ^ (r >> 1 & 3)).
-    static constexpr uint32_t kRowBytes = D * sizeof(C);
-    // the lane's places in it: key rows g (channels of j = 0 and 1), value rows 2 t
-    // and 2 t + 1, scale g; rows 8 further are 8 tokens further
+    // 16 tokens in tiles in shared memory: panels of keys and of values, and the
+    // scales of both.  16-byte chunk c of row r of a panel lies at c ^ (r & 7) (rows
+    // of 64 bytes: c ^ (r >> 1 & 3)).  The lane's places: key rows g (their first
+    // two vectors), value rows 2 t and 2 t + 1, scale g; rows 8 further are 8
+    // tokens further.
     uint32_t at_k[2], at_v[2], at_f;
+    __device__ static uint32_t chunk_at(int token, int chunk) {
+        return token * kPanel + (chunk ^ (kPanel == 128 ? token & 7 : token >> 1 & 3)) * 16;
+    }
     __device__ void places() {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             at_k[i] = chunk_at(token_of(g), i * 4 + t);
-            at_v[i] = kScaled && D == 64 ? chunk_at(token_of(2 * t + i), g >> 1) + (g & 1) * 8
-                                         : chunk_at(token_of(2 * t + i), g);
+            at_v[i] = kPanel == 64 ? chunk_at(token_of(2 * t + i), g >> 1) + (g & 1) * 8
+                                   : chunk_at(token_of(2 * t + i), g);
         }
         at_f = token_of(g);
     }
-    __device__ static uint32_t chunk_at(int token, int chunk) {
-        const int turn = !kScaled ? 0 : D == 128 ? token & 7 : token >> 1 & 3;
-        return token * kRowBytes + (chunk ^ turn) * 16;
-    }
-    __device__ void fetch(const uint8_t *keys, const uint8_t *values, const float *key_scales,
-                          const float *value_scales) {
+    // panels `panel` bytes apart
+    __device__ void fetch(const uint8_t *keys, const uint8_t *values, uint32_t panel,
+                          const float *key_scales, const float *value_scales) {
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int j = 0; j < KC; ++j)  // (codes: two at most)
-                k[r][j] = *reinterpret_cast<const uint4 *>(
-                    keys + (kScaled ? at_k[j] : at_k[0] + j * 64) + 8 * r * kRowBytes);
+            for (int j = 0; j < KC; ++j)
+                k[r][j] = *reinterpret_cast<const uint4 *>(keys + (j >> 1) * panel + at_k[j & 1] +
+                                                           8 * r * kPanel);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
             for (int c = 0; c < VV; ++c) {
-                const uint8_t *x = values + at_v[r & 1] + c * 128 + (r >> 1) * 8 * kRowBytes;
-                if constexpr (kScaled && D == 64) {
+                const uint8_t *x = values + c * panel + at_v[r & 1] + (r >> 1) * 8 * kPanel;
+                if constexpr (kPanel == 64) {
                     const uint2 y = *reinterpret_cast<const uint2 *>(x);
                     v[r][c].x = y.x;
                     v[r][c].y = y.y;

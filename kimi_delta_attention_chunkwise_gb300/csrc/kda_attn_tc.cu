@@ -192,32 +192,6 @@ __device__ __forceinline__ uint32_t all_ones(const uint4 &x) {
     y |= (x.w & 0x7F807F80u) + 0x00800080u;
     return y & 0x80008000u;
 }
-// Asks for a block of the grid that has not started, to be worked on here;
-// 16 bytes of answer go to `to`.
-__device__ __forceinline__ void request_block(uint4 *to, uint64_t *bar) {
-    mbar_arrive_expect_tx(bar, 16);
-    asm volatile(
-        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
-        "[%0], [%1];" ::"r"(smem_u32(to)),
-        "r"(smem_u32(bar))
-        : "memory");
-}
-constexpr uint32_t kNoBlock = 0xffffffffu;  // every block has started (no more requests then)
-__device__ __forceinline__ uint32_t answered_block(const uint4 *from) {
-    uint32_t got, x;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
-        "ld.shared.b128 r, [%2];\n\t"
-        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t"
-        "mov.u32 %1, 0;\n\t"
-        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
-        : "=&r"(got), "=&r"(x)
-        : "r"(smem_u32(from))
-        : "memory");
-    return got ? x : kNoBlock;
-}
-
 template <int D, int K>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
