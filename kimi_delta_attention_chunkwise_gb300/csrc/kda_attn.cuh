@@ -67,6 +67,7 @@ struct AttnStepArgs {
     const int32_t *shared_pages;     // device [1]
     void *prefix;
     int32_t splits, prefix_rows, prefix_grid;
+    int32_t prefix_sms;              // SMs that the two parts divide among them, 0: they don't
     int2 *owners;                    // by item: who has worked on it (for the join)
 };
 // Scratch of the step on the current device, for these sizes and any lengths.

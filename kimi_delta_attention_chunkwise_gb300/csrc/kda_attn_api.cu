@@ -101,7 +101,7 @@ kdaStatus_t step_sizes(const kdaPagedCache_t *cache, const kdaAttnShape_t *shape
     a.shared_pages = nullptr;
     a.prefix = nullptr;
     a.owners = nullptr;
-    a.splits = a.prefix_rows = a.prefix_grid = 0;
+    a.splits = a.prefix_rows = a.prefix_grid = a.prefix_sms = 0;
     return KDA_SUCCESS;
 }
 

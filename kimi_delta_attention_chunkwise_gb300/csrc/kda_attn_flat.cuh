@@ -24,6 +24,16 @@ namespace {
 
 constexpr long long kFlatWait = 2000000000LL;  // SM clocks, about a second
 
+// Tiled tensor load, 4-D coordinates {x innermost, y, z, w}
+__device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int32_t x, int32_t y,
+                                            int32_t z, int32_t w, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(tc::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(tc::smem_u32(bar))
+        : "memory");
+}
+
 // Where a warp is in the line: unit `tile` of `tiles` of sequence s under key-value
 // head kvh and block `block` of its query heads.
 template <bool SHARED, int UNIT>
@@ -73,12 +83,47 @@ struct FlatCfg {
     static constexpr uint32_t HALF = Core::kPanels * PANEL;       // a unit's keys, or values
     static constexpr uint32_t SMEM = kWarps * RING * SUB * (BLOCK + SCALES);
     static_assert(RING >= 2 && RING * SUB <= 32, "shared memory of an SM");
-    static_assert(PANEL % 1024 == 0, "swizzled tiles");
+    static_assert(PANEL % 1024 == 0 && (Core::kPanels == 1 || SUB == 1), "swizzled tiles");
 };
 
 // The heads of the cache's pages as tensors.
 struct FlatMaps {
     CUtensorMap k, v;
+};
+
+// The workers' shares of the line: `early` of them have 16 parts of it each, the
+// others `late` (SmSplit).  No share is empty.
+struct FlatShares {
+    int64_t units, parts;
+    int32_t early, late, number;
+    // equal shares
+    __device__ FlatShares(int64_t n, int32_t most) : units(n), late(16) {
+        number = early = workers(n, most);
+        parts = 16 * (int64_t)early;
+    }
+    __device__ FlatShares(int64_t n, int32_t most, int32_t first, int32_t weight)
+        : FlatShares(n, most) {
+        const int64_t all = 16 * (int64_t)first + weight * (int64_t)(most - first);
+        if (first <= 0 || weight >= 16 || n < first) return;
+        if (weight == 0 || n * weight < all) {
+            number = early = first;
+            parts = 16 * (int64_t)first;
+        } else {
+            early = first;
+            late = weight;
+            number = most;
+            parts = all;
+        }
+    }
+    __device__ int64_t start(int32_t c) const {
+        const int64_t at = c <= early ? 16 * (int64_t)c : 16 * (int64_t)early + late * (int64_t)(c - early);
+        return units * at / parts;
+    }
+    // the worker that has unit u: the last that starts at or before it
+    __device__ int32_t at(int64_t u) const {
+        const int64_t w = ((u + 1) * parts - 1) / units, e = 16 * (int64_t)early;
+        return (int32_t)(w < e ? w / 16 : early + (w - e) / late);
+    }
 };
 
 // Neighbouring channels of a row's result from its state (mx = -inf: no keys).
@@ -133,17 +178,22 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
     }
     Line<kThreads, SHARED, Cfg::UNIT> line;
     line.scan(a, s_scan);
-    const int64_t units = line.total * items;
-    const int32_t grid = workers(units, (int32_t)gridDim.x * kWarps);
+    FlatShares shares(line.total * items, (int32_t)gridDim.x * kWarps);
+    if (SHARED && a.prefix_sms && (int32_t)gridDim.x == a.prefix_sms * Core::kCtas) {
+        const SmSplit split =
+            sm_split(a, PrefixLine(a, shared_tokens(a)), line.total * Cfg::UNIT);
+        shares = FlatShares(line.total * items, (int32_t)gridDim.x * kWarps,
+                            (a.prefix_sms - split.prefix) * Core::kCtas * kWarps, split.late);
+    }
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         const int32_t c = (int32_t)blockIdx.x * kWarps + w;
-        if (c < grid) line.look(a, share_start(units, c, grid), items, &s_seq[w], &s_base[w]);
+        if (c < shares.number) line.look(a, shares.start(c), items, &s_seq[w], &s_base[w]);
     }
     __syncthreads();
     const int32_t c = (int32_t)blockIdx.x * kWarps + warp;  // this worker
-    if (c < grid) {
-        const int64_t u0 = share_start(units, c, grid), u1 = share_start(units, c + 1, grid);
+    if (c < shares.number) {
+        const int64_t u0 = shares.start(c), u1 = shares.start(c + 1);
         uint8_t *ring = smem + warp * (RING * 2 * Cfg::HALF);
         float *scales = reinterpret_cast<float *>(smem + kWarps * RING * 2 * Cfg::HALF) +
                         warp * (RING * 2 * Cfg::UNIT);  // (kScaled)
@@ -180,13 +230,8 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
                     uint8_t *to = ring + x * (2 * Cfg::HALF) + mine * Core::kPanel;
                     tc::mbar_arrive_expect_tx(
                         &full[x], box * (2 * Cfg::ROW + (Core::kScaled ? 8 : 0)));
-#pragma unroll
-                    for (int p = 0; p < Core::kPanels; ++p) {
-                        const int32_t ch = p * (int)(Core::kPanel / sizeof(typename Core::Cell));
-                        tc::tma_load_3d(to + p * Cfg::PANEL, &maps.k, ch, at, (int32_t)z, &full[x]);
-                        tc::tma_load_3d(to + Cfg::HALF + p * Cfg::PANEL, &maps.v, ch, at, (int32_t)z,
-                                        &full[x]);
-                    }
+                    tma_load_4d(to, &maps.k, 0, at, 0, (int32_t)z, &full[x]);
+                    tma_load_4d(to + Cfg::HALF, &maps.v, 0, at, 0, (int32_t)z, &full[x]);
                     if constexpr (Core::kScaled) {
                         const int64_t row = (z << a.page_shift) + at;
                         float *f = scales + x * (2 * Cfg::UNIT) + mine;
@@ -255,14 +300,15 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
                         tc::fence_proxy_async();  // before copies to this place
                         __syncwarp();
                     }
-                    core.fetch(keys, values, Cfg::PANEL, f, f + Cfg::UNIT);
+                    core.fetch_k(keys, Cfg::PANEL, f);
+                    core.scores();
+                    core.fetch_v(values, Cfg::PANEL, f + Cfg::UNIT);
                 }
                 if (b == SUB - 1) {
                     __syncwarp();
                     copy_next(x);
                 }
                 if (ok) {
-                    core.scores();
                     core.values(n);
                     seen = true;
                 }
@@ -303,7 +349,8 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
                 }
                 if (ends && lane == 0) {
                     int2 &to = a.owners[(int64_t)here.s * items + here.kvh * blocks + here.block];
-                    to = whole ? make_int2(c, 2) : owners_of(units, first, c, grid);
+                    const int32_t c0 = whole ? c : shares.at(first);
+                    to = make_int2(c0, (c - c0 + 1) * 2 + (!whole && shares.start(c0) != first));
                 }
                 fresh = true;
                 first_item = false;
@@ -474,19 +521,20 @@ cudaError_t launch_rows_join(const AttnStepArgs &a, const float *part, int sms,
                               parts);
 }
 
-// A cache [heads of pages, page, D] as a 3-D map whose box is a panel of up to 32
-// rows of one page, swizzled by its width.
+// A cache [heads of pages, page, D] as a 4-D map {panel, page, panels, heads} whose
+// box is all panels of up to 32 rows of one page, swizzled by the panels' width.
 template <class Core>
-bool encode_panel_map(CUtensorMap *m, const void *base, int32_t page, int32_t heads) {
+bool encode_panels_map(CUtensorMap *m, const void *base, int32_t page, int32_t heads) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint64_t es = sizeof(typename Core::Cell), row = Core::kD * es;
-    const cuuint64_t dims[3] = {(cuuint64_t)Core::kD, (cuuint64_t)page, (cuuint64_t)heads};
-    const cuuint64_t strides[2] = {row, row * page};
-    const cuuint32_t box[3] = {(cuuint32_t)(Core::kPanel / es),
-                               (cuuint32_t)std::min<int32_t>(page, FlatCfg<Core>::UNIT), 1u};
-    const cuuint32_t estr[3] = {1u, 1u, 1u};
-    return enc(m, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+    const cuuint32_t panel = (cuuint32_t)(Core::kPanel / es), panels = Core::kPanels;
+    const cuuint32_t rows = (cuuint32_t)std::min<int32_t>(page, FlatCfg<Core>::UNIT);
+    const cuuint64_t dims[4] = {panel, (cuuint64_t)page, panels, (cuuint64_t)heads};
+    const cuuint64_t strides[3] = {row, Core::kPanel, row * page};
+    const cuuint32_t box[4] = {panel, rows, panels, 1u};
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    return enc(m, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                Core::kPanel == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -505,8 +553,8 @@ cudaError_t launch_flat(AttnStepArgs a, float *part, int sms, cudaStream_t strea
     const int32_t heads = std::max(a.num_pages * a.HKV, 1);
     FlatMaps maps;
     memset(&maps, 0, sizeof(maps));
-    if (!encode_panel_map<Core>(&maps.k, a.num_pages ? a.k_cache : a.q, page, heads) ||
-        !encode_panel_map<Core>(&maps.v, a.num_pages ? a.v_cache : a.q, page, heads))
+    if (!encode_panels_map<Core>(&maps.k, a.num_pages ? a.k_cache : a.q, page, heads) ||
+        !encode_panels_map<Core>(&maps.v, a.num_pages ? a.v_cache : a.q, page, heads))
         return cudaErrorInvalidValue;
     // one wave, and no more warps than the longest possible line has units
     const int64_t capacity = (int64_t)a.max_pages << a.page_shift;

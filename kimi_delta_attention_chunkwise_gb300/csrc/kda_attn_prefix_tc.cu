@@ -59,6 +59,7 @@ struct Shared {
     uint64_t s_full[2][2], pv_done[2][2], o_free[2];  // by row tile (and its units, in turn)
     uint64_t p_full[2], p_rest[2];                    // by score tile
     uint64_t drained;
+    unsigned long long own;
     uint32_t tmem;
     int32_t abort, seq;
 };
@@ -103,11 +104,13 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap map_q,
     const int32_t shared = shared_tokens(a);
     if (blockIdx.x == 0 && tid == 0 && (*a.shared_pages < 0 || *a.shared_pages > a.max_pages))
         *a.status = KDA_ERR_INVALID_ARG;
-    const PrefixLine line(a, shared);
+    PrefixLine line(a, shared);
     const int32_t cta = (int32_t)blockIdx.x;
     if (cta >= line.grid) return;
-    const int32_t seq = sharing_sequence<kThreadsTc>(a, shared, &sh.seq);
+    const int32_t seq = sharing_sequence<kThreadsTc>(a, shared, &sh.seq, &sh.own);
     if (seq >= a.N) return;
+    line.grid = min(line.grid, sm_split(a, line, (int64_t)sh.own).prefix);
+    if (cta >= line.grid) return;
     const int32_t R = kRowTile / a.G;  // sequences of a row tile
     const int32_t *table = a.block_table + (int64_t)seq * a.max_pages;
     const int64_t u0 = share_start(line.units, cta, line.grid),

@@ -25,6 +25,7 @@ __global__ void __launch_bounds__(kThreads, Core::kCtas) attn_prefix_kernel(cons
     constexpr int D = Core::kD, R = Core::kRows;
     __shared__ Joined<Core> state;
     __shared__ int32_t s_seq;
+    __shared__ unsigned long long s_own;
     const int tid = threadIdx.x, warp = tid >> 5;
     tc::pdl_launch_dependents();
     const int32_t shared = shared_tokens(a);
@@ -33,7 +34,7 @@ __global__ void __launch_bounds__(kThreads, Core::kCtas) attn_prefix_kernel(cons
     const PrefixLine line(a, shared);
     const int32_t c = (int32_t)blockIdx.x;
     if (c >= line.grid) return;
-    const int32_t s = sharing_sequence<kThreads>(a, shared, &s_seq);
+    const int32_t s = sharing_sequence<kThreads>(a, shared, &s_seq, &s_own);
     if (s >= a.N) return;
     const int64_t u1 = share_start(line.units, c + 1, line.grid);
     Core core;
@@ -180,6 +181,7 @@ cudaError_t launch_attn_step_shared(const AttnStepArgs &args, cudaStream_t strea
     a.splits = p.splits;
     a.prefix_rows = p.rows;
     a.prefix_grid = p.grid;
+    a.prefix_sms = p.tensor ? device_sms() : 0;
     char *ws = static_cast<char *>(a.workspace);
     a.owners = reinterpret_cast<int2 *>(ws + p.part);
     a.prefix = ws + p.part + p.owners;

@@ -107,6 +107,37 @@ struct PrefixPiece {
         last = tile1 == p.tiles;
     }
 };
+// How the SMs are divided between the shared tokens' kernel on the tensor cores, one
+// CTA to an SM, and the step behind it, whose CTAs find no room beside one: the
+// former is bound by what an SM computes, the latter by memory, which fewer SMs
+// than all can keep busy.  `prefix`: so many SMs for the former that it ends when
+// the latter does.  CTAs of the step that must wait for those get shares of
+// late / 16 of the others'.  Times in SM ns: a unit of the line by what was measured
+// of it (PAIR, SINGLE), the step's rows by what one SM draws (RATE).  Both kernels
+// work it out by themselves; if their sums of tokens differ, so does the time alone.
+struct SmSplit {
+    int32_t prefix, late;
+};
+__device__ __forceinline__ SmSplit sm_split(const AttnStepArgs &a, const PrefixLine &line,
+                                            int64_t own_tokens) {
+    const int32_t sms = a.prefix_sms;
+    if (line.units == 0) return {0, 16};
+    const bool two = a.prefix_rows > 128 / a.G * a.G;  // row tiles to a unit
+    const float unit = (two ? 1700.f : 1200.f) * (a.D == 64 ? 0.7f : 1.f), start = 8000.f;
+    const float work = (float)line.units * unit;
+    const float own = (float)own_tokens * a.HKV * (4.f * a.D) / 75.f;
+    // the least number of SMs that end in time
+    int32_t best = sms;
+    for (int32_t p = (int32_t)(threadIdx.x & 31) + 1; p < sms; p += 32)
+        if (start + work / p <= (own + work + start * p) / sms) {
+            best = p;
+            break;
+        }
+    best = __reduce_min_sync(0xffffffffu, best);
+    const float all = (own + work + start * best) / sms;
+    const float left = 16.f * (all - start - work / best) / all;
+    return {best, best == sms ? 16 : min(max((int32_t)left, 0), 16)};
+}
 // One piece's states of every row (here a row is sequence * HQ + query head), and
 // the number of pieces that a row has.
 struct PrefixState {
@@ -156,20 +187,33 @@ __device__ __forceinline__ int32_t tiles_of(int32_t len) {
     return len / TILE + (len % TILE != 0);
 }
 
-// The first sequence that holds all `shared` tokens (N: none does), for the
-// whole CTA, by way of `out` in shared memory.  Sequences that hold fewer may
-// have anything in their rows of the table.
+// The first sequence that holds all `shared` tokens (N: none does), for the whole
+// CTA, by way of `out` in shared memory, and, to *own, the tokens of all
+// sequences that are not shared.  Sequences that hold fewer may have anything in
+// their rows of the table.
 template <int THREADS>
 __device__ __forceinline__ int32_t sharing_sequence(const AttnStepArgs &a, int32_t shared,
-                                                    int32_t *out) {
-    if (threadIdx.x == 0) *out = a.N;
-    __syncthreads();
-    for (int32_t s0 = 0; s0 < a.N; s0 += THREADS) {
-        const int32_t s = s0 + (int32_t)threadIdx.x;
-        const bool holds = s < a.N && clamp_len(a, s) >= shared;
-        if (holds) atomicMin(out, s);
-        if (__syncthreads_or(holds)) break;
+                                                    int32_t *out, unsigned long long *own) {
+    if (threadIdx.x == 0) {
+        *out = a.N;
+        *own = 0;
     }
+    __syncthreads();
+    int32_t first = a.N;
+    long long mine = 0;
+    for (int32_t s = (int32_t)threadIdx.x; s < a.N; s += THREADS) {
+        const int32_t len = clamp_len(a, s);
+        mine += len >= shared ? len - shared : len;
+        if (len >= shared) first = min(first, s);
+    }
+    first = __reduce_min_sync(0xffffffffu, first);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if ((threadIdx.x & 31) == 0) {
+        atomicMin_block(out, first);
+        atomicAdd_block(own, (unsigned long long)mine);
+    }
+    __syncthreads();
     return *out;
 }
 
@@ -718,14 +762,19 @@ struct MmaCore {
         at_f = token_of(g);
     }
     // panels `panel` bytes apart
-    __device__ void fetch(const uint8_t *keys, const uint8_t *values, uint32_t panel,
-                          const float *key_scales, const float *value_scales) {
+    __device__ void fetch_k(const uint8_t *keys, uint32_t panel, const float *scales) {
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int j = 0; j < KC; ++j)
                 k[r][j] = *reinterpret_cast<const uint4 *>(keys + (j >> 1) * panel + at_k[j & 1] +
                                                            8 * r * kPanel);
+        if constexpr (kScaled) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) kf[r] = scales[at_f + 8 * r];
+        }
+    }
+    __device__ void fetch_v(const uint8_t *values, uint32_t panel, const float *scales) {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -741,10 +790,7 @@ struct MmaCore {
             }
         if constexpr (kScaled) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                kf[r] = key_scales[at_f + 8 * r];
-                vf[r] = value_scales[at_f + 8 * r];
-            }
+            for (int r = 0; r < 2; ++r) vf[r] = scales[at_f + 8 * r];
         }
     }
     __device__ void scores() {
