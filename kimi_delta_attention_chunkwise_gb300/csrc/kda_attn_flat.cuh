@@ -35,9 +35,11 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int32_t
 }
 
 // Where a warp is in the line: unit `tile` of `tiles` of sequence s under key-value
-// head kvh and block `block` of its query heads.
-template <bool SHARED, int UNIT>
+// head kvh and block `block` of its query heads.  `at`: its place in the line, where
+// every item's units come behind COST places for what the item takes besides them.
+template <bool SHARED, int UNIT, int COST>
 struct LineCursor {
+    int64_t at;
     int32_t s, kvh, block, tile, tiles, first, end;
     __device__ void enter(const AttnStepArgs &a, int32_t seq) {
         s = seq;
@@ -46,16 +48,22 @@ struct LineCursor {
         end = span.end;
         tiles = tiles_of<UNIT>(span.len());
     }
-    // unit u, which is one of sequence seq's, whose units start at base
+    // the first unit at place u or behind it, u being one of sequence seq's, whose
+    // places start at base
     __device__ void seek(const AttnStepArgs &a, int32_t blocks, int32_t seq, int64_t base, int64_t u) {
         enter(a, seq);
-        const int32_t item = (int32_t)((u - base) / tiles);
-        tile = (int32_t)((u - base) - (int64_t)item * tiles);
+        const int32_t item = (int32_t)((u - base) / (tiles + COST));
+        const int32_t off = (int32_t)((u - base) - (int64_t)item * (tiles + COST));
+        tile = max(off - COST, 0);
+        at = u + max(COST - off, 0);
         kvh = item / blocks;
         block = item - kvh * blocks;
     }
-    // the next unit (there is one)
+    // the next unit, which may be behind the line
+    __device__ int64_t after() const { return at + (tile + 1 < tiles ? 1 : 1 + COST); }
+    // goes there (there is one)
     __device__ void next(const AttnStepArgs &a, int32_t blocks) {
+        at = after();
         if (++tile < tiles) return;
         tile = 0;
         if (++block < blocks) return;
@@ -79,6 +87,9 @@ struct FlatCfg {
     // its tokens is a third of the instructions
     static constexpr int SUB = ROOM >= 4 ? 2 : 1, UNIT = SUB * kWarpTokens;
     static constexpr int RING = ROOM / SUB < 4 ? ROOM / SUB : 4;  // units
+    // what an item takes besides its units (queries, results), in units: 256 sequences
+    // of 1-600 tokens, whose shares hold a few items or tens, 78-99 us without
+    static constexpr int COST = SUB == 2 ? 1 : 2;
     static constexpr uint32_t PANEL = UNIT * Core::kPanel;        // a panel of a unit's keys
     static constexpr uint32_t HALF = Core::kPanels * PANEL;       // a unit's keys, or values
     static constexpr uint32_t SMEM = kWarps * RING * SUB * (BLOCK + SCALES);
@@ -92,20 +103,21 @@ struct FlatMaps {
 };
 
 // The workers' shares of the line: `early` of them have 16 parts of it each, the
-// others `late` (SmSplit).  No share is empty.
+// others `late` (SmSplit).  No share is smaller than LEAST, unless there is one.
+template <int LEAST>
 struct FlatShares {
     int64_t units, parts;
     int32_t early, late, number;
     // equal shares
     __device__ FlatShares(int64_t n, int32_t most) : units(n), late(16) {
-        number = early = workers(n, most);
+        number = early = n > 0 ? max(workers(n / LEAST, most), 1) : 0;
         parts = 16 * (int64_t)early;
     }
     __device__ FlatShares(int64_t n, int32_t most, int32_t first, int32_t weight)
         : FlatShares(n, most) {
         const int64_t all = 16 * (int64_t)first + weight * (int64_t)(most - first);
-        if (first <= 0 || weight >= 16 || n < first) return;
-        if (weight == 0 || n * weight < all) {
+        if (first <= 0 || weight >= 16 || n < LEAST * (int64_t)first) return;
+        if (weight == 0 || n * weight < LEAST * all) {
             number = early = first;
             parts = 16 * (int64_t)first;
         } else {
@@ -157,7 +169,7 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
     using Cfg = FlatCfg<Core>;
     constexpr int D = Core::kD, R = Core::kRows, RING = Cfg::RING, SUB = Cfg::SUB;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ int64_t s_scan[kWarps], s_base[kWarps];
+    __shared__ int64_t s_scan[2 * kWarps], s_base[kWarps];
     __shared__ int32_t s_seq[kWarps];
     __shared__ uint64_t s_full[kWarps][RING];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -176,14 +188,16 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
         tc::fence_mbar_init();
         tc::fence_proxy_async();
     }
-    Line<kThreads, SHARED, Cfg::UNIT> line;
+    constexpr int COST = Cfg::COST;
+    Line<kThreads, SHARED, Cfg::UNIT, COST> line;
     line.scan(a, s_scan);
-    FlatShares shares(line.total * items, (int32_t)gridDim.x * kWarps);
+    // (a share of more than COST places has a unit)
+    using Shares = FlatShares<COST + 2>;
+    Shares shares(line.total * items, (int32_t)gridDim.x * kWarps);
     if (SHARED && a.prefix_sms && (int32_t)gridDim.x == a.prefix_sms * Core::kCtas) {
-        const SmSplit split =
-            sm_split(a, PrefixLine(a, shared_tokens(a)), line.total * Cfg::UNIT);
-        shares = FlatShares(line.total * items, (int32_t)gridDim.x * kWarps,
-                            (a.prefix_sms - split.prefix) * Core::kCtas * kWarps, split.late);
+        const SmSplit split = sm_split(a, PrefixLine(a, shared_tokens(a)), line.tokens);
+        shares = Shares(line.total * items, (int32_t)gridDim.x * kWarps,
+                        (a.prefix_sms - split.prefix) * Core::kCtas * kWarps, split.late);
     }
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
@@ -200,7 +214,7 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
         uint64_t *full = s_full[warp];
         uint32_t good = 0;   // a bit per 16 tokens in the ring: they are there
         uint32_t phase = 0;  // a bit per unit's barrier
-        LineCursor<SHARED, Cfg::UNIT> here, ahead;
+        LineCursor<SHARED, Cfg::UNIT, COST> here, ahead;
         here.seek(a, blocks, s_seq[warp], s_base[warp], u0);
         ahead = here;
         // lane i < SUB: the i-th 16 tokens of the unit at `ahead`, and the entry of the
@@ -212,12 +226,13 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
                        ? a.block_table[(int64_t)ahead.s * a.max_pages + (tok >> a.page_shift)]
                        : 0;
         };
-        int64_t au = u0;  // the unit at `ahead`
+        bool more = true;  // there is a unit at `ahead`
+        int32_t units_ahead = 0;  // copied and not worked on yet
         int32_t page = entry_of();
         // starts the copies of the unit at `ahead` to place x of the ring: whole boxes
         // (what lies behind the sequence is put out of the way in values())
         auto copy_next = [&](int32_t x) {
-            if (au >= u1) return;
+            if (!more) return;
             const int32_t tok = ahead.token() + mine, n = min(kWarpTokens, ahead.end - tok);
             const bool there = page >= 0 && page < a.num_pages, ok = there && n > 0;
             if (n > 0 && !there) *a.status = KDA_ERR_INVALID_ARG;
@@ -243,7 +258,9 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
             constexpr uint32_t all = (1u << SUB) - 1;
             good = (good & ~(all << (x * SUB))) |
                    ((__ballot_sync(0xffffffffu, ok) & all) << (x * SUB));
-            if (++au < u1) {
+            ++units_ahead;
+            more = ahead.after() < u1;
+            if (more) {
                 ahead.next(a, blocks);
                 page = entry_of();
             }
@@ -261,8 +278,7 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
         core.places();
         int32_t x = 0;  // the place in the ring
         bool fresh = true, seen = false, first_item = true;
-        int64_t u = u0;
-        for (; u < u1; ++u) {
+        for (bool last = false; !last;) {
             const int32_t rows = min(R, a.G - here.block * R);
             const int64_t head = (int64_t)here.kvh * a.G + here.block * R;
             if (fresh) {
@@ -270,6 +286,7 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
                 core.init([&](int h) { return qp + h * D; }, rows, a.scale);
                 fresh = seen = false;
             }
+            --units_ahead;
             if (!wait(x)) {
                 *a.status = KDA_ERR_TIMEOUT;
                 break;
@@ -315,8 +332,9 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
             }
             x = x + 1 == RING ? 0 : x + 1;
             const bool ends = here.tile + 1 == here.tiles;
-            if (ends || u + 1 == u1) {
-                const int64_t first = u - here.tile;  // the item's first unit
+            last = here.after() >= u1;
+            if (ends || last) {
+                const int64_t first = here.at - here.tile;  // the item's first unit
                 const bool whole = ends && first >= u0;
                 const int64_t row = (int64_t)here.s * a.HQ + head;
                 if (whole && !SHARED) {
@@ -350,17 +368,17 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
                 if (ends && lane == 0) {
                     int2 &to = a.owners[(int64_t)here.s * items + here.kvh * blocks + here.block];
                     const int32_t c0 = whole ? c : shares.at(first);
-                    to = make_int2(c0, (c - c0 + 1) * 2 + (!whole && shares.start(c0) != first));
+                    to = make_int2(c0, (c - c0 + 1) * 2 + (!whole && shares.start(c0) < first - COST));
                 }
                 fresh = true;
                 first_item = false;
             }
-            if (u + 1 < u1) here.next(a, blocks);
+            if (!last) here.next(a, blocks);
         }
         // (a wait gave up: the CTA may end when the copies behind it have landed)
-        for (; u < au; ++u) {
-            (void)wait(x);
+        for (; units_ahead > 0; --units_ahead) {
             x = x + 1 == RING ? 0 : x + 1;
+            (void)wait(x);
         }
     }
     if (SHARED) tc::pdl_wait_primaries();
@@ -558,7 +576,8 @@ cudaError_t launch_flat(AttnStepArgs a, float *part, int sms, cudaStream_t strea
         return cudaErrorInvalidValue;
     // one wave, and no more warps than the longest possible line has units
     const int64_t capacity = (int64_t)a.max_pages << a.page_shift;
-    const int64_t most = step_items<Core>(a) * (capacity / FlatCfg<Core>::UNIT + 1);
+    const int64_t most =
+        step_items<Core>(a) * (capacity / FlatCfg<Core>::UNIT + 1 + FlatCfg<Core>::COST);
     const int64_t grid = std::min((int64_t)sms * Core::kCtas, (most + kWarps - 1) / kWarps);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr = follows_on();

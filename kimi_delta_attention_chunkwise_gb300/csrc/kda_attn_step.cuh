@@ -112,9 +112,8 @@ struct PrefixPiece {
 // former is bound by what an SM computes, the latter by memory, which fewer SMs
 // than all can keep busy.  `prefix`: so many SMs for the former that it ends when
 // the latter does.  CTAs of the step that must wait for those get shares of
-// late / 16 of the others'.  Times in SM ns: a unit of the line by what was measured
-// of it (PAIR, SINGLE), the step's rows by what one SM draws (RATE).  Both kernels
-// work it out by themselves; if their sums of tokens differ, so does the time alone.
+// late / 16 of the others'.  Times in ns of an SM, by what was measured: 1.7 us to a
+// unit of the line with two row tiles, 1.2 with one, d = 128; 75 GB/s of cached rows.
 struct SmSplit {
     int32_t prefix, late;
 };
@@ -123,19 +122,23 @@ __device__ __forceinline__ SmSplit sm_split(const AttnStepArgs &a, const PrefixL
     const int32_t sms = a.prefix_sms;
     if (line.units == 0) return {0, 16};
     const bool two = a.prefix_rows > 128 / a.G * a.G;  // row tiles to a unit
-    const float unit = (two ? 1700.f : 1200.f) * (a.D == 64 ? 0.7f : 1.f), start = 8000.f;
-    const float work = (float)line.units * unit;
-    const float own = (float)own_tokens * a.HKV * (4.f * a.D) / 75.f;
+    // (each operation rounded by itself: the same division in both kernels)
+    const float unit = (two ? 1700.f : 1200.f) * (a.D == 64 ? 0.75f : 1.f), start = 8000.f;
+    const float work = __fmul_rn((float)line.units, unit);
+    const float own = __fmul_rn(__fmul_rn((float)own_tokens, (float)a.HKV), a.D / 18.75f);
+    auto all = [&](int32_t p) {
+        return __fdiv_rn(__fadd_rn(__fadd_rn(own, work), __fmul_rn(start, (float)p)), (float)sms);
+    };
+    auto ends = [&](int32_t p) { return __fadd_rn(start, __fdiv_rn(work, (float)p)); };
     // the least number of SMs that end in time
     int32_t best = sms;
     for (int32_t p = (int32_t)(threadIdx.x & 31) + 1; p < sms; p += 32)
-        if (start + work / p <= (own + work + start * p) / sms) {
+        if (ends(p) <= all(p)) {
             best = p;
             break;
         }
     best = __reduce_min_sync(0xffffffffu, best);
-    const float all = (own + work + start * best) / sms;
-    const float left = 16.f * (all - start - work / best) / all;
+    const float left = __fdiv_rn(__fmul_rn(16.f, __fsub_rn(all(best), ends(best))), all(best));
     return {best, best == sms ? 16 : min(max((int32_t)left, 0), 16)};
 }
 // One piece's states of every row (here a row is sequence * HQ + query head), and
@@ -218,19 +221,26 @@ __device__ __forceinline__ int32_t sharing_sequence(const AttnStepArgs &a, int32
 }
 
 // Prefix sums of the sequences' tiles, each thread holding a run of sequences.
-template <int THREADS, bool SHARED, int TILE = kTile>
+// COST: what an item (of at least a tile) counts for besides its tiles, in tiles.
+template <int THREADS, bool SHARED, int TILE = kTile, int COST = 0>
 struct Line {
+    __device__ static int32_t length_of(const AttnStepArgs &a, int32_t s) {
+        const int32_t tiles = tiles_of<TILE>(span_of<SHARED>(a, s).len());
+        return COST && tiles ? tiles + COST : tiles;
+    }
     int64_t total;   // tiles of all sequences
     int64_t before;  // tiles before this thread's run
+    int64_t tokens;  // (COST) tokens of all sequences
     int32_t s0, s1;  // this thread's run
-    __device__ void scan(const AttnStepArgs &a, int64_t *sm /* [THREADS / 32] */) {
+    __device__ void scan(const AttnStepArgs &a, int64_t *sm /* [THREADS / 32], COST: twice */) {
         const int tid = threadIdx.x, lane = tid & 31;
         const int32_t per = (a.N + THREADS - 1) / THREADS;
         s0 = min(tid * per, a.N);
         s1 = min(s0 + per, a.N);
-        int64_t mine = 0;
+        int64_t mine = 0, held = 0;
         for (int32_t s = s0; s < s1; ++s) {
-            mine += tiles_of<TILE>(span_of<SHARED>(a, s).len());
+            mine += length_of(a, s);
+            if (COST) held += span_of<SHARED>(a, s).len();
             if (a.seq_lens[s] > (a.max_pages << a.page_shift)) *a.status = KDA_ERR_INVALID_ARG;
         }
         int64_t incl = mine;
@@ -240,12 +250,18 @@ struct Line {
             if (lane >= o) incl += x;
         }
         if (lane == 31) sm[tid >> 5] = incl;
+        if constexpr (COST > 0) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) held += __shfl_xor_sync(0xffffffffu, held, o);
+            if (lane == 0) sm[THREADS / 32 + (tid >> 5)] = held;
+        }
         __syncthreads();
         before = incl - mine;
-        total = 0;
+        total = tokens = 0;
         for (int w = 0; w < THREADS / 32; ++w) {
             if (w < (tid >> 5)) before += sm[w];
             total += sm[w];
+            if (COST) tokens += sm[THREADS / 32 + w];
         }
     }
     // The sequence of unit u (u < total * items) and the units before it, to
@@ -260,7 +276,7 @@ struct Line {
         int64_t b = before * items;
         if (u >= b) {
             for (int32_t s = s0; s < s1; ++s) {
-                const int64_t n = (int64_t)tiles_of<TILE>(span_of<SHARED>(a, s).len()) * items;
+                const int64_t n = (int64_t)length_of(a, s) * items;
                 if (u < b + n) {
                     *seq = s;
                     *base = b;
@@ -274,7 +290,7 @@ struct Line {
     __device__ void base_of(const AttnStepArgs &a, int32_t seq, int32_t items, int64_t *base) const {
         if (seq >= s0 && seq < s1) {
             int64_t b = before;
-            for (int32_t s = s0; s < seq; ++s) b += tiles_of<TILE>(span_of<SHARED>(a, s).len());
+            for (int32_t s = s0; s < seq; ++s) b += length_of(a, s);
             *base = b * items;
         }
         __syncthreads();
