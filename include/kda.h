@@ -778,8 +778,8 @@ kdaStatus_t kda_attn_step_q8_ws(const void *q, const kdaPagedCacheQ8_t *cache,
  *
  * The result is kda_attn_step's with the same arguments (sums in another
  * order).  A sequence with fewer tokens is worked on by itself, and its row of
- * block_table may hold anything behind them.  Where the rows do differ, the
- * first such sequence's entries are taken for all.  A number below 0 or above
+ * block_table may hold anything behind them.  Where the rows do differ,
+ * each sequence's own entries or another's are taken.  A number below 0 or above
  * max_pages is cut to it and sets KDA_ERR_INVALID_ARG in the device status
  * word; so does a shared page that is negative or >= num_pages, whose tokens
  * are left out for every sequence that shares it.  Lengths, pages, scratch

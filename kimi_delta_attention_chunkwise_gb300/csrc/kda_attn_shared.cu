@@ -5,10 +5,17 @@
 // tokens before and from S on.  The first part is a product of all sequences'
 // queries of a key-value head with the same keys: one kernel takes blocks of
 // (sequence, query head) rows over them, cut among several CTAs, and leaves a
-// state (maximum, sum, weighted sum) per row and piece.  The second part is the
-// step of kda_attn_step.cuh from token S on, whose CTAs start as those of the
-// first leave; it leaves states, too, and a third kernel joins all of a row's.  A
-// sequence that holds less than S tokens is all the step's.
+// state (maximum, sum, weighted sum) per row and piece.  The second part is a
+// step from token S on, by warps for bf16 with d = 64 or 128, whose CTAs start on
+// the SMs that the first leaves free; it leaves states, too, and a third kernel
+// joins all of a row's.  A sequence that holds less than S tokens is all the
+// step's.
+//
+// Tables that are short enough for the plain step's one launch of clusters are
+// left to it: reading the shared rows from L2 for every sequence takes less than
+// three kernels do (192 + 50 tokens, 3 sequences, 8/2 heads, d = 64: 4.9 us, 11.6;
+// 1024 + 100, 8 sequences, 32/8 heads, d = 128: 10.7, 22; 1024 + 100, 32 fp32
+// sequences, 6/2 heads, d = 64: 10.5, 14).
 #include "kda_attn_flat.cuh"
 
 namespace kda {
@@ -125,6 +132,7 @@ cudaError_t launch_rest(const AttnStepArgs &a, int sms, cudaStream_t stream) {
 
 // How a call's work on the shared tokens is cut, and its scratch in bytes.
 struct Plan {
+    int direct;  // CTAs to an item of the step's direct kernel, which does it all; 0: it doesn't
     bool tensor;
     int32_t rows, grid, splits;
     size_t part, owners, prefix;  // in this order
@@ -140,6 +148,13 @@ cudaError_t plan_of(const AttnStepArgs &a, Plan &p) {
         return 0;
     });
     p.tensor = a.dtype == KDA_DTYPE_BF16 && a.D >= 64 && (int64_t)a.N * a.G > kFewRows;
+    p.direct = with_core(a.D, a.G, a.dtype, [&](auto core) -> int {
+        return step_direct_ctas<decltype(core)>(a, sms);
+    });
+    if (p.direct) {
+        p.part = p.owners = p.prefix = 0;
+        return cudaSuccess;
+    }
     int64_t slots = sms;
     if (p.tensor) {
         p.rows = prefix_tc_rows(a);
@@ -178,6 +193,10 @@ cudaError_t launch_attn_step_shared(const AttnStepArgs &args, cudaStream_t strea
     Plan p;
     cudaError_t e = plan_of(a, p);
     if (e != cudaSuccess) return e;
+    if (p.direct)
+        return with_core(a.D, a.G, a.dtype, [&](auto core) -> cudaError_t {
+            return launch_direct<decltype(core)>(a, p.direct, stream);
+        });
     a.splits = p.splits;
     a.prefix_rows = p.rows;
     a.prefix_grid = p.grid;

@@ -1308,6 +1308,9 @@ attn_step_direct_kernel(const AttnStepArgs a) {
     core.init([&](int h) { return qp + h * D; }, rows, a.scale);
     const int32_t len = clamp_len(a, s), tiles = tiles_of(len);
     if (tid == 0 && a.seq_lens[s] > (a.max_pages << a.page_shift)) *a.status = KDA_ERR_INVALID_ARG;
+    if (tid == 0 && blockIdx.x == 0 && a.shared_pages &&  // (kda_attn_step_shared's)
+        (*a.shared_pages < 0 || *a.shared_pages > a.max_pages))
+        *a.status = KDA_ERR_INVALID_ARG;
     const bool seen = walk_tiles(a, core, s, kvh, 0, len,
                                  (int32_t)((int64_t)tiles * rank / ctas),
                                  (int32_t)((int64_t)tiles * (rank + 1) / ctas));

@@ -242,8 +242,10 @@ def test_shared_streams_graphs_and_workspace(dtype, d, wide):
     need = kda.kda_attn_step_shared_workspace_size(c, shape)
     ws = torch.empty(need + 256, dtype=torch.uint8, device="cuda")
     assert torch.equal(step(0, *settings[1], workspace=ws), want[0, 1])
-    with pytest.raises(kda.KdaError):
-        step(0, *settings[1], workspace=ws[:512])
+    assert (need > 0) == wide   # (short tables take none)
+    if wide:
+        with pytest.raises(kda.KdaError):
+            step(0, *settings[1], workspace=ws[:512])
     # the library's own scratch (C entry without a workspace)
     from kimi_delta_attention_chunkwise_gb300 import binding
     out2 = torch.empty_like(want[0, 1])
