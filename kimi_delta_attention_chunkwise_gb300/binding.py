@@ -947,13 +947,36 @@ def _paged_cache(k_cache, v_cache, block_table, dev, dtype, i32, N, d):
                            size[2], width[1]), size[1]
 
 
+def _cache_q8_shape(k_cache, v_cache, k_scale, v_scale, block_table, dev, N, d, torch):
+    """Raises what is wrong with a cache of 8-bit codes."""
+    _cache_shape(k_cache, v_cache, block_table, dev, torch.int8, torch.int32, N, d)
+    _explain(k_scale, "k_scale", dev, torch.float32, k_cache.shape[:3])
+    _explain(v_scale, "v_scale", dev, torch.float32, k_cache.shape[:3])
+
+
 def _cache_q8(k_cache, v_cache, k_scale, v_scale, block_table, dev, N, d, torch):
     """(the C description of a cache of 8-bit codes, HKV)."""
-    cache, HKV = _paged_cache(k_cache, v_cache, block_table, dev, torch.int8, torch.int32, N, d)
-    size, f32 = k_cache.shape[:3], torch.float32
-    return kdaPagedCacheQ8_t(cache.k, cache.v, _whole(k_scale, "k_scale", dev, f32, size),
-                             _whole(v_scale, "v_scale", dev, f32, size), cache.block_table,
-                             cache.num_pages, cache.page_size, cache.max_pages), HKV
+    i8, f32 = torch.int8, torch.float32
+    try:
+        size, width = k_cache.shape, block_table.shape
+        rows = size[:3]
+        if not (len(size) == 4 and size[3] == d and len(width) == 2 and width[0] == N
+                and k_cache.get_device() == dev and v_cache.get_device() == dev
+                and k_scale.get_device() == dev and v_scale.get_device() == dev
+                and block_table.get_device() == dev and k_cache.dtype is i8
+                and v_cache.dtype is i8 and k_scale.dtype is f32 and v_scale.dtype is f32
+                and block_table.dtype is torch.int32 and v_cache.shape == size
+                and k_scale.shape == rows and v_scale.shape == rows and k_cache.is_contiguous()
+                and v_cache.is_contiguous() and k_scale.is_contiguous()
+                and v_scale.is_contiguous() and block_table.is_contiguous()):
+            _cache_q8_shape(k_cache, v_cache, k_scale, v_scale, block_table, dev, N, d, torch)
+    except AttributeError:
+        _cache_q8_shape(k_cache, v_cache, k_scale, v_scale, block_table, dev, N, d, torch)
+    if size[0] > _I32_MAX or width[1] > _I32_MAX:
+        _fit_i32(size[0], width[1])
+    return kdaPagedCacheQ8_t(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                             v_scale.data_ptr(), block_table.data_ptr(), size[0], size[2],
+                             width[1]), size[1]
 
 
 def _attn_out(q, shape, dev, dt, out, out_f32, stream, torch):
