@@ -405,6 +405,7 @@ __device__ __forceinline__ void load_run(const float *from, float (&x)[N]) {
 template <int D, int R, bool SHARED>
 __global__ void __launch_bounds__(kJoinThreads) attn_rows_join_kernel(const AttnStepArgs a,
                                                                       const float *part,
+                                                                      int32_t workers,
                                                                       int32_t parts) {
     constexpr int N = (D + 31) / 32;  // columns per lane
     __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
@@ -420,8 +421,11 @@ __global__ void __launch_bounds__(kJoinThreads) attn_rows_join_kernel(const Attn
     // the kernels before this one have ended
     tc::pdl_wait_primaries();
     const int2 who = a.owners[((int64_t)s * a.HKV + kvh) * blocks + block];
+    // (a kernel whose wait gave up has said so and left these as they were: anything)
     int32_t own = span.len() > 0 ? who.y >> 1 : 0;
-    const int32_t pieces = SHARED && span.first > 0 ? states.pieces[row < rows ? row : 0] : 0;
+    if (own < 0 || who.x < 0 || own > workers - who.x) own = 0;
+    int32_t pieces = SHARED && span.first > 0 ? states.pieces[row < rows ? row : 0] : 0;
+    if (SHARED) pieces = min(max(pieces, 0), a.splits - 1);
     const bool done = !SHARED && own == 1;  // written by the worker
     const int32_t all = row >= rows || done ? 0 : own + pieces;
     // state i's weighted sums, maximum and sum: a worker's slot, or a piece (its
@@ -528,6 +532,7 @@ cudaError_t launch_rows_join(const AttnStepArgs &a, const float *part, int sms,
                              cudaStream_t stream) {
     const int64_t rows = (int64_t)a.N * a.HQ;
     const int32_t parts = join_parts(rows, sms), abreast = kJoinWarps / parts;
+    const int32_t workers = sms * Core::kCtas * (Core::kAhead ? kWarps : 1);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr = follows_on();
     cfg.stream = stream;
@@ -536,7 +541,7 @@ cudaError_t launch_rows_join(const AttnStepArgs &a, const float *part, int sms,
     cfg.gridDim = dim3((unsigned)((rows + abreast - 1) / abreast));
     cfg.blockDim = dim3(kJoinThreads);
     return cudaLaunchKernelEx(&cfg, attn_rows_join_kernel<Core::kD, Core::kRows, SHARED>, a, part,
-                              parts);
+                              workers, parts);
 }
 
 // A cache [heads of pages, page, D] as a 4-D map {panel, page, panels, heads} whose
