@@ -577,7 +577,7 @@ __device__ __forceinline__ void split_weights(float w0, float w1, uint32_t &hi, 
 //   * f16 for the values, too, with at most 4 query heads, where the weights' low
 //     parts have columns of their own and go there times 2^11.  The weights are
 //     lifted by 2^7 and the scales divided by vref, a power of two that none has
-//     passed so far, so that the product lies below 2^15: weights down to 2^-28 of
+//     reached so far, so that the product lies below 2^15: weights down to 2^-28 of
 //     a row's largest keep 2^-15, smaller ones 2^-43 of the largest, times vref;
 //   * bf16 for the values else (whose range needs no reference): 0x4300 | u is
 //     v = 128 + u below u = 128 and 2 u from there on, so that with w = v - 256
@@ -864,7 +864,7 @@ struct MmaCore {
         float top[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) top[e] = fmaxf(s[0][e], s[0][e + 2]) * c2;
-        const float v_top = fmaxf(vf[0], vf[1]);
+        const float v_top = fmaxf(fabsf(vf[0]), fabsf(vf[1]));
         // (NaN compares false: a NaN score moves nothing and shows in the sums, a
         // NaN scale in the weights)
         const bool move = top[0] > ref[0][0] + (kMoveBy + kLift) ||

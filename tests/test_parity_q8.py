@@ -337,7 +337,6 @@ def test_step_small_weights_beside_a_large_one(d, HQ, below):
     Scores of tens: the roundings of their exponentials are check()'s."""
     n, page, HKV = 300, 16, 1
     g = torch.Generator().manual_seed(d)
-    ks, vs, (kc, vc, kf, vf), table = paged_q8(6, [n], HKV, d, page)
     q = torch.ones(1, HQ, d, dtype=torch.bfloat16)
     # scores: token 0 has below more than the others'
     k = torch.randint(-3, 4, (n, HKV, d), generator=g, dtype=torch.int8)
@@ -381,6 +380,76 @@ def test_step_rows_that_no_code_stands_for(dtype, d):
         out, _ = kda.kda_attn_step_q8(q, kc, vc, kf, vf, table_, i32(lens), 0.1)
         assert out[0].isnan().all()
         check_rows(q[1:], ks[1:], vs[1:], 0.1, out[1:], None, _weights(dtype, d))
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f32", 64)])
+@pytest.mark.parametrize("HQ", [2, 8])
+@pytest.mark.parametrize("wide", [False, True])
+def test_step_scales_below_zero(dtype, d, HQ, wide):
+    """A scale may have either sign."""
+    lens = [333, 40]
+    ks, vs, (kc, vc, kf, vf), table = paged_q8(15, lens, 1, d, 32)
+    kf.neg_()
+    vf[1:].neg_()
+    for s, n in enumerate(lens):
+        ks[s].neg_()
+        for j in range((n + 31) // 32):
+            if int(table[s, j]) > 0:
+                vs[s][j * 32:(j + 1) * 32].neg_()
+    q = randn(1, 2, HQ, d, dtype=dtype).cuda()
+    out, _ = kda.kda_attn_step_q8(q, kc, vc, kf, vf, widen(table) if wide else table, i32(lens), 0.1)
+    check_rows(q, ks, vs, 0.1, out, None, _weights(dtype, d))
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("bf16", 32), ("f32", 64)])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("wide", [False, True])
+def test_step_queries_that_are_no_numbers(dtype, d, value, wide):
+    """An infinity or a NaN in a head's query is that head's alone: no code stands
+    for an infinity, so that scores of +inf among others leave NaN."""
+    lens = [200, 50]
+    ks, vs, cache, table = paged_q8(16, lens, 1, d, 16)
+    q = randn(1, 2, 3, d, dtype=dtype)
+    q[0, 1, d // 2] = value
+    out, _ = kda.kda_attn_step_q8(q.cuda(), *cache, widen(table) if wide else table, i32(lens), 0.1)
+    assert out[0, 1].isnan().all()
+    for s, h in ((0, 0), (0, 2), (1, 0), (1, 1), (1, 2)):
+        one = (slice(s, s + 1), slice(h, h + 1))
+        check_rows(q[one], ks[s:s + 1], vs[s:s + 1], 0.1, out[one], None, _weights(dtype, d))
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f32", 16)])
+@pytest.mark.parametrize("left", [65, 63, 32])
+def test_step_lengths_up_to_2_31(dtype, d, left):
+    """A table of 2^31 - 32 tokens whose entries name one page of 32 over and
+    over, beside a sequence of 70 tokens.
+
+    Bound: at most four additions to an accumulator per tile of 64 tokens, with a
+    whole step of fp32 (2^-23) each; a CTA, or a warp, has its share of the tiles
+    (plus the joins', far fewer than a tenth).  The output's own rounding is 2^-8."""
+    page, top = 32, 1 << 31
+    width, lens = top // page - 1, [top - left, 70]
+    g = torch.Generator().manual_seed(d)
+    codes = torch.randint(-127, 128, (2, 1, 1, page, d), generator=g, dtype=torch.int8)
+    codes[1] = codes[1] // 4 + 90    # (means that are not near zero)
+    scales = (0.5 + torch.rand(2, 1, 1, page, generator=g)) / 127
+    k, v = (codes[i, 0, 0].double() * scales[i, 0, 0].double()[:, None] for i in (0, 1))
+    q = randn(3, 2, 1, d, dtype=dtype)
+    table = torch.zeros(2, width, dtype=torch.int32, device="cuda")
+    lse = torch.full((2, 1), float("nan"), device="cuda")
+    scale = d ** -0.5
+    out, _ = kda.kda_attn_step_q8(q.cuda(), *codes.cuda(), *scales.cuda(), table, i32(lens), scale,
+                                  None, lse)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for s, n in enumerate(lens):
+        count = n // page + (torch.arange(page) < n % page)
+        z = scale * (k @ q[s, 0].double())
+        w = count * torch.exp(z - z.max())
+        want, size = (w @ v) / w.sum(), (w @ v.abs()) / w.sum()
+        rel = 4.4 * (n / 64 / sms + 1) * 2.0 ** -23 + 1e-4
+        assert abs(lse[s, 0].item() - (z.max() + w.sum().log()).item()) <= rel + 1e-5
+        assert ((out[s, 0].cpu().double() - want).abs() <= (2 * rel + 2.0 ** -8) * size).all()
+    assert kda.kda_device_status() == kda.KDA_SUCCESS
 
 
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
