@@ -21,8 +21,14 @@
 namespace kda {
 namespace {
 
+// Pieces to an item: more leave the step behind fewer SMs and the join more to read
+// (65536 shared tokens, 64 sequences, 8/1 heads, d = 128: 64 pieces 32.1 us, one to an
+// SM 37.2; 32768, 64 sequences, 8/2 heads, d = 64: 26.8, 29.5).
 constexpr int kMaxSplits = 64;
-constexpr int kFewRows = 16;  // rows to a key-value head that the step's cores take
+// Rows to a key-value head that the step's cores take (65536 shared tokens, 32/8 heads,
+// d = 128: 4 rows 55.6 us, the tensor core's tiles 62.0; 8 rows 57.7, 62.4; 16 rows
+// 61.6, 62.2, but 33.7, 28.0 with 16/2 heads and 32.5, 23.9 with 8/1).
+constexpr int kFewRows = 8;
 
 // Blocks of kRows rows over the shared tokens, on the step's cores: fp32, narrow
 // heads, and so few rows that the tensor core's tiles would be all but empty.
