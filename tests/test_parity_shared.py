@@ -196,6 +196,98 @@ def test_shared_offsets_past_32_bits(dtype):
     check_rows(q, ks, vs, 0.1, out, None, _weights(dtype, d))
 
 
+@pytest.mark.parametrize("HQ,HKV,d,dtype", [(8, 2, 128, "bf16"), (8, 2, 64, "bf16"), (1, 1, 128, "bf16"),
+                                            (40, 1, 64, "bf16"), (6, 2, 64, "f32")])
+@pytest.mark.parametrize("where", ["shared", "own"])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+def test_shared_infinite_values(HQ, HKV, d, dtype, where, value):
+    """A non-finite value shows in its channel, however small its weight, and in no
+    other channel; in one sequence's own tokens, in that sequence's rows alone."""
+    lens = [700, 600, 520, 530, 515]
+    _, _, kc, vc, table = paged_shared(8, 8, lens, HKV, d, 64, dtype, 0.0)
+    page, row = (int(table[0, 4]), 13) if where == "shared" else (int(table[0, 9]), 21)
+    q = torch.zeros(len(lens), HQ, d, dtype=DT[dtype], device="cuda")
+    q[..., 0] = 1
+    kc[..., 0] = 0
+    vc[page, :, row, 5] = value
+    for gap in (0.0, 1.0, 30.0, 100.0, 124.0):
+        kc[page, :, row, 0] = -gap
+        out, _ = kda.kda_attn_step_shared(q, kc, vc, widen(table), i32(lens), i32([8]),
+                                          0.6931471805599453)
+        seen = out[..., 5].float()
+        has = torch.isnan(seen) if value != value else seen == value
+        hit = slice(0, None) if where == "shared" else slice(0, 1)
+        assert has[hit].all()
+        if where == "own":
+            assert torch.isfinite(seen[1:]).all()
+        rest = torch.cat((out[..., :5], out[..., 6:]), dim=-1)
+        assert torch.isfinite(rest).all()
+
+
+MANY = [
+    # shared pages, sequences, own tokens up to, HQ, HKV, d, page
+    (32, 96, 900, 32, 8, 128, 64),       # much of both kinds: the SMs divided
+    (64, 40, 40, 32, 8, 128, 64),        # nearly all of it shared
+    (2, 200, 700, 16, 4, 128, 64),       # nearly none of it
+    (16, 300, 300, 12, 2, 64, 128),
+    (24, 150, 500, 40, 4, 64, 32),       # 10 query heads to a key-value head
+    (40, 64, 300, 32, 2, 128, 32),       # 16
+]
+
+
+@pytest.mark.parametrize("common,n,most,HQ,HKV,d,page", MANY)
+def test_shared_many_sequences(common, n, most, HQ, HKV, d, page):
+    """Sequences of every length behind the shared tokens, some of none and some that
+    hold fewer than those."""
+    lens = _lens(20 + n, n, common * page, 0, most)
+    lens[3:n:17] = [common * page] * len(lens[3:n:17])
+    lens[5:n:29] = _lens(n, len(lens[5:n:29]), 0, 0, common * page - 1)
+    ks, vs, kc, vc, table = paged_shared(n, common, lens, HKV, d, page, "bf16")
+    q = randn(1, n, HQ, d, dtype="bf16").cuda()
+    lse = torch.full((n, HQ), float("nan"), device="cuda")
+    args = (q, kc, vc, widen(table), i32(lens), i32([common]), d ** -0.5)
+    out, _ = kda.kda_attn_step_shared(*args, None, lse)
+    check_rows(q, ks, vs, d ** -0.5, out, lse, ONE_PART)
+    assert kda.kda_device_status() == kda.KDA_SUCCESS
+    assert torch.equal(kda.kda_attn_step_shared(*args)[0], out)
+
+
+@pytest.mark.parametrize("dtype,d,HQ", [("bf16", 64, 1), ("bf16", 64, 16), ("f32", 16, 1)])
+@pytest.mark.parametrize("left,own", [(65, 1), (32, 1 << 30)])
+def test_shared_lengths_up_to_2_31(dtype, d, HQ, left, own):
+    """A table of 2^31 - 32 tokens whose entries name one page of 32 over and
+    over: nearly all of them shared, or half of them, by two sequences, and a third
+    of 70 tokens.
+
+    Bound: as for kda_attn_step's, with at most sixteen additions to an accumulator
+    (two to a sum) per 128 tokens and pieces for a quarter of the SMs at least; one bf16 rounding of
+    a weight (2^-8) and the output's."""
+    page, top = 32, 1 << 31
+    width = top // page - 1
+    k, v = (randn(i, 1, 1, page, d, dtype=dtype) for i in (1, 2))
+    v += 1   # (means that are not near zero)
+    q = randn(3, 3, HQ, d, dtype=dtype)
+    table = torch.zeros(3, width, dtype=torch.int32, device="cuda")
+    lens = [top - left, top - left - 5, 70]
+    shared = (top - left - 5 - (own if own > 1 else 0)) // page
+    lse = torch.full((3, HQ), float("nan"), device="cuda")
+    scale = d ** -0.5
+    out, _ = kda.kda_attn_step_shared(q.cuda(), k.cuda(), v.cuda(), table, i32(lens), i32([shared]),
+                                      scale, None, lse)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for s, n in enumerate(lens):
+        count = n // page + (torch.arange(page) < n % page)
+        z = scale * (q[s].double() @ k[0, 0].double().T)
+        w = count * torch.exp(z - z.amax(-1, keepdim=True))
+        l = w.sum(-1, keepdim=True)
+        want, size = (w @ v[0, 0].double()) / l, (w @ v[0, 0].double().abs()) / l
+        rel = 16 * (n / 128 / (sms / 4) + 1) * 2.0 ** -23 + 1e-4
+        lz = z.amax(-1) + l[:, 0].log()
+        assert ((lse[s].cpu().double() - lz).abs() <= rel / 8 + 1e-4).all()
+        assert ((out[s].cpu().double() - want).abs() <= (2 * rel + 2.0 ** -7) * size).all()
+    assert kda.kda_device_status() == kda.KDA_SUCCESS
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
 @pytest.mark.parametrize("wide", [False, True])
 def test_shared_streams_graphs_and_workspace(dtype, d, wide):
