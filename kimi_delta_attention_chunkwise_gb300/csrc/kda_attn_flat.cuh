@@ -22,6 +22,7 @@
 namespace kda {
 namespace {
 
+constexpr int kJoinGroups = kJoinThreads / 8;
 constexpr long long kFlatWait = 2000000000LL;  // SM clocks, about a second
 
 // Tiled tensor load, 4-D coordinates {x innermost, y, z, w}
@@ -384,135 +385,156 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
     if (SHARED) tc::pdl_wait_primaries();
 }
 
-// N neighbouring floats, N = 1, 2 or 4
+// N neighbouring floats, N = 2 or 4
 template <int N>
-__device__ __forceinline__ void load_run(const float *from, float (&x)[N]) {
+__device__ __forceinline__ void load_run(const float *from, float *x) {
     if constexpr (N == 4) {
         const float4 y = *reinterpret_cast<const float4 *>(from);
         x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
-    } else if constexpr (N == 2) {
+    } else {
         const float2 y = *reinterpret_cast<const float2 *>(from);
         x[0] = y.x; x[1] = y.y;
-    } else {
-        x[0] = *from;
     }
 }
 
 // Joins what workers have left of every row: parts of its item, or its item's
 // state (kda_attn_step_q8's are results already), and its states over the shared
-// tokens.  `parts` warps to a row, so many rows to a CTA as its 8 warps have;
-// a row's maxima and sums one to a lane, its weighted sums eight loads abreast.
+// tokens.  `parts` groups of 8 lanes to a row, each with every parts-th state, four
+// at a time: what bounds the kernel is the wait for its loads, the owners, then all
+// of a state together (kda_attn_step_q8, 131072 and 40007 tokens, 32/8 heads, d = 128:
+// the call 70 us, with one state at a time 75, as with a warp to a row and a state's
+// sums behind its maximum; kda_attn_step_shared, 24 rows behind 65536 shared tokens:
+// 63.4, 65.9, 65.2).
 template <int D, int R, bool SHARED>
 __global__ void __launch_bounds__(kJoinThreads) attn_rows_join_kernel(const AttnStepArgs a,
                                                                       const float *part,
                                                                       int32_t workers,
                                                                       int32_t parts) {
-    constexpr int N = (D + 31) / 32;  // columns per lane
-    __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, col = lane * N;
+    constexpr int N = D == 16 ? 2 : 4;      // neighbouring channels
+    constexpr int RUNS = D / (8 * N);       // and how many such runs a lane has
+    constexpr int B = 4;                    // states in flight
+    __shared__ __align__(16) float s_o[kJoinGroups][D];
+    __shared__ float s_m[kJoinGroups], s_l[kJoinGroups];
+    const int tid = threadIdx.x, group = tid >> 3, lane = tid & 7, mine = group % parts;
     const int32_t blocks = (a.G + R - 1) / R;
-    const int32_t abreast = kJoinWarps / parts;  // rows of the CTA
-    const int64_t row = (int64_t)blockIdx.x * abreast + warp / parts, rows = (int64_t)a.N * a.HQ;
-    const int32_t s = row < rows ? (int32_t)(row / a.HQ) : 0;
-    const int32_t hq = row < rows ? (int32_t)(row - (int64_t)s * a.HQ) : 0;
+    const int64_t rows = (int64_t)a.N * a.HQ;
+    const int64_t row = (int64_t)blockIdx.x * (kJoinGroups / parts) + group / parts;
+    const bool there = row < rows;
+    const int32_t s = there ? (int32_t)(row / a.HQ) : 0;
+    const int32_t hq = there ? (int32_t)(row - (int64_t)s * a.HQ) : 0;
     const int32_t kvh = hq / a.G, block = (hq - kvh * a.G) / R, r = hq - kvh * a.G - block * R;
     const Span span = span_of<SHARED>(a, s);
     const PrefixState states = prefix_state(a, D, 0);
     // the kernels before this one have ended
     tc::pdl_wait_primaries();
     const int2 who = a.owners[((int64_t)s * a.HKV + kvh) * blocks + block];
+    int32_t pieces = SHARED && span.first > 0 ? states.pieces[there ? row : 0] : 0;
     // (a kernel whose wait gave up has said so and left these as they were: anything)
     int32_t own = span.len() > 0 ? who.y >> 1 : 0;
     if (own < 0 || who.x < 0 || own > workers - who.x) own = 0;
-    int32_t pieces = SHARED && span.first > 0 ? states.pieces[row < rows ? row : 0] : 0;
     if (SHARED) pieces = min(max(pieces, 0), a.splits - 1);
-    const bool done = !SHARED && own == 1;  // written by the worker
-    const int32_t all = row >= rows || done ? 0 : own + pieces;
-    // state i's weighted sums, maximum and sum: a worker's slot, or a piece (its
-    // item's state: the last one) of arrays over the rows
+    const bool done = !there || (!SHARED && own == 1);  // written by the worker
+    const int32_t all = done ? 0 : own + pieces;
     const float *slots = part + (int64_t)who.x * 2 * (R * (D + 2));
-    const bool apart = own > 1;
-    auto slot_of = [&](int32_t i) -> const float * {
-        return slots + (i * 2 + (i == 0 ? who.y & 1 : 0)) * (int64_t)(R * (D + 2));
-    };
-    auto piece_of = [&](int32_t i) -> int64_t {
-        return (int64_t)(i < own ? a.splits - 1 : i - own) * rows + row;
-    };
-    auto sums_of = [&](int32_t i) -> const float * {
-        return i < own && apart ? slot_of(i) + r * D : states.o + piece_of(i) * D;
-    };
-    float mx = -INFINITY, l = 0.f, o[N];
+    float mx = -INFINITY, l = 0.f, o[RUNS][N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) o[j] = 0.f;
-    for (int32_t i0 = warp % parts; i0 < all; i0 += 32 * parts) {
-        const int32_t i = i0 + lane * parts;
-        float m = -INFINITY, sum = 0.f;
-        if (i < all) {
-            const bool slot = i < own && apart;
-            const float *sm = slot ? slot_of(i) + R * D + r : states.m + piece_of(i);
-            const float *sl = slot ? sm + R : states.l + piece_of(i);
-            m = *sm;
-            sum = *sl;
-        }
-        float top = fmaxf(mx, m);
+    for (int c = 0; c < RUNS; ++c)
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        const float ref = top == -INFINITY ? 0.f : top;
-        const float f = exp2f(mx - ref), w = exp2f(m - ref);
-        sum *= w;
+        for (int j = 0; j < N; ++j) o[c][j] = 0.f;
+    for (int32_t i0 = mine; i0 < all; i0 += B * parts) {
+        float m[B], sum[B], x[B][RUNS][N];
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        mx = top;
-        l = l * f + sum;
+        for (int b = 0; b < B; ++b) {
+            const int32_t i = i0 + b * parts;
+            m[b] = -INFINITY;
+            sum[b] = 0.f;
 #pragma unroll
-        for (int j = 0; j < N; ++j) o[j] *= f;
-        const int32_t n = min(32, (all - i0 + parts - 1) / parts);
-#pragma unroll 8
-        for (int32_t k = 0; k < n; ++k) {
-            const float wk = __shfl_sync(0xffffffffu, w, k);
-            float x[N];
-            if (col < D) {
-                load_run(sums_of(i0 + k * parts) + col, x);
+            for (int c = 0; c < RUNS; ++c)
 #pragma unroll
-                for (int j = 0; j < N; ++j) o[j] += x[j] * wk;
+                for (int j = 0; j < N; ++j) x[b][c][j] = 0.f;
+            if (i >= all) continue;
+            // a worker's slot, or a piece (the item's state: the last one) of arrays
+            // over the rows
+            const float *from, *from_m, *from_l;
+            if (i < own && own > 1) {
+                const float *slot =
+                    slots + (i * 2 + (i == 0 ? who.y & 1 : 0)) * (int64_t)(R * (D + 2));
+                from = slot + r * D;
+                from_m = slot + R * D + r;
+                from_l = from_m + R;
+            } else {
+                const int64_t at = (int64_t)(i < own ? a.splits - 1 : i - own) * rows + row;
+                from = states.o + at * D;
+                from_m = states.m + at;
+                from_l = states.l + at;
             }
-        }
-    }
-    if (parts > 1) {
-        if (col < D) {
+            m[b] = *from_m;
+            sum[b] = *from_l;
 #pragma unroll
-            for (int j = 0; j < N; ++j) s_o[warp][col + j] = o[j];
+            for (int c = 0; c < RUNS; ++c) load_run<N>(from + (c * 8 + lane) * N, x[b][c]);
         }
-        if (lane == 0) {
-            s_m[warp] = mx;
-            s_l[warp] = l;
-        }
-        __syncthreads();
-        if (warp % parts) return;
         float top = mx;
-        for (int w = 1; w < parts; ++w) top = fmaxf(top, s_m[warp + w]);
-        const float ref = top == -INFINITY ? 0.f : top;
-        const float f = exp2f(mx - ref);
+#pragma unroll
+        for (int b = 0; b < B; ++b) top = fmaxf(top, m[b]);
+        const float ref = top == -INFINITY ? 0.f : top, f = exp2f(mx - ref);
+        mx = top;
         l *= f;
 #pragma unroll
-        for (int j = 0; j < N; ++j) o[j] *= f;
-        for (int w = 1; w < parts; ++w) {
-            const float fw = exp2f(s_m[warp + w] - ref);
-            l += s_l[warp + w] * fw;
+        for (int c = 0; c < RUNS; ++c)
 #pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (col < D) o[j] += s_o[warp + w][col + j] * fw;
+            for (int j = 0; j < N; ++j) o[c][j] *= f;
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const float w = exp2f(m[b] - ref);
+            l += sum[b] * w;
+#pragma unroll
+            for (int c = 0; c < RUNS; ++c)
+#pragma unroll
+                for (int j = 0; j < N; ++j) o[c][j] += x[b][c][j] * w;
         }
-        mx = top;
     }
-    if (row >= rows || done || col >= D) return;
-    store_run(a, row, D, col, o, mx, l);
+    if (parts == 1) {
+        if (done) return;
+#pragma unroll
+        for (int c = 0; c < RUNS; ++c) store_run(a, row, D, (c * 8 + lane) * N, o[c], mx, l);
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < RUNS; ++c)
+#pragma unroll
+        for (int j = 0; j < N; ++j) s_o[group][(c * 8 + lane) * N + j] = o[c][j];
+    if (lane == 0) {
+        s_m[group] = mx;
+        s_l[group] = l;
+    }
+    __syncthreads();
+    if (done) return;
+    // the row's groups' states, by all of its lanes
+    const int first = group - mine;
+    float top = -INFINITY;
+    for (int p = 0; p < parts; ++p) top = fmaxf(top, s_m[first + p]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    for (int at = mine * 8 + lane; at < D / N; at += parts * 8) {
+        float y[N], sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < N; ++j) y[j] = 0.f;
+        for (int p = 0; p < parts; ++p) {
+            const float w = exp2f(s_m[first + p] - ref);
+            float x[N];
+            load_run<N>(&s_o[first + p][at * N], x);
+            sum += s_l[first + p] * w;
+#pragma unroll
+            for (int j = 0; j < N; ++j) y[j] += x[j] * w;
+        }
+        store_run(a, row, D, at * N, y, top, sum);
+    }
 }
 
-// Warps to a row of the join: as many as keep the GPU's warps busy.
+// Groups to a row of the join: as many as make two CTAs to an SM at most (64 rows
+// behind 4096 shared tokens, 32/8 heads: 64 groups to an SM 56.4 us, 16 58.3, 256 59.3).
 inline int32_t join_parts(int64_t rows, int sms) {
     int32_t parts = 1;
-    while (parts < kJoinWarps && rows * parts * 2 <= (int64_t)sms * 32) parts *= 2;
+    while (parts < kJoinGroups && rows * parts * 2 <= (int64_t)sms * 2 * kJoinGroups) parts *= 2;
     return parts;
 }
 
@@ -531,7 +553,7 @@ template <class Core, bool SHARED>
 cudaError_t launch_rows_join(const AttnStepArgs &a, const float *part, int sms,
                              cudaStream_t stream) {
     const int64_t rows = (int64_t)a.N * a.HQ;
-    const int32_t parts = join_parts(rows, sms), abreast = kJoinWarps / parts;
+    const int32_t parts = join_parts(rows, sms), abreast = kJoinGroups / parts;
     const int32_t workers = sms * Core::kCtas * (Core::kAhead ? kWarps : 1);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr = follows_on();
