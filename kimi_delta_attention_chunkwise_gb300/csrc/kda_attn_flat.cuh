@@ -351,7 +351,7 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
                         to_m = p.m + row;
                         to_l = p.l + row;
                     } else {
-                        to = part + ((int64_t)c * 2 + (first_item ? 0 : 1)) * (R * (D + 2));
+                        to = part + ((int64_t)c * 2 + (first_item ? 0 : 1)) * slot_floats(R, D);
                         to_m = to + R * D;
                         to_l = to_m + R;
                     }
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_rows_join_kernel(const Attn
     if (SHARED) pieces = min(max(pieces, 0), a.splits - 1);
     const bool done = !there || (!SHARED && own == 1);  // written by the worker
     const int32_t all = done ? 0 : own + pieces;
-    const float *slots = part + (int64_t)who.x * 2 * (R * (D + 2));
+    const float *slots = part + (int64_t)who.x * 2 * slot_floats(R, D);
     float mx = -INFINITY, l = 0.f, o[RUNS][N];
 #pragma unroll
     for (int c = 0; c < RUNS; ++c)
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_rows_join_kernel(const Attn
             const float *from, *from_m, *from_l;
             if (i < own && own > 1) {
                 const float *slot =
-                    slots + (i * 2 + (i == 0 ? who.y & 1 : 0)) * (int64_t)(R * (D + 2));
+                    slots + (i * 2 + (i == 0 ? who.y & 1 : 0)) * (int64_t)slot_floats(R, D);
                 from = slot + r * D;
                 from_m = slot + R * D + r;
                 from_l = from_m + R;
@@ -541,7 +541,8 @@ inline int32_t join_parts(int64_t rows, int sms) {
 // Bytes of workers' parts, and of owners.
 template <class Core>
 size_t flat_part_bytes(int sms) {
-    return (size_t)sms * Core::kCtas * kWarps * 2 * Core::kRows * (Core::kD + 2) * sizeof(float);
+    return (size_t)sms * Core::kCtas * kWarps * 2 * slot_floats(Core::kRows, Core::kD) *
+           sizeof(float);
 }
 template <class Core>
 size_t owners_bytes(const AttnStepArgs &a) {

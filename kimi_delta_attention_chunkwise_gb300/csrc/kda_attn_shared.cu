@@ -99,12 +99,13 @@ auto with_rest_core(int32_t D, int32_t G, int32_t dtype, F f) {
         return f(MmaCore<128, 2, false, __nv_bfloat16, true>{});
     }
     if (dtype == KDA_DTYPE_BF16)
-        return D == 16 ? f(SimtCore<__nv_bfloat16, 16>{}) : f(SimtCore<__nv_bfloat16, 32>{});
+        return D == 16 ? with_rows<__nv_bfloat16, 16, __nv_bfloat16>(G, f)
+                       : with_rows<__nv_bfloat16, 32, __nv_bfloat16>(G, f);
     switch (D) {
-        case 16: return f(SimtCore<float, 16>{});
-        case 32: return f(SimtCore<float, 32>{});
-        case 64: return f(SimtCore<float, 64>{});
-        default: return f(SimtCore<float, 128>{});
+        case 16: return with_rows<float, 16, float>(G, f);
+        case 32: return with_rows<float, 32, float>(G, f);
+        case 64: return with_rows<float, 64, float>(G, f);
+        default: return with_rows<float, 128, float>(G, f);
     }
 }
 

@@ -297,6 +297,10 @@ struct Line {
     }
 };
 
+// Floats of a worker's partial result for the joins: weighted sums [R, D], maxima [R]
+// and sums [R]; whole 16-byte vectors.
+__host__ __device__ constexpr int slot_floats(int R, int D) { return (R * (D + 2) + 3) / 4 * 4; }
+
 // A state's maximum as the joins take it.  -inf says that no key was seen; a
 // state that saw keys whose scores are all -inf keeps its sum of 0 with the
 // lowest finite number, so that the row comes out as the definition's 0 / 0 if
@@ -359,16 +363,19 @@ struct Eight<int8_t> {
 // Every group of D / 8 lanes keeps its own running state over its tokens.
 // T: the queries' type; C: the cache's (int8: with a scale per row, which the
 // score and the weight are multiplied by).
-template <typename T, int D, typename C = T>
+template <typename T, int D, typename C = T, int ROWS = 4>
 struct SimtCore {
     using Type = T;
     using Cell = C;
-    static constexpr int kD = D, kRows = 4, kCtas = 3;
+    static constexpr int kD = D, kRows = ROWS;
+    // (as many as the registers of so many rows let be)
+    static constexpr int kCtas = ROWS == 4 ? 3 : ROWS == 2 || D * sizeof(C) == 512 ? 4 : 5;
     static constexpr bool kAhead = false, kScaled = sizeof(C) == 1;
     static constexpr int LPT = D / 8, TPW = 32 / LPT;
     // tokens whose keys and values are in flight together: 16, or 8 where 16
-    // would take 128 registers
-    static constexpr int NB = (sizeof(C) == 4 && D == 128) ? 4 : kWarpTokens / TPW;
+    // would take 128 registers, or too many for the CTAs (8-bit codes, d = 128, G = 1:
+    // 12.4 us, with 16 and 3 CTAs 18.3)
+    static constexpr int NB = (sizeof(C) != 2 && D == 128) ? 4 : kWarpTokens / TPW;
 
     float q[kRows][8], acc[kRows][8], m[kRows], l[kRows];
     float c2;
@@ -1250,7 +1257,7 @@ attn_step_kernel(const AttnStepArgs a, float *part) {
         core.finish(state.acc[warp], state.m[warp], state.l[warp], seen);
         __syncthreads();
         const bool whole = tile0 == 0 && tile1 == tiles;
-        float *slot = part + ((int64_t)c * 2 + (u == u0 ? 0 : 1)) * (R * (D + 2));
+        float *slot = part + ((int64_t)c * 2 + (u == u0 ? 0 : 1)) * slot_floats(R, D);
         for (int i = tid; i < rows * D; i += kThreads) {
             const int r = i / D, col = i % D;
             float o, mx, sum;
@@ -1408,7 +1415,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnStepA
                 const int64_t b = share_start(units, i, grid);
                 if (b >= last) break;
                 const float *slot = part + ((int64_t)i * 2 + ((i == c0 && b != first) ? 1 : 0)) *
-                                               (R * (D + 2));
+                                               slot_floats(R, D);
                 const float sm = slot[R * D + r0 + r], sl = slot[R * D + R + r0 + r];
                 float x[N];
 #pragma unroll
@@ -1526,7 +1533,19 @@ cudaError_t launch_line(const AttnStepArgs &a, int sms, cudaStream_t stream) {
 // Scratch of the line of tiles.
 template <class Core>
 size_t line_bytes(int sms) {
-    return (size_t)sms * Core::kCtas * 2 * Core::kRows * (Core::kD + 2) * sizeof(float);
+    return (size_t)sms * Core::kCtas * 2 * slot_floats(Core::kRows, Core::kD) * sizeof(float);
+}
+// The CUDA-core core with so many rows as there are query heads to a key-value head,
+// up to 4, as a call of f(Core{}): what it takes is its arithmetic's time, and fewer
+// rows leave registers for more CTAs (8-bit cache, fp32 queries, 16 sequences of
+// 200-2000 tokens, G = 2, d = 64: 8.4 us, with 4 rows 13.3; 64 of 200-4000, d = 128:
+// 62, 97; kda_attn_step_shared, fp32, 64 of 200-4000 tokens behind 2048, d = 128, G = 1:
+// 115, 123).
+template <typename T, int D, typename C, class F>
+auto with_rows(int32_t G, F f) {
+    if (G == 1) return f(SimtCore<T, D, C, 1>{});
+    if (G == 2) return f(SimtCore<T, D, C, 2>{});
+    return f(SimtCore<T, D, C>{});
 }
 // The core of a problem whose cache has the queries' type, as a call of f(Core{}).
 template <class F>

@@ -18,8 +18,8 @@ template <class F>
 auto with_core_q8(int32_t D, int32_t G, int32_t dtype, F f) {
     if (dtype == KDA_DTYPE_BF16) {
         switch (D) {
-            case 16: return f(SimtCore<Bf16, 16, int8_t>{});
-            case 32: return f(SimtCore<Bf16, 32, int8_t>{});
+            case 16: return with_rows<Bf16, 16, int8_t>(G, f);
+            case 32: return with_rows<Bf16, 32, int8_t>(G, f);
             case 64:
                 if (G <= 4) return f(MmaCore<64, 1, true, int8_t>{});
                 if (G <= 8) return f(MmaCore<64, 1, false, int8_t>{});
@@ -31,10 +31,10 @@ auto with_core_q8(int32_t D, int32_t G, int32_t dtype, F f) {
         }
     }
     switch (D) {
-        case 16: return f(SimtCore<float, 16, int8_t>{});
-        case 32: return f(SimtCore<float, 32, int8_t>{});
-        case 64: return f(SimtCore<float, 64, int8_t>{});
-        default: return f(SimtCore<float, 128, int8_t>{});
+        case 16: return with_rows<float, 16, int8_t>(G, f);
+        case 32: return with_rows<float, 32, int8_t>(G, f);
+        case 64: return with_rows<float, 64, int8_t>(G, f);
+        default: return with_rows<float, 128, int8_t>(G, f);
     }
 }
 

@@ -382,6 +382,21 @@ def test_step_rows_that_no_code_stands_for(dtype, d):
         check_rows(q[1:], ks[1:], vs[1:], 0.1, out[1:], None, _weights(dtype, d))
 
 
+@pytest.mark.parametrize("HQ,HKV", [(2, 2), (4, 2), (3, 1), (9, 1)])
+@pytest.mark.parametrize("dtype,d", [("f32", 16), ("f32", 32), ("f32", 64), ("f32", 128), ("bf16", 16),
+                                     ("bf16", 32)])
+@pytest.mark.parametrize("lens", [[3000, 0, 17], [700, 1200, 64, 1, 0, 90]])
+@pytest.mark.parametrize("wide", [False, True])
+def test_step_every_number_of_rows(HQ, HKV, dtype, d, lens, wide):
+    """Long sequences, shared by CTAs, with every number of rows to a CTA."""
+    ks, vs, cache, table = paged_q8(d + HQ, lens, HKV, d, 64)
+    q = randn(2, len(lens), HQ, d, dtype=dtype).cuda()
+    lse = torch.full((len(lens), HQ), float("nan"), device="cuda")
+    out, _ = kda.kda_attn_step_q8(q, *cache, widen(table) if wide else table, i32(lens), d ** -0.5,
+                                  None, lse)
+    check_rows(q, ks, vs, d ** -0.5, out, lse, _weights(dtype, d))
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f32", 64)])
 @pytest.mark.parametrize("HQ", [2, 8])
 @pytest.mark.parametrize("wide", [False, True])

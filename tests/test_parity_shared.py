@@ -224,6 +224,20 @@ def test_shared_infinite_values(HQ, HKV, d, dtype, where, value):
         assert torch.isfinite(rest).all()
 
 
+@pytest.mark.parametrize("HQ,HKV", [(2, 2), (4, 2), (3, 1), (9, 1)])
+@pytest.mark.parametrize("dtype,d", [("f32", 16), ("f32", 32), ("f32", 64), ("f32", 128), ("bf16", 16),
+                                     ("bf16", 32)])
+@pytest.mark.parametrize("common,lens", [(4, [2256, 300, 4100, 256, 257, 80]), (0, [3000]), (30, [9000, 1920])])
+def test_shared_long_tails_of_few_rows(HQ, HKV, dtype, d, common, lens):
+    """Own tokens that many CTAs share, with every number of rows to a CTA."""
+    ks, vs, kc, vc, table = paged_shared(d + HQ, common, lens, HKV, d, 64, dtype)
+    q = randn(2, len(lens), HQ, d, dtype=dtype).cuda()
+    lse = torch.full((len(lens), HQ), float("nan"), device="cuda")
+    out, _ = kda.kda_attn_step_shared(q, kc, vc, widen(table), i32(lens), i32([common]), d ** -0.5,
+                                      None, lse)
+    check_rows(q, ks, vs, d ** -0.5, out, lse, _weights(dtype, d))
+
+
 MANY = [
     # shared pages, sequences, own tokens up to, HQ, HKV, d, page
     (32, 96, 900, 32, 8, 128, 64),       # much of both kinds: the SMs divided
