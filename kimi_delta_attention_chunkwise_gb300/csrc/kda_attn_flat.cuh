@@ -7,11 +7,19 @@
 // ring of its own, ahead of the one it works on and across the borders of items:
 // neighbouring rows of a page, one copy of keys and one of values (and two of
 // scales).  Nothing in the loop waits for another warp, and short items cost no
-// start of their own.  At the end of an item the warp writes
-// the item's results, or its part's state for the join.  (kda_attn_step's kernel,
-// whose CTAs share a tile of 64 tokens and hold the next one's rows in registers,
-// gets 0.63 of the memory's rate out of 8-bit rows, half as many bytes to a tile,
-// and of sequences of a few hundred tokens.)
+// start of their own.  At the end of an item the warp writes the item's results, or
+// its part's state for the join.
+//
+// Rows come by 4-D tensor copies with a swizzle that leaves the core's reads free of
+// bank conflicts (8-bit, 64 sequences of 512-8192 tokens, 32/8 heads, d = 128: 114 us,
+// 5.8 TB/s of 6.8; by bulk copies of rows with conflicts 130; by kda_attn_step's
+// kernel, whose CTAs share a tile of 64 tokens and hold the next one's rows in
+// registers, 155).  What the kernel takes is the bytes at the memory's rate and about
+// 15 us: 3 for the line's sums and the first look-ups, 5 for the join, and the rest
+// for SMs that get less of the memory than others (their last warps end 96 to 108 us
+// after the start in the case above).  Shares that CTAs take from blocks that have not
+// started, or blocks of their own at the end of the line, cost more than they even
+// out (126, 117 us).
 #pragma once
 
 #include <cstring>
@@ -88,8 +96,9 @@ struct FlatCfg {
     // its tokens is a third of the instructions
     static constexpr int SUB = ROOM >= 4 ? 2 : 1, UNIT = SUB * kWarpTokens;
     static constexpr int RING = ROOM / SUB < 4 ? ROOM / SUB : 4;  // units
-    // what an item takes besides its units (queries, results), in units: 256 sequences
-    // of 1-600 tokens, whose shares hold a few items or tens, 78-99 us without
+    // what an item takes besides its units (queries, results), in units: behind 16384
+    // shared tokens, 256 sequences of 1-600 tokens, whose shares hold a few items or
+    // tens, take 109 us without it and 97 with it
     static constexpr int COST = SUB == 2 ? 1 : 2;
     static constexpr uint32_t PANEL = UNIT * Core::kPanel;        // a panel of a unit's keys
     static constexpr uint32_t HALF = Core::kPanels * PANEL;       // a unit's keys, or values

@@ -23,6 +23,14 @@
 // copies from outside of the cache leave at zero.  References move as in
 // kda_attn_tc.cu: by more than 2^8 or not at all.
 //
+// A unit, two row tiles against 128 keys, takes 1.7 us of an SM at d = 128 (a row tile
+// alone 1.2), 0.66 of the tensor cores' measured rate: the weights of a row tile wait for
+// its scores and the next scores for its products, since two score tiles and two
+// outputs are all that TMEM holds.  Few sequences are bound by the keys' and values'
+// bytes, many by the units (32/8 heads, no tokens but the shared ones, with the join:
+// 24 sequences, 65536 keys 57 us, 4.7 TB/s; 256 sequences, 16384 keys 60 us, 1140
+// TFLOP/s).
+//
 // Warps: 0-3 and 4-7 the weights and results of row tile 0 and 1, 8 issues the
 // MMAs, 9 the copies.  Waits are bounded as there.
 #include <algorithm>

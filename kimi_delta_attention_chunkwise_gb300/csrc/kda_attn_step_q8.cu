@@ -1,11 +1,13 @@
 // kda_attn_step_q8.cu -- kda_attn_step_q8: one token of every sequence over a
-// paged cache of 8-bit codes (the kernels: kda_attn_step.cuh).
+// paged cache of 8-bit codes (the cores and the kernels for short tables:
+// kda_attn_step.cuh; the kernel for others: kda_attn_flat.cuh).
 //
 //     z_j = scale ks_j <q, kcode_j>,  o = sum_j e^{z_j} vs_j vcode_j / sum_j e^{z_j}
 //
 // A token's key and value are 2 D bytes of codes and 8 of scales to a key-value
 // head, half of what a bf16 cache holds.  The scales stay outside the products,
-// which are exact products of codes in fp32 (bf16 operands hold codes exactly).
+// which are products of codes that both 16-bit types hold exactly, summed in fp32
+// (MmaCore says how).
 #include "kda_attn_flat.cuh"
 
 namespace kda {
