@@ -11,15 +11,16 @@
 // its part's state for the join.
 //
 // Rows come by 4-D tensor copies with a swizzle that leaves the core's reads free of
-// bank conflicts (8-bit, 64 sequences of 512-8192 tokens, 32/8 heads, d = 128: 114 us,
-// 5.8 TB/s of 6.8; by bulk copies of rows with conflicts 130; by kda_attn_step's
+// bank conflicts (8-bit, 64 sequences of 512-8192 tokens, 32/8 heads, d = 128: 112 us,
+// 5.9 TB/s of 6.8; by bulk copies of rows with conflicts 130; by kda_attn_step's
 // kernel, whose CTAs share a tile of 64 tokens and hold the next one's rows in
-// registers, 155).  What the kernel takes is the bytes at the memory's rate and about
-// 15 us: 3 for the line's sums and the first look-ups, 5 for the join, and the rest
-// for SMs that get less of the memory than others (their last warps end 96 to 108 us
-// after the start in the case above).  Shares that CTAs take from blocks that have not
-// started, or blocks of their own at the end of the line, cost more than they even
-// out (126, 117 us).
+// registers, 155).  Rows are read once, and say so to L2: without that the calls that
+// follow each other take 117 us, and one behind writes that fill L2 146, not 130.
+// What the kernel takes is the bytes at the memory's rate and about 15 us: 3 for the
+// line's sums and the first look-ups, 5 for the join, and the rest for SMs that get
+// less of the memory than others (their last warps end 12 us after the first SMs').
+// Shares that CTAs take from blocks that have not started, or blocks of their own at
+// the end of the line, cost more than they even out (117 us: 126, 117).
 #pragma once
 
 #include <cstring>
@@ -32,16 +33,6 @@ namespace {
 
 constexpr int kJoinGroups = kJoinThreads / 8;
 constexpr long long kFlatWait = 2000000000LL;  // SM clocks, about a second
-
-// Tiled tensor load, 4-D coordinates {x innermost, y, z, w}
-__device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int32_t x, int32_t y,
-                                            int32_t z, int32_t w, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(tc::smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(tc::smem_u32(bar))
-        : "memory");
-}
 
 // Where a warp is in the line: unit `tile` of `tiles` of sequence s under key-value
 // head kvh and block `block` of its query heads.  `at`: its place in the line, where
@@ -255,8 +246,8 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
                     uint8_t *to = ring + x * (2 * Cfg::HALF) + mine * Core::kPanel;
                     tc::mbar_arrive_expect_tx(
                         &full[x], box * (2 * Cfg::ROW + (Core::kScaled ? 8 : 0)));
-                    tma_load_4d(to, &maps.k, 0, at, 0, (int32_t)z, &full[x]);
-                    tma_load_4d(to + Cfg::HALF, &maps.v, 0, at, 0, (int32_t)z, &full[x]);
+                    tma_load_4d_once(to, &maps.k, 0, at, 0, (int32_t)z, &full[x]);
+                    tma_load_4d_once(to + Cfg::HALF, &maps.v, 0, at, 0, (int32_t)z, &full[x]);
                     if constexpr (Core::kScaled) {
                         const int64_t row = (z << a.page_shift) + at;
                         float *f = scales + x * (2 * Cfg::UNIT) + mine;

@@ -103,6 +103,30 @@ __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Tiled tensor loads of what is read once: its lines make room in L2 first, so that
+// results, tables and whatever else is read again stay.
+__device__ __forceinline__ void tma_load_3d_once(void *dst, const void *tmap, int32_t x, int32_t y,
+                                                 int32_t z, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .b64 policy;\n\t"
+        "createpolicy.fractional.L2::evict_first.b64 policy, 1.0;\n\t"
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], policy;\n\t}" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+// (coordinates x innermost, y, z, w)
+__device__ __forceinline__ void tma_load_4d_once(void *dst, const void *tmap, int32_t x, int32_t y,
+                                                 int32_t z, int32_t w, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .b64 policy;\n\t"
+        "createpolicy.fractional.L2::evict_first.b64 policy, 1.0;\n\t"
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], policy;\n\t}" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+
 // Asks for a block of the grid that has not started, to be worked on here;
 // 16 bytes of answer go to `to`.
 __device__ __forceinline__ void request_block(uint4 *to, uint64_t *bar) {

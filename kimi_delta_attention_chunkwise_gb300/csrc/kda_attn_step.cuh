@@ -109,11 +109,14 @@ struct PrefixPiece {
 };
 // How the SMs are divided between the shared tokens' kernel on the tensor cores, one
 // CTA to an SM, and the step behind it, whose CTAs find no room beside one: the
-// former is bound by what an SM computes, the latter by memory, which fewer SMs
-// than all can keep busy.  `prefix`: so many SMs for the former that it ends when
-// the latter does.  CTAs of the step that must wait for those get shares of
-// late / 16 of the others'.  Times in ns of an SM, by what was measured: 1.7 us to a
-// unit of the line with two row tiles, 1.2 with one, d = 128; 75 GB/s of cached rows.
+// former is bound by what an SM computes, the latter by what an SM takes in, until
+// memory gives no more.  `prefix`: so many SMs for the former that it ends when the
+// latter does.  CTAs of the step that must wait for those get shares of late / 16 of
+// the others'.  Times in ns of an SM, by what was measured: 1.6 us to a unit of the
+// line with two row tiles, 1.13 with one, d = 128, behind 7 us; 75 GB/s of cached rows,
+// behind 4 us.  (256 rows behind 16384 shared tokens, 1-600 of their own, 32/8 heads, d
+// = 128: 91 us; 65 or 85 GB/s 112, 92; without the 4 us 86-92, but 83 for 78 with 128
+// rows behind 32768.)
 struct SmSplit {
     int32_t prefix, late;
 };
@@ -123,23 +126,25 @@ __device__ __forceinline__ SmSplit sm_split(const AttnStepArgs &a, const PrefixL
     if (line.units == 0) return {0, 16};
     const bool two = a.prefix_rows > 128 / a.G * a.G;  // row tiles to a unit
     // (each operation rounded by itself: the same division in both kernels)
-    const float unit = (two ? 1700.f : 1200.f) * (a.D == 64 ? 0.75f : 1.f), start = 8000.f;
+    const float unit = (two ? 1600.f : 1130.f) * (a.D == 64 ? 0.75f : 1.f);
     const float work = __fmul_rn((float)line.units, unit);
     const float own = __fmul_rn(__fmul_rn((float)own_tokens, (float)a.HKV), a.D / 18.75f);
-    auto all = [&](int32_t p) {
-        return __fdiv_rn(__fadd_rn(__fadd_rn(own, work), __fmul_rn(start, (float)p)), (float)sms);
+    auto ends = [&](int32_t p) { return __fadd_rn(7000.f, __fdiv_rn(work, (float)p)); };
+    auto step_ends = [&](int32_t p) {
+        return __fadd_rn(4000.f, __fdiv_rn(own, (float)(sms - p)));
     };
-    auto ends = [&](int32_t p) { return __fadd_rn(start, __fdiv_rn(work, (float)p)); };
     // the least number of SMs that end in time
     int32_t best = sms;
     for (int32_t p = (int32_t)(threadIdx.x & 31) + 1; p < sms; p += 32)
-        if (ends(p) <= all(p)) {
+        if (ends(p) <= step_ends(p)) {
             best = p;
             break;
         }
     best = __reduce_min_sync(0xffffffffu, best);
-    const float left = __fdiv_rn(__fmul_rn(16.f, __fsub_rn(all(best), ends(best))), all(best));
-    return {best, best == sms ? 16 : min(max((int32_t)left, 0), 16)};
+    if (best == sms) return {best, 16};
+    const float last = step_ends(best);
+    const float left = __fdiv_rn(__fmul_rn(16.f, __fsub_rn(last, ends(best))), last);
+    return {best, min(max((int32_t)left, 0), 16)};
 }
 // One piece's states of every row (here a row is sequence * HQ + query head), and
 // the number of pieces that a row has.
