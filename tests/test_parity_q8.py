@@ -382,6 +382,18 @@ def test_step_rows_that_no_code_stands_for(dtype, d):
         check_rows(q[1:], ks[1:], vs[1:], 0.1, out[1:], None, _weights(dtype, d))
 
 
+@pytest.mark.parametrize("dtype,HQ", [("bf16", 2), ("bf16", 9), ("f32", 2)])
+def test_step_thousands_of_sequences(dtype, HQ):
+    """Short sequences and empty ones by the thousand, in a table of 1024 tokens."""
+    N, d = 2500, 64
+    lens = [(7 * i) % 40 if i % 5 else 0 for i in range(N)]
+    ks, vs, cache, table = paged_q8(17, lens, 1, d, 16)
+    q = randn(2, N, HQ, d, dtype=dtype).cuda()
+    lse = torch.full((N, HQ), float("nan"), device="cuda")
+    out, _ = kda.kda_attn_step_q8(q, *cache, widen(table, 64), i32(lens), d ** -0.5, None, lse)
+    check_rows(q, ks, vs, d ** -0.5, out, lse, _weights(dtype, d))
+
+
 @pytest.mark.parametrize("HQ,HKV", [(2, 2), (4, 2), (3, 1), (9, 1)])
 @pytest.mark.parametrize("dtype,d", [("f32", 16), ("f32", 32), ("f32", 64), ("f32", 128), ("bf16", 16),
                                      ("bf16", 32)])

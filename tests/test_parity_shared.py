@@ -238,6 +238,21 @@ def test_shared_long_tails_of_few_rows(HQ, HKV, dtype, d, common, lens):
     check_rows(q, ks, vs, d ** -0.5, out, lse, _weights(dtype, d))
 
 
+@pytest.mark.parametrize("dtype,HQ", [("bf16", 2), ("bf16", 9), ("f32", 2)])
+def test_shared_thousands_of_sequences(dtype, HQ):
+    """Sequences by the thousand with few tokens of their own, none, or too few to share."""
+    N, d, common = 2500, 64, 5
+    lens = [80 + (7 * i) % 30 if i % 5 else (11 * i) % 80 for i in range(N)]
+    lens[7::50] = [80] * len(lens[7::50])
+    ks, vs, kc, vc, table = paged_shared(18, common, lens, 1, d, 16, dtype)
+    q = randn(2, N, HQ, d, dtype=dtype).cuda()
+    lse = torch.full((N, HQ), float("nan"), device="cuda")
+    out, _ = kda.kda_attn_step_shared(q, kc, vc, widen(table, 64), i32(lens), i32([common]), d ** -0.5,
+                                      None, lse)
+    check_rows(q, ks, vs, d ** -0.5, out, lse, _weights(dtype, d))
+    assert kda.kda_device_status() == kda.KDA_SUCCESS
+
+
 MANY = [
     # shared pages, sequences, own tokens up to, HQ, HKV, d, page
     (32, 96, 900, 32, 8, 128, 64),       # much of both kinds: the SMs divided
