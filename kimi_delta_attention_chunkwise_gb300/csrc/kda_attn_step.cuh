@@ -113,13 +113,19 @@ struct PrefixPiece {
 // memory gives no more.  `prefix`: so many SMs for the former that it ends when the
 // latter does.  CTAs of the step that must wait for those get shares of late / 16 of
 // the others'.  Times in ns of an SM, by what was measured: 1.6 us to a unit of the
-// line with two row tiles, 1.13 with one, d = 128, behind 7 us; 75 GB/s of cached rows,
-// behind 4 us.  (256 rows behind 16384 shared tokens, 1-600 of their own, 32/8 heads, d
-// = 128: 91 us; 65 or 85 GB/s 112, 92; without the 4 us 86-92, but 83 for 78 with 128
-// rows behind 32768.)
+// line with two row tiles, 1.13 with one, d = 128, behind 7 us; 90 GB/s of cached rows,
+// behind 4 us.  (32/8 heads, d = 128, own tokens 1-600: 256 rows behind 16384 shared
+// tokens 93 us, 128 behind 32768 84; by 75 GB/s 103, 78; by 95 89, 87.)
 struct SmSplit {
     int32_t prefix, late;
 };
+// What a sequence's `len` own tokens count for in that, in tokens: an item's start and
+// end take an SM as long as 6000 / D tokens (1000 sequences of one token of their own
+// behind 512, 8/2 heads, d = 64: 317 us where tokens alone counted, since two SMs were
+// left for them).
+__device__ __forceinline__ int32_t own_work(const AttnStepArgs &a, int32_t len) {
+    return len > 0 ? 6000 / a.D : 0;
+}
 __device__ __forceinline__ SmSplit sm_split(const AttnStepArgs &a, const PrefixLine &line,
                                             int64_t own_tokens) {
     const int32_t sms = a.prefix_sms;
@@ -128,7 +134,9 @@ __device__ __forceinline__ SmSplit sm_split(const AttnStepArgs &a, const PrefixL
     // (each operation rounded by itself: the same division in both kernels)
     const float unit = (two ? 1600.f : 1130.f) * (a.D == 64 ? 0.75f : 1.f);
     const float work = __fmul_rn((float)line.units, unit);
-    const float own = __fmul_rn(__fmul_rn((float)own_tokens, (float)a.HKV), a.D / 18.75f);
+    // (rows are taken in once for every 16 query heads)
+    const float rows = (float)(a.HKV * (a.G > 16 ? (a.G + 15) / 16 : 1));
+    const float own = __fmul_rn(__fmul_rn((float)own_tokens, rows), a.D / 22.5f);
     auto ends = [&](int32_t p) { return __fadd_rn(7000.f, __fdiv_rn(work, (float)p)); };
     auto step_ends = [&](int32_t p) {
         return __fadd_rn(4000.f, __fdiv_rn(own, (float)(sms - p)));
@@ -211,7 +219,8 @@ __device__ __forceinline__ int32_t sharing_sequence(const AttnStepArgs &a, int32
     long long mine = 0;
     for (int32_t s = (int32_t)threadIdx.x; s < a.N; s += THREADS) {
         const int32_t len = clamp_len(a, s);
-        mine += len >= shared ? len - shared : len;
+        const int32_t own_len = len >= shared ? len - shared : len;
+        mine += (int64_t)own_len + own_work(a, own_len);
         if (len >= shared) first = min(first, s);
     }
     first = __reduce_min_sync(0xffffffffu, first);
@@ -235,7 +244,7 @@ struct Line {
     }
     int64_t total;   // tiles of all sequences
     int64_t before;  // tiles before this thread's run
-    int64_t tokens;  // (COST) tokens of all sequences
+    int64_t tokens;  // (COST) tokens of all sequences, as own_work() counts
     int32_t s0, s1;  // this thread's run
     __device__ void scan(const AttnStepArgs &a, int64_t *sm /* [THREADS / 32], COST: twice */) {
         const int tid = threadIdx.x, lane = tid & 31;
@@ -245,7 +254,10 @@ struct Line {
         int64_t mine = 0, held = 0;
         for (int32_t s = s0; s < s1; ++s) {
             mine += length_of(a, s);
-            if (COST) held += span_of<SHARED>(a, s).len();
+            if (COST) {
+                const int32_t len = span_of<SHARED>(a, s).len();
+                held += (int64_t)len + own_work(a, len);
+            }
             if (a.seq_lens[s] > (a.max_pages << a.page_shift)) *a.status = KDA_ERR_INVALID_ARG;
         }
         int64_t incl = mine;
