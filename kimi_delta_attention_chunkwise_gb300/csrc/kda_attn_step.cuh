@@ -113,9 +113,9 @@ struct PrefixPiece {
 // memory gives no more.  `prefix`: so many SMs for the former that it ends when the
 // latter does.  CTAs of the step that must wait for those get shares of late / 16 of
 // the others'.  Times in ns of an SM, by what was measured: 1.6 us to a unit of the
-// line with two row tiles, 1.13 with one, d = 128, behind 7 us; 90 GB/s of cached rows,
+// line with two row tiles, 1.13 with one, d = 128, behind 7 us; 95 GB/s of cached rows,
 // behind 4 us.  (32/8 heads, d = 128, own tokens 1-600: 256 rows behind 16384 shared
-// tokens 93 us, 128 behind 32768 84; by 75 GB/s 103, 78; by 95 89, 87.)
+// tokens 89 us, 128 behind 32768 87; by 75 GB/s 103, 78; by 90 93, 84.)
 struct SmSplit {
     int32_t prefix, late;
 };
@@ -136,7 +136,7 @@ __device__ __forceinline__ SmSplit sm_split(const AttnStepArgs &a, const PrefixL
     const float work = __fmul_rn((float)line.units, unit);
     // (rows are taken in once for every 16 query heads)
     const float rows = (float)(a.HKV * (a.G > 16 ? (a.G + 15) / 16 : 1));
-    const float own = __fmul_rn(__fmul_rn((float)own_tokens, rows), a.D / 22.5f);
+    const float own = __fmul_rn(__fmul_rn((float)own_tokens, rows), a.D / 23.75f);
     auto ends = [&](int32_t p) { return __fadd_rn(7000.f, __fdiv_rn(work, (float)p)); };
     auto step_ends = [&](int32_t p) {
         return __fadd_rn(4000.f, __fdiv_rn(own, (float)(sms - p)));
