@@ -753,8 +753,9 @@ kdaStatus_t kda_cache_append_q8(const void *q, const void *k, const void *v,
 /*
  * kda_attn_step_q8 -- kda_attn_step over a cache of 8-bit codes: the keys and
  * values are code * scale.  shape->dtype is q's (and out's, unless out_f32).
- * Scales are finite or NaN.  They multiply scores and weights in fp32; the softmax
- * weights keep 2^-15 or better in every product.  Arguments, lengths, pages, scratch and
+ * Scales are finite or NaN.  They multiply scores and weights in fp32; a softmax
+ * weight times its row's scale keeps 2^-15 or better in every product, from 2^-110 up
+ * and from 2^-110 of a query head's largest up.  Arguments, lengths, pages, scratch and
  * errors as for kda_attn_step.
  */
 kdaStatus_t kda_attn_step_q8(const void *q, const kdaPagedCacheQ8_t *cache,

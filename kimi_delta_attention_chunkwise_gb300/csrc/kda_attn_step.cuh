@@ -576,12 +576,13 @@ __device__ __forceinline__ float rest_of(float w, float hi) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(lo) : "f"(w - hi), "f"(hi * 0x1p-20f), "f"(fminf(hi, 0x1p-126f)));
     return lo;
 }
-// (FINITE: no value is an infinity, and lo may be 0)
+// (FINITE: no value is an infinity, and lo may be 0; it is multiplied by `by`)
 template <bool FINITE>
-__device__ __forceinline__ void split_weights(float w0, float w1, uint32_t &hi, uint32_t &lo) {
+__device__ __forceinline__ void split_weights(float w0, float w1, uint32_t &hi, uint32_t &lo,
+                                              float by = 1.f) {
     hi = __byte_perm(__float_as_uint(w0), __float_as_uint(w1), 0x7632);
     const float h0 = __uint_as_float(hi << 16), h1 = __uint_as_float(hi & 0xFFFF0000u);
-    lo = FINITE ? tc::pack_bf16x2(w0 - h0, w1 - h1)
+    lo = FINITE ? tc::pack_bf16x2((w0 - h0) * by, (w1 - h1) * by)
                 : tc::pack_bf16x2(rest_of(w0, h0), rest_of(w1, h1));
 }
 
@@ -599,10 +600,14 @@ __device__ __forceinline__ void split_weights(float w0, float w1, uint32_t &hi, 
 //     each row times the power of two that brings its largest to 2^14 .. 2^15:
 //     exact down to 2^-31 of it, and what is smaller is off by 2^-39 of it;
 //   * f16 for the values, too, with at most 4 query heads, where the weights' low
-//     parts have columns of their own and go there times 2^11.  The weights are
-//     lifted by 2^7 and the scales divided by vref, a power of two that none has
-//     reached so far, so that the product lies below 2^15: weights down to 2^-28 of
-//     a row's largest keep 2^-15, smaller ones 2^-43 of the largest, times vref;
+//     parts have columns of their own and go there times 2^11.  A weight times its
+//     row's scale is divided by vref, which belongs to the query head: the largest such
+//     product so far lies between 2^6 and 2^15.  Products down to 2^-21 keep 2^-15 as
+//     two f16 parts; a tile with a smaller one (a mask's end, a weight 2^-27 of the
+//     largest, a scale far above the others') takes two bf16 parts instead, whose
+//     range needs no reference (64 sequences of 512-8192 tokens, 32/8 heads, d = 128:
+//     112 us where no tile does, 119 where all do, 126 with scores of +-30, which move
+//     references, too);
 //   * bf16 for the values else (whose range needs no reference): 0x4300 | u is
 //     v = 128 + u below u = 128 and 2 u from there on, so that with w = v - 256
 //     the code is w below 0 and w / 2 from there on, w - max(w / 2, 0): three
@@ -661,12 +666,13 @@ struct MmaCore {
     static constexpr int KC = kScaled ? J / 2 : J, VV = kScaled ? 1 : VC;  // as they lie in the cache
     static constexpr int MT = D / 16;  // channel tiles of O^T
     static constexpr float kMoveBy = 8.f;
-    // weights and values as f16 (kScaled): the weights' lift, and what the low
-    // parts are multiplied by
+    // weights and values as f16 (kScaled), and what the low parts are multiplied by
     static constexpr bool kF16 = kScaled && FOLD;
-    static constexpr float kLift = kF16 ? 7.f : 0.f, kLow = kF16 ? 0x1p11f : 1.f;
+    static constexpr float kLow = kF16 ? 0x1p11f : 1.f;
     static constexpr float kNoRef = kF16 ? -FLT_MAX : -INFINITY;
-    float vref, vback;  // (kF16) the scales' reference, its reciprocal
+    // (kF16) the products that two f16 parts hold
+    static constexpr float kLeast = 0x1p-21f, kMost = 0x1p15f;
+    float vref[2], vback[2];  // (kF16) the products' references, their reciprocals
 
     uint4 q[NT][J], k[2][KC], v[4][VV];
     float kf[2], vf[2];  // scales of tokens g and g + 8 (kScaled)
@@ -723,7 +729,8 @@ struct MmaCore {
     __device__ void init(Row row, int rows, float scale) {
         const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
         c2 = scale * kLog2e;
-        vref = vback = 0.f;
+        vref[0] = vref[1] = 0.f;
+        vback[0] = vback[1] = 1.f;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int h = FOLD ? g & 3 : n * 8 + g;
@@ -877,6 +884,39 @@ struct MmaCore {
             }
         }
     }
+    // References (kF16) that the tile's scores s and scales vf fit, and what is held
+    // brought to them.
+    __device__ void move_f16() {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float r = fmaxf(fmaxf(s[0][e], s[0][e + 2]) * c2, ref[0][e]);
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, x));
+            const float f = exp2f(ref[0][e] - r);
+            ref[0][e] = r;
+            sum[0][e] *= f;
+            // the products so far are f * vref of the new weights'; theirs are y at most
+            float y = 0.f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                y = fmaxf(y, tc::exp2_approx(fmaf(s[0][2 * h + e], c2, -r)) * fabsf(vf[h]));
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, x));
+            const float held = f * vref[e];
+            float now = fmaxf(held, 0x1p-126f);
+            if (y > now * kMost)  // the power of two that brings y to 2^6 .. 2^7
+                now = __uint_as_float(((__float_as_uint(y * 0x1p-7f) >> 23) + 1) << 23);
+            const float fv = held / now;
+            vref[e] = now;
+            vback[e] = 1.f / now;
+            if (fv != 1.f) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int x = e; x < 4; x += 2) o[i][0][x] *= fv;
+            }
+        }
+    }
     // values() for kF16
     __device__ void values_f16(int n_tok) {
         const int g = (threadIdx.x & 31) >> 2;
@@ -885,66 +925,67 @@ struct MmaCore {
             if (token_of(g) >= n_tok) s[0][0] = s[0][1] = -INFINITY;
             if (token_of(g + 8) >= n_tok) s[0][2] = s[0][3] = -INFINITY;
         }
-        float top[2];
+        float w[4], x[4];  // weights; times the scales over vref
+        auto weigh = [&]() {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) top[e] = fmaxf(s[0][e], s[0][e + 2]) * c2;
-        const float v_top = fmaxf(fabsf(vf[0]), fabsf(vf[1]));
+            for (int i = 0; i < 4; ++i) {
+                w[i] = tc::exp2_approx(fmaf(s[0][i], c2, -ref[0][i & 1]));
+                x[i] = w[i] * vf[i >> 1] * vback[i & 1];
+            }
+        };
+        auto most = [&]() {
+            return fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+        };
+        weigh();
         // (NaN compares false: a NaN score moves nothing and shows in the sums, a
         // NaN scale in the weights)
-        const bool move = top[0] > ref[0][0] + (kMoveBy + kLift) ||
-                          top[1] > ref[0][1] + (kMoveBy + kLift) || v_top > vref;
+        const bool move = fmaxf(s[0][0], s[0][2]) * c2 > ref[0][0] + kMoveBy ||
+                          fmaxf(s[0][1], s[0][3]) * c2 > ref[0][1] + kMoveBy || most() > kMost;
         if (__any_sync(0xffffffffu, move)) {
-            float f[2], m = v_top;
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-            float fv = 1.f;
-            if (m > vref) {  // the power of two above it
-                const uint32_t e = min((__float_as_uint(m) >> 23) + 1, 253u);
-                vback = __uint_as_float((254 - e) << 23);
-                fv = vref * vback;
-                vref = __uint_as_float(e << 23);
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float r = fmaxf(top[e], ref[0][e] + kLift);
-#pragma unroll
-                for (int x = 4; x < 32; x <<= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, x));
-                r = fmaxf(r - kLift, -FLT_MAX);
-                f[e] = exp2f(ref[0][e] - r);
-                ref[0][e] = r;
-                sum[0][e] *= f[e];
-            }
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[i][0][e] *= f[e & 1] * fv;
+            move_f16();
+            weigh();
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[0][i & 1] += w[i];
+        const float least =
+            fminf(fminf(fabsf(x[0]), fabsf(x[1])), fminf(fabsf(x[2]), fabsf(x[3])));
         uint32_t p[2];  // by half of the tokens
+        // rows g and g + 8 of channel tile i are bytes i and MT + i of a lane's
+        // vectors; words of four bytes at a time
+        if (__any_sync(0xffffffffu, least < kLeast || most() > kMost)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t hi, lo;
+                split_weights<true>(x[2 * h], x[2 * h + 1], hi, lo, kLow);
+                p[h] = transpose_8x8(low ? lo : hi);
+            }
+#pragma unroll
+            for (int w4 = 0; w4 < MT / 4; ++w4) {
+                uint32_t a[4][4];
+                value_words<0x43434343u>(w4, a);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    mma_16816(o[4 * w4 + c][0], codes_to_bf16x2(a[c][0]), codes_to_bf16x2(a[c][1]),
+                              codes_to_bf16x2(a[c][2]), codes_to_bf16x2(a[c][3]), p[0], p[1]);
+            }
+            return;
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float by = vf[h] * vback;
-            float w[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                w[e] = tc::exp2_approx(fmaf(s[0][2 * h + e], c2, -ref[0][e]));
-                sum[0][e] += w[e];
-                w[e] *= by;
-            }
-            const __half2 hi = __floats2half2_rn(w[0], w[1]);
+            const __half2 hi = __floats2half2_rn(x[2 * h], x[2 * h + 1]);
             const float2 back = __half22float2(hi);
-            const __half2 lo = __floats2half2_rn((w[0] - back.x) * kLow, (w[1] - back.y) * kLow);
+            const __half2 lo =
+                __floats2half2_rn((x[2 * h] - back.x) * kLow, (x[2 * h + 1] - back.y) * kLow);
             const __half2 mine = low ? lo : hi;
             p[h] = transpose_8x8(*reinterpret_cast<const uint32_t *>(&mine));
         }
-        // rows g and g + 8 of channel tile i are bytes i and MT + i of a lane's
-        // vectors; words of four bytes at a time
 #pragma unroll
-        for (int w = 0; w < MT / 4; ++w) {
+        for (int w4 = 0; w4 < MT / 4; ++w4) {
             uint32_t a[4][4];
-            value_words<0x64646464u>(w, a);
+            value_words<0x64646464u>(w4, a);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-                mma_16816_f16(o[4 * w + c][0], codes_to_f16x2(a[c][0]), codes_to_f16x2(a[c][1]),
+                mma_16816_f16(o[4 * w4 + c][0], codes_to_f16x2(a[c][0]), codes_to_f16x2(a[c][1]),
                               codes_to_f16x2(a[c][2]), codes_to_f16x2(a[c][3]), p[0], p[1]);
         }
     }
@@ -1084,7 +1125,7 @@ struct MmaCore {
                     for (int i = 0; i < MT; ++i) {
                         y[i] = o[i][n][e + 2 * hi];
                         if (FOLD) y[i] += __shfl_xor_sync(0xffffffffu, y[i], 2) * (1.f / kLow);
-                        if (kF16) y[i] *= vref;
+                        if (kF16) y[i] *= vref[e];
                     }
                     const int ch = !kScaled && VC == 2 ? 64 * hi + 8 * g : 2 * MT * g + MT * hi;
                     if (h < rows) put(h, ch, y, state_max(ref[n][e], seen), l);
@@ -1115,7 +1156,7 @@ struct MmaCore {
                                              : 8 * g + 4 * (e >> 1) + i;
                     float x = o[i][n][e];
                     if (FOLD) x += __shfl_xor_sync(0xffffffffu, x, 2) * (1.f / kLow);
-                    if (kF16) x *= vref;
+                    if (kF16) x *= vref[e & 1];
                     if (h < kRows) sacc[h * D + ch] = x;
                 }
         }
