@@ -11,8 +11,12 @@
 // key tile j, in the order (0, 0), (1, 0), (0, 1), ...:
 //
 //     S = Q_t K_j^T            tcgen05, operands in shared memory, D in TMEM
-//     P = 2^{c S - ref}        one thread per row; bf16, over S's columns
-//     O_t (+)= P V_j           tcgen05, A = P from TMEM, V_j as it lies
+//     P = 2^{c S - ref}        one thread per row; two bf16 parts, over S's columns
+//     O_t (+)= P V_j           tcgen05, A = P's parts from TMEM, V_j as it lies
+//
+// The parts leave 2^-15 of a weight out, as kda_attn_step's do: one part, 2^-8, would
+// make a sequence's result depend on how many others share its pages (MmaCore's cores
+// work on up to kFewRows rows).  The second product is half as much tensor work again.
 //
 // Two score tiles take the units in turn and the scores run two units ahead of
 // the products: with two row tiles the tensor core works for one while the
@@ -23,13 +27,12 @@
 // copies from outside of the cache leave at zero.  References move as in
 // kda_attn_tc.cu: by more than 2^8 or not at all.
 //
-// A unit, two row tiles against 128 keys, takes 1.7 us of an SM at d = 128 (a row tile
-// alone 1.2), 0.66 of the tensor cores' measured rate: the weights of a row tile wait for
-// its scores and the next scores for its products, since two score tiles and two
-// outputs are all that TMEM holds.  Few sequences are bound by the keys' and values'
-// bytes, many by the units (32/8 heads, no tokens but the shared ones, with the join:
-// 24 sequences, 65536 keys 57 us, 4.7 TB/s; 256 sequences, 16384 keys 60 us, 1140
-// TFLOP/s).
+// A unit, two row tiles against 128 keys, takes 2.27 us of an SM at d = 128 (a row tile
+// alone 1.65; d = 64: 1.77 and 1.01), with the second parts 25 MFLOP: 0.88 of the tensor
+// cores' measured rate (with one part 1.6 us, 0.83).  A row tile alone waits for its own
+// weights and they for its scores.  Few sequences are bound by the keys' and values'
+// bytes, many by the units (32/8 heads, d = 128, no tokens but the shared ones, with the
+// join: 32 sequences, 32768 keys 40.5 us, 3.3 TB/s; 256 sequences 142 us, 1450 TFLOP/s).
 //
 // Warps: 0-3 and 4-7 the weights and results of row tile 0 and 1, 8 issues the
 // MMAs, 9 the copies.  Waits are bounded as there.
@@ -56,7 +59,9 @@ struct Cfg {
     static constexpr int PANELS = D / 64;
     static constexpr uint32_t PANEL = kRowTile * 128, TILE = PANELS * PANEL;  // bytes: Q, K and V alike
     static constexpr int STAGES = D == 128 ? 4 : 8;  // K and V tiles in flight
-    static constexpr int EARLY = D == 128 ? 32 : 64;  // keys whose weights go to the product first
+    // keys whose weights go to the product first (256 sequences, 32768 keys, d = 128:
+    // 142 us, with 32 153)
+    static constexpr int EARLY = 64;
     static constexpr uint32_t O_BASE = 2 * kKeys;     // TMEM columns: two score tiles, O_0, O_1
     static constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, kKeys);
     static constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D) | (1u << 16);  // V is N-major
@@ -92,6 +97,20 @@ struct Rows {
     }
     __device__ bool two() const { return n[1] > 0; }
 };
+
+// Two weights as two bf16 parts each that leave 2^-15 out: hi is w less 2^-9 of it, cut
+// off, and lo the rest, rounded.  Less 2^-9, so that lo is positive where hi is (an
+// infinite value times a low part of 0 would be a NaN); for w in 1 .. 2 the rest is below
+// 2^-7 + 2^-8, and half a step of it 2^-15, as of 2^-7.
+__device__ __forceinline__ void split_weight_pair(float2 w, uint32_t &hi, uint32_t &lo) {
+    constexpr float kLess = 1.f - 0x1p-9f;
+    const float2 h = f2_mul(w, make_float2(kLess, kLess));
+    const uint32_t x = __float_as_uint(h.x), y = __float_as_uint(h.y);
+    hi = __byte_perm(x, y, 0x7632);
+    const float2 rest = f2_add(w, make_float2(__uint_as_float((x & 0xFFFF0000u) | 0x80000000u),
+                                              __uint_as_float((y & 0xFFFF0000u) | 0x80000000u)));
+    lo = pack_bf16x2(rest.x, rest.y);
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreadsTc, 1)
@@ -265,23 +284,25 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap map_q,
                 const float2 c22 = make_float2(c2, c2), neg2 = make_float2(neg, neg);
                 float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
 #pragma unroll
-                for (int h = 0; h < kKeys / 32; ++h) {
-                    uint32_t p[16];
+                for (int h = 0; h < kKeys / 16; ++h) {
+                    // (16 keys at a time: 32 spill 244 bytes of registers, this 52)
+                    uint32_t hi[8], lo[8];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float2 x = f2_fma(make_float2(s[h * 32 + 2 * i], s[h * 32 + 2 * i + 1]), c22,
+                    for (int i = 0; i < 8; ++i) {
+                        float2 x = f2_fma(make_float2(s[h * 16 + 2 * i], s[h * 16 + 2 * i + 1]), c22,
                                           neg2);
                         x.x = exp2_approx(x.x);
                         x.y = exp2_approx(x.y);
                         if (i & 1) acc1 = f2_add(acc1, x);
                         else acc0 = f2_add(acc0, x);
-                        p[i] = pack_bf16x2(x.x, x.y);
+                        split_weight_pair(x, hi[i], lo[i]);
                     }
-                    st16_nowait(s_addr + h * 16, p);
-                    if (h == C::EARLY / 32 - 1 || h == kKeys / 32 - 1) {
+                    st8_nowait(s_addr + h * 8, hi);
+                    st8_nowait(s_addr + kKeys / 2 + h * 8, lo);
+                    if (h == C::EARLY / 16 - 1 || h == kKeys / 16 - 1) {
                         tmem_wait_st();
                         tc_fence_before();
-                        arrive_warp(h == C::EARLY / 32 - 1 ? &sh.p_full[slot] : &sh.p_rest[slot]);
+                        arrive_warp(h == C::EARLY / 16 - 1 ? &sh.p_full[slot] : &sh.p_rest[slot]);
                         __syncwarp();
                     }
                 }
@@ -386,9 +407,11 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap map_q,
                         if (!ok) return;
                         tc_fence_after();
                         auto product = [&](int ks) {
-                            mma_tmem_a(tmem + C::O_BASE + t * D, tmem + slot * kKeys + ks * 8,
-                                       vd + ks * (2048 >> 4), C::IDESC_PV,
+                            const uint32_t o = tmem + C::O_BASE + t * D;
+                            const uint32_t p = tmem + slot * kKeys + ks * 8;
+                            mma_tmem_a(o, p, vd + ks * (2048 >> 4), C::IDESC_PV,
                                        (j > 0 || ks > 0) ? 1u : 0u);
+                            mma_tmem_a(o, p + kKeys / 2, vd + ks * (2048 >> 4), C::IDESC_PV, 1u);
                         };
 #pragma unroll
                         for (int ks = 0; ks < C::EARLY / 16; ++ks)

@@ -112,8 +112,8 @@ struct PrefixPiece {
 // former is bound by what an SM computes, the latter by what an SM takes in, until
 // memory gives no more.  `prefix`: so many SMs for the former that it ends when the
 // latter does.  CTAs of the step that must wait for those get shares of late / 16 of
-// the others'.  Times in ns of an SM, by what was measured: 1.6 us to a unit of the
-// line with two row tiles, 1.13 with one, d = 128, behind 7 us; 95 GB/s of cached rows,
+// the others'.  Times in ns of an SM, by what was measured: 2.27 us to a unit of the
+// line with two row tiles, 1.65 with one (d = 64: 1.77, 1.01), behind 7 us; 95 GB/s of cached rows,
 // behind 4 us.  (32/8 heads, d = 128, own tokens 1-600: 256 rows behind 16384 shared
 // tokens 89 us, 128 behind 32768 87; by 75 GB/s 103, 78; by 90 93, 84.)
 struct SmSplit {
@@ -132,7 +132,7 @@ __device__ __forceinline__ SmSplit sm_split(const AttnStepArgs &a, const PrefixL
     if (line.units == 0) return {0, 16};
     const bool two = a.prefix_rows > 128 / a.G * a.G;  // row tiles to a unit
     // (each operation rounded by itself: the same division in both kernels)
-    const float unit = (two ? 1600.f : 1130.f) * (a.D == 64 ? 0.75f : 1.f);
+    const float unit = a.D == 64 ? (two ? 1770.f : 1010.f) : (two ? 2270.f : 1650.f);
     const float work = __fmul_rn((float)line.units, unit);
     // (rows are taken in once for every 16 query heads)
     const float rows = (float)(a.HKV * (a.G > 16 ? (a.G + 15) / 16 : 1));
