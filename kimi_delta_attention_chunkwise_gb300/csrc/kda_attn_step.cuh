@@ -113,9 +113,11 @@ struct PrefixPiece {
 // memory gives no more.  `prefix`: so many SMs for the former that it ends when the
 // latter does.  CTAs of the step that must wait for those get shares of late / 16 of
 // the others'.  Times in ns of an SM, by what was measured: 2.27 us to a unit of the
-// line with two row tiles, 1.65 with one (d = 64: 1.77, 1.01), behind 7 us; 95 GB/s of cached rows,
-// behind 4 us.  (32/8 heads, d = 128, own tokens 1-600: 256 rows behind 16384 shared
-// tokens 89 us, 128 behind 32768 87; by 75 GB/s 103, 78; by 90 93, 84.)
+// line with two row tiles, 1.65 with one (d = 64: 1.77, 1.01), behind 5 us; 95 GB/s
+// of cached rows, behind 4 us.  The starts and the rate were fitted over 18 sizes (20-500
+// sequences of up to 5000 tokens behind 4096-65536, 5/1, 8/1, 8/2, 16/2, 16/4, 28/4, 32/8,
+// 40/8, 64/8 heads, both widths): mean times 53.6 us, with 7 us 54.3, 11 us 56.5, with
+// 85 GB/s 53.6, 75 54.1, 110 GB/s and 7 us 57.2; single sizes lie up to 7% above their best.
 struct SmSplit {
     int32_t prefix, late;
 };
@@ -137,7 +139,7 @@ __device__ __forceinline__ SmSplit sm_split(const AttnStepArgs &a, const PrefixL
     // (rows are taken in once for every 16 query heads)
     const float rows = (float)(a.HKV * (a.G > 16 ? (a.G + 15) / 16 : 1));
     const float own = __fmul_rn(__fmul_rn((float)own_tokens, rows), a.D / 23.75f);
-    auto ends = [&](int32_t p) { return __fadd_rn(7000.f, __fdiv_rn(work, (float)p)); };
+    auto ends = [&](int32_t p) { return __fadd_rn(5000.f, __fdiv_rn(work, (float)p)); };
     auto step_ends = [&](int32_t p) {
         return __fadd_rn(4000.f, __fdiv_rn(own, (float)(sms - p)));
     };
