@@ -196,7 +196,10 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
     using Shares = FlatShares<COST + 2>;
     Shares shares(line.total * items, (int32_t)gridDim.x * kWarps);
     if (SHARED && a.prefix_sms && (int32_t)gridDim.x == a.prefix_sms * Core::kCtas) {
-        const SmSplit split = sm_split(a, PrefixLine(a, shared_tokens(a)), line.tokens);
+        // (where no sequence holds the shared tokens, nobody works on them: 16 sequences
+        // of 500-2000 tokens, 65536 said to be shared, 51 us where SMs were left for that, 25)
+        const PrefixLine prefix(a, line.shares ? shared_tokens(a) : 0);
+        const SmSplit split = sm_split(a, prefix, line.tokens);
         shares = Shares(line.total * items, (int32_t)gridDim.x * kWarps,
                         (a.prefix_sms - split.prefix) * Core::kCtas * kWarps, split.late);
     }

@@ -247,6 +247,7 @@ struct Line {
     int64_t total;   // tiles of all sequences
     int64_t before;  // tiles before this thread's run
     int64_t tokens;  // (COST) tokens of all sequences, as own_work() counts
+    bool shares;     // (COST, SHARED) a sequence holds the shared tokens
     int32_t s0, s1;  // this thread's run
     __device__ void scan(const AttnStepArgs &a, int64_t *sm /* [THREADS / 32], COST: twice */) {
         const int tid = threadIdx.x, lane = tid & 31;
@@ -254,11 +255,13 @@ struct Line {
         s0 = min(tid * per, a.N);
         s1 = min(s0 + per, a.N);
         int64_t mine = 0, held = 0;
+        int holds = 0;
         for (int32_t s = s0; s < s1; ++s) {
             mine += length_of(a, s);
             if (COST) {
-                const int32_t len = span_of<SHARED>(a, s).len();
-                held += (int64_t)len + own_work(a, len);
+                const Span span = span_of<SHARED>(a, s);
+                held += (int64_t)span.len() + own_work(a, span.len());
+                holds |= span.first;
             }
             if (a.seq_lens[s] > (a.max_pages << a.page_shift)) *a.status = KDA_ERR_INVALID_ARG;
         }
@@ -274,7 +277,8 @@ struct Line {
             for (int o = 16; o > 0; o >>= 1) held += __shfl_xor_sync(0xffffffffu, held, o);
             if (lane == 0) sm[THREADS / 32 + (tid >> 5)] = held;
         }
-        __syncthreads();
+        if constexpr (COST > 0 && SHARED) shares = __syncthreads_or(holds);
+        else __syncthreads();
         before = incl - mine;
         total = tokens = 0;
         for (int w = 0; w < THREADS / 32; ++w) {
