@@ -1323,8 +1323,8 @@ def kda_attn_step_shared(q, k_cache, v_cache, block_table, seq_lens, shared_page
                          out=None, lse=None, *, workspace=None, stream=None,
                          out_f32: bool = False):
     """kda_attn_step for sequences that have their first pages in common, which
-    are read once for all of them (C: kda_attn_step_shared_ws).  Returns
-    ``(out, lse)``.
+    are read once for many of them (C: kda_attn_step_shared_ws, which says for how
+    many).  Returns ``(out, lse)``.
 
     ``shared_pages``: int32 [1] on the device: so many leading entries of
     block_table are the same in the row of every sequence that has that many

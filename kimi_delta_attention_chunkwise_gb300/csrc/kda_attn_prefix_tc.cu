@@ -129,8 +129,7 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap map_q,
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();
     const int32_t shared = shared_tokens(a);
-    if (blockIdx.x == 0 && tid == 0 && (*a.shared_pages < 0 || *a.shared_pages > a.max_pages))
-        *a.status = KDA_ERR_INVALID_ARG;
+    if (blockIdx.x == 0 && tid == 0) check_shared_pages(a);
     PrefixLine line(a, shared);
     const int32_t cta = (int32_t)blockIdx.x;
     if (cta >= line.grid) return;

@@ -11,11 +11,17 @@
 // joins all of a row's.  A sequence that holds less than S tokens is all the
 // step's.
 //
-// Tables that are short enough for the plain step's one launch of clusters are
-// left to it: reading the shared rows from L2 for every sequence takes less than
-// three kernels do (192 + 50 tokens, 3 sequences, 8/2 heads, d = 64: 4.9 us, 11.6;
-// 1024 + 100, 8 sequences, 32/8 heads, d = 128: 10.7, 22; 1024 + 100, 32 fp32
-// sequences, 6/2 heads, d = 64: 10.5, 14).
+// The plain step does it all (Plan::plain) where
+//   * the table is short enough for its one launch of clusters: reading the shared
+//     rows from L2 for every sequence takes less than three kernels do (192 + 50 tokens,
+//     3 sequences, 8/2 heads, d = 64: 4.9 us, 11.6; 1024 + 100, 8 sequences, 32/8 heads,
+//     d = 128: 10.7, 22; 1024 + 100, 32 fp32 sequences, 6/2 heads, d = 64: 10.5, 14);
+//   * the CUDA-core blocks here would not be fewer than its own, as with 4, 8, ... query
+//     heads to a key-value head, so that the shared keys are read as often, and it has
+//     kPlainItems items or more (1-200 tokens behind 2304, 57 sequences, 16/2 heads, fp32,
+//     d = 64: 40 us, 43; 32/8 heads, d = 16: 31, 37; behind 8192, 2 sequences, d = 128:
+//     32/8 heads 28.9, 31.8; 16/2, 8 items, 18.9, 19.3, but at d = 64 14.4, 13.8; 8/2, 4
+//     items, 15.0, 10.8).
 #include "kda_attn_flat.cuh"
 
 namespace kda {
@@ -27,8 +33,9 @@ namespace {
 constexpr int kMaxSplits = 64;
 // Rows to a key-value head that the step's cores take (65536 shared tokens, 32/8 heads,
 // d = 128: 4 rows 55.6 us, the tensor core's tiles 62.0; 8 rows 57.7, 62.4; 16 rows
-// 61.6, 62.2, but 33.7, 28.0 with 16/2 heads and 32.5, 23.9 with 8/1).
+// 61.6, 62.0, but 33.7, 27.4 with 16/2 heads and 32.5, 25.2 with 8/1).
 constexpr int kFewRows = 8;
+constexpr int kPlainItems = 16;
 
 // Blocks of kRows rows over the shared tokens, on the step's cores: fp32, narrow
 // heads, and so few rows that the tensor core's tiles would be all but empty.
@@ -42,8 +49,7 @@ __global__ void __launch_bounds__(kThreads, Core::kCtas) attn_prefix_kernel(cons
     const int tid = threadIdx.x, warp = tid >> 5;
     tc::pdl_launch_dependents();
     const int32_t shared = shared_tokens(a);
-    if (blockIdx.x == 0 && tid == 0 && (*a.shared_pages < 0 || *a.shared_pages > a.max_pages))
-        *a.status = KDA_ERR_INVALID_ARG;
+    if (blockIdx.x == 0 && tid == 0) check_shared_pages(a);
     const PrefixLine line(a, shared);
     const int32_t c = (int32_t)blockIdx.x;
     if (c >= line.grid) return;
@@ -139,7 +145,7 @@ cudaError_t launch_rest(const AttnStepArgs &a, int sms, cudaStream_t stream) {
 
 // How a call's work on the shared tokens is cut, and its scratch in bytes.
 struct Plan {
-    int direct;  // CTAs to an item of the step's direct kernel, which does it all; 0: it doesn't
+    bool plain;  // kda_attn_step's kernels do it all
     bool tensor;
     int32_t rows, grid, splits;
     size_t part, owners, prefix;  // in this order
@@ -155,13 +161,6 @@ cudaError_t plan_of(const AttnStepArgs &a, Plan &p) {
         return 0;
     });
     p.tensor = a.dtype == KDA_DTYPE_BF16 && a.D >= 64 && (int64_t)a.N * a.G > kFewRows;
-    p.direct = with_core(a.D, a.G, a.dtype, [&](auto core) -> int {
-        return step_direct_ctas<decltype(core)>(a, sms);
-    });
-    if (p.direct) {
-        p.part = p.owners = p.prefix = 0;
-        return cudaSuccess;
-    }
     int64_t slots = sms;
     if (p.tensor) {
         p.rows = prefix_tc_rows(a);
@@ -173,8 +172,17 @@ cudaError_t plan_of(const AttnStepArgs &a, Plan &p) {
             return 0;
         });
     }
-    // no more CTAs than the longest line has tiles, and than kMaxSplits to an item
     const int64_t items = (int64_t)a.HKV * (((int64_t)a.N * a.G + p.rows - 1) / p.rows);
+    p.plain = with_core(a.D, a.G, a.dtype, [&](auto core) -> bool {
+        using Core = decltype(core);
+        const int64_t own = step_items<Core>(a);
+        return step_direct_ctas<Core>(a, sms) || (!p.tensor && own <= items && own >= kPlainItems);
+    });
+    if (p.plain) {
+        p.owners = p.prefix = 0;
+        return attn_step_workspace_bytes(a, &p.part);
+    }
+    // no more CTAs than the longest line has tiles, and than kMaxSplits to an item
     const int64_t capacity = (int64_t)a.max_pages << a.page_shift;
     const int64_t tiles = std::max<int64_t>(1, (capacity + kPrefixTile - 1) / kPrefixTile);
     const int64_t most = std::min<int64_t>(tiles, kMaxSplits);
@@ -200,10 +208,7 @@ cudaError_t launch_attn_step_shared(const AttnStepArgs &args, cudaStream_t strea
     Plan p;
     cudaError_t e = plan_of(a, p);
     if (e != cudaSuccess) return e;
-    if (p.direct)
-        return with_core(a.D, a.G, a.dtype, [&](auto core) -> cudaError_t {
-            return launch_direct<decltype(core)>(a, p.direct, stream);
-        });
+    if (p.plain) return launch_attn_step(a, stream);
     a.splits = p.splits;
     a.prefix_rows = p.rows;
     a.prefix_grid = p.grid;

@@ -52,6 +52,11 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 __device__ __forceinline__ int32_t shared_tokens(const AttnStepArgs &a) {
     return min(max(*a.shared_pages, 0), a.max_pages) << a.page_shift;
 }
+// What a call says that is out of range (nullptr: not kda_attn_step_shared's).
+__device__ __forceinline__ void check_shared_pages(const AttnStepArgs &a) {
+    if (a.shared_pages && (*a.shared_pages < 0 || *a.shared_pages > a.max_pages))
+        *a.status = KDA_ERR_INVALID_ARG;
+}
 constexpr int kPrefixTile = 128;  // tokens
 
 // CTA c of `grid` takes units share_start(c) .. share_start(c + 1) - 1 of a line.
@@ -1284,6 +1289,7 @@ attn_step_kernel(const AttnStepArgs a, float *part) {
     line.scan(a, s_scan);
     const int64_t units = line.total * items;
     const int32_t grid = workers(units, (int32_t)gridDim.x), c = (int32_t)blockIdx.x;
+    if (!SHARED && tid == 0 && c == 0) check_shared_pages(a);
     // sequences without keys (SHARED: the join's)
     for (int32_t s = c; s < a.N && !SHARED; s += gridDim.x) {
         if (clamp_len(a, s) > 0) continue;
@@ -1379,9 +1385,7 @@ attn_step_direct_kernel(const AttnStepArgs a) {
     core.init([&](int h) { return qp + h * D; }, rows, a.scale);
     const int32_t len = clamp_len(a, s), tiles = tiles_of(len);
     if (tid == 0 && a.seq_lens[s] > (a.max_pages << a.page_shift)) *a.status = KDA_ERR_INVALID_ARG;
-    if (tid == 0 && blockIdx.x == 0 && a.shared_pages &&  // (kda_attn_step_shared's)
-        (*a.shared_pages < 0 || *a.shared_pages > a.max_pages))
-        *a.status = KDA_ERR_INVALID_ARG;
+    if (tid == 0 && blockIdx.x == 0) check_shared_pages(a);
     const bool seen = walk_tiles(a, core, s, kvh, 0, len,
                                  (int32_t)((int64_t)tiles * rank / ctas),
                                  (int32_t)((int64_t)tiles * (rank + 1) / ctas));

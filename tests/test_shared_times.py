@@ -1,5 +1,6 @@
-"""kda_attn_step_shared leaves no SMs to work that there is not: times against the
-same call's with nothing shared, medians of replayed graphs in turn."""
+"""kda_attn_step_shared leaves no SMs to work that there is not, and does not share
+where nothing is gained: times against the same call's with nothing shared and
+against kda_attn_step's, medians of replayed graphs in turn."""
 import pytest
 import torch
 
@@ -57,3 +58,24 @@ def test_shared_pages_that_no_sequence_holds(n, common):
     none, unheld = _medians([
         _captured(lambda: kda.kda_attn_step_shared(q, kc, vc, table, lens, p, 0.1)) for p in pages])
     assert unheld < 1.4 * none, f"{unheld * 100:.1f} us, with none shared {none * 100:.1f}"
+
+
+@pytest.mark.parametrize("HQ,HKV,d,dtype", [(32, 8, 16, torch.float32), (16, 2, 16, torch.float32),
+                                            (16, 2, 32, torch.bfloat16)])
+def test_sharing_that_saves_no_reads(HQ, HKV, d, dtype):
+    """With 4 or 8 query heads to a key-value head the CUDA-core blocks behind shared
+    pages are as many as kda_attn_step's: the call takes no longer than that."""
+    n, common, page = 57, 36, 64
+    g = torch.Generator(device="cuda").manual_seed(d)
+    lens = common * page + torch.randint(1, 200, (n,), generator=g, device="cuda", dtype=torch.int32)
+    kc, vc = (torch.randn(common + 4 * n, HKV, page, d, generator=g, device="cuda").to(dtype)
+              for _ in range(2))
+    table = torch.arange(common, dtype=torch.int32, device="cuda").repeat(n, 1)
+    table = torch.cat((table, common + torch.arange(4 * n, dtype=torch.int32, device="cuda").view(n, 4)),
+                      dim=1)
+    q = torch.randn(n, HQ, d, generator=g, device="cuda").to(dtype)
+    pages = torch.tensor([common], dtype=torch.int32, device="cuda")
+    shared, plain = _medians([
+        _captured(lambda: kda.kda_attn_step_shared(q, kc, vc, table, lens, pages, 0.1)),
+        _captured(lambda: kda.kda_attn_step(q, kc, vc, table, lens, 0.1))])
+    assert shared < 1.08 * plain, f"{shared * 100:.1f} us, kda_attn_step {plain * 100:.1f}"

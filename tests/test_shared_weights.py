@@ -84,3 +84,25 @@ def test_a_sequence_alone_and_among_others(d, HQ):
         plain, _ = kda.kda_attn_step(*args, 1.0, out_f32=True)
         for o in (out, plain):
             _rows(q[:2], ks, vs, o, lse, TWO_PARTS)
+
+
+@pytest.mark.parametrize("dtype,HQ,HKV,d", [("f32", 4, 1, 64), ("f32", 16, 2, 16), ("bf16", 8, 2, 32)])
+def test_calls_that_the_plain_step_does(dtype, HQ, HKV, d):
+    """Row blocks that sharing would not save: kda_attn_step's kernels, and its bits,
+    with the shared form's own checks of pages and of their number."""
+    common, page = 8, 32
+    lens = [common * page + 11 * i % 97 for i in range(20)] + [100, 0, 3]
+    q, ks, vs, kc, vc, table = _peaked(d, common, lens, HQ, HKV, d, page, dtype)
+    wide, n, q = widen(table), i32(lens), q.cuda()
+    lse = torch.empty(len(lens), HQ, device="cuda")
+    out, _ = kda.kda_attn_step_shared(q, kc, vc, wide, n, i32([common]), 1.0, None, lse, out_f32=True)
+    _rows(q.cpu(), ks, vs, out, lse, FP32)
+    assert torch.equal(out, kda.kda_attn_step(q, kc, vc, wide, n, 1.0, out_f32=True)[0])
+    assert kda.kda_device_status() == kda.KDA_SUCCESS
+    for bad in (-1, wide.shape[1] + 1):
+        got, _ = kda.kda_attn_step_shared(q, kc, vc, wide, n, i32([bad]), 1.0, out_f32=True)
+        assert kda.kda_device_status() == kda.KDA_ERR_INVALID_ARG
+        assert torch.equal(got, out)
+    wide[:20, 2] = kc.shape[0]
+    kda.kda_attn_step_shared(q, kc, vc, wide, n, i32([common]), 1.0)
+    assert kda.kda_device_status() == kda.KDA_ERR_INVALID_ARG
