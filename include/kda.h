@@ -801,6 +801,33 @@ kdaStatus_t kda_attn_step_shared_ws(const void *q, const kdaPagedCache_t *cache,
                                     const kdaAttnShape_t *shape, void *workspace,
                                     size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * kda_attn_step_q8_ws_diag, kda_attn_step_shared_ws_diag -- diagnostic forms of the
+ * calls without _diag, for tests of the failure path (no page counterpart).  Every
+ * bounded wait for a copy is limited to `wait_cycles` SM clocks (<= 0: the default,
+ * ~1 s).  `withhold`: one copy is made and never taken as landed; the wait for it runs
+ * out, its kernel sets KDA_ERR_TIMEOUT in the device status word, waits (with the same
+ * limit) for its copies and ends, and out and lse hold anything.  KDA_ERR_UNSUPPORTED
+ * where the call has no such wait (fp32, d = 16 or 32, short tables).
+ */
+typedef enum {
+    KDA_WITHHOLD_NONE = 0,
+    KDA_WITHHOLD_STEP = 1,   /* the first rows of a sequence's own tokens */
+    KDA_WITHHOLD_SHARED = 2  /* the first shared keys on the tensor cores (more than 8
+                                rows to a key-value head; kda_attn_step_shared) */
+} kdaWithhold_t;
+kdaStatus_t kda_attn_step_q8_ws_diag(const void *q, const kdaPagedCacheQ8_t *cache,
+                                     const int32_t *seq_lens, float scale, void *out, float *lse,
+                                     const kdaAttnShape_t *shape, void *workspace,
+                                     size_t workspace_bytes, int32_t withhold, int64_t wait_cycles,
+                                     cudaStream_t stream);
+kdaStatus_t kda_attn_step_shared_ws_diag(const void *q, const kdaPagedCache_t *cache,
+                                         const int32_t *seq_lens, const int32_t *shared_pages,
+                                         float scale, void *out, float *lse,
+                                         const kdaAttnShape_t *shape, void *workspace,
+                                         size_t workspace_bytes, int32_t withhold,
+                                         int64_t wait_cycles, cudaStream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char *kda_status_string(kdaStatus_t status);
 

@@ -192,9 +192,13 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                                                         ctypes.POINTER(ctypes.c_size_t)]
     lib.kda_attn_step_shared_ws.argtypes = [vp, cachep, ip, ip, ctypes.c_float, vp, fp, ashp, vp,
                                             ctypes.c_size_t, vp]
+    diag = [ctypes.c_int32, ctypes.c_int64, vp]  # (tests of the failure path)
+    lib.kda_attn_step_q8_ws_diag.argtypes = lib.kda_attn_step_q8_ws.argtypes[:-1] + diag
+    lib.kda_attn_step_shared_ws_diag.argtypes = lib.kda_attn_step_shared_ws.argtypes[:-1] + diag
     for name in ("cache_append_q8", "attn_step_q8", "attn_step_q8_workspace_size",
-                 "attn_step_q8_ws", "attn_step_shared", "attn_step_shared_workspace_size",
-                 "attn_step_shared_ws"):
+                 "attn_step_q8_ws", "attn_step_q8_ws_diag", "attn_step_shared",
+                 "attn_step_shared_workspace_size", "attn_step_shared_ws",
+                 "attn_step_shared_ws_diag"):
         getattr(lib, "kda_" + name).restype = ctypes.c_int
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_status_string.restype = ctypes.c_char_p

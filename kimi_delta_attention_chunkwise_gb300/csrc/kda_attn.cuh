@@ -69,10 +69,16 @@ struct AttnStepArgs {
     int32_t splits, prefix_rows, prefix_grid;
     int32_t prefix_sms;              // SMs that the two parts divide among them, 0: they don't
     int2 *owners;                    // by item: who has worked on it (for the join)
+    // what the waits for copies are limited to, in SM clocks, and a copy that is never
+    // taken as landed (kdaWithhold_t)
+    long long wait_limit;
+    int32_t withhold;
 };
 // Scratch of the step on the current device, for these sizes and any lengths.
 cudaError_t attn_step_workspace_bytes(const AttnStepArgs &a, size_t *bytes);
 cudaError_t launch_attn_step(const AttnStepArgs &a, cudaStream_t stream);
+constexpr long long kStepWait = 2000000000LL;  // SM clocks, about a second
+// (these two: cudaErrorNotSupported where a.withhold is none of the call's waits)
 cudaError_t attn_step_q8_workspace_bytes(const AttnStepArgs &a, size_t *bytes);
 cudaError_t launch_attn_step_q8(const AttnStepArgs &a, cudaStream_t stream);
 cudaError_t attn_step_shared_workspace_bytes(const AttnStepArgs &a, size_t *bytes);

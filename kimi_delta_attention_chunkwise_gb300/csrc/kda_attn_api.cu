@@ -102,6 +102,8 @@ kdaStatus_t step_sizes(const kdaPagedCache_t *cache, const kdaAttnShape_t *shape
     a.prefix = nullptr;
     a.owners = nullptr;
     a.splits = a.prefix_rows = a.prefix_grid = a.prefix_sms = 0;
+    a.wait_limit = kStepWait;
+    a.withhold = KDA_WITHHOLD_NONE;
     return KDA_SUCCESS;
 }
 
@@ -196,7 +198,16 @@ kdaStatus_t run_step_ws(AttnStepArgs &a, StepBytes bytes, StepLaunch launch, voi
     a.workspace = workspace;
     a.status = device_status_word();
     if (!a.status) return cuda_status(cudaErrorUnknown);
-    return cuda_status(launch(a, stream));
+    const cudaError_t e = launch(a, stream);
+    return a.withhold && e == cudaErrorNotSupported ? KDA_ERR_UNSUPPORTED : cuda_status(e);
+}
+
+// What the diagnostic forms say besides.
+kdaStatus_t diagnose(AttnStepArgs &a, int32_t withhold, int64_t wait_cycles) {
+    if (withhold < KDA_WITHHOLD_NONE || withhold > KDA_WITHHOLD_SHARED) return KDA_ERR_INVALID_ARG;
+    a.withhold = withhold;
+    if (wait_cycles > 0) a.wait_limit = wait_cycles;
+    return KDA_SUCCESS;
 }
 
 // With scratch taken on the stream.
@@ -388,6 +399,19 @@ kdaStatus_t kda_attn_step_q8_ws(const void *q, const kdaPagedCacheQ8_t *cache,
                        workspace_bytes, stream);
 }
 
+kdaStatus_t kda_attn_step_q8_ws_diag(const void *q, const kdaPagedCacheQ8_t *cache,
+                                     const int32_t *seq_lens, float scale, void *out, float *lse,
+                                     const kdaAttnShape_t *shape, void *workspace,
+                                     size_t workspace_bytes, int32_t withhold, int64_t wait_cycles,
+                                     cudaStream_t stream) {
+    AttnStepArgs a;
+    kdaStatus_t st = plan_step_q8(q, cache, seq_lens, scale, out, lse, shape, a);
+    if (st == KDA_SUCCESS) st = diagnose(a, withhold, wait_cycles);
+    if (st != KDA_SUCCESS) return st;
+    return run_step_ws(a, attn_step_q8_workspace_bytes, launch_attn_step_q8, workspace,
+                       workspace_bytes, stream);
+}
+
 kdaStatus_t kda_attn_step_q8(const void *q, const kdaPagedCacheQ8_t *cache,
                              const int32_t *seq_lens, float scale, void *out, float *lse,
                              const kdaAttnShape_t *shape, cudaStream_t stream) {
@@ -414,6 +438,20 @@ kdaStatus_t kda_attn_step_shared_ws(const void *q, const kdaPagedCache_t *cache,
     AttnStepArgs a;
     const kdaStatus_t st =
         plan_step_shared(q, cache, seq_lens, shared_pages, scale, out, lse, shape, a);
+    if (st != KDA_SUCCESS) return st;
+    return run_step_ws(a, attn_step_shared_workspace_bytes, launch_attn_step_shared, workspace,
+                       workspace_bytes, stream);
+}
+
+kdaStatus_t kda_attn_step_shared_ws_diag(const void *q, const kdaPagedCache_t *cache,
+                                         const int32_t *seq_lens, const int32_t *shared_pages,
+                                         float scale, void *out, float *lse,
+                                         const kdaAttnShape_t *shape, void *workspace,
+                                         size_t workspace_bytes, int32_t withhold,
+                                         int64_t wait_cycles, cudaStream_t stream) {
+    AttnStepArgs a;
+    kdaStatus_t st = plan_step_shared(q, cache, seq_lens, shared_pages, scale, out, lse, shape, a);
+    if (st == KDA_SUCCESS) st = diagnose(a, withhold, wait_cycles);
     if (st != KDA_SUCCESS) return st;
     return run_step_ws(a, attn_step_shared_workspace_bytes, launch_attn_step_shared, workspace,
                        workspace_bytes, stream);

@@ -32,7 +32,6 @@ namespace kda {
 namespace {
 
 constexpr int kJoinGroups = kJoinThreads / 8;
-constexpr long long kFlatWait = 2000000000LL;  // SM clocks, about a second
 
 // Where a warp is in the line: unit `tile` of `tiles` of sequence s under key-value
 // head kvh and block `block` of its query heads.  `at`: its place in the line, where
@@ -185,7 +184,9 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
     const int32_t box = min(1 << a.page_shift, Cfg::UNIT), copies = Cfg::UNIT / box;
     if (tid == 0) {
         for (int w = 0; w < kWarps; ++w)
-            for (int x = 0; x < RING; ++x) tc::mbar_init(&s_full[w][x], copies);
+            for (int x = 0; x < RING; ++x)
+                tc::mbar_init(&s_full[w][x], copies + (a.withhold == KDA_WITHHOLD_STEP &&
+                                                       blockIdx.x == 0 && w == 0 && x == 0));
         tc::fence_mbar_init();
         tc::fence_proxy_async();
     }
@@ -273,7 +274,7 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
             const uint32_t p = phase >> x & 1;
             phase ^= 1u << x;
             const bool done = tc::mbar_try_wait(&full[x], p) ||
-                              tc::mbar_wait_bounded(&full[x], p, kFlatWait);
+                              tc::mbar_wait_bounded(&full[x], p, a.wait_limit);
             return __all_sync(0xffffffffu, done);
         };
 #pragma unroll
@@ -290,11 +291,12 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
                 core.init([&](int h) { return qp + h * D; }, rows, a.scale);
                 fresh = seen = false;
             }
-            --units_ahead;
             if (!wait(x)) {
                 *a.status = KDA_ERR_TIMEOUT;
+                phase ^= 1u << x;  // (its copy may land yet)
                 break;
             }
+            --units_ahead;
             const uint32_t blocks_good = good >> (x * SUB);
             const int32_t left = here.end - here.token();
 #pragma unroll
@@ -379,10 +381,10 @@ attn_flat_kernel(const AttnStepArgs a, float *part, const __grid_constant__ Flat
             }
             if (!last) here.next(a, blocks);
         }
-        // (a wait gave up: the CTA may end when the copies behind it have landed)
+        // (a wait gave up: the CTA may end when its copy and those behind it have landed)
         for (; units_ahead > 0; --units_ahead) {
-            x = x + 1 == RING ? 0 : x + 1;
             (void)wait(x);
+            x = x + 1 == RING ? 0 : x + 1;
         }
     }
     if (SHARED) tc::pdl_wait_primaries();

@@ -50,7 +50,6 @@ namespace prefix_tc {
 
 constexpr int kThreadsTc = 384;
 constexpr int kRowTile = 128, kKeys = kPrefixTile;
-constexpr long long kWaitLimit = 2000000000LL;  // SM clocks, about a second
 constexpr float kMoveBy = 8.f;
 constexpr uint32_t kStage = 32 * 128;  // bytes a warp's results pass through
 
@@ -155,7 +154,8 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap map_q,
             mbar_init(&sh.p_rest[t], 4);
         }
         for (int i = 0; i < C::STAGES; ++i) {
-            mbar_init(&sh.kv_full[i], 1);
+            mbar_init(&sh.kv_full[i],
+                      1 + (a.withhold == KDA_WITHHOLD_SHARED && cta == 0 && i == 0));
             mbar_init(&sh.kv_empty[i], 1);
         }
         mbar_init(&sh.drained, 1);
@@ -177,7 +177,7 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap map_q,
     // Waits of one thread and of a whole warp; `use` counts the barrier's phases.
     auto wait = [&](uint64_t *bar, uint32_t use) -> bool {
         if (mbar_try_wait(bar, use & 1)) return true;
-        if (mbar_wait_bounded(bar, use & 1, kWaitLimit)) return true;
+        if (mbar_wait_bounded(bar, use & 1, a.wait_limit)) return true;
         sh.abort = 1;
         *a.status = KDA_ERR_TIMEOUT;
         return false;
@@ -514,12 +514,12 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap map_q,
             // one of its barriers has arrived
             for (int t = 0; t < 2; ++t)
                 if (used[t]) {
-                    (void)mbar_wait_bounded(&sh.q_full[t], (used[t] - 1) & 1, kWaitLimit);
+                    (void)mbar_wait_bounded(&sh.q_full[t], (used[t] - 1) & 1, a.wait_limit);
                     if (ok && !sh.abort) ok = wait_warp(&sh.q_empty[t], used[t] - 1);
                 }
             for (uint32_t e = e0 > C::STAGES ? e0 - C::STAGES : 0; e < e0; ++e) {
                 if (ok && !sh.abort) ok = wait_warp(&sh.kv_empty[e % C::STAGES], e / C::STAGES);
-                else (void)mbar_wait_bounded(&sh.kv_full[e % C::STAGES], (e / C::STAGES) & 1, kWaitLimit);
+                else (void)mbar_wait_bounded(&sh.kv_full[e % C::STAGES], (e / C::STAGES) & 1, a.wait_limit);
             }
         }
     }
@@ -530,7 +530,7 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap map_q,
             // MMAs may still be in flight: one more commit follows them all
             if (elect_one()) {
                 mma_commit(&sh.drained);
-                (void)mbar_wait_bounded(&sh.drained, 0, kWaitLimit);
+                (void)mbar_wait_bounded(&sh.drained, 0, a.wait_limit);
             }
             __syncwarp();
         }

@@ -208,6 +208,10 @@ cudaError_t launch_attn_step_shared(const AttnStepArgs &args, cudaStream_t strea
     Plan p;
     cudaError_t e = plan_of(a, p);
     if (e != cudaSuccess) return e;
+    // (the step behind takes its rows by copies wherever the widths are the tensor core's)
+    const bool waits = a.withhold == KDA_WITHHOLD_SHARED ? p.tensor
+                                                         : a.dtype == KDA_DTYPE_BF16 && a.D >= 64;
+    if (a.withhold && (p.plain || !waits)) return cudaErrorNotSupported;
     if (p.plain) return launch_attn_step(a, stream);
     a.splits = p.splits;
     a.prefix_rows = p.rows;

@@ -50,7 +50,10 @@ size_t q8_bytes(const AttnStepArgs &a, int sms) {
 
 template <class Core>
 cudaError_t launch_q8(AttnStepArgs a, int sms, cudaStream_t stream) {
-    if (const int ctas = step_direct_ctas<Core>(a, sms)) return launch_direct<Core>(a, ctas, stream);
+    const int ctas = step_direct_ctas<Core>(a, sms);
+    if (a.withhold && (ctas || !Core::kAhead || a.withhold != KDA_WITHHOLD_STEP))
+        return cudaErrorNotSupported;
+    if (ctas) return launch_direct<Core>(a, ctas, stream);
     if constexpr (Core::kAhead) {
         float *part = static_cast<float *>(a.workspace);
         a.owners = reinterpret_cast<int2 *>(static_cast<char *>(a.workspace) +
