@@ -755,8 +755,10 @@ kdaStatus_t kda_cache_append_q8(const void *q, const void *k, const void *v,
  * values are code * scale.  shape->dtype is q's (and out's, unless out_f32).
  * Scales are finite or NaN.  They multiply scores and weights in fp32; a softmax
  * weight times its row's scale keeps 2^-15 or better in every product, from 2^-110 up
- * and from 2^-110 of a query head's largest up.  Arguments, lengths, pages, scratch and
- * errors as for kda_attn_step.
+ * and from 2^-110 of a query head's largest up.  Rows are brought in by runs of up to
+ * 32 of a page: those behind a sequence's length may be read, but neither what they hold
+ * nor what is written to them meanwhile changes a result.  Arguments, lengths, pages,
+ * scratch and errors else as for kda_attn_step.
  */
 kdaStatus_t kda_attn_step_q8(const void *q, const kdaPagedCacheQ8_t *cache,
                              const int32_t *seq_lens, float scale, void *out, float *lse,
@@ -785,9 +787,9 @@ kdaStatus_t kda_attn_step_q8_ws(const void *q, const kdaPagedCacheQ8_t *cache,
  * each sequence's own entries or another's are taken.  A number below 0 or above
  * max_pages is cut to it and sets KDA_ERR_INVALID_ARG in the device status
  * word; so does a shared page that is negative or >= num_pages, whose tokens
- * are left out for every sequence that shares it.  Lengths, pages, scratch
- * (the rows' partial results over the shared tokens among it) and errors as
- * for kda_attn_step.
+ * are left out for every sequence that shares it.  Rows behind a sequence's
+ * length as for kda_attn_step_q8; lengths, pages, scratch (the rows' partial
+ * results over the shared tokens among it) and errors else as for kda_attn_step.
  */
 kdaStatus_t kda_attn_step_shared(const void *q, const kdaPagedCache_t *cache,
                                  const int32_t *seq_lens, const int32_t *shared_pages, float scale,

@@ -12,15 +12,15 @@
 //
 // Rows come by 4-D tensor copies with a swizzle that leaves the core's reads free of
 // bank conflicts (8-bit, 64 sequences of 512-8192 tokens, 32/8 heads, d = 128: 112 us,
-// 5.9 TB/s of 6.8; by bulk copies of rows with conflicts 130; by kda_attn_step's
+// 5.8 TB/s of 6.8; by bulk copies of rows with conflicts 130; by kda_attn_step's
 // kernel, whose CTAs share a tile of 64 tokens and hold the next one's rows in
 // registers, 155).  Rows are read once, and say so to L2: without that the calls that
-// follow each other take 117 us, and one behind writes that fill L2 146, not 130.
+// follow each other take 5 us more, and one behind writes that fill L2 16.
 // What the kernel takes is the bytes at the memory's rate and about 15 us: 3 for the
 // line's sums and the first look-ups, 5 for the join, and the rest for SMs that get
 // less of the memory than others (their last warps end 12 us after the first SMs').
 // Shares that CTAs take from blocks that have not started, or blocks of their own at
-// the end of the line, cost more than they even out (117 us: 126, 117).
+// the end of the line, cost as much as they even out or 9 us more.
 #pragma once
 
 #include <cstring>
@@ -88,7 +88,7 @@ struct FlatCfg {
     static constexpr int RING = ROOM / SUB < 4 ? ROOM / SUB : 4;  // units
     // what an item takes besides its units (queries, results), in units: behind 16384
     // shared tokens, 256 sequences of 1-600 tokens, whose shares hold a few items or
-    // tens, take 109 us without it and 97 with it
+    // tens, took 12 us more without it
     static constexpr int COST = SUB == 2 ? 1 : 2;
     static constexpr uint32_t PANEL = UNIT * Core::kPanel;        // a panel of a unit's keys
     static constexpr uint32_t HALF = Core::kPanels * PANEL;       // a unit's keys, or values
@@ -406,10 +406,10 @@ __device__ __forceinline__ void load_run(const float *from, float *x) {
 // state (kda_attn_step_q8's are results already), and its states over the shared
 // tokens.  `parts` groups of 8 lanes to a row, each with every parts-th state, four
 // at a time: what bounds the kernel is the wait for its loads, the owners, then all
-// of a state together (kda_attn_step_q8, 131072 and 40007 tokens, 32/8 heads, d = 128:
-// the call 70 us, with one state at a time 75, as with a warp to a row and a state's
-// sums behind its maximum; kda_attn_step_shared, 24 rows behind 65536 shared tokens:
-// 63.4, 65.9, 65.2).
+// of a state together (kda_attn_step_q8, 131072 and 40007 tokens, 32/8 heads, d = 128,
+// now 69 us: one state at a time costs 5 us more, as a warp to a row and a state's
+// sums behind its maximum do; kda_attn_step_shared, 24 rows behind 65536 shared tokens,
+// 64 us: 2.5 and 1.8 more).
 template <int D, int R, bool SHARED>
 __global__ void __launch_bounds__(kJoinThreads) attn_rows_join_kernel(const AttnStepArgs a,
                                                                       const float *part,
@@ -536,7 +536,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_rows_join_kernel(const Attn
 }
 
 // Groups to a row of the join: as many as make two CTAs to an SM at most (64 rows
-// behind 4096 shared tokens, 32/8 heads: 64 groups to an SM 56.4 us, 16 58.3, 256 59.3).
+// behind 4096 shared tokens, 32/8 heads, 53 us: 16 groups to an SM, not 64, cost 2 us
+// more, 256 3).
 inline int32_t join_parts(int64_t rows, int sms) {
     int32_t parts = 1;
     while (parts < kJoinGroups && rows * parts * 2 <= (int64_t)sms * 2 * kJoinGroups) parts *= 2;

@@ -97,6 +97,13 @@ struct Rows {
     __device__ bool two() const { return n[1] > 0; }
 };
 
+// 8 columns of TMEM (st16_nowait, half of it)
+__device__ __forceinline__ void st8_nowait(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+        : "memory");
+}
 // Two weights as two bf16 parts each that leave 2^-15 out: hi is w less 2^-9 of it, cut
 // off, and lo the rest, rounded.  Less 2^-9, so that lo is positive where hi is (an
 // infinite value times a low part of 0 would be a NaN); for w in 1 .. 2 the rest is below

@@ -275,6 +275,7 @@ __device__ __forceinline__ void store_codes(int8_t *to, const float (&c)[V]) {
     else *reinterpret_cast<uint32_t *>(to) = w[0];
 }
 
+// (8 CTAs to an SM: 64 registers, bf16 rows spill 8-28 bytes of them; 9 CTAs cost more)
 template <typename T, int D, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 8 : 1) cache_append_q8_kernel(const AppendArgs a) {
     constexpr int V = Row<T>::V;
