@@ -918,7 +918,7 @@ struct MmaCore {
             const float held = f * vref[e];
             float now = fmaxf(held, 0x1p-126f);
             if (y > now * kMost)  // the power of two that brings y to 2^6 .. 2^7
-                now = __uint_as_float(((__float_as_uint(y * 0x1p-7f) >> 23) + 1) << 23);
+                now = __uint_as_float(min((__float_as_uint(y * 0x1p-7f) >> 23) + 1, 254u) << 23);
             const float fv = held / now;
             vref[e] = now;
             vback[e] = 1.f / now;

@@ -78,4 +78,4 @@ def test_sharing_that_saves_no_reads(HQ, HKV, d, dtype):
     shared, plain = _medians([
         _captured(lambda: kda.kda_attn_step_shared(q, kc, vc, table, lens, pages, 0.1)),
         _captured(lambda: kda.kda_attn_step(q, kc, vc, table, lens, 0.1))])
-    assert shared < 1.08 * plain, f"{shared * 100:.1f} us, kda_attn_step {plain * 100:.1f}"
+    assert shared < 1.1 * plain, f"{shared * 100:.1f} us, kda_attn_step {plain * 100:.1f}"
