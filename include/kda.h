@@ -774,8 +774,8 @@ kdaStatus_t kda_attn_step_q8_ws(const void *q, const kdaPagedCacheQ8_t *cache,
  * kda_attn_step_shared -- kda_attn_step for sequences that have their first
  * pages in common (a system prompt, several answers to one prompt): those
  * pages are read once for many of them, with bf16 and d = 64 or 128 for up to 256
- * rows (a row: a sequence's query head) of a key-value head, else for 4.  fp32 and
- * narrower heads with 4, 8, ... query heads to a key-value head gain nothing by it.
+ * rows (a row: a sequence's query head) of a key-value head, else for 4: with fp32 or
+ * narrower heads and 4, 8, ... query heads to a key-value head as often as by kda_attn_step.
  *
  *   shared_pages  [1] int32 device: the first *shared_pages entries of
  *                 block_table are the same in the row of every sequence that
